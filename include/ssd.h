@@ -75,7 +75,11 @@ typedef enum {
     SSD_ERR_DEVICE_CHECK = 6   /* a device-side consistency check failed (cu_seqlens) */
 } ssd_status_t;
 
-typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype_t;
+typedef enum {
+    SSD_F32 = 0,
+    SSD_BF16 = 1,
+    SSD_E4M3 = 2   /* 8 bits (4 exponent, 3 mantissa, largest 448): ssd_add_norm's rows, ssd_linear's operands */
+} ssd_dtype_t;
 
 typedef struct {
     int64_t batch;      /* batch rows (1 when cu_seqlens is given)                  */
@@ -253,6 +257,57 @@ SSD_API int ssd_bwd(const ssd_params_t* p,
  * One launch on `stream`, no workspace; bitwise deterministic. */
 SSD_API int ssd_gate_norm(int64_t rows, int32_t width, int32_t group_size, int32_t dtype,
              const void* y, const void* z, const float* weight, float eps, void* out, void* stream);
+
+/* Root-mean-square norm with the residual's addition, in one pass: the pre-norm
+ * of a layer, which also carries the residual stream.  Per row r of `width`
+ * elements:
+ *
+ *     h[k]   = x[k] + residual[k]                 (residual NULL: h = x)
+ *     rstd   = 1 / sqrt(mean_k h[k]^2 + eps)
+ *     out[k] = h[k] * rstd * weight[k]
+ *
+ * out_dtype is dtype, or SSD_E4M3: then scales[r] = max(max_k |out[k]|, 1e-30) / 448
+ * and out holds out[k] / scales[r], rounded to nearest even.  h is normalised as it was summed (fp32),
+ * before it is rounded to residual_out's type.
+ *   x             (rows, width) dtype (SSD_F32 or SSD_BF16)
+ *   residual      (rows, width) residual_dtype, or NULL.  residual_dtype is SSD_F32,
+ *                 or SSD_BF16 where dtype is.
+ *   weight        (width) fp32
+ *   out           (rows, width) out_dtype; may be x where the types are equal
+ *   scales        (rows) fp32, for SSD_E4M3 (ignored otherwise)
+ *   residual_out  (rows, width) residual_dtype, or NULL; may be residual (in place), or x where the types are equal
+ *   rstd          (rows) fp32, or NULL: kept for ssd_add_norm_bwd()
+ * Row-major, contiguous, each base aligned to its element (16-byte aligned bases
+ * and widths of whole 16-byte vectors of x run faster).  rows >= 0 (0: nothing is launched); 1 <=
+ * width <= 16384 (else SSD_ERR_UNSUPPORTED).  A NaN or an infinity makes its whole row NaN or
+ * zero as the formula does.  One launch, no workspace; bitwise deterministic. */
+SSD_API int ssd_add_norm(int64_t rows, int32_t width, int32_t dtype, int32_t residual_dtype, int32_t out_dtype,
+             const void* x, const void* residual, const float* weight, float eps,
+             void* out, float* scales, void* residual_out, float* rstd, void* stream);
+
+/* Bytes of device workspace ssd_add_norm_bwd() needs (0 on invalid sizes or rows == 0). */
+SSD_API size_t ssd_add_norm_bwd_workspace_size(int64_t rows, int32_t width);
+
+/* Gradients of ssd_add_norm() (with out_dtype == dtype): of <dout, out> + <dresidual_out, residual_out>.
+ * With xh = h * rstd and p = weight * dout,
+ *
+ *     dh = rstd * (p - xh * mean_k(p * xh)) + dresidual_out
+ *     dweight = sum_rows dout * xh
+ *
+ * and dh is the gradient of x and of residual alike.
+ *   dout           (rows, width) dtype
+ *   h              (rows, width) residual_dtype: the forward's residual_out (or x where it had no residual)
+ *   rstd           (rows) fp32, from the forward
+ *   dresidual_out  (rows, width) residual_dtype, or NULL (zeros)
+ *   dx             (rows, width) dtype, or NULL;          may be dout
+ *   dresidual      (rows, width) residual_dtype, or NULL; may be dresidual_out
+ *   dweight        (width) fp32, written
+ * At least one of dx and dresidual is given.  Other layouts as ssd_add_norm(); rows == 0 writes zeros to dweight.
+ * `workspace`: ssd_add_norm_bwd_workspace_size() bytes, 16-byte aligned.
+ * Two launches; bitwise deterministic (dweight is summed in a fixed order). */
+SSD_API int ssd_add_norm_bwd(int64_t rows, int32_t width, int32_t dtype, int32_t residual_dtype,
+             const void* dout, const void* h, const float* weight, const float* rstd, const void* dresidual_out,
+             void* dx, void* dresidual, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
 /* One autoregressive (decode) step: a single new token per batch row from a
  * resident state.  "State Space Duality and Mamba-2", section "Performance and

@@ -14,7 +14,10 @@ import importlib
 
 import torch
 
-SSD_F32, SSD_BF16 = 0, 1
+SSD_F32, SSD_BF16, SSD_E4M3 = 0, 1, 2
+
+# the operators around the scan (layer.py), loaded with the library on first use
+_LAYER = ("add_norm", "add_norm_bwd")
 
 
 class _LazyLib:
@@ -31,9 +34,14 @@ _lib = _LazyLib()
 def __getattr__(name):
     if name == "SSDError":
         return _lib.SSDError
+    if name in _LAYER:
+        fn = getattr(importlib.import_module(__name__ + ".layer"), name)
+        globals()[name] = fn
+        return fn
     raise AttributeError(name)
 
-__all__ = ["ssd_fwd", "SSDForward", "ssd_bwd", "ssd_step", "gate_norm", "segsum_dump", "check_status", "SSDError", "plan"]
+__all__ = ["ssd_fwd", "SSDForward", "ssd_bwd", "ssd_step", "gate_norm", "segsum_dump", "check_status", "SSDError", "plan",
+           *_LAYER]
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -12,7 +12,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libssd.so")
 
-SSD_F32, SSD_BF16 = 0, 1
+SSD_F32, SSD_BF16, SSD_E4M3 = 0, 1, 2
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED", 3: "SSD_ERR_WORKSPACE",
           4: "SSD_ERR_CUDA", 5: "SSD_ERR_TIMEOUT", 6: "SSD_ERR_DEVICE_CHECK"}
 
@@ -20,7 +20,8 @@ STATUS = {0: "SSD_OK", 1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED", 3: "S
 EXPORTS = ("ssd_fwd_workspace_size", "ssd_workspace_init", "ssd_fwd", "ssd_check_status",
            "ssd_status_string", "ssd_fwd_plan", "ssd_segsum_dump", "ssd_fwd_static_scratch", "ssd_step",
            "ssd_bwd_workspace_size", "ssd_bwd_workspace_size_doc_states", "ssd_bwd", "ssd_fwd_timed",
-           "ssd_gate_norm", "ssd_check_status_where", "ssd_fwd_fault_inject")
+           "ssd_gate_norm", "ssd_check_status_where", "ssd_fwd_fault_inject", "ssd_add_norm",
+           "ssd_add_norm_bwd_workspace_size", "ssd_add_norm_bwd")
 
 
 class SSDParams(ctypes.Structure):
@@ -76,6 +77,13 @@ def _load():
     lib.ssd_step.restype = ctypes.c_int
     lib.ssd_segsum_dump.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp]
     lib.ssd_segsum_dump.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.ssd_add_norm.argtypes = [i64, i32, i32, i32, i32, vp, vp, vp, f32, vp, vp, vp, vp, vp]
+    lib.ssd_add_norm.restype = ctypes.c_int
+    lib.ssd_add_norm_bwd_workspace_size.argtypes = [i64, i32]
+    lib.ssd_add_norm_bwd_workspace_size.restype = sz
+    lib.ssd_add_norm_bwd.argtypes = [i64, i32, i32, i32] + [vp] * 9 + [sz, vp]
+    lib.ssd_add_norm_bwd.restype = ctypes.c_int
     return lib
 
 

@@ -1,0 +1,340 @@
+// Root-mean-square norm with the residual's addition, and its gradient:
+//   ssd_add_norm_kernel       h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps),
+//                             out = h rstd w  (bf16, fp32, or e4m3 rows with a scale each)
+//   ssd_add_norm_bwd_kernel   dh = rstd (w do - xh mean(w do xh)) + dres,  xh = h rstd,
+//                             and each row slot's share of dw = sum_rows do xh
+//   ssd_add_norm_bwd_reduce   dw from the shares, in a fixed order
+//
+// A row is held in registers from its one read to its one write, so both passes
+// are bound by HBM.  A row belongs to kRow consecutive threads of a CTA, 16
+// elements each (8 in the backward): as 16-byte vectors of x where the width and the addresses
+// allow, one by one (strided by the row's threads, so that a warp's accesses
+// stay contiguous) where they do not.  Rows that fit a warp take one
+// each, several rows to a CTA; longer rows take a CTA.
+//
+// The sums are fp32; h is normalised as it was summed, before its rounding to the
+// residual stream's type.  e4m3: scale = max(max |out|, 1e-30) / 448, and the row
+// holds out / scale rounded to nearest even; the floor keeps the quotient of an
+// all-zero row finite.
+#include "ssd_common.cuh"
+#include "ssd_kernels.h"
+#include "ssd_vec.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kElems = 16;      // elements of a row per thread
+constexpr int kBwdElems = 8;    // the same in the backward
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxMin = 1e-30f;
+
+// Sum (or NaN-keeping maximum) over the threads of a row: a warp, or the CTA
+// (every thread of it calls; the partials are combined in warp order).
+template <bool kMax>
+__device__ __forceinline__ float row_reduce(float v, bool one_warp, float* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, v, o);
+        v = kMax ? max_nan(v, u) : v + u;
+    }
+    if (one_warp) return v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = part[0];
+    const int nw = blockDim.x >> 5;
+    for (int k = 1; k < nw; ++k) r = kMax ? max_nan(r, part[k]) : r + part[k];
+    return r;
+}
+
+template <typename T, typename R, typename O, int V>
+__global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
+    constexpr int C = kElems / V;
+    __shared__ float part[2][32];
+    const bool one_warp = a.rows_per_cta > 1 || blockDim.x == 32;
+    const int slot = one_warp ? threadIdx.x >> 5 : 0;
+    const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
+    const int nt = one_warp ? 32 : blockDim.x;
+    const int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot;
+    if (row >= a.rows) return;   // whole warps of a many-row CTA, which has no barrier
+    const int W = a.width;
+    const size_t base = (size_t)row * W;
+    const T* x = static_cast<const T*>(a.x) + base;
+    const R* res = a.residual ? static_cast<const R*>(a.residual) + base : nullptr;
+    Raw<T, V> xr[C];
+    Raw<R, V> rr[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (tid + c * nt) * V;
+        xr[c].zero();
+        rr[c].zero();
+        if (e < W) {
+            xr[c].load(x + e);
+            if (res) rr[c].load(res + e);
+        }
+    }
+    float h[C][V];
+    float ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float r[V];
+        xr[c].get(h[c]);
+        rr[c].get(r);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            h[c][k] += r[k];
+            ss = fmaf(h[c][k], h[c][k], ss);
+        }
+    }
+    ss = row_reduce<false>(ss, one_warp, part[0]);
+    const float rstd = 1.f / sqrtf(ss / (float)W + a.eps);
+    if (a.rstd && tid == 0) a.rstd[row] = rstd;
+    if (a.residual_out) {
+        R* ro = static_cast<R*>(a.residual_out) + base;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (tid + c * nt) * V;
+            if (e < W) {
+                Raw<R, V> q;
+                q.set(h[c]);
+                q.store(ro + e);
+            }
+        }
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (tid + c * nt) * V;
+        if (e < W) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                h[c][k] = h[c][k] * rstd * __ldg(a.weight + e + k);
+                amax = max_nan(amax, fabsf(h[c][k]));
+            }
+        }
+    }
+    float inv = 1.f;
+    if constexpr (sizeof(O) == 1) {
+        amax = max_nan(row_reduce<true>(amax, one_warp, part[1]), kAmaxMin);
+        const float scale = amax / kE4m3Max;
+        if (tid == 0) a.scales[row] = scale;
+        inv = 1.f / scale;
+    }
+    O* out = static_cast<O*>(a.out) + base;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (tid + c * nt) * V;
+        if (e < W) {
+            if constexpr (sizeof(O) == 1) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) h[c][k] *= inv;
+            }
+            Raw<O, V> q;
+            q.set(h[c]);
+            q.store(out + e);
+        }
+    }
+}
+
+// E: elements of a row per thread, V of them at a time.
+template <typename T, typename R, int V, int E>
+__global__ void __launch_bounds__(1024) ssd_add_norm_bwd_kernel(AddNormBwdArgs a) {
+    constexpr int C = E / V;
+    __shared__ float part[2][32];
+    const bool one_warp = a.rows_per_cta > 1 || blockDim.x == 32;
+    const int slot = one_warp ? threadIdx.x >> 5 : 0;
+    const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
+    const int nt = one_warp ? 32 : blockDim.x;
+    const int W = a.width;
+    float dw[C][V];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < V; ++k) dw[c][k] = 0.f;
+    const int64_t stride = (int64_t)gridDim.x * a.rows_per_cta;
+    int turn = 0;
+    for (int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot; row < a.rows; row += stride) {
+        const size_t base = (size_t)row * W;
+        Raw<T, V> dr[C];
+        Raw<R, V> hr[C], sr[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (tid + c * nt) * V;
+            dr[c].zero();
+            hr[c].zero();
+            sr[c].zero();
+            if (e < W) {
+                dr[c].load(static_cast<const T*>(a.dout) + base + e);
+                hr[c].load(static_cast<const R*>(a.h) + base + e);
+                if (a.dres) sr[c].load(static_cast<const R*>(a.dres) + base + e);
+            }
+        }
+        const float rstd = __ldg(a.rstd + row);
+        float p[C][V], xh[C][V];
+        float dot = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (tid + c * nt) * V;
+            dr[c].get(p[c]);
+            hr[c].get(xh[c]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                xh[c][k] *= rstd;
+                dw[c][k] = fmaf(p[c][k], xh[c][k], dw[c][k]);
+                if (e < W) p[c][k] *= __ldg(a.weight + e + k);
+                dot = fmaf(p[c][k], xh[c][k], dot);
+            }
+        }
+        // the partials of consecutive rows alternate between two arrays: a row's last
+        // reader is past the next row's barrier before a third row writes
+        dot = row_reduce<false>(dot, one_warp, part[turn]) / (float)W;
+        turn ^= 1;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (tid + c * nt) * V;
+            if (e < W) {
+                float s[V];
+                sr[c].get(s);
+#pragma unroll
+                for (int k = 0; k < V; ++k) s[k] = fmaf(p[c][k] - xh[c][k] * dot, rstd, s[k]);
+                if (a.dx) {
+                    Raw<T, V> q;
+                    q.set(s);
+                    q.store(static_cast<T*>(a.dx) + base + e);
+                }
+                if (a.dres_out) {
+                    Raw<R, V> q;
+                    q.set(s);
+                    q.store(static_cast<R*>(a.dres_out) + base + e);
+                }
+            }
+        }
+    }
+    float* share = a.shares + ((size_t)blockIdx.x * a.rows_per_cta + slot) * W;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (tid + c * nt) * V;
+        if (e < W) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) share[e + k] = dw[c][k];
+        }
+    }
+}
+
+// dw[e] = sum over the shares: 32 columns per CTA, the shares dealt to its 32
+// warps, whose sums are added in warp order.
+__global__ void __launch_bounds__(1024) ssd_add_norm_bwd_reduce(const float* shares, int nshares, int W, float* dw) {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (e < W)
+        for (int k = w; k < nshares; k += 32) s += shares[(size_t)k * W + e];
+    part[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && e < W) {
+        float t = 0.f;
+        for (int k = 0; k < 32; ++k) t += part[k][lane];
+        dw[e] = t;
+    }
+}
+
+struct RowShape {
+    int threads, rows_per_cta;
+};
+
+RowShape row_shape(int width, int64_t rows, int elems) {
+    RowShape s;
+    if (width <= 32 * elems) {
+        s.rows_per_cta = rows < 4 ? (int)rows : 4;
+        s.threads = 32 * s.rows_per_cta;
+    } else {
+        s.rows_per_cta = 1;
+        s.threads = ((width + elems - 1) / elems + 31) / 32 * 32;
+    }
+    return s;
+}
+
+// Elements per thread of the backward: 8 leave room in 64 registers for the row,
+// its gradient and the dw share; only rows beyond 1024 x 8 take 16.
+int bwd_elems(int width) { return width <= 1024 * kBwdElems ? kBwdElems : kElems; }
+
+bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+template <typename T, typename R, typename O>
+cudaError_t launch_fwd_typed(const AddNormArgs& a, int threads, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = a.width % V == 0 && on16(a.x) && on16(a.residual) && on16(a.out) && on16(a.residual_out);
+    const unsigned grid = (unsigned)((a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
+    if (vec)
+        ssd_add_norm_kernel<T, R, O, V><<<grid, threads, 0, st>>>(a);
+    else
+        ssd_add_norm_kernel<T, R, O, 1><<<grid, threads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, typename R>
+cudaError_t launch_fwd_res(const AddNormArgs& a, int threads, cudaStream_t st) {
+    if (a.out_dtype == SSD_E4M3) return launch_fwd_typed<T, R, e4m3_t>(a, threads, st);
+    return launch_fwd_typed<T, R, T>(a, threads, st);
+}
+
+template <typename T, typename R>
+cudaError_t launch_bwd_typed(const AddNormBwdArgs& a, unsigned grid, int threads, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = a.width % V == 0 && on16(a.dout) && on16(a.h) && on16(a.dres) && on16(a.dx) && on16(a.dres_out);
+    const bool wide = bwd_elems(a.width) > kBwdElems;
+    void (*kern)(AddNormBwdArgs) = vec ? (wide ? ssd_add_norm_bwd_kernel<T, R, V, kElems> : ssd_add_norm_bwd_kernel<T, R, V, kBwdElems>)
+                                       : (wide ? ssd_add_norm_bwd_kernel<T, R, 1, kElems> : ssd_add_norm_bwd_kernel<T, R, 1, kBwdElems>);
+    kern<<<grid, threads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+// Row slots of the backward's grid: as many as fill the SMs, so that each slot's
+// dw share sums many rows and the shares stay a few percent of the traffic.
+int64_t bwd_slots(int64_t rows, int width, int* rows_per_cta, int* threads, int64_t* grid) {
+    const RowShape s = row_shape(width, rows, bwd_elems(width));
+    const int per_sm = 768 / s.threads > 0 ? 768 / s.threads : 1;
+    int64_t g = (rows + s.rows_per_cta - 1) / s.rows_per_cta;
+    const int64_t most = (int64_t)kAddNormSMs * per_sm;
+    if (g > most) g = most;
+    *rows_per_cta = s.rows_per_cta;
+    *threads = s.threads;
+    *grid = g;
+    return g * s.rows_per_cta;
+}
+
+}  // namespace
+
+cudaError_t launch_add_norm(const AddNormArgs& args, cudaStream_t st) {
+    AddNormArgs a = args;
+    const RowShape s = row_shape(a.width, a.rows, kElems);
+    a.rows_per_cta = s.rows_per_cta;
+    if (a.dtype == SSD_BF16)
+        return a.residual_dtype == SSD_F32 ? launch_fwd_res<bf16_t, float>(a, s.threads, st)
+                                           : launch_fwd_res<bf16_t, bf16_t>(a, s.threads, st);
+    return launch_fwd_res<float, float>(a, s.threads, st);
+}
+
+int64_t add_norm_bwd_shares(int64_t rows, int width) {
+    int rpc, threads;
+    int64_t grid;
+    return bwd_slots(rows, width, &rpc, &threads, &grid);
+}
+
+cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& args, cudaStream_t st) {
+    AddNormBwdArgs a = args;
+    int threads;
+    int64_t grid;
+    const int64_t nshares = bwd_slots(a.rows, a.width, &a.rows_per_cta, &threads, &grid);
+    cudaError_t e;
+    if (a.dtype == SSD_BF16)
+        e = a.residual_dtype == SSD_F32 ? launch_bwd_typed<bf16_t, float>(a, (unsigned)grid, threads, st)
+                                        : launch_bwd_typed<bf16_t, bf16_t>(a, (unsigned)grid, threads, st);
+    else
+        e = launch_bwd_typed<float, float>(a, (unsigned)grid, threads, st);
+    if (e != cudaSuccess) return e;
+    ssd_add_norm_bwd_reduce<<<(unsigned)((a.width + 31) / 32), 1024, 0, st>>>(a.shares, (int)nshares, a.width, a.dweight);
+    return cudaGetLastError();
+}
+
+}  // namespace ssd

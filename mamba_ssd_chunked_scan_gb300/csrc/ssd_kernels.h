@@ -131,6 +131,39 @@ struct GateNormArgs {
     void* out;
 };
 
+// Residual RMS norm (ssd_add_norm) and its gradient (ssd_add_norm_bwd).
+constexpr int kAddNormMaxWidth = 16384;   // 1024 threads x 16 elements
+constexpr int kAddNormSMs = 152;          // SMs the backward's row slots (and its workspace) are sized for
+struct AddNormArgs {
+    int64_t rows;
+    int width;
+    int dtype, residual_dtype, out_dtype;
+    float eps;
+    const void* x;
+    const void* residual;  // or NULL
+    const float* weight;
+    void* out;
+    float* scales;         // e4m3 out: [rows]
+    void* residual_out;    // or NULL
+    float* rstd;           // [rows], or NULL
+    int rows_per_cta;
+};
+struct AddNormBwdArgs {
+    int64_t rows;
+    int width;
+    int dtype, residual_dtype;
+    const void* dout;
+    const void* h;
+    const float* weight;
+    const float* rstd;
+    const void* dres;      // or NULL
+    void* dx;              // dtype, or NULL
+    void* dres_out;        // residual_dtype, or NULL
+    float* dweight;
+    float* shares;         // [row slots * width]
+    int rows_per_cta;
+};
+
 // Constants of division by an invariant divisor d >= 1 through one high
 // multiply and a shift (Granlund and Montgomery, "Division by Invariant
 // Integers using Multiplication", 1994): l = ceil(log2 d),
@@ -165,6 +198,9 @@ cudaError_t launch_agg_tc(const FwdArgs& a, cudaStream_t st);
 cudaError_t launch_agg_rev_tc(const FwdArgs& a, cudaStream_t st);
 cudaError_t launch_split_rscan(const FwdArgs& a, const float* dfin, cudaStream_t st);
 cudaError_t launch_gate_norm(const GateNormArgs& a, cudaStream_t st);
+cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
+int64_t add_norm_bwd_shares(int64_t rows, int width);   // row slots of the backward
+cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
 size_t bwd_smem_bytes(int Qb, int P, int N);
 int bwd_chunk(int P, int N, size_t smem_limit);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t st);
