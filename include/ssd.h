@@ -309,6 +309,68 @@ SSD_API int ssd_add_norm_bwd(int64_t rows, int32_t width, int32_t dtype, int32_t
              const void* dout, const void* h, const float* weight, const float* rstd, const void* dresidual_out,
              void* dx, void* dresidual, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gated linear recurrence: one decay per channel and token (the scan above has one per head and token).
+ * Per row b, token t and channel d, with gate logits g and inputs x,
+ *
+ *     a_t = 1 / (1 + exp(-g_t)),   h_t = a_t h_{t-1} + (1 - a_t) x_t,   y_t = h_t
+ *
+ * from h = initial_states (or zero).  Packed documents (cu_seqlens, batch 1) restart from
+ * initial_states[document] (or zero) at each document's first token, as in ssd_fwd(). */
+typedef struct {
+    int64_t batch;      /* rows (1 when cu_seqlens is given)                                   */
+    int64_t seqlen;     /* tokens per row (total packed length with cu_seqlens)                 */
+    int64_t g_stride;   /* elements from one token of g (and dg) to the next, >= width          */
+    int64_t x_stride;   /* the same of x (and dx): both may be column ranges of a wider matrix  */
+    int32_t width;      /* channels                                                             */
+    int32_t ndocs;      /* documents when cu_seqlens is given, else 0                           */
+    int32_t dtype;      /* SSD_F32 or SSD_BF16: g, x, y and their gradients                     */
+} ssd_gate_scan_params_t;
+
+/* Bytes of device workspace ssd_gate_scan() and ssd_gate_scan_bwd() need; 0 on invalid parameters. */
+SSD_API size_t ssd_gate_scan_workspace_size(const ssd_gate_scan_params_t* p);
+
+/* The recurrence over whole sequences.
+ *   g, x            (batch, seqlen, width) dtype, token strides g_stride, x_stride (row b starts at token
+ *                   b * seqlen); each base aligned to its element
+ *   initial_states  (nstates, width) fp32, or NULL (zeros); nstates = ndocs with cu_seqlens, else batch
+ *   cu_seqlens      (ndocs + 1) int32, as for ssd_fwd(), or NULL
+ *   y               (batch, seqlen, width) dtype, contiguous
+ *   final_states    (nstates, width) fp32, or NULL; may not be initial_states
+ * The state is fp32 throughout; y is rounded once.  No output may overlap an input.
+ * `workspace`: at least ssd_gate_scan_workspace_size(p) bytes, 256-byte aligned (else
+ * SSD_ERR_WORKSPACE); it needs no initialisation, and calls that share it must be ordered on one
+ * stream.  A clear of its head (status word, tickets, flags) and one launch, asynchronous on `stream`; it
+ * can be captured in a CUDA graph.  Tiles of a sequence hand their states on through the workspace; every wait is
+ * bounded, and one that runs out records SSD_ERR_TIMEOUT (where 51: a tile's map, 52: a block's
+ * state) in the status word read by ssd_check_status(), as offsets that break their rule
+ * record SSD_ERR_DEVICE_CHECK.  Bitwise deterministic. */
+SSD_API int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x, const float* initial_states,
+             const int32_t* cu_seqlens, void* y, float* final_states, void* workspace, size_t workspace_bytes,
+             void* stream);
+
+/* Gradients of <dy, y> + <dfinal_states, final_states> of ssd_gate_scan():
+ *
+ *     lam_t = dy_t + a_{t+1} lam_{t+1}            (+ dfinal_states at a row's or document's last token)
+ *     dx_t  = (1 - a_t) lam_t,   dg_t = lam_t (h_{t-1} - x_t) a_t (1 - a_t),   dinitial = a_1 lam_1
+ *
+ *   g, x, initial_states, cu_seqlens  as for the forward;  y  the forward's output (contiguous)
+ *   dy             (batch, seqlen, width) dtype, contiguous
+ *   dfinal_states  (nstates, width) fp32, or NULL (zeros)
+ *   dg, dx         (batch, seqlen, width) dtype, token strides g_stride, x_stride; written
+ *   dinitial_states (nstates, width) fp32, or NULL
+ * h_{t-1} is recomputed in fp32 from the h of every 16th token, which is read from y.
+ * Workspace, launches, errors and aliasing as for ssd_gate_scan(). */
+SSD_API int ssd_gate_scan_bwd(const ssd_gate_scan_params_t* p, const void* g, const void* x, const void* y,
+             const float* initial_states, const int32_t* cu_seqlens, const void* dy, const float* dfinal_states,
+             void* dg, void* dx, float* dinitial_states, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per row of the same recurrence from a resident state (decoding):
+ *   g, x (batch, width) dtype, row strides g_stride, x_stride (elements, >= width); y (batch, width) dtype;
+ *   state_in, state_out (batch, width) fp32: equal (in place) or disjoint.
+ * batch >= 0 (0: nothing is launched).  One launch, no workspace. */
+SSD_API int ssd_gate_scan_step(int64_t batch, int32_t width, int32_t dtype, int64_t g_stride, int64_t x_stride,
+             const void* g, const void* x, const float* state_in, float* state_out, void* y, void* stream);
+
 /* One autoregressive (decode) step: a single new token per batch row from a
  * resident state.  "State Space Duality and Mamba-2", section "Performance and
  * Serving Economics": generation keeps a fixed-size recurrent state and costs

@@ -21,13 +21,20 @@ EXPORTS = ("ssd_fwd_workspace_size", "ssd_workspace_init", "ssd_fwd", "ssd_check
            "ssd_status_string", "ssd_fwd_plan", "ssd_segsum_dump", "ssd_fwd_static_scratch", "ssd_step",
            "ssd_bwd_workspace_size", "ssd_bwd_workspace_size_doc_states", "ssd_bwd", "ssd_fwd_timed",
            "ssd_gate_norm", "ssd_check_status_where", "ssd_fwd_fault_inject", "ssd_add_norm",
-           "ssd_add_norm_bwd_workspace_size", "ssd_add_norm_bwd")
+           "ssd_add_norm_bwd_workspace_size", "ssd_add_norm_bwd", "ssd_gate_scan_workspace_size", "ssd_gate_scan",
+           "ssd_gate_scan_bwd", "ssd_gate_scan_step")
 
 
 class SSDParams(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int32),
                 ("headdim", ctypes.c_int32), ("dstate", ctypes.c_int32), ("ngroups", ctypes.c_int32),
                 ("chunk", ctypes.c_int32), ("split_len", ctypes.c_int32), ("ndocs", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class GateScanParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("g_stride", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("width", ctypes.c_int32), ("ndocs", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
 
 
@@ -84,6 +91,15 @@ def _load():
     lib.ssd_add_norm_bwd_workspace_size.restype = sz
     lib.ssd_add_norm_bwd.argtypes = [i64, i32, i32, i32] + [vp] * 9 + [sz, vp]
     lib.ssd_add_norm_bwd.restype = ctypes.c_int
+    G = ctypes.POINTER(GateScanParams)
+    lib.ssd_gate_scan_workspace_size.argtypes = [G]
+    lib.ssd_gate_scan_workspace_size.restype = sz
+    lib.ssd_gate_scan.argtypes = [G] + [vp] * 7 + [sz, vp]
+    lib.ssd_gate_scan.restype = ctypes.c_int
+    lib.ssd_gate_scan_bwd.argtypes = [G] + [vp] * 11 + [sz, vp]
+    lib.ssd_gate_scan_bwd.restype = ctypes.c_int
+    lib.ssd_gate_scan_step.argtypes = [i64, i32, i32, i64, i64] + [vp] * 6
+    lib.ssd_gate_scan_step.restype = ctypes.c_int
     return lib
 
 

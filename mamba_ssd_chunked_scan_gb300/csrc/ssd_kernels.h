@@ -164,6 +164,53 @@ struct AddNormBwdArgs {
     int rows_per_cta;
 };
 
+// Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of kScanTok tokens x
+// kScanCh channels; a state is handed over once per kScanBlock tiles of a sequence.
+constexpr int kScanTok = 128, kScanCh = 64, kScanBlock = 16;
+struct GateScanArgs {
+    int64_t batch, seqlen;
+    int width;
+    int dtype;
+    int64_t g_stride, x_stride;   // elements between tokens of g, dg and of x, dx
+    int ndocs;
+    const void* g;
+    const void* x;
+    const float* init;
+    const int32_t* cu;
+    void* y;               // forward: written; backward: the forward's output
+    float* fin;
+    const void* dy;
+    const float* dfin;
+    void* dg;
+    void* dx;
+    float* dinit;
+    // set at the launch
+    WsHeader* ws;
+    uint32_t* ticket;
+    uint32_t* map_flag;
+    uint32_t* carry_flag;
+    float4* maps;
+    float2* carry;
+    int64_t nchunks;       // tiles along a sequence
+    int ngroups;           // channel groups
+};
+struct GateScanLayout {    // workspace, in bytes
+    int64_t nchunks;
+    int ngroups;
+    size_t ticket_off, map_flag_off, carry_flag_off, clear_bytes, maps_off, carry_off, total;
+};
+struct GateStepArgs {
+    int64_t batch;
+    int width;
+    int dtype;
+    int64_t g_stride, x_stride;
+    const void* g;
+    const void* x;
+    const float* state_in;
+    float* state_out;
+    void* y;
+};
+
 // Constants of division by an invariant divisor d >= 1 through one high
 // multiply and a shift (Granlund and Montgomery, "Division by Invariant
 // Integers using Multiplication", 1994): l = ceil(log2 d),
@@ -201,6 +248,9 @@ cudaError_t launch_gate_norm(const GateNormArgs& a, cudaStream_t st);
 cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
 int64_t add_norm_bwd_shares(int64_t rows, int width);   // row slots of the backward
 cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
+GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width);
+cudaError_t launch_gate_scan(const GateScanArgs& a, void* workspace, bool bwd, cudaStream_t st);
+cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st);
 size_t bwd_smem_bytes(int Qb, int P, int N);
 int bwd_chunk(int P, int N, size_t smem_limit);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t st);

@@ -1,4 +1,4 @@
-"""The operators around the scan: residual RMS norm.
+"""The operators around the scan: residual RMS norm, gated recurrence.
 
 Thin wrappers over the C ABI like the package's other entry points: they check
 tensors, take device pointers and the stream, and call the library.  Outputs
@@ -7,6 +7,7 @@ and workspaces are allocated on the stream that the call runs on.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
@@ -144,3 +145,131 @@ def add_norm_bwd(dout, h, weight, rstd, dresidual=None, *, stream=None):
                                      dweight.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev))
     _check(rc, "ssd_add_norm_bwd")
     return {"dx": dx, "dresidual": dx if dres is None else dres, "dweight": dweight}
+
+
+def _token_stride(name, t, dtype, shape, dev):
+    """Elements between the tokens of a (..., width) tensor whose rows may be column ranges of a wider
+    matrix: the channels lie together and the leading dimensions are packed."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise _wrong(name, t, dtype, shape, dev)
+    if t.is_contiguous():
+        return shape[-1]
+    st = t.stride()
+    step = st[-2]
+    ok = (st[-1] == 1 or shape[-1] == 1) and step >= shape[-1]
+    for k in range(len(shape) - 2):
+        ok = ok and (shape[k] == 1 or st[k] == step * shape[-2] if k == len(shape) - 3 else shape[k] == 1)
+    if not ok:
+        raise ValueError(f"{name}: expected channels together and tokens at one stride, got strides {st} for {tuple(shape)}")
+    return step
+
+
+def _scan_args(g, x, initial_states, cu_seqlens):
+    dev = _device("g", g)
+    dtype, shape = g.dtype, g.shape
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"g must be bf16 or fp32, got {dtype}")
+    if len(shape) != 3:
+        raise ValueError(f"g: expected (batch, seqlen, width), got {tuple(shape)}")
+    batch, seqlen, width = shape
+    ndocs = 0
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or \
+                cu_seqlens.get_device() != dev or not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens: expected int32 (ndocs + 1) on the device")
+        ndocs = cu_seqlens.numel() - 1
+    p = _lib.GateScanParams(batch, seqlen, _token_stride("g", g, dtype, shape, dev), _token_stride("x", x, dtype, shape, dev),
+                            width, ndocs, _CODE[dtype])
+    states = (ndocs or batch, width)
+    if initial_states is not None:
+        _need("initial_states", initial_states, _F32, states, dev)
+    nbytes = _lib_c.ssd_gate_scan_workspace_size(ctypes.byref(p))
+    if nbytes == 0:
+        raise _lib.SSDError(1, f"gate scan of {tuple(shape)} with {ndocs} documents")
+    return dev, p, states, nbytes
+
+
+def gate_scan(g, x, initial_states=None, cu_seqlens=None, *, return_final_states=False, check_status=False, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(g), one decay per channel and token.
+
+    g, x (batch, seqlen, width) bf16 or fp32, contiguous or column ranges of a
+    wider matrix; initial_states (batch or ndocs, width) fp32 or None;
+    cu_seqlens (ndocs + 1) int32 or None (batch 1).  Returns y (g's type), or
+    (y, final_states) when asked.  With check_status, also synchronises the stream and raises if the
+    device recorded an error (offsets that are not increasing from 0 to seqlen)."""
+    dev, p, states, nbytes = _scan_args(g, x, initial_states, cu_seqlens)
+    with _on(dev, stream):
+        y = torch.empty(g.shape, dtype=g.dtype, device=g.device)
+        fin = torch.empty(states, dtype=_F32, device=g.device) if return_final_states else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
+        st = _raw_stream(dev)
+        _check(_lib_c.ssd_gate_scan(ctypes.byref(p), g.data_ptr(), x.data_ptr(), _ptr(initial_states), _ptr(cu_seqlens),
+                                    y.data_ptr(), _ptr(fin), ws.data_ptr(), nbytes, st), "ssd_gate_scan")
+        if check_status:
+            _check(_lib_c.ssd_check_status(ws.data_ptr(), st), "ssd_gate_scan device status")
+    return (y, fin) if return_final_states else y
+
+
+def gate_scan_bwd(g, x, y, dy, initial_states=None, dfinal_states=None, cu_seqlens=None, *, want_dinit=None, dg=None,
+                  dx=None, check_status=False, stream=None):
+    """Gradients of <dy, y> + <dfinal_states, final_states> of one gate_scan call, whose output was y.
+
+    dg and dx may be given to be written in place: of g's and x's shapes and token strides (column ranges of a
+    projection's gradient, say); by default they are allocated, as ranges of one matrix where g and x are strided.
+    Returns a dict with dg, dx and dinit (None unless want_dinit; by default with initial_states)."""
+    dev, p, states, nbytes = _scan_args(g, x, initial_states, cu_seqlens)
+    dtype, shape = g.dtype, g.shape
+    _need("y", y, dtype, shape, dev)
+    _need("dy", dy, dtype, shape, dev)
+    if dfinal_states is not None:
+        _need("dfinal_states", dfinal_states, _F32, states, dev)
+    if want_dinit is None:
+        want_dinit = initial_states is not None
+    for name, t, step in (("dg", dg, p.g_stride), ("dx", dx, p.x_stride)):
+        if t is not None and _token_stride(name, t, dtype, shape, dev) != step:
+            raise ValueError(f"{name}: expected the token stride of {name[1:]}, {step}")
+    with _on(dev, stream):
+        if dg is None:
+            dg = _like_rows(g, p.g_stride)
+        if dx is None:
+            dx = _like_rows(x, p.x_stride)
+        dinit = torch.empty(states, dtype=_F32, device=g.device) if want_dinit else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
+        st = _raw_stream(dev)
+        _check(_lib_c.ssd_gate_scan_bwd(ctypes.byref(p), g.data_ptr(), x.data_ptr(), y.data_ptr(), _ptr(initial_states),
+                                        _ptr(cu_seqlens), dy.data_ptr(), _ptr(dfinal_states), dg.data_ptr(), dx.data_ptr(),
+                                        _ptr(dinit), ws.data_ptr(), nbytes, st), "ssd_gate_scan_bwd")
+        if check_status:
+            _check(_lib_c.ssd_check_status(ws.data_ptr(), st), "ssd_gate_scan_bwd device status")
+    return {"dg": dg, "dx": dx, "dinit": dinit}
+
+
+def _like_rows(t, step):
+    """An uninitialised tensor of t's shape with `step` elements between tokens."""
+    if step == t.shape[-1]:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty(*t.shape[:-1], step, dtype=t.dtype, device=t.device)[..., : t.shape[-1]]
+
+
+def gate_scan_step(state, g, x, *, state_out=None, stream=None):
+    """One token per row of the gated recurrence: state (batch, width) fp32 is
+    updated in place unless state_out is given; g, x (batch, width) bf16 or
+    fp32 (rows may be column ranges).  Returns y (batch, width) in g's type."""
+    dev = _device("g", g)
+    dtype, shape = g.dtype, g.shape
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"g must be bf16 or fp32, got {dtype}")
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"g: expected (batch, width), got {tuple(shape)}")
+    gs, xs = _token_stride("g", g, dtype, shape, dev), _token_stride("x", x, dtype, shape, dev)
+    _need("state", state, _F32, shape, dev)
+    if state_out is None:
+        state_out = state
+    else:
+        _need("state_out", state_out, _F32, shape, dev)
+    with _on(dev, stream):
+        y = torch.empty(shape, dtype=dtype, device=g.device)
+        rc = _lib_c.ssd_gate_scan_step(shape[0], shape[1], _CODE[dtype], gs, xs, g.data_ptr(), x.data_ptr(),
+                                       state.data_ptr(), state_out.data_ptr(), y.data_ptr(), _raw_stream(dev))
+    _check(rc, "ssd_gate_scan_step")
+    return y

@@ -59,3 +59,75 @@ def test_nothing_to_do(L):
     assert L.ssd_add_norm_bwd_workspace_size(16, 0) == 0
     assert L.ssd_add_norm_bwd_workspace_size(16, 20000) == 0
     assert L.ssd_add_norm_bwd_workspace_size(16, 256) == 16 * 256 * 4
+
+
+def scan_params(**kw):
+    from mamba_ssd_chunked_scan_gb300 import _lib
+    d = dict(batch=2, seqlen=1000, g_stride=256, x_stride=256, width=128, ndocs=0, dtype=1)
+    d.update(kw)
+    return _lib.GateScanParams(*d.values())
+
+
+SCAN_PARAMS = [
+    (dict(batch=0), 1), (dict(seqlen=0), 1), (dict(width=0), 1), (dict(g_stride=127), 1), (dict(x_stride=0), 1),
+    (dict(dtype=2), 1), (dict(ndocs=-1), 1), (dict(ndocs=2), 1), (dict(seqlen=1 << 31), 2), (dict(batch=1 << 31), 2),
+    (dict(g_stride=1 << 31), 2), (dict(batch=1 << 20, seqlen=1 << 20, width=4096, g_stride=4096, x_stride=4096), 2),
+]
+
+
+@pytest.mark.parametrize("kw,code", SCAN_PARAMS)
+def test_gate_scan_parameters(L, kw, code):
+    p = scan_params(**kw)
+    assert L.ssd_gate_scan_workspace_size(p) == 0
+    assert L.ssd_gate_scan(p, G, 2 * G, None, None, 3 * G, None, 4 * G, 1 << 28, None) == code
+    assert L.ssd_gate_scan_bwd(p, G, 2 * G, 3 * G, None, None, 4 * G, None, 5 * G, 6 * G, None, 7 * G, 1 << 28, None) == code
+
+
+def scan(L, p=None, **kw):
+    d = dict(g=G, x=G + 256, init=2 * G, cu=None, y=3 * G, fin=4 * G, ws=5 * G, wsb=1 << 28, stream=None)
+    d.update(kw)
+    return L.ssd_gate_scan(p or scan_params(), *d.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(g=None), 1), (dict(x=None), 1), (dict(y=None), 1), (dict(cu=6 * G), 1), (dict(g=G + 1), 1), (dict(fin=4 * G + 2), 1),
+    (dict(ws=None), 3), (dict(wsb=100), 3), (dict(ws=5 * G + 16), 3), (dict(y=G), 1), (dict(y=G + 256), 1), (dict(fin=2 * G), 1),
+    (dict(fin=3 * G + 64), 1), (dict(y=5 * G + 64), 1), (dict(fin=2 * G + 512), 1),
+])
+def test_gate_scan_refusals(L, kw, code):
+    assert scan(L, **kw) == code
+
+
+def test_gate_scan_refuses_documents_without_offsets(L):
+    assert scan(L, scan_params(batch=1, ndocs=3)) == 1
+
+
+def scan_bwd(L, **kw):
+    # dg and dx: the two halves of one matrix
+    d = dict(g=G, x=G + 256, y=2 * G, init=3 * G, cu=None, dy=4 * G, dfin=5 * G, dg=6 * G, dx=6 * G + 256, dinit=7 * G, ws=8 * G,
+             wsb=1 << 28, stream=None)
+    d.update(kw)
+    return L.ssd_gate_scan_bwd(scan_params(), *d.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dy=None), 1), (dict(y=None), 1), (dict(dg=None), 1), (dict(dx=None), 1), (dict(dx=6 * G + 128), 1), (dict(dx=6 * G + 384), 1),
+    (dict(dg=G), 1), (dict(dx=4 * G), 1), (dict(dinit=5 * G), 1), (dict(ws=8 * G + 8), 3), (dict(wsb=0), 3), (dict(dinit=8 * G), 1),
+])
+def test_gate_scan_bwd_refusals(L, kw, code):
+    assert scan_bwd(L, **kw) == code
+
+
+def step(L, **kw):
+    d = dict(batch=4, width=128, dtype=1, gs=256, xs=256, g=G, x=G + 256, si=2 * G, so=2 * G, y=3 * G, stream=None)
+    d.update(kw)
+    return L.ssd_gate_scan_step(*d.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), 1), (dict(width=0), 1), (dict(dtype=2), 1), (dict(gs=100), 1), (dict(g=None), 1), (dict(y=None), 1),
+    (dict(si=None), 1), (dict(so=2 * G + 4), 1), (dict(y=2 * G), 1), (dict(y=G), 1), (dict(so=G), 1), (dict(x=G + 257), 1),
+    (dict(batch=1 << 36), 2), (dict(batch=0), 0),
+])
+def test_gate_scan_step_refusals(L, kw, code):
+    assert step(L, **kw) == code
