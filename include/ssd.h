@@ -309,6 +309,58 @@ SSD_API int ssd_add_norm_bwd(int64_t rows, int32_t width, int32_t dtype, int32_t
              const void* dout, const void* h, const float* weight, const float* rstd, const void* dresidual_out,
              void* dx, void* dresidual, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Matrix product with its epilogue, for the projections before and after the scan:
+ *
+ *     v[m,n] = sx[m] sw[n] sum_k x[m,k] w[n,k] + bias[n]       (the scales with SSD_E4M3 only)
+ *     y[m,n] = act(v[m,n]) + residual[m,n]
+ *
+ * silu(v) = v / (1 + exp(-v));  gelu(v) = v / 2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))). */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2 } ssd_act_t;
+typedef struct {
+    int64_t m;      /* rows of x and y (0: nothing is launched)                                        */
+    int64_t ldx;    /* elements from one row of x to the next, >= k (x may be a column range)          */
+    int32_t n;      /* columns of y, rows of w                                                         */
+    int32_t k;      /* columns of x and w                                                              */
+    int32_t dtype;  /* of x and w: SSD_BF16, or SSD_E4M3 with scales                                   */
+    int32_t act;    /* ssd_act_t                                                                       */
+} ssd_linear_params_t;
+
+/* Bytes of device workspace for ssd_linear() and ssd_linear_bwd(); 0 on invalid parameters (bwd: also
+ * unless dtype is SSD_BF16). */
+SSD_API size_t ssd_linear_workspace_size(const ssd_linear_params_t* p);
+SSD_API size_t ssd_linear_bwd_workspace_size(const ssd_linear_params_t* p);
+
+/* y (and optionally v, for the backward pass) as defined above.
+ *   x         (m, k) dtype, row stride ldx;  w (n, k) dtype, contiguous; both 16-byte aligned, with rows of
+ *             whole 16-byte units: k and ldx multiples of 8 (bf16) or 16 (e4m3), else SSD_ERR_UNSUPPORTED
+ *   x_scales  (m) fp32, w_scales (n) fp32: both with SSD_E4M3, both NULL otherwise
+ *   bias      (n) fp32, or NULL
+ *   residual  (m, n) bf16, contiguous, or NULL; may be y (in place)
+ *   y         (m, n) bf16, contiguous
+ *   pre       (m, n) bf16, or NULL: v, rounded
+ * Sums are fp32 and y is rounded once.  `workspace`: ssd_linear_workspace_size(p) bytes, 256-byte
+ * aligned; needs no initialisation; calls that share it must be ordered on one stream.  One launch, or two where
+ * the contraction is split over CTAs.  The device waits are bounded: one that runs out records
+ * SSD_ERR_TIMEOUT (where 61-65: stage free, stage loaded, accumulator free, accumulator done, drain) in the status word,
+ * which each call clears, read by ssd_check_status().  Bitwise deterministic. */
+SSD_API int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* w, const float* x_scales,
+             const float* w_scales, const float* bias, const void* residual, void* y, void* pre,
+             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of <dy, y> of ssd_linear() (dtype SSD_BF16):
+ *
+ *     dpre = dy * act'(pre);   dx = dpre w;   dw = dpre^T x;   dbias = sum_m dpre
+ *
+ * (the residual's gradient is dy itself.)  With an activation, or where n is not a multiple of 8, dpre is rounded
+ * to bf16 in the workspace as the products' operand; dbias sums the unrounded values.
+ *   x, w    as for the forward;   dy (m, n) bf16, contiguous, 16-byte aligned
+ *   pre     (m, n) bf16: the forward's; NULL with SSD_ACT_NONE
+ *   dx      (m, k) bf16, contiguous, or NULL;  dw (n, k) bf16, or NULL;  dbias (n) fp32, or NULL
+ * m == 0 writes zeros to dw and dbias.  No output may overlap an input.  Workspace, errors and
+ * determinism as for ssd_linear(), with ssd_linear_bwd_workspace_size(p). */
+SSD_API int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, const void* pre, const void* dy,
+             void* dx, void* dw, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Gated linear recurrence: one decay per channel and token (the scan above has one per head and token).
  * Per row b, token t and channel d, with gate logits g and inputs x,
  *

@@ -17,7 +17,7 @@ import torch
 SSD_F32, SSD_BF16, SSD_E4M3 = 0, 1, 2
 
 # the operators around the scan (layer.py), loaded with the library on first use
-_LAYER = ("add_norm", "add_norm_bwd", "gate_scan", "gate_scan_bwd", "gate_scan_step")
+_LAYER = ("add_norm", "add_norm_bwd", "gate_scan", "gate_scan_bwd", "gate_scan_step", "linear", "linear_bwd")
 
 
 class _LazyLib:

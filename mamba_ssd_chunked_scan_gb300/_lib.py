@@ -22,7 +22,8 @@ EXPORTS = ("ssd_fwd_workspace_size", "ssd_workspace_init", "ssd_fwd", "ssd_check
            "ssd_bwd_workspace_size", "ssd_bwd_workspace_size_doc_states", "ssd_bwd", "ssd_fwd_timed",
            "ssd_gate_norm", "ssd_check_status_where", "ssd_fwd_fault_inject", "ssd_add_norm",
            "ssd_add_norm_bwd_workspace_size", "ssd_add_norm_bwd", "ssd_gate_scan_workspace_size", "ssd_gate_scan",
-           "ssd_gate_scan_bwd", "ssd_gate_scan_step")
+           "ssd_gate_scan_bwd", "ssd_gate_scan_step", "ssd_linear_workspace_size", "ssd_linear_bwd_workspace_size",
+           "ssd_linear", "ssd_linear_bwd")
 
 
 class SSDParams(ctypes.Structure):
@@ -36,6 +37,11 @@ class GateScanParams(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("g_stride", ctypes.c_int64),
                 ("x_stride", ctypes.c_int64), ("width", ctypes.c_int32), ("ndocs", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class LinearParams(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("ldx", ctypes.c_int64), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 class SSDError(RuntimeError):
@@ -100,6 +106,14 @@ def _load():
     lib.ssd_gate_scan_bwd.restype = ctypes.c_int
     lib.ssd_gate_scan_step.argtypes = [i64, i32, i32, i64, i64] + [vp] * 6
     lib.ssd_gate_scan_step.restype = ctypes.c_int
+    N = ctypes.POINTER(LinearParams)
+    for fn in (lib.ssd_linear_workspace_size, lib.ssd_linear_bwd_workspace_size):
+        fn.argtypes = [N]
+        fn.restype = sz
+    lib.ssd_linear.argtypes = [N] + [vp] * 9 + [sz, vp]
+    lib.ssd_linear.restype = ctypes.c_int
+    lib.ssd_linear_bwd.argtypes = [N] + [vp] * 8 + [sz, vp]
+    lib.ssd_linear_bwd.restype = ctypes.c_int
     return lib
 
 

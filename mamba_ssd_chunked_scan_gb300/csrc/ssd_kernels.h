@@ -1,6 +1,7 @@
 // Host-side declarations shared by the libssd CUDA sources.
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -211,6 +212,50 @@ struct GateStepArgs {
     void* y;
 };
 
+// Matrix product with its epilogue (ssd_linear, ssd_linear_bwd): D = X W^T.
+constexpr int kLinearSwap = 64;       // up to this many rows of x the product is computed transposed
+constexpr int kLinearSMs = 152;       // SMs the plan (and so the workspace) is made for
+constexpr int kLinearMaxSplits = 16;
+struct LinearOperand {
+    const void* p;
+    int64_t ld;            // elements between its rows in memory
+    bool along_rows;       // the contraction runs along its rows (the operand is stored transposed; bf16)
+};
+struct LinearArgs {
+    int64_t m;             // rows of D
+    int n;                 // columns of D
+    int64_t k;             // contraction
+    int dtype;             // of the operands: SSD_BF16 or SSD_E4M3
+    int act;               // ssd_act_t
+    LinearOperand x, w;
+    const float* x_scales; // [m], or NULL
+    const float* w_scales; // [n], or NULL
+    const float* bias;     // [n], or NULL
+    const void* residual;  // (m, n) bf16, or NULL
+    void* y;               // (m, n) bf16
+    void* pre;             // (m, n) bf16, or NULL
+    float* parts;          // [splits * m * n]
+    WsHeader* ws;
+    int keep_status;       // the status word was cleared by the call already
+    int swap, vec;         // set at the launch
+};
+struct LinearPlan {
+    int tile_n, splits;
+    bool swap;
+    size_t parts_bytes;
+};
+struct LinearDpreArgs {
+    int64_t m;
+    int n;
+    int act;
+    int64_t ldp;
+    const void* dy;
+    const void* pre;       // or NULL (no activation)
+    void* dpre;            // (m, ldp) bf16, or NULL
+    float* shares;         // [slabs * n], or NULL
+    float* dbias;          // [n], or NULL
+};
+
 // Constants of division by an invariant divisor d >= 1 through one high
 // multiply and a shift (Granlund and Montgomery, "Division by Invariant
 // Integers using Multiplication", 1994): l = ceil(log2 d),
@@ -251,6 +296,11 @@ cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
 GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width);
 cudaError_t launch_gate_scan(const GateScanArgs& a, void* workspace, bool bwd, cudaStream_t st);
 cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st);
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // NULL when the driver has none
+LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap);
+cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& plan, cudaStream_t st);
+int64_t linear_dpre_slabs(int64_t m);
+cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st);
 size_t bwd_smem_bytes(int Qb, int P, int N);
 int bwd_chunk(int P, int N, size_t smem_limit);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t st);

@@ -1,4 +1,4 @@
-// C ABI of the operators around the scan (residual norm, gated recurrence):
+// C ABI of the operators around the scan (residual norm, projection, gated recurrence):
 // argument checks and dispatch.  Nothing here allocates device memory; every launch is asynchronous
 // on the caller's stream.
 #include "ssd_common.cuh"
@@ -64,6 +64,42 @@ int check_scan(const ssd_gate_scan_params_t* p) {
     const int64_t tiles = ((p->seqlen + kScanTok - 1) / kScanTok) * ((p->width + kScanCh - 1) / kScanCh);
     if (tiles >= big / p->batch) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
+}
+
+int check_linear(const ssd_linear_params_t* p) {
+    if (!p) return SSD_ERR_INVALID_ARG;
+    if (p->m < 0 || p->n < 1 || p->k < 1 || p->ldx < p->k) return SSD_ERR_INVALID_ARG;
+    if (p->dtype != SSD_BF16 && p->dtype != SSD_E4M3) return SSD_ERR_INVALID_ARG;
+    if (p->act != SSD_ACT_NONE && p->act != SSD_ACT_SILU && p->act != SSD_ACT_GELU) return SSD_ERR_INVALID_ARG;
+    const int unit = p->dtype == SSD_BF16 ? 8 : 16;   // elements per 16 bytes
+    if (p->k % unit != 0 || p->ldx % unit != 0) return SSD_ERR_UNSUPPORTED;
+    // tile numbers (parts of the contraction among them) and tile coordinates are 32-bit
+    const int64_t big = (int64_t)1 << 30;
+    if (p->m >= big || p->n >= big || p->k >= big || p->ldx >= big) return SSD_ERR_UNSUPPORTED;
+    const int64_t tm = p->m / 64 + 1, tn = p->n / 64 + 1, tk = p->k / 64 + 1;
+    if (tm > big / kLinearMaxSplits / tn || tm > big / kLinearMaxSplits / tk || tn > big / kLinearMaxSplits / tk) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Workspace of the projection's backward, in bytes from its start: the status word, dpre
+// where it is not dy itself, the slabs' shares of dbias, and the parts of whichever product runs.
+struct LinearBwdLayout {
+    bool own_dpre;
+    int64_t ldp;
+    size_t dpre_off, shares_off, parts_off, total;
+    LinearPlan dx, dw;
+};
+LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p) {
+    LinearBwdLayout l;
+    l.own_dpre = p->act != SSD_ACT_NONE || p->n % 8 != 0;
+    l.ldp = (p->n + 7) / 8 * 8;
+    l.dpre_off = sizeof(WsHeader);
+    l.shares_off = l.dpre_off + (l.own_dpre ? align_up((size_t)p->m * l.ldp * 2, 256) : 0);
+    l.parts_off = l.shares_off + align_up((size_t)linear_dpre_slabs(p->m) * p->n * 4, 256);
+    l.dx = linear_plan(p->m, p->k, (int64_t)p->n * 2, false);
+    l.dw = linear_plan(p->n, p->k, p->m * 2, false);
+    l.total = l.parts_off + (l.dx.parts_bytes > l.dw.parts_bytes ? l.dx.parts_bytes : l.dw.parts_bytes);
+    return l;
 }
 
 }  // namespace
@@ -232,6 +268,106 @@ int ssd_gate_scan_step(int64_t batch, int32_t width, int32_t dtype, int64_t g_st
     a.batch = batch; a.width = width; a.dtype = dtype; a.g_stride = g_stride; a.x_stride = x_stride;
     a.g = g; a.x = x; a.state_in = state_in; a.state_out = state_out; a.y = y;
     return launch_gate_scan_step(a, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+size_t ssd_linear_workspace_size(const ssd_linear_params_t* p) {
+    if (check_linear(p) != SSD_OK) return 0;
+    if (p->m == 0) return sizeof(WsHeader);
+    return sizeof(WsHeader) + linear_plan(p->m, p->n, (int64_t)p->k * elem(p->dtype), true).parts_bytes;
+}
+
+size_t ssd_linear_bwd_workspace_size(const ssd_linear_params_t* p) {
+    if (check_linear(p) != SSD_OK || p->dtype != SSD_BF16) return 0;
+    return p->m == 0 ? sizeof(WsHeader) : linear_bwd_layout(p).total;
+}
+
+int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* w, const float* x_scales, const float* w_scales,
+               const float* bias, const void* residual, void* y, void* pre, void* workspace, size_t workspace_bytes,
+               void* stream) {
+    const int rc = check_linear(p);
+    if (rc != SSD_OK) return rc;
+    const bool e4m3 = p->dtype == SSD_E4M3;
+    if (e4m3 != (w_scales != nullptr) || (!e4m3 && x_scales) || (e4m3 && !x_scales && p->m > 0)) return SSD_ERR_INVALID_ARG;
+    if (p->m == 0) return SSD_OK;
+    if (!x || !w || !y) return SSD_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(bias, 4) ||
+        !aligned(residual, 2) || !aligned(y, 2) || !aligned(pre, 2))
+        return SSD_ERR_INVALID_ARG;
+    const size_t es = elem(p->dtype);
+    const LinearPlan plan = linear_plan(p->m, p->n, (int64_t)p->k * es, true);
+    const size_t need = sizeof(WsHeader) + plan.parts_bytes;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
+    const Mat in[] = {{x, p->m, p->k, p->ldx, es}, {w, p->n, p->k, p->k, es}, {x_scales, 1, p->m, p->m, 4},
+                      {w_scales, 1, p->n, p->n, 4}, {bias, 1, p->n, p->n, 4}};
+    const Mat my = {y, p->m, p->n, p->n, 2}, mp = {pre, p->m, p->n, p->n, 2}, mr = {residual, p->m, p->n, p->n, 2},
+              mw = {workspace, 1, (int64_t)need, (int64_t)need, 1};
+    for (const Mat& m : in)
+        if (touch(my, m) || touch(mp, m) || touch(mw, m)) return SSD_ERR_INVALID_ARG;
+    if (touch(my, mp) || touch(mp, mr) || touch(mw, my) || touch(mw, mp) || touch(mw, mr) ||
+        (y != residual && touch(my, mr)))
+        return SSD_ERR_INVALID_ARG;
+    LinearArgs a = {};
+    a.m = p->m; a.n = p->n; a.k = p->k; a.dtype = p->dtype; a.act = p->act;
+    a.x = {x, p->ldx, false};
+    a.w = {w, p->k, false};
+    a.x_scales = x_scales; a.w_scales = w_scales; a.bias = bias; a.residual = residual; a.y = y; a.pre = pre;
+    a.ws = (WsHeader*)workspace;
+    a.parts = (float*)((char*)workspace + sizeof(WsHeader));
+    return launch_linear(a, plan, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, const void* pre, const void* dy, void* dx,
+                   void* dw, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_linear(p);
+    if (rc != SSD_OK) return rc;
+    if (p->dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (!aligned(dw, 2) || !aligned(dbias, 4) || !aligned(dx, 2)) return SSD_ERR_INVALID_ARG;
+    if (p->m == 0) {
+        if (dw && cudaMemsetAsync(dw, 0, (size_t)p->n * p->k * 2, st) != cudaSuccess) return SSD_ERR_CUDA;
+        if (dbias && cudaMemsetAsync(dbias, 0, (size_t)p->n * 4, st) != cudaSuccess) return SSD_ERR_CUDA;
+        return SSD_OK;
+    }
+    if (!x || !w || !dy || (!dx && !dw && !dbias) || (p->act != SSD_ACT_NONE) != (pre != nullptr)) return SSD_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(dy, 16) || !aligned(pre, 2)) return SSD_ERR_INVALID_ARG;
+    const LinearBwdLayout l = linear_bwd_layout(p);
+    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
+    const Mat in[] = {{x, p->m, p->k, p->ldx, 2}, {w, p->n, p->k, p->k, 2}, {pre, p->m, p->n, p->n, 2}, {dy, p->m, p->n, p->n, 2}};
+    const Mat out[] = {{dx, p->m, p->k, p->k, 2}, {dw, p->n, p->k, p->k, 2}, {dbias, 1, p->n, p->n, 4},
+                       {workspace, 1, (int64_t)l.total, (int64_t)l.total, 1}};
+    for (int i = 0; i < 4; ++i) {
+        for (const Mat& m : in)
+            if (touch(out[i], m)) return SSD_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (touch(out[i], out[j])) return SSD_ERR_INVALID_ARG;
+    }
+    char* ws = (char*)workspace;
+    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return SSD_ERR_CUDA;
+    LinearDpreArgs d = {};
+    d.m = p->m; d.n = p->n; d.act = p->act; d.ldp = l.ldp; d.dy = dy; d.pre = pre;
+    d.dpre = l.own_dpre && (dx || dw) ? ws + l.dpre_off : nullptr;
+    d.shares = dbias ? (float*)(ws + l.shares_off) : nullptr;
+    d.dbias = dbias;
+    if ((d.dpre || dbias) && launch_linear_dpre(d, st) != cudaSuccess) return SSD_ERR_CUDA;
+    const LinearOperand g = {l.own_dpre ? (const void*)(ws + l.dpre_off) : dy, l.own_dpre ? l.ldp : p->n, false};
+    LinearArgs a = {};
+    a.dtype = SSD_BF16; a.act = SSD_ACT_NONE;
+    a.ws = (WsHeader*)workspace;
+    a.parts = (float*)(ws + l.parts_off);
+    a.keep_status = 1;
+    if (dx) {   // (m, k) = dpre (m, n) w (n, k): w's contraction runs along its rows
+        a.m = p->m; a.n = p->k; a.k = p->n; a.y = dx;
+        a.x = g;
+        a.w = {w, p->k, true};
+        if (launch_linear(a, l.dx, st) != cudaSuccess) return SSD_ERR_CUDA;
+    }
+    if (dw) {   // (n, k) = dpre^T (n, m) x (m, k): both contractions run along the rows
+        a.m = p->n; a.n = p->k; a.k = p->m; a.y = dw;
+        a.x = {g.p, g.ld, true};
+        a.w = {x, p->ldx, true};
+        if (launch_linear(a, l.dw, st) != cudaSuccess) return SSD_ERR_CUDA;
+    }
+    return SSD_OK;
 }
 
 }  // extern "C"

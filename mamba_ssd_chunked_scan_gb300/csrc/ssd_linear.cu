@@ -1,0 +1,551 @@
+// Matrix product with bias, activation and residual in its epilogue, and its gradients:
+//   ssd_linear_tc       D = A B^T over 128 x TN tiles on the tensor cores (tcgen05), the epilogue on
+//                       the accumulator as it leaves tensor memory
+//   ssd_linear_join     the sum of a split contraction's parts, then the same epilogue
+//   ssd_linear_dpre     dy act'(pre) (rounded to bf16, the gradients' operand) and the shares of dbias
+//   ssd_linear_dbias    dbias from the shares, in a fixed order
+//
+// One persistent CTA per SM walks tiles (or tiles' parts along the contraction): one thread loads
+// 128-byte-wide operand tiles by TMA into a ring of stages, one issues the MMAs, four warps run the
+// epilogue of the previous tile from the other half of tensor memory meanwhile.
+// Operands are bf16 or e4m3; a bf16 operand may also be stored with its contraction along the rows
+// (dx = dpre W reads W so, dw = dpre^T x both), which the shared-memory descriptors express: no
+// operand is ever transposed in memory.
+//
+// Up to 64 rows of x (decoding) the product is computed transposed, D^T = W x^T: W's rows
+// fill the 128 rows of a tile and x is the narrow operand, so the MMAs and the loads are W's
+// and almost nothing is padding; its bound is W's one pass from HBM.
+//
+// Sums are fp32 in tensor memory.  Products whose tiles would leave SMs idle are split along
+// the contraction into parts summed in a fixed order (ssd_linear_join), so results are deterministic.
+#include <string.h>
+
+#include <atomic>
+
+#include "ssd_common.cuh"
+#include "ssd_kernels.h"
+#include "ssd_vec.cuh"
+#include "tc_ptx.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 256;          // warp 0 loads, 1 MMAs, 2 tensor memory, 4-7 epilogue
+constexpr int kRowB = 128;             // bytes of the contraction per tile row and stage
+constexpr int kTileM = 128;
+constexpr uint32_t kWhereEmpty = 61, kWhereFull = 62, kWhereAccFree = 63, kWhereAcc = 64, kWhereDrain = 65;
+
+template <int TN>
+struct Cfg {
+    static constexpr uint32_t kA = kTileM * kRowB, kB = TN * kRowB, kStage = kA + kB;
+    static constexpr int kStages = TN >= 256 ? 4 : TN >= 128 ? 6 : TN >= 64 ? 8 : TN >= 32 ? 9 : 10;
+    static constexpr uint32_t kCols = 2 * TN < 32 ? 32 : 2 * TN;   // two accumulators
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage;
+};
+
+struct LinearParams {
+    CUtensorMap tm_a, tm_b;
+    LinearArgs a;
+    int tiles_r, tiles_c;   // tiles over D's rows and columns
+    int kblocks;            // 128-byte blocks of the contraction
+    int splits;             // parts of the contraction
+    int items;              // tiles_r * tiles_c * splits
+};
+
+struct Small {
+    uint64_t full[10], empty[10], acc[2], acc_free[2], done;
+    uint32_t tmem_base;
+    int abort, never;
+};
+
+__device__ __forceinline__ bool lin_wait(Small& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
+    if (ptx::mbar_wait(bar, parity, &sh.abort, kDefaultWaitIters)) return true;
+    if (!*(volatile int*)&sh.abort) {
+        record_error(ws, SSD_ERR_TIMEOUT, where);
+        *(volatile int*)&sh.abort = 1;
+    }
+    return false;
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, uint64_t* bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(tm), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B (both K-major), fp32 accumulator.
+constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// s(v) = 1 / (1 + exp(-v)) with the special-function unit's exponential and reciprocal
+// (relative error of a few 2^-22, far below the rounding of the bf16 results).
+__device__ __forceinline__ float sigmoid(float v) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-v * kLog2e));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+constexpr float kGeluC = 0.7978845608028654f, kGeluA = 0.044715f;   // sqrt(2 / pi)
+
+// silu(v) = v s(v);  gelu(v) = v (1 + tanh u) / 2 = v s(2u), u = sqrt(2/pi) (v + 0.044715 v^3)
+__device__ __forceinline__ float act_value(float v, int act) {
+    if (act == SSD_ACT_SILU) return v * sigmoid(v);
+    if (act == SSD_ACT_GELU) return v * sigmoid(2.f * kGeluC * (v + kGeluA * v * v * v));
+    return v;
+}
+__device__ __forceinline__ float act_slope(float v, int act) {
+    if (act == SSD_ACT_SILU) {
+        const float s = sigmoid(v);
+        return s * (1.f + v * (1.f - s));
+    }
+    if (act == SSD_ACT_GELU) {
+        const float s = sigmoid(2.f * kGeluC * (v + kGeluA * v * v * v));
+        return s + v * s * (1.f - s) * 2.f * kGeluC * (1.f + 3.f * kGeluA * v * v);
+    }
+    return 1.f;
+}
+
+// One element of y from its sum: scales, bias, activation, residual.
+__device__ __forceinline__ void finish(const LinearArgs& a, float v, int64_t m, int n) {
+    if (a.x_scales) v *= __ldg(a.x_scales + m) * __ldg(a.w_scales + n);
+    if (a.bias) v += __ldg(a.bias + n);
+    const size_t at = (size_t)m * a.n + n;
+    if (a.pre) static_cast<bf16_t*>(a.pre)[at] = __float2bfloat16_rn(v);
+    v = act_value(v, a.act);
+    if (a.residual) v += __bfloat162float(static_cast<const bf16_t*>(a.residual)[at]);
+    static_cast<bf16_t*>(a.y)[at] = __float2bfloat16_rn(v);
+}
+
+// Eight consecutive columns of one row (16-byte aligned rows of y).
+__device__ __forceinline__ void finish8(const LinearArgs& a, float (&v)[8], int64_t m, int n, float xs) {
+    if (a.x_scales) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= xs * __ldg(a.w_scales + n + k);
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += __ldg(a.bias + n + k);
+    }
+    const size_t at = (size_t)m * a.n + n;
+    Raw<bf16_t, 8> q;
+    if (a.pre) {
+        q.set(v);
+        *reinterpret_cast<uint4*>(static_cast<bf16_t*>(a.pre) + at) = q.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], a.act);
+    if (a.residual) {
+        float r[8];
+        q.load(static_cast<const bf16_t*>(a.residual) + at);
+        q.get(r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += r[k];
+    }
+    q.set(v);
+    *reinterpret_cast<uint4*>(static_cast<bf16_t*>(a.y) + at) = q.w;
+}
+
+// Tile (r, c) of the t-th tile: bands of kBand row tiles walk the columns together, so that the tiles in
+// flight share their operands in L2.
+constexpr int kBand = 16;
+__device__ __forceinline__ void tile_at(const LinearParams& p, int t, int& r, int& c) {
+    const int per = kBand * p.tiles_c;
+    const int band = t / per, in = t - band * per;
+    const int rows = p.tiles_r - band * kBand < kBand ? p.tiles_r - band * kBand : kBand;
+    c = in / rows;
+    r = band * kBand + in - c * rows;
+}
+
+// E4M3: 8-bit operands.  AMN / BMN: the operand's contraction runs along its rows in memory (bf16).
+template <int TN, bool E4M3, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_constant__ LinearParams p) {
+    using C = Cfg<TN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ Small sh;
+    const LinearArgs& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kElems = E4M3 ? 128 : 64;   // contraction elements per stage
+    if (threadIdx.x == 0) {
+        if (blockIdx.x == 0 && !a.keep_status) a.ws->status = 0;   // a wait gives up after seconds, long after this
+        for (int i = 0; i < C::kStages; ++i) {
+            ptx::mbar_init(&sh.full[i], 1);
+            ptx::mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.acc[i], 1);
+            ptx::mbar_init(&sh.acc_free[i], 4);
+        }
+        ptx::mbar_init(&sh.done, 1);
+        sh.abort = 0;
+        sh.never = 0;
+        ptx::mbar_fence_init();
+        ptx::prefetch_tmap(&p.tm_a);
+        ptx::prefetch_tmap(&p.tm_b);
+    }
+    if (warp == 2) ptx::tmem_alloc(&sh.tmem_base, C::kCols);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tb = sh.tmem_base;
+    const int per = (p.kblocks + p.splits - 1) / p.splits;   // contraction blocks per part
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ loads
+            uint32_t it = 0;
+            bool go = true;
+            for (int item = blockIdx.x; go && item < p.items; item += gridDim.x) {
+                const int s = item % p.splits;
+                int r, c;
+                tile_at(p, item / p.splits, r, c);
+                const int k1 = (s + 1) * per < p.kblocks ? (s + 1) * per : p.kblocks;
+                for (int kb = s * per; kb < k1; ++kb, ++it) {
+                    const int st = it % C::kStages;
+                    if (it >= (uint32_t)C::kStages &&
+                        !lin_wait(sh, a.ws, &sh.empty[st], ((it / C::kStages) - 1) & 1, kWhereEmpty)) {
+                        go = false;
+                        break;
+                    }
+                    uint8_t* dst = sm + st * C::kStage;
+                    ptx::mbar_expect_tx(&sh.full[st], C::kStage);
+                    if constexpr (AMN) {
+#pragma unroll
+                        for (int j = 0; j < kTileM / 64; ++j)
+                            tma_load_2d(dst + j * 8192, &p.tm_a, &sh.full[st], r * kTileM + 64 * j, kb * kElems);
+                    } else {
+                        tma_load_2d(dst, &p.tm_a, &sh.full[st], kb * kElems, r * kTileM);
+                    }
+                    if constexpr (BMN) {
+#pragma unroll
+                        for (int j = 0; j < TN / 64; ++j)
+                            tma_load_2d(dst + C::kA + j * 8192, &p.tm_b, &sh.full[st], c * TN + 64 * j, kb * kElems);
+                    } else {
+                        tma_load_2d(dst + C::kA, &p.tm_b, &sh.full[st], kb * kElems, c * TN);
+                    }
+                }
+            }
+            // every load that was issued has landed before the CTA may leave
+            for (uint32_t st = 0; st < (uint32_t)C::kStages && st < it; ++st) {
+                const uint32_t last = ((it - 1 - st) / C::kStages) * C::kStages + st;
+                if (!ptx::mbar_wait(&sh.full[st], (last / C::kStages) & 1, &sh.never, kDefaultWaitIters)) {
+                    record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
+                    *(volatile int*)&sh.abort = 1;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ MMAs
+            constexpr uint32_t id = E4M3 ? idesc_e4m3(kTileM, TN) : ptx::idesc_bf16(kTileM, TN, AMN, BMN);
+            uint32_t it = 0, tile = 0;
+            bool go = true;
+            for (int item = blockIdx.x; go && item < p.items; item += gridDim.x, ++tile) {
+                const int s = item % p.splits;
+                const int k0 = s * per, k1 = k0 + per < p.kblocks ? k0 + per : p.kblocks;
+                const uint32_t buf = tile & 1, d = tb + buf * TN;
+                if (tile >= 2 && !lin_wait(sh, a.ws, &sh.acc_free[buf], ((tile >> 1) - 1) & 1, kWhereAccFree)) break;
+                ptx::tc_fence_after();
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int st = it % C::kStages;
+                    if (!lin_wait(sh, a.ws, &sh.full[st], (it / C::kStages) & 1, kWhereFull)) {
+                        go = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t sa = ptx::smem_u32(sm + st * C::kStage), sb = sa + C::kA;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {   // 32 bytes of the contraction (or 16 of its rows) per MMA
+                        const uint64_t da = AMN ? ptx::sdesc_sw128(sa + k * 2048, 8192, 1024) : ptx::sdesc_sw128(sa + k * 32, 16, 1024);
+                        const uint64_t db = BMN ? ptx::sdesc_sw128(sb + k * 2048, 8192, 1024) : ptx::sdesc_sw128(sb + k * 32, 16, 1024);
+                        if constexpr (E4M3) mma_f8(d, da, db, id, kb > k0 || k > 0);
+                        else ptx::mma_ss(d, da, db, id, kb > k0 || k > 0);
+                    }
+                    ptx::mma_commit(&sh.empty[st]);
+                }
+                ptx::mma_commit(&sh.acc[buf]);
+            }
+            ptx::mma_commit(&sh.done);
+            if (!ptx::mbar_wait(&sh.done, 0, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------- epilogue
+        const int q = warp & 3;   // the warp's quarter of tensor memory's lanes
+        uint32_t tile = 0;
+        for (int item = blockIdx.x; item < p.items; item += gridDim.x, ++tile) {
+            const int s = item % p.splits;
+            int r, c;
+            tile_at(p, item / p.splits, r, c);
+            const uint32_t buf = tile & 1;
+            bool ok = true;
+            if (lane == 0) ok = lin_wait(sh, a.ws, &sh.acc[buf], (tile >> 1) & 1, kWhereAcc);
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t d = tb + buf * TN + ((uint32_t)(32 * q) << 16);
+            const int row = r * kTileM + 32 * q + lane;   // D's row of this thread
+            const bool row_ok = row < (a.swap ? a.n : a.m);
+            const int ncol = a.swap ? (int)a.m : a.n;
+            const float xs = (a.x_scales && !a.swap && row_ok) ? __ldg(a.x_scales + row) : 1.f;
+            constexpr int CW = TN < 32 ? TN : 32;   // columns per read of tensor memory
+#pragma unroll 1
+            for (int j = 0; j < TN; j += CW) {
+                __syncwarp();   // lanes past the last row or column skip the stores, not the load
+                uint32_t w[CW];
+                if constexpr (CW == 32) ptx::tmem_load32(d + j, w);
+                else ptx::tmem_load16(d + j, w);
+                if (j + CW >= TN) {   // the accumulator is in registers: the next tile may have it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sh.acc_free[buf]);
+                }
+                const int col = c * TN + j;
+                if (!row_ok || col >= ncol) continue;
+                if (p.splits > 1) {
+                    float* part = a.parts + (size_t)s * a.m * a.n;
+#pragma unroll
+                    for (int k = 0; k < CW; ++k)
+                        if (col + k < ncol) {
+                            if (a.swap) part[(size_t)(col + k) * a.n + row] = __uint_as_float(w[k]);
+                            else part[(size_t)row * a.n + col + k] = __uint_as_float(w[k]);
+                        }
+                } else if (a.swap) {
+#pragma unroll
+                    for (int k = 0; k < CW; ++k)
+                        if (col + k < ncol) finish(a, __uint_as_float(w[k]), col + k, row);
+                } else if (a.vec) {
+#pragma unroll
+                    for (int k = 0; k < CW; k += 8) {
+                        if (col + k >= ncol) break;   // whole vectors: n is a multiple of 8
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[k + e]);
+                        finish8(a, v, row, col + k, xs);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < CW; ++k)
+                        if (col + k < ncol) finish(a, __uint_as_float(w[k]), row, col + k);
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tb, C::kCols);
+    }
+}
+
+// y from the parts of a split contraction, added in their order.
+__global__ void __launch_bounds__(256) ssd_linear_join(LinearArgs a, int splits) {
+    const size_t total = (size_t)a.m * a.n;
+    const size_t k = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (k >= total) return;
+    float v = a.parts[k];
+    for (int s = 1; s < splits; ++s) v += a.parts[(size_t)s * total + k];
+    const int64_t m = (int64_t)(k / a.n);
+    finish(a, v, m, (int)(k - (size_t)m * a.n));
+}
+
+// dpre = dy act'(pre), rounded to bf16 into rows of ldp elements, and each row slab's sums over its
+// rows (of the unrounded products).  256 threads: 32 pairs of columns x 8 rows at a time.
+constexpr int kSlabRows = 128;
+__global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
+    __shared__ float2 part[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const unsigned ncol = (unsigned)(a.n + 63) / 64, slab = blockIdx.x / ncol;
+    const int n0 = (int)(blockIdx.x - slab * ncol) * 64 + 2 * lane;
+    const int64_t m0 = (int64_t)slab * kSlabRows;
+    const bool ok0 = n0 < a.n, ok1 = n0 + 1 < a.n;
+    const bf16_t* dy = static_cast<const bf16_t*>(a.dy);
+    const bf16_t* pre = static_cast<const bf16_t*>(a.pre);
+    bf16_t* dp = static_cast<bf16_t*>(a.dpre);
+    float2 sum = make_float2(0.f, 0.f);
+    for (int k = w; k < kSlabRows; k += 8) {
+        const int64_t m = m0 + k;
+        if (m >= a.m) break;
+        const size_t at = (size_t)m * a.n + n0;
+        float v0 = ok0 ? __bfloat162float(dy[at]) : 0.f, v1 = ok1 ? __bfloat162float(dy[at + 1]) : 0.f;
+        if (pre) {
+            if (ok0) v0 *= act_slope(__bfloat162float(pre[at]), a.act);
+            if (ok1) v1 *= act_slope(__bfloat162float(pre[at + 1]), a.act);
+        }
+        if (dp) {
+            bf16_t* q = dp + (size_t)m * a.ldp + n0;
+            if (ok0) q[0] = __float2bfloat16_rn(v0);
+            if (ok1) q[1] = __float2bfloat16_rn(v1);
+        }
+        sum.x += v0;
+        sum.y += v1;
+    }
+    if (!a.shares) return;
+    part[w][lane] = sum;
+    __syncthreads();
+    if (w == 0) {
+        for (int k = 1; k < 8; ++k) {
+            sum.x += part[k][lane].x;
+            sum.y += part[k][lane].y;
+        }
+        float* s = a.shares + (size_t)slab * a.n + n0;
+        if (ok0) s[0] = sum.x;
+        if (ok1) s[1] = sum.y;
+    }
+}
+
+// dbias[e] = sum over the slabs' shares: 32 columns per CTA, the shares dealt to its 32
+// warps, whose sums are added in warp order.
+__global__ void __launch_bounds__(1024) ssd_linear_dbias(const float* shares, int nshares, int n, float* dbias) {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (e < n)
+        for (int k = w; k < nshares; k += 32) s += shares[(size_t)k * n + e];
+    part[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && e < n) {
+        float t = 0.f;
+        for (int k = 0; k < 32; ++k) t += part[k][lane];
+        dbias[e] = t;
+    }
+}
+
+// A (rows, inner) matrix read in boxes of `box_rows` rows x 128 bytes, 128-byte swizzle.
+bool encode_2d(CUtensorMap* tm, const void* base, int dtype, int64_t inner, int64_t rows, int64_t ld, int box_rows) {
+    const auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int es = dtype == SSD_E4M3 ? 1 : 2;
+    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
+    cuuint32_t box[2] = {(cuuint32_t)(kRowB / es), (cuuint32_t)box_rows};
+    cuuint32_t step[2] = {1, 1};
+    return enc(tm, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+               dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int TN, bool E4M3, bool AMN, bool BMN>
+cudaError_t launch_tile(const LinearParams& p, int grid, cudaStream_t st) {
+    constexpr size_t smem = Cfg<TN>::kSmem;
+    const auto kern = ssd_linear_tc<TN, E4M3, AMN, BMN>;
+    static std::atomic<uint8_t> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        ready[dev].store(1, std::memory_order_release);
+    }
+    kern<<<(unsigned)grid, kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <bool E4M3, bool AMN, bool BMN>
+cudaError_t launch_kind(const LinearParams& p, int tile_n, int grid, cudaStream_t st) {
+    if (tile_n == 256) return launch_tile<256, E4M3, AMN, BMN>(p, grid, st);
+    if (tile_n == 128) return launch_tile<128, E4M3, AMN, BMN>(p, grid, st);
+    if constexpr (!AMN && !BMN) {
+        if (tile_n == 32) return launch_tile<32, E4M3, AMN, BMN>(p, grid, st);
+        if (tile_n == 16) return launch_tile<16, E4M3, AMN, BMN>(p, grid, st);
+    }
+    return launch_tile<64, E4M3, AMN, BMN>(p, grid, st);
+}
+
+}  // namespace
+
+// How a product of `rows` x `cols` results over a contraction of `kbytes` bytes runs.  Up to kLinearSwap
+// rows it is computed transposed.  Otherwise the tile width and the number of parts minimise a
+// count of tensor-core cycles: waves of tiles, each its blocks' MMAs (a 128-byte block
+// takes 2 cycles per column of the tile, but no fewer than reading both operands from shared memory at
+// 128 bytes a cycle) and a fixed start; parts add the join's launch and its traffic.
+LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
+    LinearPlan best = {};
+    const int64_t kblocks = (kbytes + kRowB - 1) / kRowB;
+    const bool swap = may_swap && rows <= kLinearSwap;
+    const int64_t dr = swap ? cols : rows, dc = swap ? rows : cols;
+    double least = 0;
+    const int widths[] = {256, 128, 64, 32, 16};
+    for (int tn : widths) {
+        if (swap ? (tn > kLinearSwap || (tn < dc && tn < kLinearSwap) || (tn > 16 && tn / 2 >= dc)) : tn < 64) continue;
+        const int64_t tiles = ((dr + kTileM - 1) / kTileM) * ((dc + tn - 1) / tn);
+        const double block = 2.0 * tn > tn + 128 ? 2.0 * tn : tn + 128;
+        for (int s = 1; s <= kLinearMaxSplits; ++s) {
+            const int64_t per = (kblocks + s - 1) / s;
+            if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;   // every part has blocks
+            const int64_t waves = (tiles * s + kLinearSMs - 1) / kLinearSMs;
+            double cost = (double)waves * (per * block + 600) + 2.0 * tn;
+            if (s > 1) cost += 5000 + (double)rows * cols * 8 * s / 3500;   // about 3500 bytes of HBM a cycle
+            if (least == 0 || cost < least) {
+                least = cost;
+                best.tile_n = tn;
+                best.splits = s;
+                best.swap = swap;
+                best.parts_bytes = s > 1 ? (size_t)rows * cols * 4 * s : 0;
+            }
+            if (tiles * s >= 4 * kLinearSMs) break;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaStream_t st) {
+    LinearParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = args;
+    LinearArgs& a = p.a;
+    a.swap = plan.swap;
+    a.vec = a.n % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0 && ((uintptr_t)a.pre & 15) == 0;
+    const int64_t dr = a.swap ? a.n : a.m, dc = a.swap ? a.m : a.n;
+    const int tn = plan.tile_n, es = a.dtype == SSD_E4M3 ? 1 : 2;
+    p.tiles_r = (int)((dr + kTileM - 1) / kTileM);
+    p.tiles_c = (int)((dc + tn - 1) / tn);
+    p.kblocks = (int)((a.k * es + kRowB - 1) / kRowB);
+    p.splits = plan.splits;
+    p.items = p.tiles_r * p.tiles_c * p.splits;
+    // the wide operand gives D's rows, 128 at a time; operands with their contraction along the rows
+    // are read in boxes of 64 x 64
+    const LinearOperand& oa = a.swap ? a.w : a.x;
+    const LinearOperand& ob = a.swap ? a.x : a.w;
+    const bool ea = oa.along_rows ? encode_2d(&p.tm_a, oa.p, a.dtype, dr, a.k, oa.ld, 64)
+                                  : encode_2d(&p.tm_a, oa.p, a.dtype, a.k, dr, oa.ld, kTileM);
+    const bool eb = ob.along_rows ? encode_2d(&p.tm_b, ob.p, a.dtype, dc, a.k, ob.ld, 64)
+                                  : encode_2d(&p.tm_b, ob.p, a.dtype, a.k, dc, ob.ld, tn);
+    if (!ea || !eb) return cudaErrorInvalidValue;
+    const int nsm = device_sms();
+    const int grid = p.items < nsm || nsm <= 0 ? p.items : nsm;
+    cudaError_t e;
+    if (a.dtype == SSD_E4M3) e = launch_kind<true, false, false>(p, tn, grid, st);
+    else if (oa.along_rows) e = launch_kind<false, true, true>(p, tn, grid, st);
+    else if (ob.along_rows) e = launch_kind<false, false, true>(p, tn, grid, st);
+    else e = launch_kind<false, false, false>(p, tn, grid, st);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const size_t total = (size_t)a.m * a.n;
+    ssd_linear_join<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a, p.splits);
+    return cudaGetLastError();
+}
+
+int64_t linear_dpre_slabs(int64_t m) { return (m + kSlabRows - 1) / kSlabRows; }
+
+cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st) {
+    const int64_t slabs = linear_dpre_slabs(a.m);
+    ssd_linear_dpre<<<(unsigned)(slabs * ((a.n + 63) / 64)), 256, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.dbias) return e;
+    ssd_linear_dbias<<<(unsigned)((a.n + 31) / 32), 1024, 0, st>>>(a.shares, (int)slabs, a.n, a.dbias);
+    return cudaGetLastError();
+}
+
+}  // namespace ssd

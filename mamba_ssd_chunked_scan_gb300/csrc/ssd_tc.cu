@@ -1141,7 +1141,7 @@ cudaError_t launch_doc_init_agg(const FwdArgs& a, cudaStream_t st) {
     return launch_kernel(ssd_doc_init_agg, (unsigned)grid, kDocInitThreads, 0, st, a.pdl != 0, a);
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     if (!fn) {
         cudaDriverEntryPointQueryResult q;
@@ -1157,7 +1157,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 // 4-D map over a (batch, L, heads_or_groups, inner) bf16 tensor; box = one
 // 64-element x 128-row tile of one head (group), 128-byte swizzle.
 bool encode_4d(CUtensorMap* tm, const void* base, int64_t inner, int64_t mid, int64_t L, int64_t batch) {
-    auto enc = get_encode();
+    auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)mid, (cuuint64_t)L, (cuuint64_t)batch};
     cuuint64_t strides[3] = {(cuuint64_t)(inner * 2), (cuuint64_t)(inner * mid * 2),

@@ -1,4 +1,4 @@
-"""The operators around the scan: residual RMS norm, gated recurrence.
+"""The operators around the scan: residual RMS norm, projection, gated recurrence.
 
 Thin wrappers over the C ABI like the package's other entry points: they check
 tensors, take device pointers and the stream, and call the library.  Outputs
@@ -273,3 +273,102 @@ def gate_scan_step(state, g, x, *, state_out=None, stream=None):
                                        state.data_ptr(), state_out.data_ptr(), y.data_ptr(), _raw_stream(dev))
     _check(rc, "ssd_gate_scan_step")
     return y
+
+
+_ACT = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _linear_params(x, w, act, name="x"):
+    """(device, rows' shape, parameters) of a product x w^T."""
+    dev = _device(name, x)
+    dtype, shape = x.dtype, x.shape
+    if dtype is not _BF16 and dtype is not _E4M3:
+        raise TypeError(f"{name} must be bf16 or float8_e4m3fn, got {dtype}")
+    if len(shape) < 1 or w.dim() != 2 or w.shape[1] != shape[-1]:
+        raise ValueError(f"expected x (..., k) and w (n, k), got {tuple(shape)} and {tuple(w.shape)}")
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {tuple(_ACT)}, got {act!r}")
+    n, k = w.shape
+    _need("w", w, dtype, w.shape, dev)
+    ldx = k if x.is_contiguous() else _row_stride(name, x)
+    return dev, shape[:-1], _lib.LinearParams(x.numel() // k if k else 0, ldx, n, k, _CODE[dtype], _ACT[act])
+
+
+def _row_stride(name, t):
+    """Elements between the rows of a (..., k) tensor whose leading dimensions are packed."""
+    st, shape = t.stride(), t.shape
+    ok = len(shape) > 1 and (st[-1] == 1 or shape[-1] == 1) and st[-2] >= shape[-1]
+    for k in range(len(shape) - 2):
+        ok = ok and (shape[k] == 1 or st[k] == st[k + 1] * shape[k + 1])
+    if not ok:
+        raise ValueError(f"{name}: expected columns together and rows at one stride, got strides {st} for {tuple(shape)}")
+    return st[-2]
+
+
+def linear(x, w, bias=None, residual=None, *, act="none", x_scales=None, w_scales=None, return_pre=False,
+           check_status=False, stream=None):
+    """y = act(x w^T + bias) + residual in one product on the tensor cores.
+
+    x (..., k) bf16, or float8_e4m3fn with x_scales (...) and w_scales (n) fp32
+    (add_norm's ``out`` and ``scales``, say); rows may be column ranges of a wider matrix. w (n, k) of
+    x's type; bias (n) fp32 or None; residual (..., n) bf16 or None; act "none", "silu" or "gelu" (tanh form).
+    k is a multiple of 8 (bf16) or 16 (e4m3).  Returns y (..., n) bf16, or (y, pre) with return_pre: pre is the
+    activation's argument in bf16, for linear_bwd."""
+    dev, lead, p = _linear_params(x, w, act)
+    m, n = p.m, p.n
+    if x.dtype is _E4M3:
+        if x_scales is None or w_scales is None:
+            raise ValueError("x_scales, w_scales: e4m3 operands come with both")
+        _need("x_scales", x_scales, _F32, lead, dev)
+        _need("w_scales", w_scales, _F32, (n,), dev)
+    elif x_scales is not None or w_scales is not None:
+        raise ValueError("x_scales, w_scales: only with e4m3 operands")
+    if bias is not None:
+        _need("bias", bias, _F32, (n,), dev)
+    out_shape = (*lead, n)
+    if residual is not None:
+        _need("residual", residual, _BF16, out_shape, dev)
+    nbytes = _lib_c.ssd_linear_workspace_size(ctypes.byref(p))
+    if nbytes == 0:
+        raise _lib.SSDError(2, f"linear of {tuple(x.shape)} and {tuple(w.shape)}, row stride {p.ldx}")
+    with _on(dev, stream):
+        y = torch.empty(out_shape, dtype=_BF16, device=x.device)
+        pre = torch.empty(out_shape, dtype=_BF16, device=x.device) if return_pre else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        st = _raw_stream(dev)
+        _check(_lib_c.ssd_linear(ctypes.byref(p), x.data_ptr(), w.data_ptr(), _ptr(x_scales), _ptr(w_scales), _ptr(bias),
+                                 _ptr(residual), y.data_ptr(), _ptr(pre), ws.data_ptr(), nbytes, st), "ssd_linear")
+        if check_status and m:
+            _check(_lib_c.ssd_check_status(ws.data_ptr(), st), "ssd_linear device status")
+    return (y, pre) if return_pre else y
+
+
+def linear_bwd(dy, x, w, pre=None, *, act="none", want_dx=True, want_dw=True, want_dbias=False, check_status=False, stream=None):
+    """Gradients of <dy, y> of one linear call of bf16 operands: dy (..., n) bf16, x and w as given to it, pre
+    its second result (with an activation).  Returns a dict: ``dx`` (..., k) bf16, ``dw`` (n, k) bf16 and
+    ``dbias`` (n) fp32, None where not wanted.  (The residual's gradient is dy.)"""
+    dev, lead, p = _linear_params(x, w, act)
+    if x.dtype is not _BF16:
+        raise TypeError(f"x must be bf16, got {x.dtype}")
+    out_shape = (*lead, p.n)
+    _need("dy", dy, _BF16, out_shape, dev)
+    if (pre is None) != (act == "none"):
+        raise ValueError("pre: given with an activation, and only then")
+    if pre is not None:
+        _need("pre", pre, _BF16, out_shape, dev)
+    if not (want_dx or want_dw or want_dbias):
+        raise ValueError("no gradient wanted")
+    nbytes = _lib_c.ssd_linear_bwd_workspace_size(ctypes.byref(p))
+    if nbytes == 0:
+        raise _lib.SSDError(2, f"linear_bwd of {tuple(x.shape)} and {tuple(w.shape)}, row stride {p.ldx}")
+    with _on(dev, stream):
+        dx = torch.empty((*lead, p.k), dtype=_BF16, device=x.device) if want_dx else None
+        dw = torch.empty((p.n, p.k), dtype=_BF16, device=x.device) if want_dw else None
+        db = torch.empty(p.n, dtype=_F32, device=x.device) if want_dbias else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        st = _raw_stream(dev)
+        _check(_lib_c.ssd_linear_bwd(ctypes.byref(p), x.data_ptr(), w.data_ptr(), _ptr(pre), dy.data_ptr(), _ptr(dx), _ptr(dw),
+                                     _ptr(db), ws.data_ptr(), nbytes, st), "ssd_linear_bwd")
+        if check_status and p.m:
+            _check(_lib_c.ssd_check_status(ws.data_ptr(), st), "ssd_linear_bwd device status")
+    return {"dx": dx, "dw": dw, "dbias": db}

@@ -131,3 +131,75 @@ def step(L, **kw):
 ])
 def test_gate_scan_step_refusals(L, kw, code):
     assert step(L, **kw) == code
+
+
+def linear_params(**kw):
+    from mamba_ssd_chunked_scan_gb300 import _lib
+    d = dict(m=32, ldx=256, n=512, k=256, dtype=1, act=0)
+    d.update(kw)
+    return _lib.LinearParams(*d.values())
+
+
+LINEAR_PARAMS = [
+    (dict(m=-1), 1), (dict(n=0), 1), (dict(k=0), 1), (dict(ldx=248), 1), (dict(dtype=0), 1), (dict(dtype=5), 1), (dict(act=3), 1),
+    (dict(act=-1), 1), (dict(k=252), 2), (dict(ldx=260), 2), (dict(dtype=2, k=248), 2), (dict(m=1 << 30), 2),
+    (dict(m=1 << 29, n=1 << 29), 2), (dict(ldx=1 << 31), 2),
+]
+
+
+@pytest.mark.parametrize("kw,code", LINEAR_PARAMS)
+def test_linear_parameters(L, kw, code):
+    p = linear_params(**kw)
+    assert L.ssd_linear_workspace_size(p) == 0 and L.ssd_linear_bwd_workspace_size(p) == 0
+    assert L.ssd_linear(p, G, 2 * G, None, None, None, None, 3 * G, None, 4 * G, 1 << 29, None) == code
+    if kw.get("dtype") != 2:
+        assert L.ssd_linear_bwd(p, G, 2 * G, None, 3 * G, 4 * G, 5 * G, None, 6 * G, 1 << 29, None) == code
+
+
+def lin(L, p=None, **kw):
+    d = dict(x=G, w=2 * G, xs=None, ws=None, bias=3 * G, res=4 * G, y=5 * G, pre=6 * G, work=7 * G, wb=1 << 29, stream=None)
+    d.update(kw)
+    return L.ssd_linear(p or linear_params(), *d.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), 1), (dict(w=None), 1), (dict(y=None), 1), (dict(x=G + 8), 1), (dict(w=2 * G + 2), 1), (dict(bias=3 * G + 2), 1),
+    (dict(y=5 * G + 1), 1), (dict(xs=8 * G), 1), (dict(xs=8 * G, ws=9 * G), 1), (dict(work=None), 3), (dict(wb=64), 3),
+    (dict(work=7 * G + 16), 3), (dict(y=G), 1), (dict(y=2 * G + 2), 1), (dict(y=6 * G), 1), (dict(pre=4 * G), 1), (dict(y=4 * G + 2), 1),
+    (dict(y=7 * G), 1), (dict(pre=3 * G), 1), (dict(res=7 * G), 1),
+])
+def test_linear_refusals(L, kw, code):
+    assert lin(L, **kw) == code
+
+
+def test_linear_scales_come_with_e4m3(L):
+    p = linear_params(dtype=2)
+    assert lin(L, p) == 1 and lin(L, p, xs=8 * G) == 1 and lin(L, p, ws=9 * G) == 1
+    assert lin(L, p, xs=8 * G, ws=9 * G, y=8 * G) == 1
+    assert lin(L, linear_params(m=0), x=None, y=None) == 0
+    assert L.ssd_linear_bwd(p, G, 2 * G, None, 3 * G, 4 * G, 5 * G, None, 6 * G, 1 << 29, None) == 2
+
+
+def lin_bwd(L, act=1, **kw):
+    d = dict(x=G, w=2 * G, pre=3 * G, dy=4 * G, dx=5 * G, dw=6 * G, db=7 * G, work=8 * G, wb=1 << 29, stream=None)
+    d.update(kw)
+    return L.ssd_linear_bwd(linear_params(act=act), *d.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), 1), (dict(w=None), 1), (dict(dy=None), 1), (dict(pre=None), 1), (dict(act=0), 1), (dict(dx=None, dw=None, db=None), 1),
+    (dict(dy=4 * G + 8), 1), (dict(db=7 * G + 2), 1), (dict(dx=G), 1), (dict(dw=2 * G), 1), (dict(dx=4 * G + 64), 1), (dict(dw=5 * G), 1),
+    (dict(db=6 * G), 1), (dict(dx=8 * G), 1), (dict(work=None), 3), (dict(wb=256), 3), (dict(work=8 * G + 128), 3),
+])
+def test_linear_bwd_refusals(L, kw, code):
+    assert lin_bwd(L, **kw) == code
+
+
+def test_linear_plans_have_work_in_every_part(L):
+    """Every workspace is a whole number of parts, and small products stay unsplit or split evenly."""
+    for m in (1, 8, 64, 65, 128, 500, 4099, 16384):
+        for n in (1, 33, 512, 2560, 10240):
+            for k in (16, 64, 512, 2560, 5120):
+                size = L.ssd_linear_workspace_size(linear_params(m=m, n=n, k=k, ldx=k))
+                parts = (size - 256) / (4 * m * n)
+                assert parts == int(parts) and 0 <= parts <= 16 and parts <= max(1, k * 2 / 128 / 4)
