@@ -391,10 +391,10 @@ SSD_API size_t ssd_gate_scan_workspace_size(const ssd_gate_scan_params_t* p);
  * The state is fp32 throughout; y is rounded once.  No output may overlap an input.
  * `workspace`: at least ssd_gate_scan_workspace_size(p) bytes, 256-byte aligned (else
  * SSD_ERR_WORKSPACE); it needs no initialisation, and calls that share it must be ordered on one
- * stream.  A clear of its head (status word, tickets, flags) and one launch, asynchronous on `stream`; it
+ * stream.  A clear of it (status word, tickets, states on their way) and one launch, asynchronous on `stream`; it
  * can be captured in a CUDA graph.  Tiles of a sequence hand their states on through the workspace; every wait is
  * bounded, and one that runs out records SSD_ERR_TIMEOUT (where 51: a tile's map, 52: a block's
- * state) in the status word read by ssd_check_status(), as offsets that break their rule
+ * state, 53-56: waits inside a CTA) in the status word read by ssd_check_status(), as offsets that break their rule
  * record SSD_ERR_DEVICE_CHECK.  Bitwise deterministic. */
 SSD_API int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x, const float* initial_states,
              const int32_t* cu_seqlens, void* y, float* final_states, void* workspace, size_t workspace_bytes,
@@ -410,7 +410,7 @@ SSD_API int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const 
  *   dfinal_states  (nstates, width) fp32, or NULL (zeros)
  *   dg, dx         (batch, seqlen, width) dtype, token strides g_stride, x_stride; written
  *   dinitial_states (nstates, width) fp32, or NULL
- * h_{t-1} is recomputed in fp32 from the h of every 16th token, which is read from y.
+ * h_{t-1} is recomputed in fp32 from the h of every 8th token, which is read from y.
  * Workspace, launches, errors and aliasing as for ssd_gate_scan(). */
 SSD_API int ssd_gate_scan_bwd(const ssd_gate_scan_params_t* p, const void* g, const void* x, const void* y,
              const float* initial_states, const int32_t* cu_seqlens, const void* dy, const float* dfinal_states,

@@ -1,31 +1,43 @@
 // Gated linear recurrence, one decay per channel and token:
-//   ssd_gate_scan_kernel       h_t = a_t h_{t-1} + (1 - a_t) x_t,  a_t = 1 / (1 + exp(-g_t)),  y = h
-//   ssd_gate_scan_bwd_kernel   lam_t = dy_t + a_{t+1} lam_{t+1};  dx = (1 - a) lam,
+//   ssd_gate_scan_kernel<fwd>  h_t = a_t h_{t-1} + (1 - a_t) x_t,  a_t = 1 / (1 + exp(-g_t)),  y = h
+//   ssd_gate_scan_kernel<bwd>  lam_t = dy_t + a_{t+1} lam_{t+1};  dx = (1 - a) lam,
 //                              dg = lam (h_{t-1} - x) a (1 - a),  dinit = a_1 lam_1
 //   ssd_gate_scan_step_kernel  one token from a resident state
 //
 // Each step is an affine map of the state, and the maps of consecutive steps
-// compose: (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2).  A CTA takes one tile of
-// kTok tokens x kCh channels: a warp holds a segment of kSeg tokens, a thread two
-// channels of it, with the tile's decays and inputs in registers from their one
-// read to the one write of y.  A tile needs the state that enters it.  Its map
-// is published as soon as it is known; the state follows from the maps of the
-// tiles before it in its block of kBlock tiles and from the state that enters the
-// block, which the last tile of the block before publishes.  So only one hand-over
-// per block is a chain, every input is read once, and the order in which maps are
-// composed is fixed: results do not depend on which tile ran first.  Tiles are
-// taken by ticket in the order of the sequence (a tile only waits for tiles
-// with smaller tickets, which running CTAs hold), and every wait is bounded.
+// compose: (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2).  The work is cut into tiles of
+// kMain segments of SEG tokens x kCh channels.  A CTA has eight main warps, one per segment, a
+// thread holding two channels; two hand-over warps, a thread per channel; and a loading warp:
+//   loading    takes the next tile by ticket and brings its inputs into a ring of shared-memory stages
+//              (TMA tiles, or 16-byte aligned windows of each row where rows are not aligned),
+//              and sends a finished tile's outputs off from the same stage;
+//   main       forms the decays and the segment's map, keeping 1 - a in registers; waits for the state
+//              that enters the segment; walks the segment again and writes the outputs;
+//   hand-over  composes the segments' maps to the tile's, publishes it, and works out the state that
+//              enters the tile and from it those that enter the segments.
+// Every input is read from HBM once.  The state that enters a tile follows from the maps of the tiles
+// before it in its block of kScanBlock tiles and from the state that enters the block, which the last tile
+// of the block before publishes: one hand-over per block is a chain, and the order
+// in which maps are composed is fixed, so results do not depend on which tile ran first.  A map
+// is one 64-bit word per channel that is never zero once written, so the word is its own flag.  Tickets run
+// in the order of the sequences: a tile only waits for tiles of smaller tickets, and a CTA works on its own in
+// their order, so the smallest unfinished ticket never waits; every wait is bounded all the same.
 //
 // The backward pass walks the same maps from the end: mu_t = a_t lam_t obeys
 // mu_t = a_t (dy_t + mu_{t+1}).  h_{t-1} inside a segment is recomputed from
 // the h before it, which is read from y (rounded to y's type once, at every
-// kSeg-th token); keeping every h would cost as many bytes again as g.
+// SEG-th token); keeping every h would cost as many bytes again as g.
 //
 // A document's first token cuts the map (A = 0) and takes the document's own state.
 //
-// 1 - a is formed as e / (1 + e), e = exp(-g), not as a difference: a channel
-// with a long memory has a close to 1.
+// 1 - a is formed as e / (1 + e), e = exp(-g), not as a difference, and kept in place of a:
+// a channel with a long memory has a close to 1, where a = 1 - m is right to the last bit and
+// m = 1 - a would not be; a step is a h + m x, exact where a gate forgets all, rather than h + m (x - h).
+// Arithmetic on a thread's two channels is packed (f32x2), which rounds each as the scalar form does.
+#include <string.h>
+
+#include <atomic>
+
 #include "ssd_common.cuh"
 #include "ssd_kernels.h"
 #include "ssd_vec.cuh"
@@ -34,15 +46,34 @@
 namespace ssd {
 namespace {
 
-constexpr int kSeg = 16;               // tokens per segment (one warp)
-constexpr int kWarps = kScanTok / kSeg;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCh = kScanCh;           // channels per tile: two per thread
-constexpr int kTok = kScanTok;
+constexpr int kMain = 8;               // main warps: segments per tile
+constexpr int kCh = kScanCh;           // channels per tile: two per main thread, one per hand-over thread
+constexpr int kThreads = 32 * (kMain + 2 + 1);
 constexpr int kBlock = kScanBlock;
+static_assert(kCh == 64, "two channels per lane, two hand-over warps");
 
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kWhereTile = 51, kWhereBlock = 52;
+constexpr uint32_t kWhereTile = 51, kWhereBlock = 52, kWhereStage = 53, kWhereMaps = 54, kWhereState = 55, kWhereDone = 56;
+
+typedef uint64_t f2;   // two floats, one per channel of a thread
+__device__ __forceinline__ f2 pk(float a, float b) { return ptx::f2_pack(a, b); }
+__device__ __forceinline__ float2 un(f2 v) {
+    float2 r;
+    ptx::f2_unpack(v, r.x, r.y);
+    return r;
+}
+__device__ __forceinline__ f2 mul(f2 a, f2 b) { return ptx::f2_mul(a, b); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return ptx::f2_fma(a, b, c); }
+__device__ __forceinline__ f2 add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 // a = 1 / (1 + e), m = e / (1 + e) with e = exp(-g), capped where e would overflow
 // (a is then 1e-38, m one).  bf16 operands take the special-function unit's
@@ -51,411 +82,601 @@ template <typename T>
 __device__ __forceinline__ void gate(float g, float& a, float& m) {
     if constexpr (sizeof(T) == 2) {
         float e;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(-g * kLog2e, 126.f)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(min_nan(-g * kLog2e, 126.f)));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
         m = e * a;
     } else {
-        const float e = expf(fminf(-g, 87.f));
+        const float e = expf(min_nan(-g, 87.f));
         a = __frcp_rn(1.f + e);
         m = e * a;
     }
-    if (g != g) a = m = g;   // fminf drops a NaN
+}
+template <typename T>
+__device__ __forceinline__ void gate2(f2 g, f2& a, f2& m) {
+    if constexpr (sizeof(T) == 2) {
+        const float2 t = un(mul(g, pk(-kLog2e, -kLog2e)));
+        float e0, e1, a0, a1;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(min_nan(t.x, 126.f)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(min_nan(t.y, 126.f)));
+        const f2 e = pk(e0, e1);
+        const float2 d = un(add(e, pk(1.f, 1.f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(d.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(d.y));
+        a = pk(a0, a1);
+        m = mul(e, a);
+    } else {
+        const float2 t = un(g);
+        float a0, a1, m0, m1;
+        gate<float>(t.x, a0, m0);
+        gate<float>(t.y, a1, m1);
+        a = pk(a0, a1);
+        m = pk(m0, m1);
+    }
 }
 
-// The two channels of a thread: neighbours (one access) where rows allow it, else
-// 32 apart (two accesses, each contiguous over the warp).
-template <typename T, bool PAIR>
-struct Two {
-    T lo, hi;   // as stored
-    __device__ __forceinline__ void load(const T* p, bool ok0, bool ok1) {
-        if constexpr (PAIR) {
-            Raw<T, 2> r;
-            r.zero();
-            if (ok0) r.load(p);
-            const T* e = reinterpret_cast<const T*>(&r.w);
-            lo = e[0];
-            hi = e[1];
-        } else {
-            Raw<T, 1> r, q;
-            r.zero();
-            q.zero();
-            if (ok0) r.load(p);
-            if (ok1) q.load(p + 32);
-            lo = *reinterpret_cast<const T*>(&r.w);
-            hi = *reinterpret_cast<const T*>(&q.w);
-        }
-    }
-    static __device__ __forceinline__ void store(T* p, bool ok0, bool ok1, float v0, float v1) {
-        if constexpr (PAIR) {
-            const float v[2] = {v0, v1};
-            Raw<T, 2> r;
-            r.set(v);
-            if (ok0) r.store(p);
-        } else {
-            const float a[1] = {v0}, b[1] = {v1};
-            Raw<T, 1> r, q;
-            r.set(a);
-            q.set(b);
-            if (ok0) r.store(p);
-            if (ok1) q.store(p + 32);
-        }
-    }
-    __device__ __forceinline__ float f0() const { return (float)lo; }
-    __device__ __forceinline__ float f1() const { return (float)hi; }
+template <typename T> struct PairWord;
+template <> struct PairWord<bf16_t> { typedef uint32_t type; };
+template <> struct PairWord<float> { typedef uint64_t type; };
+
+// Shapes of a kernel instance.  ROWS: rows are not 16-byte aligned; a stage holds a 16-byte aligned
+// window around each row's channels, and outputs are stored by the main warps.
+template <typename T, bool ROWS, bool BWD>
+struct Shape {
+    static constexpr int ES = sizeof(T);
+    static constexpr int SEG = scan_seg(BWD, ES == 2 ? SSD_BF16 : SSD_F32), TOK = SEG * kMain;
+    static constexpr int PITCH = kCh * ES + (ROWS ? 16 : 0);
+    static constexpr int ARR = TOK * PITCH;                 // one operand's tile
+    static constexpr int NA = BWD ? 3 : 2;                  // g, x (and dy)
+    static constexpr int STAGE = NA * ARR + (BWD ? kMain * PITCH : 0);   // and, backwards, the h before each segment
+    static constexpr int NS = ROWS || (BWD && ES == 4) ? 2 : 3;
+    static constexpr size_t kSmem = 128 + (size_t)NS * ((STAGE + 127) / 128 * 128);
+    static constexpr int kStep = (STAGE + 127) / 128 * 128;
+};
+
+struct ScanParams {
+    CUtensorMap g, x, y, dy, dg, dx;
+    GateScanArgs a;
 };
 
 struct Tile {
-    int64_t row, chunk;    // batch row, tile along the sequence
+    int row, group;        // batch row, channel group
+    int step;              // place in the walk of its sequence
+    int ntok;              // its tokens; 0: no tile is left
     int64_t t0;            // its first token
-    int group;             // channel group
-    int ntok;              // its tokens
 };
 
-// Documents that start inside the tile (or at the token after it): doc[k] = the
-// document that starts at token t0 + k, or -1.  Offsets outside the tile are skipped,
-// so nothing they hold can index out of bounds.
-__device__ void find_docs(const GateScanArgs& a, int64_t t0, int* doc) {
-    for (int k = threadIdx.x; k <= kTok; k += kThreads) doc[k] = -1;
-    __syncthreads();
-    // the first document whose offset is >= t0
-    int lo = 0, hi = a.ndocs;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu + mid) < t0) lo = mid + 1;
-        else hi = mid;
-    }
-    for (int d = lo + threadIdx.x; d < a.ndocs; d += kThreads) {
-        const int64_t k = (int64_t)__ldg(a.cu + d) - t0;
-        if (k > kTok) break;
-        if (k >= 0) doc[k] = d;
-    }
-    __syncthreads();
-}
-
-struct Maps {   // a segment's map per channel
-    float2 A[kWarps][32], B[kWarps][32];
-};
-
-// The maps of the tile's predecessors in its block, and the state that enters the block.
-struct Before {
-    float2 A[kBlock][32], B[kBlock][32];
-    float2 carry[32];
-    int ok;
-};
-
-__device__ __forceinline__ bool wait_flag(const uint32_t* flag, WsHeader* ws, uint32_t where) {
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 0;; ++it) {
-        uint32_t v;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
-        if (v) return true;
-        if ((it & 63) == 63 && (ptx::globaltimer() - t0 > kWaitNs || it > (1u << 26))) {
-            record_error(ws, SSD_ERR_TIMEOUT, where);
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ void raise_flag(uint32_t* flag) {
-    asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flag) : "memory");
-}
-
-// Takes the next tile in sequence order (tickets), or the CTA's own where the call
-// has one tile per sequence.
-template <bool REV>
-__device__ bool take_tile(const GateScanArgs& a, Tile& t, int* slot) {
-    uint32_t k = blockIdx.x;
-    if (a.nchunks > 1) {
-        if (threadIdx.x == 0) *slot = (int)atomicAdd(a.ticket, 1u);
-        __syncthreads();
-        k = (uint32_t)*slot;
-    }
+template <bool REV, int TOK>
+__device__ __forceinline__ Tile tile_of(const GateScanArgs& a, uint32_t k) {
+    Tile t;
     const uint32_t per = (uint32_t)(a.batch * a.ngroups);
     const uint32_t c = k / per, r = k - c * per;
-    t.row = r / (uint32_t)a.ngroups;
+    t.row = (int)(r / (uint32_t)a.ngroups);
     t.group = (int)(r - (uint32_t)t.row * a.ngroups);
-    t.chunk = REV ? a.nchunks - 1 - c : c;
-    t.t0 = t.chunk * kTok;
-    t.ntok = (int)((a.seqlen - t.t0 < kTok) ? a.seqlen - t.t0 : kTok);
-    return true;
+    t.step = (int)c;
+    t.t0 = (REV ? a.nchunks - 1 - c : c) * TOK;
+    t.ntok = k < a.ntiles ? (int)(a.seqlen - t.t0 < TOK ? a.seqlen - t.t0 : TOK) : 0;
+    return t;
 }
 
-// Publishes the tile's map and returns the value that enters it, per channel: `init`
-// enters the sequence's first tile.  `step` is the tile's place in the order
-// of the walk.  Called by every thread; the map (A, B) of the whole tile is valid in warp 0.
-__device__ float2 enter_tile(const GateScanArgs& a, const Tile& t, int64_t step, float2 A, float2 B, float2 init, Before& bf) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (a.nchunks == 1) return init;
-    const int64_t line = t.row * a.ngroups + t.group;         // sequence of tiles
-    const int64_t base = line * a.nchunks;                    // its first slot
-    const int in_block = (int)(step % kBlock);
-    const int64_t block = step / kBlock;
-    const int64_t nblocks = (a.nchunks + kBlock - 1) / kBlock;
-    if (warp == 0 && in_block != kBlock - 1 && step != a.nchunks - 1) {
-        a.maps[(base + step) * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) raise_flag(a.map_flag + base + step);
+// Documents that start inside a tile, or at the token after it: doc[k] = the
+// document that starts at token t0 + k, or -1.  One warp; offsets outside the tile are skipped,
+// so nothing they hold can index out of bounds.
+template <int TOK>
+__device__ void find_docs(const GateScanArgs& a, int64_t t0, int* doc) {
+    const int lane = threadIdx.x & 31;
+    for (int k = lane; k <= TOK; k += 32) doc[k] = -1;
+    __syncwarp();
+    // the first document whose offset is >= t0, 32 probes at a time
+    int lo = 0, hi = a.ndocs;
+    while (lo < hi) {
+        const int gap = (hi - lo + 31) / 32;
+        const int at = lo + (lane + 1) * gap - 1;
+        const bool below = at < hi && __ldg(a.cu + at) < t0;
+        const int n = __popc(__ballot_sync(0xffffffffu, below));
+        lo += n * gap;
+        if (lo > hi) lo = hi;
+        if (lo + gap - 1 < hi) hi = lo + gap - 1;
     }
-    if (threadIdx.x == 0) bf.ok = 1;
-    __syncthreads();
-    // warp w fetches the maps of predecessors w, w + kWarps, ...; the last warp the carry
-    for (int p = warp; p < in_block; p += kWarps) {
-        bool ok = true;
-        if (lane == 0) ok = wait_flag(a.map_flag + base + block * kBlock + p, a.ws, kWhereTile);
-        if (!ok) bf.ok = 0;
-        __syncwarp();
-        const float4 m = __ldcg(a.maps + (base + block * kBlock + p) * 32 + lane);
-        bf.A[p][lane] = make_float2(m.x, m.y);
-        bf.B[p][lane] = make_float2(m.z, m.w);
-    }
-    if (warp == kWarps - 1) {
-        float2 c = init;
-        if (block > 0) {
-            bool ok = true;
-            if (lane == 0) ok = wait_flag(a.carry_flag + line * nblocks + block - 1, a.ws, kWhereBlock);
-            if (!ok) bf.ok = 0;
-            __syncwarp();
-            c = __ldcg(a.carry + (line * nblocks + block - 1) * 32 + lane);
-        }
-        bf.carry[lane] = c;
-    }
-    __syncthreads();
-    float2 h = bf.carry[lane];
-    for (int p = 0; p < in_block; ++p) {
-        h.x = fmaf(bf.A[p][lane].x, h.x, bf.B[p][lane].x);
-        h.y = fmaf(bf.A[p][lane].y, h.y, bf.B[p][lane].y);
-    }
-    if (warp == 0 && in_block == kBlock - 1 && step != a.nchunks - 1) {
-        a.carry[(line * nblocks + block) * 32 + lane] = make_float2(fmaf(A.x, h.x, B.x), fmaf(A.y, h.y, B.y));
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) raise_flag(a.carry_flag + line * nblocks + block);
-    }
-    return h;
-}
-
-// The map of segments [from, to) (in the walk's order), composed in order.
-template <bool REV>
-__device__ __forceinline__ void compose(const Maps& mp, int n, int lane, float2& A, float2& B) {
-    A = make_float2(1.f, 1.f);
-    B = make_float2(0.f, 0.f);
-    for (int k = 0; k < n; ++k) {
-        const int w = REV ? kWarps - 1 - k : k;
-        const float2 a = mp.A[w][lane], b = mp.B[w][lane];
-        B.x = fmaf(a.x, B.x, b.x);
-        B.y = fmaf(a.y, B.y, b.y);
-        A.x *= a.x;
-        A.y *= a.y;
+    for (int d = lo; d < a.ndocs; d += 32) {
+        int64_t k = TOK + 1;
+        if (d + lane < a.ndocs) k = (int64_t)__ldg(a.cu + d + lane) - t0;
+        if (k >= 0 && k <= TOK) doc[k] = d + lane;
+        if (__all_sync(0xffffffffu, k > TOK)) break;
     }
 }
 
-template <typename T, bool PAIR, bool DOCS>
-__global__ void __launch_bounds__(kThreads) ssd_gate_scan_kernel(GateScanArgs a) {
-    __shared__ Maps mp;
-    __shared__ Before bf;
-    __shared__ int doc[DOCS ? kTok + 1 : 1];
-    __shared__ int slot;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Tile t;
-    take_tile<false>(a, t, &slot);
-    if (DOCS) {
-        find_docs(a, t.t0, doc);
-        if (blockIdx.x == 0) check_cu_seqlens(a.cu, a.ndocs, a.seqlen, a.ws, threadIdx.x, kThreads);
+constexpr int kRing = 4;   // tiles whose numbers and documents are kept: one more than stages
+template <int TOK, bool DOCS>
+struct Shared {
+    float2 seg[kMain][kCh];          // each segment's map per channel (A, B); then .x: the state that enters it
+    Tile tile[kRing];
+    int doc[DOCS ? kRing : 1][DOCS ? TOK + 1 : 1];
+    uint64_t full[3], done[3];       // per stage: inputs there; outputs written
+    uint64_t maps, states;           // the segments' maps are in seg; the states that enter them are
+    int abort, never;
+};
+
+template <typename S>
+__device__ __forceinline__ bool bar_wait(S& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
+    if (ptx::mbar_wait(bar, parity, &sh.abort, kDefaultWaitIters)) return true;
+    if (!*(volatile int*)&sh.abort) {
+        record_error(ws, SSD_ERR_TIMEOUT, where);
+        *(volatile int*)&sh.abort = 1;
     }
-    const int c0 = t.group * kCh + (PAIR ? 2 * lane : lane), c1 = c0 + (PAIR ? 1 : 32);
-    const bool ok0 = c0 < a.width, ok1 = c1 < a.width;
-    const int s0 = warp * kSeg;   // first token of the segment in the tile
-    const int64_t tok = t.row * a.seqlen + t.t0 + s0;
-    const T* g = static_cast<const T*>(a.g) + tok * a.g_stride + c0;
-    const T* x = static_cast<const T*>(a.x) + tok * a.x_stride + c0;
-    Two<T, PAIR> gr[kSeg], xr[kSeg];
-#pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
-        const bool in = s0 + k < t.ntok;
-        gr[k].load(g + k * a.g_stride, ok0 && in, ok1 && in);
-        xr[k].load(x + k * a.x_stride, ok0 && in, ok1 && in);
+    return false;
+}
+
+// Words that tiles leave for each other: written once per call, zero before.
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void leave(uint64_t* p, uint64_t v) {
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+template <typename S>
+__device__ __forceinline__ uint64_t await(const uint64_t* p, uint64_t v, S& sh, WsHeader* ws, uint32_t where) {
+    if (v) return v;
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 1; it < (1u << 28); ++it) {
+        v = peek(p);
+        if (v) return v;
+        if ((it & 63) == 0 && (*(volatile int*)&sh.abort || ptx::globaltimer() - t0 > kWaitNs)) break;
     }
-    // the segment's map; its decays and inputs stay in registers
-    float2 av[kSeg], bv[kSeg];
-    float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
-        if (s0 + k >= t.ntok) {   // past the sequence's end: the identity
-            av[k] = make_float2(1.f, 1.f);
-            bv[k] = make_float2(0.f, 0.f);
-            continue;
-        }
-        float m0, m1;
-        gate<T>(gr[k].f0(), av[k].x, m0);
-        gate<T>(gr[k].f1(), av[k].y, m1);
-        bv[k] = make_float2(m0 * xr[k].f0(), m1 * xr[k].f1());
-        if (DOCS && doc[s0 + k] >= 0) {
-            const float* in = a.init ? a.init + (int64_t)doc[s0 + k] * a.width + c0 : nullptr;
-            if (in && ok0) bv[k].x = fmaf(av[k].x, __ldg(in), bv[k].x);
-            if (in && ok1) bv[k].y = fmaf(av[k].y, __ldg(in + c1 - c0), bv[k].y);
-            av[k] = make_float2(0.f, 0.f);
-        }
-        B.x = fmaf(av[k].x, B.x, bv[k].x);
-        B.y = fmaf(av[k].y, B.y, bv[k].y);
-        A.x *= av[k].x;
-        A.y *= av[k].y;
-    }
-    mp.A[warp][lane] = A;
-    mp.B[warp][lane] = B;
-    __syncthreads();
-    float2 init = make_float2(0.f, 0.f);
-    if (!DOCS && a.init) {
-        const float* in = a.init + t.row * a.width + c0;
-        if (ok0) init.x = __ldg(in);
-        if (ok1) init.y = __ldg(in + c1 - c0);
-    }
-    if (warp == 0) compose<false>(mp, kWarps, lane, A, B);
-    float2 h = enter_tile(a, t, t.chunk, A, B, init, bf);
-    compose<false>(mp, warp, lane, A, B);
-    h.x = fmaf(A.x, h.x, B.x);
-    h.y = fmaf(A.y, h.y, B.y);
-    T* y = static_cast<T*>(a.y) + tok * a.width + c0;
-#pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
-        const bool in = s0 + k < t.ntok;
-        h.x = fmaf(av[k].x, h.x, bv[k].x);
-        h.y = fmaf(av[k].y, h.y, bv[k].y);
-        Two<T, PAIR>::store(y + (int64_t)k * a.width, ok0 && in, ok1 && in, h.x, h.y);
-        if (a.fin && in) {
-            const bool last = t.t0 + s0 + k == a.seqlen - 1;
-            int64_t at = -1;
-            if (DOCS) at = last ? a.ndocs - 1 : doc[s0 + k + 1] - 1;   // the document before the one that starts next
-            else if (last) at = t.row;
-            if (at >= 0) {
-                float* f = a.fin + at * a.width + c0;
-                if (ok0) f[0] = h.x;
-                if (ok1) f[c1 - c0] = h.y;
+    record_error(ws, SSD_ERR_TIMEOUT, where);
+    *(volatile int*)&sh.abort = 1;
+    return 0;
+}
+// A map (A, B): A >= 0 (or NaN) goes out with its sign bit set, so the word is not zero.
+__device__ __forceinline__ uint64_t map_word(float A, float B) {
+    return ((uint64_t)__float_as_uint(B) << 32) | (__float_as_uint(A) | 0x80000000u);
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, uint64_t* bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(tm), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
+                 "r"(ptx::smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, uint64_t src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     ptx::smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------- loading warp
+template <typename T, bool ROWS, bool DOCS, bool BWD>
+__device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared<Shape<T, ROWS, BWD>::TOK, DOCS>& sh) {
+    typedef Shape<T, ROWS, BWD> H;
+    const GateScanArgs& a = p.a;
+    const int lane = threadIdx.x & 31;
+    int n = 0, filled = 0;   // tiles, and phases of the stages' `full` begun (the end's among them)
+    auto send = [&](int j) {   // lane 0: tile j's outputs from its stage
+        if constexpr (!ROWS) {
+            const Tile& t = sh.tile[j % kRing];
+            const uint8_t* st = sm + (j % H::NS) * H::kStep;
+            if (BWD) {
+                tma_store_3d(&p.dg, st, t.group * kCh, (int)t.t0, t.row);
+                tma_store_3d(&p.dx, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
+            } else {
+                tma_store_3d(&p.y, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
             }
+            ptx::bulk_commit();
         }
-    }
-}
-
-template <typename T, bool PAIR, bool DOCS>
-__global__ void __launch_bounds__(kThreads) ssd_gate_scan_bwd_kernel(GateScanArgs a) {
-    __shared__ Maps mp;
-    __shared__ Before bf;
-    __shared__ int doc[DOCS ? kTok + 1 : 1];
-    __shared__ int slot;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Tile t;
-    take_tile<true>(a, t, &slot);
-    if (DOCS) {
-        find_docs(a, t.t0, doc);
-        if (blockIdx.x == 0) check_cu_seqlens(a.cu, a.ndocs, a.seqlen, a.ws, threadIdx.x, kThreads);
-    }
-    const int c0 = t.group * kCh + (PAIR ? 2 * lane : lane), c1 = c0 + (PAIR ? 1 : 32);
-    const bool ok0 = c0 < a.width, ok1 = c1 < a.width;
-    const int s0 = warp * kSeg;
-    const int64_t tok = t.row * a.seqlen + t.t0 + s0;
-    const T* g = static_cast<const T*>(a.g) + tok * a.g_stride + c0;
-    const T* x = static_cast<const T*>(a.x) + tok * a.x_stride + c0;
-    const T* dy = static_cast<const T*>(a.dy) + tok * a.width + c0;
-    Two<T, PAIR> gr[kSeg], xr[kSeg], dr[kSeg], hr;
-#pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
-        const bool in = s0 + k < t.ntok;
-        gr[k].load(g + k * a.g_stride, ok0 && in, ok1 && in);
-        xr[k].load(x + k * a.x_stride, ok0 && in, ok1 && in);
-        dr[k].load(dy + (int64_t)k * a.width, ok0 && in, ok1 && in);
-    }
-    // h before the segment: the output before it, or the state that enters the sequence
-    const bool first = t.t0 + s0 == 0;
-    const bool any = s0 < t.ntok && !first;
-    hr.load(static_cast<const T*>(a.y) + (tok - (any ? 1 : 0)) * a.width + c0, ok0 && any, ok1 && any);
-    float2 h = make_float2(hr.f0(), hr.f1());
-    if (first && !DOCS && a.init) {
-        const float* in = a.init + t.row * a.width + c0;
-        if (ok0) h.x = __ldg(in);
-        if (ok1) h.y = __ldg(in + c1 - c0);
-    }
-    // forwards through the segment: uv = d(h_t)/d(g_t) = (h_{t-1} - x) a (1 - a), mv = 1 - a
-    float2 uv[kSeg], mv[kSeg];
-#pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
-        float a0, a1;
-        const float x0 = xr[k].f0(), x1 = xr[k].f1();
-        gate<T>(gr[k].f0(), a0, mv[k].x);
-        gate<T>(gr[k].f1(), a1, mv[k].y);
-        if (DOCS && s0 + k < t.ntok && doc[s0 + k] >= 0) {
-            h = make_float2(0.f, 0.f);
-            const float* in = a.init ? a.init + (int64_t)doc[s0 + k] * a.width + c0 : nullptr;
-            if (in && ok0) h.x = __ldg(in);
-            if (in && ok1) h.y = __ldg(in + c1 - c0);
-        }
-        const float e0 = h.x - x0, e1 = h.y - x1;
-        uv[k].x = e0 * a0 * mv[k].x;
-        uv[k].y = e1 * a1 * mv[k].y;
-        h.x = fmaf(a0, h.x, mv[k].x * x0);
-        h.y = fmaf(a1, h.y, mv[k].y * x1);
-    }
-    // backwards: the map of mu over the segment.  dfin enters at a document's (or row's) last
-    // token, which cuts the map.
-    float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
-    auto ends = [&](int k) { return DOCS && (doc[s0 + k + 1] >= 0 || t.t0 + s0 + k == a.seqlen - 1); };
-    auto dfin_of = [&](int k) {
-        float2 d = make_float2(0.f, 0.f);
-        const int64_t at = t.t0 + s0 + k == a.seqlen - 1 ? a.ndocs - 1 : doc[s0 + k + 1] - 1;
-        if (a.dfin && at >= 0) {
-            const float* f = a.dfin + at * a.width + c0;
-            if (ok0) d.x = __ldg(f);
-            if (ok1) d.y = __ldg(f + c1 - c0);
-        }
-        return d;
     };
-#pragma unroll
-    for (int k = kSeg - 1; k >= 0; --k) {
-        if (s0 + k >= t.ntok) continue;
-        if (DOCS && ends(k)) {
-            A = make_float2(0.f, 0.f);
-            B = dfin_of(k);
+    bool go = true;
+    for (;; ++n) {
+        uint32_t k = 0;
+        if (lane == 0) k = a.nchunks > 1 ? atomicAdd(a.ticket, 1u) : (uint32_t)(blockIdx.x + gridDim.x * n);
+        k = __shfl_sync(0xffffffffu, k, 0);
+        const Tile t = tile_of<BWD, H::TOK>(a, k);
+        // the slot's last tile, n - kRing, is done with: a later one's outputs have been waited for
+        if (lane == 0) sh.tile[n % kRing] = t;
+        if (DOCS && t.ntok) find_docs<H::TOK>(a, t.t0, sh.doc[n % kRing]);
+        const int st = n % H::NS;
+        if (n >= H::NS) {
+            if (lane == 0) {
+                go = bar_wait(sh, a.ws, &sh.done[st], ((n / H::NS) - 1) & 1, kWhereDone);
+                if (go) send(n - H::NS);
+                if (!ROWS) ptx::bulk_wait_read0();
+            }
+            go = __shfl_sync(0xffffffffu, (int)go, 0) != 0;
+            if (!go) break;
         }
-        const float a0 = 1.f - mv[k].x, a1 = 1.f - mv[k].y;
-        B.x = a0 * (dr[k].f0() + B.x);
-        B.y = a1 * (dr[k].f1() + B.y);
-        A.x *= a0;
-        A.y *= a1;
-    }
-    mp.A[warp][lane] = A;
-    mp.B[warp][lane] = B;
-    __syncthreads();
-    float2 last = make_float2(0.f, 0.f);
-    if (!DOCS && a.dfin) {
-        const float* f = a.dfin + t.row * a.width + c0;
-        if (ok0) last.x = __ldg(f);
-        if (ok1) last.y = __ldg(f + c1 - c0);
-    }
-    if (warp == 0) compose<true>(mp, kWarps, lane, A, B);
-    float2 mu = enter_tile(a, t, a.nchunks - 1 - t.chunk, A, B, last, bf);
-    compose<true>(mp, kWarps - 1 - warp, lane, A, B);
-    mu.x = fmaf(A.x, mu.x, B.x);
-    mu.y = fmaf(A.y, mu.y, B.y);
-    T* dg = static_cast<T*>(a.dg) + tok * a.g_stride + c0;
-    T* dx = static_cast<T*>(a.dx) + tok * a.x_stride + c0;
+        __syncwarp();
+        uint64_t* full = &sh.full[st];
+        if (!t.ntok) {
+            if (lane == 0) ptx::mbar_arrive(full);
+            ++filled;
+            break;
+        }
+        ++filled;
+        uint8_t* dst = sm + st * H::kStep;
+        if constexpr (!ROWS) {
+            if (lane == 0) {
+                ptx::mbar_expect_tx(full, H::STAGE);
+                const int c = t.group * kCh, t0 = (int)t.t0;
+                tma_load_3d(dst, &p.g, full, c, t0, t.row);
+                tma_load_3d(dst + H::ARR, &p.x, full, c, t0, t.row);
+                if (BWD) {
+                    tma_load_3d(dst + 2 * H::ARR, &p.dy, full, c, t0, t.row);
+                    // the h before each segment (before the sequence: out of range, zeros)
+                    for (int s = 0; s < kMain; ++s)
+                        tma_load_3d(dst + H::NA * H::ARR + s * H::PITCH, &p.y, full, c, t0 + s * H::SEG - 1, t.row);
+                }
+            }
+        } else {
+            // Windows of whole 16-byte units around each row's channels.  A unit that holds one byte of a
+            // tensor lies in the tensor's memory pages, so the bytes around its ends can be read; no one uses them.
+            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0;
+            const int cols = a.width - t.group * kCh < kCh ? a.width - t.group * kCh : kCh;
+            const void* base[3] = {a.g, a.x, a.dy};
+            const int64_t pitch[3] = {a.g_stride, a.x_stride, a.width};
+            uint32_t total = 0;
+            for (int pass = 0; pass < 2; ++pass) {
+                auto row = [&](uint64_t at, uint8_t* to) {
+                    const uint64_t lo = at & ~15ull, hi = (at + (uint32_t)cols * H::ES + 15) & ~15ull;
+                    if (pass == 0) total += (uint32_t)(hi - lo);
+                    else bulk_load(to, lo, (uint32_t)(hi - lo), full);
+                };
 #pragma unroll
-    for (int k = kSeg - 1; k >= 0; --k) {
-        const bool in = s0 + k < t.ntok;
-        if (!in) continue;
-        if (DOCS && ends(k)) mu = dfin_of(k);
-        const float l0 = dr[k].f0() + mu.x, l1 = dr[k].f1() + mu.y;
-        Two<T, PAIR>::store(dg + k * a.g_stride, ok0, ok1, l0 * uv[k].x, l1 * uv[k].y);
-        Two<T, PAIR>::store(dx + k * a.x_stride, ok0, ok1, l0 * mv[k].x, l1 * mv[k].y);
-        mu.x = (1.f - mv[k].x) * l0;
-        mu.y = (1.f - mv[k].y) * l1;
-        if (a.dinit) {
-            int64_t at = -1;
-            if (DOCS) at = doc[s0 + k];
-            else if (t.t0 + s0 + k == 0) at = t.row;
-            if (at >= 0) {
-                float* f = a.dinit + at * a.width + c0;
-                if (ok0) f[0] = mu.x;
-                if (ok1) f[c1 - c0] = mu.y;
+                for (int r = 0; r < H::NA; ++r)
+                    for (int k = lane; k < t.ntok; k += 32)
+                        row((uint64_t)(uintptr_t)base[r] + (uint64_t)((tok + k) * pitch[r] + t.group * kCh) * H::ES,
+                            dst + r * H::ARR + k * H::PITCH);
+                if (BWD && lane < kMain && lane * H::SEG < t.ntok && t.t0 + lane * H::SEG > 0)
+                    row((uint64_t)(uintptr_t)a.y + (uint64_t)((tok + lane * H::SEG - 1) * a.width + t.group * kCh) * H::ES,
+                        dst + H::NA * H::ARR + lane * H::PITCH);
+                if (pass == 0) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+                    if (lane == 0) ptx::mbar_expect_tx(full, total);
+                    __syncwarp();
+                }
             }
         }
+    }
+    if (lane != 0) return;
+    // the outputs of the tiles still in stages, then everything in flight
+    const int first = n - H::NS + 1 > 0 ? n - H::NS + 1 : 0;
+    for (int j = first; go && j < n; ++j) {
+        go = bar_wait(sh, a.ws, &sh.done[j % H::NS], (j / H::NS) & 1, kWhereDone);
+        if (go) send(j);
+    }
+    for (int st = 0; st < H::NS && st < filled; ++st) {
+        const int last = ((filled - 1 - st) / H::NS) * H::NS + st;
+        if (!ptx::mbar_wait(&sh.full[st], (last / H::NS) & 1, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereStage);
+    }
+    if (!ROWS) ptx::bulk_wait0();
+}
+
+// ---------------------------------------------------------------------- hand-over warps
+template <bool REV, typename S>
+__device__ __forceinline__ void hand_over(const GateScanArgs& a, S& sh) {
+    const int c = threadIdx.x - 32 * kMain, lane = threadIdx.x & 31;   // channel of the tile
+    for (int n = 0;; ++n) {
+        if (!bar_wait(sh, a.ws, &sh.maps, n & 1, kWhereMaps)) return;
+        const Tile t = sh.tile[n % kRing];
+        if (!t.ntok) return;
+        const int ch = t.group * kCh + c;
+        float2 m[kMain];
+        float A = 1.f, B = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMain; ++k) {
+            m[k] = sh.seg[REV ? kMain - 1 - k : k][c];
+            B = fmaf(m[k].x, B, m[k].y);
+            A *= m[k].x;
+        }
+        const int in_block = t.step % kBlock, block = t.step / kBlock;
+        const bool more = t.step != a.nchunks - 1, closes = in_block == kBlock - 1;
+        const int64_t line = (int64_t)t.row * a.ngroups + t.group;
+        uint64_t* maps = a.maps + (line * a.nchunks + (int64_t)block * kBlock) * kCh + c;
+        uint64_t* carry = a.carry + (line * a.nblocks + block) * kCh + c;
+        if (more && !closes) leave(maps + in_block * kCh, map_word(A, B));
+        // the predecessors' maps, all asked for before the first is waited for
+        uint64_t w[kBlock - 1], cw = 1;
+#pragma unroll
+        for (int p = 0; p < kBlock - 1; ++p) w[p] = p < in_block ? peek(maps + p * kCh) : 0;
+        if (block > 0) cw = peek(carry - kCh);
+        float h = 0.f;
+        if (block > 0) h = __uint_as_float((uint32_t)(await(carry - kCh, cw, sh, a.ws, kWhereBlock) >> 32));
+        else if (!a.cu && a.enter && ch < a.width) h = __ldg(a.enter + (int64_t)t.row * a.width + ch);
+#pragma unroll
+        for (int p = 0; p < kBlock - 1; ++p)
+            if (p < in_block) {
+                const uint64_t v = await(maps + p * kCh, w[p], sh, a.ws, kWhereTile);
+                h = fmaf(__uint_as_float((uint32_t)v & 0x7FFFFFFFu), h, __uint_as_float((uint32_t)(v >> 32)));
+            }
+#pragma unroll
+        for (int k = 0; k < kMain; ++k) {
+            sh.seg[REV ? kMain - 1 - k : k][c].x = h;
+            h = fmaf(m[k].x, h, m[k].y);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.states);
+        if (more && closes) leave(carry, ((uint64_t)__float_as_uint(h) << 32) | 1u);
+        // the state that leaves the sequence: the final state, or the initial state's gradient
+        if (!more && !a.cu && a.leave && ch < a.width) a.leave[(int64_t)t.row * a.width + ch] = h;
+    }
+}
+
+// ---------------------------------------------------------------------- main warps
+// A thread's two channels: neighbours in aligned tiles, 32 apart in windows of rows.
+template <typename T, bool ROWS, bool DOCS, bool BWD>
+struct Main {
+    typedef Shape<T, ROWS, BWD> H;
+    typedef typename PairWord<T>::type W;
+    static constexpr int SEG = H::SEG, kApart = ROWS ? 32 : 1;
+    const GateScanArgs& a;
+    Shared<H::TOK, DOCS>& sh;
+    int lane, warp;
+    // the tile at hand
+    Tile t;
+    const int* doc;
+    uint8_t* st;       // its stage, at this thread's segment and channels
+    int s0, c0;        // the segment's first token in the tile; the thread's first channel
+    bool ok0, ok1;
+    uint32_t skew[3], step[3];   // ROWS: low bits of the first row's address, and of the rows' pitch
+
+    __device__ __forceinline__ void open(const Tile& tile, const int* d, uint8_t* stage) {
+        t = tile;
+        doc = d;
+        s0 = warp * SEG;
+        c0 = t.group * kCh + (ROWS ? lane : 2 * lane);
+        ok0 = c0 < a.width;
+        ok1 = c0 + kApart < a.width;
+        st = stage + s0 * H::PITCH + (ROWS ? lane : 2 * lane) * H::ES;
+        if constexpr (ROWS) {
+            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
+            const void* base[3] = {a.g, a.x, a.dy};
+            const int64_t pitch[3] = {a.g_stride, a.x_stride, a.width};
+#pragma unroll
+            for (int r = 0; r < H::NA; ++r) {
+                skew[r] = (uint32_t)(uintptr_t)base[r] + (uint32_t)((tok * pitch[r] + t.group * kCh) * H::ES);
+                step[r] = (uint32_t)(pitch[r] * H::ES);
+            }
+        }
+    }
+    static __device__ __forceinline__ f2 widen(W w) {
+        if constexpr (sizeof(T) == 2) return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        else return w;
+    }
+    static __device__ __forceinline__ W narrow(f2 v) {
+        if constexpr (sizeof(T) == 2) {
+            const float2 f = un(v);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+            return *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+            return v;
+        }
+    }
+    static __device__ __forceinline__ f2 two(const uint8_t* q) {   // ROWS: channels kApart apart, element-aligned
+        if constexpr (sizeof(T) == 2)
+            return pk(__uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(q) << 16),
+                      __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(q + 64) << 16));
+        else
+            return pk(*reinterpret_cast<const float*>(q), *reinterpret_cast<const float*>(q + 128));
+    }
+    // operand r (g, x, dy) at token k of the segment
+    __device__ __forceinline__ f2 in(int r, int k) const {
+        const uint8_t* q = st + r * H::ARR + k * H::PITCH;
+        if constexpr (ROWS) return two(q + ((skew[r] + k * step[r]) & 15));
+        else return widen(*reinterpret_cast<const W*>(q));
+    }
+    // result over operand r's place in the stage, or straight to memory
+    __device__ __forceinline__ void out(int r, T* base, int64_t pitch, int k, f2 v) const {
+        const W w = narrow(v);
+        if constexpr (!ROWS) {
+            *reinterpret_cast<W*>(st + r * H::ARR + k * H::PITCH) = w;
+        } else {
+            T* q = base + ((int64_t)t.row * a.seqlen + t.t0 + s0 + k) * pitch + c0;
+            const T* e = reinterpret_cast<const T*>(&w);
+            if (ok0) q[0] = e[0];
+            if (ok1) q[kApart] = e[1];
+        }
+    }
+    // two channels of row `row` of a (rows, width) fp32 array, zero without one
+    __device__ __forceinline__ f2 state(const float* p, int64_t row) const {
+        if (!p) return pk(0.f, 0.f);
+        p += row * a.width + c0;
+        return pk(ok0 ? __ldg(p) : 0.f, ok1 ? __ldg(p + kApart) : 0.f);
+    }
+    __device__ __forceinline__ void put_state(float* p, int64_t row, f2 v) const {
+        const float2 f = un(v);
+        p += row * a.width + c0;
+        if (ok0) p[0] = f.x;
+        if (ok1) p[kApart] = f.y;
+    }
+    __device__ __forceinline__ void put_map(f2 A, f2 B) const {
+        const float2 fa = un(A), fb = un(B);
+        float2* q = sh.seg[warp];
+        if constexpr (ROWS) {
+            q[lane] = make_float2(fa.x, fb.x);
+            q[lane + 32] = make_float2(fa.y, fb.y);
+        } else {
+            *reinterpret_cast<float4*>(q + 2 * lane) = make_float4(fa.x, fb.x, fa.y, fb.y);
+        }
+    }
+    __device__ __forceinline__ f2 entered() const {
+        const float2* q = sh.seg[warp];
+        if constexpr (ROWS) return pk(q[lane].x, q[lane + 32].x);
+        const float4 e = *reinterpret_cast<const float4*>(q + 2 * lane);
+        return pk(e.x, e.z);
+    }
+    __device__ __forceinline__ bool starts(int k) const { return DOCS && doc[s0 + k] >= 0; }
+    // whether token k of the segment ends a document, and which
+    __device__ __forceinline__ bool ends(int k) const {
+        return DOCS && (doc[s0 + k + 1] >= 0 || t.t0 + s0 + k == a.seqlen - 1);
+    }
+    __device__ __forceinline__ int ending(int k) const {
+        return t.t0 + s0 + k == a.seqlen - 1 ? a.ndocs - 1 : doc[s0 + k + 1] - 1;
+    }
+
+    f2 mv[SEG], uv[BWD ? SEG : 1];
+
+    // WHOLE: every token of the segment is inside the sequence
+    template <bool WHOLE>
+    __device__ __forceinline__ void first_fwd() {
+        f2 A = pk(1.f, 1.f), B = pk(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < SEG; ++k) {
+            if (!WHOLE && s0 + k >= t.ntok) break;
+            f2 av;
+            gate2<T>(in(0, k), av, mv[k]);
+            if (starts(k)) {
+                A = pk(0.f, 0.f);
+                B = state(a.init, doc[s0 + k]);
+            }
+            A = mul(A, av);
+            B = fma2(av, B, mul(mv[k], in(1, k)));
+        }
+        put_map(A, B);
+    }
+    template <bool WHOLE>
+    __device__ __forceinline__ void second_fwd() {
+        f2 h = entered();
+        const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+#pragma unroll
+        for (int k = 0; k < SEG; ++k) {
+            if (!WHOLE && s0 + k >= t.ntok) break;
+            if (starts(k)) h = state(a.init, doc[s0 + k]);
+            h = fma2(fma2(mv[k], minus, one), h, mul(mv[k], in(1, k)));
+            out(1, static_cast<T*>(a.y), a.width, k, h);
+            if (DOCS && a.leave && ends(k)) {
+                const int at = ending(k);
+                if (at >= 0) put_state(a.leave, at, h);
+            }
+        }
+    }
+    template <bool WHOLE>
+    __device__ __forceinline__ void first_bwd() {
+        const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+        f2 h;
+        if (t.t0 + s0 == 0) {
+            h = DOCS ? pk(0.f, 0.f) : state(a.init, t.row);
+        } else {
+            const uint8_t* q = st - s0 * H::PITCH + H::NA * H::ARR + warp * H::PITCH;
+            if constexpr (ROWS) {
+                const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0 - 1;
+                h = two(q + (((uint32_t)(uintptr_t)a.y + (uint32_t)((tok * a.width + t.group * kCh) * H::ES)) & 15));
+            } else {
+                h = widen(*reinterpret_cast<const W*>(q));
+            }
+        }
+        // forwards through the segment: u = d(h_t)/d(g_t) = (h_{t-1} - x) a (1 - a)
+#pragma unroll
+        for (int k = 0; k < SEG; ++k) {
+            if (!WHOLE && s0 + k >= t.ntok) break;
+            f2 av;
+            const f2 xv = in(1, k);
+            gate2<T>(in(0, k), av, mv[k]);
+            if (starts(k)) h = state(a.init, doc[s0 + k]);
+            uv[k] = mul(fma2(xv, minus, h), mul(av, mv[k]));
+            h = fma2(av, h, mul(mv[k], xv));
+        }
+        // backwards: the map of mu over the segment
+        f2 A = one, B = pk(0.f, 0.f);
+#pragma unroll
+        for (int k = SEG - 1; k >= 0; --k) {
+            if (!WHOLE && s0 + k >= t.ntok) continue;
+            if (ends(k)) {
+                const int at = ending(k);
+                A = pk(0.f, 0.f);
+                B = at >= 0 ? state(a.enter, at) : A;
+            }
+            const f2 av = fma2(mv[k], minus, one);
+            B = mul(av, add(in(2, k), B));
+            A = mul(A, av);
+        }
+        put_map(A, B);
+    }
+    template <bool WHOLE>
+    __device__ __forceinline__ void second_bwd() {
+        f2 mu = entered();
+        const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+#pragma unroll
+        for (int k = SEG - 1; k >= 0; --k) {
+            if (!WHOLE && s0 + k >= t.ntok) continue;
+            if (ends(k)) {
+                const int at = ending(k);
+                mu = at >= 0 ? state(a.enter, at) : pk(0.f, 0.f);
+            }
+            const f2 lam = add(in(2, k), mu);
+            out(0, static_cast<T*>(a.dg), a.g_stride, k, mul(lam, uv[k]));
+            out(1, static_cast<T*>(a.dx), a.x_stride, k, mul(lam, mv[k]));
+            mu = mul(fma2(mv[k], minus, one), lam);
+            if (DOCS && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
+        }
+    }
+
+    __device__ __forceinline__ void run(uint8_t* sm) {
+        for (int n = 0;; ++n) {
+            const int stage = n % H::NS;
+            if (!bar_wait(sh, a.ws, &sh.full[stage], (n / H::NS) & 1, kWhereStage)) return;
+            open(sh.tile[n % kRing], sh.doc[DOCS ? n % kRing : 0], sm + stage * H::kStep);
+            const bool whole = s0 + SEG <= t.ntok;
+            if (t.ntok) {
+                if constexpr (BWD) {
+                    if (whole) first_bwd<true>();
+                    else first_bwd<false>();
+                } else {
+                    if (whole) first_fwd<true>();
+                    else first_fwd<false>();
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.maps);
+            if (!t.ntok) return;
+            if (!bar_wait(sh, a.ws, &sh.states, n & 1, kWhereState)) return;
+            if constexpr (BWD) {
+                if (whole) second_bwd<true>();
+                else second_bwd<false>();
+            } else {
+                if (whole) second_fwd<true>();
+                else second_fwd<false>();
+            }
+            if (!ROWS) ptx::fence_proxy_async();   // the outputs in the stage, before they are sent off
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.done[stage]);
+        }
+    }
+};
+
+template <typename T, bool ROWS, bool DOCS, bool BWD>
+__global__ void __launch_bounds__(kThreads, 2) ssd_gate_scan_kernel(const __grid_constant__ ScanParams p) {
+    typedef Shape<T, ROWS, BWD> H;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 127) & ~(uintptr_t)127);
+    __shared__ __align__(16) Shared<H::TOK, DOCS> sh;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 3; ++i) {
+            ptx::mbar_init(&sh.full[i], 1);
+            ptx::mbar_init(&sh.done[i], kMain);
+        }
+        ptx::mbar_init(&sh.maps, kMain);
+        ptx::mbar_init(&sh.states, 2);
+        sh.abort = 0;
+        sh.never = 0;
+        ptx::mbar_fence_init();
+    }
+    __syncthreads();
+    if (warp < kMain) {
+        Main<T, ROWS, DOCS, BWD> m = {p.a, sh, (int)(threadIdx.x & 31), warp};
+        m.run(sm);
+    } else if (warp < kMain + 2) {
+        hand_over<BWD>(p.a, sh);
+    } else {
+        if (DOCS && blockIdx.x == 0) check_cu_seqlens(p.a.cu, p.a.ndocs, p.a.seqlen, p.a.ws, threadIdx.x & 31, 32);
+        loading<T, ROWS, DOCS, BWD>(p, sm, sh);
     }
 }
 
@@ -478,9 +699,9 @@ __global__ void __launch_bounds__(256) ssd_gate_scan_step_kernel(GateStepArgs a)
     sr.get(h);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        float d, m;
-        gate<float>(g[j], d, m);
-        h[j] = fmaf(d, h[j], m * x[j]);
+        float a, m;
+        gate<float>(g[j], a, m);
+        h[j] = fmaf(a, h[j], m * x[j]);
     }
     sr.set(h);
     sr.store(a.state_out + b * a.width + c);
@@ -491,56 +712,91 @@ __global__ void __launch_bounds__(256) ssd_gate_scan_step_kernel(GateStepArgs a)
 
 bool on(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
+// A (batch, seqlen, width) tensor of token stride `stride`, in boxes of kCh channels x `tokens`.
+bool encode_3d(CUtensorMap* tm, const void* base, int es, const GateScanArgs& a, int64_t stride, int tokens) {
+    const auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)a.width, (cuuint64_t)a.seqlen, (cuuint64_t)a.batch};
+    cuuint64_t strides[2] = {(cuuint64_t)(stride * es), (cuuint64_t)(a.seqlen * stride * es)};
+    cuuint32_t box[3] = {(cuuint32_t)kCh, (cuuint32_t)tokens, 1};
+    cuuint32_t step[3] = {1, 1, 1};
+    return enc(tm, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base),
+               dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, bool ROWS, bool DOCS, bool BWD>
+cudaError_t launch_one(const ScanParams& p, cudaStream_t st) {
+    const auto kern = ssd_gate_scan_kernel<T, ROWS, DOCS, BWD>;
+    constexpr size_t smem = Shape<T, ROWS, BWD>::kSmem;
+    // once per device and kernel: the shared-memory opt-in
+    static std::atomic<uint8_t> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        ready[dev].store(1, std::memory_order_release);
+    }
+    // two CTAs per SM; with tickets any number of them finishes the work
+    const int nsm = device_sms();
+    const int64_t most = 2 * (int64_t)(nsm > 0 ? nsm : 152);
+    kern<<<(unsigned)(p.a.ntiles < most ? p.a.ntiles : most), kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T, bool BWD>
 cudaError_t launch_typed(const GateScanArgs& a, cudaStream_t st) {
-    const size_t two = 2 * sizeof(T);
-    bool pair = a.width % 2 == 0 && a.g_stride % 2 == 0 && a.x_stride % 2 == 0 && on(a.g, two) && on(a.x, two) && on(a.y, two);
-    if (BWD) pair = pair && on(a.dy, two) && on(a.dg, two) && on(a.dx, two);
-    const bool docs = a.cu != nullptr;
-    void (*kern)(GateScanArgs);
-    if (BWD)
-        kern = pair ? (docs ? ssd_gate_scan_bwd_kernel<T, true, true> : ssd_gate_scan_bwd_kernel<T, true, false>)
-                    : (docs ? ssd_gate_scan_bwd_kernel<T, false, true> : ssd_gate_scan_bwd_kernel<T, false, false>);
-    else
-        kern = pair ? (docs ? ssd_gate_scan_kernel<T, true, true> : ssd_gate_scan_kernel<T, true, false>)
-                    : (docs ? ssd_gate_scan_kernel<T, false, true> : ssd_gate_scan_kernel<T, false, false>);
-    const int64_t grid = a.nchunks * a.batch * a.ngroups;
-    kern<<<(unsigned)grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    ScanParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = a;
+    constexpr int es = sizeof(T), unit = 16 / es, tok = Shape<T, false, BWD>::TOK;
+    bool tiles = a.width % unit == 0 && a.g_stride % unit == 0 && a.x_stride % unit == 0 && on(a.g, 16) && on(a.x, 16) && on(a.y, 16);
+    if (BWD) tiles = tiles && on(a.dy, 16) && on(a.dg, 16) && on(a.dx, 16);
+    if (tiles) {
+        bool ok = encode_3d(&p.g, a.g, es, a, a.g_stride, tok) && encode_3d(&p.x, a.x, es, a, a.x_stride, tok) &&
+                  encode_3d(&p.y, a.y, es, a, a.width, BWD ? 1 : tok);
+        if (BWD)
+            ok = ok && encode_3d(&p.dy, a.dy, es, a, a.width, tok) && encode_3d(&p.dg, a.dg, es, a, a.g_stride, tok) &&
+                 encode_3d(&p.dx, a.dx, es, a, a.x_stride, tok);
+        if (!ok) return cudaErrorInvalidValue;
+        return a.cu ? launch_one<T, false, true, BWD>(p, st) : launch_one<T, false, false, BWD>(p, st);
+    }
+    return a.cu ? launch_one<T, true, true, BWD>(p, st) : launch_one<T, true, false, BWD>(p, st);
 }
 
 }  // namespace
 
-GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width) {
+GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width, int dtype, bool bwd) {
     GateScanLayout l;
-    l.nchunks = (seqlen + kTok - 1) / kTok;
+    const int tok = scan_seg(bwd, dtype) * kMain;
+    l.nchunks = (seqlen + tok - 1) / tok;
     l.ngroups = (width + kCh - 1) / kCh;
-    const size_t lines = (size_t)batch * l.ngroups, nblocks = (size_t)((l.nchunks + kBlock - 1) / kBlock);
+    l.nblocks = (l.nchunks + kBlock - 1) / kBlock;
+    const size_t lines = (size_t)batch * l.ngroups;
     l.ticket_off = sizeof(WsHeader);
-    l.map_flag_off = l.ticket_off + 256;
-    l.carry_flag_off = l.map_flag_off + lines * l.nchunks * 4;
-    l.clear_bytes = align_up(l.carry_flag_off + lines * nblocks * 4, 256);
-    l.maps_off = l.clear_bytes;
-    l.carry_off = l.maps_off + lines * l.nchunks * 32 * 16;
-    l.total = l.carry_off + lines * nblocks * 32 * 8;
-    if (l.nchunks == 1) l.total = l.clear_bytes = sizeof(WsHeader);
+    l.maps_off = l.ticket_off + 256;
+    l.carry_off = l.maps_off + lines * l.nchunks * kCh * 8;
+    l.total = l.carry_off + lines * l.nblocks * kCh * 8;
+    if (l.nchunks == 1) l.total = sizeof(WsHeader);
     return l;
 }
 
 cudaError_t launch_gate_scan(const GateScanArgs& args, void* workspace, bool bwd, cudaStream_t st) {
     GateScanArgs a = args;
-    const GateScanLayout l = gate_scan_layout(a.batch, a.seqlen, a.width);
+    const GateScanLayout l = gate_scan_layout(a.batch, a.seqlen, a.width, a.dtype, bwd);
     char* w = static_cast<char*>(workspace);
     a.nchunks = l.nchunks;
     a.ngroups = l.ngroups;
+    a.nblocks = l.nblocks;
+    a.ntiles = (uint32_t)(a.batch * l.ngroups * l.nchunks);
     a.ws = reinterpret_cast<WsHeader*>(w);
     a.ticket = reinterpret_cast<uint32_t*>(w + l.ticket_off);
-    a.map_flag = reinterpret_cast<uint32_t*>(w + l.map_flag_off);
-    a.carry_flag = reinterpret_cast<uint32_t*>(w + l.carry_flag_off);
-    a.maps = reinterpret_cast<float4*>(w + l.maps_off);
-    a.carry = reinterpret_cast<float2*>(w + l.carry_off);
-    // status word, tickets and flags start from zero
-    const cudaError_t e = cudaMemsetAsync(workspace, 0, l.clear_bytes, st);
+    a.maps = reinterpret_cast<uint64_t*>(w + l.maps_off);
+    a.carry = reinterpret_cast<uint64_t*>(w + l.carry_off);
+    // status word, tickets, maps and carried states start from zero
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, l.total, st);
     if (e != cudaSuccess) return e;
     if (a.dtype == SSD_BF16) return bwd ? launch_typed<bf16_t, true>(a, st) : launch_typed<bf16_t, false>(a, st);
     return bwd ? launch_typed<float, true>(a, st) : launch_typed<float, false>(a, st);

@@ -165,9 +165,11 @@ struct AddNormBwdArgs {
     int rows_per_cta;
 };
 
-// Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of kScanTok tokens x
-// kScanCh channels; a state is handed over once per kScanBlock tiles of a sequence.
-constexpr int kScanTok = 128, kScanCh = 64, kScanBlock = 16;
+// Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of eight segments x kScanCh
+// channels.  A segment holds 16 tokens where that many fit a thread's registers (forward, bf16), else 8.
+// A state is handed over once per kScanBlock tiles of a sequence.
+constexpr int kScanCh = 64, kScanBlock = 16, kScanMinTok = 64;
+constexpr int scan_seg(bool bwd, int dtype) { return !bwd && dtype == 1 /* SSD_BF16 */ ? 16 : 8; }
 struct GateScanArgs {
     int64_t batch, seqlen;
     int width;
@@ -179,26 +181,27 @@ struct GateScanArgs {
     const float* init;
     const int32_t* cu;
     void* y;               // forward: written; backward: the forward's output
-    float* fin;
     const void* dy;
-    const float* dfin;
     void* dg;
     void* dx;
-    float* dinit;
+    // per row or document, what enters the walk and what leaves it: initial and final states forwards,
+    // the final states' and the initial states' gradients backwards
+    const float* enter;
+    float* leave;
     // set at the launch
     WsHeader* ws;
     uint32_t* ticket;
-    uint32_t* map_flag;
-    uint32_t* carry_flag;
-    float4* maps;
-    float2* carry;
+    uint64_t* maps;        // per tile and channel
+    uint64_t* carry;       // per block and channel
     int64_t nchunks;       // tiles along a sequence
+    int64_t nblocks;       // blocks of tiles along a sequence
     int ngroups;           // channel groups
+    uint32_t ntiles;
 };
 struct GateScanLayout {    // workspace, in bytes
-    int64_t nchunks;
+    int64_t nchunks, nblocks;
     int ngroups;
-    size_t ticket_off, map_flag_off, carry_flag_off, clear_bytes, maps_off, carry_off, total;
+    size_t ticket_off, maps_off, carry_off, total;
 };
 struct GateStepArgs {
     int64_t batch;
@@ -293,7 +296,7 @@ cudaError_t launch_gate_norm(const GateNormArgs& a, cudaStream_t st);
 cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
 int64_t add_norm_bwd_shares(int64_t rows, int width);   // row slots of the backward
 cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
-GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width);
+GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width, int dtype, bool bwd);
 cudaError_t launch_gate_scan(const GateScanArgs& a, void* workspace, bool bwd, cudaStream_t st);
 cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st);
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // NULL when the driver has none

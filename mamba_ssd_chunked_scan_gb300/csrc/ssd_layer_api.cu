@@ -59,9 +59,9 @@ int check_scan(const ssd_gate_scan_params_t* p) {
     if (p->ndocs > 0 && p->batch != 1) return SSD_ERR_INVALID_ARG;
     const int64_t big = (int64_t)1 << 31;
     // token offsets and tile numbers are 32-bit; element offsets are 64-bit
-    if (p->seqlen >= big - kScanTok || p->batch >= big || p->batch * p->seqlen >= big << 8 || p->g_stride >= big || p->x_stride >= big)
+    if (p->seqlen >= big - 256 || p->batch >= big || p->batch * p->seqlen >= big << 8 || p->g_stride >= big || p->x_stride >= big)
         return SSD_ERR_UNSUPPORTED;
-    const int64_t tiles = ((p->seqlen + kScanTok - 1) / kScanTok) * ((p->width + kScanCh - 1) / kScanCh);
+    const int64_t tiles = ((p->seqlen + kScanMinTok - 1) / kScanMinTok) * ((p->width + kScanCh - 1) / kScanCh);
     if (tiles >= big / p->batch) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -181,7 +181,9 @@ int ssd_add_norm_bwd(int64_t rows, int32_t width, int32_t dtype, int32_t residua
 
 size_t ssd_gate_scan_workspace_size(const ssd_gate_scan_params_t* p) {
     if (check_scan(p) != SSD_OK) return 0;
-    return gate_scan_layout(p->batch, p->seqlen, p->width).total;
+    const size_t f = gate_scan_layout(p->batch, p->seqlen, p->width, p->dtype, false).total;
+    const size_t b = gate_scan_layout(p->batch, p->seqlen, p->width, p->dtype, true).total;
+    return f > b ? f : b;
 }
 
 int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x, const float* initial_states,
@@ -194,7 +196,7 @@ int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x,
     if (!aligned(g, es) || !aligned(x, es) || !aligned(y, es) || !aligned(initial_states, 4) ||
         !aligned(final_states, 4) || !aligned(cu_seqlens, 4))
         return SSD_ERR_INVALID_ARG;
-    const size_t need = gate_scan_layout(p->batch, p->seqlen, p->width).total;
+    const size_t need = ssd_gate_scan_workspace_size(p);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
     const int64_t rows = p->batch * p->seqlen, nst = p->ndocs > 0 ? p->ndocs : p->batch;
     const Mat in[] = {{g, rows, p->width, p->g_stride, es}, {x, rows, p->width, p->x_stride, es},
@@ -210,7 +212,8 @@ int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x,
     GateScanArgs a = {};
     a.batch = p->batch; a.seqlen = p->seqlen; a.width = p->width; a.dtype = p->dtype; a.ndocs = p->ndocs;
     a.g_stride = p->g_stride; a.x_stride = p->x_stride;
-    a.g = g; a.x = x; a.init = initial_states; a.cu = cu_seqlens; a.y = y; a.fin = final_states;
+    a.g = g; a.x = x; a.init = initial_states; a.cu = cu_seqlens; a.y = y;
+    a.enter = initial_states; a.leave = final_states;
     return launch_gate_scan(a, workspace, false, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -226,7 +229,7 @@ int ssd_gate_scan_bwd(const ssd_gate_scan_params_t* p, const void* g, const void
         !aligned(dx, es) || !aligned(initial_states, 4) || !aligned(dfinal_states, 4) || !aligned(dinitial_states, 4) ||
         !aligned(cu_seqlens, 4))
         return SSD_ERR_INVALID_ARG;
-    const size_t need = gate_scan_layout(p->batch, p->seqlen, p->width).total;
+    const size_t need = ssd_gate_scan_workspace_size(p);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
     const int64_t rows = p->batch * p->seqlen, nst = p->ndocs > 0 ? p->ndocs : p->batch;
     const int64_t w = p->width;
@@ -245,7 +248,7 @@ int ssd_gate_scan_bwd(const ssd_gate_scan_params_t* p, const void* g, const void
     a.batch = p->batch; a.seqlen = p->seqlen; a.width = p->width; a.dtype = p->dtype; a.ndocs = p->ndocs;
     a.g_stride = p->g_stride; a.x_stride = p->x_stride;
     a.g = g; a.x = x; a.init = initial_states; a.cu = cu_seqlens; a.y = const_cast<void*>(y);
-    a.dy = dy; a.dfin = dfinal_states; a.dg = dg; a.dx = dx; a.dinit = dinitial_states;
+    a.dy = dy; a.dg = dg; a.dx = dx; a.enter = dfinal_states; a.leave = dinitial_states;
     return launch_gate_scan(a, workspace, true, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

@@ -6,7 +6,7 @@ the function; a and 1 - a add a reciprocal and a product; a token's step and the
 tiles' maps round a handful of times per token.  So token t adds at most U (12 + 4 |g_t|) H_t to the error,
 H_t = a_t H_{t-1} + (1 - a_t) |x_t| being the recurrence of the magnitudes, and what came before decays
 with a_t.  The adjoint obeys the same with its own magnitudes.  The gradient of g sees h_{t-1} from an
-output rounded to y's type at every 16th token, whose error decays as H does."""
+output rounded to y's type at some tokens, whose error decays as H does."""
 import numpy as np
 import pytest
 import torch
