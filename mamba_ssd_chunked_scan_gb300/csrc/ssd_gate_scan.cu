@@ -215,19 +215,6 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
 __device__ __forceinline__ void leave(uint64_t* p, uint64_t v) {
     asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
-template <typename S>
-__device__ __forceinline__ uint64_t await(const uint64_t* p, uint64_t v, S& sh, WsHeader* ws, uint32_t where) {
-    if (v) return v;
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 1; it < (1u << 28); ++it) {
-        v = peek(p);
-        if (v) return v;
-        if ((it & 63) == 0 && (*(volatile int*)&sh.abort || ptx::globaltimer() - t0 > kWaitNs)) break;
-    }
-    record_error(ws, SSD_ERR_TIMEOUT, where);
-    *(volatile int*)&sh.abort = 1;
-    return 0;
-}
 // A map (A, B): A >= 0 (or NaN) goes out with its sign bit set, so the word is not zero.
 __device__ __forceinline__ uint64_t map_word(float A, float B) {
     return ((uint64_t)__float_as_uint(B) << 32) | (__float_as_uint(A) | 0x80000000u);
@@ -381,20 +368,35 @@ __device__ __forceinline__ void hand_over(const GateScanArgs& a, S& sh) {
         uint64_t* maps = a.maps + (line * a.nchunks + (int64_t)block * kBlock) * kCh + c;
         uint64_t* carry = a.carry + (line * a.nblocks + block) * kCh + c;
         if (more && !closes) leave(maps + in_block * kCh, map_word(A, B));
-        // the predecessors' maps, all asked for before the first is waited for
+        // the predecessors' maps and the block's state: all that are missing are asked for at once, so a
+        // round takes one trip to L2 however many there are
         uint64_t w[kBlock - 1], cw = 1;
 #pragma unroll
-        for (int p = 0; p < kBlock - 1; ++p) w[p] = p < in_block ? peek(maps + p * kCh) : 0;
+        for (int p = 0; p < kBlock - 1; ++p) w[p] = p < in_block ? peek(maps + p * kCh) : 1;
         if (block > 0) cw = peek(carry - kCh);
+        uint64_t since = 0;
+        for (uint32_t it = 1;; ++it) {
+            bool missing = cw == 0;
+#pragma unroll
+            for (int p = 0; p < kBlock - 1; ++p) missing = missing || w[p] == 0;
+            if (!missing) break;
+            if (it == 1) since = ptx::globaltimer();
+            if ((it & 15) == 0 && (it > (1u << 26) || *(volatile int*)&sh.abort || ptx::globaltimer() - since > kWaitNs)) {
+                record_error(a.ws, SSD_ERR_TIMEOUT, cw == 0 ? kWhereBlock : kWhereTile);
+                *(volatile int*)&sh.abort = 1;
+                break;
+            }
+#pragma unroll
+            for (int p = 0; p < kBlock - 1; ++p)
+                if (w[p] == 0) w[p] = peek(maps + p * kCh);
+            if (cw == 0) cw = peek(carry - kCh);
+        }
         float h = 0.f;
-        if (block > 0) h = __uint_as_float((uint32_t)(await(carry - kCh, cw, sh, a.ws, kWhereBlock) >> 32));
+        if (block > 0) h = __uint_as_float((uint32_t)(cw >> 32));
         else if (!a.cu && a.enter && ch < a.width) h = __ldg(a.enter + (int64_t)t.row * a.width + ch);
 #pragma unroll
         for (int p = 0; p < kBlock - 1; ++p)
-            if (p < in_block) {
-                const uint64_t v = await(maps + p * kCh, w[p], sh, a.ws, kWhereTile);
-                h = fmaf(__uint_as_float((uint32_t)v & 0x7FFFFFFFu), h, __uint_as_float((uint32_t)(v >> 32)));
-            }
+            if (p < in_block) h = fmaf(__uint_as_float((uint32_t)w[p] & 0x7FFFFFFFu), h, __uint_as_float((uint32_t)(w[p] >> 32)));
 #pragma unroll
         for (int k = 0; k < kMain; ++k) {
             sh.seg[REV ? kMain - 1 - k : k][c].x = h;
