@@ -6,13 +6,14 @@
 //
 // Each step is an affine map of the state, and the maps of consecutive steps
 // compose: (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2).  The work is cut into tiles of
-// kMain segments of SEG tokens x kCh channels.  A CTA has eight main warps, one per segment, a
-// thread holding two channels; two hand-over warps, a thread per channel; and a loading warp:
+// kMain segments of SEG tokens x kCh channels.  One CTA per SM has sixteen main warps, one per segment, a
+// thread holding two channels; two hand-over warps, a thread per channel; and loading warps:
 //   loading    takes the next tile by ticket and brings its inputs into a ring of shared-memory stages
-//              (TMA tiles, or 16-byte aligned windows of each row where rows are not aligned),
+//              (one warp and TMA tiles, or a few warps and 4-byte copies where rows are not aligned to 16),
 //              and sends a finished tile's outputs off from the same stage;
-//   main       forms the decays and the segment's map, keeping 1 - a in registers; waits for the state
-//              that enters the segment; walks the segment again and writes the outputs;
+//   main       forms the next tile's decays and its segment's map, keeping 1 - a in registers; then waits for
+//              the state that enters its segment of the tile before, walks that segment again and writes the
+//              outputs.  So a tile's state has a whole tile's time to arrive;
 //   hand-over  composes the segments' maps to the tile's, publishes it, and works out the state that
 //              enters the tile and from it those that enter the segments.
 // Every input is read from HBM once.  The state that enters a tile follows from the maps of the tiles
@@ -46,9 +47,12 @@
 namespace ssd {
 namespace {
 
-constexpr int kMain = 8;               // main warps: segments per tile
+constexpr int kMain = kScanSegs;       // main warps: segments per tile
 constexpr int kCh = kScanCh;           // channels per tile: two per main thread, one per hand-over thread
-constexpr int kThreads = 32 * (kMain + 2 + 1);
+// Loading warps: one for TMA tiles; where rows are copied, as many as leave the main warps the registers they need
+// (registers are given out to four warps at a time: 24 warps have 80 each, 20 have 96).
+constexpr int load_warps(bool rows, bool bwd) { return !rows ? 1 : bwd ? 2 : 6; }
+constexpr int threads(bool rows, bool bwd) { return 32 * (kMain + 2 + load_warps(rows, bwd)); }
 constexpr int kBlock = kScanBlock;
 static_assert(kCh == 64, "two channels per lane, two hand-over warps");
 
@@ -118,19 +122,20 @@ template <typename T> struct PairWord;
 template <> struct PairWord<bf16_t> { typedef uint32_t type; };
 template <> struct PairWord<float> { typedef uint64_t type; };
 
-// Shapes of a kernel instance.  ROWS: rows are not 16-byte aligned; a stage holds a 16-byte aligned
-// window around each row's channels, and outputs are stored by the main warps.
+// Shapes of a kernel instance.  ROWS: rows are not 16-byte aligned; a stage holds, for each row, the aligned
+// 4-byte words around its channels.
 template <typename T, bool ROWS, bool BWD>
 struct Shape {
     static constexpr int ES = sizeof(T);
-    static constexpr int SEG = scan_seg(BWD, ES == 2 ? SSD_BF16 : SSD_F32), TOK = SEG * kMain;
-    static constexpr int PITCH = kCh * ES + (ROWS ? 16 : 0);
+    static constexpr int SEG = scan_seg(BWD, ES == 2 ? SSD_BF16 : SSD_F32, ROWS), TOK = SEG * kMain;
+    static constexpr int PITCH = kCh * ES + (ROWS && ES == 2 ? 4 : 0);
     static constexpr int ARR = TOK * PITCH;                 // one operand's tile
     static constexpr int NA = BWD ? 3 : 2;                  // g, x (and dy)
     static constexpr int STAGE = NA * ARR + (BWD ? kMain * PITCH : 0);   // and, backwards, the h before each segment
-    static constexpr int NS = ROWS || (BWD && ES == 4) ? 2 : 3;
-    static constexpr size_t kSmem = 128 + (size_t)NS * ((STAGE + 127) / 128 * 128);
     static constexpr int kStep = (STAGE + 127) / 128 * 128;
+    static constexpr int NS = 4 * kStep <= 212 * 1024 ? 4 : 3;
+    static constexpr size_t kSmem = 128 + (size_t)NS * kStep;
+    static_assert(kSmem <= 212 * 1024, "stages, beside 15 KB of maps and documents");
 };
 
 struct ScanParams {
@@ -185,14 +190,14 @@ __device__ void find_docs(const GateScanArgs& a, int64_t t0, int* doc) {
     }
 }
 
-constexpr int kRing = 4;   // tiles whose numbers and documents are kept: one more than stages
+constexpr int kRing = 8;   // tiles whose numbers and documents are kept: more than one above the stages
 template <int TOK, bool DOCS>
 struct Shared {
-    float2 seg[kMain][kCh];          // each segment's map per channel (A, B); then .x: the state that enters it
+    float2 seg[2][kMain][kCh];       // each segment's map per channel (A, B); then .x: the state that enters it
     Tile tile[kRing];
     int doc[DOCS ? kRing : 1][DOCS ? TOK + 1 : 1];
-    uint64_t full[3], done[3];       // per stage: inputs there; outputs written
-    uint64_t maps, states;           // the segments' maps are in seg; the states that enter them are
+    uint64_t full[4], done[4];       // per stage: inputs there; outputs written
+    uint64_t maps[2], states[2];     // of tiles in turn: the segments' maps are in seg; the states that enter them are
     int abort, never;
 };
 
@@ -232,37 +237,32 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* 
                  "r"(ptx::smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-__device__ __forceinline__ void bulk_load(void* dst, uint64_t src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     ptx::smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
-                 : "memory");
+// ---------------------------------------------------------------------- loading warps
+__device__ __forceinline__ uint32_t next_ticket(const GateScanArgs& a, int n) {
+    return a.nchunks > 1 ? atomicAdd(a.ticket, 1u) : (uint32_t)(blockIdx.x + gridDim.x * n);
 }
 
-// ---------------------------------------------------------------------- loading warp
-template <typename T, bool ROWS, bool DOCS, bool BWD>
-__device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared<Shape<T, ROWS, BWD>::TOK, DOCS>& sh) {
-    typedef Shape<T, ROWS, BWD> H;
+template <typename T, bool DOCS, bool BWD>
+__device__ __forceinline__ void load_tiles(const ScanParams& p, uint8_t* sm, Shared<Shape<T, false, BWD>::TOK, DOCS>& sh) {
+    typedef Shape<T, false, BWD> H;
     const GateScanArgs& a = p.a;
     const int lane = threadIdx.x & 31;
-    int n = 0, filled = 0;   // tiles, and phases of the stages' `full` begun (the end's among them)
     auto send = [&](int j) {   // lane 0: tile j's outputs from its stage
-        if constexpr (!ROWS) {
-            const Tile& t = sh.tile[j % kRing];
-            const uint8_t* st = sm + (j % H::NS) * H::kStep;
-            if (BWD) {
-                tma_store_3d(&p.dg, st, t.group * kCh, (int)t.t0, t.row);
-                tma_store_3d(&p.dx, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
-            } else {
-                tma_store_3d(&p.y, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
-            }
-            ptx::bulk_commit();
+        const Tile& t = sh.tile[j % kRing];
+        const uint8_t* st = sm + (j % H::NS) * H::kStep;
+        if (BWD) {
+            tma_store_3d(&p.dg, st, t.group * kCh, (int)t.t0, t.row);
+            tma_store_3d(&p.dx, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
+        } else {
+            tma_store_3d(&p.y, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
         }
+        ptx::bulk_commit();
     };
+    int n = 0, filled = 0;   // tiles, and phases of the stages' `full` begun (the end's among them)
     bool go = true;
     for (;; ++n) {
         uint32_t k = 0;
-        if (lane == 0) k = a.nchunks > 1 ? atomicAdd(a.ticket, 1u) : (uint32_t)(blockIdx.x + gridDim.x * n);
+        if (lane == 0) k = next_ticket(a, n);
         k = __shfl_sync(0xffffffffu, k, 0);
         const Tile t = tile_of<BWD, H::TOK>(a, k);
         // the slot's last tile, n - kRing, is done with: a later one's outputs have been waited for
@@ -273,68 +273,35 @@ __device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared
             if (lane == 0) {
                 go = bar_wait(sh, a.ws, &sh.done[st], ((n / H::NS) - 1) & 1, kWhereDone);
                 if (go) send(n - H::NS);
-                if (!ROWS) ptx::bulk_wait_read0();
+                ptx::bulk_wait_read0();
             }
             go = __shfl_sync(0xffffffffu, (int)go, 0) != 0;
             if (!go) break;
         }
         __syncwarp();
         uint64_t* full = &sh.full[st];
-        if (!t.ntok) {
-            if (lane == 0) ptx::mbar_arrive(full);
-            ++filled;
-            break;
-        }
         ++filled;
-        uint8_t* dst = sm + st * H::kStep;
-        if constexpr (!ROWS) {
-            if (lane == 0) {
+        if (lane == 0) {
+            if (!t.ntok) {
+                ptx::mbar_arrive(full);
+            } else {
+                uint8_t* dst = sm + st * H::kStep;
                 ptx::mbar_expect_tx(full, H::STAGE);
                 const int c = t.group * kCh, t0 = (int)t.t0;
                 tma_load_3d(dst, &p.g, full, c, t0, t.row);
                 tma_load_3d(dst + H::ARR, &p.x, full, c, t0, t.row);
                 if (BWD) {
                     tma_load_3d(dst + 2 * H::ARR, &p.dy, full, c, t0, t.row);
-                    // the h before each segment (before the sequence: out of range, zeros)
-                    for (int s = 0; s < kMain; ++s)
-                        tma_load_3d(dst + H::NA * H::ARR + s * H::PITCH, &p.y, full, c, t0 + s * H::SEG - 1, t.row);
-                }
-            }
-        } else {
-            // Windows of whole 16-byte units around each row's channels.  A unit that holds one byte of a
-            // tensor lies in the tensor's memory pages, so the bytes around its ends can be read; no one uses them.
-            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0;
-            const int cols = a.width - t.group * kCh < kCh ? a.width - t.group * kCh : kCh;
-            const void* base[3] = {a.g, a.x, a.dy};
-            const int64_t pitch[3] = {a.g_stride, a.x_stride, a.width};
-            uint32_t total = 0;
-            for (int pass = 0; pass < 2; ++pass) {
-                auto row = [&](uint64_t at, uint8_t* to) {
-                    const uint64_t lo = at & ~15ull, hi = (at + (uint32_t)cols * H::ES + 15) & ~15ull;
-                    if (pass == 0) total += (uint32_t)(hi - lo);
-                    else bulk_load(to, lo, (uint32_t)(hi - lo), full);
-                };
-#pragma unroll
-                for (int r = 0; r < H::NA; ++r)
-                    for (int k = lane; k < t.ntok; k += 32)
-                        row((uint64_t)(uintptr_t)base[r] + (uint64_t)((tok + k) * pitch[r] + t.group * kCh) * H::ES,
-                            dst + r * H::ARR + k * H::PITCH);
-                if (BWD && lane < kMain && lane * H::SEG < t.ntok && t.t0 + lane * H::SEG > 0)
-                    row((uint64_t)(uintptr_t)a.y + (uint64_t)((tok + lane * H::SEG - 1) * a.width + t.group * kCh) * H::ES,
-                        dst + H::NA * H::ARR + lane * H::PITCH);
-                if (pass == 0) {
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-                    if (lane == 0) ptx::mbar_expect_tx(full, total);
-                    __syncwarp();
+                    // the h before each segment: every SEG-th row from t0 - 1 (before the sequence: zeros)
+                    tma_load_3d(dst + H::NA * H::ARR, &p.y, full, c, t0 - 1, t.row);
                 }
             }
         }
+        if (!t.ntok) break;
     }
     if (lane != 0) return;
     // the outputs of the tiles still in stages, then everything in flight
-    const int first = n - H::NS + 1 > 0 ? n - H::NS + 1 : 0;
-    for (int j = first; go && j < n; ++j) {
+    for (int j = n - H::NS + 1 > 0 ? n - H::NS + 1 : 0; go && j < n; ++j) {
         go = bar_wait(sh, a.ws, &sh.done[j % H::NS], (j / H::NS) & 1, kWhereDone);
         if (go) send(j);
     }
@@ -342,7 +309,104 @@ __device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared
         const int last = ((filled - 1 - st) / H::NS) * H::NS + st;
         if (!ptx::mbar_wait(&sh.full[st], (last / H::NS) & 1, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereStage);
     }
-    if (!ROWS) ptx::bulk_wait0();
+    ptx::bulk_wait0();
+}
+
+__device__ __forceinline__ void copy_word(uint8_t* dst, uint64_t src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+// The aligned 4-byte words around the channels of rows k, k + WARPS, ... (of `bytes` bytes each, `pitch` bytes
+// apart, row 0 at `at`) into smem rows of PITCH bytes, by a warp.  All of a row's PITCH / 4 words are
+// copied where they lie inside the tensor [begin, end) even past the channels; in tiles at its ends only words with
+// channels are, and one that reaches past it (half of it an element) by halves.
+template <int ES, int PITCH, int WARPS>
+__device__ __forceinline__ void copy_rows(uint8_t* dst, uint64_t at, int64_t pitch, int bytes, int k, int rows, uint64_t begin,
+                                          uint64_t end) {
+    const int lane = threadIdx.x & 31;
+    const uint64_t last = at + (uint64_t)((rows - 1) * pitch);
+    if ((at & ~3ull) >= begin && (last & ~3ull) + PITCH <= end) {
+        uint64_t src = at + (uint64_t)(k * pitch);
+        uint8_t* to = dst + k * PITCH + 4 * lane;
+#pragma unroll 4
+        for (int r = k; r < rows; r += WARPS) {
+            copy_word(to, (src & ~3ull) + 4 * lane);
+            if (ES == 4) copy_word(to + 128, src + 4 * lane + 128);
+            src += (uint64_t)(WARPS * pitch);
+            to += WARPS * PITCH;
+        }
+        if (ES == 2)   // the rows' 33rd words
+            for (int r = 32 * k + lane; r < rows; r += 32 * WARPS)
+                copy_word(dst + r * PITCH + 128, ((at + (uint64_t)(r * pitch)) & ~3ull) + 128);
+        return;
+    }
+    for (int r = k; r < rows; r += WARPS) {
+        const uint64_t row = at + (uint64_t)(r * pitch), lo = row & ~3ull;
+        const int words = (int)((row + bytes + 3 - lo) >> 2);
+        for (int w = lane; w < words; w += 32) {
+            const uint64_t src = lo + 4 * w;
+            if (ES == 4 || (src >= begin && src + 4 <= end)) {
+                copy_word(dst + r * PITCH + 4 * w, src);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; h += 2)
+                    if (src + h >= begin && src + h < end)
+                        *reinterpret_cast<uint16_t*>(dst + r * PITCH + 4 * w + h) = *reinterpret_cast<const uint16_t*>(src + h);
+            }
+        }
+    }
+}
+
+template <typename T, bool DOCS, bool BWD>
+__device__ __forceinline__ void load_rows(const ScanParams& p, uint8_t* sm, Shared<Shape<T, true, BWD>::TOK, DOCS>& sh) {
+    typedef Shape<T, true, BWD> H;
+    const GateScanArgs& a = p.a;
+    constexpr int WARPS = load_warps(true, BWD);
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kMain - 2;
+    const void* base[3] = {a.g, a.x, a.dy};
+    const int64_t pitch[3] = {a.g_stride, a.x_stride, a.width};
+    for (int n = 0;; ++n) {
+        if (w == 0) {
+            uint32_t k = 0;
+            if (lane == 0) k = next_ticket(a, n);
+            k = __shfl_sync(0xffffffffu, k, 0);
+            const Tile t = tile_of<BWD, H::TOK>(a, k);
+            if (lane == 0) sh.tile[n % kRing] = t;
+            if (DOCS && t.ntok) find_docs<H::TOK>(a, t.t0, sh.doc[n % kRing]);
+        }
+        const int st = n % H::NS;
+        bool go = n < H::NS || bar_wait(sh, a.ws, &sh.done[st], ((n / H::NS) - 1) & 1, kWhereDone);
+        // the tile's number is there; the warps go on or stop together
+        go = !ptx::named_bar_any(1, 32 * WARPS, !go);
+        if (!go) break;
+        const Tile t = sh.tile[n % kRing];
+        uint64_t* full = &sh.full[st];
+        if (t.ntok) {
+            uint8_t* dst = sm + st * H::kStep;
+            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0;
+            const int c = t.group * kCh, cols = a.width - c < kCh ? a.width - c : kCh;
+            const int64_t rows = a.batch * a.seqlen;
+#pragma unroll
+            for (int r = 0; r < H::NA; ++r) {
+                const uint64_t b = (uint64_t)(uintptr_t)base[r];
+                copy_rows<H::ES, H::PITCH, WARPS>(dst + r * H::ARR, b + (uint64_t)(tok * pitch[r] + c) * H::ES, pitch[r] * H::ES,
+                                                  cols * H::ES, w, t.ntok, b, b + (uint64_t)((rows - 1) * pitch[r] + a.width) * H::ES);
+            }
+            if (BWD) {   // the h before each segment; none before the sequence's first
+                const uint64_t b = (uint64_t)(uintptr_t)a.y;
+                const int none = t.t0 == 0 ? 1 : 0, segs = (t.ntok + H::SEG - 1) / H::SEG - none;
+                if (segs > 0)
+                    copy_rows<H::ES, H::PITCH, WARPS>(dst + H::NA * H::ARR + none * H::PITCH,
+                                                      b + (uint64_t)((tok + none * H::SEG - 1) * a.width + c) * H::ES,
+                                                      (int64_t)H::SEG * a.width * H::ES, cols * H::ES, w, segs, b,
+                                                      b + (uint64_t)(rows * a.width) * H::ES);
+            }
+        }
+        // two arrivals per thread: its plain stores, and its copies when they have landed
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(full)) : "memory");
+        ptx::mbar_arrive(full);
+        if (!t.ntok) break;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------- hand-over warps
@@ -350,15 +414,16 @@ template <bool REV, typename S>
 __device__ __forceinline__ void hand_over(const GateScanArgs& a, S& sh) {
     const int c = threadIdx.x - 32 * kMain, lane = threadIdx.x & 31;   // channel of the tile
     for (int n = 0;; ++n) {
-        if (!bar_wait(sh, a.ws, &sh.maps, n & 1, kWhereMaps)) return;
+        if (!bar_wait(sh, a.ws, &sh.maps[n & 1], (n >> 1) & 1, kWhereMaps)) return;
         const Tile t = sh.tile[n % kRing];
+        float2 (*seg)[kCh] = sh.seg[n & 1];
         if (!t.ntok) return;
         const int ch = t.group * kCh + c;
         float2 m[kMain];
         float A = 1.f, B = 0.f;
 #pragma unroll
         for (int k = 0; k < kMain; ++k) {
-            m[k] = sh.seg[REV ? kMain - 1 - k : k][c];
+            m[k] = seg[REV ? kMain - 1 - k : k][c];
             B = fmaf(m[k].x, B, m[k].y);
             A *= m[k].x;
         }
@@ -399,11 +464,11 @@ __device__ __forceinline__ void hand_over(const GateScanArgs& a, S& sh) {
             if (p < in_block) h = fmaf(__uint_as_float((uint32_t)w[p] & 0x7FFFFFFFu), h, __uint_as_float((uint32_t)(w[p] >> 32)));
 #pragma unroll
         for (int k = 0; k < kMain; ++k) {
-            sh.seg[REV ? kMain - 1 - k : k][c].x = h;
+            seg[REV ? kMain - 1 - k : k][c].x = h;
             h = fmaf(m[k].x, h, m[k].y);
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.states);
+        if (lane == 0) ptx::mbar_arrive(&sh.states[n & 1]);
         if (more && closes) leave(carry, ((uint64_t)__float_as_uint(h) << 32) | 1u);
         // the state that leaves the sequence: the final state, or the initial state's gradient
         if (!more && !a.cu && a.leave && ch < a.width) a.leave[(int64_t)t.row * a.width + ch] = h;
@@ -423,20 +488,23 @@ struct Main {
     // the tile at hand
     Tile t;
     const int* doc;
+    float2* seg;       // the segment's maps, then states
     uint8_t* st;       // its stage, at this thread's segment and channels
     int s0, c0;        // the segment's first token in the tile; the thread's first channel
     bool ok0, ok1;
     uint32_t skew[3], step[3];   // ROWS: low bits of the first row's address, and of the rows' pitch
 
-    __device__ __forceinline__ void open(const Tile& tile, const int* d, uint8_t* stage) {
-        t = tile;
-        doc = d;
+    // Tile n of the walk, for its first or its second visit.
+    __device__ __forceinline__ void open(int n, uint8_t* sm) {
+        t = sh.tile[n % kRing];
+        doc = sh.doc[DOCS ? n % kRing : 0];
+        seg = sh.seg[n & 1][warp];
         s0 = warp * SEG;
         c0 = t.group * kCh + (ROWS ? lane : 2 * lane);
         ok0 = c0 < a.width;
         ok1 = c0 + kApart < a.width;
-        st = stage + s0 * H::PITCH + (ROWS ? lane : 2 * lane) * H::ES;
-        if constexpr (ROWS) {
+        st = sm + (n % H::NS) * H::kStep + s0 * H::PITCH + (ROWS ? lane : 2 * lane) * H::ES;
+        if constexpr (ROWS && sizeof(T) == 2) {
             const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
             const void* base[3] = {a.g, a.x, a.dy};
             const int64_t pitch[3] = {a.g_stride, a.x_stride, a.width};
@@ -470,19 +538,63 @@ struct Main {
     // operand r (g, x, dy) at token k of the segment
     __device__ __forceinline__ f2 in(int r, int k) const {
         const uint8_t* q = st + r * H::ARR + k * H::PITCH;
-        if constexpr (ROWS) return two(q + ((skew[r] + k * step[r]) & 15));
-        else return widen(*reinterpret_cast<const W*>(q));
+        if constexpr (!ROWS) return widen(*reinterpret_cast<const W*>(q));
+        else if constexpr (sizeof(T) == 2) return two(q + ((skew[r] + k * step[r]) & 2));
+        else return two(q);
     }
-    // result over operand r's place in the stage, or straight to memory
-    __device__ __forceinline__ void out(int r, T* base, int64_t pitch, int k, f2 v) const {
-        const W w = narrow(v);
-        if constexpr (!ROWS) {
-            *reinterpret_cast<W*>(st + r * H::ARR + k * H::PITCH) = w;
-        } else {
-            T* q = base + ((int64_t)t.row * a.seqlen + t.t0 + s0 + k) * pitch + c0;
-            const T* e = reinterpret_cast<const T*>(&w);
-            if (ok0) q[0] = e[0];
-            if (ok1) q[kApart] = e[1];
+    // A result of the segment, SEG rows of two channels per thread.  Aligned tiles leave it over operand r's
+    // place in the stage, from where it is sent off.  Rows of half words are put together in the stage
+    // as the aligned words that they are in memory and stored by words, those of whole words directly.
+    struct Out {
+        W w[SEG];
+    };
+    __device__ __forceinline__ void put(Out& o, int r, int k, f2 v) const {
+        if constexpr (ROWS) o.w[k] = narrow(v);
+        else *reinterpret_cast<W*>(st + r * H::ARR + k * H::PITCH) = narrow(v);
+    }
+    __device__ __forceinline__ void flush(const Out& o, int r, void* base, int64_t pitch) const {
+        if constexpr (ROWS) {
+            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
+            const int rows = t.ntok - s0 < SEG ? t.ntok - s0 : SEG;
+            if constexpr (sizeof(T) == 4) {
+                float* q = static_cast<float*>(base) + tok * pitch + c0;
+#pragma unroll
+                for (int k = 0; k < SEG; ++k)
+                    if (k < rows) {
+                        const float2 f = un(o.w[k]);
+                        if (ok0) q[k * pitch] = f.x;
+                        if (ok1) q[k * pitch + kApart] = f.y;
+                    }
+            } else {
+                uint8_t* mine = st + r * H::ARR;                      // at this lane's element
+                uint64_t at = (uint64_t)(uintptr_t)base + (uint64_t)(tok * pitch + t.group * kCh) * 2;
+                const uint32_t low = (uint32_t)at, by = (uint32_t)(pitch * 2);
+                __syncwarp();   // every lane has read the operand
+#pragma unroll
+                for (int k = 0; k < SEG; ++k) {
+                    uint8_t* q = mine + k * H::PITCH + ((low + k * by) & 2);
+                    *reinterpret_cast<uint16_t*>(q) = (uint16_t)o.w[k];
+                    *reinterpret_cast<uint16_t*>(q + 64) = (uint16_t)(o.w[k] >> 16);
+                }
+                __syncwarp();
+                const int bytes = 2 * (a.width - t.group * kCh < kCh ? a.width - t.group * kCh : kCh);
+                const uint8_t* words = mine + 2 * lane;                // word `lane` of the row
+#pragma unroll
+                for (int k = 0; k < SEG; ++k) {
+                    if (k < rows) {
+                        const int skip = (int)(at & 2);
+                        uint8_t* to = reinterpret_cast<uint8_t*>(at - skip) + 4 * lane;
+                        const int o0 = 4 * lane - skip;                // the word's place in the row, in bytes
+                        const uint32_t v = *reinterpret_cast<const uint32_t*>(words + k * H::PITCH);
+                        if (o0 >= 0 && o0 + 4 <= bytes) *reinterpret_cast<uint32_t*>(to) = v;
+                        else if (o0 < 0) *reinterpret_cast<uint16_t*>(to + 2) = (uint16_t)(v >> 16);
+                        else if (o0 < bytes) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v;
+                        if (skip && lane == 0 && bytes == 2 * kCh)     // the last element, in a 33rd word
+                            *reinterpret_cast<uint16_t*>(to + 128) = *reinterpret_cast<const uint16_t*>(words + k * H::PITCH + 128);
+                    }
+                    at += by;
+                }
+            }
         }
     }
     // two channels of row `row` of a (rows, width) fp32 array, zero without one
@@ -499,7 +611,7 @@ struct Main {
     }
     __device__ __forceinline__ void put_map(f2 A, f2 B) const {
         const float2 fa = un(A), fb = un(B);
-        float2* q = sh.seg[warp];
+        float2* q = seg;
         if constexpr (ROWS) {
             q[lane] = make_float2(fa.x, fb.x);
             q[lane + 32] = make_float2(fa.y, fb.y);
@@ -508,7 +620,7 @@ struct Main {
         }
     }
     __device__ __forceinline__ f2 entered() const {
-        const float2* q = sh.seg[warp];
+        const float2* q = seg;
         if constexpr (ROWS) return pk(q[lane].x, q[lane + 32].x);
         const float4 e = *reinterpret_cast<const float4*>(q + 2 * lane);
         return pk(e.x, e.z);
@@ -522,67 +634,73 @@ struct Main {
         return t.t0 + s0 + k == a.seqlen - 1 ? a.ndocs - 1 : doc[s0 + k + 1] - 1;
     }
 
-    f2 mv[SEG], uv[BWD ? SEG : 1];
+    // what the first visit keeps for the second: 1 - a and, backwards, u = d(h_t)/d(g_t)
+    struct Keep {
+        f2 m[SEG], u[BWD ? SEG : 1];
+    };
 
     // WHOLE: every token of the segment is inside the sequence
     template <bool WHOLE>
-    __device__ __forceinline__ void first_fwd() {
+    __device__ __forceinline__ void first_fwd(Keep& q) {
         f2 A = pk(1.f, 1.f), B = pk(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!WHOLE && s0 + k >= t.ntok) break;
             f2 av;
-            gate2<T>(in(0, k), av, mv[k]);
+            gate2<T>(in(0, k), av, q.m[k]);
             if (starts(k)) {
                 A = pk(0.f, 0.f);
                 B = state(a.init, doc[s0 + k]);
             }
             A = mul(A, av);
-            B = fma2(av, B, mul(mv[k], in(1, k)));
+            B = fma2(av, B, mul(q.m[k], in(1, k)));
         }
         put_map(A, B);
     }
     template <bool WHOLE>
-    __device__ __forceinline__ void second_fwd() {
+    __device__ __forceinline__ void second_fwd(const Keep& q) {
         f2 h = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+        Out y;
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!WHOLE && s0 + k >= t.ntok) break;
             if (starts(k)) h = state(a.init, doc[s0 + k]);
-            h = fma2(fma2(mv[k], minus, one), h, mul(mv[k], in(1, k)));
-            out(1, static_cast<T*>(a.y), a.width, k, h);
+            h = fma2(fma2(q.m[k], minus, one), h, mul(q.m[k], in(1, k)));
+            put(y, 1, k, h);
             if (DOCS && a.leave && ends(k)) {
                 const int at = ending(k);
                 if (at >= 0) put_state(a.leave, at, h);
             }
         }
+        flush(y, 1, a.y, a.width);
     }
     template <bool WHOLE>
-    __device__ __forceinline__ void first_bwd() {
+    __device__ __forceinline__ void first_bwd(Keep& q) {
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
         f2 h;
         if (t.t0 + s0 == 0) {
             h = DOCS ? pk(0.f, 0.f) : state(a.init, t.row);
         } else {
-            const uint8_t* q = st - s0 * H::PITCH + H::NA * H::ARR + warp * H::PITCH;
-            if constexpr (ROWS) {
-                const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0 - 1;
-                h = two(q + (((uint32_t)(uintptr_t)a.y + (uint32_t)((tok * a.width + t.group * kCh) * H::ES)) & 15));
+            const uint8_t* r = st - s0 * H::PITCH + H::NA * H::ARR + warp * H::PITCH;
+            if constexpr (!ROWS) {
+                h = widen(*reinterpret_cast<const W*>(r));
             } else {
-                h = widen(*reinterpret_cast<const W*>(q));
+                const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0 - 1;
+                const uint32_t low = (uint32_t)(uintptr_t)a.y + (uint32_t)((tok * a.width + t.group * kCh) * H::ES);
+                h = two(r + (sizeof(T) == 2 ? low & 2 : 0));
             }
         }
-        // forwards through the segment: u = d(h_t)/d(g_t) = (h_{t-1} - x) a (1 - a)
+        // forwards through the segment: u = (h_{t-1} - x) a (1 - a)
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!WHOLE && s0 + k >= t.ntok) break;
             f2 av;
             const f2 xv = in(1, k);
-            gate2<T>(in(0, k), av, mv[k]);
+            gate2<T>(in(0, k), av, q.m[k]);
             if (starts(k)) h = state(a.init, doc[s0 + k]);
-            uv[k] = mul(fma2(xv, minus, h), mul(av, mv[k]));
-            h = fma2(av, h, mul(mv[k], xv));
+            q.u[k] = mul(fma2(xv, minus, h), mul(av, q.m[k]));
+            h = fma2(av, h, mul(q.m[k], xv));
         }
         // backwards: the map of mu over the segment
         f2 A = one, B = pk(0.f, 0.f);
@@ -594,16 +712,17 @@ struct Main {
                 A = pk(0.f, 0.f);
                 B = at >= 0 ? state(a.enter, at) : A;
             }
-            const f2 av = fma2(mv[k], minus, one);
+            const f2 av = fma2(q.m[k], minus, one);
             B = mul(av, add(in(2, k), B));
             A = mul(A, av);
         }
         put_map(A, B);
     }
     template <bool WHOLE>
-    __device__ __forceinline__ void second_bwd() {
+    __device__ __forceinline__ void second_bwd(const Keep& q) {
         f2 mu = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+        Out dg, dx;
 #pragma unroll
         for (int k = SEG - 1; k >= 0; --k) {
             if (!WHOLE && s0 + k >= t.ntok) continue;
@@ -612,60 +731,77 @@ struct Main {
                 mu = at >= 0 ? state(a.enter, at) : pk(0.f, 0.f);
             }
             const f2 lam = add(in(2, k), mu);
-            out(0, static_cast<T*>(a.dg), a.g_stride, k, mul(lam, uv[k]));
-            out(1, static_cast<T*>(a.dx), a.x_stride, k, mul(lam, mv[k]));
-            mu = mul(fma2(mv[k], minus, one), lam);
+            put(dg, 0, k, mul(lam, q.u[k]));
+            put(dx, 1, k, mul(lam, q.m[k]));
+            mu = mul(fma2(q.m[k], minus, one), lam);
             if (DOCS && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
         }
+        flush(dg, 0, a.dg, a.g_stride);
+        flush(dx, 1, a.dx, a.x_stride);
     }
 
-    __device__ __forceinline__ void run(uint8_t* sm) {
-        for (int n = 0;; ++n) {
-            const int stage = n % H::NS;
-            if (!bar_wait(sh, a.ws, &sh.full[stage], (n / H::NS) & 1, kWhereStage)) return;
-            open(sh.tile[n % kRing], sh.doc[DOCS ? n % kRing : 0], sm + stage * H::kStep);
+    // The first visit to tile n; false: there is none, or a wait ran out.
+    __device__ __forceinline__ bool first(int n, uint8_t* sm, Keep& q) {
+        if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
+        open(n, sm);
+        if (t.ntok) {
             const bool whole = s0 + SEG <= t.ntok;
-            if (t.ntok) {
-                if constexpr (BWD) {
-                    if (whole) first_bwd<true>();
-                    else first_bwd<false>();
-                } else {
-                    if (whole) first_fwd<true>();
-                    else first_fwd<false>();
-                }
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sh.maps);
-            if (!t.ntok) return;
-            if (!bar_wait(sh, a.ws, &sh.states, n & 1, kWhereState)) return;
             if constexpr (BWD) {
-                if (whole) second_bwd<true>();
-                else second_bwd<false>();
+                if (whole) first_bwd<true>(q);
+                else first_bwd<false>(q);
             } else {
-                if (whole) second_fwd<true>();
-                else second_fwd<false>();
+                if (whole) first_fwd<true>(q);
+                else first_fwd<false>(q);
             }
-            if (!ROWS) ptx::fence_proxy_async();   // the outputs in the stage, before they are sent off
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sh.done[stage]);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.maps[n & 1]);
+        return t.ntok != 0;
+    }
+    __device__ __forceinline__ bool second(int n, uint8_t* sm, const Keep& q) {
+        if (!bar_wait(sh, a.ws, &sh.states[n & 1], (n >> 1) & 1, kWhereState)) return false;
+        open(n, sm);
+        const bool whole = s0 + SEG <= t.ntok;
+        if constexpr (BWD) {
+            if (whole) second_bwd<true>(q);
+            else second_bwd<false>(q);
+        } else {
+            if (whole) second_fwd<true>(q);
+            else second_fwd<false>(q);
+        }
+        if (!ROWS) ptx::fence_proxy_async();   // the outputs in the stage, before they are sent off
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.done[n % H::NS]);
+        return true;
+    }
+    __device__ __forceinline__ void run(uint8_t* sm) {
+        Keep cur, next;
+        bool more = first(0, sm, cur);
+        for (int n = 0; more; ++n) {
+            more = first(n + 1, sm, next);
+            if (!second(n, sm, cur)) return;
+            cur = next;
         }
     }
 };
 
 template <typename T, bool ROWS, bool DOCS, bool BWD>
-__global__ void __launch_bounds__(kThreads, 2) ssd_gate_scan_kernel(const __grid_constant__ ScanParams p) {
+__global__ void __launch_bounds__(threads(ROWS, BWD), 1) ssd_gate_scan_kernel(const __grid_constant__ ScanParams p) {
     typedef Shape<T, ROWS, BWD> H;
+    static_assert(H::kSmem + sizeof(Shared<H::TOK, DOCS>) <= 227 * 1024, "a CTA's shared memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 127) & ~(uintptr_t)127);
     __shared__ __align__(16) Shared<H::TOK, DOCS> sh;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 3; ++i) {
-            ptx::mbar_init(&sh.full[i], 1);
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(&sh.full[i], ROWS ? 2 * 32 * load_warps(ROWS, BWD) : 1);
             ptx::mbar_init(&sh.done[i], kMain);
         }
-        ptx::mbar_init(&sh.maps, kMain);
-        ptx::mbar_init(&sh.states, 2);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.maps[i], kMain);
+            ptx::mbar_init(&sh.states[i], 2);
+        }
         sh.abort = 0;
         sh.never = 0;
         ptx::mbar_fence_init();
@@ -677,8 +813,10 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_gate_scan_kernel(const __grid
     } else if (warp < kMain + 2) {
         hand_over<BWD>(p.a, sh);
     } else {
-        if (DOCS && blockIdx.x == 0) check_cu_seqlens(p.a.cu, p.a.ndocs, p.a.seqlen, p.a.ws, threadIdx.x & 31, 32);
-        loading<T, ROWS, DOCS, BWD>(p, sm, sh);
+        if (DOCS && blockIdx.x == 0 && warp == kMain + 2)
+            check_cu_seqlens(p.a.cu, p.a.ndocs, p.a.seqlen, p.a.ws, threadIdx.x & 31, 32);
+        if constexpr (ROWS) load_rows<T, DOCS, BWD>(p, sm, sh);
+        else load_tiles<T, DOCS, BWD>(p, sm, sh);
     }
 }
 
@@ -714,14 +852,15 @@ __global__ void __launch_bounds__(256) ssd_gate_scan_step_kernel(GateStepArgs a)
 
 bool on(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
-// A (batch, seqlen, width) tensor of token stride `stride`, in boxes of kCh channels x `tokens`.
-bool encode_3d(CUtensorMap* tm, const void* base, int es, const GateScanArgs& a, int64_t stride, int tokens) {
+// A (batch, seqlen, width) tensor of token stride `stride`, in boxes of kCh channels x `tokens`, of which every
+// `every`-th is read.
+bool encode_3d(CUtensorMap* tm, const void* base, int es, const GateScanArgs& a, int64_t stride, int tokens, int every = 1) {
     const auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)a.width, (cuuint64_t)a.seqlen, (cuuint64_t)a.batch};
     cuuint64_t strides[2] = {(cuuint64_t)(stride * es), (cuuint64_t)(a.seqlen * stride * es)};
     cuuint32_t box[3] = {(cuuint32_t)kCh, (cuuint32_t)tokens, 1};
-    cuuint32_t step[3] = {1, 1, 1};
+    cuuint32_t step[3] = {1, (cuuint32_t)every, 1};
     return enc(tm, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base),
                dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -741,38 +880,40 @@ cudaError_t launch_one(const ScanParams& p, cudaStream_t st) {
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
         ready[dev].store(1, std::memory_order_release);
     }
-    // two CTAs per SM; with tickets any number of them finishes the work
+    // one CTA per SM; with tickets any number of them finishes the work
     const int nsm = device_sms();
-    const int64_t most = 2 * (int64_t)(nsm > 0 ? nsm : 152);
-    kern<<<(unsigned)(p.a.ntiles < most ? p.a.ntiles : most), kThreads, smem, st>>>(p);
+    const uint32_t most = nsm > 0 ? nsm : 152;
+    kern<<<p.a.ntiles < most ? p.a.ntiles : most, threads(ROWS, BWD), smem, st>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, bool BWD>
-cudaError_t launch_typed(const GateScanArgs& a, cudaStream_t st) {
+cudaError_t launch_typed(const GateScanArgs& a, bool rows, cudaStream_t st) {
     ScanParams p;
     memset(&p, 0, sizeof(p));
     p.a = a;
-    constexpr int es = sizeof(T), unit = 16 / es, tok = Shape<T, false, BWD>::TOK;
-    bool tiles = a.width % unit == 0 && a.g_stride % unit == 0 && a.x_stride % unit == 0 && on(a.g, 16) && on(a.x, 16) && on(a.y, 16);
-    if (BWD) tiles = tiles && on(a.dy, 16) && on(a.dg, 16) && on(a.dx, 16);
-    if (tiles) {
-        bool ok = encode_3d(&p.g, a.g, es, a, a.g_stride, tok) && encode_3d(&p.x, a.x, es, a, a.x_stride, tok) &&
-                  encode_3d(&p.y, a.y, es, a, a.width, BWD ? 1 : tok);
-        if (BWD)
-            ok = ok && encode_3d(&p.dy, a.dy, es, a, a.width, tok) && encode_3d(&p.dg, a.dg, es, a, a.g_stride, tok) &&
-                 encode_3d(&p.dx, a.dx, es, a, a.x_stride, tok);
-        if (!ok) return cudaErrorInvalidValue;
-        return a.cu ? launch_one<T, false, true, BWD>(p, st) : launch_one<T, false, false, BWD>(p, st);
-    }
-    return a.cu ? launch_one<T, true, true, BWD>(p, st) : launch_one<T, true, false, BWD>(p, st);
+    if (rows) return a.cu ? launch_one<T, true, true, BWD>(p, st) : launch_one<T, true, false, BWD>(p, st);
+    typedef Shape<T, false, BWD> H;
+    constexpr int es = sizeof(T);
+    bool ok = encode_3d(&p.g, a.g, es, a, a.g_stride, H::TOK) && encode_3d(&p.x, a.x, es, a, a.x_stride, H::TOK) &&
+              encode_3d(&p.y, a.y, es, a, a.width, H::TOK, BWD ? H::SEG : 1);
+    if (BWD)
+        ok = ok && encode_3d(&p.dy, a.dy, es, a, a.width, H::TOK) && encode_3d(&p.dg, a.dg, es, a, a.g_stride, H::TOK) &&
+             encode_3d(&p.dx, a.dx, es, a, a.x_stride, H::TOK);
+    if (!ok) return cudaErrorInvalidValue;
+    return a.cu ? launch_one<T, false, true, BWD>(p, st) : launch_one<T, false, false, BWD>(p, st);
 }
 
-}  // namespace
+// Whether rows can be moved as TMA tiles: every row of every operand starts on a 16-byte boundary.
+bool aligned_rows(const GateScanArgs& a, bool bwd) {
+    const int unit = a.dtype == SSD_BF16 ? 8 : 4;
+    if (a.width % unit || a.g_stride % unit || a.x_stride % unit || !on(a.g, 16) || !on(a.x, 16) || !on(a.y, 16)) return false;
+    return !bwd || (on(a.dy, 16) && on(a.dg, 16) && on(a.dx, 16));
+}
 
-GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width, int dtype, bool bwd) {
+GateScanLayout layout(int64_t batch, int64_t seqlen, int width, int dtype, bool bwd, bool rows) {
     GateScanLayout l;
-    const int tok = scan_seg(bwd, dtype) * kMain;
+    const int tok = scan_seg(bwd, dtype, rows) * kMain;
     l.nchunks = (seqlen + tok - 1) / tok;
     l.ngroups = (width + kCh - 1) / kCh;
     l.nblocks = (l.nchunks + kBlock - 1) / kBlock;
@@ -785,9 +926,21 @@ GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width, int dt
     return l;
 }
 
+}  // namespace
+
+size_t gate_scan_workspace(int64_t batch, int64_t seqlen, int width, int dtype) {
+    size_t most = 0;
+    for (int k = 0; k < 4; ++k) {
+        const size_t t = layout(batch, seqlen, width, dtype, k & 1, k & 2).total;
+        if (t > most) most = t;
+    }
+    return most;
+}
+
 cudaError_t launch_gate_scan(const GateScanArgs& args, void* workspace, bool bwd, cudaStream_t st) {
     GateScanArgs a = args;
-    const GateScanLayout l = gate_scan_layout(a.batch, a.seqlen, a.width, a.dtype, bwd);
+    const bool rows = !aligned_rows(a, bwd);
+    const GateScanLayout l = layout(a.batch, a.seqlen, a.width, a.dtype, bwd, rows);
     char* w = static_cast<char*>(workspace);
     a.nchunks = l.nchunks;
     a.ngroups = l.ngroups;
@@ -800,8 +953,8 @@ cudaError_t launch_gate_scan(const GateScanArgs& args, void* workspace, bool bwd
     // status word, tickets, maps and carried states start from zero
     const cudaError_t e = cudaMemsetAsync(workspace, 0, l.total, st);
     if (e != cudaSuccess) return e;
-    if (a.dtype == SSD_BF16) return bwd ? launch_typed<bf16_t, true>(a, st) : launch_typed<bf16_t, false>(a, st);
-    return bwd ? launch_typed<float, true>(a, st) : launch_typed<float, false>(a, st);
+    if (a.dtype == SSD_BF16) return bwd ? launch_typed<bf16_t, true>(a, rows, st) : launch_typed<bf16_t, false>(a, rows, st);
+    return bwd ? launch_typed<float, true>(a, rows, st) : launch_typed<float, false>(a, rows, st);
 }
 
 cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st) {

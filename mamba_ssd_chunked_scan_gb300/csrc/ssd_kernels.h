@@ -165,11 +165,14 @@ struct AddNormBwdArgs {
     int rows_per_cta;
 };
 
-// Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of eight segments x kScanCh
-// channels.  A segment holds 16 tokens where that many fit a thread's registers (forward, bf16), else 8.
+// Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of kScanSegs segments x kScanCh
+// channels.  A segment holds as many tokens as let two tiles' values stay in a thread's registers (one 1 - a
+// per element forwards, two values backwards) and three or four tiles' operands in shared memory.
 // A state is handed over once per kScanBlock tiles of a sequence.
-constexpr int kScanCh = 64, kScanBlock = 16, kScanMinTok = 64;
-constexpr int scan_seg(bool bwd, int dtype) { return !bwd && dtype == 1 /* SSD_BF16 */ ? 16 : 8; }
+constexpr int kScanSegs = 16, kScanCh = 64, kScanBlock = 16, kScanMinTok = 64;
+constexpr int scan_seg(bool bwd, int dtype, bool rows) {
+    return dtype == 1 /* SSD_BF16 */ ? (bwd || rows ? 8 : 16) : (bwd ? 4 : 8);
+}
 struct GateScanArgs {
     int64_t batch, seqlen;
     int width;
@@ -296,7 +299,7 @@ cudaError_t launch_gate_norm(const GateNormArgs& a, cudaStream_t st);
 cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
 int64_t add_norm_bwd_shares(int64_t rows, int width);   // row slots of the backward
 cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
-GateScanLayout gate_scan_layout(int64_t batch, int64_t seqlen, int width, int dtype, bool bwd);
+size_t gate_scan_workspace(int64_t batch, int64_t seqlen, int width, int dtype);
 cudaError_t launch_gate_scan(const GateScanArgs& a, void* workspace, bool bwd, cudaStream_t st);
 cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st);
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // NULL when the driver has none

@@ -181,9 +181,7 @@ int ssd_add_norm_bwd(int64_t rows, int32_t width, int32_t dtype, int32_t residua
 
 size_t ssd_gate_scan_workspace_size(const ssd_gate_scan_params_t* p) {
     if (check_scan(p) != SSD_OK) return 0;
-    const size_t f = gate_scan_layout(p->batch, p->seqlen, p->width, p->dtype, false).total;
-    const size_t b = gate_scan_layout(p->batch, p->seqlen, p->width, p->dtype, true).total;
-    return f > b ? f : b;
+    return gate_scan_workspace(p->batch, p->seqlen, p->width, p->dtype);
 }
 
 int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x, const float* initial_states,
