@@ -7,10 +7,10 @@
 // Each step is an affine map of the state, and the maps of consecutive steps
 // compose: (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2).  The work is cut into tiles of
 // kMain segments of SEG tokens x kCh channels.  One CTA per SM has sixteen main warps, one per segment, a
-// thread holding two channels; two hand-over warps, a thread per channel; and loading warps:
-//   loading    takes the next tile by ticket and brings its inputs into a ring of shared-memory stages
-//              (one warp and TMA tiles, or a few warps and 4-byte copies where rows are not aligned to 16),
-//              and sends a finished tile's outputs off from the same stage;
+// thread holding two channels; two hand-over warps, a thread per channel; and a loading warp:
+//   loading    takes the next tile by ticket and brings its inputs into a ring of shared-memory stages (TMA), and
+//              sends a finished tile's outputs off from the same stage.  Where rows are not aligned to 16 bytes
+//              it only takes the tickets, and the main warps load a tile ahead into registers and store directly;
 //   main       forms the next tile's decays and its segment's map, keeping 1 - a in registers; then waits for
 //              the state that enters its segment of the tile before, walks that segment again and writes the
 //              outputs.  So a tile's state has a whole tile's time to arrive;
@@ -49,10 +49,7 @@ namespace {
 
 constexpr int kMain = kScanSegs;       // main warps: segments per tile
 constexpr int kCh = kScanCh;           // channels per tile: two per main thread, one per hand-over thread
-// Loading warps: one for TMA tiles; where rows are copied, as many as leave the main warps the registers they need
-// (registers are given out to four warps at a time: 24 warps have 80 each, 20 have 96).
-constexpr int load_warps(bool rows, bool bwd) { return !rows ? 1 : bwd ? 2 : 6; }
-constexpr int threads(bool rows, bool bwd) { return 32 * (kMain + 2 + load_warps(rows, bwd)); }
+constexpr int kThreads = 32 * (kMain + 2 + 1);
 constexpr int kBlock = kScanBlock;
 static_assert(kCh == 64, "two channels per lane, two hand-over warps");
 
@@ -122,20 +119,16 @@ template <typename T> struct PairWord;
 template <> struct PairWord<bf16_t> { typedef uint32_t type; };
 template <> struct PairWord<float> { typedef uint64_t type; };
 
-// Shapes of a kernel instance.  ROWS: rows are not 16-byte aligned; a stage holds, for each row, the aligned
-// 4-byte words around its channels.
+// Shapes of a kernel instance.  ROWS: rows are not 16-byte aligned, and pass through registers only.
 template <typename T, bool ROWS, bool BWD>
 struct Shape {
     static constexpr int ES = sizeof(T);
     static constexpr int SEG = scan_seg(BWD, ES == 2 ? SSD_BF16 : SSD_F32, ROWS), TOK = SEG * kMain;
-    static constexpr int PITCH = kCh * ES + (ROWS && ES == 2 ? 4 : 0);
-    static constexpr int ARR = TOK * PITCH;                 // one operand's tile
-    static constexpr int NA = BWD ? 3 : 2;                  // g, x (and dy)
+    static constexpr int PITCH = kCh * ES, ARR = TOK * PITCH;   // one operand's tile
+    static constexpr int NA = BWD ? 3 : 2;                      // g, x (and dy)
     static constexpr int STAGE = NA * ARR + (BWD ? kMain * PITCH : 0);   // and, backwards, the h before each segment
-    static constexpr int kStep = (STAGE + 127) / 128 * 128;
-    static constexpr int NS = 4 * kStep <= 212 * 1024 ? 4 : 3;
-    static constexpr size_t kSmem = 128 + (size_t)NS * kStep;
-    static_assert(kSmem <= 212 * 1024, "stages, beside 15 KB of maps and documents");
+    static constexpr int NS = ROWS || 4 * STAGE <= 212 * 1024 ? 4 : 3;
+    static constexpr size_t kSmem = ROWS ? 0 : 128 + (size_t)NS * STAGE;
 };
 
 struct ScanParams {
@@ -165,14 +158,25 @@ __device__ __forceinline__ Tile tile_of(const GateScanArgs& a, uint32_t k) {
 
 // Documents that start inside a tile, or at the token after it: doc[k] = the
 // document that starts at token t0 + k, or -1.  One warp; offsets outside the tile are skipped,
-// so nothing they hold can index out of bounds.
-template <int TOK>
-__device__ void find_docs(const GateScanArgs& a, int64_t t0, int* doc) {
+// so nothing they hold can index out of bounds.  Tiles come in the order of the sequence: the 32 offsets about
+// where the last tile's were found (`near`) mostly hold all that this one needs, in one load.  Returns the next `near`.
+template <int TOK, bool REV>
+__device__ int find_docs(const GateScanArgs& a, int64_t t0, int near, int* doc) {
     const int lane = threadIdx.x & 31;
     for (int k = lane; k <= TOK; k += 32) doc[k] = -1;
+    int lo = near - (REV ? 24 : 4);
+    if (lo < 0) lo = 0;
+    constexpr int64_t kNone = (int64_t)1 << 40;
+    int64_t k = lo + lane < a.ndocs ? (int64_t)__ldg(a.cu + lo + lane) - t0 : kNone;
+    const bool from = lo == 0 || __shfl_sync(0xffffffffu, k, 0) < 0, to = __shfl_sync(0xffffffffu, k, 31) > TOK;
     __syncwarp();
+    if (from && to) {
+        if (k >= 0 && k <= TOK) doc[k] = lo + lane;
+        return lo + __popc(__ballot_sync(0xffffffffu, k < 0));
+    }
     // the first document whose offset is >= t0, 32 probes at a time
-    int lo = 0, hi = a.ndocs;
+    lo = 0;
+    int hi = a.ndocs;
     while (lo < hi) {
         const int gap = (hi - lo + 31) / 32;
         const int at = lo + (lane + 1) * gap - 1;
@@ -183,11 +187,11 @@ __device__ void find_docs(const GateScanArgs& a, int64_t t0, int* doc) {
         if (lo + gap - 1 < hi) hi = lo + gap - 1;
     }
     for (int d = lo; d < a.ndocs; d += 32) {
-        int64_t k = TOK + 1;
-        if (d + lane < a.ndocs) k = (int64_t)__ldg(a.cu + d + lane) - t0;
+        k = d + lane < a.ndocs ? (int64_t)__ldg(a.cu + d + lane) - t0 : kNone;
         if (k >= 0 && k <= TOK) doc[k] = d + lane;
         if (__all_sync(0xffffffffu, k > TOK)) break;
     }
+    return lo;
 }
 
 constexpr int kRing = 8;   // tiles whose numbers and documents are kept: more than one above the stages
@@ -237,19 +241,16 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* 
                  "r"(ptx::smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-// ---------------------------------------------------------------------- loading warps
-__device__ __forceinline__ uint32_t next_ticket(const GateScanArgs& a, int n) {
-    return a.nchunks > 1 ? atomicAdd(a.ticket, 1u) : (uint32_t)(blockIdx.x + gridDim.x * n);
-}
-
-template <typename T, bool DOCS, bool BWD>
-__device__ __forceinline__ void load_tiles(const ScanParams& p, uint8_t* sm, Shared<Shape<T, false, BWD>::TOK, DOCS>& sh) {
-    typedef Shape<T, false, BWD> H;
+// ---------------------------------------------------------------------- loading warp
+template <typename T, bool ROWS, bool DOCS, bool BWD>
+__device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared<Shape<T, ROWS, BWD>::TOK, DOCS>& sh) {
+    typedef Shape<T, ROWS, BWD> H;
     const GateScanArgs& a = p.a;
     const int lane = threadIdx.x & 31;
     auto send = [&](int j) {   // lane 0: tile j's outputs from its stage
+        if constexpr (ROWS) return;
         const Tile& t = sh.tile[j % kRing];
-        const uint8_t* st = sm + (j % H::NS) * H::kStep;
+        const uint8_t* st = sm + (j % H::NS) * H::STAGE;
         if (BWD) {
             tma_store_3d(&p.dg, st, t.group * kCh, (int)t.t0, t.row);
             tma_store_3d(&p.dx, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
@@ -258,16 +259,17 @@ __device__ __forceinline__ void load_tiles(const ScanParams& p, uint8_t* sm, Sha
         }
         ptx::bulk_commit();
     };
+    int near = 0;            // documents that start before the last tile, about
     int n = 0, filled = 0;   // tiles, and phases of the stages' `full` begun (the end's among them)
     bool go = true;
     for (;; ++n) {
         uint32_t k = 0;
-        if (lane == 0) k = next_ticket(a, n);
+        if (lane == 0) k = a.nchunks > 1 ? atomicAdd(a.ticket, 1u) : (uint32_t)(blockIdx.x + gridDim.x * n);
         k = __shfl_sync(0xffffffffu, k, 0);
         const Tile t = tile_of<BWD, H::TOK>(a, k);
         // the slot's last tile, n - kRing, is done with: a later one's outputs have been waited for
         if (lane == 0) sh.tile[n % kRing] = t;
-        if (DOCS && t.ntok) find_docs<H::TOK>(a, t.t0, sh.doc[n % kRing]);
+        if (DOCS && t.ntok) near = find_docs<H::TOK, BWD>(a, t.t0, near, sh.doc[n % kRing]);
         const int st = n % H::NS;
         if (n >= H::NS) {
             if (lane == 0) {
@@ -282,10 +284,10 @@ __device__ __forceinline__ void load_tiles(const ScanParams& p, uint8_t* sm, Sha
         uint64_t* full = &sh.full[st];
         ++filled;
         if (lane == 0) {
-            if (!t.ntok) {
+            if (ROWS || !t.ntok) {
                 ptx::mbar_arrive(full);
             } else {
-                uint8_t* dst = sm + st * H::kStep;
+                uint8_t* dst = sm + st * H::STAGE;
                 ptx::mbar_expect_tx(full, H::STAGE);
                 const int c = t.group * kCh, t0 = (int)t.t0;
                 tma_load_3d(dst, &p.g, full, c, t0, t.row);
@@ -310,103 +312,6 @@ __device__ __forceinline__ void load_tiles(const ScanParams& p, uint8_t* sm, Sha
         if (!ptx::mbar_wait(&sh.full[st], (last / H::NS) & 1, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereStage);
     }
     ptx::bulk_wait0();
-}
-
-__device__ __forceinline__ void copy_word(uint8_t* dst, uint64_t src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
-// The aligned 4-byte words around the channels of rows k, k + WARPS, ... (of `bytes` bytes each, `pitch` bytes
-// apart, row 0 at `at`) into smem rows of PITCH bytes, by a warp.  All of a row's PITCH / 4 words are
-// copied where they lie inside the tensor [begin, end) even past the channels; in tiles at its ends only words with
-// channels are, and one that reaches past it (half of it an element) by halves.
-template <int ES, int PITCH, int WARPS>
-__device__ __forceinline__ void copy_rows(uint8_t* dst, uint64_t at, int64_t pitch, int bytes, int k, int rows, uint64_t begin,
-                                          uint64_t end) {
-    const int lane = threadIdx.x & 31;
-    const uint64_t last = at + (uint64_t)((rows - 1) * pitch);
-    if ((at & ~3ull) >= begin && (last & ~3ull) + PITCH <= end) {
-        uint64_t src = at + (uint64_t)(k * pitch);
-        uint8_t* to = dst + k * PITCH + 4 * lane;
-#pragma unroll 4
-        for (int r = k; r < rows; r += WARPS) {
-            copy_word(to, (src & ~3ull) + 4 * lane);
-            if (ES == 4) copy_word(to + 128, src + 4 * lane + 128);
-            src += (uint64_t)(WARPS * pitch);
-            to += WARPS * PITCH;
-        }
-        if (ES == 2)   // the rows' 33rd words
-            for (int r = 32 * k + lane; r < rows; r += 32 * WARPS)
-                copy_word(dst + r * PITCH + 128, ((at + (uint64_t)(r * pitch)) & ~3ull) + 128);
-        return;
-    }
-    for (int r = k; r < rows; r += WARPS) {
-        const uint64_t row = at + (uint64_t)(r * pitch), lo = row & ~3ull;
-        const int words = (int)((row + bytes + 3 - lo) >> 2);
-        for (int w = lane; w < words; w += 32) {
-            const uint64_t src = lo + 4 * w;
-            if (ES == 4 || (src >= begin && src + 4 <= end)) {
-                copy_word(dst + r * PITCH + 4 * w, src);
-            } else {
-#pragma unroll
-                for (int h = 0; h < 4; h += 2)
-                    if (src + h >= begin && src + h < end)
-                        *reinterpret_cast<uint16_t*>(dst + r * PITCH + 4 * w + h) = *reinterpret_cast<const uint16_t*>(src + h);
-            }
-        }
-    }
-}
-
-template <typename T, bool DOCS, bool BWD>
-__device__ __forceinline__ void load_rows(const ScanParams& p, uint8_t* sm, Shared<Shape<T, true, BWD>::TOK, DOCS>& sh) {
-    typedef Shape<T, true, BWD> H;
-    const GateScanArgs& a = p.a;
-    constexpr int WARPS = load_warps(true, BWD);
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kMain - 2;
-    const void* base[3] = {a.g, a.x, a.dy};
-    const int64_t pitch[3] = {a.g_stride, a.x_stride, a.width};
-    for (int n = 0;; ++n) {
-        if (w == 0) {
-            uint32_t k = 0;
-            if (lane == 0) k = next_ticket(a, n);
-            k = __shfl_sync(0xffffffffu, k, 0);
-            const Tile t = tile_of<BWD, H::TOK>(a, k);
-            if (lane == 0) sh.tile[n % kRing] = t;
-            if (DOCS && t.ntok) find_docs<H::TOK>(a, t.t0, sh.doc[n % kRing]);
-        }
-        const int st = n % H::NS;
-        bool go = n < H::NS || bar_wait(sh, a.ws, &sh.done[st], ((n / H::NS) - 1) & 1, kWhereDone);
-        // the tile's number is there; the warps go on or stop together
-        go = !ptx::named_bar_any(1, 32 * WARPS, !go);
-        if (!go) break;
-        const Tile t = sh.tile[n % kRing];
-        uint64_t* full = &sh.full[st];
-        if (t.ntok) {
-            uint8_t* dst = sm + st * H::kStep;
-            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0;
-            const int c = t.group * kCh, cols = a.width - c < kCh ? a.width - c : kCh;
-            const int64_t rows = a.batch * a.seqlen;
-#pragma unroll
-            for (int r = 0; r < H::NA; ++r) {
-                const uint64_t b = (uint64_t)(uintptr_t)base[r];
-                copy_rows<H::ES, H::PITCH, WARPS>(dst + r * H::ARR, b + (uint64_t)(tok * pitch[r] + c) * H::ES, pitch[r] * H::ES,
-                                                  cols * H::ES, w, t.ntok, b, b + (uint64_t)((rows - 1) * pitch[r] + a.width) * H::ES);
-            }
-            if (BWD) {   // the h before each segment; none before the sequence's first
-                const uint64_t b = (uint64_t)(uintptr_t)a.y;
-                const int none = t.t0 == 0 ? 1 : 0, segs = (t.ntok + H::SEG - 1) / H::SEG - none;
-                if (segs > 0)
-                    copy_rows<H::ES, H::PITCH, WARPS>(dst + H::NA * H::ARR + none * H::PITCH,
-                                                      b + (uint64_t)((tok + none * H::SEG - 1) * a.width + c) * H::ES,
-                                                      (int64_t)H::SEG * a.width * H::ES, cols * H::ES, w, segs, b,
-                                                      b + (uint64_t)(rows * a.width) * H::ES);
-            }
-        }
-        // two arrivals per thread: its plain stores, and its copies when they have landed
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(full)) : "memory");
-        ptx::mbar_arrive(full);
-        if (!t.ntok) break;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------- hand-over warps
@@ -492,9 +397,11 @@ struct Main {
     uint8_t* st;       // its stage, at this thread's segment and channels
     int s0, c0;        // the segment's first token in the tile; the thread's first channel
     bool ok0, ok1;
-    uint32_t skew[3], step[3];   // ROWS: low bits of the first row's address, and of the rows' pitch
+    bool plain;        // the segment is inside the sequence, and no document starts or ends in it
+    // ROWS: the operands of the tile to come, and the h before its segment
+    W raw[ROWS ? H::NA : 1][ROWS ? SEG : 1], hraw;
 
-    // Tile n of the walk, for its first or its second visit.
+    // Tile n of the walk, for one of its visits.
     __device__ __forceinline__ void open(int n, uint8_t* sm) {
         t = sh.tile[n % kRing];
         doc = sh.doc[DOCS ? n % kRing : 0];
@@ -503,16 +410,11 @@ struct Main {
         c0 = t.group * kCh + (ROWS ? lane : 2 * lane);
         ok0 = c0 < a.width;
         ok1 = c0 + kApart < a.width;
-        st = sm + (n % H::NS) * H::kStep + s0 * H::PITCH + (ROWS ? lane : 2 * lane) * H::ES;
-        if constexpr (ROWS && sizeof(T) == 2) {
-            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
-            const void* base[3] = {a.g, a.x, a.dy};
-            const int64_t pitch[3] = {a.g_stride, a.x_stride, a.width};
-#pragma unroll
-            for (int r = 0; r < H::NA; ++r) {
-                skew[r] = (uint32_t)(uintptr_t)base[r] + (uint32_t)((tok * pitch[r] + t.group * kCh) * H::ES);
-                step[r] = (uint32_t)(pitch[r] * H::ES);
-            }
+        st = sm + (n % H::NS) * H::STAGE + s0 * H::PITCH + 2 * lane * H::ES;
+        plain = s0 + SEG <= t.ntok;
+        if (DOCS) {
+            const bool event = lane <= SEG && s0 + lane <= H::TOK && doc[s0 + lane] >= 0;
+            plain = !__any_sync(0xffffffffu, event) && t.t0 + s0 + SEG < a.seqlen;
         }
     }
     static __device__ __forceinline__ f2 widen(W w) {
@@ -528,73 +430,59 @@ struct Main {
             return v;
         }
     }
-    static __device__ __forceinline__ f2 two(const uint8_t* q) {   // ROWS: channels kApart apart, element-aligned
-        if constexpr (sizeof(T) == 2)
-            return pk(__uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(q) << 16),
-                      __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(q + 64) << 16));
-        else
-            return pk(*reinterpret_cast<const float*>(q), *reinterpret_cast<const float*>(q + 128));
+    // ROWS: the thread's two elements in one row
+    __device__ __forceinline__ W fetch(const T* q, bool in) const {
+        if constexpr (sizeof(T) == 2) {
+            uint16_t lo = 0, hi = 0;
+            if (in && ok0) lo = __ldcs(reinterpret_cast<const uint16_t*>(q));
+            if (in && ok1) hi = __ldcs(reinterpret_cast<const uint16_t*>(q) + kApart);
+            return (uint32_t)lo | ((uint32_t)hi << 16);
+        } else {
+            return pk(in && ok0 ? __ldcs(q) : 0.f, in && ok1 ? __ldcs(q + kApart) : 0.f);
+        }
     }
-    // operand r (g, x, dy) at token k of the segment
-    __device__ __forceinline__ f2 in(int r, int k) const {
-        const uint8_t* q = st + r * H::ARR + k * H::PITCH;
-        if constexpr (!ROWS) return widen(*reinterpret_cast<const W*>(q));
-        else if constexpr (sizeof(T) == 2) return two(q + ((skew[r] + k * step[r]) & 2));
-        else return two(q);
-    }
-    // A result of the segment, SEG rows of two channels per thread.  Aligned tiles leave it over operand r's
-    // place in the stage, from where it is sent off.  Rows of half words are put together in the stage
-    // as the aligned words that they are in memory and stored by words, those of whole words directly.
-    struct Out {
-        W w[SEG];
-    };
-    __device__ __forceinline__ void put(Out& o, int r, int k, f2 v) const {
-        if constexpr (ROWS) o.w[k] = narrow(v);
-        else *reinterpret_cast<W*>(st + r * H::ARR + k * H::PITCH) = narrow(v);
-    }
-    __device__ __forceinline__ void flush(const Out& o, int r, void* base, int64_t pitch) const {
+    __device__ __forceinline__ bool load(int n, uint8_t* sm) {
         if constexpr (ROWS) {
+            if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
+            open(n, sm);
+            if (!t.ntok) return true;
             const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
-            const int rows = t.ntok - s0 < SEG ? t.ntok - s0 : SEG;
-            if constexpr (sizeof(T) == 4) {
-                float* q = static_cast<float*>(base) + tok * pitch + c0;
+            const T* g = static_cast<const T*>(a.g) + tok * a.g_stride + c0;
+            const T* x = static_cast<const T*>(a.x) + tok * a.x_stride + c0;
+            const T* dy = static_cast<const T*>(a.dy) + tok * a.width + c0;
 #pragma unroll
-                for (int k = 0; k < SEG; ++k)
-                    if (k < rows) {
-                        const float2 f = un(o.w[k]);
-                        if (ok0) q[k * pitch] = f.x;
-                        if (ok1) q[k * pitch + kApart] = f.y;
-                    }
-            } else {
-                uint8_t* mine = st + r * H::ARR;                      // at this lane's element
-                uint64_t at = (uint64_t)(uintptr_t)base + (uint64_t)(tok * pitch + t.group * kCh) * 2;
-                const uint32_t low = (uint32_t)at, by = (uint32_t)(pitch * 2);
-                __syncwarp();   // every lane has read the operand
-#pragma unroll
-                for (int k = 0; k < SEG; ++k) {
-                    uint8_t* q = mine + k * H::PITCH + ((low + k * by) & 2);
-                    *reinterpret_cast<uint16_t*>(q) = (uint16_t)o.w[k];
-                    *reinterpret_cast<uint16_t*>(q + 64) = (uint16_t)(o.w[k] >> 16);
-                }
-                __syncwarp();
-                const int bytes = 2 * (a.width - t.group * kCh < kCh ? a.width - t.group * kCh : kCh);
-                const uint8_t* words = mine + 2 * lane;                // word `lane` of the row
-#pragma unroll
-                for (int k = 0; k < SEG; ++k) {
-                    if (k < rows) {
-                        const int skip = (int)(at & 2);
-                        uint8_t* to = reinterpret_cast<uint8_t*>(at - skip) + 4 * lane;
-                        const int o0 = 4 * lane - skip;                // the word's place in the row, in bytes
-                        const uint32_t v = *reinterpret_cast<const uint32_t*>(words + k * H::PITCH);
-                        if (o0 >= 0 && o0 + 4 <= bytes) *reinterpret_cast<uint32_t*>(to) = v;
-                        else if (o0 < 0) *reinterpret_cast<uint16_t*>(to + 2) = (uint16_t)(v >> 16);
-                        else if (o0 < bytes) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v;
-                        if (skip && lane == 0 && bytes == 2 * kCh)     // the last element, in a 33rd word
-                            *reinterpret_cast<uint16_t*>(to + 128) = *reinterpret_cast<const uint16_t*>(words + k * H::PITCH + 128);
-                    }
-                    at += by;
+            for (int k = 0; k < SEG; ++k) {
+                const bool in = s0 + k < t.ntok;
+                raw[0][k] = fetch(g, in);
+                raw[1][k] = fetch(x, in);
+                g += a.g_stride;
+                x += a.x_stride;
+                if constexpr (BWD) {
+                    raw[2][k] = fetch(dy, in);
+                    dy += a.width;
                 }
             }
+            // the h before the segment: the output before it
+            if constexpr (BWD) hraw = fetch(static_cast<const T*>(a.y) + (tok - 1) * a.width + c0, s0 < t.ntok && t.t0 + s0 > 0);
+        }
+        return true;
+    }
+    // operand r (g, x, dy) at token k of the segment.  The second visit's (x forwards, dy backwards) are kept
+    // where the operands pass through registers.
+    __device__ __forceinline__ f2 in(int r, int k) const {
+        if constexpr (ROWS) return widen(raw[r][k]);
+        else return widen(*reinterpret_cast<const W*>(st + r * H::ARR + k * H::PITCH));
+    }
+    // A result over operand r's place in the stage, from where it is sent off, or straight to memory.
+    __device__ __forceinline__ void put(int r, void* base, int64_t pitch, int k, f2 v) const {
+        const W w = narrow(v);
+        if constexpr (!ROWS) {
+            *reinterpret_cast<W*>(st + r * H::ARR + k * H::PITCH) = w;
+        } else {
+            T* q = static_cast<T*>(base) + ((int64_t)t.row * a.seqlen + t.t0 + s0) * pitch + c0 + k * pitch;
+            const T* e = reinterpret_cast<const T*>(&w);
+            if (ok0) q[0] = e[0];
+            if (ok1) q[kApart] = e[1];
         }
     }
     // two channels of row `row` of a (rows, width) fp32 array, zero without one
@@ -634,110 +522,104 @@ struct Main {
         return t.t0 + s0 + k == a.seqlen - 1 ? a.ndocs - 1 : doc[s0 + k + 1] - 1;
     }
 
-    // what the first visit keeps for the second: 1 - a and, backwards, u = d(h_t)/d(g_t)
+    // what the first visit keeps for the second: 1 - a and, backwards, u = d(h_t)/d(g_t); and an operand where it
+    // came through registers
     struct Keep {
         f2 m[SEG], u[BWD ? SEG : 1];
+        W r[ROWS ? SEG : 1];
     };
+    __device__ __forceinline__ f2 kept(const Keep& q, int k) const {
+        if constexpr (ROWS) return widen(q.r[k]);
+        else return in(BWD ? 2 : 1, k);
+    }
 
-    // WHOLE: every token of the segment is inside the sequence
-    template <bool WHOLE>
+    // PLAIN: every token of the segment is inside the sequence, and no document starts or ends in it
+    template <bool PLAIN>
     __device__ __forceinline__ void first_fwd(Keep& q) {
         f2 A = pk(1.f, 1.f), B = pk(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
-            if (!WHOLE && s0 + k >= t.ntok) break;
+            if (!PLAIN && s0 + k >= t.ntok) break;
             f2 av;
             gate2<T>(in(0, k), av, q.m[k]);
-            if (starts(k)) {
+            if (!PLAIN && starts(k)) {
                 A = pk(0.f, 0.f);
                 B = state(a.init, doc[s0 + k]);
             }
             A = mul(A, av);
             B = fma2(av, B, mul(q.m[k], in(1, k)));
+            if constexpr (ROWS) q.r[k] = raw[1][k];
         }
         put_map(A, B);
     }
-    template <bool WHOLE>
+    template <bool PLAIN>
     __device__ __forceinline__ void second_fwd(const Keep& q) {
         f2 h = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
-        Out y;
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
-            if (!WHOLE && s0 + k >= t.ntok) break;
-            if (starts(k)) h = state(a.init, doc[s0 + k]);
-            h = fma2(fma2(q.m[k], minus, one), h, mul(q.m[k], in(1, k)));
-            put(y, 1, k, h);
-            if (DOCS && a.leave && ends(k)) {
+            if (!PLAIN && s0 + k >= t.ntok) break;
+            if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
+            h = fma2(fma2(q.m[k], minus, one), h, mul(q.m[k], kept(q, k)));
+            put(1, a.y, a.width, k, h);
+            if (DOCS && !PLAIN && a.leave && ends(k)) {
                 const int at = ending(k);
                 if (at >= 0) put_state(a.leave, at, h);
             }
         }
-        flush(y, 1, a.y, a.width);
     }
-    template <bool WHOLE>
+    template <bool PLAIN>
     __device__ __forceinline__ void first_bwd(Keep& q) {
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
         f2 h;
-        if (t.t0 + s0 == 0) {
-            h = DOCS ? pk(0.f, 0.f) : state(a.init, t.row);
-        } else {
-            const uint8_t* r = st - s0 * H::PITCH + H::NA * H::ARR + warp * H::PITCH;
-            if constexpr (!ROWS) {
-                h = widen(*reinterpret_cast<const W*>(r));
-            } else {
-                const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0 - 1;
-                const uint32_t low = (uint32_t)(uintptr_t)a.y + (uint32_t)((tok * a.width + t.group * kCh) * H::ES);
-                h = two(r + (sizeof(T) == 2 ? low & 2 : 0));
-            }
-        }
+        if (t.t0 + s0 == 0) h = DOCS ? pk(0.f, 0.f) : state(a.init, t.row);
+        else if constexpr (ROWS) h = widen(hraw);
+        else h = widen(*reinterpret_cast<const W*>(st - s0 * H::PITCH + H::NA * H::ARR + warp * H::PITCH));
         // forwards through the segment: u = (h_{t-1} - x) a (1 - a)
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
-            if (!WHOLE && s0 + k >= t.ntok) break;
+            if (!PLAIN && s0 + k >= t.ntok) break;
             f2 av;
             const f2 xv = in(1, k);
             gate2<T>(in(0, k), av, q.m[k]);
-            if (starts(k)) h = state(a.init, doc[s0 + k]);
+            if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
             q.u[k] = mul(fma2(xv, minus, h), mul(av, q.m[k]));
             h = fma2(av, h, mul(q.m[k], xv));
+            if constexpr (ROWS) q.r[k] = raw[2][k];
         }
         // backwards: the map of mu over the segment
         f2 A = one, B = pk(0.f, 0.f);
 #pragma unroll
         for (int k = SEG - 1; k >= 0; --k) {
-            if (!WHOLE && s0 + k >= t.ntok) continue;
-            if (ends(k)) {
+            if (!PLAIN && s0 + k >= t.ntok) continue;
+            if (!PLAIN && ends(k)) {
                 const int at = ending(k);
                 A = pk(0.f, 0.f);
                 B = at >= 0 ? state(a.enter, at) : A;
             }
             const f2 av = fma2(q.m[k], minus, one);
-            B = mul(av, add(in(2, k), B));
+            B = mul(av, add(kept(q, k), B));
             A = mul(A, av);
         }
         put_map(A, B);
     }
-    template <bool WHOLE>
+    template <bool PLAIN>
     __device__ __forceinline__ void second_bwd(const Keep& q) {
         f2 mu = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
-        Out dg, dx;
 #pragma unroll
         for (int k = SEG - 1; k >= 0; --k) {
-            if (!WHOLE && s0 + k >= t.ntok) continue;
-            if (ends(k)) {
+            if (!PLAIN && s0 + k >= t.ntok) continue;
+            if (!PLAIN && ends(k)) {
                 const int at = ending(k);
                 mu = at >= 0 ? state(a.enter, at) : pk(0.f, 0.f);
             }
-            const f2 lam = add(in(2, k), mu);
-            put(dg, 0, k, mul(lam, q.u[k]));
-            put(dx, 1, k, mul(lam, q.m[k]));
+            const f2 lam = add(kept(q, k), mu);
+            put(0, a.dg, a.g_stride, k, mul(lam, q.u[k]));
+            put(1, a.dx, a.x_stride, k, mul(lam, q.m[k]));
             mu = mul(fma2(q.m[k], minus, one), lam);
-            if (DOCS && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
+            if (DOCS && !PLAIN && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
         }
-        flush(dg, 0, a.dg, a.g_stride);
-        flush(dx, 1, a.dx, a.x_stride);
     }
 
     // The first visit to tile n; false: there is none, or a wait ran out.
@@ -745,12 +627,11 @@ struct Main {
         if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
         open(n, sm);
         if (t.ntok) {
-            const bool whole = s0 + SEG <= t.ntok;
             if constexpr (BWD) {
-                if (whole) first_bwd<true>(q);
+                if (plain) first_bwd<true>(q);
                 else first_bwd<false>(q);
             } else {
-                if (whole) first_fwd<true>(q);
+                if (plain) first_fwd<true>(q);
                 else first_fwd<false>(q);
             }
         }
@@ -761,12 +642,11 @@ struct Main {
     __device__ __forceinline__ bool second(int n, uint8_t* sm, const Keep& q) {
         if (!bar_wait(sh, a.ws, &sh.states[n & 1], (n >> 1) & 1, kWhereState)) return false;
         open(n, sm);
-        const bool whole = s0 + SEG <= t.ntok;
         if constexpr (BWD) {
-            if (whole) second_bwd<true>(q);
+            if (plain) second_bwd<true>(q);
             else second_bwd<false>(q);
         } else {
-            if (whole) second_fwd<true>(q);
+            if (plain) second_fwd<true>(q);
             else second_fwd<false>(q);
         }
         if (!ROWS) ptx::fence_proxy_async();   // the outputs in the stage, before they are sent off
@@ -776,9 +656,12 @@ struct Main {
     }
     __device__ __forceinline__ void run(uint8_t* sm) {
         Keep cur, next;
+        if (!load(0, sm)) return;
         bool more = first(0, sm, cur);
+        if (more && !load(1, sm)) return;
         for (int n = 0; more; ++n) {
             more = first(n + 1, sm, next);
+            if (more && !load(n + 2, sm)) return;
             if (!second(n, sm, cur)) return;
             cur = next;
         }
@@ -786,7 +669,7 @@ struct Main {
 };
 
 template <typename T, bool ROWS, bool DOCS, bool BWD>
-__global__ void __launch_bounds__(threads(ROWS, BWD), 1) ssd_gate_scan_kernel(const __grid_constant__ ScanParams p) {
+__global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid_constant__ ScanParams p) {
     typedef Shape<T, ROWS, BWD> H;
     static_assert(H::kSmem + sizeof(Shared<H::TOK, DOCS>) <= 227 * 1024, "a CTA's shared memory");
     extern __shared__ uint8_t smem_raw[];
@@ -795,7 +678,7 @@ __global__ void __launch_bounds__(threads(ROWS, BWD), 1) ssd_gate_scan_kernel(co
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
-            ptx::mbar_init(&sh.full[i], ROWS ? 2 * 32 * load_warps(ROWS, BWD) : 1);
+            ptx::mbar_init(&sh.full[i], 1);
             ptx::mbar_init(&sh.done[i], kMain);
         }
         for (int i = 0; i < 2; ++i) {
@@ -813,10 +696,8 @@ __global__ void __launch_bounds__(threads(ROWS, BWD), 1) ssd_gate_scan_kernel(co
     } else if (warp < kMain + 2) {
         hand_over<BWD>(p.a, sh);
     } else {
-        if (DOCS && blockIdx.x == 0 && warp == kMain + 2)
-            check_cu_seqlens(p.a.cu, p.a.ndocs, p.a.seqlen, p.a.ws, threadIdx.x & 31, 32);
-        if constexpr (ROWS) load_rows<T, DOCS, BWD>(p, sm, sh);
-        else load_tiles<T, DOCS, BWD>(p, sm, sh);
+        if (DOCS && blockIdx.x == 0) check_cu_seqlens(p.a.cu, p.a.ndocs, p.a.seqlen, p.a.ws, threadIdx.x & 31, 32);
+        loading<T, ROWS, DOCS, BWD>(p, sm, sh);
     }
 }
 
@@ -883,7 +764,7 @@ cudaError_t launch_one(const ScanParams& p, cudaStream_t st) {
     // one CTA per SM; with tickets any number of them finishes the work
     const int nsm = device_sms();
     const uint32_t most = nsm > 0 ? nsm : 152;
-    kern<<<p.a.ntiles < most ? p.a.ntiles : most, threads(ROWS, BWD), smem, st>>>(p);
+    kern<<<p.a.ntiles < most ? p.a.ntiles : most, kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
