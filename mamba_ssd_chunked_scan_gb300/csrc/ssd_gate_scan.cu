@@ -128,7 +128,9 @@ struct Shape {
     static constexpr int NA = BWD ? 3 : 2;                      // g, x (and dy)
     static constexpr int STAGE = NA * ARR + (BWD ? kMain * PITCH : 0);   // and, backwards, the h before each segment
     static constexpr int NS = ROWS || 4 * STAGE <= 212 * 1024 ? 4 : 3;
-    static constexpr size_t kSmem = ROWS ? 0 : 128 + (size_t)NS * STAGE;
+    // ROWS: what the first visits of two tiles keep for the second, per token and thread
+    static constexpr int kKeep = 2 * SEG * 32 * kMain * (8 + (BWD ? 8 : 0) + 2 * ES);
+    static constexpr size_t kSmem = 128 + (ROWS ? (size_t)kKeep : (size_t)NS * STAGE);
 };
 
 struct ScanParams {
@@ -398,8 +400,12 @@ struct Main {
     int s0, c0;        // the segment's first token in the tile; the thread's first channel
     bool ok0, ok1;
     bool plain;        // the segment is inside the sequence, and no document starts or ends in it
-    // ROWS: the operands of the tile to come, and the h before its segment
-    W raw[ROWS ? H::NA : 1][ROWS ? SEG : 1], hraw;
+    // ROWS: the operands of the tile to come, and the h before its segment, as loaded (nothing touches them
+    // before the tile's first visit, so they arrive during the second visit of the tile before)
+    struct Pair {
+        uint32_t lo, hi;
+    };
+    Pair raw[ROWS ? H::NA : 1][ROWS ? SEG : 1], hraw;
 
     // Tile n of the walk, for one of its visits.
     __device__ __forceinline__ void open(int n, uint8_t* sm) {
@@ -431,15 +437,22 @@ struct Main {
         }
     }
     // ROWS: the thread's two elements in one row
-    __device__ __forceinline__ W fetch(const T* q, bool in) const {
+    __device__ __forceinline__ Pair fetch(const T* q, bool in) const {
+        Pair p = {0u, 0u};
         if constexpr (sizeof(T) == 2) {
-            uint16_t lo = 0, hi = 0;
-            if (in && ok0) lo = __ldcs(reinterpret_cast<const uint16_t*>(q));
-            if (in && ok1) hi = __ldcs(reinterpret_cast<const uint16_t*>(q) + kApart);
-            return (uint32_t)lo | ((uint32_t)hi << 16);
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
+            if (in && ok0) p.lo = __ldcs(e);
+            if (in && ok1) p.hi = __ldcs(e + kApart);
         } else {
-            return pk(in && ok0 ? __ldcs(q) : 0.f, in && ok1 ? __ldcs(q + kApart) : 0.f);
+            const uint32_t* e = reinterpret_cast<const uint32_t*>(q);
+            if (in && ok0) p.lo = __ldcs(e);
+            if (in && ok1) p.hi = __ldcs(e + kApart);
         }
+        return p;
+    }
+    static __device__ __forceinline__ f2 widen(Pair p) {
+        if constexpr (sizeof(T) == 2) return pk(__uint_as_float(p.lo << 16), __uint_as_float(p.hi << 16));
+        else return pk(__uint_as_float(p.lo), __uint_as_float(p.hi));
     }
     __device__ __forceinline__ bool load(int n, uint8_t* sm) {
         if constexpr (ROWS) {
@@ -467,8 +480,7 @@ struct Main {
         }
         return true;
     }
-    // operand r (g, x, dy) at token k of the segment.  The second visit's (x forwards, dy backwards) are kept
-    // where the operands pass through registers.
+    // operand r (g, x, dy) at token k of the segment
     __device__ __forceinline__ f2 in(int r, int k) const {
         if constexpr (ROWS) return widen(raw[r][k]);
         else return widen(*reinterpret_cast<const W*>(st + r * H::ARR + k * H::PITCH));
@@ -522,14 +534,43 @@ struct Main {
         return t.t0 + s0 + k == a.seqlen - 1 ? a.ndocs - 1 : doc[s0 + k + 1] - 1;
     }
 
-    // what the first visit keeps for the second: 1 - a and, backwards, u = d(h_t)/d(g_t); and an operand where it
-    // came through registers
+    // What the first visit keeps for the second: m = 1 - a and, backwards, u = d(h_t)/d(g_t), in registers beside
+    // the operands in the stage; ROWS: in shared memory, with the operand that the second visit needs (r).
     struct Keep {
-        f2 m[SEG], u[BWD ? SEG : 1];
-        W r[ROWS ? SEG : 1];
+        f2 m[ROWS ? 1 : SEG], u[BWD && !ROWS ? SEG : 1];
+        uint8_t* at;
     };
+    __device__ __forceinline__ void bind(Keep& q, int n, uint8_t* sm) const {
+        if constexpr (ROWS) q.at = sm + (n & 1) * (H::kKeep / 2) + (warp * 32 + lane) * 8;
+    }
+    static constexpr int kSlots = SEG * 32 * kMain * 8;   // bytes of one value of 8 bytes
+    __device__ __forceinline__ void set_m(Keep& q, int k, f2 v) const {
+        if constexpr (ROWS) *reinterpret_cast<f2*>(q.at + k * 32 * kMain * 8) = v;
+        else q.m[k] = v;
+    }
+    __device__ __forceinline__ f2 get_m(const Keep& q, int k) const {
+        if constexpr (ROWS) return *reinterpret_cast<const f2*>(q.at + k * 32 * kMain * 8);
+        else return q.m[k];
+    }
+    __device__ __forceinline__ void set_u(Keep& q, int k, f2 v) const {
+        if constexpr (ROWS) *reinterpret_cast<f2*>(q.at + kSlots + k * 32 * kMain * 8) = v;
+        else q.u[k] = v;
+    }
+    __device__ __forceinline__ f2 get_u(const Keep& q, int k) const {
+        if constexpr (ROWS) return *reinterpret_cast<const f2*>(q.at + kSlots + k * 32 * kMain * 8);
+        else return q.u[k];
+    }
+    __device__ __forceinline__ W* kept_at(const Keep& q, int k) const {
+        uint8_t* base = q.at - (warp * 32 + lane) * 8 + (BWD ? 2 : 1) * kSlots;
+        return reinterpret_cast<W*>(base) + k * 32 * kMain + warp * 32 + lane;
+    }
+    __device__ __forceinline__ void set_r(Keep& q, int k, Pair p) const {
+        if constexpr (!ROWS) return;
+        else if constexpr (sizeof(T) == 2) *kept_at(q, k) = p.lo | (p.hi << 16);
+        else *kept_at(q, k) = widen(p);
+    }
     __device__ __forceinline__ f2 kept(const Keep& q, int k) const {
-        if constexpr (ROWS) return widen(q.r[k]);
+        if constexpr (ROWS) return widen(*kept_at(q, k));
         else return in(BWD ? 2 : 1, k);
     }
 
@@ -540,15 +581,16 @@ struct Main {
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
-            f2 av;
-            gate2<T>(in(0, k), av, q.m[k]);
+            f2 av, mv;
+            gate2<T>(in(0, k), av, mv);
             if (!PLAIN && starts(k)) {
                 A = pk(0.f, 0.f);
                 B = state(a.init, doc[s0 + k]);
             }
             A = mul(A, av);
-            B = fma2(av, B, mul(q.m[k], in(1, k)));
-            if constexpr (ROWS) q.r[k] = raw[1][k];
+            B = fma2(av, B, mul(mv, in(1, k)));
+            set_m(q, k, mv);
+            set_r(q, k, raw[ROWS ? 1 : 0][ROWS ? k : 0]);
         }
         put_map(A, B);
     }
@@ -560,7 +602,8 @@ struct Main {
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
-            h = fma2(fma2(q.m[k], minus, one), h, mul(q.m[k], kept(q, k)));
+            const f2 mv = get_m(q, k);
+            h = fma2(fma2(mv, minus, one), h, mul(mv, kept(q, k)));
             put(1, a.y, a.width, k, h);
             if (DOCS && !PLAIN && a.leave && ends(k)) {
                 const int at = ending(k);
@@ -579,13 +622,14 @@ struct Main {
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
-            f2 av;
+            f2 av, mv;
             const f2 xv = in(1, k);
-            gate2<T>(in(0, k), av, q.m[k]);
+            gate2<T>(in(0, k), av, mv);
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
-            q.u[k] = mul(fma2(xv, minus, h), mul(av, q.m[k]));
-            h = fma2(av, h, mul(q.m[k], xv));
-            if constexpr (ROWS) q.r[k] = raw[2][k];
+            set_u(q, k, mul(fma2(xv, minus, h), mul(av, mv)));
+            set_m(q, k, mv);
+            h = fma2(av, h, mul(mv, xv));
+            set_r(q, k, raw[ROWS ? 2 : 0][ROWS ? k : 0]);
         }
         // backwards: the map of mu over the segment
         f2 A = one, B = pk(0.f, 0.f);
@@ -597,8 +641,8 @@ struct Main {
                 A = pk(0.f, 0.f);
                 B = at >= 0 ? state(a.enter, at) : A;
             }
-            const f2 av = fma2(q.m[k], minus, one);
-            B = mul(av, add(kept(q, k), B));
+            const f2 av = fma2(get_m(q, k), minus, one);
+            B = mul(av, add(in(2, k), B));
             A = mul(A, av);
         }
         put_map(A, B);
@@ -615,9 +659,10 @@ struct Main {
                 mu = at >= 0 ? state(a.enter, at) : pk(0.f, 0.f);
             }
             const f2 lam = add(kept(q, k), mu);
-            put(0, a.dg, a.g_stride, k, mul(lam, q.u[k]));
-            put(1, a.dx, a.x_stride, k, mul(lam, q.m[k]));
-            mu = mul(fma2(q.m[k], minus, one), lam);
+            const f2 mv = get_m(q, k);
+            put(0, a.dg, a.g_stride, k, mul(lam, get_u(q, k)));
+            put(1, a.dx, a.x_stride, k, mul(lam, mv));
+            mu = mul(fma2(mv, minus, one), lam);
             if (DOCS && !PLAIN && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
         }
     }
@@ -626,6 +671,7 @@ struct Main {
     __device__ __forceinline__ bool first(int n, uint8_t* sm, Keep& q) {
         if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
         open(n, sm);
+        bind(q, n, sm);
         if (t.ntok) {
             if constexpr (BWD) {
                 if (plain) first_bwd<true>(q);
