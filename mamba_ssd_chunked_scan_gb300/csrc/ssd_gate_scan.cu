@@ -436,47 +436,55 @@ struct Main {
             return v;
         }
     }
-    // ROWS: the thread's two elements in one row
+    // ROWS: row k, `pitch` bytes apart, from p (one multiply-add: 64-bit sums would cost two instructions a row)
+    template <typename P>
+    static __device__ __forceinline__ P* row(P* p, int k, uint32_t pitch) {
+        return reinterpret_cast<P*>(reinterpret_cast<uint64_t>(p) + (uint64_t)(uint32_t)k * pitch);
+    }
+    // ROWS: the thread's two elements in one row.  ALL: both exist.
+    template <bool ALL>
     __device__ __forceinline__ Pair fetch(const T* q, bool in) const {
         Pair p = {0u, 0u};
         if constexpr (sizeof(T) == 2) {
             const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
-            if (in && ok0) p.lo = __ldcs(e);
-            if (in && ok1) p.hi = __ldcs(e + kApart);
+            if (ALL || (in && ok0)) p.lo = __ldcs(e);
+            if (ALL || (in && ok1)) p.hi = __ldcs(e + kApart);
         } else {
             const uint32_t* e = reinterpret_cast<const uint32_t*>(q);
-            if (in && ok0) p.lo = __ldcs(e);
-            if (in && ok1) p.hi = __ldcs(e + kApart);
+            if (ALL || (in && ok0)) p.lo = __ldcs(e);
+            if (ALL || (in && ok1)) p.hi = __ldcs(e + kApart);
         }
         return p;
+    }
+    template <bool ALL>
+    __device__ __forceinline__ void fetch_all() {
+        const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
+        const T* g = static_cast<const T*>(a.g) + tok * a.g_stride + c0;
+        const T* x = static_cast<const T*>(a.x) + tok * a.x_stride + c0;
+        const T* dy = static_cast<const T*>(a.dy) + tok * a.width + c0;
+#pragma unroll
+        for (int k = 0; k < SEG; ++k) {
+            const bool in = s0 + k < t.ntok;
+            raw[0][k] = fetch<ALL>(row(g, k, (uint32_t)a.g_stride * H::ES), in);
+            raw[1][k] = fetch<ALL>(row(x, k, (uint32_t)a.x_stride * H::ES), in);
+            if constexpr (BWD) raw[2][k] = fetch<ALL>(row(dy, k, (uint32_t)a.width * H::ES), in);
+        }
+        // the h before the segment: the output before it
+        if constexpr (BWD) hraw = fetch<false>(static_cast<const T*>(a.y) + (tok - 1) * a.width + c0, s0 < t.ntok && t.t0 + s0 > 0);
     }
     static __device__ __forceinline__ f2 widen(Pair p) {
         if constexpr (sizeof(T) == 2) return pk(__uint_as_float(p.lo << 16), __uint_as_float(p.hi << 16));
         else return pk(__uint_as_float(p.lo), __uint_as_float(p.hi));
     }
+    // whether the segment's tokens and the tile's channels all exist
+    __device__ __forceinline__ bool all() const { return s0 + SEG <= t.ntok && (t.group + 1) * kCh <= a.width; }
     __device__ __forceinline__ bool load(int n, uint8_t* sm) {
         if constexpr (ROWS) {
             if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
             open(n, sm);
             if (!t.ntok) return true;
-            const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
-            const T* g = static_cast<const T*>(a.g) + tok * a.g_stride + c0;
-            const T* x = static_cast<const T*>(a.x) + tok * a.x_stride + c0;
-            const T* dy = static_cast<const T*>(a.dy) + tok * a.width + c0;
-#pragma unroll
-            for (int k = 0; k < SEG; ++k) {
-                const bool in = s0 + k < t.ntok;
-                raw[0][k] = fetch(g, in);
-                raw[1][k] = fetch(x, in);
-                g += a.g_stride;
-                x += a.x_stride;
-                if constexpr (BWD) {
-                    raw[2][k] = fetch(dy, in);
-                    dy += a.width;
-                }
-            }
-            // the h before the segment: the output before it
-            if constexpr (BWD) hraw = fetch(static_cast<const T*>(a.y) + (tok - 1) * a.width + c0, s0 < t.ntok && t.t0 + s0 > 0);
+            if (all()) fetch_all<true>();
+            else fetch_all<false>();
         }
         return true;
     }
@@ -485,17 +493,26 @@ struct Main {
         if constexpr (ROWS) return widen(raw[r][k]);
         else return widen(*reinterpret_cast<const W*>(st + r * H::ARR + k * H::PITCH));
     }
-    // A result over operand r's place in the stage, from where it is sent off, or straight to memory.
-    __device__ __forceinline__ void put(int r, void* base, int64_t pitch, int k, f2 v) const {
+    // A result over operand r's place in the stage, from where it is sent off; ROWS: straight to memory, to row k of
+    // `base` (the segment's first row, at the thread's channels).
+    template <bool ALL>
+    __device__ __forceinline__ void put(int r, T* base, int64_t pitch, int k, f2 v) const {
         const W w = narrow(v);
         if constexpr (!ROWS) {
             *reinterpret_cast<W*>(st + r * H::ARR + k * H::PITCH) = w;
+        } else if constexpr (sizeof(T) == 2) {
+            uint16_t* q = reinterpret_cast<uint16_t*>(row(base, k, (uint32_t)pitch * H::ES));
+            if (ALL || ok0) q[0] = (uint16_t)w;
+            if (ALL || ok1) q[kApart] = (uint16_t)(w >> 16);
         } else {
-            T* q = static_cast<T*>(base) + ((int64_t)t.row * a.seqlen + t.t0 + s0) * pitch + c0 + k * pitch;
-            const T* e = reinterpret_cast<const T*>(&w);
-            if (ok0) q[0] = e[0];
-            if (ok1) q[kApart] = e[1];
+            T* q = row(base, k, (uint32_t)pitch * H::ES);
+            const float2 f = un(w);
+            if (ALL || ok0) q[0] = f.x;
+            if (ALL || ok1) q[kApart] = f.y;
         }
+    }
+    __device__ __forceinline__ T* mine(void* base, int64_t pitch) const {
+        return static_cast<T*>(base) + ((int64_t)t.row * a.seqlen + t.t0 + s0) * pitch + c0;
     }
     // two channels of row `row` of a (rows, width) fp32 array, zero without one
     __device__ __forceinline__ f2 state(const float* p, int64_t row) const {
@@ -594,17 +611,19 @@ struct Main {
         }
         put_map(A, B);
     }
-    template <bool PLAIN>
+    // ALL: the tile's channels all exist
+    template <bool PLAIN, bool ALL>
     __device__ __forceinline__ void second_fwd(const Keep& q) {
         f2 h = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+        T* y = mine(a.y, a.width);
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
             const f2 mv = get_m(q, k);
             h = fma2(fma2(mv, minus, one), h, mul(mv, kept(q, k)));
-            put(1, a.y, a.width, k, h);
+            put<ALL>(1, y, a.width, k, h);
             if (DOCS && !PLAIN && a.leave && ends(k)) {
                 const int at = ending(k);
                 if (at >= 0) put_state(a.leave, at, h);
@@ -647,10 +666,11 @@ struct Main {
         }
         put_map(A, B);
     }
-    template <bool PLAIN>
+    template <bool PLAIN, bool ALL>
     __device__ __forceinline__ void second_bwd(const Keep& q) {
         f2 mu = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+        T *dg = mine(a.dg, a.g_stride), *dx = mine(a.dx, a.x_stride);
 #pragma unroll
         for (int k = SEG - 1; k >= 0; --k) {
             if (!PLAIN && s0 + k >= t.ntok) continue;
@@ -660,8 +680,8 @@ struct Main {
             }
             const f2 lam = add(kept(q, k), mu);
             const f2 mv = get_m(q, k);
-            put(0, a.dg, a.g_stride, k, mul(lam, get_u(q, k)));
-            put(1, a.dx, a.x_stride, k, mul(lam, mv));
+            put<ALL>(0, dg, a.g_stride, k, mul(lam, get_u(q, k)));
+            put<ALL>(1, dx, a.x_stride, k, mul(lam, mv));
             mu = mul(fma2(mv, minus, one), lam);
             if (DOCS && !PLAIN && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
         }
@@ -689,11 +709,11 @@ struct Main {
         if (!bar_wait(sh, a.ws, &sh.states[n & 1], (n >> 1) & 1, kWhereState)) return false;
         open(n, sm);
         if constexpr (BWD) {
-            if (plain) second_bwd<true>(q);
-            else second_bwd<false>(q);
+            if (plain && (!ROWS || all())) second_bwd<true, true>(q);
+            else second_bwd<false, false>(q);
         } else {
-            if (plain) second_fwd<true>(q);
-            else second_fwd<false>(q);
+            if (plain && (!ROWS || all())) second_fwd<true, true>(q);
+            else second_fwd<false, false>(q);
         }
         if (!ROWS) ptx::fence_proxy_async();   // the outputs in the stage, before they are sent off
         __syncwarp();

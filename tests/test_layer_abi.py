@@ -71,7 +71,7 @@ def scan_params(**kw):
 SCAN_PARAMS = [
     (dict(batch=0), 1), (dict(seqlen=0), 1), (dict(width=0), 1), (dict(g_stride=127), 1), (dict(x_stride=0), 1),
     (dict(dtype=2), 1), (dict(ndocs=-1), 1), (dict(ndocs=2), 1), (dict(seqlen=1 << 31), 2), (dict(batch=1 << 31), 2),
-    (dict(g_stride=1 << 31), 2), (dict(batch=1 << 20, seqlen=1 << 20, width=4096, g_stride=4096, x_stride=4096), 2),
+    (dict(g_stride=1 << 31), 2), (dict(g_stride=1 << 29), 2), (dict(batch=1 << 20, seqlen=1 << 20, width=4096, g_stride=4096, x_stride=4096), 2),
 ]
 
 
