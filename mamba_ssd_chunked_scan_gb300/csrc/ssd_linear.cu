@@ -7,7 +7,10 @@
 //
 // One persistent CTA per SM walks tiles (or tiles' parts along the contraction): one thread loads
 // 128-byte-wide operand tiles by TMA into a ring of stages, one issues the MMAs, four warps run the
-// epilogue of the previous tile from the other half of tensor memory meanwhile.
+// epilogue of the previous tile from the other half of tensor memory meanwhile.  Where there are enough
+// tiles, two SMs of a cluster share one of 256 rows (PAIR): each holds the accumulator of its 128 rows and loads
+// its rows of A and half of B's, and the first one issues the MMAs of both.  Operands come from L2, and a pair asks
+// for 64 bytes per SM and cycle of bf16 MMAs where a single CTA asks for 96, more than L2 gives.
 // Operands are bf16 or e4m3; a bf16 operand may also be stored with its contraction along the rows
 // (dx = dpre W reads W so, dw = dpre^T x both), which the shared-memory descriptors express: no
 // operand is ever transposed in memory.
@@ -35,10 +38,12 @@ constexpr int kRowB = 128;             // bytes of the contraction per tile row 
 constexpr int kTileM = 128;
 constexpr uint32_t kWhereEmpty = 61, kWhereFull = 62, kWhereAccFree = 63, kWhereAcc = 64, kWhereDrain = 65;
 
-template <int TN>
+// TB: columns of the tile whose operand rows this CTA loads (half of them in a pair)
+template <int TN, bool PAIR>
 struct Cfg {
-    static constexpr uint32_t kA = kTileM * kRowB, kB = TN * kRowB, kStage = kA + kB;
-    static constexpr int kStages = TN >= 256 ? 4 : TN >= 128 ? 6 : TN >= 64 ? 8 : TN >= 32 ? 9 : 10;
+    static constexpr int TB = PAIR ? TN / 2 : TN;
+    static constexpr uint32_t kA = kTileM * kRowB, kB = TB * kRowB, kStage = kA + kB;
+    static constexpr int kStages = TB >= 256 ? 4 : TB >= 128 ? 6 : TB >= 64 ? 8 : TB >= 32 ? 9 : 10;
     static constexpr uint32_t kCols = 2 * TN < 32 ? 32 : 2 * TN;   // two accumulators
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage;
 };
@@ -67,19 +72,86 @@ __device__ __forceinline__ bool lin_wait(Small& sh, WsHeader* ws, uint64_t* bar,
     return false;
 }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, uint64_t* bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            ptx::smem_u32(dst)),
-        "l"(tm), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1)
-        : "memory");
+// Loads into this CTA's shared memory; in a pair the bytes count on the first CTA's barrier (`bar` is its address).
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, uint32_t bar, int c0, int c1) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], "
+            "[%2];" ::"r"(ptx::smem_u32(dst)),
+            "l"(tm), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                ptx::smem_u32(dst)),
+            "l"(tm), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
 }
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+template <bool E4M3, bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (!PAIR && !E4M3)
+        ptx::mma_ss(d, a, b, idesc, acc);
+    else if constexpr (!PAIR)
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else if constexpr (!E4M3)
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// Arrival on a barrier when the MMAs issued so far are done; in a pair, on the same barrier of both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                ptx::smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        ptx::mma_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(slot)), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        ptx::tmem_alloc(slot, ncols);
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    else
+        ptx::tmem_dealloc(taddr, ncols);
+}
+// Address of `p` in the pair's first CTA.
+__device__ __forceinline__ uint32_t in_first(const void* p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(ptx::smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Instruction descriptor of kind::f8f6f4: e4m3 A and B (both K-major), fp32 accumulator.
@@ -167,15 +239,19 @@ __device__ __forceinline__ void tile_at(const LinearParams& p, int t, int& r, in
 }
 
 // E4M3: 8-bit operands.  AMN / BMN: the operand's contraction runs along its rows in memory (bf16).
-template <int TN, bool E4M3, bool AMN, bool BMN>
+// PAIR: two CTAs per tile of 256 rows.
+template <int TN, bool E4M3, bool AMN, bool BMN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_constant__ LinearParams p) {
-    using C = Cfg<TN>;
+    using C = Cfg<TN, PAIR>;
+    constexpr int kRows = PAIR ? 2 * kTileM : kTileM;   // rows of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ Small sh;
     const LinearArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kElems = E4M3 ? 128 : 64;   // contraction elements per stage
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
     if (threadIdx.x == 0) {
         if (blockIdx.x == 0 && !a.keep_status) a.ws->status = 0;   // a wait gives up after seconds, long after this
         for (int i = 0; i < C::kStages; ++i) {
@@ -184,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh.acc[i], 1);
-            ptx::mbar_init(&sh.acc_free[i], 4);
+            ptx::mbar_init(&sh.acc_free[i], PAIR ? 8 : 4);
         }
         ptx::mbar_init(&sh.done, 1);
         sh.abort = 0;
@@ -193,9 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         ptx::prefetch_tmap(&p.tm_a);
         ptx::prefetch_tmap(&p.tm_b);
     }
-    if (warp == 2) ptx::tmem_alloc(&sh.tmem_base, C::kCols);
+    if (warp == 2) tmem_alloc<PAIR>(&sh.tmem_base, C::kCols);
     ptx::tc_fence_before();
-    __syncthreads();
+    if (PAIR) cluster_sync();   // both CTAs' barriers are there
+    else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tb = sh.tmem_base;
     const int per = (p.kblocks + p.splits - 1) / p.splits;   // contraction blocks per part
@@ -205,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             // ------------------------------------------------------------ loads
             uint32_t it = 0;
             bool go = true;
-            for (int item = blockIdx.x; go && item < p.items; item += gridDim.x) {
+            for (int item = worker; go && item < p.items; item += workers) {
                 const int s = item % p.splits;
                 int r, c;
                 tile_at(p, item / p.splits, r, c);
@@ -218,25 +295,28 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                         break;
                     }
                     uint8_t* dst = sm + st * C::kStage;
-                    ptx::mbar_expect_tx(&sh.full[st], C::kStage);
+                    // a pair's loads all count on the first CTA's barrier, which expects the bytes of both
+                    const uint32_t bar = PAIR ? in_first(&sh.full[st]) : ptx::smem_u32(&sh.full[st]);
+                    if (rank == 0) ptx::mbar_expect_tx(&sh.full[st], PAIR ? 2 * C::kStage : C::kStage);
+                    const int row = r * kRows + rank * kTileM, col = c * TN + rank * C::TB;
                     if constexpr (AMN) {
 #pragma unroll
-                        for (int j = 0; j < kTileM / 64; ++j)
-                            tma_load_2d(dst + j * 8192, &p.tm_a, &sh.full[st], r * kTileM + 64 * j, kb * kElems);
+                        for (int j = 0; j < kTileM / 64; ++j) tma_load_2d<PAIR>(dst + j * 8192, &p.tm_a, bar, row + 64 * j, kb * kElems);
                     } else {
-                        tma_load_2d(dst, &p.tm_a, &sh.full[st], kb * kElems, r * kTileM);
+                        tma_load_2d<PAIR>(dst, &p.tm_a, bar, kb * kElems, row);
                     }
                     if constexpr (BMN) {
 #pragma unroll
-                        for (int j = 0; j < TN / 64; ++j)
-                            tma_load_2d(dst + C::kA + j * 8192, &p.tm_b, &sh.full[st], c * TN + 64 * j, kb * kElems);
+                        for (int j = 0; j < C::TB / 64; ++j)
+                            tma_load_2d<PAIR>(dst + C::kA + j * 8192, &p.tm_b, bar, col + 64 * j, kb * kElems);
                     } else {
-                        tma_load_2d(dst + C::kA, &p.tm_b, &sh.full[st], kb * kElems, c * TN);
+                        tma_load_2d<PAIR>(dst + C::kA, &p.tm_b, bar, kb * kElems, col);
                     }
                 }
             }
-            // every load that was issued has landed before the CTA may leave
-            for (uint32_t st = 0; st < (uint32_t)C::kStages && st < it; ++st) {
+            // every load that was issued has landed before the CTA may leave (a pair's count on the first's barriers, and
+            // the pair leaves together)
+            if (rank == 0) for (uint32_t st = 0; st < (uint32_t)C::kStages && st < it; ++st) {
                 const uint32_t last = ((it - 1 - st) / C::kStages) * C::kStages + st;
                 if (!ptx::mbar_wait(&sh.full[st], (last / C::kStages) & 1, &sh.never, kDefaultWaitIters)) {
                     record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
@@ -245,16 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ MMAs
-            constexpr uint32_t id = E4M3 ? idesc_e4m3(kTileM, TN) : ptx::idesc_bf16(kTileM, TN, AMN, BMN);
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------------------ MMAs (a pair's from its first CTA)
+            constexpr uint32_t id = E4M3 ? idesc_e4m3(kRows, TN) : ptx::idesc_bf16(kRows, TN, AMN, BMN);
             uint32_t it = 0, tile = 0;
             bool go = true;
-            for (int item = blockIdx.x; go && item < p.items; item += gridDim.x, ++tile) {
+            for (int item = worker; go && item < p.items; item += workers, ++tile) {
                 const int s = item % p.splits;
                 const int k0 = s * per, k1 = k0 + per < p.kblocks ? k0 + per : p.kblocks;
                 const uint32_t buf = tile & 1, d = tb + buf * TN;
                 if (tile >= 2 && !lin_wait(sh, a.ws, &sh.acc_free[buf], ((tile >> 1) - 1) & 1, kWhereAccFree)) break;
+                if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");   // the other CTA's warps arrive there too
                 ptx::tc_fence_after();
                 for (int kb = k0; kb < k1; ++kb, ++it) {
                     const int st = it % C::kStages;
@@ -268,21 +349,20 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                     for (int k = 0; k < 4; ++k) {   // 32 bytes of the contraction (or 16 of its rows) per MMA
                         const uint64_t da = AMN ? ptx::sdesc_sw128(sa + k * 2048, 8192, 1024) : ptx::sdesc_sw128(sa + k * 32, 16, 1024);
                         const uint64_t db = BMN ? ptx::sdesc_sw128(sb + k * 2048, 8192, 1024) : ptx::sdesc_sw128(sb + k * 32, 16, 1024);
-                        if constexpr (E4M3) mma_f8(d, da, db, id, kb > k0 || k > 0);
-                        else ptx::mma_ss(d, da, db, id, kb > k0 || k > 0);
+                        mma<E4M3, PAIR>(d, da, db, id, kb > k0 || k > 0);
                     }
-                    ptx::mma_commit(&sh.empty[st]);
+                    mma_commit<PAIR>(&sh.empty[st]);
                 }
-                ptx::mma_commit(&sh.acc[buf]);
+                mma_commit<PAIR>(&sh.acc[buf]);
             }
-            ptx::mma_commit(&sh.done);
+            mma_commit<PAIR>(&sh.done);
             if (!ptx::mbar_wait(&sh.done, 0, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3;   // the warp's quarter of tensor memory's lanes
         uint32_t tile = 0;
-        for (int item = blockIdx.x; item < p.items; item += gridDim.x, ++tile) {
+        for (int item = worker; item < p.items; item += workers, ++tile) {
             const int s = item % p.splits;
             int r, c;
             tile_at(p, item / p.splits, r, c);
@@ -293,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t d = tb + buf * TN + ((uint32_t)(32 * q) << 16);
-            const int row = r * kTileM + 32 * q + lane;   // D's row of this thread
+            const int row = r * kRows + rank * kTileM + 32 * q + lane;   // D's row of this thread
             const bool row_ok = row < (a.swap ? a.n : a.m);
             const int ncol = a.swap ? (int)a.m : a.n;
             const float xs = (a.x_scales && !a.swap && row_ok) ? __ldg(a.x_scales + row) : 1.f;
@@ -307,7 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                 if (j + CW >= TN) {   // the accumulator is in registers: the next tile may have it
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&sh.acc_free[buf]);
+                    if (lane == 0) {
+                        if (PAIR)
+                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(&sh.acc_free[buf])) : "memory");
+                        else
+                            ptx::mbar_arrive(&sh.acc_free[buf]);
+                    }
                 }
                 const int col = c * TN + j;
                 if (!row_ok || col >= ncol) continue;
@@ -341,10 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         }
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    if (PAIR) cluster_sync();   // neither CTA leaves while the other may still use its memory or barriers
+    else __syncthreads();
     if (warp == 2) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tb, C::kCols);
+        tmem_dealloc<PAIR>(tb, C::kCols);
     }
 }
 
@@ -436,68 +522,95 @@ bool encode_2d(CUtensorMap* tm, const void* base, int dtype, int64_t inner, int6
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN, bool E4M3, bool AMN, bool BMN>
-cudaError_t launch_tile(const LinearParams& p, int grid, cudaStream_t st) {
-    constexpr size_t smem = Cfg<TN>::kSmem;
-    const auto kern = ssd_linear_tc<TN, E4M3, AMN, BMN>;
-    static std::atomic<uint8_t> ready[kMaxDevices];
+template <int TN, bool E4M3, bool AMN, bool BMN, bool PAIR>
+cudaError_t launch_tile(const LinearParams& p, cudaStream_t st) {
+    constexpr size_t smem = Cfg<TN, PAIR>::kSmem;
+    const auto kern = ssd_linear_tc<TN, E4M3, AMN, BMN, PAIR>;
+    // once per device and kernel: the shared-memory opt-in, and the CTAs (pairs) that run at once
+    static std::atomic<int> workers[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!ready[dev].load(std::memory_order_acquire)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    int most = workers[dev].load(std::memory_order_acquire);
+    if (most == 0) {
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-        ready[dev].store(1, std::memory_order_release);
+        most = device_sms();
+        if (PAIR) {
+            cfg.gridDim = dim3(most > 1 ? most / 2 * 2 : 2);
+            if ((e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg)) != cudaSuccess) return e;
+        }
+        if (most < 1) return cudaErrorInvalidConfiguration;
+        workers[dev].store(most, std::memory_order_release);
     }
-    kern<<<(unsigned)grid, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    const int n = p.items < most ? p.items : most;
+    cfg.gridDim = dim3(PAIR ? 2 * n : n);
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <bool E4M3, bool AMN, bool BMN>
-cudaError_t launch_kind(const LinearParams& p, int tile_n, int grid, cudaStream_t st) {
-    if (tile_n == 256) return launch_tile<256, E4M3, AMN, BMN>(p, grid, st);
-    if (tile_n == 128) return launch_tile<128, E4M3, AMN, BMN>(p, grid, st);
+cudaError_t launch_kind(const LinearParams& p, const LinearPlan& plan, cudaStream_t st) {
+    const int tn = plan.tile_n;
+    if (plan.pair) return tn == 256 ? launch_tile<256, E4M3, AMN, BMN, true>(p, st) : launch_tile<128, E4M3, AMN, BMN, true>(p, st);
+    if (tn == 256) return launch_tile<256, E4M3, AMN, BMN, false>(p, st);
+    if (tn == 128) return launch_tile<128, E4M3, AMN, BMN, false>(p, st);
     if constexpr (!AMN && !BMN) {
-        if (tile_n == 32) return launch_tile<32, E4M3, AMN, BMN>(p, grid, st);
-        if (tile_n == 16) return launch_tile<16, E4M3, AMN, BMN>(p, grid, st);
+        if (tn == 32) return launch_tile<32, E4M3, AMN, BMN, false>(p, st);
+        if (tn == 16) return launch_tile<16, E4M3, AMN, BMN, false>(p, st);
     }
-    return launch_tile<64, E4M3, AMN, BMN>(p, grid, st);
+    return launch_tile<64, E4M3, AMN, BMN, false>(p, st);
 }
 
 }  // namespace
 
 // How a product of `rows` x `cols` results over a contraction of `kbytes` bytes runs.  Up to kLinearSwap
-// rows it is computed transposed.  Otherwise the tile width and the number of parts minimise a
-// count of tensor-core cycles: waves of tiles, each its blocks' MMAs (a 128-byte block
-// takes 2 cycles per column of the tile, but no fewer than reading both operands from shared memory at
-// 128 bytes a cycle) and a fixed start; parts add the join's launch and its traffic.
-LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
+// rows it is computed transposed.  Otherwise the tile (128 rows by one CTA or 256 by a pair, 64 to 256 columns)
+// and the number of parts minimise a count of cycles: waves of tiles, each its 128-byte blocks and a fixed start.
+// A block takes the longer of its MMAs (2 cycles per column of bf16 operands, 1 of e4m3; a pair's two SMs work on
+// twice the rows) and of its operands' way from L2, about 60 bytes per SM and cycle; parts add the join's launch and its traffic.
+LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool e4m3, bool may_swap) {
     LinearPlan best = {};
     const int64_t kblocks = (kbytes + kRowB - 1) / kRowB;
     const bool swap = may_swap && rows <= kLinearSwap;
     const int64_t dr = swap ? cols : rows, dc = swap ? rows : cols;
     double least = 0;
     const int widths[] = {256, 128, 64, 32, 16};
-    for (int tn : widths) {
-        if (swap ? (tn > kLinearSwap || (tn < dc && tn < kLinearSwap) || (tn > 16 && tn / 2 >= dc)) : tn < 64) continue;
-        const int64_t tiles = ((dr + kTileM - 1) / kTileM) * ((dc + tn - 1) / tn);
-        const double block = 2.0 * tn > tn + 128 ? 2.0 * tn : tn + 128;
-        for (int s = 1; s <= kLinearMaxSplits; ++s) {
-            const int64_t per = (kblocks + s - 1) / s;
-            if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;   // every part has blocks
-            const int64_t waves = (tiles * s + kLinearSMs - 1) / kLinearSMs;
-            double cost = (double)waves * (per * block + 600) + 2.0 * tn;
-            if (s > 1) cost += 5000 + (double)rows * cols * 8 * s / 3500;   // about 3500 bytes of HBM a cycle
-            if (least == 0 || cost < least) {
-                least = cost;
-                best.tile_n = tn;
-                best.splits = s;
-                best.swap = swap;
-                best.parts_bytes = s > 1 ? (size_t)rows * cols * 4 * s : 0;
+    for (int pair = 1; pair >= 0; --pair)
+        for (int tn : widths) {
+            if (pair && (swap || tn < 128)) continue;
+            if (swap ? (tn > kLinearSwap || (tn < dc && tn < kLinearSwap) || (tn > 16 && tn / 2 >= dc)) : tn < 64) continue;
+            const int64_t tm = pair ? 2 * kTileM : kTileM;
+            const int64_t tiles = ((dr + tm - 1) / tm) * ((dc + tn - 1) / tn), workers = pair ? kLinearSMs / 2 : kLinearSMs;
+            const double mma = (e4m3 ? 1.0 : 2.0) * tn, fill = (128 + (pair ? tn / 2 : tn)) * 128 / 60.0;
+            const double block = mma > fill ? mma : fill;
+            for (int s = 1; s <= kLinearMaxSplits; ++s) {
+                const int64_t per = (kblocks + s - 1) / s;
+                if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;   // every part has blocks
+                const int64_t waves = (tiles * s + workers - 1) / workers;
+                double cost = (double)waves * (per * block + 600) + 2.0 * tn;
+                if (s > 1) cost += 5000 + (double)rows * cols * 8 * s / 3500;   // about 3500 bytes of HBM a cycle
+                if (least == 0 || cost < least) {
+                    least = cost;
+                    best.tile_n = tn;
+                    best.splits = s;
+                    best.swap = swap;
+                    best.pair = pair != 0;
+                    best.parts_bytes = s > 1 ? (size_t)rows * cols * 4 * s : 0;
+                }
+                if (tiles * s >= 4 * workers) break;
             }
-            if (tiles * s >= 4 * kLinearSMs) break;
         }
-    }
     return best;
 }
 
@@ -510,7 +623,8 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     a.vec = a.n % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0 && ((uintptr_t)a.pre & 15) == 0;
     const int64_t dr = a.swap ? a.n : a.m, dc = a.swap ? a.m : a.n;
     const int tn = plan.tile_n, es = a.dtype == SSD_E4M3 ? 1 : 2;
-    p.tiles_r = (int)((dr + kTileM - 1) / kTileM);
+    const int tm = plan.pair ? 2 * kTileM : kTileM, tb = plan.pair ? tn / 2 : tn;
+    p.tiles_r = (int)((dr + tm - 1) / tm);
     p.tiles_c = (int)((dc + tn - 1) / tn);
     p.kblocks = (int)((a.k * es + kRowB - 1) / kRowB);
     p.splits = plan.splits;
@@ -522,15 +636,13 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     const bool ea = oa.along_rows ? encode_2d(&p.tm_a, oa.p, a.dtype, dr, a.k, oa.ld, 64)
                                   : encode_2d(&p.tm_a, oa.p, a.dtype, a.k, dr, oa.ld, kTileM);
     const bool eb = ob.along_rows ? encode_2d(&p.tm_b, ob.p, a.dtype, dc, a.k, ob.ld, 64)
-                                  : encode_2d(&p.tm_b, ob.p, a.dtype, a.k, dc, ob.ld, tn);
+                                  : encode_2d(&p.tm_b, ob.p, a.dtype, a.k, dc, ob.ld, tb);
     if (!ea || !eb) return cudaErrorInvalidValue;
-    const int nsm = device_sms();
-    const int grid = p.items < nsm || nsm <= 0 ? p.items : nsm;
     cudaError_t e;
-    if (a.dtype == SSD_E4M3) e = launch_kind<true, false, false>(p, tn, grid, st);
-    else if (oa.along_rows) e = launch_kind<false, true, true>(p, tn, grid, st);
-    else if (ob.along_rows) e = launch_kind<false, false, true>(p, tn, grid, st);
-    else e = launch_kind<false, false, false>(p, tn, grid, st);
+    if (a.dtype == SSD_E4M3) e = launch_kind<true, false, false>(p, plan, st);
+    else if (oa.along_rows) e = launch_kind<false, true, true>(p, plan, st);
+    else if (ob.along_rows) e = launch_kind<false, false, true>(p, plan, st);
+    else e = launch_kind<false, false, false>(p, plan, st);
     if (e != cudaSuccess || p.splits == 1) return e;
     const size_t total = (size_t)a.m * a.n;
     ssd_linear_join<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a, p.splits);
