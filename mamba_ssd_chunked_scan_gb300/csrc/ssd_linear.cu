@@ -6,8 +6,9 @@
 //   ssd_linear_dbias    dbias from the shares, in a fixed order
 //
 // One persistent CTA per SM walks tiles (or tiles' parts along the contraction): one thread loads
-// 128-byte-wide operand tiles by TMA into a ring of stages, one issues the MMAs, four warps run the
-// epilogue of the previous tile from the other half of tensor memory meanwhile.  Where there are enough
+// 128-byte-wide operand tiles by TMA into a ring of stages, one issues the MMAs, eight warps run the
+// epilogue of the previous tile from the other half of tensor memory meanwhile.  A thread holds one row of 32 columns
+// there; blocks of 32 rows x 64 bytes go through shared memory, so that memory sees whole sectors.  Where there are enough
 // tiles, two SMs of a cluster share one of 256 rows (PAIR): each holds the accumulator of its 128 rows and loads
 // its rows of A and half of B's, and the first one issues the MMAs of both.  Operands come from L2, and a pair asks
 // for 64 bytes per SM and cycle of bf16 MMAs where a single CTA asks for 96, more than L2 gives.
@@ -33,7 +34,8 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256;          // warp 0 loads, 1 MMAs, 2 tensor memory, 4-7 epilogue
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (4 + kEpiWarps);   // warp 0 loads, 1 MMAs, 2 tensor memory, 4-11 epilogue
 constexpr int kRowB = 128;             // bytes of the contraction per tile row and stage
 constexpr int kTileM = 128;
 constexpr uint32_t kWhereEmpty = 61, kWhereFull = 62, kWhereAccFree = 63, kWhereAcc = 64, kWhereDrain = 65;
@@ -45,7 +47,9 @@ struct Cfg {
     static constexpr uint32_t kA = kTileM * kRowB, kB = TB * kRowB, kStage = kA + kB;
     static constexpr int kStages = TB >= 256 ? 4 : TB >= 128 ? 6 : TB >= 64 ? 8 : TB >= 32 ? 9 : 10;
     static constexpr uint32_t kCols = 2 * TN < 32 ? 32 : 2 * TN;   // two accumulators
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage;
+    static constexpr uint32_t kBlocks = kStages * kStage;                  // the epilogue warps' 32 x 64-byte blocks
+    static constexpr uint32_t kVec = kBlocks + kEpiWarps * 2048;           // bias and w_scales of two tiles' columns
+    static constexpr size_t kSmem = 1024 + (size_t)kVec + 2 * 2 * TN * 4;
 };
 
 struct LinearParams {
@@ -187,44 +191,133 @@ __device__ __forceinline__ float act_slope(float v, int act) {
     return 1.f;
 }
 
-// One element of y from its sum: scales, bias, activation, residual.
-__device__ __forceinline__ void finish(const LinearArgs& a, float v, int64_t m, int n) {
-    if (a.x_scales) v *= __ldg(a.x_scales + m) * __ldg(a.w_scales + n);
-    if (a.bias) v += __ldg(a.bias + n);
-    const size_t at = (size_t)m * a.n + n;
+// One element of y from v, its sum with scales and bias: the rounded v for the backward pass, activation, residual.
+__device__ __forceinline__ void finish(const LinearArgs& a, float v, size_t at) {
     if (a.pre) static_cast<bf16_t*>(a.pre)[at] = __float2bfloat16_rn(v);
     v = act_value(v, a.act);
     if (a.residual) v += __bfloat162float(static_cast<const bf16_t*>(a.residual)[at]);
     static_cast<bf16_t*>(a.y)[at] = __float2bfloat16_rn(v);
 }
 
-// Eight consecutive columns of one row (16-byte aligned rows of y).
-__device__ __forceinline__ void finish8(const LinearArgs& a, float (&v)[8], int64_t m, int n, float xs) {
+// 32 rows of 64 bytes through shared memory, by a warp: lane r has row r as four 16-byte words, and they leave as whole
+// rows (four lanes each).  The words of a row are permuted so that neither side's accesses share a bank.
+__device__ __forceinline__ uint8_t* word_at(uint8_t* block, int row, int word) {
+    return block + row * 64 + ((word ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void put_block(uint8_t* block, const uint4 (&w)[4]) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();   // the last block has left
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(word_at(block, lane, k)) = w[k];
+    __syncwarp();
+}
+// The block to memory: row r to base + r * pitch bytes, for r < rows.  `bytes` of each row exist (ELEM of them per
+// element); VEC: whole 16-byte words, aligned.
+template <int ELEM>
+__device__ __forceinline__ void send_block(const uint8_t* block, uint8_t* base, size_t pitch, int rows, int bytes, bool vec) {
+    const int lane = threadIdx.x & 31;
+    uint8_t* const blk = const_cast<uint8_t*>(block);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2), word = lane & 3;
+            const uint4 v = *reinterpret_cast<const uint4*>(word_at(blk, row, word));
+            if (row < rows && 16 * word < bytes) *reinterpret_cast<uint4*>(base + row * pitch + 16 * word) = v;
+        }
+    } else {
+        // one row at a time, an element per lane
+        for (int row = 0; row < rows; ++row)
+            if (lane * ELEM < 64 && lane * ELEM < bytes) {
+                const uint8_t* from = word_at(blk, row, (lane * ELEM) >> 4) + ((lane * ELEM) & 15);
+                if constexpr (ELEM == 2) *reinterpret_cast<uint16_t*>(base + row * pitch + 2 * lane) = *reinterpret_cast<const uint16_t*>(from);
+                else *reinterpret_cast<uint32_t*>(base + row * pitch + 4 * lane) = *reinterpret_cast<const uint32_t*>(from);
+            }
+    }
+}
+
+// 32 columns (one row per lane) of a tile from their sums `w`: D's rows `row` to `row` + 31, columns col on.
+// `vec`: this chunk's scales (then bias) by column, in shared memory, TN apart; xs: the row's scale.
+__device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t (&w)[32], int64_t row, int col, float xs,
+                                            const float* ws, const float* bias, uint8_t* block) {
+    const int lane = threadIdx.x & 31;
+    const int rows = a.m - row < 32 ? (int)(a.m - row) : 32, cols = a.n - col < 32 ? a.n - col : 32;
+    const size_t at = (size_t)row * a.n + col;
+    uint4 r[4];
+    if (a.residual) {
+        const bf16_t* res = static_cast<const bf16_t*>(a.residual);
+        if (a.vec) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                r[k] = make_uint4(0, 0, 0, 0);
+                if (lane < rows && 8 * k < cols) r[k] = __ldcs(reinterpret_cast<const uint4*>(res + at + (size_t)lane * a.n + 8 * k));
+            }
+        } else {   // row by row through the block
+            __syncwarp();
+            for (int i = 0; i < rows; ++i)
+                if (lane < cols) *reinterpret_cast<bf16_t*>(word_at(block, i, lane >> 3) + 2 * (lane & 7)) = res[at + (size_t)i * a.n + lane];
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const uint4*>(word_at(block, lane, k));
+        }
+    }
+    float v[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(w[k]);
     if (a.x_scales) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= xs * __ldg(a.w_scales + n + k);
+        for (int k = 0; k < 32; k += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(ws + k);
+            v[k] *= xs * q.x;
+            v[k + 1] *= xs * q.y;
+            v[k + 2] *= xs * q.z;
+            v[k + 3] *= xs * q.w;
+        }
     }
     if (a.bias) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += __ldg(a.bias + n + k);
+        for (int k = 0; k < 32; k += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(bias + k);
+            v[k] += q.x;
+            v[k + 1] += q.y;
+            v[k + 2] += q.z;
+            v[k + 3] += q.w;
+        }
     }
-    const size_t at = (size_t)m * a.n + n;
-    Raw<bf16_t, 8> q;
+    auto pack = [&](uint4 (&o)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t* q = reinterpret_cast<uint32_t*>(&o[k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]);
+                q[e] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+    };
+    uint4 o[4];
     if (a.pre) {
-        q.set(v);
-        *reinterpret_cast<uint4*>(static_cast<bf16_t*>(a.pre) + at) = q.w;
+        pack(o);
+        put_block(block, o);
+        send_block<2>(block, static_cast<uint8_t*>(a.pre) + at * 2, (size_t)a.n * 2, rows, cols * 2, a.vec);
     }
+    if (a.act != SSD_ACT_NONE) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], a.act);
+        for (int k = 0; k < 32; ++k) v[k] = act_value(v[k], a.act);
+    }
     if (a.residual) {
-        float r[8];
-        q.load(static_cast<const bf16_t*>(a.residual) + at);
-        q.get(r);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += r[k];
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(&r[k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[8 * k + 2 * e] += __uint_as_float(q[e] << 16);
+                v[8 * k + 2 * e + 1] += __uint_as_float(q[e] & 0xFFFF0000u);
+            }
+        }
     }
-    q.set(v);
-    *reinterpret_cast<uint4*>(static_cast<bf16_t*>(a.y) + at) = q.w;
+    pack(o);
+    put_block(block, o);
+    send_block<2>(block, static_cast<uint8_t*>(a.y) + at * 2, (size_t)a.n * 2, rows, cols * 2, a.vec);
 }
 
 // Tile (r, c) of the t-th tile: bands of kBand row tiles walk the columns together, so that the tiles in
@@ -260,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh.acc[i], 1);
-            ptx::mbar_init(&sh.acc_free[i], PAIR ? 8 : 4);
+            ptx::mbar_init(&sh.acc_free[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
         }
         ptx::mbar_init(&sh.done, 1);
         sh.abort = 0;
@@ -360,67 +453,98 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue
-        const int q = warp & 3;   // the warp's quarter of tensor memory's lanes
+        const int q = warp & 3;                 // the warp's quarter of tensor memory's lanes
+        const int half = (warp - 4) >> 2;       // and half of the columns (all of them in tiles below 64)
+        constexpr int kSpan = TN >= 64 ? TN / 2 : TN;
+        uint8_t* block = sm + C::kBlocks + (warp - 4) * 2048;
         uint32_t tile = 0;
         for (int item = worker; item < p.items; item += workers, ++tile) {
             const int s = item % p.splits;
             int r, c;
             tile_at(p, item / p.splits, r, c);
             const uint32_t buf = tile & 1;
+            const bool whole = p.splits == 1 && !a.swap;   // rows of y leave from here
+            float* vec = reinterpret_cast<float*>(sm + C::kVec) + buf * 2 * TN;
+            if (whole && (a.bias || a.x_scales)) {
+                // the columns' scales and bias, once per tile, while its MMAs run; the other tile's are still in use
+                for (int k = threadIdx.x - 128; k < TN; k += 32 * kEpiWarps) {
+                    const int n = c * TN + k;
+                    vec[k] = a.x_scales && n < a.n ? __ldg(a.w_scales + n) : 0.f;
+                    vec[TN + k] = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
+                }
+                ptx::named_bar(1, 32 * kEpiWarps);
+            }
+            const int row0 = r * kRows + rank * kTileM + 32 * q, row = row0 + lane;   // D's row of this thread
+            const int nrow = a.swap ? a.n : (int)a.m, ncol = a.swap ? (int)a.m : a.n;
+            const bool row_ok = row < nrow;
+            // the row's scale and bias (transposed: of the row of w)
+            const float rs = a.x_scales && row_ok ? __ldg((a.swap ? a.w_scales : a.x_scales) + row) : 1.f;
+            const float rb = a.swap && a.bias && row_ok ? __ldg(a.bias + row) : 0.f;
             bool ok = true;
             if (lane == 0) ok = lin_wait(sh, a.ws, &sh.acc[buf], (tile >> 1) & 1, kWhereAcc);
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            // a wait that runs out stops all of the warps, which share the barrier above
+            if (whole && (a.bias || a.x_scales)) ok = !ptx::named_bar_any(2, 32 * kEpiWarps, !ok);
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t d = tb + buf * TN + ((uint32_t)(32 * q) << 16);
-            const int row = r * kRows + rank * kTileM + 32 * q + lane;   // D's row of this thread
-            const bool row_ok = row < (a.swap ? a.n : a.m);
-            const int ncol = a.swap ? (int)a.m : a.n;
-            const float xs = (a.x_scales && !a.swap && row_ok) ? __ldg(a.x_scales + row) : 1.f;
+            const uint32_t d = tb + buf * TN + ((uint32_t)(32 * q) << 16) + (TN >= 64 ? half * kSpan : 0);
             constexpr int CW = TN < 32 ? TN : 32;   // columns per read of tensor memory
+            const bool idle = TN < 64 && half;
 #pragma unroll 1
-            for (int j = 0; j < TN; j += CW) {
-                __syncwarp();   // lanes past the last row or column skip the stores, not the load
+            for (int j = 0; j < kSpan; j += CW) {
+                __syncwarp();
                 uint32_t w[CW];
-                if constexpr (CW == 32) ptx::tmem_load32(d + j, w);
-                else ptx::tmem_load16(d + j, w);
-                if (j + CW >= TN) {   // the accumulator is in registers: the next tile may have it
+                if (!idle) {
+                    if constexpr (CW == 32) ptx::tmem_load32(d + j, w);
+                    else ptx::tmem_load16(d + j, w);
+                }
+                if (j + CW >= kSpan) {   // the accumulator is in registers: the next tile may have it
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
                         if (PAIR)
-                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(&sh.acc_free[buf])) : "memory");
+                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(&sh.acc_free[buf]))
+                                         : "memory");
                         else
                             ptx::mbar_arrive(&sh.acc_free[buf]);
                     }
                 }
-                const int col = c * TN + j;
-                if (!row_ok || col >= ncol) continue;
-                if (p.splits > 1) {
-                    float* part = a.parts + (size_t)s * a.m * a.n;
+                const int col = c * TN + (TN >= 64 ? half * kSpan : 0) + j;
+                if (idle || row0 >= nrow || col >= ncol) continue;   // the same for the whole warp
+                if (a.swap) {
+                    // a lane per column of y: 32 of them lie together in a row
+                    if (row_ok) {
+                        float* part = a.parts + (size_t)s * a.m * a.n + row;
 #pragma unroll
-                    for (int k = 0; k < CW; ++k)
-                        if (col + k < ncol) {
-                            if (a.swap) part[(size_t)(col + k) * a.n + row] = __uint_as_float(w[k]);
-                            else part[(size_t)row * a.n + col + k] = __uint_as_float(w[k]);
-                        }
-                } else if (a.swap) {
-#pragma unroll
-                    for (int k = 0; k < CW; ++k)
-                        if (col + k < ncol) finish(a, __uint_as_float(w[k]), col + k, row);
-                } else if (a.vec) {
-#pragma unroll
-                    for (int k = 0; k < CW; k += 8) {
-                        if (col + k >= ncol) break;   // whole vectors: n is a multiple of 8
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[k + e]);
-                        finish8(a, v, row, col + k, xs);
+                        for (int k = 0; k < CW; ++k)
+                            if (col + k < ncol) {
+                                float v = __uint_as_float(w[k]);
+                                if (p.splits > 1) {
+                                    part[(size_t)(col + k) * a.n] = v;
+                                } else {
+                                    if (a.x_scales) v *= rs * __ldg(a.x_scales + col + k);
+                                    finish(a, v + rb, (size_t)(col + k) * a.n + row);
+                                }
+                            }
                     }
-                } else {
+                } else if constexpr (CW == 32) {
+                    if (p.splits > 1) {
+                        float* part = a.parts + ((size_t)s * a.m + row0) * a.n + col;
+                        const int rows = nrow - row0 < 32 ? nrow - row0 : 32;
 #pragma unroll
-                    for (int k = 0; k < CW; ++k)
-                        if (col + k < ncol) finish(a, __uint_as_float(w[k]), row, col + k);
+                        for (int k = 0; k < 32; k += 16) {
+                            uint4 o[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[e] = make_uint4(w[k + 4 * e], w[k + 4 * e + 1], w[k + 4 * e + 2], w[k + 4 * e + 3]);
+                            const int left = (ncol - col - k) * 4;
+                            if (left <= 0) break;
+                            put_block(block, o);
+                            send_block<4>(block, reinterpret_cast<uint8_t*>(part + k), (size_t)a.n * 4, rows, left < 64 ? left : 64, a.n % 4 == 0);
+                        }
+                    } else {
+                        const int k = TN >= 64 ? half * kSpan + j : j;
+                        finish_rows(a, w, row0, col, rs, vec + k, vec + TN + k, block);
+                    }
                 }
             }
         }
@@ -434,15 +558,47 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     }
 }
 
-// y from the parts of a split contraction, added in their order.
+// y from the parts of a split contraction, added in their order.  V elements of a row per thread.
+template <int V>
 __global__ void __launch_bounds__(256) ssd_linear_join(LinearArgs a, int splits) {
     const size_t total = (size_t)a.m * a.n;
-    const size_t k = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t k = ((size_t)blockIdx.x * 256 + threadIdx.x) * V;
     if (k >= total) return;
-    float v = a.parts[k];
-    for (int s = 1; s < splits; ++s) v += a.parts[(size_t)s * total + k];
-    const int64_t m = (int64_t)(k / a.n);
-    finish(a, v, m, (int)(k - (size_t)m * a.n));
+    float v[V];
+    for (int s = 0; s < splits; ++s) {
+        Raw<float, V> q;
+        q.load(a.parts + (size_t)s * total + k);
+        float u[V];
+        q.get(u);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = s ? v[e] + u[e] : u[e];
+    }
+    const int64_t m = (int64_t)(k / (unsigned)a.n);
+    const int n = (int)(k - (size_t)m * a.n);
+    const float xs = a.x_scales ? __ldg(a.x_scales + m) : 1.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (a.x_scales) v[e] *= xs * __ldg(a.w_scales + n + e);
+        if (a.bias) v[e] += __ldg(a.bias + n + e);
+    }
+    Raw<bf16_t, V> o;
+    if (a.pre) {
+        o.set(v);
+        o.store(static_cast<bf16_t*>(a.pre) + k);
+    }
+    if (a.residual) {
+        float r[V];
+        Raw<bf16_t, V> q;
+        q.load(static_cast<const bf16_t*>(a.residual) + k);
+        q.get(r);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = act_value(v[e], a.act) + r[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = act_value(v[e], a.act);
+    }
+    o.set(v);
+    o.store(static_cast<bf16_t*>(a.y) + k);
 }
 
 // dpre = dy act'(pre), rounded to bf16 into rows of ldp elements, and each row slab's sums over its
@@ -645,7 +801,8 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     else e = launch_kind<false, false, false>(p, plan, st);
     if (e != cudaSuccess || p.splits == 1) return e;
     const size_t total = (size_t)a.m * a.n;
-    ssd_linear_join<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a, p.splits);
+    if (a.vec) ssd_linear_join<4><<<(unsigned)((total / 4 + 255) / 256), 256, 0, st>>>(a, p.splits);
+    else ssd_linear_join<1><<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a, p.splits);
     return cudaGetLastError();
 }
 
