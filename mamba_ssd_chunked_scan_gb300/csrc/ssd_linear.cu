@@ -153,6 +153,38 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// One lane of the (whole) warp, the same each time.  The loading and the MMA warp run their loops with all lanes and
+// only let this one issue: addresses and descriptors then stay in uniform registers, where the instructions want
+// them (from a branch that one lane took, each had to be moved there, about 500 cycles per block of four MMAs).
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+// The same on a barrier where the cluster's other CTA arrives too.  (An acquire of the wait's own: a fence after it
+// held the MMAs up for 1600 cycles per tile.)
+__device__ __forceinline__ bool cluster_wait(Small& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 0; it < kDefaultWaitIters; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(ptx::smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((it & 63) == 63 && (*(volatile int*)&sh.abort || ptx::globaltimer() - t0 > ptx::kWaitLimitNs)) break;
+    }
+    if (!*(volatile int*)&sh.abort) {
+        record_error(ws, SSD_ERR_TIMEOUT, where);
+        *(volatile int*)&sh.abort = 1;
+    }
+    return false;
+}
+// A wait by a whole warp, whose lanes go on or give up together.
+__device__ __forceinline__ bool warp_wait(Small& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
+    return __all_sync(0xffffffffu, lin_wait(sh, ws, bar, parity, where));
+}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -371,27 +403,25 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     const int per = (p.kblocks + p.splits - 1) / p.splits;   // contraction blocks per part
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ loads
-            uint32_t it = 0;
-            bool go = true;
-            for (int item = worker; go && item < p.items; item += workers) {
-                const int s = item % p.splits;
-                int r, c;
-                tile_at(p, item / p.splits, r, c);
-                const int k1 = (s + 1) * per < p.kblocks ? (s + 1) * per : p.kblocks;
-                for (int kb = s * per; kb < k1; ++kb, ++it) {
-                    const int st = it % C::kStages;
-                    if (it >= (uint32_t)C::kStages &&
-                        !lin_wait(sh, a.ws, &sh.empty[st], ((it / C::kStages) - 1) & 1, kWhereEmpty)) {
-                        go = false;
-                        break;
-                    }
-                    uint8_t* dst = sm + st * C::kStage;
-                    // a pair's loads all count on the first CTA's barrier, which expects the bytes of both
-                    const uint32_t bar = PAIR ? in_first(&sh.full[st]) : ptx::smem_u32(&sh.full[st]);
+        // ---------------------------------------------------------------- loads
+        uint32_t it = 0, st = 0, phase = 0;
+        bool go = true;
+        for (int item = worker; go && item < p.items; item += workers) {
+            const int s = item % p.splits;
+            int r, c;
+            tile_at(p, item / p.splits, r, c);
+            const int k1 = (s + 1) * per < p.kblocks ? (s + 1) * per : p.kblocks;
+            const int row = r * kRows + rank * kTileM, col = c * TN + rank * C::TB;
+            for (int kb = s * per; kb < k1; ++kb) {
+                if (it >= (uint32_t)C::kStages && !warp_wait(sh, a.ws, &sh.empty[st], phase ^ 1, kWhereEmpty)) {
+                    go = false;
+                    break;
+                }
+                uint8_t* dst = sm + st * C::kStage;
+                // a pair's loads all count on the first CTA's barrier, which expects the bytes of both
+                const uint32_t bar = PAIR ? in_first(&sh.full[st]) : ptx::smem_u32(&sh.full[st]);
+                if (elected()) {
                     if (rank == 0) ptx::mbar_expect_tx(&sh.full[st], PAIR ? 2 * C::kStage : C::kStage);
-                    const int row = r * kRows + rank * kTileM, col = c * TN + rank * C::TB;
                     if constexpr (AMN) {
 #pragma unroll
                         for (int j = 0; j < kTileM / 64; ++j) tma_load_2d<PAIR>(dst + j * 8192, &p.tm_a, bar, row + 64 * j, kb * kElems);
@@ -406,49 +436,70 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                         tma_load_2d<PAIR>(dst + C::kA, &p.tm_b, bar, kb * kElems, col);
                     }
                 }
+                __syncwarp();
+                ++it;
+                if (++st == (uint32_t)C::kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
-            // every load that was issued has landed before the CTA may leave (a pair's count on the first's barriers, and
-            // the pair leaves together)
-            if (rank == 0) for (uint32_t st = 0; st < (uint32_t)C::kStages && st < it; ++st) {
-                const uint32_t last = ((it - 1 - st) / C::kStages) * C::kStages + st;
-                if (!ptx::mbar_wait(&sh.full[st], (last / C::kStages) & 1, &sh.never, kDefaultWaitIters)) {
+        }
+        // every load that was issued has landed before the CTA may leave (a pair's count on the first's barriers, and
+        // the pair leaves together)
+        if (rank == 0 && lane == 0)
+            for (uint32_t i = 0; i < (uint32_t)C::kStages && i < it; ++i) {
+                const uint32_t last = ((it - 1 - i) / C::kStages) * C::kStages + i;
+                if (!ptx::mbar_wait(&sh.full[i], (last / C::kStages) & 1, &sh.never, kDefaultWaitIters)) {
                     record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
                     *(volatile int*)&sh.abort = 1;
                 }
             }
-        }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ------------------------------------------------------------ MMAs (a pair's from its first CTA)
             constexpr uint32_t id = E4M3 ? idesc_e4m3(kRows, TN) : ptx::idesc_bf16(kRows, TN, AMN, BMN);
-            uint32_t it = 0, tile = 0;
+            // the first stage's descriptors; a stage, and 32 bytes of the contraction (or 16 of its rows), further on
+            // is an addition in their address field
+            const uint32_t base = ptx::smem_u32(sm);
+            const uint64_t da0 = AMN ? ptx::sdesc_sw128(base, 8192, 1024) : ptx::sdesc_sw128(base, 16, 1024);
+            const uint64_t db0 = BMN ? ptx::sdesc_sw128(base + C::kA, 8192, 1024) : ptx::sdesc_sw128(base + C::kA, 16, 1024);
+            constexpr uint32_t ka = (AMN ? 2048 : 32) >> 4, kb_ = (BMN ? 2048 : 32) >> 4;
+            uint32_t tile = 0, st = 0, phase = 0;
             bool go = true;
             for (int item = worker; go && item < p.items; item += workers, ++tile) {
                 const int s = item % p.splits;
                 const int k0 = s * per, k1 = k0 + per < p.kblocks ? k0 + per : p.kblocks;
                 const uint32_t buf = tile & 1, d = tb + buf * TN;
-                if (tile >= 2 && !lin_wait(sh, a.ws, &sh.acc_free[buf], ((tile >> 1) - 1) & 1, kWhereAccFree)) break;
-                if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");   // the other CTA's warps arrive there too
+                if (tile >= 2) {
+                    const uint32_t parity = ((tile >> 1) - 1) & 1;
+                    if (PAIR ? !__all_sync(0xffffffffu, cluster_wait(sh, a.ws, &sh.acc_free[buf], parity, kWhereAccFree))
+                             : !warp_wait(sh, a.ws, &sh.acc_free[buf], parity, kWhereAccFree))
+                        break;
+                }
                 ptx::tc_fence_after();
-                for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int st = it % C::kStages;
-                    if (!lin_wait(sh, a.ws, &sh.full[st], (it / C::kStages) & 1, kWhereFull)) {
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!warp_wait(sh, a.ws, &sh.full[st], phase, kWhereFull)) {
                         go = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t sa = ptx::smem_u32(sm + st * C::kStage), sb = sa + C::kA;
+                    const uint64_t da = da0 + st * (C::kStage >> 4), db = db0 + st * (C::kStage >> 4);
+                    if (elected()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {   // 32 bytes of the contraction (or 16 of its rows) per MMA
-                        const uint64_t da = AMN ? ptx::sdesc_sw128(sa + k * 2048, 8192, 1024) : ptx::sdesc_sw128(sa + k * 32, 16, 1024);
-                        const uint64_t db = BMN ? ptx::sdesc_sw128(sb + k * 2048, 8192, 1024) : ptx::sdesc_sw128(sb + k * 32, 16, 1024);
-                        mma<E4M3, PAIR>(d, da, db, id, kb > k0 || k > 0);
+                        for (int k = 0; k < 4; ++k) mma<E4M3, PAIR>(d, da + k * ka, db + k * kb_, id, kb > k0 || k > 0);
+                        mma_commit<PAIR>(&sh.empty[st]);
                     }
-                    mma_commit<PAIR>(&sh.empty[st]);
+                    __syncwarp();
+                    if (++st == (uint32_t)C::kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
-                mma_commit<PAIR>(&sh.acc[buf]);
+                if (elected()) mma_commit<PAIR>(&sh.acc[buf]);
+                __syncwarp();
             }
-            mma_commit<PAIR>(&sh.done);
+            if (elected()) mma_commit<PAIR>(&sh.done);
+            __syncwarp();
             if (!ptx::mbar_wait(&sh.done, 0, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
         }
     } else if (warp >= 4) {
