@@ -241,13 +241,15 @@ struct LinearArgs {
     const void* residual;  // (m, n) bf16, or NULL
     void* y;               // (m, n) bf16
     void* pre;             // (m, n) bf16, or NULL
-    float* parts;          // [splits * m * n]
+    float* parts;          // per part, a tile of fp32 sums
     WsHeader* ws;
     int keep_status;       // the status word was cleared by the call already
     int swap, vec;         // set at the launch
 };
 struct LinearPlan {
-    int tile_n, splits;
+    int tile_n;
+    int64_t whole;         // tiles computed whole; the others in `splits` parts
+    int splits;
     bool swap, pair;
     size_t parts_bytes;
 };
@@ -304,7 +306,7 @@ size_t gate_scan_workspace(int64_t batch, int64_t seqlen, int width, int dtype);
 cudaError_t launch_gate_scan(const GateScanArgs& a, void* workspace, bool bwd, cudaStream_t st);
 cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st);
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // NULL when the driver has none
-LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool e4m3, bool may_swap);
+LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap);
 cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& plan, cudaStream_t st);
 int64_t linear_dpre_slabs(int64_t m);
 cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st);

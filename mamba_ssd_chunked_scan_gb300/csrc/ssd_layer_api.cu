@@ -97,8 +97,8 @@ LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p) {
     l.dpre_off = sizeof(WsHeader);
     l.shares_off = l.dpre_off + (l.own_dpre ? align_up((size_t)p->m * l.ldp * 2, 256) : 0);
     l.parts_off = l.shares_off + align_up((size_t)linear_dpre_slabs(p->m) * p->n * 4, 256);
-    l.dx = linear_plan(p->m, p->k, (int64_t)p->n * 2, false, false);
-    l.dw = linear_plan(p->n, p->k, p->m * 2, false, false);
+    l.dx = linear_plan(p->m, p->k, (int64_t)p->n * 2, false);
+    l.dw = linear_plan(p->n, p->k, p->m * 2, false);
     l.total = l.parts_off + (l.dx.parts_bytes > l.dw.parts_bytes ? l.dx.parts_bytes : l.dw.parts_bytes);
     return l;
 }
@@ -275,7 +275,7 @@ int ssd_gate_scan_step(int64_t batch, int32_t width, int32_t dtype, int64_t g_st
 size_t ssd_linear_workspace_size(const ssd_linear_params_t* p) {
     if (check_linear(p) != SSD_OK) return 0;
     if (p->m == 0) return sizeof(WsHeader);
-    return sizeof(WsHeader) + linear_plan(p->m, p->n, (int64_t)p->k * elem(p->dtype), p->dtype == SSD_E4M3, true).parts_bytes;
+    return sizeof(WsHeader) + linear_plan(p->m, p->n, (int64_t)p->k * elem(p->dtype), true).parts_bytes;
 }
 
 size_t ssd_linear_bwd_workspace_size(const ssd_linear_params_t* p) {
@@ -296,7 +296,7 @@ int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* w, const
         !aligned(residual, 2) || !aligned(y, 2) || !aligned(pre, 2))
         return SSD_ERR_INVALID_ARG;
     const size_t es = elem(p->dtype);
-    const LinearPlan plan = linear_plan(p->m, p->n, (int64_t)p->k * es, e4m3, true);
+    const LinearPlan plan = linear_plan(p->m, p->n, (int64_t)p->k * es, true);
     const size_t need = sizeof(WsHeader) + plan.parts_bytes;
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
     const Mat in[] = {{x, p->m, p->k, p->ldx, es}, {w, p->n, p->k, p->k, es}, {x_scales, 1, p->m, p->m, 4},

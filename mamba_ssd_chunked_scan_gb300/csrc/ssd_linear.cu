@@ -20,8 +20,9 @@
 // fill the 128 rows of a tile and x is the narrow operand, so the MMAs and the loads are W's
 // and almost nothing is padding; its bound is W's one pass from HBM.
 //
-// Sums are fp32 in tensor memory.  Products whose tiles would leave SMs idle are split along
-// the contraction into parts summed in a fixed order (ssd_linear_join), so results are deterministic.
+// Sums are fp32 in tensor memory.  Tiles run in waves of one per SM (or pair); those of the last wave, which would
+// leave SMs idle, are split along the contraction into parts that are summed in a fixed order
+// (ssd_linear_join), so results are deterministic.
 #include <string.h>
 
 #include <atomic>
@@ -57,8 +58,15 @@ struct LinearParams {
     LinearArgs a;
     int tiles_r, tiles_c;   // tiles over D's rows and columns
     int kblocks;            // 128-byte blocks of the contraction
-    int splits;             // parts of the contraction
-    int items;              // tiles_r * tiles_c * splits
+    int whole;              // tiles [0, whole) are computed whole, the others in `splits` parts
+    int splits;
+    int items;              // whole + (tiles_r * tiles_c - whole) * splits
+    int per;                // blocks per part
+};
+
+// What a worker does: a tile and its blocks [k0, k1) of the contraction; part: the part's number among all, or -1.
+struct Item {
+    int r, c, k0, k1, part;
 };
 
 struct Small {
@@ -362,6 +370,15 @@ __device__ __forceinline__ void tile_at(const LinearParams& p, int t, int& r, in
     c = in / rows;
     r = band * kBand + in - c * rows;
 }
+__device__ __forceinline__ Item item_at(const LinearParams& p, int item) {
+    Item i;
+    i.part = item < p.whole ? -1 : item - p.whole;
+    const int t = i.part < 0 ? item : p.whole + i.part / p.splits;
+    tile_at(p, t, i.r, i.c);
+    i.k0 = i.part < 0 ? 0 : (i.part % p.splits) * p.per;
+    i.k1 = i.part < 0 || i.k0 + p.per > p.kblocks ? p.kblocks : i.k0 + p.per;
+    return i;
+}
 
 // E4M3: 8-bit operands.  AMN / BMN: the operand's contraction runs along its rows in memory (bf16).
 // PAIR: two CTAs per tile of 256 rows.
@@ -373,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ Small sh;
     const LinearArgs& a = p.a;
+    pdl_trigger();   // the join may start on the threads that this grid leaves free
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kElems = E4M3 ? 128 : 64;   // contraction elements per stage
     const int rank = PAIR ? (int)cluster_rank() : 0;
@@ -400,19 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tb = sh.tmem_base;
-    const int per = (p.kblocks + p.splits - 1) / p.splits;   // contraction blocks per part
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
         uint32_t it = 0, st = 0, phase = 0;
         bool go = true;
         for (int item = worker; go && item < p.items; item += workers) {
-            const int s = item % p.splits;
-            int r, c;
-            tile_at(p, item / p.splits, r, c);
-            const int k1 = (s + 1) * per < p.kblocks ? (s + 1) * per : p.kblocks;
-            const int row = r * kRows + rank * kTileM, col = c * TN + rank * C::TB;
-            for (int kb = s * per; kb < k1; ++kb) {
+            const Item i = item_at(p, item);
+            const int row = i.r * kRows + rank * kTileM, col = i.c * TN + rank * C::TB;
+            for (int kb = i.k0; kb < i.k1; ++kb) {
                 if (it >= (uint32_t)C::kStages && !warp_wait(sh, a.ws, &sh.empty[st], phase ^ 1, kWhereEmpty)) {
                     go = false;
                     break;
@@ -467,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             uint32_t tile = 0, st = 0, phase = 0;
             bool go = true;
             for (int item = worker; go && item < p.items; item += workers, ++tile) {
-                const int s = item % p.splits;
-                const int k0 = s * per, k1 = k0 + per < p.kblocks ? k0 + per : p.kblocks;
+                const Item i = item_at(p, item);
+                const int k0 = i.k0, k1 = i.k1;
                 const uint32_t buf = tile & 1, d = tb + buf * TN;
                 if (tile >= 2) {
                     const uint32_t parity = ((tile >> 1) - 1) & 1;
@@ -510,11 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         uint8_t* block = sm + C::kBlocks + (warp - 4) * 2048;
         uint32_t tile = 0;
         for (int item = worker; item < p.items; item += workers, ++tile) {
-            const int s = item % p.splits;
-            int r, c;
-            tile_at(p, item / p.splits, r, c);
+            const Item i = item_at(p, item);
+            const int r = i.r, c = i.c;
             const uint32_t buf = tile & 1;
-            const bool whole = p.splits == 1 && !a.swap;   // rows of y leave from here
+            const bool whole = i.part < 0 && !a.swap;   // rows of y leave from here
             float* vec = reinterpret_cast<float*>(sm + C::kVec) + buf * 2 * TN;
             if (whole && (a.bias || a.x_scales)) {
                 // the columns' scales and bias, once per tile, while its MMAs run; the other tile's are still in use
@@ -565,13 +578,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                 if (a.swap) {
                     // a lane per column of y: 32 of them lie together in a row
                     if (row_ok) {
-                        float* part = a.parts + (size_t)s * a.m * a.n + row;
+                        // a part: TN rows of y by kRows columns
+                        float* part = a.parts + ((size_t)(i.part < 0 ? 0 : i.part) * TN + (col - c * TN)) * kRows + row - r * kRows;
 #pragma unroll
                         for (int k = 0; k < CW; ++k)
                             if (col + k < ncol) {
                                 float v = __uint_as_float(w[k]);
-                                if (p.splits > 1) {
-                                    part[(size_t)(col + k) * a.n] = v;
+                                if (i.part >= 0) {
+                                    part[k * kRows] = v;
                                 } else {
                                     if (a.x_scales) v *= rs * __ldg(a.x_scales + col + k);
                                     finish(a, v + rb, (size_t)(col + k) * a.n + row);
@@ -579,18 +593,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                             }
                     }
                 } else if constexpr (CW == 32) {
-                    if (p.splits > 1) {
-                        float* part = a.parts + ((size_t)s * a.m + row0) * a.n + col;
-                        const int rows = nrow - row0 < 32 ? nrow - row0 : 32;
+                    if (i.part >= 0) {   // a part: kRows rows of y by TN columns, whole
+                        float* part = a.parts + ((size_t)i.part * kRows + row0 - r * kRows) * TN + col - c * TN;
 #pragma unroll
                         for (int k = 0; k < 32; k += 16) {
                             uint4 o[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[e] = make_uint4(w[k + 4 * e], w[k + 4 * e + 1], w[k + 4 * e + 2], w[k + 4 * e + 3]);
-                            const int left = (ncol - col - k) * 4;
-                            if (left <= 0) break;
                             put_block(block, o);
-                            send_block<4>(block, reinterpret_cast<uint8_t*>(part + k), (size_t)a.n * 4, rows, left < 64 ? left : 64, a.n % 4 == 0);
+                            send_block<4>(block, reinterpret_cast<uint8_t*>(part + k), TN * 4, 32, 64, true);
                         }
                     } else {
                         const int k = TN >= 64 ? half * kSpan + j : j;
@@ -609,47 +620,60 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     }
 }
 
-// y from the parts of a split contraction, added in their order.  V elements of a row per thread.
-template <int V>
-__global__ void __launch_bounds__(256) ssd_linear_join(LinearArgs a, int splits) {
-    const size_t total = (size_t)a.m * a.n;
-    const size_t k = ((size_t)blockIdx.x * 256 + threadIdx.x) * V;
-    if (k >= total) return;
-    float v[V];
-    for (int s = 0; s < splits; ++s) {
-        Raw<float, V> q;
-        q.load(a.parts + (size_t)s * total + k);
-        float u[V];
-        q.get(u);
+// y's elements of the tiles that were computed in parts, the parts added in their order.  A thread takes four columns of
+// a row; a tile holds `yr` rows by `yc` columns of y.
+__global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ LinearParams p, int yr, int yc) {
+    const LinearArgs& a = p.a;
+    const int quads = yr * yc / 4, ctas = quads / 256;
+    const int tile = blockIdx.x / ctas, k = (blockIdx.x - tile * ctas) * 256 + threadIdx.x;
+    int r, c;
+    tile_at(p, p.whole + tile, r, c);
+    const int row = k / (yc / 4), col = (k - row * (yc / 4)) * 4;
+    const int64_t m = (int64_t)(a.swap ? c : r) * yr + row;
+    const int n = (a.swap ? r : c) * yc + col;
+    const float* part = a.parts + (size_t)tile * p.splits * yr * yc + (size_t)row * yc + col;
+    pdl_wait();   // launched while the parts are still being made
+    if (m >= a.m || n >= a.n) return;
+    float v[4];
+    for (int s = 0; s < p.splits; ++s) {
+        const float4 q = __ldcs(reinterpret_cast<const float4*>(part + (size_t)s * yr * yc));
+        const float u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = s ? v[e] + u[e] : u[e];
+        for (int e = 0; e < 4; ++e) v[e] = s ? v[e] + u[e] : u[e];
     }
-    const int64_t m = (int64_t)(k / (unsigned)a.n);
-    const int n = (int)(k - (size_t)m * a.n);
     const float xs = a.x_scales ? __ldg(a.x_scales + m) : 1.f;
+    const size_t at = (size_t)m * a.n + n;
+    if (a.vec) {   // n is a multiple of 8: the four columns exist and are aligned
+        Raw<bf16_t, 4> o;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        if (a.x_scales) v[e] *= xs * __ldg(a.w_scales + n + e);
-        if (a.bias) v[e] += __ldg(a.bias + n + e);
-    }
-    Raw<bf16_t, V> o;
-    if (a.pre) {
+        for (int e = 0; e < 4; ++e) {
+            if (a.x_scales) v[e] *= xs * __ldg(a.w_scales + n + e);
+            if (a.bias) v[e] += __ldg(a.bias + n + e);
+        }
+        if (a.pre) {
+            o.set(v);
+            o.store(static_cast<bf16_t*>(a.pre) + at);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_value(v[e], a.act);
+        if (a.residual) {
+            float t[4];
+            o.load(static_cast<const bf16_t*>(a.residual) + at);
+            o.get(t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += t[e];
+        }
         o.set(v);
-        o.store(static_cast<bf16_t*>(a.pre) + k);
-    }
-    if (a.residual) {
-        float r[V];
-        Raw<bf16_t, V> q;
-        q.load(static_cast<const bf16_t*>(a.residual) + k);
-        q.get(r);
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = act_value(v[e], a.act) + r[e];
+        o.store(static_cast<bf16_t*>(a.y) + at);
     } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = act_value(v[e], a.act);
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.n) {
+                if (a.x_scales) v[e] *= xs * __ldg(a.w_scales + n + e);
+                if (a.bias) v[e] += __ldg(a.bias + n + e);
+                finish(a, v[e], at + e);
+            }
     }
-    o.set(v);
-    o.store(static_cast<bf16_t*>(a.y) + k);
 }
 
 // dpre = dy act'(pre), rounded to bf16 into rows of ldp elements, and each row slab's sums over its
@@ -783,10 +807,11 @@ cudaError_t launch_kind(const LinearParams& p, const LinearPlan& plan, cudaStrea
 
 // How a product of `rows` x `cols` results over a contraction of `kbytes` bytes runs.  Up to kLinearSwap
 // rows it is computed transposed.  Otherwise the tile (128 rows by one CTA or 256 by a pair, 64 to 256 columns)
-// and the number of parts minimise a count of cycles: waves of tiles, each its 128-byte blocks and a fixed start.
-// A block takes the longer of its MMAs (2 cycles per column of bf16 operands, 1 of e4m3; a pair's two SMs work on
-// twice the rows) and of its operands' way from L2, about 60 bytes per SM and cycle; parts add the join's launch and its traffic.
-LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool e4m3, bool may_swap) {
+// and the parts of the last wave's tiles minimise a count of cycles: a 128-byte block of a tile takes the longer of its
+// MMAs (2 cycles per column of the tile; a pair's two SMs work on twice the rows) and its operands' way from L2, about
+// 64 bytes per SM and cycle; a tile another 600 for its start, and its epilogue behind the last one.
+// Parts cost their way to L2 and back (about 3500 bytes a cycle) and the join's launch.
+LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
     LinearPlan best = {};
     const int64_t kblocks = (kbytes + kRowB - 1) / kRowB;
     const bool swap = may_swap && rows <= kLinearSwap;
@@ -799,23 +824,24 @@ LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool e4m3, bo
             if (swap ? (tn > kLinearSwap || (tn < dc && tn < kLinearSwap) || (tn > 16 && tn / 2 >= dc)) : tn < 64) continue;
             const int64_t tm = pair ? 2 * kTileM : kTileM;
             const int64_t tiles = ((dr + tm - 1) / tm) * ((dc + tn - 1) / tn), workers = pair ? kLinearSMs / 2 : kLinearSMs;
-            const double mma = (e4m3 ? 1.0 : 2.0) * tn, fill = (128 + (pair ? tn / 2 : tn)) * 128 / 60.0;
+            const double mma = 2.0 * tn, fill = (128 + (pair ? tn / 2 : tn)) * 128 / 64.0;
             const double block = mma > fill ? mma : fill;
-            for (int s = 1; s <= kLinearMaxSplits; ++s) {
+            const int64_t full = tiles / workers, rest = tiles - full * workers;
+            for (int s = 1; s <= kLinearMaxSplits && (s == 1 || rest); ++s) {
                 const int64_t per = (kblocks + s - 1) / s;
                 if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;   // every part has blocks
-                const int64_t waves = (tiles * s + workers - 1) / workers;
-                double cost = (double)waves * (per * block + 600) + 2.0 * tn;
-                if (s > 1) cost += 5000 + (double)rows * cols * 8 * s / 3500;   // about 3500 bytes of HBM a cycle
+                double cost = (double)full * (kblocks * block + 600) + 12.0 * tn;
+                cost += (double)((rest * s + workers - 1) / workers) * (per * block + 600);
+                if (s > 1) cost += 4000 + (double)rest * s * tm * tn * 8 / 3500;
                 if (least == 0 || cost < least) {
                     least = cost;
                     best.tile_n = tn;
                     best.splits = s;
                     best.swap = swap;
                     best.pair = pair != 0;
-                    best.parts_bytes = s > 1 ? (size_t)rows * cols * 4 * s : 0;
+                    best.whole = s > 1 ? full * workers : tiles;
+                    best.parts_bytes = s > 1 ? (size_t)rest * s * tm * tn * 4 : 0;
                 }
-                if (tiles * s >= 4 * workers) break;
             }
         }
     return best;
@@ -835,7 +861,9 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     p.tiles_c = (int)((dc + tn - 1) / tn);
     p.kblocks = (int)((a.k * es + kRowB - 1) / kRowB);
     p.splits = plan.splits;
-    p.items = p.tiles_r * p.tiles_c * p.splits;
+    p.per = (p.kblocks + p.splits - 1) / p.splits;
+    p.whole = (int)plan.whole;
+    p.items = p.whole + (p.tiles_r * p.tiles_c - p.whole) * p.splits;
     // the wide operand gives D's rows, 128 at a time; operands with their contraction along the rows
     // are read in boxes of 64 x 64
     const LinearOperand& oa = a.swap ? a.w : a.x;
@@ -851,10 +879,8 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     else if (ob.along_rows) e = launch_kind<false, false, true>(p, plan, st);
     else e = launch_kind<false, false, false>(p, plan, st);
     if (e != cudaSuccess || p.splits == 1) return e;
-    const size_t total = (size_t)a.m * a.n;
-    if (a.vec) ssd_linear_join<4><<<(unsigned)((total / 4 + 255) / 256), 256, 0, st>>>(a, p.splits);
-    else ssd_linear_join<1><<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a, p.splits);
-    return cudaGetLastError();
+    const int yr = a.swap ? tn : tm, yc = a.swap ? tm : tn, rest = p.tiles_r * p.tiles_c - p.whole;
+    return launch_kernel(ssd_linear_join, (unsigned)(rest * (yr * yc / 1024)), 256, 0, st, true, p, yr, yc);
 }
 
 int64_t linear_dpre_slabs(int64_t m) { return (m + kSlabRows - 1) / kSlabRows; }
