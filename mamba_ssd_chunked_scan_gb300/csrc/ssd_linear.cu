@@ -277,21 +277,24 @@ __device__ __forceinline__ void send_block(const uint8_t* block, uint8_t* base, 
 
 // 32 columns (one row per lane) of a tile from their sums `w`: D's rows `row` to `row` + 31, columns col on.
 // `vec`: this chunk's scales (then bias) by column, in shared memory, TN apart; xs: the row's scale.
-__device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t (&w)[32], int64_t row, int col, float xs,
-                                            const float* ws, const float* bias, uint8_t* block) {
+// r: the residual's elements, asked for ahead (aligned rows).
+__device__ __forceinline__ void ask_residual(const LinearArgs& a, uint4 (&r)[4], int64_t row, int col) {
+    const int lane = threadIdx.x & 31;
+    const bf16_t* res = static_cast<const bf16_t*>(a.residual) + (size_t)(row + lane) * a.n + col;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        r[k] = make_uint4(0, 0, 0, 0);
+        if (row + lane < a.m && col + 8 * k < a.n) r[k] = __ldcs(reinterpret_cast<const uint4*>(res + 8 * k));
+    }
+}
+__device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t (&w)[32], uint4 (&r)[4], int64_t row, int col,
+                                            float xs, const float* ws, const float* bias, uint8_t* block) {
     const int lane = threadIdx.x & 31;
     const int rows = a.m - row < 32 ? (int)(a.m - row) : 32, cols = a.n - col < 32 ? a.n - col : 32;
     const size_t at = (size_t)row * a.n + col;
-    uint4 r[4];
     if (a.residual) {
         const bf16_t* res = static_cast<const bf16_t*>(a.residual);
-        if (a.vec) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                r[k] = make_uint4(0, 0, 0, 0);
-                if (lane < rows && 8 * k < cols) r[k] = __ldcs(reinterpret_cast<const uint4*>(res + at + (size_t)lane * a.n + 8 * k));
-            }
-        } else {   // row by row through the block
+        if (!a.vec) {   // row by row through the block
             __syncwarp();
             for (int i = 0; i < rows; ++i)
                 if (lane < cols) *reinterpret_cast<bf16_t*>(word_at(block, i, lane >> 3) + 2 * (lane & 7)) = res[at + (size_t)i * a.n + lane];
@@ -544,6 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             // the row's scale and bias (transposed: of the row of w)
             const float rs = a.x_scales && row_ok ? __ldg((a.swap ? a.w_scales : a.x_scales) + row) : 1.f;
             const float rb = a.swap && a.bias && row_ok ? __ldg(a.bias + row) : 0.f;
+            // the residual of the first 32 columns comes while the MMAs run, that of the next while these are finished
+            const bool ask = whole && a.residual && a.vec;
+            uint4 res[4], next[4];
+            if (ask) ask_residual(a, res, row0, c * TN + (TN >= 64 ? half * kSpan : 0));
             bool ok = true;
             if (lane == 0) ok = lin_wait(sh, a.ws, &sh.acc[buf], (tile >> 1) & 1, kWhereAcc);
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -605,7 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                         }
                     } else {
                         const int k = TN >= 64 ? half * kSpan + j : j;
-                        finish_rows(a, w, row0, col, rs, vec + k, vec + TN + k, block);
+                        if (ask && j + CW < kSpan) ask_residual(a, next, row0, col + CW);
+                        finish_rows(a, w, res, row0, col, rs, vec + k, vec + TN + k, block);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) res[e] = next[e];
                     }
                 }
             }
@@ -677,47 +687,72 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
 }
 
 // dpre = dy act'(pre), rounded to bf16 into rows of ldp elements, and each row slab's sums over its
-// rows (of the unrounded products).  256 threads: 32 pairs of columns x 8 rows at a time.
-constexpr int kSlabRows = 128;
+// rows (of the unrounded products).  A CTA takes 256 columns of kSlabRows rows, a warp every eighth row, a lane eight
+// columns: together (V = 8: rows are whole 16-byte words) or 32 apart (V = 1).  Bound by HBM: four rows' loads are in
+// flight per warp.
+constexpr int kSlabRows = 128, kSlabCols = 256;
+template <int V>
 __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
-    __shared__ float2 part[8][32];
+    __shared__ float part[8][kSlabCols];
+    constexpr int C = 8 / V, kRowsAhead = 4;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const unsigned ncol = (unsigned)(a.n + 63) / 64, slab = blockIdx.x / ncol;
-    const int n0 = (int)(blockIdx.x - slab * ncol) * 64 + 2 * lane;
+    const unsigned ncol = (unsigned)(a.n + kSlabCols - 1) / kSlabCols, slab = blockIdx.x / ncol;
+    const int c0 = (int)(blockIdx.x - slab * ncol) * kSlabCols, n0 = c0 + lane * V;
     const int64_t m0 = (int64_t)slab * kSlabRows;
-    const bool ok0 = n0 < a.n, ok1 = n0 + 1 < a.n;
-    const bf16_t* dy = static_cast<const bf16_t*>(a.dy);
-    const bf16_t* pre = static_cast<const bf16_t*>(a.pre);
-    bf16_t* dp = static_cast<bf16_t*>(a.dpre);
-    float2 sum = make_float2(0.f, 0.f);
-    for (int k = w; k < kSlabRows; k += 8) {
-        const int64_t m = m0 + k;
-        if (m >= a.m) break;
-        const size_t at = (size_t)m * a.n + n0;
-        float v0 = ok0 ? __bfloat162float(dy[at]) : 0.f, v1 = ok1 ? __bfloat162float(dy[at + 1]) : 0.f;
-        if (pre) {
-            if (ok0) v0 *= act_slope(__bfloat162float(pre[at]), a.act);
-            if (ok1) v1 *= act_slope(__bfloat162float(pre[at + 1]), a.act);
-        }
-        if (dp) {
-            bf16_t* q = dp + (size_t)m * a.ldp + n0;
-            if (ok0) q[0] = __float2bfloat16_rn(v0);
-            if (ok1) q[1] = __float2bfloat16_rn(v1);
-        }
-        sum.x += v0;
-        sum.y += v1;
+    const int rows = a.m - m0 < kSlabRows ? (int)(a.m - m0) : kSlabRows;
+    const bf16_t* dy = static_cast<const bf16_t*>(a.dy) + (size_t)m0 * a.n + n0;
+    const bf16_t* pre = a.pre ? static_cast<const bf16_t*>(a.pre) + (size_t)m0 * a.n + n0 : nullptr;
+    bf16_t* dp = a.dpre ? static_cast<bf16_t*>(a.dpre) + (size_t)m0 * a.ldp + n0 : nullptr;
+    float sum[C][V] = {};
+    for (int k0 = w; k0 < rows; k0 += 8 * kRowsAhead) {
+        Raw<bf16_t, V> d[kRowsAhead][C], q[kRowsAhead][C];
+#pragma unroll
+        for (int u = 0; u < kRowsAhead; ++u)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int k = k0 + 8 * u;
+                d[u][c].zero();
+                q[u][c].zero();
+                if (k < rows && n0 + 32 * c < a.n) {
+                    d[u][c].load(dy + (size_t)k * a.n + 32 * c);
+                    if (pre) q[u][c].load(pre + (size_t)k * a.n + 32 * c);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < kRowsAhead; ++u)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int k = k0 + 8 * u;
+                if (k >= rows || n0 + 32 * c >= a.n) continue;
+                float v[V], t[V];
+                d[u][c].get(v);
+                if (pre) {
+                    q[u][c].get(t);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] *= act_slope(t[e], a.act);
+                }
+                if (dp) {
+                    Raw<bf16_t, V> o;
+                    o.set(v);
+                    // read next by the products, so left in L2
+                    *reinterpret_cast<typename Raw<bf16_t, V>::W*>(dp + (size_t)k * a.ldp + 32 * c) = o.w;
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[c][e] += v[e];
+            }
     }
     if (!a.shares) return;
-    part[w][lane] = sum;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[w][lane * V + 32 * c + e] = sum[c][e];
     __syncthreads();
-    if (w == 0) {
-        for (int k = 1; k < 8; ++k) {
-            sum.x += part[k][lane].x;
-            sum.y += part[k][lane].y;
-        }
-        float* s = a.shares + (size_t)slab * a.n + n0;
-        if (ok0) s[0] = sum.x;
-        if (ok1) s[1] = sum.y;
+    const int n = c0 + threadIdx.x;
+    if (n < a.n) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += part[k][threadIdx.x];
+        a.shares[(size_t)slab * a.n + n] = t;
     }
 }
 
@@ -809,7 +844,8 @@ cudaError_t launch_kind(const LinearParams& p, const LinearPlan& plan, cudaStrea
 // rows it is computed transposed.  Otherwise the tile (128 rows by one CTA or 256 by a pair, 64 to 256 columns)
 // and the parts of the last wave's tiles minimise a count of cycles: a 128-byte block of a tile takes the longer of its
 // MMAs (2 cycles per column of the tile; a pair's two SMs work on twice the rows) and its operands' way from L2, about
-// 64 bytes per SM and cycle; a tile another 600 for its start, and its epilogue behind the last one.
+// 88 bytes per SM and cycle at best (measured per block of 128 x 256: 541 cycles by a CTA, 520 by a pair); a tile another
+// 600 for its start, and its epilogue behind the last one.
 // Parts cost their way to L2 and back (about 3500 bytes a cycle) and the join's launch.
 LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
     LinearPlan best = {};
@@ -824,7 +860,7 @@ LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap
             if (swap ? (tn > kLinearSwap || (tn < dc && tn < kLinearSwap) || (tn > 16 && tn / 2 >= dc)) : tn < 64) continue;
             const int64_t tm = pair ? 2 * kTileM : kTileM;
             const int64_t tiles = ((dr + tm - 1) / tm) * ((dc + tn - 1) / tn), workers = pair ? kLinearSMs / 2 : kLinearSMs;
-            const double mma = 2.0 * tn, fill = (128 + (pair ? tn / 2 : tn)) * 128 / 64.0;
+            const double mma = 2.0 * tn, fill = (128 + (pair ? tn / 2 : tn)) * 128 / 88.0;
             const double block = mma > fill ? mma : fill;
             const int64_t full = tiles / workers, rest = tiles - full * workers;
             for (int s = 1; s <= kLinearMaxSplits && (s == 1 || rest); ++s) {
@@ -887,7 +923,9 @@ int64_t linear_dpre_slabs(int64_t m) { return (m + kSlabRows - 1) / kSlabRows; }
 
 cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st) {
     const int64_t slabs = linear_dpre_slabs(a.m);
-    ssd_linear_dpre<<<(unsigned)(slabs * ((a.n + 63) / 64)), 256, 0, st>>>(a);
+    const unsigned grid = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
+    if (a.n % 8 == 0 && ((uintptr_t)a.pre & 15) == 0) ssd_linear_dpre<8><<<grid, 256, 0, st>>>(a);
+    else ssd_linear_dpre<1><<<grid, 256, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dbias) return e;
     ssd_linear_dbias<<<(unsigned)((a.n + 31) / 32), 1024, 0, st>>>(a.shares, (int)slabs, a.n, a.dbias);
