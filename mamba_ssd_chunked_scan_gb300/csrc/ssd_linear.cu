@@ -251,9 +251,8 @@ __device__ __forceinline__ void put_block(uint8_t* block, const uint4 (&w)[4]) {
     for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(word_at(block, lane, k)) = w[k];
     __syncwarp();
 }
-// The block to memory: row r to base + r * pitch bytes, for r < rows.  `bytes` of each row exist (ELEM of them per
-// element); VEC: whole 16-byte words, aligned.
-template <int ELEM>
+// The block to memory: row r to base + r * pitch bytes, for r < rows.  `bytes` of each row exist; vec: whole 16-byte
+// words, aligned.
 __device__ __forceinline__ void send_block(const uint8_t* block, uint8_t* base, size_t pitch, int rows, int bytes, bool vec) {
     const int lane = threadIdx.x & 31;
     uint8_t* const blk = const_cast<uint8_t*>(block);
@@ -265,13 +264,11 @@ __device__ __forceinline__ void send_block(const uint8_t* block, uint8_t* base, 
             if (row < rows && 16 * word < bytes) *reinterpret_cast<uint4*>(base + row * pitch + 16 * word) = v;
         }
     } else {
-        // one row at a time, an element per lane
+        // one row at a time, a bf16 per lane
         for (int row = 0; row < rows; ++row)
-            if (lane * ELEM < 64 && lane * ELEM < bytes) {
-                const uint8_t* from = word_at(blk, row, (lane * ELEM) >> 4) + ((lane * ELEM) & 15);
-                if constexpr (ELEM == 2) *reinterpret_cast<uint16_t*>(base + row * pitch + 2 * lane) = *reinterpret_cast<const uint16_t*>(from);
-                else *reinterpret_cast<uint32_t*>(base + row * pitch + 4 * lane) = *reinterpret_cast<const uint32_t*>(from);
-            }
+            if (2 * lane < bytes)
+                *reinterpret_cast<uint16_t*>(base + row * pitch + 2 * lane) =
+                    *reinterpret_cast<const uint16_t*>(word_at(blk, row, lane >> 3) + 2 * (lane & 7));
     }
 }
 
@@ -341,7 +338,7 @@ __device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t 
     if (a.pre) {
         pack(o);
         put_block(block, o);
-        send_block<2>(block, static_cast<uint8_t*>(a.pre) + at * 2, (size_t)a.n * 2, rows, cols * 2, a.vec);
+        send_block(block, static_cast<uint8_t*>(a.pre) + at * 2, (size_t)a.n * 2, rows, cols * 2, a.vec);
     }
     if (a.act != SSD_ACT_NONE) {
 #pragma unroll
@@ -360,7 +357,7 @@ __device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t 
     }
     pack(o);
     put_block(block, o);
-    send_block<2>(block, static_cast<uint8_t*>(a.y) + at * 2, (size_t)a.n * 2, rows, cols * 2, a.vec);
+    send_block(block, static_cast<uint8_t*>(a.y) + at * 2, (size_t)a.n * 2, rows, cols * 2, a.vec);
 }
 
 // Tile (r, c) of the t-th tile: bands of kBand row tiles walk the columns together, so that the tiles in
@@ -582,41 +579,30 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                 }
                 const int col = c * TN + (TN >= 64 ? half * kSpan : 0) + j;
                 if (idle || row0 >= nrow || col >= ncol) continue;   // the same for the whole warp
-                if (a.swap) {
+                if (i.part >= 0) {
+                    // a part, whole: quads of columns, in each the tile's rows, so that a warp's stores lie together
+                    float4* part = reinterpret_cast<float4*>(a.parts) + ((size_t)i.part * (TN / 4) + (col - c * TN) / 4) * kRows + row - r * kRows;
+#pragma unroll
+                    for (int k = 0; k < CW; k += 4)
+                        part[(k / 4) * kRows] = make_float4(__uint_as_float(w[k]), __uint_as_float(w[k + 1]), __uint_as_float(w[k + 2]),
+                                                            __uint_as_float(w[k + 3]));
+                } else if (a.swap) {
                     // a lane per column of y: 32 of them lie together in a row
-                    if (row_ok) {
-                        // a part: TN rows of y by kRows columns
-                        float* part = a.parts + ((size_t)(i.part < 0 ? 0 : i.part) * TN + (col - c * TN)) * kRows + row - r * kRows;
+                    if (row_ok && i.part < 0) {
 #pragma unroll
                         for (int k = 0; k < CW; ++k)
                             if (col + k < ncol) {
                                 float v = __uint_as_float(w[k]);
-                                if (i.part >= 0) {
-                                    part[k * kRows] = v;
-                                } else {
-                                    if (a.x_scales) v *= rs * __ldg(a.x_scales + col + k);
-                                    finish(a, v + rb, (size_t)(col + k) * a.n + row);
-                                }
+                                if (a.x_scales) v *= rs * __ldg(a.x_scales + col + k);
+                                finish(a, v + rb, (size_t)(col + k) * a.n + row);
                             }
                     }
                 } else if constexpr (CW == 32) {
-                    if (i.part >= 0) {   // a part: kRows rows of y by TN columns, whole
-                        float* part = a.parts + ((size_t)i.part * kRows + row0 - r * kRows) * TN + col - c * TN;
+                    const int k = TN >= 64 ? half * kSpan + j : j;
+                    if (ask && j + CW < kSpan) ask_residual(a, next, row0, col + CW);
+                    finish_rows(a, w, res, row0, col, rs, vec + k, vec + TN + k, block);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 16) {
-                            uint4 o[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[e] = make_uint4(w[k + 4 * e], w[k + 4 * e + 1], w[k + 4 * e + 2], w[k + 4 * e + 3]);
-                            put_block(block, o);
-                            send_block<4>(block, reinterpret_cast<uint8_t*>(part + k), TN * 4, 32, 64, true);
-                        }
-                    } else {
-                        const int k = TN >= 64 ? half * kSpan + j : j;
-                        if (ask && j + CW < kSpan) ask_residual(a, next, row0, col + CW);
-                        finish_rows(a, w, res, row0, col, rs, vec + k, vec + TN + k, block);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) res[e] = next[e];
-                    }
+                    for (int e = 0; e < 4; ++e) res[e] = next[e];
                 }
             }
         }
@@ -630,27 +616,41 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     }
 }
 
-// y's elements of the tiles that were computed in parts, the parts added in their order.  A thread takes four columns of
-// a row; a tile holds `yr` rows by `yc` columns of y.
-__global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ LinearParams p, int yr, int yc) {
+// y's elements of the tiles that were computed in parts, the parts added in their order.  A part holds quads of D's columns,
+// in each the tile's rows.  A thread takes a quad; a warp 4 rows x 8 quads, 64 bytes together on either side.  (Transposed
+// products have y's columns along D's rows: there a thread's four values lie in four rows of y.)
+__global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ LinearParams p, int tm, int tn) {
     const LinearArgs& a = p.a;
-    const int quads = yr * yc / 4, ctas = quads / 256;
-    const int tile = blockIdx.x / ctas, k = (blockIdx.x - tile * ctas) * 256 + threadIdx.x;
+    const int ctas = tm * tn / 1024;
+    const int tile = blockIdx.x / ctas, w = (blockIdx.x - tile * ctas) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     int r, c;
     tile_at(p, p.whole + tile, r, c);
-    const int row = k / (yc / 4), col = (k - row * (yc / 4)) * 4;
-    const int64_t m = (int64_t)(a.swap ? c : r) * yr + row;
-    const int n = (a.swap ? r : c) * yc + col;
-    const float* part = a.parts + (size_t)tile * p.splits * yr * yc + (size_t)row * yc + col;
+    // transposed: 32 rows of one quad per warp
+    const int across = a.swap ? 1 : 8, down = 32 / across, groups = tm / down;
+    const int row = (w % groups) * down + lane / across, quad = (w / groups) * across + lane % across;
+    const float4* part = reinterpret_cast<const float4*>(a.parts) + ((size_t)tile * p.splits * (tn / 4) + quad) * tm + row;
+    const int dr = r * tm + row, dc = c * tn + 4 * quad;
     pdl_wait();   // launched while the parts are still being made
-    if (m >= a.m || n >= a.n) return;
+    if (dr >= (a.swap ? a.n : a.m) || dc >= (a.swap ? a.m : a.n)) return;
     float v[4];
     for (int s = 0; s < p.splits; ++s) {
-        const float4 q = __ldcs(reinterpret_cast<const float4*>(part + (size_t)s * yr * yc));
+        const float4 q = __ldcs(part + (size_t)s * (tn / 4) * tm);
         const float u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = s ? v[e] + u[e] : u[e];
     }
+    if (a.swap) {
+        const float ws = a.x_scales ? __ldg(a.w_scales + dr) : 1.f, b = a.bias ? __ldg(a.bias + dr) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (dc + e < a.m) {
+                if (a.x_scales) v[e] *= __ldg(a.x_scales + dc + e) * ws;
+                finish(a, v[e] + b, (size_t)(dc + e) * a.n + dr);
+            }
+        return;
+    }
+    const int64_t m = dr;
+    const int n = dc;
     const float xs = a.x_scales ? __ldg(a.x_scales + m) : 1.f;
     const size_t at = (size_t)m * a.n + n;
     if (a.vec) {   // n is a multiple of 8: the four columns exist and are aligned
@@ -915,8 +915,8 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     else if (ob.along_rows) e = launch_kind<false, false, true>(p, plan, st);
     else e = launch_kind<false, false, false>(p, plan, st);
     if (e != cudaSuccess || p.splits == 1) return e;
-    const int yr = a.swap ? tn : tm, yc = a.swap ? tm : tn, rest = p.tiles_r * p.tiles_c - p.whole;
-    return launch_kernel(ssd_linear_join, (unsigned)(rest * (yr * yc / 1024)), 256, 0, st, true, p, yr, yc);
+    const int rest = p.tiles_r * p.tiles_c - p.whole;
+    return launch_kernel(ssd_linear_join, (unsigned)(rest * (tm * tn / 1024)), 256, 0, st, true, p, tm, tn);
 }
 
 int64_t linear_dpre_slabs(int64_t m) { return (m + kSlabRows - 1) / kSlabRows; }
