@@ -842,12 +842,12 @@ cudaError_t launch_kind(const LinearParams& p, const LinearPlan& plan, cudaStrea
 
 // How a product of `rows` x `cols` results over a contraction of `kbytes` bytes runs.  Up to kLinearSwap
 // rows it is computed transposed.  Otherwise the tile (128 rows by one CTA or 256 by a pair, 64 to 256 columns)
-// and the parts of the last wave's tiles minimise a count of cycles: a 128-byte block of a tile takes the longer of its
-// MMAs (2 cycles per column of the tile; a pair's two SMs work on twice the rows) and its operands' way from L2, about
-// 88 bytes per SM and cycle at best (measured per block of 128 x 256: 541 cycles by a CTA, 520 by a pair); a tile another
-// 600 for its start, and its epilogue behind the last one.
-// Parts cost their way to L2 and back (about 3500 bytes a cycle) and the join's launch.
-LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
+// and the parts of the last wave's tiles minimise a count of cycles.  Measured: a 128-byte block of a tile takes
+// 520 cycles by a pair and 541 by a CTA at 256 columns, where the MMAs bound it, but 417 at 128 and 390 at 64 (the
+// rows of A are read from shared memory for each MMA however few the columns); a tile's start 600; a
+// launch's first loads and last epilogue about 15 a column, and 3000 more for clusters; parts 6300 for the
+// join and a cycle per 4000 bytes of them, written and read.
+static LinearPlan find_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
     LinearPlan best = {};
     const int64_t kblocks = (kbytes + kRowB - 1) / kRowB;
     const bool swap = may_swap && rows <= kLinearSwap;
@@ -860,15 +860,15 @@ LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap
             if (swap ? (tn > kLinearSwap || (tn < dc && tn < kLinearSwap) || (tn > 16 && tn / 2 >= dc)) : tn < 64) continue;
             const int64_t tm = pair ? 2 * kTileM : kTileM;
             const int64_t tiles = ((dr + tm - 1) / tm) * ((dc + tn - 1) / tn), workers = pair ? kLinearSMs / 2 : kLinearSMs;
-            const double mma = 2.0 * tn, fill = (128 + (pair ? tn / 2 : tn)) * 128 / 88.0;
-            const double block = mma > fill ? mma : fill;
+            const double mma = 2.0 * tn + (pair ? 8 : 29), least_block = 365 + 0.4 * tn;
+            const double block = mma > least_block ? mma : least_block;
             const int64_t full = tiles / workers, rest = tiles - full * workers;
             for (int s = 1; s <= kLinearMaxSplits && (s == 1 || rest); ++s) {
                 const int64_t per = (kblocks + s - 1) / s;
                 if (s > 1 && (per < 4 || (kblocks + per - 1) / per != s)) continue;   // every part has blocks
-                double cost = (double)full * (kblocks * block + 600) + 12.0 * tn;
+                double cost = (double)full * (kblocks * block + 600) + 15.0 * tn + (pair ? 3000 : 0);
                 cost += (double)((rest * s + workers - 1) / workers) * (per * block + 600);
-                if (s > 1) cost += 4000 + (double)rest * s * tm * tn * 8 / 3500;
+                if (s > 1) cost += 6300 + (double)rest * s * tm * tn * 8 / 4000;
                 if (least == 0 || cost < least) {
                     least = cost;
                     best.tile_n = tn;
@@ -881,6 +881,21 @@ LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap
             }
         }
     return best;
+}
+
+// The search takes a microsecond or two, which a decoding step would feel twice (sizing and launching): each
+// host thread remembers its last few shapes' plans.
+LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
+    struct Known {
+        int64_t rows, cols, kbytes;
+        bool may_swap;
+        LinearPlan plan;
+    };
+    static thread_local Known known[64];   // rows 0: empty
+    Known& k = known[((uint64_t)rows * 0x9E3779B97F4A7C15ull + (uint64_t)cols * 0xC2B2AE3D27D4EB4Full + (uint64_t)kbytes) >> 32 & 63];
+    if (k.rows != rows || k.cols != cols || k.kbytes != kbytes || k.may_swap != may_swap)
+        k = Known{rows, cols, kbytes, may_swap, find_plan(rows, cols, kbytes, may_swap)};
+    return k.plan;
 }
 
 cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaStream_t st) {
