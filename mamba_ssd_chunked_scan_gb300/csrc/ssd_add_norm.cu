@@ -25,6 +25,8 @@ namespace {
 
 constexpr int kElems = 16;      // elements of a row per thread
 constexpr int kBwdElems = 8;    // the same in the backward
+// Threads per SM that the backward's registers allow (96 a thread, with the next row loaded ahead).
+constexpr int kBwdThreadsSM = 640;
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxMin = 1e-30f;
 
@@ -44,6 +46,23 @@ __device__ __forceinline__ float row_reduce(float v, bool one_warp, float* part)
     const int nw = blockDim.x >> 5;
     for (int k = 1; k < nw; ++k) r = kMax ? max_nan(r, part[k]) : r + part[k];
     return r;
+}
+
+// V weights (16-byte aligned where V > 1), kept in the caches.
+template <int V>
+__device__ __forceinline__ void load_weights(const float* p, float (&w)[V]) {
+    if constexpr (V == 1) {
+        w[0] = __ldg(p);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(p + k));
+            w[k] = q.x;
+            w[k + 1] = q.y;
+            w[k + 2] = q.z;
+            w[k + 3] = q.w;
+        }
+    }
 }
 
 template <typename T, typename R, typename O, int V>
@@ -105,9 +124,11 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
     for (int c = 0; c < C; ++c) {
         const int e = (tid + c * nt) * V;
         if (e < W) {
+            float w[V];
+            load_weights(a.weight + e, w);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                h[c][k] = h[c][k] * rstd * __ldg(a.weight + e + k);
+                h[c][k] = h[c][k] * rstd * w[k];
                 amax = max_nan(amax, fabsf(h[c][k]));
             }
         }
@@ -135,52 +156,72 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
     }
 }
 
-// E: elements of a row per thread, V of them at a time.
-template <typename T, typename R, int V, int E>
-__global__ void __launch_bounds__(1024) ssd_add_norm_bwd_kernel(AddNormBwdArgs a) {
+// E: elements of a row per thread, V of them at a time.  Rows of up to 640 threads (THREADS) have the registers to
+// load the next row while the present one is reduced and written.
+template <typename T, typename R, int V, int E, int THREADS>
+__global__ void __launch_bounds__(THREADS) ssd_add_norm_bwd_kernel(AddNormBwdArgs a) {
     constexpr int C = E / V;
+    constexpr bool kAhead = THREADS <= kBwdThreadsSM;
     __shared__ float part[2][32];
     const bool one_warp = a.rows_per_cta > 1 || blockDim.x == 32;
     const int slot = one_warp ? threadIdx.x >> 5 : 0;
     const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
     const int nt = one_warp ? 32 : blockDim.x;
     const int W = a.width;
-    float dw[C][V];
+    pdl_trigger();
+    float dw[C][V], wt[C][V];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+        const int e = (tid + c * nt) * V;
 #pragma unroll
-        for (int k = 0; k < V; ++k) dw[c][k] = 0.f;
-    const int64_t stride = (int64_t)gridDim.x * a.rows_per_cta;
-    int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot; row < a.rows; row += stride) {
+        for (int k = 0; k < V; ++k) dw[c][k] = wt[c][k] = 0.f;
+        if (e < W) load_weights(a.weight + e, wt[c]);
+    }
+    struct Row {
+        Raw<T, V> d[C];
+        Raw<R, V> h[C], s[C];
+        float rstd;
+    };
+    auto load = [&](Row& r, int64_t row) {
         const size_t base = (size_t)row * W;
-        Raw<T, V> dr[C];
-        Raw<R, V> hr[C], sr[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = (tid + c * nt) * V;
-            dr[c].zero();
-            hr[c].zero();
-            sr[c].zero();
+            r.d[c].zero();
+            r.h[c].zero();
+            r.s[c].zero();
             if (e < W) {
-                dr[c].load(static_cast<const T*>(a.dout) + base + e);
-                hr[c].load(static_cast<const R*>(a.h) + base + e);
-                if (a.dres) sr[c].load(static_cast<const R*>(a.dres) + base + e);
+                r.d[c].load(static_cast<const T*>(a.dout) + base + e);
+                r.h[c].load(static_cast<const R*>(a.h) + base + e);
+                if (a.dres) r.s[c].load(static_cast<const R*>(a.dres) + base + e);
             }
         }
-        const float rstd = __ldg(a.rstd + row);
+        r.rstd = __ldg(a.rstd + row);
+    };
+    const int64_t stride = (int64_t)gridDim.x * a.rows_per_cta;
+    int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot;
+    Row cur;
+    if (kAhead && row < a.rows) load(cur, row);
+    int turn = 0;
+    for (; row < a.rows; row += stride) {
+        Row next;
+        if (kAhead) {
+            if (row + stride < a.rows) load(next, row + stride);
+        } else {
+            load(cur, row);
+        }
+        const size_t base = (size_t)row * W;
         float p[C][V], xh[C][V];
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = (tid + c * nt) * V;
-            dr[c].get(p[c]);
-            hr[c].get(xh[c]);
+            cur.d[c].get(p[c]);
+            cur.h[c].get(xh[c]);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                xh[c][k] *= rstd;
+                xh[c][k] *= cur.rstd;
                 dw[c][k] = fmaf(p[c][k], xh[c][k], dw[c][k]);
-                if (e < W) p[c][k] *= __ldg(a.weight + e + k);
+                p[c][k] *= wt[c][k];
                 dot = fmaf(p[c][k], xh[c][k], dot);
             }
         }
@@ -193,9 +234,9 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_bwd_kernel(AddNormBwdArgs a
             const int e = (tid + c * nt) * V;
             if (e < W) {
                 float s[V];
-                sr[c].get(s);
+                cur.s[c].get(s);
 #pragma unroll
-                for (int k = 0; k < V; ++k) s[k] = fmaf(p[c][k] - xh[c][k] * dot, rstd, s[k]);
+                for (int k = 0; k < V; ++k) s[k] = fmaf(p[c][k] - xh[c][k] * dot, cur.rstd, s[k]);
                 if (a.dx) {
                     Raw<T, V> q;
                     q.set(s);
@@ -208,6 +249,7 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_bwd_kernel(AddNormBwdArgs a
                 }
             }
         }
+        if (kAhead) cur = next;
     }
     float* share = a.shares + ((size_t)blockIdx.x * a.rows_per_cta + slot) * W;
 #pragma unroll
@@ -227,6 +269,7 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_bwd_reduce(const float* sha
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + lane;
     float s = 0.f;
+    pdl_wait();   // launched while the shares are still being summed
     if (e < W)
         for (int k = w; k < nshares; k += 32) s += shares[(size_t)k * W + e];
     part[w][lane] = s;
@@ -263,7 +306,7 @@ bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 template <typename T, typename R, typename O>
 cudaError_t launch_fwd_typed(const AddNormArgs& a, int threads, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.width % V == 0 && on16(a.x) && on16(a.residual) && on16(a.out) && on16(a.residual_out);
+    const bool vec = a.width % V == 0 && on16(a.weight) && on16(a.x) && on16(a.residual) && on16(a.out) && on16(a.residual_out);
     const unsigned grid = (unsigned)((a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
     if (vec)
         ssd_add_norm_kernel<T, R, O, V><<<grid, threads, 0, st>>>(a);
@@ -281,10 +324,12 @@ cudaError_t launch_fwd_res(const AddNormArgs& a, int threads, cudaStream_t st) {
 template <typename T, typename R>
 cudaError_t launch_bwd_typed(const AddNormBwdArgs& a, unsigned grid, int threads, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.width % V == 0 && on16(a.dout) && on16(a.h) && on16(a.dres) && on16(a.dx) && on16(a.dres_out);
-    const bool wide = bwd_elems(a.width) > kBwdElems;
-    void (*kern)(AddNormBwdArgs) = vec ? (wide ? ssd_add_norm_bwd_kernel<T, R, V, kElems> : ssd_add_norm_bwd_kernel<T, R, V, kBwdElems>)
-                                       : (wide ? ssd_add_norm_bwd_kernel<T, R, 1, kElems> : ssd_add_norm_bwd_kernel<T, R, 1, kBwdElems>);
+    const bool vec = a.width % V == 0 && on16(a.weight) && on16(a.dout) && on16(a.h) && on16(a.dres) && on16(a.dx) && on16(a.dres_out);
+    const int size = bwd_elems(a.width) > kBwdElems ? 2 : threads > kBwdThreadsSM ? 1 : 0;
+    void (*const kerns[2][3])(AddNormBwdArgs) = {
+        {ssd_add_norm_bwd_kernel<T, R, 1, kBwdElems, kBwdThreadsSM>, ssd_add_norm_bwd_kernel<T, R, 1, kBwdElems, 1024>, ssd_add_norm_bwd_kernel<T, R, 1, kElems, 1024>},
+        {ssd_add_norm_bwd_kernel<T, R, V, kBwdElems, kBwdThreadsSM>, ssd_add_norm_bwd_kernel<T, R, V, kBwdElems, 1024>, ssd_add_norm_bwd_kernel<T, R, V, kElems, 1024>}};
+    void (*kern)(AddNormBwdArgs) = kerns[vec][size];
     kern<<<grid, threads, 0, st>>>(a);
     return cudaGetLastError();
 }
@@ -293,7 +338,7 @@ cudaError_t launch_bwd_typed(const AddNormBwdArgs& a, unsigned grid, int threads
 // dw share sums many rows and the shares stay a few percent of the traffic.
 int64_t bwd_slots(int64_t rows, int width, int* rows_per_cta, int* threads, int64_t* grid) {
     const RowShape s = row_shape(width, rows, bwd_elems(width));
-    const int per_sm = 768 / s.threads > 0 ? 768 / s.threads : 1;
+    const int per_sm = kBwdThreadsSM / s.threads > 0 ? kBwdThreadsSM / s.threads : 1;
     int64_t g = (rows + s.rows_per_cta - 1) / s.rows_per_cta;
     const int64_t most = (int64_t)kAddNormSMs * per_sm;
     if (g > most) g = most;
@@ -333,8 +378,8 @@ cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& args, cudaStream_t st) {
     else
         e = launch_bwd_typed<float, float>(a, (unsigned)grid, threads, st);
     if (e != cudaSuccess) return e;
-    ssd_add_norm_bwd_reduce<<<(unsigned)((a.width + 31) / 32), 1024, 0, st>>>(a.shares, (int)nshares, a.width, a.dweight);
-    return cudaGetLastError();
+    return launch_kernel(ssd_add_norm_bwd_reduce, (unsigned)((a.width + 31) / 32), 1024, 0, st, true, (const float*)a.shares,
+                         (int)nshares, a.width, a.dweight);
 }
 
 }  // namespace ssd
