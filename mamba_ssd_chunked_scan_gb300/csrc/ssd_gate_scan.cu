@@ -7,15 +7,16 @@
 // Each step is an affine map of the state, and the maps of consecutive steps
 // compose: (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2).  The work is cut into tiles of
 // kMain segments of SEG tokens x kCh channels.  One CTA per SM has sixteen main warps, one per segment, a
-// thread holding two channels; two hand-over warps, a thread per channel; and a loading warp:
+// thread holding two channels; three hand-over warps; and a loading warp:
 //   loading    takes the next tile by ticket and brings its inputs into a ring of shared-memory stages (TMA), and
 //              sends a finished tile's outputs off from the same stage.  Where rows are not aligned to 16 bytes
 //              it only takes the tickets, and the main warps load a tile ahead into registers and store directly;
 //   main       forms the next tile's decays and its segment's map, keeping 1 - a in registers; then waits for
 //              the state that enters its segment of the tile before, walks that segment again and writes the
 //              outputs.  So a tile's state has a whole tile's time to arrive;
-//   hand-over  composes the segments' maps to the tile's, publishes it, and works out the state that
-//              enters the tile and from it those that enter the segments.
+//   hand-over  one warp composes the segments' maps to the tile's and publishes it; two (a thread per channel) work out the
+//              state that enters the tile and from it those that enter the segments.  (With one set of warps for both, a
+//              tile's map waited behind the tile before still waiting for its state.)
 // Every input is read from HBM once.  The state that enters a tile follows from the maps of the tiles
 // before it in its block of kScanBlock tiles and from the state that enters the block, which the last tile
 // of the block before publishes: one hand-over per block is a chain, and the order
@@ -48,8 +49,8 @@ namespace ssd {
 namespace {
 
 constexpr int kMain = kScanSegs;       // main warps: segments per tile
-constexpr int kCh = kScanCh;           // channels per tile: two per main thread, one per hand-over thread
-constexpr int kThreads = 32 * (kMain + 2 + 1);
+constexpr int kCh = kScanCh;           // channels per tile: two per main or publishing thread, one per thread that takes states
+constexpr int kThreads = 32 * (kMain + 2 + 1 + 1);
 constexpr int kBlock = kScanBlock;
 static_assert(kCh == 64, "two channels per lane, two hand-over warps");
 
@@ -181,7 +182,8 @@ struct Shared {
     Tile tile[kRing];
     int doc[DOCS ? kRing : 1][DOCS ? TOK + 1 : 1];
     uint64_t full[4], done[4];       // per stage: inputs there; outputs written
-    uint64_t maps[2], states[2];     // of tiles in turn: the segments' maps are in seg; the states that enter them are
+    uint64_t maps[2], told[2], states[2];   // of tiles in turn: the segments' maps are in seg; the tile's is published;
+                                            // the states that enter the segments are in seg
     int abort, never;
 };
 
@@ -296,7 +298,34 @@ __device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared
 
 // ---------------------------------------------------------------------- hand-over warps
 template <bool REV, typename S>
-__device__ __forceinline__ void hand_over(const GateScanArgs& a, S& sh) {
+__device__ __forceinline__ void publish_maps(const GateScanArgs& a, S& sh) {
+    const int lane = threadIdx.x & 31;   // channels 2 * lane, 2 * lane + 1
+    for (int n = 0;; ++n) {
+        if (!bar_wait(sh, a.ws, &sh.maps[n & 1], (n >> 1) & 1, kWhereMaps)) return;
+        const Tile t = sh.tile[n % kRing];
+        if (!t.ntok) return;
+        if (t.step % kBlock != kBlock - 1 && t.step != a.nchunks - 1) {   // another tile of the block needs it
+            float4 q[kMain];
+#pragma unroll
+            for (int k = 0; k < kMain; ++k) q[k] = *reinterpret_cast<const float4*>(&sh.seg[n & 1][REV ? kMain - 1 - k : k][2 * lane]);
+            float A0 = 1.f, B0 = 0.f, A1 = 1.f, B1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMain; ++k) {
+                B0 = fmaf(q[k].x, B0, q[k].y);
+                B1 = fmaf(q[k].z, B1, q[k].w);
+                A0 *= q[k].x;
+                A1 *= q[k].z;
+            }
+            uint64_t* to = a.maps + (((int64_t)t.row * a.ngroups + t.group) * a.nchunks + t.step) * kCh + 2 * lane;
+            leave(to, map_word(A0, B0));
+            leave(to + 1, map_word(A1, B1));
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.told[n & 1]);
+    }
+}
+template <bool REV, typename S>
+__device__ __forceinline__ void take_states(const GateScanArgs& a, S& sh) {
     const int c = threadIdx.x - 32 * kMain, lane = threadIdx.x & 31;   // channel of the tile
     for (int n = 0;; ++n) {
         if (!bar_wait(sh, a.ws, &sh.maps[n & 1], (n >> 1) & 1, kWhereMaps)) return;
@@ -304,20 +333,11 @@ __device__ __forceinline__ void hand_over(const GateScanArgs& a, S& sh) {
         float2 (*seg)[kCh] = sh.seg[n & 1];
         if (!t.ntok) return;
         const int ch = t.group * kCh + c;
-        float2 m[kMain];
-        float A = 1.f, B = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMain; ++k) {
-            m[k] = seg[REV ? kMain - 1 - k : k][c];
-            B = fmaf(m[k].x, B, m[k].y);
-            A *= m[k].x;
-        }
         const int in_block = t.step % kBlock, block = t.step / kBlock;
         const bool more = t.step != a.nchunks - 1, closes = in_block == kBlock - 1;
         const int64_t line = (int64_t)t.row * a.ngroups + t.group;
         uint64_t* maps = a.maps + (line * a.nchunks + (int64_t)block * kBlock) * kCh + c;
         uint64_t* carry = a.carry + (line * a.nblocks + block) * kCh + c;
-        if (more && !closes) leave(maps + in_block * kCh, map_word(A, B));
         // the predecessors' maps and the block's state: all that are missing are asked for at once, so a
         // round takes one trip to L2 however many there are
         uint64_t w[kBlock - 1], cw = 1;
@@ -347,6 +367,10 @@ __device__ __forceinline__ void hand_over(const GateScanArgs& a, S& sh) {
 #pragma unroll
         for (int p = 0; p < kBlock - 1; ++p)
             if (p < in_block) h = fmaf(__uint_as_float((uint32_t)w[p] & 0x7FFFFFFFu), h, __uint_as_float((uint32_t)(w[p] >> 32)));
+        float2 m[kMain];
+#pragma unroll
+        for (int k = 0; k < kMain; ++k) m[k] = seg[REV ? kMain - 1 - k : k][c];
+        if (!bar_wait(sh, a.ws, &sh.told[n & 1], (n >> 1) & 1, kWhereMaps)) return;   // the maps have been read
 #pragma unroll
         for (int k = 0; k < kMain; ++k) {
             seg[REV ? kMain - 1 - k : k][c].x = h;
@@ -727,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh.maps[i], kMain);
+            ptx::mbar_init(&sh.told[i], 1);
             ptx::mbar_init(&sh.states[i], 2);
         }
         sh.abort = 0;
@@ -738,7 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
         Main<T, ROWS, DOCS, BWD> m = {p.a, sh, (int)(threadIdx.x & 31), warp};
         m.run(sm);
     } else if (warp < kMain + 2) {
-        hand_over<BWD>(p.a, sh);
+        take_states<BWD>(p.a, sh);
+    } else if (warp == kMain + 2) {
+        publish_maps<BWD>(p.a, sh);
     } else {
         if (DOCS && blockIdx.x == 0) check_cu_seqlens(p.a.cu, p.a.ndocs, p.a.seqlen, p.a.ws, threadIdx.x & 31, 32);
         loading<T, ROWS, DOCS, BWD>(p, sm, sh);
