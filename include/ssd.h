@@ -339,7 +339,8 @@ SSD_API size_t ssd_linear_bwd_workspace_size(const ssd_linear_params_t* p);
  *   y         (m, n) bf16, contiguous
  *   pre       (m, n) bf16, or NULL: v, rounded
  * Sums are fp32 and y is rounded once.  `workspace`: ssd_linear_workspace_size(p) bytes, 256-byte
- * aligned; needs no initialisation; calls that share it must be ordered on one stream.  One launch, or two where
+ * aligned; needs no initialisation; calls that share it must be ordered on one stream; where the size is 256 (only
+ * the status word) it may be NULL, and nothing is recorded.  One launch, or two where
  * the contraction is split over CTAs.  The device waits are bounded: one that runs out records
  * SSD_ERR_TIMEOUT (where 61-65: stage free, stage loaded, accumulator free, accumulator done, drain) in the status word,
  * which each call clears, read by ssd_check_status().  Bitwise deterministic. */
@@ -391,7 +392,7 @@ SSD_API size_t ssd_gate_scan_workspace_size(const ssd_gate_scan_params_t* p);
  * The state is fp32 throughout; y is rounded once.  No output may overlap an input.
  * `workspace`: at least ssd_gate_scan_workspace_size(p) bytes, 256-byte aligned (else
  * SSD_ERR_WORKSPACE); it needs no initialisation, and calls that share it must be ordered on one
- * stream.  A clear of it (status word, tickets, states on their way) and one launch, asynchronous on `stream`; it
+ * stream; where the size is 256 (only the status word) it may be NULL, and nothing is recorded.  A clear of it (status word, tickets, states on their way) and one launch, asynchronous on `stream`; it
  * can be captured in a CUDA graph.  Tiles of a sequence hand their states on through the workspace; every wait is
  * bounded, and one that runs out records SSD_ERR_TIMEOUT (where 51: a tile's map, 52: a block's
  * state, 53-56: waits inside a CTA) in the status word read by ssd_check_status(), as offsets that break their rule

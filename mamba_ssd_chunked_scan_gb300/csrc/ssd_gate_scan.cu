@@ -39,6 +39,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ssd_common.cuh"
 #include "ssd_kernels.h"
@@ -117,11 +118,13 @@ struct ScanParams {
     GateScanArgs a;
 };
 
-struct Tile {
+struct alignas(16) Tile {
     int row, group;        // batch row, channel group
     int step;              // place in the walk of its sequence
     int ntok;              // its tokens; 0: no tile is left
     int64_t t0;            // its first token
+    // elements from the start of g, of x, and of a contiguous operand to the tile's first
+    int64_t og, ox, oy;
 };
 
 template <bool REV, int TOK>
@@ -134,6 +137,10 @@ __device__ __forceinline__ Tile tile_of(const GateScanArgs& a, uint32_t k) {
     t.step = (int)c;
     t.t0 = (REV ? a.nchunks - 1 - c : c) * TOK;
     t.ntok = k < a.ntiles ? (int)(a.seqlen - t.t0 < TOK ? a.seqlen - t.t0 : TOK) : 0;
+    const int64_t tok = (int64_t)t.row * a.seqlen + t.t0;
+    t.og = tok * a.g_stride + t.group * kCh;
+    t.ox = tok * a.x_stride + t.group * kCh;
+    t.oy = tok * a.width + t.group * kCh;
     return t;
 }
 
@@ -438,6 +445,12 @@ struct Main {
             return v;
         }
     }
+    // The segment's first row of an operand, at the thread's channels; `at`: the tile's offset in it.
+    template <typename P>
+    __device__ __forceinline__ auto mine(P* base, int64_t at, int64_t pitch) const {
+        typedef typename std::conditional<std::is_const<P>::value, const T, T>::type E;
+        return static_cast<E*>(base) + at + (uint64_t)(uint32_t)s0 * (uint32_t)pitch + lane;
+    }
     // ROWS: row k, `pitch` bytes apart, from p (one multiply-add: 64-bit sums would cost two instructions a row)
     template <typename P>
     static __device__ __forceinline__ P* row(P* p, int k, uint32_t pitch) {
@@ -460,10 +473,9 @@ struct Main {
     }
     template <bool ALL>
     __device__ __forceinline__ void fetch_all() {
-        const int64_t tok = (int64_t)t.row * a.seqlen + t.t0 + s0;
-        const T* g = static_cast<const T*>(a.g) + tok * a.g_stride + c0;
-        const T* x = static_cast<const T*>(a.x) + tok * a.x_stride + c0;
-        const T* dy = static_cast<const T*>(a.dy) + tok * a.width + c0;
+        const T* g = mine(a.g, t.og, a.g_stride);
+        const T* x = mine(a.x, t.ox, a.x_stride);
+        const T* dy = mine(a.dy, t.oy, a.width);
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             const bool in = s0 + k < t.ntok;
@@ -472,7 +484,7 @@ struct Main {
             if constexpr (BWD) raw[2][k] = fetch<ALL>(row(dy, k, (uint32_t)a.width * H::ES), in);
         }
         // the h before the segment: the output before it
-        if constexpr (BWD) hraw = fetch<false>(static_cast<const T*>(a.y) + (tok - 1) * a.width + c0, s0 < t.ntok && t.t0 + s0 > 0);
+        if constexpr (BWD) hraw = fetch<false>(mine(a.y, t.oy, a.width) - a.width, s0 < t.ntok && t.t0 + s0 > 0);
     }
     static __device__ __forceinline__ f2 widen(Pair p) {
         if constexpr (sizeof(T) == 2) return pk(__uint_as_float(p.lo << 16), __uint_as_float(p.hi << 16));
@@ -512,9 +524,6 @@ struct Main {
             if (ALL || ok0) q[0] = f.x;
             if (ALL || ok1) q[kApart] = f.y;
         }
-    }
-    __device__ __forceinline__ T* mine(void* base, int64_t pitch) const {
-        return static_cast<T*>(base) + ((int64_t)t.row * a.seqlen + t.t0 + s0) * pitch + c0;
     }
     // two channels of row `row` of a (rows, width) fp32 array, zero without one
     __device__ __forceinline__ f2 state(const float* p, int64_t row) const {
@@ -618,7 +627,7 @@ struct Main {
     __device__ __forceinline__ void second_fwd(const Keep& q) {
         f2 h = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
-        T* y = mine(a.y, a.width);
+        T* y = mine(a.y, t.oy, a.width);
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
@@ -672,7 +681,7 @@ struct Main {
     __device__ __forceinline__ void second_bwd(const Keep& q) {
         f2 mu = entered();
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
-        T *dg = mine(a.dg, a.g_stride), *dx = mine(a.dx, a.x_stride);
+        T *dg = mine(a.dg, t.og, a.g_stride), *dx = mine(a.dx, t.ox, a.x_stride);
 #pragma unroll
         for (int k = SEG - 1; k >= 0; --k) {
             if (!PLAIN && s0 + k >= t.ntok) continue;
@@ -902,7 +911,7 @@ cudaError_t launch_gate_scan(const GateScanArgs& args, void* workspace, bool bwd
     a.maps = reinterpret_cast<uint64_t*>(w + l.maps_off);
     a.carry = reinterpret_cast<uint64_t*>(w + l.carry_off);
     // status word, tickets, maps and carried states start from zero
-    const cudaError_t e = cudaMemsetAsync(workspace, 0, l.total, st);
+    const cudaError_t e = workspace ? cudaMemsetAsync(workspace, 0, l.total, st) : cudaSuccess;
     if (e != cudaSuccess) return e;
     if (a.dtype == SSD_BF16) return bwd ? launch_typed<bf16_t, true>(a, rows, st) : launch_typed<bf16_t, false>(a, rows, st);
     return bwd ? launch_typed<float, true>(a, rows, st) : launch_typed<float, false>(a, rows, st);

@@ -20,6 +20,12 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 // Overlap other than being the same array with elements of the same size.
 bool clash(const void* a, size_t na, const void* b, size_t nb) { return overlap(a, na, b, nb) && !(a == b && na == nb); }
 
+// A workspace of `need` bytes, 256-byte aligned; none where only the status word would be in it (a wait that runs out is
+// then not reported).
+bool workspace_ok(const void* ws, size_t bytes, size_t need) {
+    return ws ? bytes >= need && aligned(ws, 256) : need == sizeof(WsHeader);
+}
+
 // Types and width of the residual norm; SSD_OK or the status to return.
 int check_norm(int64_t rows, int32_t width, int32_t dtype, int32_t residual_dtype) {
     if (rows < 0 || width < 1) return SSD_ERR_INVALID_ARG;
@@ -196,7 +202,7 @@ int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x,
         !aligned(final_states, 4) || !aligned(cu_seqlens, 4))
         return SSD_ERR_INVALID_ARG;
     const size_t need = ssd_gate_scan_workspace_size(p);
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
     const int64_t rows = p->batch * p->seqlen, nst = p->ndocs > 0 ? p->ndocs : p->batch;
     const Mat in[] = {{g, rows, p->width, p->g_stride, es}, {x, rows, p->width, p->x_stride, es},
                       {initial_states, nst, p->width, p->width, 4}, {cu_seqlens, 1, p->ndocs + 1, p->ndocs + 1, 4}};
@@ -229,7 +235,7 @@ int ssd_gate_scan_bwd(const ssd_gate_scan_params_t* p, const void* g, const void
         !aligned(cu_seqlens, 4))
         return SSD_ERR_INVALID_ARG;
     const size_t need = ssd_gate_scan_workspace_size(p);
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
     const int64_t rows = p->batch * p->seqlen, nst = p->ndocs > 0 ? p->ndocs : p->batch;
     const int64_t w = p->width;
     const Mat in[] = {{g, rows, w, p->g_stride, es}, {x, rows, w, p->x_stride, es}, {y, rows, w, w, es}, {dy, rows, w, w, es},
@@ -298,7 +304,7 @@ int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* w, const
     const size_t es = elem(p->dtype);
     const LinearPlan plan = linear_plan(p->m, p->n, (int64_t)p->k * es, true);
     const size_t need = sizeof(WsHeader) + plan.parts_bytes;
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
     const Mat in[] = {{x, p->m, p->k, p->ldx, es}, {w, p->n, p->k, p->k, es}, {x_scales, 1, p->m, p->m, 4},
                       {w_scales, 1, p->n, p->n, 4}, {bias, 1, p->n, p->n, 4}};
     const Mat my = {y, p->m, p->n, p->n, 2}, mp = {pre, p->m, p->n, p->n, 2}, mr = {residual, p->m, p->n, p->n, 2},
@@ -314,7 +320,7 @@ int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* w, const
     a.w = {w, p->k, false};
     a.x_scales = x_scales; a.w_scales = w_scales; a.bias = bias; a.residual = residual; a.y = y; a.pre = pre;
     a.ws = (WsHeader*)workspace;
-    a.parts = (float*)((char*)workspace + sizeof(WsHeader));
+    a.parts = workspace ? (float*)((char*)workspace + sizeof(WsHeader)) : nullptr;
     return launch_linear(a, plan, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

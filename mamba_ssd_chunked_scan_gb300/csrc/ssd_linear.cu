@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     const int rank = PAIR ? (int)cluster_rank() : 0;
     const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
     if (threadIdx.x == 0) {
-        if (blockIdx.x == 0 && !a.keep_status) a.ws->status = 0;   // a wait gives up after seconds, long after this
+        if (blockIdx.x == 0 && a.ws && !a.keep_status) a.ws->status = 0;   // a wait gives up after seconds, long after this
         for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(&sh.full[i], 1);
             ptx::mbar_init(&sh.empty[i], 1);

@@ -54,6 +54,16 @@ def _need(name, t, dtype, shape, dev):
         raise _wrong(name, t, dtype, shape, dev)
 
 
+_STATUS_ONLY = 256   # a workspace that holds only the status word
+
+
+def _workspace(nbytes, device, check_status):
+    """A call's workspace, or None where it would hold only a status word that nobody reads."""
+    if nbytes == _STATUS_ONLY and not check_status:
+        return None
+    return _empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -221,10 +231,10 @@ def linear(x, w, bias=None, residual=None, *, act="none", x_scales=None, w_scale
         raise _lib.SSDError(2, f"linear of {tuple(x.shape)} and {tuple(w.shape)}, row stride {p.ldx}")
     y = _empty(out_shape, dtype=_BF16, device=device)
     pre = _empty(out_shape, dtype=_BF16, device=device) if return_pre else None
-    ws = _empty(nbytes, dtype=torch.uint8, device=device)
+    ws = _workspace(nbytes, device, check_status)
     st = _raw_stream(dev)
     rc = _lib_c.ssd_linear(ref, x.data_ptr(), w.data_ptr(), _ptr(x_scales), _ptr(w_scales), _ptr(bias), _ptr(residual),
-                           y.data_ptr(), _ptr(pre), ws.data_ptr(), nbytes, st)
+                           y.data_ptr(), _ptr(pre), _ptr(ws), nbytes, st)
     if rc:
         _check(rc, "ssd_linear")
     if check_status and p.m:
@@ -320,10 +330,10 @@ def gate_scan(g, x, initial_states=None, cu_seqlens=None, *, return_final_states
     device = g.device
     y = _empty(g.shape, dtype=g.dtype, device=device)
     fin = _empty(states, dtype=_F32, device=device) if return_final_states else None
-    ws = _empty(nbytes, dtype=torch.uint8, device=device)
+    ws = _workspace(nbytes, device, check_status)
     st = _raw_stream(dev)
     rc = _lib_c.ssd_gate_scan(ref, g.data_ptr(), x.data_ptr(), _ptr(initial_states), _ptr(cu_seqlens), y.data_ptr(), _ptr(fin),
-                              ws.data_ptr(), nbytes, st)
+                              _ptr(ws), nbytes, st)
     if rc:
         _check(rc, "ssd_gate_scan")
     if check_status:
@@ -366,10 +376,10 @@ def gate_scan_bwd(g, x, y, dy, initial_states=None, dfinal_states=None, cu_seqle
     if dx is None:
         dx = _like_rows(x, p.x_stride)
     dinit = _empty(states, dtype=_F32, device=g.device) if want_dinit else None
-    ws = _empty(nbytes, dtype=torch.uint8, device=g.device)
+    ws = _workspace(nbytes, g.device, check_status)
     st = _raw_stream(dev)
     rc = _lib_c.ssd_gate_scan_bwd(ref, g.data_ptr(), x.data_ptr(), y.data_ptr(), _ptr(initial_states), _ptr(cu_seqlens),
-                                  dy.data_ptr(), _ptr(dfinal_states), dg.data_ptr(), dx.data_ptr(), _ptr(dinit), ws.data_ptr(),
+                                  dy.data_ptr(), _ptr(dfinal_states), dg.data_ptr(), dx.data_ptr(), _ptr(dinit), _ptr(ws),
                                   nbytes, st)
     if rc:
         _check(rc, "ssd_gate_scan_bwd")

@@ -164,12 +164,20 @@ def lin(L, p=None, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), 1), (dict(w=None), 1), (dict(y=None), 1), (dict(x=G + 8), 1), (dict(w=2 * G + 2), 1), (dict(bias=3 * G + 2), 1),
-    (dict(y=5 * G + 1), 1), (dict(xs=8 * G), 1), (dict(xs=8 * G, ws=9 * G), 1), (dict(work=None), 3), (dict(wb=64), 3),
+    (dict(y=5 * G + 1), 1), (dict(xs=8 * G), 1), (dict(xs=8 * G, ws=9 * G), 1), (dict(wb=64), 3),
     (dict(work=7 * G + 16), 3), (dict(y=G), 1), (dict(y=2 * G + 2), 1), (dict(y=6 * G), 1), (dict(pre=4 * G), 1), (dict(y=4 * G + 2), 1),
     (dict(y=7 * G), 1), (dict(pre=3 * G), 1), (dict(res=7 * G), 1),
 ])
 def test_linear_refusals(L, kw, code):
     assert lin(L, **kw) == code
+
+
+def test_linear_workspace_missing(L):
+    """Only a workspace that would hold no more than the status word may be left out (this product's parts need one)."""
+    p = linear_params(m=8, n=2560, k=5120, ldx=5120)
+    assert L.ssd_linear_workspace_size(p) > 256
+    assert lin(L, p, work=None) == 3
+    assert L.ssd_linear_workspace_size(linear_params()) == 256
 
 
 def test_linear_scales_come_with_e4m3(L):
