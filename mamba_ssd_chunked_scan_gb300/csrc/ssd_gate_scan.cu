@@ -109,7 +109,7 @@ struct Shape {
     static constexpr int STAGE = NA * ARR + (BWD ? kMain * PITCH : 0);   // and, backwards, the h before each segment
     static constexpr int NS = ROWS || 4 * STAGE <= 212 * 1024 ? 4 : 3;
     // ROWS: what the first visits of two tiles keep for the second, per token and thread
-    static constexpr int kKeep = 2 * SEG * 32 * kMain * (8 + (BWD ? 8 : 0) + 2 * ES);
+    static constexpr int kKeep = 2 * SEG * 32 * kMain * 8 * (BWD ? 3 : 2);
     static constexpr size_t kSmem = 128 + (ROWS ? (size_t)kKeep : (size_t)NS * STAGE);
 };
 
@@ -456,19 +456,24 @@ struct Main {
     static __device__ __forceinline__ P* row(P* p, int k, uint32_t pitch) {
         return reinterpret_cast<P*>(reinterpret_cast<uint64_t>(p) + (uint64_t)(uint32_t)k * pitch);
     }
+    // One element's bits, straight into and out of a 32-bit register (16-bit values of the language pass through
+    // conversions first).
+    static __device__ __forceinline__ uint32_t element(const T* q) {
+        uint32_t v;
+        if constexpr (sizeof(T) == 2) asm volatile("ld.global.cs.u16 %0, [%1];" : "=r"(v) : "l"(q));
+        else asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(v) : "l"(q));
+        return v;
+    }
+    static __device__ __forceinline__ void put_element(T* q, uint32_t v) {
+        if constexpr (sizeof(T) == 2) asm volatile("st.global.u16 [%0], %1;" ::"l"(q), "r"(v) : "memory");
+        else asm volatile("st.global.u32 [%0], %1;" ::"l"(q), "r"(v) : "memory");
+    }
     // ROWS: the thread's two elements in one row.  ALL: both exist.
     template <bool ALL>
     __device__ __forceinline__ Pair fetch(const T* q, bool in) const {
         Pair p = {0u, 0u};
-        if constexpr (sizeof(T) == 2) {
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
-            if (ALL || (in && ok0)) p.lo = __ldcs(e);
-            if (ALL || (in && ok1)) p.hi = __ldcs(e + kApart);
-        } else {
-            const uint32_t* e = reinterpret_cast<const uint32_t*>(q);
-            if (ALL || (in && ok0)) p.lo = __ldcs(e);
-            if (ALL || (in && ok1)) p.hi = __ldcs(e + kApart);
-        }
+        if (ALL || (in && ok0)) p.lo = element(q);
+        if (ALL || (in && ok1)) p.hi = element(q + kApart);
         return p;
     }
     template <bool ALL>
@@ -514,15 +519,19 @@ struct Main {
         const W w = narrow(v);
         if constexpr (!ROWS) {
             *reinterpret_cast<W*>(st + r * H::ARR + k * H::PITCH) = w;
-        } else if constexpr (sizeof(T) == 2) {
-            uint16_t* q = reinterpret_cast<uint16_t*>(row(base, k, (uint32_t)pitch * H::ES));
-            if (ALL || ok0) q[0] = (uint16_t)w;
-            if (ALL || ok1) q[kApart] = (uint16_t)(w >> 16);
         } else {
             T* q = row(base, k, (uint32_t)pitch * H::ES);
-            const float2 f = un(w);
-            if (ALL || ok0) q[0] = f.x;
-            if (ALL || ok1) q[kApart] = f.y;
+            uint32_t lo, hi;
+            if constexpr (sizeof(T) == 2) {
+                lo = w;
+                hi = w >> 16;
+            } else {
+                const float2 f = un(w);
+                lo = __float_as_uint(f.x);
+                hi = __float_as_uint(f.y);
+            }
+            if (ALL || ok0) put_element(q, lo);
+            if (ALL || ok1) put_element(q + kApart, hi);
         }
     }
     // two channels of row `row` of a (rows, width) fp32 array, zero without one
@@ -563,7 +572,7 @@ struct Main {
     }
 
     // What the first visit keeps for the second: m = 1 - a and, backwards, u = d(h_t)/d(g_t), in registers beside
-    // the operands in the stage; ROWS: in shared memory, with the operand that the second visit needs (r).
+    // the operands in the stage; ROWS: in shared memory, with what else the second visit needs (m x forwards, dy backwards).
     struct Keep {
         f2 m[ROWS ? 1 : SEG], u[BWD && !ROWS ? SEG : 1];
         uint8_t* at;
@@ -588,18 +597,11 @@ struct Main {
         if constexpr (ROWS) return *reinterpret_cast<const f2*>(q.at + kSlots + k * 32 * kMain * 8);
         else return q.u[k];
     }
-    __device__ __forceinline__ W* kept_at(const Keep& q, int k) const {
-        uint8_t* base = q.at - (warp * 32 + lane) * 8 + (BWD ? 2 : 1) * kSlots;
-        return reinterpret_cast<W*>(base) + k * 32 * kMain + warp * 32 + lane;
+    __device__ __forceinline__ void set_r(Keep& q, int k, f2 v) const {
+        if constexpr (ROWS) *reinterpret_cast<f2*>(q.at + (BWD ? 2 : 1) * kSlots + k * 32 * kMain * 8) = v;
     }
-    __device__ __forceinline__ void set_r(Keep& q, int k, Pair p) const {
-        if constexpr (!ROWS) return;
-        else if constexpr (sizeof(T) == 2) *kept_at(q, k) = p.lo | (p.hi << 16);
-        else *kept_at(q, k) = widen(p);
-    }
-    __device__ __forceinline__ f2 kept(const Keep& q, int k) const {
-        if constexpr (ROWS) return widen(*kept_at(q, k));
-        else return in(BWD ? 2 : 1, k);
+    __device__ __forceinline__ f2 get_r(const Keep& q, int k) const {
+        return *reinterpret_cast<const f2*>(q.at + (BWD ? 2 : 1) * kSlots + k * 32 * kMain * 8);
     }
 
     // PLAIN: every token of the segment is inside the sequence, and no document starts or ends in it
@@ -616,9 +618,10 @@ struct Main {
                 B = state(a.init, doc[s0 + k]);
             }
             A = mul(A, av);
-            B = fma2(av, B, mul(mv, in(1, k)));
+            const f2 b = mul(mv, in(1, k));
+            B = fma2(av, B, b);
             set_m(q, k, mv);
-            set_r(q, k, raw[ROWS ? 1 : 0][ROWS ? k : 0]);
+            set_r(q, k, b);
         }
         put_map(A, B);
     }
@@ -633,7 +636,10 @@ struct Main {
             if (!PLAIN && s0 + k >= t.ntok) break;
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
             const f2 mv = get_m(q, k);
-            h = fma2(fma2(mv, minus, one), h, mul(mv, kept(q, k)));
+            f2 b;
+            if constexpr (ROWS) b = get_r(q, k);
+            else b = mul(mv, in(1, k));
+            h = fma2(fma2(mv, minus, one), h, b);
             put<ALL>(1, y, a.width, k, h);
             if (DOCS && !PLAIN && a.leave && ends(k)) {
                 const int at = ending(k);
@@ -659,7 +665,7 @@ struct Main {
             set_u(q, k, mul(fma2(xv, minus, h), mul(av, mv)));
             set_m(q, k, mv);
             h = fma2(av, h, mul(mv, xv));
-            set_r(q, k, raw[ROWS ? 2 : 0][ROWS ? k : 0]);
+            if constexpr (ROWS) set_r(q, k, in(2, k));
         }
         // backwards: the map of mu over the segment
         f2 A = one, B = pk(0.f, 0.f);
@@ -689,7 +695,9 @@ struct Main {
                 const int at = ending(k);
                 mu = at >= 0 ? state(a.enter, at) : pk(0.f, 0.f);
             }
-            const f2 lam = add(kept(q, k), mu);
+            f2 lam;
+            if constexpr (ROWS) lam = add(get_r(q, k), mu);
+            else lam = add(in(2, k), mu);
             const f2 mv = get_m(q, k);
             put<ALL>(0, dg, a.g_stride, k, mul(lam, get_u(q, k)));
             put<ALL>(1, dx, a.x_stride, k, mul(lam, mv));
