@@ -144,13 +144,27 @@ __device__ __forceinline__ Tile tile_of(const GateScanArgs& a, uint32_t k) {
     return t;
 }
 
+// A document's state rows (the group's channels) on their way to L2 when its tile is found, a tile or more before they are
+// needed: a segment that fetches one from HBM holds up its tile, and the tiles behind it, for a microsecond.
+__device__ __forceinline__ void expect_state(const float* p, const GateScanArgs& a, int64_t row, int group) {
+    if (!p || row < 0) return;
+    p += row * a.width + group * kCh;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    if (group * kCh + 32 < a.width) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 32));
+}
+
 // Documents that start inside a tile, or at the token after it: doc[k] = the
 // document that starts at token t0 + k, or -1.  One warp; offsets outside the tile are skipped,
 // so nothing they hold can index out of bounds.  Tiles come in the order of the sequence: the 32 offsets about
 // where the last tile's were found (`near`) mostly hold all that this one needs, in one load.  Returns the next `near`.
 template <int TOK, bool REV>
-__device__ int find_docs(const GateScanArgs& a, int64_t t0, int near, int* doc) {
+__device__ int find_docs(const GateScanArgs& a, int64_t t0, int group, int near, int* doc) {
     const int lane = threadIdx.x & 31;
+    auto found = [&](int64_t k, int d) {
+        doc[k] = d;
+        expect_state(a.init, a, d, group);
+        if (REV) expect_state(a.enter, a, d - 1, group);   // what enters at the end of the document before
+    };
     for (int k = lane; k <= TOK; k += 32) doc[k] = -1;
     int lo = near - (REV ? 24 : 4);
     if (lo < 0) lo = 0;
@@ -159,7 +173,7 @@ __device__ int find_docs(const GateScanArgs& a, int64_t t0, int near, int* doc) 
     const bool from = lo == 0 || __shfl_sync(0xffffffffu, k, 0) < 0, to = __shfl_sync(0xffffffffu, k, 31) > TOK;
     __syncwarp();
     if (from && to) {
-        if (k >= 0 && k <= TOK) doc[k] = lo + lane;
+        if (k >= 0 && k <= TOK) found(k, lo + lane);
         return lo + __popc(__ballot_sync(0xffffffffu, k < 0));
     }
     // the first document whose offset is >= t0, 32 probes at a time
@@ -176,7 +190,7 @@ __device__ int find_docs(const GateScanArgs& a, int64_t t0, int near, int* doc) 
     }
     for (int d = lo; d < a.ndocs; d += 32) {
         k = d + lane < a.ndocs ? (int64_t)__ldg(a.cu + d + lane) - t0 : kNone;
-        if (k >= 0 && k <= TOK) doc[k] = d + lane;
+        if (k >= 0 && k <= TOK) found(k, d + lane);
         if (__all_sync(0xffffffffu, k > TOK)) break;
     }
     return lo;
@@ -258,7 +272,7 @@ __device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared
         const Tile t = tile_of<BWD, H::TOK>(a, k);
         // the slot's last tile, n - kRing, is done with: a later one's outputs have been waited for
         if (lane == 0) sh.tile[n % kRing] = t;
-        if (DOCS && t.ntok) near = find_docs<H::TOK, BWD>(a, t.t0, near, sh.doc[n % kRing]);
+        if (DOCS && t.ntok) near = find_docs<H::TOK, BWD>(a, t.t0, t.group, near, sh.doc[n % kRing]);
         const int st = n % H::NS;
         if (n >= H::NS) {
             if (lane == 0) {
