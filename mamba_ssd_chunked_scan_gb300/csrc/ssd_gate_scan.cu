@@ -423,6 +423,8 @@ struct Main {
     int s0, c0;        // the segment's first token in the tile; the thread's first channel
     bool ok0, ok1;
     bool plain;        // the segment is inside the sequence, and no document starts or ends in it
+    uint32_t marks;    // bit k: a document starts at the segment's token k (SEG: at the token after it)
+    int final;         // the sequence's last token, counted from the segment's first
     // ROWS: the operands of the tile to come, and the h before its segment, as loaded (nothing touches them
     // before the tile's first visit, so they arrive during the second visit of the tile before)
     struct Pair {
@@ -442,8 +444,9 @@ struct Main {
         st = sm + (n % H::NS) * H::STAGE + s0 * H::PITCH + 2 * lane * H::ES;
         plain = s0 + SEG <= t.ntok;
         if (DOCS) {
-            const bool event = lane <= SEG && s0 + lane <= H::TOK && doc[s0 + lane] >= 0;
-            plain = !__any_sync(0xffffffffu, event) && t.t0 + s0 + SEG < a.seqlen;
+            marks = __ballot_sync(0xffffffffu, lane <= SEG && doc[s0 + lane] >= 0);
+            final = a.seqlen - t.t0 < H::TOK + 1 ? (int)(a.seqlen - t.t0) - 1 - s0 : H::TOK + 1;
+            plain = marks == 0 && final >= SEG;
         }
     }
     static __device__ __forceinline__ f2 widen(W w) {
@@ -576,14 +579,10 @@ struct Main {
         const float4 e = *reinterpret_cast<const float4*>(q + 2 * lane);
         return pk(e.x, e.z);
     }
-    __device__ __forceinline__ bool starts(int k) const { return DOCS && doc[s0 + k] >= 0; }
+    __device__ __forceinline__ bool starts(int k) const { return DOCS && (marks >> k & 1); }
     // whether token k of the segment ends a document, and which
-    __device__ __forceinline__ bool ends(int k) const {
-        return DOCS && (doc[s0 + k + 1] >= 0 || t.t0 + s0 + k == a.seqlen - 1);
-    }
-    __device__ __forceinline__ int ending(int k) const {
-        return t.t0 + s0 + k == a.seqlen - 1 ? a.ndocs - 1 : doc[s0 + k + 1] - 1;
-    }
+    __device__ __forceinline__ bool ends(int k) const { return DOCS && ((marks >> (k + 1) & 1) || k == final); }
+    __device__ __forceinline__ int ending(int k) const { return k == final ? a.ndocs - 1 : doc[s0 + k + 1] - 1; }
 
     // What the first visit keeps for the second: m = 1 - a and, backwards, u = d(h_t)/d(g_t), in registers beside
     // the operands in the stage; ROWS: in shared memory, with what else the second visit needs (m x forwards, dy backwards).
