@@ -2,6 +2,7 @@
 //   ssd_gate_scan_kernel<fwd>  h_t = a_t h_{t-1} + (1 - a_t) x_t,  a_t = 1 / (1 + exp(-g_t)),  y = h
 //   ssd_gate_scan_kernel<bwd>  lam_t = dy_t + a_{t+1} lam_{t+1};  dx = (1 - a) lam,
 //                              dg = lam (h_{t-1} - x) a (1 - a),  dinit = a_1 lam_1
+//   ssd_gate_scan_clear        the workspace's words to zero, which the other two start from
 //   ssd_gate_scan_step_kernel  one token from a resident state
 //
 // Each step is an affine map of the state, and the maps of consecutive steps
@@ -789,6 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
         ptx::mbar_fence_init();
     }
     __syncthreads();
+    // The workspace is being cleared by the launch before, which this one does not wait for to start: whoever uses the
+    // workspace does.  (What earlier work left for this call is there: the clearing waited for it.)
+    if (warp >= kMain) pdl_wait();
     if (warp < kMain) {
         Main<T, ROWS, DOCS, BWD> m = {p.a, sh, (int)(threadIdx.x & 31), warp};
         m.run(sm);
@@ -800,6 +804,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
         if (DOCS && blockIdx.x == 0) check_cu_seqlens(p.a.cu, p.a.ndocs, p.a.seqlen, p.a.ws, threadIdx.x & 31, 32);
         loading<T, ROWS, DOCS, BWD>(p, sm, sh);
     }
+}
+
+__global__ void __launch_bounds__(256) ssd_gate_scan_clear(uint4* p, size_t words) {
+    pdl_trigger();
+    for (size_t k = (size_t)blockIdx.x * 256 + threadIdx.x; k < words; k += (size_t)gridDim.x * 256) p[k] = make_uint4(0, 0, 0, 0);
 }
 
 // One token per batch row: V channels per thread.
@@ -864,8 +873,7 @@ cudaError_t launch_one(const ScanParams& p, cudaStream_t st) {
     // one CTA per SM; with tickets any number of them finishes the work
     const int nsm = device_sms();
     const uint32_t most = nsm > 0 ? nsm : 152;
-    kern<<<p.a.ntiles < most ? p.a.ntiles : most, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(kern, p.a.ntiles < most ? p.a.ntiles : most, kThreads, smem, st, p.a.ws != nullptr, p);
 }
 
 template <typename T, bool BWD>
@@ -889,6 +897,9 @@ cudaError_t launch_typed(const GateScanArgs& a, bool rows, cudaStream_t st) {
 bool aligned_rows(const GateScanArgs& a, bool bwd) {
     const int unit = a.dtype == SSD_BF16 ? 8 : 4;
     if (a.width % unit || a.g_stride % unit || a.x_stride % unit || !on(a.g, 16) || !on(a.x, 16) || !on(a.y, 16)) return false;
+    // a tensor map's strides are below 2^40 bytes
+    const int64_t most = ((int64_t)1 << 40) / a.seqlen / 4;
+    if (a.g_stride >= most || a.x_stride >= most) return false;
     return !bwd || (on(a.dy, 16) && on(a.dg, 16) && on(a.dx, 16));
 }
 
@@ -932,8 +943,12 @@ cudaError_t launch_gate_scan(const GateScanArgs& args, void* workspace, bool bwd
     a.maps = reinterpret_cast<uint64_t*>(w + l.maps_off);
     a.carry = reinterpret_cast<uint64_t*>(w + l.carry_off);
     // status word, tickets, maps and carried states start from zero
-    const cudaError_t e = workspace ? cudaMemsetAsync(workspace, 0, l.total, st) : cudaSuccess;
-    if (e != cudaSuccess) return e;
+    if (workspace) {
+        const size_t words = l.total / 16, ctas = (words + 1023) / 1024;
+        ssd_gate_scan_clear<<<(unsigned)(ctas < 304 ? ctas : 304), 256, 0, st>>>(static_cast<uint4*>(workspace), words);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     if (a.dtype == SSD_BF16) return bwd ? launch_typed<bf16_t, true>(a, rows, st) : launch_typed<bf16_t, false>(a, rows, st);
     return bwd ? launch_typed<float, true>(a, rows, st) : launch_typed<float, false>(a, rows, st);
 }

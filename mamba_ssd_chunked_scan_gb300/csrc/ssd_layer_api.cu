@@ -350,7 +350,8 @@ int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, c
             if (touch(out[i], out[j])) return SSD_ERR_INVALID_ARG;
     }
     char* ws = (char*)workspace;
-    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return SSD_ERR_CUDA;
+    // the first product clears the status word
+    if (!dx && !dw && cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return SSD_ERR_CUDA;
     LinearDpreArgs d = {};
     d.m = p->m; d.n = p->n; d.act = p->act; d.ldp = l.ldp; d.dy = dy; d.pre = pre;
     d.dpre = l.own_dpre && (dx || dw) ? ws + l.dpre_off : nullptr;
@@ -362,7 +363,6 @@ int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, c
     a.dtype = SSD_BF16; a.act = SSD_ACT_NONE;
     a.ws = (WsHeader*)workspace;
     a.parts = (float*)(ws + l.parts_off);
-    a.keep_status = 1;
     if (dx) {   // (m, k) = dpre (m, n) w (n, k): w's contraction runs along its rows
         a.m = p->m; a.n = p->k; a.k = p->n; a.y = dx;
         a.x = g;
@@ -372,6 +372,7 @@ int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, c
     if (dw) {   // (n, k) = dpre^T (n, m) x (m, k): both contractions run along the rows
         a.m = p->n; a.n = p->k; a.k = p->m; a.y = dw;
         a.x = {g.p, g.ld, true};
+        a.keep_status = dx != nullptr;
         a.w = {x, p->ldx, true};
         if (launch_linear(a, l.dw, st) != cudaSuccess) return SSD_ERR_CUDA;
     }
