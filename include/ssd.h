@@ -1,6 +1,7 @@
 /*
  * libssd: Mamba-2 structured-state-space-duality (SSD) chunked-scan forward
- * pass for NVIDIA GB300 (sm_103a).  C ABI: plain pointers and sizes only.
+ * pass for NVIDIA GB300 (sm_103a), its backward pass and decoding step, and the operators around it (residual
+ * norm, projection, gated recurrence).  C ABI: plain pointers and sizes only.
  *
  * The operation ("State Space Duality and Mamba-2", sections "The
  * Mathematical Bridge" and "The SSD Block Decomposition Algorithm"; the

@@ -33,6 +33,11 @@
 //
 // A document's first token cuts the map (A = 0) and takes the document's own state.
 //
+// Measured: 65536 x 2048 bf16 in one row, strided, 140 us (5.8 TB/s; the bytes need 119 us at the rate of a copy), bound by
+// the main warps' two visits (about 3800 of a tile's 4700 cycles) and by reads of 5.4 TB/s without the rest; fp32
+// 255 us (93 %); 8 x 2048 x 5120 bf16 backward 137 us (6.1 TB/s); 32767 x 1533, 37 documents, 102 us: rows off 16-byte
+// alignment go through registers by elements, twice the instructions.
+//
 // 1 - a is formed as e / (1 + e), e = exp(-g), not as a difference, and kept in place of a:
 // a channel with a long memory has a close to 1, where a = 1 - m is right to the last bit and
 // m = 1 - a would not be; a step is a h + m x, exact where a gate forgets all, rather than h + m (x - h).
