@@ -7,9 +7,9 @@
 //
 // A row is held in registers from its one read to its one write, so both passes
 // are bound by HBM: 16384 x 2560, bf16 with an fp32 residual, 75.7 us forward (6.65 TB/s), e4m3 rows 72 us;
-// 12289 x 2560 backward 82 us (6.1 TB/s; a plain copy reaches 6.77).  A row belongs to kRow consecutive threads of a CTA, 16
-// elements each (8 in the backward): as 16-byte vectors of x where the width and the addresses
-// allow, one by one (strided by the row's threads, so that a warp's accesses
+// 12289 x 2560 backward 82 us (6.1 TB/s; a plain copy reaches 6.77).  A row belongs to consecutive threads of a CTA, 16
+// elements each (8 or 16 in the backward): as 16-byte vectors of x where the width and the addresses
+// allow (in the backward, whatever the width), one by one (strided by the row's threads, so that a warp's accesses
 // stay contiguous) where they do not.  Rows that fit a warp take one
 // each, several rows to a CTA; longer rows take a CTA.
 //
@@ -25,28 +25,36 @@ namespace ssd {
 namespace {
 
 constexpr int kElems = 16;      // elements of a row per thread
-constexpr int kBwdElems = 8;    // the same in the backward
+constexpr int kBwdElems = 8;    // the same in the backward's narrower rows
 // Threads per SM that the backward's registers allow (96 a thread, with the next row loaded ahead).
 constexpr int kBwdThreadsSM = 640;
+// The same with 16 elements (128 registers a thread).
+constexpr int kBwdLeanThreads = 512;
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxMin = 1e-30f;
 
-// Sum (or NaN-keeping maximum) over the threads of a row: a warp, or the CTA
-// (every thread of it calls; the partials are combined in warp order).
+// Sum (or NaN-keeping maximum) over a warp, the same in every lane.
 template <bool kMax>
-__device__ __forceinline__ float row_reduce(float v, bool one_warp, float* part) {
+__device__ __forceinline__ float warp_reduce(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float u = __shfl_xor_sync(0xffffffffu, v, o);
         v = kMax ? max_nan(v, u) : v + u;
     }
+    return v;
+}
+
+// The same over the threads of a row: a warp, or the CTA (every thread of it calls; each warp combines the
+// warps' partials for itself, in one order; 0 is neutral to the sum and to a maximum of magnitudes).  The backward's
+// rows wait for this: a loop over the partials and a division by the width took 8192 columns of bf16 from 45 to 67 us.
+template <bool kMax>
+__device__ __forceinline__ float row_reduce(float v, bool one_warp, float* part) {
+    v = warp_reduce<kMax>(v);
     if (one_warp) return v;
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    float r = part[0];
-    const int nw = blockDim.x >> 5;
-    for (int k = 1; k < nw; ++k) r = kMax ? max_nan(r, part[k]) : r + part[k];
-    return r;
+    return warp_reduce<kMax>(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f);
 }
 
 // V weights (16-byte aligned where V > 1), kept in the caches.
@@ -157,96 +165,150 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
     }
 }
 
-// E: elements of a row per thread, V of them at a time.  Rows of up to 640 threads (THREADS) have the registers to
-// load the next row while the present one is reduced and written.
-template <typename T, typename R, int V, int E, int THREADS>
+// E: elements of a row per thread, V of them at a time.  Rows of up to 640 threads of 8 elements, or 512 of 16, have the
+// registers to load the next row while the present one is reduced and written; with 16 elements the weights wait in
+// shared memory and the residual's gradient is loaded with its own row.
+//
+// SHIFTED: rows of W elements, W not a multiple of V.  Vectors lie on V-element boundaries of the whole array: a row
+// starts `shift` elements into its first one.  Those at its ends hold a neighbour's elements too, which are read with
+// them (whatever they are, or are being replaced by: the values are dropped) and never written.  A slot's rows are a
+// multiple of 8 apart (or it has one): their shift is one number, and a thread's columns stay its own for dw.
+template <typename T, typename R, int V, int E, int THREADS, bool SHIFTED>
 __global__ void __launch_bounds__(THREADS) ssd_add_norm_bwd_kernel(AddNormBwdArgs a) {
     constexpr int C = E / V;
-    constexpr bool kAhead = THREADS <= kBwdThreadsSM;
+    constexpr bool kAhead = E == kBwdElems || THREADS <= kBwdLeanThreads;
+    constexpr bool kLean = kAhead && E > kBwdElems;
     __shared__ float part[2][32];
+    __shared__ __align__(16) float weights[kLean ? THREADS * E : 1];
     const bool one_warp = a.rows_per_cta > 1 || blockDim.x == 32;
     const int slot = one_warp ? threadIdx.x >> 5 : 0;
     const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
     const int nt = one_warp ? 32 : blockDim.x;
     const int W = a.width;
     pdl_trigger();
-    float dw[C][V], wt[C][V];
+    const int64_t stride = (int64_t)gridDim.x * a.rows_per_cta;
+    int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot;
+    const int shift = SHIFTED ? (int)((uint64_t)(row * W) % V) : 0;
+    // first column of a thread's vector c, and whether all of it lies in the row
+    auto column = [&](int c) { return (tid + c * nt) * V - shift; };
+    auto whole = [&](int e) { return !SHIFTED || (e >= 0 && e + V <= W); };
+    auto in = [&](int e) { return !SHIFTED || (e >= 0 && e < W); };
+    auto fetch = [&](auto& v, const auto* p, int64_t row, size_t base, int e) {
+        p += base + e;
+        if (!SHIFTED || e + V <= W || row + 1 < a.rows) v.load(p);
+        else v.load_some(p, W - e);   // the array's last elements
+    };
+    float dw[C][V], wt[kLean ? 1 : C][V];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int e = (tid + c * nt) * V;
+        const int e = column(c);
+        float w[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) dw[c][k] = wt[c][k] = 0.f;
-        if (e < W) load_weights(a.weight + e, wt[c]);
+        for (int k = 0; k < V; ++k) {
+            dw[c][k] = w[k] = 0.f;
+            if (SHIFTED && in(e + k)) w[k] = __ldg(a.weight + e + k);
+        }
+        if (!SHIFTED && e < W) load_weights(a.weight + e, w);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if constexpr (kLean) weights[(tid + c * nt) * V + k] = w[k];   // read by this thread alone
+            else wt[c][k] = w[k];
+        }
     }
     struct Row {
         Raw<T, V> d[C];
-        Raw<R, V> h[C], s[C];
+        Raw<R, V> h[C], s[kLean ? 1 : C];
         float rstd;
     };
     auto load = [&](Row& r, int64_t row) {
         const size_t base = (size_t)row * W;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = (tid + c * nt) * V;
+            const int e = column(c);
             r.d[c].zero();
             r.h[c].zero();
-            r.s[c].zero();
+            if constexpr (!kLean) r.s[c].zero();
             if (e < W) {
-                r.d[c].load(static_cast<const T*>(a.dout) + base + e);
-                r.h[c].load(static_cast<const R*>(a.h) + base + e);
-                if (a.dres) r.s[c].load(static_cast<const R*>(a.dres) + base + e);
+                fetch(r.d[c], static_cast<const T*>(a.dout), row, base, e);
+                fetch(r.h[c], static_cast<const R*>(a.h), row, base, e);
+                if constexpr (!kLean)
+                    if (a.dres) fetch(r.s[c], static_cast<const R*>(a.dres), row, base, e);
             }
         }
         r.rstd = __ldg(a.rstd + row);
     };
-    const int64_t stride = (int64_t)gridDim.x * a.rows_per_cta;
-    int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot;
     Row cur;
     if (kAhead && row < a.rows) load(cur, row);
     int turn = 0;
     for (; row < a.rows; row += stride) {
+        const size_t base = (size_t)row * W;
+        Raw<R, V> late[kLean ? C : 1];
+        if constexpr (kLean) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int e = column(c);
+                late[c].zero();
+                if (a.dres && e < W) fetch(late[c], static_cast<const R*>(a.dres), row, base, e);
+            }
+        }
         Row next;
         if (kAhead) {
             if (row + stride < a.rows) load(next, row + stride);
         } else {
             load(cur, row);
         }
-        const size_t base = (size_t)row * W;
         float p[C][V], xh[C][V];
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             cur.d[c].get(p[c]);
             cur.h[c].get(xh[c]);
+            const int e = column(c);
+            if (!whole(e)) {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (!in(e + k)) p[c][k] = xh[c][k] = 0.f;
+            }
+            float w[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if constexpr (kLean) w[k] = weights[(tid + c * nt) * V + k];
+                else w[k] = wt[c][k];
+            }
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 xh[c][k] *= cur.rstd;
                 dw[c][k] = fmaf(p[c][k], xh[c][k], dw[c][k]);
-                p[c][k] *= wt[c][k];
+                p[c][k] *= w[k];
                 dot = fmaf(p[c][k], xh[c][k], dot);
             }
         }
         // the partials of consecutive rows alternate between two arrays: a row's last
         // reader is past the next row's barrier before a third row writes
-        dot = row_reduce<false>(dot, one_warp, part[turn]) / (float)W;
+        dot = row_reduce<false>(dot, one_warp, part[turn]) * a.inv_width;
         turn ^= 1;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = (tid + c * nt) * V;
+            const int e = column(c);
             if (e < W) {
                 float s[V];
-                cur.s[c].get(s);
+                if constexpr (kLean) late[c].get(s);
+                else cur.s[c].get(s);
 #pragma unroll
                 for (int k = 0; k < V; ++k) s[k] = fmaf(p[c][k] - xh[c][k] * dot, cur.rstd, s[k]);
                 if (a.dx) {
+                    T* dx = static_cast<T*>(a.dx) + base;
                     Raw<T, V> q;
                     q.set(s);
-                    q.store(static_cast<T*>(a.dx) + base + e);
+                    if (whole(e)) q.store(dx + e);
+                    else q.store_within(dx, e, W);
                 }
                 if (a.dres_out) {
+                    R* dr = static_cast<R*>(a.dres_out) + base;
                     Raw<R, V> q;
                     q.set(s);
-                    q.store(static_cast<R*>(a.dres_out) + base + e);
+                    if (whole(e)) q.store(dr + e);
+                    else q.store_within(dr, e, W);
                 }
             }
         }
@@ -255,11 +317,10 @@ __global__ void __launch_bounds__(THREADS) ssd_add_norm_bwd_kernel(AddNormBwdArg
     float* share = a.shares + ((size_t)blockIdx.x * a.rows_per_cta + slot) * W;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int e = (tid + c * nt) * V;
-        if (e < W) {
+        const int e = column(c);
 #pragma unroll
-            for (int k = 0; k < V; ++k) share[e + k] = dw[c][k];
-        }
+        for (int k = 0; k < V; ++k)
+            if (e < W && in(e + k)) share[e + k] = dw[c][k];
     }
 }
 
@@ -298,9 +359,14 @@ RowShape row_shape(int width, int64_t rows, int elems) {
     return s;
 }
 
-// Elements per thread of the backward: 8 leave room in 64 registers for the row,
-// its gradient and the dw share; only rows beyond 1024 x 8 take 16.
-int bwd_elems(int width) { return width <= 1024 * kBwdElems ? kBwdElems : kElems; }
+// Elements that the backward's vectors of a row span: rows of other than whole vectors may reach into one more.
+int bwd_span(int width) { return width % 8 == 0 ? width : width + 7; }
+
+// Elements per thread of the backward: 8 where 640 threads of 8 span a row, else 16; lean: 16 beyond 1280 columns already.
+int bwd_elems(int width, bool lean) {
+    const int span = bwd_span(width);
+    return span > kBwdThreadsSM * kBwdElems || (lean && span > 1280) ? kElems : kBwdElems;
+}
 
 bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -322,24 +388,15 @@ cudaError_t launch_fwd_res(const AddNormArgs& a, int threads, cudaStream_t st) {
     return launch_fwd_typed<T, R, T>(a, threads, st);
 }
 
-template <typename T, typename R>
-cudaError_t launch_bwd_typed(const AddNormBwdArgs& a, unsigned grid, int threads, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    const bool vec = a.width % V == 0 && on16(a.weight) && on16(a.dout) && on16(a.h) && on16(a.dres) && on16(a.dx) && on16(a.dres_out);
-    const int size = bwd_elems(a.width) > kBwdElems ? 2 : threads > kBwdThreadsSM ? 1 : 0;
-    void (*const kerns[2][3])(AddNormBwdArgs) = {
-        {ssd_add_norm_bwd_kernel<T, R, 1, kBwdElems, kBwdThreadsSM>, ssd_add_norm_bwd_kernel<T, R, 1, kBwdElems, 1024>, ssd_add_norm_bwd_kernel<T, R, 1, kElems, 1024>},
-        {ssd_add_norm_bwd_kernel<T, R, V, kBwdElems, kBwdThreadsSM>, ssd_add_norm_bwd_kernel<T, R, V, kBwdElems, 1024>, ssd_add_norm_bwd_kernel<T, R, V, kElems, 1024>}};
-    void (*kern)(AddNormBwdArgs) = kerns[vec][size];
-    kern<<<grid, threads, 0, st>>>(a);
-    return cudaGetLastError();
-}
-
 // Row slots of the backward's grid: as many as fill the SMs, so that each slot's
 // dw share sums many rows and the shares stay a few percent of the traffic.
-int64_t bwd_slots(int64_t rows, int width, int* rows_per_cta, int* threads, int64_t* grid) {
-    const RowShape s = row_shape(width, rows, bwd_elems(width));
-    const int per_sm = kBwdThreadsSM / s.threads > 0 ? kBwdThreadsSM / s.threads : 1;
+// Slots with several rows have 152 n CTAs' rows between them, a multiple of 8.
+static_assert(kAddNormSMs % 8 == 0, "a slot's rows keep their shift");
+int64_t bwd_slots(int64_t rows, int width, bool lean, int* rows_per_cta, int* threads, int64_t* grid) {
+    const int elems = bwd_elems(width, lean);
+    const RowShape s = row_shape(bwd_span(width), rows, elems);
+    const int room = elems == kBwdElems ? kBwdThreadsSM : kBwdLeanThreads;
+    const int per_sm = room / s.threads > 0 ? room / s.threads : 1;
     int64_t g = (rows + s.rows_per_cta - 1) / s.rows_per_cta;
     const int64_t most = (int64_t)kAddNormSMs * per_sm;
     if (g > most) g = most;
@@ -347,6 +404,40 @@ int64_t bwd_slots(int64_t rows, int width, int* rows_per_cta, int* threads, int6
     *threads = s.threads;
     *grid = g;
     return g * s.rows_per_cta;
+}
+
+// 16-byte vectors where every array starts on 16 bytes and rows hold one at least, elements otherwise.  33.5 M elements,
+// us by the rule and by the other side of it (fp32 residual unless said):
+//   lean, bf16 beyond 1280 columns   2560 columns 88.0 (8 elements 88.2), 4096 90.3 (94.4); bf16 residual 43.9 (54.1)
+//   not lean, fp32                   5120 columns 85.4 (97.2; it spills)
+//   not lean, bf16 shifted           2049 columns 99 (112; it spills), 4001 102 (107); bf16 residual lean, 4001 53 (62)
+//   rows beyond 5120 columns         8192 columns 91.6, fp32 83.7, bf16 residual 45 (1024 threads of 8, without the
+//                                    next row ahead: 119, 106)
+//   shifted vectors                  6001 columns 117, fp32 116 (elements 148, 139)
+template <typename T, typename R>
+cudaError_t launch_bwd_typed(AddNormBwdArgs& a, int64_t* nshares, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const bool shifted = a.width % V != 0;
+    const bool vec = a.width >= V && bwd_span(a.width) <= 1024 * kElems && on16(a.dout) && on16(a.h) && on16(a.dres) &&
+                     on16(a.dx) && on16(a.dres_out) && (shifted || on16(a.weight));
+    const bool lean = vec && sizeof(T) == 2 && (!shifted || sizeof(R) == 2);
+    int threads;
+    int64_t grid;
+    *nshares = bwd_slots(a.rows, a.width, lean, &a.rows_per_cta, &threads, &grid);
+    void (*kern)(AddNormBwdArgs);
+    if (bwd_elems(a.width, lean) == kBwdElems)
+        kern = !vec      ? ssd_add_norm_bwd_kernel<T, R, 1, kBwdElems, kBwdThreadsSM, false>
+               : shifted ? ssd_add_norm_bwd_kernel<T, R, V, kBwdElems, kBwdThreadsSM, true>
+                         : ssd_add_norm_bwd_kernel<T, R, V, kBwdElems, kBwdThreadsSM, false>;
+    else if (vec && threads <= kBwdLeanThreads)
+        kern = shifted ? ssd_add_norm_bwd_kernel<T, R, V, kElems, kBwdLeanThreads, true>
+                       : ssd_add_norm_bwd_kernel<T, R, V, kElems, kBwdLeanThreads, false>;
+    else
+        kern = !vec      ? ssd_add_norm_bwd_kernel<T, R, 1, kElems, 1024, false>
+               : shifted ? ssd_add_norm_bwd_kernel<T, R, V, kElems, 1024, true>
+                         : ssd_add_norm_bwd_kernel<T, R, V, kElems, 1024, false>;
+    kern<<<(unsigned)grid, threads < 1024 ? threads : 1024, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -361,23 +452,25 @@ cudaError_t launch_add_norm(const AddNormArgs& args, cudaStream_t st) {
     return launch_fwd_res<float, float>(a, s.threads, st);
 }
 
+// Enough for either shape: which one a call takes depends on its addresses too.
 int64_t add_norm_bwd_shares(int64_t rows, int width) {
     int rpc, threads;
     int64_t grid;
-    return bwd_slots(rows, width, &rpc, &threads, &grid);
+    const int64_t n = bwd_slots(rows, width, false, &rpc, &threads, &grid);
+    const int64_t m = bwd_slots(rows, width, true, &rpc, &threads, &grid);
+    return n > m ? n : m;
 }
 
 cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& args, cudaStream_t st) {
     AddNormBwdArgs a = args;
-    int threads;
-    int64_t grid;
-    const int64_t nshares = bwd_slots(a.rows, a.width, &a.rows_per_cta, &threads, &grid);
+    a.inv_width = 1.f / (float)a.width;
+    int64_t nshares;
     cudaError_t e;
     if (a.dtype == SSD_BF16)
-        e = a.residual_dtype == SSD_F32 ? launch_bwd_typed<bf16_t, float>(a, (unsigned)grid, threads, st)
-                                        : launch_bwd_typed<bf16_t, bf16_t>(a, (unsigned)grid, threads, st);
+        e = a.residual_dtype == SSD_F32 ? launch_bwd_typed<bf16_t, float>(a, &nshares, st)
+                                        : launch_bwd_typed<bf16_t, bf16_t>(a, &nshares, st);
     else
-        e = launch_bwd_typed<float, float>(a, (unsigned)grid, threads, st);
+        e = launch_bwd_typed<float, float>(a, &nshares, st);
     if (e != cudaSuccess) return e;
     return launch_kernel(ssd_add_norm_bwd_reduce, (unsigned)((a.width + 31) / 32), 1024, 0, st, true, (const float*)a.shares,
                          (int)nshares, a.width, a.dweight);

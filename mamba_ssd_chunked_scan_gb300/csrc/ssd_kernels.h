@@ -163,6 +163,7 @@ struct AddNormBwdArgs {
     float* dweight;
     float* shares;         // [row slots * width]
     int rows_per_cta;
+    float inv_width;
 };
 
 // Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of kScanSegs segments x kScanCh

@@ -42,6 +42,26 @@ struct Raw {
             __stcs(reinterpret_cast<W*>(p), w);
         }
     }
+    // The first n of the V elements, one by one.
+    __device__ __forceinline__ void load_some(const T* p, int n) {
+        T* v = reinterpret_cast<T*>(&w);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (k < n) v[k] = p[k];
+    }
+    // Those of the V elements from column e of a row that lie in its columns [0, n), one by one.
+    __device__ __forceinline__ void store_within(T* row, int e, int n) const {
+        const T* v = reinterpret_cast<const T*>(&w);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (e + k >= 0 && e + k < n) row[e + k] = v[k];
+    }
+    // The compiler is not to reuse what it made of the elements before.
+    __device__ __forceinline__ void forget() {
+        uint32_t* v = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(W) / 4; ++k) asm volatile("" : "+r"(v[k]));
+    }
     __device__ __forceinline__ void zero() {
         if constexpr (sizeof(T) * V == 32) w.lo = w.hi = make_uint4(0, 0, 0, 0);
         else if constexpr (sizeof(T) * V == 16) w = make_uint4(0, 0, 0, 0);

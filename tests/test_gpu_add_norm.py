@@ -93,6 +93,28 @@ def test_backward(rows, width, offset, dtype, rtype, with_res):
     close(got["dweight"], terms.sum(0), (rows + 64) * U * terms.abs().sum(0) + 1e-30, "dweight")
 
 
+# rows of every shift against 16 bytes, several to a slot; the widest spans of each kernel shape; fewer columns than a vector
+@pytest.mark.parametrize("rows,width", [(2500, 5), (1300, 9), (700, 1283), (1251, 1276), (500, 4001), (330, 5114), (320, 6001),
+                                        (310, 8177), (310, 8186), (160, 16377), (155, 16378)])
+@pytest.mark.parametrize("dtype,rtype", [(BF, BF), (BF, F4), (F4, F4)])
+def test_backward_rows_off_16_bytes(rows, width, dtype, rtype):
+    test_backward(rows, width, 0, dtype, rtype, True)
+    test_backward(rows, width, 1, dtype, rtype, False)
+
+
+@pytest.mark.parametrize("width", [1283, 4001, 333])
+def test_backward_neighbouring_rows_stay_apart(width):
+    """A row of NaNs or infinities reaches dweight, and no other row's gradient."""
+    dout, h, w = make(912, width, BF, BF, width)
+    rstd = (1 / torch.sqrt((h.double() ** 2).mean(-1) + 1e-5)).float()
+    clean = ssd.add_norm_bwd(dout, h, w, rstd)["dx"]
+    dout[5], h[8] = float("nan"), float("inf")
+    got = ssd.add_norm_bwd(dout, h, w, rstd)["dx"]
+    keep = torch.ones(912, dtype=torch.bool, device="cuda")
+    keep[[5, 8]] = False
+    assert torch.equal(got[keep], clean[keep]) and not got[~keep].isfinite().any()
+
+
 def test_gradient_against_differences():
     x, res, w = make(6, 200, F4, F4, 11)
     g = torch.Generator(device="cuda").manual_seed(5)
