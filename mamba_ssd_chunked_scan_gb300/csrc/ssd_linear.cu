@@ -22,7 +22,7 @@
 //
 // Measured: 16384 x 10240 x 2560 bf16 435 us back to back (1.97 PFLOP/s; the library's product 419) and 508 under
 // the power cap (1.69; the library's sustained rate 1.72); both gradients of it 906 us (library 880); e4m3
-// 4099 x 2560 x 5120 with its residual 39 us in L2, 51 from HBM; 8 rows of e4m3 by 10240 x 2560 10 us, of which
+// 4099 x 2560 x 5120 with its residual 49 us, from HBM; 8 rows of e4m3 by 10240 x 2560 10 us, of which
 // W's bytes need 3.9.  dpre of 8192 x 5120 41 us (6.1 TB/s).
 //
 // Sums are fp32 in tensor memory.  Tiles run in waves of one per SM (or pair); those of the last wave, which would
@@ -279,14 +279,17 @@ __device__ __forceinline__ void send_block(const uint8_t* block, uint8_t* base, 
 
 // 32 columns (one row per lane) of a tile from their sums `w`: D's rows `row` to `row` + 31, columns col on.
 // `vec`: this chunk's scales (then bias) by column, in shared memory, TN apart; xs: the row's scale.
-// r: the residual's elements, asked for ahead (aligned rows).
+// r: the residual's elements, asked for ahead (aligned rows) as they lie in memory, whole rows of 64 bytes by four lanes
+// each: asked for by a row per lane they hold up the MMAs' operands (16384 x 10240 x 2560 509 us, so 462).
 __device__ __forceinline__ void ask_residual(const LinearArgs& a, uint4 (&r)[4], int64_t row, int col) {
     const int lane = threadIdx.x & 31;
-    const bf16_t* res = static_cast<const bf16_t*>(a.residual) + (size_t)(row + lane) * a.n + col;
+    row += lane >> 2;
+    col += 8 * (lane & 3);
+    const bf16_t* res = static_cast<const bf16_t*>(a.residual) + (size_t)row * a.n + col;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        r[k] = make_uint4(0, 0, 0, 0);
-        if (row + lane < a.m && col + 8 * k < a.n) r[k] = __ldcs(reinterpret_cast<const uint4*>(res + 8 * k));
+    for (int i = 0; i < 4; ++i) {
+        r[i] = make_uint4(0, 0, 0, 0);
+        if (row + 8 * i < a.m && col < a.n) r[i] = __ldcs(reinterpret_cast<const uint4*>(res + (size_t)8 * i * a.n));
     }
 }
 __device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t (&w)[32], uint4 (&r)[4], int64_t row, int col,
@@ -296,14 +299,17 @@ __device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t 
     const size_t at = (size_t)row * a.n + col;
     if (a.residual) {
         const bf16_t* res = static_cast<const bf16_t*>(a.residual);
-        if (!a.vec) {   // row by row through the block
-            __syncwarp();
+        __syncwarp();
+        if (a.vec) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(word_at(block, 8 * i + (lane >> 2), lane & 3)) = r[i];
+        } else {   // row by row
             for (int i = 0; i < rows; ++i)
                 if (lane < cols) *reinterpret_cast<bf16_t*>(word_at(block, i, lane >> 3) + 2 * (lane & 7)) = res[at + (size_t)i * a.n + lane];
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const uint4*>(word_at(block, lane, k));
         }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const uint4*>(word_at(block, lane, k));
     }
     float v[32];
 #pragma unroll
