@@ -11,7 +11,7 @@
 // thread holding two channels; three hand-over warps; and a loading warp:
 //   loading    takes the next tile by ticket and brings its inputs into a ring of shared-memory stages (TMA), and
 //              sends a finished tile's outputs off from the same stage.  Where rows are not aligned to 16 bytes
-//              it only takes the tickets, and the main warps load a tile ahead into registers and store directly;
+//              they come by their alignment's classes, and the main warps store the outputs themselves;
 //   main       forms the next tile's decays and its segment's map, keeping 1 - a in registers; then waits for
 //              the state that enters its segment of the tile before, walks that segment again and writes the
 //              outputs.  So a tile's state has a whole tile's time to arrive;
@@ -35,8 +35,9 @@
 //
 // Measured: 65536 x 2048 bf16 in one row, strided, 140 us (5.8 TB/s; the bytes need 119 us at the rate of a copy), bound by
 // the main warps' two visits (about 3800 of a tile's 4700 cycles) and by reads of 5.4 TB/s without the rest; fp32
-// 255 us (93 %); 8 x 2048 x 5120 bf16 backward 137 us (6.1 TB/s); 32767 x 1533, 37 documents, 102 us: rows off 16-byte
-// alignment go through registers by elements, twice the instructions.
+// 255 us (93 %); 8 x 2048 x 5120 bf16 backward 137 us (6.1 TB/s); 32767 x 1533, 37 documents, 93 us (1536 columns 71):
+// elements off alignment are read from shared memory and stored one by one, and tiles are half as long.  (Loaded by
+// elements into registers, a tile ahead: 99 us, 65536 x 2047 231 instead of 190, 8 x 2048 x 5119 backward 224 instead of 202.)
 //
 // 1 - a is formed as e / (1 + e), e = exp(-g), not as a difference, and kept in place of a:
 // a channel with a long memory has a close to 1, where a = 1 - m is right to the last bit and
@@ -105,22 +106,35 @@ template <typename T> struct PairWord;
 template <> struct PairWord<bf16_t> { typedef uint32_t type; };
 template <> struct PairWord<float> { typedef uint64_t type; };
 
-// Shapes of a kernel instance.  ROWS: rows are not 16-byte aligned, and pass through registers only.
+// Shapes of a kernel instance.  ROWS: rows are not 16-byte aligned.  Those P apart are off alignment by the same
+// bytes, so each of P classes is a matrix of its own, of 16-byte aligned rows that start up to P - 1 elements early: a tile
+// comes as P boxes, kCh + P columns wide, and a row's elements lie off by its class's shift.
 template <typename T, bool ROWS, bool BWD>
 struct Shape {
-    static constexpr int ES = sizeof(T);
+    static constexpr int ES = sizeof(T), P = 16 / ES;
     static constexpr int SEG = scan_seg(BWD, ES == 2 ? SSD_BF16 : SSD_F32, ROWS), TOK = SEG * kMain;
-    static constexpr int PITCH = kCh * ES, ARR = TOK * PITCH;   // one operand's tile
+    static constexpr int PITCH = (kCh + (ROWS ? P : 0)) * ES, ARR = TOK * PITCH;   // one operand's tile
     static constexpr int NA = BWD ? 3 : 2;                      // g, x (and dy)
     static constexpr int STAGE = NA * ARR + (BWD ? kMain * PITCH : 0);   // and, backwards, the h before each segment
-    static constexpr int NS = ROWS || 4 * STAGE <= 212 * 1024 ? 4 : 3;
-    // ROWS: what the first visits of two tiles keep for the second, per token and thread
-    static constexpr int kKeep = 2 * SEG * 32 * kMain * 8 * (BWD ? 3 : 2);
-    static constexpr size_t kSmem = 128 + (ROWS ? (size_t)kKeep : (size_t)NS * STAGE);
+    static constexpr int NS = 4 * STAGE <= 212 * 1024 ? 4 : 3;
+    static constexpr size_t kSmem = 128 + (size_t)NS * STAGE;
+    static_assert(!ROWS || (SEG % P == 0 && (!BWD || SEG == P)), "a segment's classes are those of its first P tokens");
 };
 
+// The operands' tensor maps: one each, or (ROWS) one a class.
+template <typename T, bool ROWS, bool BWD>
 struct ScanParams {
     CUtensorMap g, x, y, dy, dg, dx;
+    GateScanArgs a;
+};
+template <typename T>
+struct ScanParams<T, true, false> {
+    CUtensorMap g[16 / sizeof(T)], x[16 / sizeof(T)];
+    GateScanArgs a;
+};
+template <typename T>
+struct ScanParams<T, true, true> {
+    CUtensorMap g[16 / sizeof(T)], x[16 / sizeof(T)], dy[16 / sizeof(T)], y[16 / sizeof(T)];
     GateScanArgs a;
 };
 
@@ -245,6 +259,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, ui
         "l"(tm), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, uint64_t* bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(tm), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
                  "r"(ptx::smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
@@ -252,21 +273,22 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* 
 }
 // ---------------------------------------------------------------------- loading warp
 template <typename T, bool ROWS, bool DOCS, bool BWD>
-__device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared<Shape<T, ROWS, BWD>::TOK, DOCS>& sh) {
+__device__ __forceinline__ void loading(const ScanParams<T, ROWS, BWD>& p, uint8_t* sm, Shared<Shape<T, ROWS, BWD>::TOK, DOCS>& sh) {
     typedef Shape<T, ROWS, BWD> H;
     const GateScanArgs& a = p.a;
     const int lane = threadIdx.x & 31;
     auto send = [&](int j) {   // lane 0: tile j's outputs from its stage
-        if constexpr (ROWS) return;
-        const Tile& t = sh.tile[j % kRing];
-        const uint8_t* st = sm + (j % H::NS) * H::STAGE;
-        if (BWD) {
-            tma_store_3d(&p.dg, st, t.group * kCh, (int)t.t0, t.row);
-            tma_store_3d(&p.dx, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
-        } else {
-            tma_store_3d(&p.y, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
+        if constexpr (!ROWS) {
+            const Tile& t = sh.tile[j % kRing];
+            const uint8_t* st = sm + (j % H::NS) * H::STAGE;
+            if (BWD) {
+                tma_store_3d(&p.dg, st, t.group * kCh, (int)t.t0, t.row);
+                tma_store_3d(&p.dx, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
+            } else {
+                tma_store_3d(&p.y, st + H::ARR, t.group * kCh, (int)t.t0, t.row);
+            }
+            ptx::bulk_commit();
         }
-        ptx::bulk_commit();
     };
     int near = 0;            // documents that start before the last tile, about
     int n = 0, filled = 0;   // tiles, and phases of the stages' `full` begun (the end's among them)
@@ -293,22 +315,40 @@ __device__ __forceinline__ void loading(const ScanParams& p, uint8_t* sm, Shared
         uint64_t* full = &sh.full[st];
         ++filled;
         if (lane == 0) {
-            if (ROWS || !t.ntok) {
+            if (!t.ntok) {
                 ptx::mbar_arrive(full);
             } else {
-                uint8_t* dst = sm + st * H::STAGE;
                 ptx::mbar_expect_tx(full, H::STAGE);
-                const int c = t.group * kCh, t0 = (int)t.t0;
-                tma_load_3d(dst, &p.g, full, c, t0, t.row);
-                tma_load_3d(dst + H::ARR, &p.x, full, c, t0, t.row);
-                if (BWD) {
-                    tma_load_3d(dst + 2 * H::ARR, &p.dy, full, c, t0, t.row);
-                    // the h before each segment: every SEG-th row from t0 - 1 (before the sequence: zeros)
-                    tma_load_3d(dst + H::NA * H::ARR, &p.y, full, c, t0 - 1, t.row);
+                if constexpr (!ROWS) {
+                    uint8_t* dst = sm + st * H::STAGE;
+                    const int c = t.group * kCh, t0 = (int)t.t0;
+                    tma_load_3d(dst, &p.g, full, c, t0, t.row);
+                    tma_load_3d(dst + H::ARR, &p.x, full, c, t0, t.row);
+                    if (BWD) {
+                        tma_load_3d(dst + 2 * H::ARR, &p.dy, full, c, t0, t.row);
+                        // the h before each segment: every SEG-th row from t0 - 1 (before the sequence: zeros)
+                        tma_load_3d(dst + H::NA * H::ARR, &p.y, full, c, t0 - 1, t.row);
+                    }
                 }
             }
         }
         if (!t.ntok) break;
+        if constexpr (ROWS) {
+            // lane j: the tile's tokens j, j + P, ...; lane P, backwards: the h before each segment
+            __syncwarp();
+            uint8_t* dst = sm + st * H::STAGE;
+            const int c = t.group * kCh;
+            const int64_t r = (int64_t)t.row * a.seqlen + t.t0 + (lane < H::P ? lane : -1);
+            const int k = (int)(r & (H::P - 1)), q = (int)(r >> (H::P == 8 ? 3 : 2));
+            if (lane < H::P) {
+                dst += lane * (H::ARR / H::P);
+                tma_load_2d(dst, &p.g[k], full, c, q);
+                tma_load_2d(dst + H::ARR, &p.x[k], full, c, q);
+                if constexpr (BWD) tma_load_2d(dst + 2 * H::ARR, &p.dy[k], full, c, q);
+            }
+            if constexpr (BWD)
+                if (lane == H::P) tma_load_2d(dst + H::NA * H::ARR, &p.y[k], full, c, q);
+        }
     }
     if (lane != 0) return;
     // the outputs of the tiles still in stages, then everything in flight
@@ -412,7 +452,7 @@ __device__ __forceinline__ void take_states(const GateScanArgs& a, S& sh) {
 }
 
 // ---------------------------------------------------------------------- main warps
-// A thread's two channels: neighbours in aligned tiles, 32 apart in windows of rows.
+// A thread's two channels: neighbours in aligned tiles, 32 apart in shifted rows.
 template <typename T, bool ROWS, bool DOCS, bool BWD>
 struct Main {
     typedef Shape<T, ROWS, BWD> H;
@@ -431,12 +471,8 @@ struct Main {
     bool plain;        // the segment is inside the sequence, and no document starts or ends in it
     uint32_t marks;    // bit k: a document starts at the segment's token k (SEG: at the token after it)
     int final;         // the sequence's last token, counted from the segment's first
-    // ROWS: the operands of the tile to come, and the h before its segment, as loaded (nothing touches them
-    // before the tile's first visit, so they arrive during the second visit of the tile before)
-    struct Pair {
-        uint32_t lo, hi;
-    };
-    Pair raw[ROWS ? H::NA : 1][ROWS ? SEG : 1], hraw;
+    // ROWS: the low bits of the addresses of the tile's first row and of the bytes from one to the next, per operand
+    uint32_t low[ROWS ? H::NA : 1], step[ROWS ? H::NA : 1];
 
     // Tile n of the walk, for one of its visits.
     __device__ __forceinline__ void open(int n, uint8_t* sm) {
@@ -447,7 +483,18 @@ struct Main {
         c0 = t.group * kCh + (ROWS ? lane : 2 * lane);
         ok0 = c0 < a.width;
         ok1 = c0 + kApart < a.width;
-        st = sm + (n % H::NS) * H::STAGE + s0 * H::PITCH + 2 * lane * H::ES;
+        st = sm + (n % H::NS) * H::STAGE + (ROWS ? s0 / H::P * H::PITCH + lane * H::ES : s0 * H::PITCH + 2 * lane * H::ES);
+        if constexpr (ROWS) {
+            auto first = [](const void* base, int64_t at) { return (uint32_t)(uintptr_t)base + (uint32_t)at * H::ES; };
+            low[0] = first(a.g, t.og);
+            low[1] = first(a.x, t.ox);
+            step[0] = (uint32_t)a.g_stride * H::ES;
+            step[1] = (uint32_t)a.x_stride * H::ES;
+            if constexpr (BWD) {
+                low[2] = first(a.dy, t.oy);
+                step[2] = (uint32_t)a.width * H::ES;
+            }
+        }
         plain = s0 + SEG <= t.ntok;
         if (DOCS) {
             marks = __ballot_sync(0xffffffffu, lane <= SEG && doc[s0 + lane] >= 0);
@@ -474,66 +521,31 @@ struct Main {
         typedef typename std::conditional<std::is_const<P>::value, const T, T>::type E;
         return static_cast<E*>(base) + at + (uint64_t)(uint32_t)s0 * (uint32_t)pitch + lane;
     }
-    // ROWS: row k, `pitch` bytes apart, from p (one multiply-add: 64-bit sums would cost two instructions a row)
+    // Row k, `pitch` bytes apart, from p (one multiply-add: 64-bit sums would cost two instructions a row)
     template <typename P>
     static __device__ __forceinline__ P* row(P* p, int k, uint32_t pitch) {
         return reinterpret_cast<P*>(reinterpret_cast<uint64_t>(p) + (uint64_t)(uint32_t)k * pitch);
     }
-    // One element's bits, straight into and out of a 32-bit register (16-bit values of the language pass through
-    // conversions first).
-    static __device__ __forceinline__ uint32_t element(const T* q) {
-        uint32_t v;
-        if constexpr (sizeof(T) == 2) asm volatile("ld.global.cs.u16 %0, [%1];" : "=r"(v) : "l"(q));
-        else asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(v) : "l"(q));
-        return v;
-    }
+    // One element's bits from a 32-bit register (16-bit values of the language pass through conversions first).
     static __device__ __forceinline__ void put_element(T* q, uint32_t v) {
         if constexpr (sizeof(T) == 2) asm volatile("st.global.u16 [%0], %1;" ::"l"(q), "r"(v) : "memory");
         else asm volatile("st.global.u32 [%0], %1;" ::"l"(q), "r"(v) : "memory");
     }
-    // ROWS: the thread's two elements in one row.  ALL: both exist.
-    template <bool ALL>
-    __device__ __forceinline__ Pair fetch(const T* q, bool in) const {
-        Pair p = {0u, 0u};
-        if (ALL || (in && ok0)) p.lo = element(q);
-        if (ALL || (in && ok1)) p.hi = element(q + kApart);
-        return p;
-    }
-    template <bool ALL>
-    __device__ __forceinline__ void fetch_all() {
-        const T* g = mine(a.g, t.og, a.g_stride);
-        const T* x = mine(a.x, t.ox, a.x_stride);
-        const T* dy = mine(a.dy, t.oy, a.width);
-#pragma unroll
-        for (int k = 0; k < SEG; ++k) {
-            const bool in = s0 + k < t.ntok;
-            raw[0][k] = fetch<ALL>(row(g, k, (uint32_t)a.g_stride * H::ES), in);
-            raw[1][k] = fetch<ALL>(row(x, k, (uint32_t)a.x_stride * H::ES), in);
-            if constexpr (BWD) raw[2][k] = fetch<ALL>(row(dy, k, (uint32_t)a.width * H::ES), in);
-        }
-        // the h before the segment: the output before it
-        if constexpr (BWD) hraw = fetch<false>(mine(a.y, t.oy, a.width) - a.width, s0 < t.ntok && t.t0 + s0 > 0);
-    }
-    static __device__ __forceinline__ f2 widen(Pair p) {
-        if constexpr (sizeof(T) == 2) return pk(__uint_as_float(p.lo << 16), __uint_as_float(p.hi << 16));
-        else return pk(__uint_as_float(p.lo), __uint_as_float(p.hi));
+    // ROWS: the thread's two elements from its first one's place
+    static __device__ __forceinline__ f2 pair(const uint8_t* q) {
+        typedef typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type E;
+        const uint32_t lo = *reinterpret_cast<const E*>(q), hi = *reinterpret_cast<const E*>(q + kApart * H::ES);
+        if constexpr (sizeof(T) == 2) return pk(__uint_as_float(lo << 16), __uint_as_float(hi << 16));
+        else return pk(__uint_as_float(lo), __uint_as_float(hi));
     }
     // whether the segment's tokens and the tile's channels all exist
     __device__ __forceinline__ bool all() const { return s0 + SEG <= t.ntok && (t.group + 1) * kCh <= a.width; }
-    __device__ __forceinline__ bool load(int n, uint8_t* sm) {
-        if constexpr (ROWS) {
-            if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
-            open(n, sm);
-            if (!t.ntok) return true;
-            if (all()) fetch_all<true>();
-            else fetch_all<false>();
-        }
-        return true;
-    }
     // operand r (g, x, dy) at token k of the segment
     __device__ __forceinline__ f2 in(int r, int k) const {
-        if constexpr (ROWS) return widen(raw[r][k]);
-        else return widen(*reinterpret_cast<const W*>(st + r * H::ARR + k * H::PITCH));
+        if constexpr (ROWS)
+            return pair(st + r * H::ARR + (k % H::P * (H::TOK / H::P) + k / H::P) * H::PITCH + ((low[r] + k % H::P * step[r]) & 15));
+        else
+            return widen(*reinterpret_cast<const W*>(st + r * H::ARR + k * H::PITCH));
     }
     // A result over operand r's place in the stage, from where it is sent off; ROWS: straight to memory, to row k of
     // `base` (the segment's first row, at the thread's channels).
@@ -590,38 +602,11 @@ struct Main {
     __device__ __forceinline__ bool ends(int k) const { return DOCS && ((marks >> (k + 1) & 1) || k == final); }
     __device__ __forceinline__ int ending(int k) const { return k == final ? a.ndocs - 1 : doc[s0 + k + 1] - 1; }
 
-    // What the first visit keeps for the second: m = 1 - a and, backwards, u = d(h_t)/d(g_t), in registers beside
-    // the operands in the stage; ROWS: in shared memory, with what else the second visit needs (m x forwards, dy backwards).
+    // What the first visit keeps for the second, in registers beside the operands in the stage: m = 1 - a and,
+    // backwards, u = d(h_t)/d(g_t).  ROWS, forwards: u = m x, which reading x again would cost more than its registers.
     struct Keep {
-        f2 m[ROWS ? 1 : SEG], u[BWD && !ROWS ? SEG : 1];
-        uint8_t* at;
+        f2 m[SEG], u[BWD || ROWS ? SEG : 1];
     };
-    __device__ __forceinline__ void bind(Keep& q, int n, uint8_t* sm) const {
-        if constexpr (ROWS) q.at = sm + (n & 1) * (H::kKeep / 2) + (warp * 32 + lane) * 8;
-    }
-    enum { kSlots = SEG * 32 * kMain * 8 };   // bytes of one value of 8 bytes
-    __device__ __forceinline__ void set_m(Keep& q, int k, f2 v) const {
-        if constexpr (ROWS) *reinterpret_cast<f2*>(q.at + k * 32 * kMain * 8) = v;
-        else q.m[k] = v;
-    }
-    __device__ __forceinline__ f2 get_m(const Keep& q, int k) const {
-        if constexpr (ROWS) return *reinterpret_cast<const f2*>(q.at + k * 32 * kMain * 8);
-        else return q.m[k];
-    }
-    __device__ __forceinline__ void set_u(Keep& q, int k, f2 v) const {
-        if constexpr (ROWS) *reinterpret_cast<f2*>(q.at + kSlots + k * 32 * kMain * 8) = v;
-        else q.u[k] = v;
-    }
-    __device__ __forceinline__ f2 get_u(const Keep& q, int k) const {
-        if constexpr (ROWS) return *reinterpret_cast<const f2*>(q.at + kSlots + k * 32 * kMain * 8);
-        else return q.u[k];
-    }
-    __device__ __forceinline__ void set_r(Keep& q, int k, f2 v) const {
-        if constexpr (ROWS) *reinterpret_cast<f2*>(q.at + (BWD ? 2 : 1) * kSlots + k * 32 * kMain * 8) = v;
-    }
-    __device__ __forceinline__ f2 get_r(const Keep& q, int k) const {
-        return *reinterpret_cast<const f2*>(q.at + (BWD ? 2 : 1) * kSlots + k * 32 * kMain * 8);
-    }
 
     // PLAIN: every token of the segment is inside the sequence, and no document starts or ends in it
     template <bool PLAIN>
@@ -639,8 +624,8 @@ struct Main {
             A = mul(A, av);
             const f2 b = mul(mv, in(1, k));
             B = fma2(av, B, b);
-            set_m(q, k, mv);
-            set_r(q, k, b);
+            q.m[k] = mv;
+            if constexpr (ROWS) q.u[k] = b;
         }
         put_map(A, B);
     }
@@ -654,9 +639,9 @@ struct Main {
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
-            const f2 mv = get_m(q, k);
+            const f2 mv = q.m[k];
             f2 b;
-            if constexpr (ROWS) b = get_r(q, k);
+            if constexpr (ROWS) b = q.u[k];
             else b = mul(mv, in(1, k));
             h = fma2(fma2(mv, minus, one), h, b);
             put<ALL>(1, y, a.width, k, h);
@@ -671,7 +656,9 @@ struct Main {
         const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
         f2 h;
         if (t.t0 + s0 == 0) h = DOCS ? pk(0.f, 0.f) : state(a.init, t.row);
-        else if constexpr (ROWS) h = widen(hraw);
+        else if constexpr (ROWS)
+            h = pair(st - s0 / H::P * H::PITCH + H::NA * H::ARR + warp * H::PITCH +
+                     (((uint32_t)(uintptr_t)a.y + (uint32_t)(t.oy - a.width) * H::ES) & 15));
         else h = widen(*reinterpret_cast<const W*>(st - s0 * H::PITCH + H::NA * H::ARR + warp * H::PITCH));
         // forwards through the segment: u = (h_{t-1} - x) a (1 - a)
 #pragma unroll
@@ -681,10 +668,9 @@ struct Main {
             const f2 xv = in(1, k);
             gate2(in(0, k), av, mv);
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
-            set_u(q, k, mul(fma2(xv, minus, h), mul(av, mv)));
-            set_m(q, k, mv);
+            q.u[k] = mul(fma2(xv, minus, h), mul(av, mv));
+            q.m[k] = mv;
             h = fma2(av, h, mul(mv, xv));
-            if constexpr (ROWS) set_r(q, k, in(2, k));
         }
         // backwards: the map of mu over the segment
         f2 A = one, B = pk(0.f, 0.f);
@@ -696,7 +682,7 @@ struct Main {
                 A = pk(0.f, 0.f);
                 B = at >= 0 ? state(a.enter, at) : A;
             }
-            const f2 av = fma2(get_m(q, k), minus, one);
+            const f2 av = fma2(q.m[k], minus, one);
             B = mul(av, add(in(2, k), B));
             A = mul(A, av);
         }
@@ -714,11 +700,8 @@ struct Main {
                 const int at = ending(k);
                 mu = at >= 0 ? state(a.enter, at) : pk(0.f, 0.f);
             }
-            f2 lam;
-            if constexpr (ROWS) lam = add(get_r(q, k), mu);
-            else lam = add(in(2, k), mu);
-            const f2 mv = get_m(q, k);
-            put<ALL>(0, dg, a.g_stride, k, mul(lam, get_u(q, k)));
+            const f2 lam = add(in(2, k), mu), mv = q.m[k];
+            put<ALL>(0, dg, a.g_stride, k, mul(lam, q.u[k]));
             put<ALL>(1, dx, a.x_stride, k, mul(lam, mv));
             mu = mul(fma2(mv, minus, one), lam);
             if (DOCS && !PLAIN && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
@@ -729,7 +712,6 @@ struct Main {
     __device__ __forceinline__ bool first(int n, uint8_t* sm, Keep& q) {
         if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
         open(n, sm);
-        bind(q, n, sm);
         if (t.ntok) {
             if constexpr (BWD) {
                 if (plain) first_bwd<true>(q);
@@ -760,12 +742,9 @@ struct Main {
     }
     __device__ __forceinline__ void run(uint8_t* sm) {
         Keep cur, next;
-        if (!load(0, sm)) return;
         bool more = first(0, sm, cur);
-        if (more && !load(1, sm)) return;
         for (int n = 0; more; ++n) {
             more = first(n + 1, sm, next);
-            if (more && !load(n + 2, sm)) return;
             if (!second(n, sm, cur)) return;
             cur = next;
         }
@@ -773,7 +752,7 @@ struct Main {
 };
 
 template <typename T, bool ROWS, bool DOCS, bool BWD>
-__global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid_constant__ ScanParams p) {
+__global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid_constant__ ScanParams<T, ROWS, BWD> p) {
     typedef Shape<T, ROWS, BWD> H;
     static_assert(H::kSmem + sizeof(Shared<H::TOK, DOCS>) <= 227 * 1024, "a CTA's shared memory");
     extern __shared__ uint8_t smem_raw[];
@@ -862,7 +841,7 @@ bool encode_3d(CUtensorMap* tm, const void* base, int es, const GateScanArgs& a,
 }
 
 template <typename T, bool ROWS, bool DOCS, bool BWD>
-cudaError_t launch_one(const ScanParams& p, cudaStream_t st) {
+cudaError_t launch_one(const ScanParams<T, ROWS, BWD>& p, cudaStream_t st) {
     const auto kern = ssd_gate_scan_kernel<T, ROWS, DOCS, BWD>;
     constexpr size_t smem = Shape<T, ROWS, BWD>::kSmem;
     // once per device and kernel: the shared-memory opt-in
@@ -881,12 +860,50 @@ cudaError_t launch_one(const ScanParams& p, cudaStream_t st) {
     return launch_kernel(kern, p.a.ntiles < most ? p.a.ntiles : most, kThreads, smem, st, p.a.ws != nullptr, p);
 }
 
+// Class k of P of a matrix's rows (its rows k, k + P, ...), in boxes of kCh + P columns x `box` rows.  Its rows are aligned as
+// its first one is, and are read from the 16-byte boundary before it.  A class without rows is not looked at; its
+// map holds the first row.
+template <typename T>
+bool encode_class(CUtensorMap* tm, const void* base, int64_t rows, int width, int64_t stride, int k, int box) {
+    constexpr int es = sizeof(T), P = 16 / es;
+    const auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const uintptr_t at = (uintptr_t)base + (k < rows ? (uintptr_t)k * stride * es : 0), from = at & ~(uintptr_t)15;
+    const int64_t n = k < rows ? (rows - k + P - 1) / P : 1;
+    cuuint64_t dims[2] = {(cuuint64_t)(width + (at - from) / es), (cuuint64_t)n};
+    // a single row has no stride, and that of several is within the memory that they lie in
+    cuuint64_t strides[1] = {(cuuint64_t)(n > 1 ? stride : width + P) * es * P};
+    cuuint32_t boxes[2] = {(cuuint32_t)(kCh + P), (cuuint32_t)box};
+    cuuint32_t step[2] = {1, 1};
+    return enc(tm, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, reinterpret_cast<void*>(from),
+               dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, bool BWD>
+cudaError_t launch_rows(const GateScanArgs& a, cudaStream_t st) {
+    typedef Shape<T, true, BWD> H;
+    ScanParams<T, true, BWD> p;
+    p.a = a;
+    const int64_t rows = a.batch * a.seqlen;
+    for (int k = 0; k < H::P; ++k) {
+        const int box = H::TOK / H::P;
+        bool ok = encode_class<T>(&p.g[k], a.g, rows, a.width, a.g_stride, k, box) &&
+                  encode_class<T>(&p.x[k], a.x, rows, a.width, a.x_stride, k, box);
+        if constexpr (BWD)
+            ok = ok && encode_class<T>(&p.dy[k], a.dy, rows, a.width, a.width, k, box) &&
+                 encode_class<T>(&p.y[k], a.y, rows, a.width, a.width, k, kMain);
+        if (!ok) return cudaErrorInvalidValue;
+    }
+    return a.cu ? launch_one<T, true, true, BWD>(p, st) : launch_one<T, true, false, BWD>(p, st);
+}
+
 template <typename T, bool BWD>
 cudaError_t launch_typed(const GateScanArgs& a, bool rows, cudaStream_t st) {
-    ScanParams p;
+    if (rows) return launch_rows<T, BWD>(a, st);
+    ScanParams<T, false, BWD> p;
     memset(&p, 0, sizeof(p));
     p.a = a;
-    if (rows) return a.cu ? launch_one<T, true, true, BWD>(p, st) : launch_one<T, true, false, BWD>(p, st);
     typedef Shape<T, false, BWD> H;
     constexpr int es = sizeof(T);
     bool ok = encode_3d(&p.g, a.g, es, a, a.g_stride, H::TOK) && encode_3d(&p.x, a.x, es, a, a.x_stride, H::TOK) &&

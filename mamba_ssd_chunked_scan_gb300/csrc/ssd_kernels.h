@@ -168,12 +168,12 @@ struct AddNormBwdArgs {
 
 // Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of kScanSegs segments x kScanCh
 // channels.  A segment holds as many tokens as let two tiles' values stay in a thread's registers (one 1 - a
-// per element forwards, two values backwards) and three or four tiles' operands in shared memory; fewer where the
-// operands pass through registers (rows).
+// per element forwards, two values backwards) and three or four tiles' operands in shared memory; fewer where
+// rows are off 16-byte alignment (two values forwards too).
 // A state is handed over once per kScanBlock tiles of a sequence.
 constexpr int kScanSegs = 16, kScanCh = 64, kScanBlock = 16, kScanMinTok = 64;
 constexpr int scan_seg(bool bwd, int dtype, bool rows) {
-    return dtype == 1 /* SSD_BF16 */ ? (bwd ? (rows ? 4 : 8) : (rows ? 8 : 16)) : (bwd || rows ? 4 : 8);
+    return dtype == 1 /* SSD_BF16 */ ? (bwd || rows ? 8 : 16) : (bwd || rows ? 4 : 8);
 }
 struct GateScanArgs {
     int64_t batch, seqlen;

@@ -65,7 +65,7 @@ int check_scan(const ssd_gate_scan_params_t* p) {
     if (p->ndocs > 0 && p->batch != 1) return SSD_ERR_INVALID_ARG;
     const int64_t big = (int64_t)1 << 31;
     // token offsets, tile numbers and the bytes between tokens are 32-bit; element offsets are 64-bit
-    if (p->seqlen >= big - 256 || p->batch >= big || p->batch * p->seqlen >= big << 8 || p->g_stride >= big / 4 ||
+    if (p->seqlen >= big - 256 || p->batch >= big || p->batch * p->seqlen >= big << 2 || p->g_stride >= big / 4 ||
         p->x_stride >= big / 4)
         return SSD_ERR_UNSUPPORTED;
     const int64_t tiles = ((p->seqlen + kScanMinTok - 1) / kScanMinTok) * ((p->width + kScanCh - 1) / kScanCh);

@@ -133,6 +133,16 @@ def test_sequences(case, dtype, states):
     close(got["dinit"], mus, bound, "dinit")
 
 
+# rows off 16-byte alignment fall into classes by their shift: fewer rows than classes, batch rows that start in any of
+# them, strides of every shift
+@pytest.mark.parametrize("batch,seqlen,width,pad,off", [
+    (1, 1, 1, 0, 0), (1, 3, 5, 0, 0), (3, 1, 63, 0, 0), (1, 7, 64, 3, 1), (5, 9, 65, 0, 0), (9, 129, 3, 1, 1), (3, 131, 70, 2, 2),
+    (2, 127, 128, 4, 4), (4, 66, 66, 6, 3), (2, 258, 191, 5, 5), (1, 1030, 12, 1, 0)])
+@pytest.mark.parametrize("dtype", [BF, F4])
+def test_rows_of_every_shift(batch, seqlen, width, pad, off, dtype):
+    test_sequences((batch, seqlen, width, pad, off, None), dtype, True)
+
+
 def test_gradients_against_differences():
     g, x, r = make(2, 150, 6, F4, 4)
     init, dy, dfin = r(2, 6), r(2, 150, 6), r(2, 6)
