@@ -270,8 +270,9 @@ __device__ __forceinline__ void send_block(const uint8_t* block, uint8_t* base, 
         }
     } else {
         // one row at a time, a bf16 per lane
-        for (int row = 0; row < rows; ++row)
-            if (2 * lane < bytes)
+#pragma unroll 8
+        for (int row = 0; row < 32; ++row)
+            if (row < rows && 2 * lane < bytes)
                 *reinterpret_cast<uint16_t*>(base + row * pitch + 2 * lane) =
                     *reinterpret_cast<const uint16_t*>(word_at(blk, row, lane >> 3) + 2 * (lane & 7));
     }
@@ -303,9 +304,13 @@ __device__ __forceinline__ void finish_rows(const LinearArgs& a, const uint32_t 
         if (a.vec) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(word_at(block, 8 * i + (lane >> 2), lane & 3)) = r[i];
-        } else {   // row by row
-            for (int i = 0; i < rows; ++i)
-                if (lane < cols) *reinterpret_cast<bf16_t*>(word_at(block, i, lane >> 3) + 2 * (lane & 7)) = res[at + (size_t)i * a.n + lane];
+        } else {   // an element per lane and row, all of them asked for before the first is used
+            uint16_t e[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                e[i] = i < rows && lane < cols ? __ldcs(reinterpret_cast<const unsigned short*>(res + at + (size_t)i * a.n + lane)) : 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) *reinterpret_cast<uint16_t*>(word_at(block, i, lane >> 3) + 2 * (lane & 7)) = e[i];
         }
         __syncwarp();
 #pragma unroll
