@@ -236,12 +236,14 @@ __device__ __forceinline__ float act_slope(float v, int act) {
     return 1.f;
 }
 
-// One element of y from v, its sum with scales and bias: the rounded v for the backward pass, activation, residual.
-__device__ __forceinline__ void finish(const LinearArgs& a, float v, size_t at) {
+// One element of y from v, its sum with scales and bias: the rounded v for the backward pass, activation, and the
+// residual's element, asked for before (y may be the residual, so a load here would wait for the stores of other elements).
+__device__ __forceinline__ float residual_at(const LinearArgs& a, size_t at) {
+    return a.residual ? __bfloat162float(static_cast<const bf16_t*>(a.residual)[at]) : 0.f;
+}
+__device__ __forceinline__ void finish(const LinearArgs& a, float v, size_t at, float res) {
     if (a.pre) static_cast<bf16_t*>(a.pre)[at] = __float2bfloat16_rn(v);
-    v = act_value(v, a.act);
-    if (a.residual) v += __bfloat162float(static_cast<const bf16_t*>(a.residual)[at]);
-    static_cast<bf16_t*>(a.y)[at] = __float2bfloat16_rn(v);
+    static_cast<bf16_t*>(a.y)[at] = __float2bfloat16_rn(act_value(v, a.act) + res);
 }
 
 // 32 rows of 64 bytes through shared memory, by a warp: lane r has row r as four 16-byte words, and they leave as whole
@@ -537,6 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         const int q = warp & 3;                 // the warp's quarter of tensor memory's lanes
         const int half = (warp - 4) >> 2;       // and half of the columns (all of them in tiles below 64)
         constexpr int kSpan = TN >= 64 ? TN / 2 : TN;
+        constexpr int CW = TN < 32 ? TN : 32;   // columns per read of tensor memory
+        constexpr bool kMaySwap = TN <= kLinearSwap;
+        static_assert(!kMaySwap || kSpan == CW, "a transposed tile's threads have one read each");
         uint8_t* block = sm + C::kBlocks + (warp - 4) * 2048;
         uint32_t tile = 0;
         for (int item = worker; item < p.items; item += workers, ++tile) {
@@ -564,6 +569,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             const bool ask = whole && a.residual && a.vec;
             uint4 res[4], next[4];
             if (ask) ask_residual(a, res, row0, c * TN + (TN >= 64 ? half * kSpan : 0));
+            // transposed: the residual's elements and x's scales of this thread's only columns
+            float tr[kMaySwap ? CW : 1], tx[kMaySwap ? CW : 1];
+            if (kMaySwap && a.swap) {
+                const int col = c * TN + (TN >= 64 ? half * kSpan : 0);
+#pragma unroll
+                for (int k = 0; k < CW; ++k) {
+                    const bool in = row_ok && i.part < 0 && col + k < ncol;
+                    tr[k] = in ? residual_at(a, (size_t)(col + k) * a.n + row) : 0.f;
+                    tx[k] = in && a.x_scales ? rs * __ldg(a.x_scales + col + k) : 1.f;
+                }
+            }
             bool ok = true;
             if (lane == 0) ok = lin_wait(sh, a.ws, &sh.acc[buf], (tile >> 1) & 1, kWhereAcc);
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -572,7 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t d = tb + buf * TN + ((uint32_t)(32 * q) << 16) + (TN >= 64 ? half * kSpan : 0);
-            constexpr int CW = TN < 32 ? TN : 32;   // columns per read of tensor memory
             const bool idle = TN < 64 && half;
 #pragma unroll 1
             for (int j = 0; j < kSpan; j += CW) {
@@ -602,16 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                     for (int k = 0; k < CW; k += 4)
                         part[(k / 4) * kRows] = make_float4(__uint_as_float(w[k]), __uint_as_float(w[k + 1]), __uint_as_float(w[k + 2]),
                                                             __uint_as_float(w[k + 3]));
-                } else if (a.swap) {
+                } else if (kMaySwap && a.swap) {
                     // a lane per column of y: 32 of them lie together in a row
-                    if (row_ok && i.part < 0) {
+                    if (row_ok) {
 #pragma unroll
                         for (int k = 0; k < CW; ++k)
-                            if (col + k < ncol) {
-                                float v = __uint_as_float(w[k]);
-                                if (a.x_scales) v *= rs * __ldg(a.x_scales + col + k);
-                                finish(a, v + rb, (size_t)(col + k) * a.n + row);
-                            }
+                            if (col + k < ncol) finish(a, __uint_as_float(w[k]) * tx[k] + rb, (size_t)(col + k) * a.n + row, tr[k]);
                     }
                 } else if constexpr (CW == 32) {
                     const int k = TN >= 64 ? half * kSpan + j : j;
@@ -646,36 +657,34 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
     const int row = (w % groups) * down + lane / across, quad = (w / groups) * across + lane % across;
     const float4* part = reinterpret_cast<const float4*>(a.parts) + ((size_t)tile * p.splits * (tn / 4) + quad) * tm + row;
     const int dr = r * tm + row, dc = c * tn + 4 * quad;
+    const bool some = dr < (a.swap ? a.n : a.m) && dc < (a.swap ? a.m : a.n);
+    // what the call brought is there already
+    const int ncol = a.swap ? (int)a.m : a.n;
+    const float* along = a.swap ? a.x_scales : a.w_scales;   // scales by D's columns
+    const float down_scale = a.x_scales && some ? __ldg((a.swap ? a.w_scales : a.x_scales) + dr) : 1.f;
+    float res[4], scale[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool in = some && dc + e < ncol;
+        scale[e] = in && a.x_scales ? down_scale * __ldg(along + dc + e) : 1.f;
+        bias[e] = in && a.bias ? __ldg(a.bias + (a.swap ? dr : dc + e)) : 0.f;
+        res[e] = in && (a.swap || !a.vec) ? residual_at(a, a.swap ? (size_t)(dc + e) * a.n + dr : (size_t)dr * a.n + dc + e) : 0.f;
+    }
     pdl_wait();   // launched while the parts are still being made
-    if (dr >= (a.swap ? a.n : a.m) || dc >= (a.swap ? a.m : a.n)) return;
+    if (!some) return;
     float v[4];
+#pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
         const float4 q = __ldcs(part + (size_t)s * (tn / 4) * tm);
         const float u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = s ? v[e] + u[e] : u[e];
     }
-    if (a.swap) {
-        const float ws = a.x_scales ? __ldg(a.w_scales + dr) : 1.f, b = a.bias ? __ldg(a.bias + dr) : 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (dc + e < a.m) {
-                if (a.x_scales) v[e] *= __ldg(a.x_scales + dc + e) * ws;
-                finish(a, v[e] + b, (size_t)(dc + e) * a.n + dr);
-            }
-        return;
-    }
-    const int64_t m = dr;
-    const int n = dc;
-    const float xs = a.x_scales ? __ldg(a.x_scales + m) : 1.f;
-    const size_t at = (size_t)m * a.n + n;
-    if (a.vec) {   // n is a multiple of 8: the four columns exist and are aligned
+    for (int e = 0; e < 4; ++e) v[e] = v[e] * scale[e] + bias[e];
+    if (!a.swap && a.vec) {   // n is a multiple of 8: the four columns exist and are aligned
+        const size_t at = (size_t)dr * a.n + dc;
         Raw<bf16_t, 4> o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (a.x_scales) v[e] *= xs * __ldg(a.w_scales + n + e);
-            if (a.bias) v[e] += __ldg(a.bias + n + e);
-        }
         if (a.pre) {
             o.set(v);
             o.store(static_cast<bf16_t*>(a.pre) + at);
@@ -694,11 +703,7 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (n + e < a.n) {
-                if (a.x_scales) v[e] *= xs * __ldg(a.w_scales + n + e);
-                if (a.bias) v[e] += __ldg(a.bias + n + e);
-                finish(a, v[e], at + e);
-            }
+            if (dc + e < ncol) finish(a, v[e], a.swap ? (size_t)(dc + e) * a.n + dr : (size_t)dr * a.n + dc + e, res[e]);
     }
 }
 
