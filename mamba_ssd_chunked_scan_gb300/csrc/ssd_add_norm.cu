@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
     const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
     const int nt = one_warp ? 32 : blockDim.x;
     const int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot;
+    pdl_trigger();   // a projection of the rows may prepare while the last of them are written
     if (row >= a.rows) return;   // whole warps of a many-row CTA, which has no barrier
     const int W = a.width;
     const size_t base = (size_t)row * W;

@@ -408,13 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ Small sh;
     const LinearArgs& a = p.a;
-    pdl_trigger();   // the join may start on the threads that this grid leaves free
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kElems = E4M3 ? 128 : 64;   // contraction elements per stage
     const int rank = PAIR ? (int)cluster_rank() : 0;
     const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
     if (threadIdx.x == 0) {
-        if (blockIdx.x == 0 && a.ws && !a.keep_status) a.ws->status = 0;   // a wait gives up after seconds, long after this
         for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(&sh.full[i], 1);
             ptx::mbar_init(&sh.empty[i], 1);
@@ -436,9 +434,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tb = sh.tmem_base;
-
-    if (warp == 0) {
+    // So far nothing was read or written that earlier launches may still be working on: this one may start while they
+    // end.  Whoever goes on to global memory waits for them.
+    if (warp == 3) {
+        pdl_wait();
+        if (blockIdx.x == 0 && lane == 0 && a.ws && !a.keep_status) a.ws->status = 0;   // a wait gives up seconds after this
+        pdl_trigger();   // the join may start on the threads that this grid leaves free; what the call brought is there
+    } else if (warp == 0) {
         // ---------------------------------------------------------------- loads
+        pdl_wait();
         uint32_t it = 0, st = 0, phase = 0;
         bool go = true;
         for (int item = worker; go && item < p.items; item += workers) {
@@ -541,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         constexpr int kSpan = TN >= 64 ? TN / 2 : TN;
         constexpr int CW = TN < 32 ? TN : 32;   // columns per read of tensor memory
         constexpr bool kMaySwap = TN <= kLinearSwap;
+        pdl_wait();
         static_assert(!kMaySwap || kSpan == CW, "a transposed tile's threads have one read each");
         uint8_t* block = sm + C::kBlocks + (warp - 4) * 2048;
         uint32_t tile = 0;
@@ -657,6 +662,7 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
     const int row = (w % groups) * down + lane / across, quad = (w / groups) * across + lane % across;
     const float4* part = reinterpret_cast<const float4*>(a.parts) + ((size_t)tile * p.splits * (tn / 4) + quad) * tm + row;
     const int dr = r * tm + row, dc = c * tn + 4 * quad;
+    pdl_trigger();
     const bool some = dr < (a.swap ? a.n : a.m) && dc < (a.swap ? a.m : a.n);
     // what the call brought is there already
     const int ncol = a.swap ? (int)a.m : a.n;
@@ -716,6 +722,7 @@ template <int V>
 __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     __shared__ float part[8][kSlabCols];
     constexpr int C = 8 / V, kRowsAhead = 4;
+    pdl_trigger();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const unsigned ncol = (unsigned)(a.n + kSlabCols - 1) / kSlabCols, slab = blockIdx.x / ncol;
     const int c0 = (int)(blockIdx.x - slab * ncol) * kSlabCols, n0 = c0 + lane * V;
@@ -784,6 +791,8 @@ __global__ void __launch_bounds__(1024) ssd_linear_dbias(const float* shares, in
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + lane;
     float s = 0.f;
+    pdl_trigger();
+    pdl_wait();   // launched while the shares are still being summed
     if (e < n)
         for (int k = w; k < nshares; k += 32) s += shares[(size_t)k * n + e];
     part[w][lane] = s;
@@ -823,13 +832,15 @@ cudaError_t launch_tile(const LinearParams& p, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 1 : 0;
+    cfg.numAttrs = PAIR ? 2 : 1;
     int most = workers[dev].load(std::memory_order_acquire);
     if (most == 0) {
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
@@ -964,8 +975,8 @@ cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st) {
     else ssd_linear_dpre<1><<<grid, 256, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dbias) return e;
-    ssd_linear_dbias<<<(unsigned)((a.n + 31) / 32), 1024, 0, st>>>(a.shares, (int)slabs, a.n, a.dbias);
-    return cudaGetLastError();
+    return launch_kernel(ssd_linear_dbias, (unsigned)((a.n + 31) / 32), 1024, 0, st, true, (const float*)a.shares, (int)slabs, a.n,
+                         a.dbias);
 }
 
 }  // namespace ssd
