@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
     const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
     const int nt = one_warp ? 32 : blockDim.x;
     const int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot;
-    pdl_trigger();   // a projection of the rows may prepare while the last of them are written
+    pdl_wait();
     if (row >= a.rows) return;   // whole warps of a many-row CTA, which has no barrier
     const int W = a.width;
     const size_t base = (size_t)row * W;
@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(THREADS) ssd_add_norm_bwd_kernel(AddNormBwdArg
     const int nt = one_warp ? 32 : blockDim.x;
     const int W = a.width;
     pdl_trigger();
+    pdl_wait();
     const int64_t stride = (int64_t)gridDim.x * a.rows_per_cta;
     int64_t row = (int64_t)blockIdx.x * a.rows_per_cta + slot;
     const int shift = SHIFTED ? (int)((uint64_t)(row * W) % V) : 0;
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_bwd_reduce(const float* sha
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + lane;
     float s = 0.f;
+    pdl_trigger();
     pdl_wait();   // launched while the shares are still being summed
     if (e < W)
         for (int k = w; k < nshares; k += 32) s += shares[(size_t)k * W + e];
@@ -376,11 +378,7 @@ cudaError_t launch_fwd_typed(const AddNormArgs& a, int threads, cudaStream_t st)
     constexpr int V = 16 / sizeof(T);
     const bool vec = a.width % V == 0 && on16(a.weight) && on16(a.x) && on16(a.residual) && on16(a.out) && on16(a.residual_out);
     const unsigned grid = (unsigned)((a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
-    if (vec)
-        ssd_add_norm_kernel<T, R, O, V><<<grid, threads, 0, st>>>(a);
-    else
-        ssd_add_norm_kernel<T, R, O, 1><<<grid, threads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(vec ? ssd_add_norm_kernel<T, R, O, V> : ssd_add_norm_kernel<T, R, O, 1>, grid, (unsigned)threads, 0, st, true, a);
 }
 
 template <typename T, typename R>
@@ -437,8 +435,7 @@ cudaError_t launch_bwd_typed(AddNormBwdArgs& a, int64_t* nshares, cudaStream_t s
         kern = !vec      ? ssd_add_norm_bwd_kernel<T, R, 1, kElems, 1024, false>
                : shifted ? ssd_add_norm_bwd_kernel<T, R, V, kElems, 1024, true>
                          : ssd_add_norm_bwd_kernel<T, R, V, kElems, 1024, false>;
-    kern<<<(unsigned)grid, threads < 1024 ? threads : 1024, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(kern, (unsigned)grid, threads < 1024 ? threads : 1024, 0, st, true, a);
 }
 
 }  // namespace

@@ -776,6 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
     __syncthreads();
     // The workspace is being cleared by the launch before, which this one does not wait for to start: whoever uses the
     // workspace does.  (What earlier work left for this call is there: the clearing waited for it.)
+    // It does not let its own successor start early: a clearing that waits on the SMs costs 65536 x 2048 2 us.
     if (warp >= kMain) pdl_wait();
     if (warp < kMain) {
         Main<T, ROWS, DOCS, BWD> m = {p.a, sh, (int)(threadIdx.x & 31), warp};
@@ -791,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
 }
 
 __global__ void __launch_bounds__(256) ssd_gate_scan_clear(uint4* p, size_t words) {
+    pdl_wait();      // (in this order: what earlier launches leave is there when the main one starts)
     pdl_trigger();
     for (size_t k = (size_t)blockIdx.x * 256 + threadIdx.x; k < words; k += (size_t)gridDim.x * 256) p[k] = make_uint4(0, 0, 0, 0);
 }
@@ -798,6 +800,8 @@ __global__ void __launch_bounds__(256) ssd_gate_scan_clear(uint4* p, size_t word
 // One token per batch row: V channels per thread.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) ssd_gate_scan_step_kernel(GateStepArgs a) {
+    pdl_trigger();
+    pdl_wait();
     const int per_row = (a.width + V - 1) / V;
     const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (k >= a.batch * per_row) return;
@@ -967,8 +971,8 @@ cudaError_t launch_gate_scan(const GateScanArgs& args, void* workspace, bool bwd
     // status word, tickets, maps and carried states start from zero
     if (workspace) {
         const size_t words = l.total / 16, ctas = (words + 1023) / 1024;
-        ssd_gate_scan_clear<<<(unsigned)(ctas < 304 ? ctas : 304), 256, 0, st>>>(static_cast<uint4*>(workspace), words);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_kernel(ssd_gate_scan_clear, (unsigned)(ctas < 304 ? ctas : 304), 256, 0, st, true,
+                                            static_cast<uint4*>(workspace), words);
         if (e != cudaSuccess) return e;
     }
     if (a.dtype == SSD_BF16) return bwd ? launch_typed<bf16_t, true>(a, rows, st) : launch_typed<bf16_t, false>(a, rows, st);
@@ -981,14 +985,10 @@ cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st) {
                      on(a.y, 4 * e) && on(a.state_in, 16) && on(a.state_out, 16);
     const int64_t n = a.batch * ((a.width + (vec ? 3 : 0)) / (vec ? 4 : 1));
     const unsigned grid = (unsigned)((n + 255) / 256);
-    if (a.dtype == SSD_BF16) {
-        if (vec) ssd_gate_scan_step_kernel<bf16_t, 4><<<grid, 256, 0, st>>>(a);
-        else ssd_gate_scan_step_kernel<bf16_t, 1><<<grid, 256, 0, st>>>(a);
-    } else {
-        if (vec) ssd_gate_scan_step_kernel<float, 4><<<grid, 256, 0, st>>>(a);
-        else ssd_gate_scan_step_kernel<float, 1><<<grid, 256, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    void (*const kern)(GateStepArgs) =
+        a.dtype == SSD_BF16 ? (vec ? ssd_gate_scan_step_kernel<bf16_t, 4> : ssd_gate_scan_step_kernel<bf16_t, 1>)
+                            : (vec ? ssd_gate_scan_step_kernel<float, 4> : ssd_gate_scan_step_kernel<float, 1>);
+    return launch_kernel(kern, grid, 256, 0, st, true, a);
 }
 
 }  // namespace ssd

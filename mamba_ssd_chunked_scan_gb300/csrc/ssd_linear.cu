@@ -723,6 +723,7 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     __shared__ float part[8][kSlabCols];
     constexpr int C = 8 / V, kRowsAhead = 4;
     pdl_trigger();
+    pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const unsigned ncol = (unsigned)(a.n + kSlabCols - 1) / kSlabCols, slab = blockIdx.x / ncol;
     const int c0 = (int)(blockIdx.x - slab * ncol) * kSlabCols, n0 = c0 + lane * V;
@@ -971,9 +972,8 @@ int64_t linear_dpre_slabs(int64_t m) { return (m + kSlabRows - 1) / kSlabRows; }
 cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st) {
     const int64_t slabs = linear_dpre_slabs(a.m);
     const unsigned grid = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
-    if (a.n % 8 == 0 && ((uintptr_t)a.pre & 15) == 0) ssd_linear_dpre<8><<<grid, 256, 0, st>>>(a);
-    else ssd_linear_dpre<1><<<grid, 256, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const bool vec = a.n % 8 == 0 && ((uintptr_t)a.pre & 15) == 0;
+    const cudaError_t e = launch_kernel(vec ? ssd_linear_dpre<8> : ssd_linear_dpre<1>, grid, 256, 0, st, true, a);
     if (e != cudaSuccess || !a.dbias) return e;
     return launch_kernel(ssd_linear_dbias, (unsigned)((a.n + 31) / 32), 1024, 0, st, true, (const float*)a.shares, (int)slabs, a.n,
                          a.dbias);
