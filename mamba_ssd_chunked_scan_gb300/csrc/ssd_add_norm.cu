@@ -6,8 +6,8 @@
 //   ssd_add_norm_bwd_reduce   dw from the shares, in a fixed order
 //
 // A row is held in registers from its one read to its one write, so both passes
-// are bound by HBM: 16384 x 2560, bf16 with an fp32 residual, 75.7 us forward (6.65 TB/s), e4m3 rows 72 us;
-// 12289 x 2560 backward 82 us (6.1 TB/s; a plain copy reaches 6.77).  A row belongs to consecutive threads of a CTA, 16
+// are bound by HBM: 16384 x 2560, bf16 with an fp32 residual, 73.9 us forward (6.81 TB/s), e4m3 rows 69 us;
+// 12289 x 2560 backward 81.6 us (6.2 TB/s; a plain copy reaches 6.77).  A row belongs to consecutive threads of a CTA, 16
 // elements each (8 or 16 in the backward): as 16-byte vectors of x where the width and the addresses
 // allow (in the backward, whatever the width), one by one (strided by the row's threads, so that a warp's accesses
 // stay contiguous) where they do not.  Rows that fit a warp take one

@@ -33,9 +33,9 @@
 //
 // A document's first token cuts the map (A = 0) and takes the document's own state.
 //
-// Measured: 65536 x 2048 bf16 in one row, strided, 140 us (5.8 TB/s; the bytes need 119 us at the rate of a copy), bound by
+// Measured: 65536 x 2048 bf16 in one row, strided, 139 us (5.8 TB/s; the bytes need 119 us at the rate of a copy), bound by
 // the main warps' two visits (about 3800 of a tile's 4700 cycles) and by reads of 5.4 TB/s without the rest; fp32
-// 255 us (93 %); 8 x 2048 x 5120 bf16 backward 137 us (6.1 TB/s); 32767 x 1533, 37 documents, 93 us (1536 columns 71):
+// 255 us (93 %); 8 x 2048 x 5120 bf16 backward 135 us (6.2 TB/s); 32767 x 1533, 37 documents, 91 us (1536 columns 70):
 // elements off alignment are read from shared memory and stored one by one, and tiles are half as long.  (Loaded by
 // elements into registers, a tile ahead: 99 us, 65536 x 2047 231 instead of 190, 8 x 2048 x 5119 backward 224 instead of 202.)
 //

@@ -20,10 +20,10 @@
 // fill the 128 rows of a tile and x is the narrow operand, so the MMAs and the loads are W's
 // and almost nothing is padding; its bound is W's one pass from HBM.
 //
-// Measured: 16384 x 10240 x 2560 bf16 435 us back to back (1.97 PFLOP/s; the library's product 419) and 508 under
-// the power cap (1.69; the library's sustained rate 1.72); both gradients of it 906 us (library 880); e4m3
-// 4099 x 2560 x 5120 with its residual 49 us, from HBM; 8 rows of e4m3 by 10240 x 2560 10 us, of which
-// W's bytes need 3.9.  dpre of 8192 x 5120 41 us (6.1 TB/s).
+// Measured: 16384 x 10240 x 2560 bf16 430-435 us back to back (1.97 PFLOP/s; the library's product 419) and 507 under
+// the power cap (1.69; the library's sustained rate 1.72); both gradients of it 906-928 us (library 880); e4m3
+// 4099 x 2560 x 5120 with its residual 46 us, from HBM; 8 rows of e4m3 by 10240 x 2560 7.2 us in a graph, of which
+// W's bytes need 3.9.  dpre of 8192 x 5120 42 us (6.0 TB/s).
 //
 // Sums are fp32 in tensor memory.  Tiles run in waves of one per SM (or pair); those of the last wave, which would
 // leave SMs idle, are split along the contraction into parts that are summed in a fixed order
