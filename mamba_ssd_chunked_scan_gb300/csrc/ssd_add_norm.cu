@@ -7,7 +7,7 @@
 //
 // A row is held in registers from its one read to its one write, so both passes
 // are bound by HBM: 16384 x 2560, bf16 with an fp32 residual, 73.9 us forward (6.81 TB/s), e4m3 rows 69 us;
-// 12289 x 2560 backward 81.6 us (6.2 TB/s; a plain copy reaches 6.77).  A row belongs to consecutive threads of a CTA, 16
+// 12289 x 2560 backward 80.7 us (6.2 TB/s; a plain copy reaches 6.77).  A row belongs to consecutive threads of a CTA, 16
 // elements each (8 or 16 in the backward): as 16-byte vectors of x where the width and the addresses
 // allow (in the backward, whatever the width), one by one (strided by the row's threads, so that a warp's accesses
 // stay contiguous) where they do not.  Rows that fit a warp take one
@@ -326,21 +326,26 @@ __global__ void __launch_bounds__(THREADS) ssd_add_norm_bwd_kernel(AddNormBwdArg
     }
 }
 
-// dw[e] = sum over the shares: 32 columns per CTA, the shares dealt to its 32
-// warps, whose sums are added in warp order.
+// dw[e] = sum over the shares: COLS columns (16 or 32) per CTA, the shares dealt to its 1024 / COLS rows of threads, whose
+// sums are added in their order.
+template <int COLS>
 __global__ void __launch_bounds__(1024) ssd_add_norm_bwd_reduce(const float* shares, int nshares, int W, float* dw) {
-    __shared__ float part[32][33];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int e = blockIdx.x * 32 + lane;
+    __shared__ float part[32][COLS + 1];
+    const int lane = threadIdx.x % COLS, w = threadIdx.x / COLS;
+    const int e = blockIdx.x * COLS + lane;
     float s = 0.f;
     pdl_trigger();
     pdl_wait();   // launched while the shares are still being summed
-    if (e < W)
-        for (int k = w; k < nshares; k += 32) s += shares[(size_t)k * W + e];
-    part[w][lane] = s;
+    if (e < W) {
+#pragma unroll 4
+        for (int k = w; k < nshares; k += 1024 / COLS) s += shares[(size_t)k * W + e];
+    }
+    if (COLS == 16) s += __shfl_xor_sync(0xffffffffu, s, 16);   // the warp's two rows
+    if ((threadIdx.x & 31) < COLS) part[threadIdx.x >> 5][lane] = s;
     __syncthreads();
-    if (w == 0 && e < W) {
+    if (threadIdx.x < COLS && e < W) {
         float t = 0.f;
+#pragma unroll
         for (int k = 0; k < 32; ++k) t += part[k][lane];
         dw[e] = t;
     }
@@ -470,8 +475,10 @@ cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& args, cudaStream_t st) {
     else
         e = launch_bwd_typed<float, float>(a, &nshares, st);
     if (e != cudaSuccess) return e;
-    return launch_kernel(ssd_add_norm_bwd_reduce, (unsigned)((a.width + 31) / 32), 1024, 0, st, true, (const float*)a.shares,
-                         (int)nshares, a.width, a.dweight);
+    // 16 columns a CTA while all CTAs run at once (20000 x 256 in a graph 17.2 us, with 32 18.6; 4096 x 8192 94 and 89)
+    const int cols = a.width <= 16 * 2 * kAddNormSMs ? 16 : 32;
+    return launch_kernel(cols == 16 ? ssd_add_norm_bwd_reduce<16> : ssd_add_norm_bwd_reduce<32>, (unsigned)((a.width + cols - 1) / cols),
+                         1024, 0, st, true, (const float*)a.shares, (int)nshares, a.width, a.dweight);
 }
 
 }  // namespace ssd
