@@ -264,6 +264,7 @@ struct LinearDpreArgs {
     void* dpre;            // (m, ldp) bf16, or NULL
     float* shares;         // [slabs * n], or NULL
     float* dbias;          // [n], or NULL
+    int slab_rows;
 };
 
 // Constants of division by an invariant divisor d >= 1 through one high
@@ -309,7 +310,7 @@ cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st);
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // NULL when the driver has none
 LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap);
 cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& plan, cudaStream_t st);
-int64_t linear_dpre_slabs(int64_t m);
+int64_t linear_dpre_slabs(int64_t m, int n);
 cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st);
 size_t bwd_smem_bytes(int Qb, int P, int N);
 int bwd_chunk(int P, int N, size_t smem_limit);

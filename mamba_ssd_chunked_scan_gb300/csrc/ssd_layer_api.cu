@@ -102,7 +102,7 @@ LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p) {
     l.ldp = (p->n + 7) / 8 * 8;
     l.dpre_off = sizeof(WsHeader);
     l.shares_off = l.dpre_off + (l.own_dpre ? align_up((size_t)p->m * l.ldp * 2, 256) : 0);
-    l.parts_off = l.shares_off + align_up((size_t)linear_dpre_slabs(p->m) * p->n * 4, 256);
+    l.parts_off = l.shares_off + align_up((size_t)linear_dpre_slabs(p->m, p->n) * p->n * 4, 256);
     l.dx = linear_plan(p->m, p->k, (int64_t)p->n * 2, false);
     l.dw = linear_plan(p->n, p->k, p->m * 2, false);
     l.total = l.parts_off + (l.dx.parts_bytes > l.dw.parts_bytes ? l.dx.parts_bytes : l.dw.parts_bytes);

@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
 }
 
 // dpre = dy act'(pre), rounded to bf16 into rows of ldp elements, and each row slab's sums over its
-// rows (of the unrounded products).  A CTA takes 256 columns of kSlabRows rows, a warp every eighth row, a lane eight
+// rows (of the unrounded products).  A CTA takes 256 columns of up to kSlabRows rows, a warp every eighth row, a lane eight
 // columns: together (V = 8: rows are whole 16-byte words) or 32 apart (V = 1).  Bound by HBM: four rows' loads are in
 // flight per warp.
 constexpr int kSlabRows = 128, kSlabCols = 256;
@@ -725,10 +725,10 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const unsigned ncol = (unsigned)(a.n + kSlabCols - 1) / kSlabCols, slab = blockIdx.x / ncol;
+    const unsigned ncol = (unsigned)(a.n + kSlabCols - 1) / kSlabCols, slab = blockIdx.x / ncol, slab_rows = a.slab_rows;
     const int c0 = (int)(blockIdx.x - slab * ncol) * kSlabCols, n0 = c0 + lane * V;
-    const int64_t m0 = (int64_t)slab * kSlabRows;
-    const int rows = a.m - m0 < kSlabRows ? (int)(a.m - m0) : kSlabRows;
+    const int64_t m0 = (int64_t)slab * slab_rows;
+    const int rows = a.m - m0 < slab_rows ? (int)(a.m - m0) : (int)slab_rows;
     const bf16_t* dy = static_cast<const bf16_t*>(a.dy) + (size_t)m0 * a.n + n0;
     const bf16_t* pre = a.pre ? static_cast<const bf16_t*>(a.pre) + (size_t)m0 * a.n + n0 : nullptr;
     bf16_t* dp = a.dpre ? static_cast<bf16_t*>(a.dpre) + (size_t)m0 * a.ldp + n0 : nullptr;
@@ -967,10 +967,24 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     return launch_kernel(ssd_linear_join, (unsigned)(rest * (tm * tn / 1024)), 256, 0, st, true, p, tm, tn);
 }
 
-int64_t linear_dpre_slabs(int64_t m) { return (m + kSlabRows - 1) / kSlabRows; }
+// Rows of a slab: kSlabRows, which keeps the shares few, or fewer where that would leave SMs idle (both gradients of
+// 2307 x 1783 x 656 57 us with 128 rows, 46 with 32).
+static int dpre_slab_rows(int64_t m, int n) {
+    const int64_t ncol = (n + kSlabCols - 1) / kSlabCols;
+    int rows = kSlabRows;
+    while (rows > 32 && (m + rows - 1) / rows * ncol < 4 * kLinearSMs) rows /= 2;
+    return rows;
+}
 
-cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st) {
-    const int64_t slabs = linear_dpre_slabs(a.m);
+int64_t linear_dpre_slabs(int64_t m, int n) {
+    const int rows = dpre_slab_rows(m, n);
+    return (m + rows - 1) / rows;
+}
+
+cudaError_t launch_linear_dpre(const LinearDpreArgs& args, cudaStream_t st) {
+    LinearDpreArgs a = args;
+    a.slab_rows = dpre_slab_rows(a.m, a.n);
+    const int64_t slabs = linear_dpre_slabs(a.m, a.n);
     const unsigned grid = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
     const bool vec = a.n % 8 == 0 && ((uintptr_t)a.pre & 15) == 0;
     const cudaError_t e = launch_kernel(vec ? ssd_linear_dpre<8> : ssd_linear_dpre<1>, grid, 256, 0, st, true, a);
