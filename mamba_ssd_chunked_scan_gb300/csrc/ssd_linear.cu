@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
     if (warp == 3) {
         pdl_wait();
         if (blockIdx.x == 0 && lane == 0 && a.ws && !a.keep_status) a.ws->status = 0;   // a wait gives up seconds after this
-        pdl_trigger();   // the join may start on the threads that this grid leaves free; what the call brought is there
+        pdl_trigger();   // the join may start on the threads that this grid leaves free
     } else if (warp == 0) {
         // ---------------------------------------------------------------- loads
         pdl_wait();
@@ -664,20 +664,21 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
     const int dr = r * tm + row, dc = c * tn + 4 * quad;
     pdl_trigger();
     const bool some = dr < (a.swap ? a.n : a.m) && dc < (a.swap ? a.m : a.n);
-    // what the call brought is there already
+    // Launched while the parts are still being made.  Nothing is read before this, the call's scales, bias and residual
+    // neither: that the launch before has seen what earlier ones wrote to them does not make it visible here.
+    pdl_wait();
+    if (!some) return;
     const int ncol = a.swap ? (int)a.m : a.n;
     const float* along = a.swap ? a.x_scales : a.w_scales;   // scales by D's columns
-    const float down_scale = a.x_scales && some ? __ldg((a.swap ? a.w_scales : a.x_scales) + dr) : 1.f;
+    const float down_scale = a.x_scales ? __ldg((a.swap ? a.w_scales : a.x_scales) + dr) : 1.f;
     float res[4], scale[4], bias[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const bool in = some && dc + e < ncol;
+        const bool in = dc + e < ncol;
         scale[e] = in && a.x_scales ? down_scale * __ldg(along + dc + e) : 1.f;
         bias[e] = in && a.bias ? __ldg(a.bias + (a.swap ? dr : dc + e)) : 0.f;
         res[e] = in && (a.swap || !a.vec) ? residual_at(a, a.swap ? (size_t)(dc + e) * a.n + dr : (size_t)dr * a.n + dc + e) : 0.f;
     }
-    pdl_wait();   // launched while the parts are still being made
-    if (!some) return;
     float v[4];
 #pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
