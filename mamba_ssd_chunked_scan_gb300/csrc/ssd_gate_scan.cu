@@ -774,10 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
         ptx::mbar_fence_init();
     }
     __syncthreads();
-    // The workspace is being cleared by the launch before, which this one does not wait for to start: whoever uses the
-    // workspace does.  (What earlier work left for this call is there: the clearing waited for it.)
+    // The workspace is being cleared by the launch before, which this one does not wait for to start.  Every warp waits here:
+    // the main ones read states, and that the clearing has seen what earlier work wrote to them does not make it visible here.
     // It does not let its own successor start early: a clearing that waits on the SMs costs 65536 x 2048 2 us.
-    if (warp >= kMain) pdl_wait();
+    pdl_wait();
     if (warp < kMain) {
         Main<T, ROWS, DOCS, BWD> m = {p.a, sh, (int)(threadIdx.x & 31), warp};
         m.run(sm);
@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_gate_scan_kernel(const __grid
 }
 
 __global__ void __launch_bounds__(256) ssd_gate_scan_clear(uint4* p, size_t words) {
-    pdl_wait();      // (in this order: what earlier launches leave is there when the main one starts)
+    pdl_wait();      // (in this order: this launch's end is then the end of all before it)
     pdl_trigger();
     for (size_t k = (size_t)blockIdx.x * 256 + threadIdx.x; k < words; k += (size_t)gridDim.x * 256) p[k] = make_uint4(0, 0, 0, 0);
 }

@@ -100,3 +100,42 @@ def test_norm_scales_feed_a_split_product():
         wait()
 
     chain(step, lambda: out)
+
+
+# batch, tokens, width, documents: one tile, several, rows off 16-byte alignment, documents whose states the main warps read
+@pytest.mark.parametrize("batch,seqlen,width,docs", [(3, 100, 64, None), (2, 1500, 128, None), (2, 1500, 61, None), (1, 1500, 128, [1, 200, 3, 1296]),
+                                                     (1, 1500, 61, [700, 1, 1, 798])])
+@pytest.mark.parametrize("dtype", [BF, F4])
+def test_recurrence_on_rewritten_states(batch, seqlen, width, docs, dtype):
+    """The final states of one call, copied over its initial states, are the next one's."""
+    g = gen(seqlen + width)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    gates, xs = [(r(batch, seqlen, width) + 3).to(dtype) for _ in range(3)], [r(batch, seqlen, width).to(dtype) for _ in range(2)]
+    dy = r(batch, seqlen, width).to(dtype)
+    n = len(docs) if docs else batch
+    cu = torch.tensor([sum(docs[:k]) for k in range(n + 1)], dtype=torch.int32, device="cuda") if docs else None
+    start, dstart = r(n, width), r(n, width)
+    init, dfin, out = start.clone(), dstart.clone(), []
+
+    def step(i, wait):
+        if i == 0:
+            init.copy_(start)
+            dfin.copy_(dstart)
+        wait()
+        y, fin = ssd.gate_scan(gates[i % 3], xs[i % 2], init, cu, return_final_states=True)
+        wait()
+        got = ssd.gate_scan_bwd(gates[i % 3], xs[i % 2], y, dy, init, dfin, cu)
+        wait()
+        # from one call to the next without anything between: a step updates the states in place
+        again = ssd.gate_scan(gates[i % 3], xs[i % 2], fin, cu, return_final_states=True)
+        wait()
+        ssd.gate_scan_step(again[1], gates[i % 3][0, :1].expand(n, width).contiguous(), xs[i % 2][0, :1].expand(n, width).contiguous())
+        wait()
+        last = ssd.gate_scan(gates[i % 3], xs[i % 2], again[1], cu)
+        wait()
+        init.copy_(fin)
+        dfin.copy_(got["dinit"] + 1)
+        wait()
+        out[:] = [y, fin, got["dg"], got["dx"], got["dinit"], again[0], again[1], last]
+
+    chain(step, lambda: out)
