@@ -12,7 +12,7 @@
 //   loading    takes the next tile by ticket and brings its inputs into a ring of shared-memory stages (TMA), and
 //              sends a finished tile's outputs off from the same stage.  Where rows are not aligned to 16 bytes
 //              they come by their alignment's classes, and the main warps store the outputs themselves;
-//   main       forms the next tile's decays and its segment's map, keeping 1 - a in registers; then waits for
+//   main       forms the next tile's decays and its segment's map, keeping exp(-g) in registers; then waits for
 //              the state that enters its segment of the tile before, walks that segment again and writes the
 //              outputs.  So a tile's state has a whole tile's time to arrive;
 //   hand-over  one warp composes the segments' maps to the tile's and publishes it; two (a thread per channel) work out the
@@ -33,15 +33,16 @@
 //
 // A document's first token cuts the map (A = 0) and takes the document's own state.
 //
-// Measured: 65536 x 2048 bf16 in one row, strided, 139 us (5.8 TB/s; the bytes need 119 us at the rate of a copy), bound by
-// the main warps' two visits (about 3800 of a tile's 4700 cycles) and by reads of 5.4 TB/s without the rest; fp32
-// 255 us (93 %); 8 x 2048 x 5120 bf16 backward 135 us (6.2 TB/s); 32767 x 1533, 37 documents, 91 us (1536 columns 70):
+// Measured: 65536 x 2048 bf16 in one row, strided, 143 us (5.6 TB/s; the bytes need 119 us at the rate of a copy), bound by
+// the main warps' two visits and by reads of 5.4 TB/s without the rest; fp32
+// 251 us (95 %); 8 x 2048 x 5120 bf16 backward 135 us (6.2 TB/s); 32767 x 1533, 37 documents, 89 us (1536 columns 71):
 // elements off alignment are read from shared memory and stored one by one, and tiles are half as long.  (Loaded by
-// elements into registers, a tile ahead: 99 us, 65536 x 2047 231 instead of 190, 8 x 2048 x 5119 backward 224 instead of 202.)
+// elements into registers, a tile ahead: 99 us, 65536 x 2047 231 instead of 185, 8 x 2048 x 5119 backward 224 instead of 190.)
 //
-// 1 - a is formed as e / (1 + e), e = exp(-g), not as a difference, and kept in place of a:
-// a channel with a long memory has a close to 1, where a = 1 - m is right to the last bit and
-// m = 1 - a would not be; a step is a h + m x, exact where a gate forgets all, rather than h + m (x - h).
+// a = 1 / (1 + e) and 1 - a = e a are each formed from e = exp(-g), never one from the other: a channel with a long memory
+// needs all digits of 1 - a, a gate that closes all digits of a (the initial states' gradient is a_1 lam_1, and what a large
+// state leaves behind is a h).  So e is kept between the visits, and the second one takes the reciprocal of 1 + e again.  (With
+// a from a kept 1 - a 65536 x 2048 bf16 took 138 us, fp32 250, and a of a gate at -17 was all rounding.)
 // Arithmetic on a thread's two channels is packed (f32x2), which rounds each as the scalar form does.
 #include <string.h>
 
@@ -85,21 +86,23 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return r;
 }
 
-// a = 1 / (1 + e), m = e / (1 + e) with e = exp(-g) = 2^(-g log2 e), the exponent capped where e would overflow (a is
+// a = 1 / (1 + e), m = 1 - a = e a with e = exp(-g) = 2^(-g log2 e), the exponent capped where e would overflow (a is
 // then 1e-38, m one).  Power and reciprocal are the special-function unit's, of relative errors up to 2^-22 and 2^-23; the
 // exponent's rounding adds |g| 2^-24.  (expf and a rounded reciprocal for fp32 operands cost 65536 x 2048 16 of 272 us
 // and left the same error against 64 bits, 1.4e-7.)
-__device__ __forceinline__ void gate2(f2 g, f2& a, f2& m) {
+__device__ __forceinline__ f2 forget2(f2 g) {   // e
     const float2 t = un(mul(g, pk(-kLog2e, -kLog2e)));
-    float e0, e1, a0, a1;
+    float e0, e1;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(min_nan(t.x, 126.f)));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(min_nan(t.y, 126.f)));
-    const f2 e = pk(e0, e1);
+    return pk(e0, e1);
+}
+__device__ __forceinline__ f2 decay2(f2 e) {    // a
     const float2 d = un(add(e, pk(1.f, 1.f)));
+    float a0, a1;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(d.y));
-    a = pk(a0, a1);
-    m = mul(e, a);
+    return pk(a0, a1);
 }
 
 template <typename T> struct PairWord;
@@ -602,10 +605,11 @@ struct Main {
     __device__ __forceinline__ bool ends(int k) const { return DOCS && ((marks >> (k + 1) & 1) || k == final); }
     __device__ __forceinline__ int ending(int k) const { return k == final ? a.ndocs - 1 : doc[s0 + k + 1] - 1; }
 
-    // What the first visit keeps for the second, in registers beside the operands in the stage: m = 1 - a and,
-    // backwards, u = d(h_t)/d(g_t).  ROWS, forwards: u = m x, which reading x again would cost more than its registers.
+    // What the first visit keeps for the second, in registers beside the operands in the stage: e = exp(-g) and,
+    // backwards, u = d(h_t)/d(g_t).  ROWS, forwards: a in place of e and u = m x, which reading x again would cost more
+    // than its registers.
     struct Keep {
-        f2 m[SEG], u[BWD || ROWS ? SEG : 1];
+        f2 e[SEG], u[BWD || ROWS ? SEG : 1];
     };
 
     // PLAIN: every token of the segment is inside the sequence, and no document starts or ends in it
@@ -615,16 +619,15 @@ struct Main {
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
-            f2 av, mv;
-            gate2(in(0, k), av, mv);
+            const f2 e = forget2(in(0, k)), av = decay2(e);
             if (!PLAIN && starts(k)) {
                 A = pk(0.f, 0.f);
                 B = state(a.init, doc[s0 + k]);
             }
             A = mul(A, av);
-            const f2 b = mul(mv, in(1, k));
+            const f2 b = mul(mul(e, av), in(1, k));
             B = fma2(av, B, b);
-            q.m[k] = mv;
+            q.e[k] = ROWS ? av : e;
             if constexpr (ROWS) q.u[k] = b;
         }
         put_map(A, B);
@@ -633,17 +636,20 @@ struct Main {
     template <bool PLAIN, bool ALL>
     __device__ __forceinline__ void second_fwd(const Keep& q) {
         f2 h = entered();
-        const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
         T* y = mine(a.y, t.oy, a.width);
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
-            const f2 mv = q.m[k];
-            f2 b;
-            if constexpr (ROWS) b = q.u[k];
-            else b = mul(mv, in(1, k));
-            h = fma2(fma2(mv, minus, one), h, b);
+            f2 av, b;
+            if constexpr (ROWS) {
+                av = q.e[k];
+                b = q.u[k];
+            } else {
+                av = decay2(q.e[k]);
+                b = mul(mul(q.e[k], av), in(1, k));
+            }
+            h = fma2(av, h, b);
             put<ALL>(1, y, a.width, k, h);
             if (DOCS && !PLAIN && a.leave && ends(k)) {
                 const int at = ending(k);
@@ -653,45 +659,40 @@ struct Main {
     }
     template <bool PLAIN>
     __device__ __forceinline__ void first_bwd(Keep& q) {
-        const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
+        const f2 minus = pk(-1.f, -1.f);
         f2 h;
         if (t.t0 + s0 == 0) h = DOCS ? pk(0.f, 0.f) : state(a.init, t.row);
         else if constexpr (ROWS)
             h = pair(st - s0 / H::P * H::PITCH + H::NA * H::ARR + warp * H::PITCH +
                      (((uint32_t)(uintptr_t)a.y + (uint32_t)(t.oy - a.width) * H::ES) & 15));
         else h = widen(*reinterpret_cast<const W*>(st - s0 * H::PITCH + H::NA * H::ARR + warp * H::PITCH));
-        // forwards through the segment: u = (h_{t-1} - x) a (1 - a)
+        // Forwards through the segment: u = (h_{t-1} - x) a (1 - a), and the map of mu over the tokens so far, which the
+        // next one's extends from its far end: A is the product of their decays, B the sum of A dy.  A document that ends cuts it.
+        f2 A = pk(1.f, 1.f), B = pk(0.f, 0.f);
+        bool cut = false;
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             if (!PLAIN && s0 + k >= t.ntok) break;
-            f2 av, mv;
-            const f2 xv = in(1, k);
-            gate2(in(0, k), av, mv);
+            const f2 xv = in(1, k), e = forget2(in(0, k)), av = decay2(e), mv = mul(e, av);
             if (!PLAIN && starts(k)) h = state(a.init, doc[s0 + k]);
             q.u[k] = mul(fma2(xv, minus, h), mul(av, mv));
-            q.m[k] = mv;
+            q.e[k] = e;
             h = fma2(av, h, mul(mv, xv));
-        }
-        // backwards: the map of mu over the segment
-        f2 A = one, B = pk(0.f, 0.f);
-#pragma unroll
-        for (int k = SEG - 1; k >= 0; --k) {
-            if (!PLAIN && s0 + k >= t.ntok) continue;
+            if (!PLAIN && cut) continue;
+            A = mul(A, av);
+            B = fma2(A, in(2, k), B);
             if (!PLAIN && ends(k)) {
                 const int at = ending(k);
+                if (at >= 0) B = fma2(A, state(a.enter, at), B);
                 A = pk(0.f, 0.f);
-                B = at >= 0 ? state(a.enter, at) : A;
+                cut = true;
             }
-            const f2 av = fma2(q.m[k], minus, one);
-            B = mul(av, add(in(2, k), B));
-            A = mul(A, av);
         }
         put_map(A, B);
     }
     template <bool PLAIN, bool ALL>
     __device__ __forceinline__ void second_bwd(const Keep& q) {
         f2 mu = entered();
-        const f2 minus = pk(-1.f, -1.f), one = pk(1.f, 1.f);
         T *dg = mine(a.dg, t.og, a.g_stride), *dx = mine(a.dx, t.ox, a.x_stride);
 #pragma unroll
         for (int k = SEG - 1; k >= 0; --k) {
@@ -700,10 +701,10 @@ struct Main {
                 const int at = ending(k);
                 mu = at >= 0 ? state(a.enter, at) : pk(0.f, 0.f);
             }
-            const f2 lam = add(in(2, k), mu), mv = q.m[k];
+            const f2 lam = add(in(2, k), mu), av = decay2(q.e[k]), mv = mul(q.e[k], av);
             put<ALL>(0, dg, a.g_stride, k, mul(lam, q.u[k]));
             put<ALL>(1, dx, a.x_stride, k, mul(lam, mv));
-            mu = mul(fma2(mv, minus, one), lam);
+            mu = mul(av, lam);
             if (DOCS && !PLAIN && a.leave && starts(k)) put_state(a.leave, doc[s0 + k], mu);
         }
     }

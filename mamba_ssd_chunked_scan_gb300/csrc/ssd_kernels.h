@@ -167,7 +167,7 @@ struct AddNormBwdArgs {
 };
 
 // Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of kScanSegs segments x kScanCh
-// channels.  A segment holds as many tokens as let two tiles' values stay in a thread's registers (one 1 - a
+// channels.  A segment holds as many tokens as let two tiles' values stay in a thread's registers (one exp(-g)
 // per element forwards, two values backwards) and three or four tiles' operands in shared memory; fewer where
 // rows are off 16-byte alignment (two values forwards too).
 // A state is handed over once per kScanBlock tiles of a sequence.
