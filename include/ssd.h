@@ -268,7 +268,7 @@ SSD_API int ssd_gate_norm(int64_t rows, int32_t width, int32_t group_size, int32
  *     out[k] = h[k] * rstd * weight[k]
  *
  * out_dtype is dtype, or SSD_E4M3: then scales[r] = max(max_k |out[k]|, 1e-30) / 448
- * and out holds out[k] / scales[r], rounded to nearest even.  h is normalised as it was summed (fp32),
+ * and out holds the fp32 quotient out[k] / scales[r], rounded to nearest even.  h is normalised as it was summed (fp32),
  * before it is rounded to residual_out's type.
  *   x             (rows, width) dtype (SSD_F32 or SSD_BF16)
  *   residual      (rows, width) residual_dtype, or NULL.  residual_dtype is SSD_F32,

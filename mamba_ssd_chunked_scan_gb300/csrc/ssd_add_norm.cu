@@ -15,8 +15,10 @@
 //
 // The sums are fp32; h is normalised as it was summed, before its rounding to the
 // residual stream's type.  e4m3: scale = max(max |out|, 1e-30) / 448, and the row
-// holds out / scale rounded to nearest even; the floor keeps the quotient of an
-// all-zero row finite.
+// holds the fp32 quotient out / scale rounded to nearest even; the floor keeps the quotient of an
+// all-zero row finite.  The quotient is the product with the reciprocal, corrected by its remainder, which an fma gives
+// exactly (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990): a
+// product alone would put values beside the midpoint of two e4m3 numbers on the wrong side.
 #include "ssd_common.cuh"
 #include "ssd_kernels.h"
 #include "ssd_vec.cuh"
@@ -143,12 +145,13 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
             }
         }
     }
-    float inv = 1.f;
+    float scale = 1.f, inv = 1.f;
     if constexpr (sizeof(O) == 1) {
         amax = max_nan(row_reduce<true>(amax, one_warp, part[1]), kAmaxMin);
-        const float scale = amax / kE4m3Max;
+        scale = amax / kE4m3Max;
         if (tid == 0) a.scales[row] = scale;
         inv = 1.f / scale;
+        if (inv == 0.f) scale = 0.f;   // an infinite row: the remainders below are then the elements, and change nothing
     }
     O* out = static_cast<O*>(a.out) + base;
 #pragma unroll
@@ -157,7 +160,10 @@ __global__ void __launch_bounds__(1024) ssd_add_norm_kernel(AddNormArgs a) {
         if (e < W) {
             if constexpr (sizeof(O) == 1) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) h[c][k] *= inv;
+                for (int k = 0; k < V; ++k) {
+                    const float q = h[c][k] * inv;
+                    h[c][k] = fmaf(fmaf(-q, scale, h[c][k]), inv, q);
+                }
             }
             Raw<O, V> q;
             q.set(h[c]);
