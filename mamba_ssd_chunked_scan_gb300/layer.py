@@ -170,14 +170,21 @@ def add_norm_bwd(dout, h, weight, rstd, dresidual=None, *, stream=None):
 # --------------------------------------------------------------------------------------------- projection
 
 def _row_stride(name, t):
-    """Elements between the rows of a (..., k) tensor whose leading dimensions are packed."""
+    """Elements between the rows of a (..., k) tensor whose rows lie at one stride (its length where there is one row);
+    the strides of dimensions of one say nothing."""
     st, shape = t.stride(), t.shape
-    ok = len(shape) > 1 and (st[-1] == 1 or shape[-1] == 1) and st[-2] >= shape[-1]
-    for k in range(len(shape) - 2):
-        ok = ok and (shape[k] == 1 or st[k] == st[k + 1] * shape[k + 1])
-    if not ok:
+    ok = len(shape) > 1 and (st[-1] == 1 or shape[-1] == 1)
+    step, rows = shape[-1], 1
+    for k in range(len(shape) - 2, -1, -1):
+        if shape[k] == 1:
+            continue
+        if rows == 1:
+            step = st[k]
+        ok = ok and st[k] == step * rows
+        rows *= shape[k]
+    if not ok or step < shape[-1]:
         raise ValueError(f"{name}: expected columns together and rows at one stride, got strides {st} for {tuple(shape)}")
-    return st[-2]
+    return step
 
 
 def _linear_params(x, w, act, dev):
