@@ -862,7 +862,7 @@ cudaError_t launch_tile(const LinearParams& p, cudaStream_t st) {
 template <bool E4M3, bool AMN, bool BMN>
 cudaError_t launch_kind(const LinearParams& p, const LinearPlan& plan, cudaStream_t st) {
     const int tn = plan.tile_n;
-    if (plan.pair) return tn == 256 ? launch_tile<256, E4M3, AMN, BMN, true>(p, st) : launch_tile<128, E4M3, AMN, BMN, true>(p, st);
+    if (plan.pair) return launch_tile<256, E4M3, AMN, BMN, true>(p, st);
     if (tn == 256) return launch_tile<256, E4M3, AMN, BMN, false>(p, st);
     if (tn == 128) return launch_tile<128, E4M3, AMN, BMN, false>(p, st);
     if constexpr (!AMN && !BMN) {
@@ -875,7 +875,7 @@ cudaError_t launch_kind(const LinearParams& p, const LinearPlan& plan, cudaStrea
 }  // namespace
 
 // How a product of `rows` x `cols` results over a contraction of `kbytes` bytes runs.  Up to kLinearSwap
-// rows it is computed transposed.  Otherwise the tile (128 rows by one CTA or 256 by a pair, 64 to 256 columns)
+// rows it is computed transposed.  Otherwise the tile (128 rows by one CTA and 64 to 256 columns, or 256 by 256 by a pair)
 // and the parts of the last wave's tiles minimise a count of cycles.  Measured: a 128-byte block of a tile takes
 // 520 cycles by a pair and 541 by a CTA at 256 columns, where the MMAs bound it, but 417 at 128 and 390 at 64 (the
 // rows of A are read from shared memory for each MMA however few the columns); a tile's start 600; a
@@ -890,7 +890,7 @@ static LinearPlan find_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may
     const int widths[] = {256, 128, 64, 32, 16};
     for (int pair = 1; pair >= 0; --pair)
         for (int tn : widths) {
-            if (pair && (swap || tn < 128)) continue;
+            if (pair && (swap || tn < 256)) continue;   // narrower, a CTA's tile takes as long, without the cluster's start
             if (swap ? (tn > kLinearSwap || (tn < dc && tn < kLinearSwap) || (tn > 16 && tn / 2 >= dc)) : tn < 64) continue;
             const int64_t tm = pair ? 2 * kTileM : kTileM;
             const int64_t tiles = ((dr + tm - 1) / tm) * ((dc + tn - 1) / tn), workers = pair ? kLinearSMs / 2 : kLinearSMs;

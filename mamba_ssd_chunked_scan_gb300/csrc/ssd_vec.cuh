@@ -56,12 +56,6 @@ struct Raw {
         for (int k = 0; k < V; ++k)
             if (e + k >= 0 && e + k < n) row[e + k] = v[k];
     }
-    // The compiler is not to reuse what it made of the elements before.
-    __device__ __forceinline__ void forget() {
-        uint32_t* v = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(W) / 4; ++k) asm volatile("" : "+r"(v[k]));
-    }
     __device__ __forceinline__ void zero() {
         if constexpr (sizeof(T) * V == 32) w.lo = w.hi = make_uint4(0, 0, 0, 0);
         else if constexpr (sizeof(T) * V == 16) w = make_uint4(0, 0, 0, 0);
