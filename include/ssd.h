@@ -363,6 +363,19 @@ SSD_API int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* 
 SSD_API int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, const void* pre, const void* dy,
              void* dx, void* dw, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
+/* How a product of ssd_linear() or ssd_linear_bwd() runs (diagnostic, as ssd_fwd_plan(); needs no GPU).  product: 0 y,
+ * 1 dx, 2 dw (both with SSD_BF16 only).  Returns SSD_OK, or the status that the call would return for these parameters;
+ * m == 0 has no tiles. */
+typedef struct {
+    int64_t tiles;        /* tiles of the product                                                     */
+    int64_t whole;        /* tiles computed by one worker each; the others are split along the contraction */
+    int32_t splits;       /* parts of each of those others (1: all tiles are whole)                   */
+    int32_t tile_rows;    /* 128: a worker is a CTA; 256: a pair of them                              */
+    int32_t tile_cols;
+    int32_t transposed;   /* 1: the tiles are those of the transposed product (y of up to 64 rows)    */
+} ssd_linear_plan_t;
+SSD_API int ssd_linear_plan(const ssd_linear_params_t* p, int product, ssd_linear_plan_t* plan);
+
 /* Gated linear recurrence: one decay per channel and token (the scan above has one per head and token).
  * Per row b, token t and channel d, with gate logits g and inputs x,
  *

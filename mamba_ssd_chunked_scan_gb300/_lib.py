@@ -23,7 +23,7 @@ EXPORTS = ("ssd_fwd_workspace_size", "ssd_workspace_init", "ssd_fwd", "ssd_check
            "ssd_gate_norm", "ssd_check_status_where", "ssd_fwd_fault_inject", "ssd_add_norm",
            "ssd_add_norm_bwd_workspace_size", "ssd_add_norm_bwd", "ssd_gate_scan_workspace_size", "ssd_gate_scan",
            "ssd_gate_scan_bwd", "ssd_gate_scan_step", "ssd_linear_workspace_size", "ssd_linear_bwd_workspace_size",
-           "ssd_linear", "ssd_linear_bwd")
+           "ssd_linear", "ssd_linear_bwd", "ssd_linear_plan")
 
 
 class SSDParams(ctypes.Structure):
@@ -42,6 +42,11 @@ class GateScanParams(ctypes.Structure):
 class LinearParams(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("ldx", ctypes.c_int64), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class LinearPlan(ctypes.Structure):
+    _fields_ = [("tiles", ctypes.c_int64), ("whole", ctypes.c_int64), ("splits", ctypes.c_int32), ("tile_rows", ctypes.c_int32),
+                ("tile_cols", ctypes.c_int32), ("transposed", ctypes.c_int32)]
 
 
 class SSDError(RuntimeError):
@@ -114,6 +119,8 @@ def _load():
     lib.ssd_linear.restype = ctypes.c_int
     lib.ssd_linear_bwd.argtypes = [N] + [vp] * 8 + [sz, vp]
     lib.ssd_linear_bwd.restype = ctypes.c_int
+    lib.ssd_linear_plan.argtypes = [N, ctypes.c_int, ctypes.POINTER(LinearPlan)]
+    lib.ssd_linear_plan.restype = ctypes.c_int
     return lib
 
 
@@ -134,6 +141,13 @@ def plan(p: SSDParams, has_init: bool = False, has_final: bool = False):
     n, s = ctypes.c_int(0), ctypes.c_int(0)
     fam = lib.ssd_fwd_plan(ctypes.byref(p), int(has_init), int(has_final), ctypes.byref(n), ctypes.byref(s))
     return fam, n.value, s.value
+
+
+def linear_plan(m: int, n: int, k: int, dtype: int, product: int = 0) -> LinearPlan:
+    """How a linear call's product (0: y, 1: dx, 2: dw) runs."""
+    out = LinearPlan()
+    check(lib.ssd_linear_plan(ctypes.byref(LinearParams(m, k, n, k, dtype, 0)), product, ctypes.byref(out)), "ssd_linear_plan")
+    return out
 
 
 def check(code: int, what: str) -> None:

@@ -222,6 +222,7 @@ struct GateStepArgs {
 
 // Matrix product with its epilogue (ssd_linear, ssd_linear_bwd): D = X W^T.
 constexpr int kLinearSwap = 64;       // up to this many rows of x the product is computed transposed
+constexpr int kLinearTileRows = 128;  // of a CTA's tile; a pair's has twice as many
 constexpr int kLinearSMs = 152;       // SMs the plan (and so the workspace) is made for
 constexpr int kLinearMaxSplits = 16;
 struct LinearOperand {

@@ -289,6 +289,26 @@ size_t ssd_linear_bwd_workspace_size(const ssd_linear_params_t* p) {
     return p->m == 0 ? sizeof(WsHeader) : linear_bwd_layout(p).total;
 }
 
+int ssd_linear_plan(const ssd_linear_params_t* p, int product, ssd_linear_plan_t* plan) {
+    const int rc = check_linear(p);
+    if (rc != SSD_OK) return rc;
+    if (!plan || product < 0 || product > 2) return SSD_ERR_INVALID_ARG;
+    if (product && p->dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
+    *plan = ssd_linear_plan_t();
+    if (p->m == 0) return SSD_OK;
+    const int64_t rows = product == 2 ? p->n : p->m, cols = product ? p->k : p->n;
+    const int64_t kbytes = product == 0 ? (int64_t)p->k * elem(p->dtype) : product == 1 ? (int64_t)p->n * 2 : p->m * 2;
+    const LinearPlan l = linear_plan(rows, cols, kbytes, product == 0);
+    plan->tile_rows = l.pair ? 2 * kLinearTileRows : kLinearTileRows;
+    plan->tile_cols = l.tile_n;
+    plan->transposed = l.swap;
+    plan->whole = l.whole;
+    plan->splits = l.splits;
+    const int64_t dr = l.swap ? cols : rows, dc = l.swap ? rows : cols;
+    plan->tiles = ((dr + plan->tile_rows - 1) / plan->tile_rows) * ((dc + l.tile_n - 1) / l.tile_n);
+    return SSD_OK;
+}
+
 int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* w, const float* x_scales, const float* w_scales,
                const float* bias, const void* residual, void* y, void* pre, void* workspace, size_t workspace_bytes,
                void* stream) {

@@ -43,7 +43,7 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);   // warp 0 loads, 1 MMAs, 2 tensor memory, 4-11 epilogue
 constexpr int kRowB = 128;             // bytes of the contraction per tile row and stage
-constexpr int kTileM = 128;
+constexpr int kTileM = kLinearTileRows;
 constexpr uint32_t kWhereEmpty = 61, kWhereFull = 62, kWhereAccFree = 63, kWhereAcc = 64, kWhereDrain = 65;
 
 // TB: columns of the tile whose operand rows this CTA loads (half of them in a pair)

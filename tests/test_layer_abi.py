@@ -212,3 +212,19 @@ def test_linear_workspaces_hold_few_parts(L):
                 assert 256 <= size <= 256 + 16 * 152 * 128 * 256 * 4
                 if k * 2 <= 4 * 128:
                     assert size == 256   # too short to split
+
+
+def test_linear_plan_query(L):
+    from mamba_ssd_chunked_scan_gb300 import _lib
+    out = _lib.LinearPlan()
+    p = linear_params()
+    for kw, code in LINEAR_PARAMS:
+        assert L.ssd_linear_plan(linear_params(**kw), 0, out) == code
+    assert L.ssd_linear_plan(p, 3, out) == 1 and L.ssd_linear_plan(p, -1, out) == 1 and L.ssd_linear_plan(p, 0, None) == 1
+    assert L.ssd_linear_plan(linear_params(dtype=2), 1, out) == 2 and L.ssd_linear_plan(linear_params(dtype=2), 0, out) == 0
+    assert L.ssd_linear_plan(linear_params(m=0), 0, out) == 0 and out.tiles == 0
+    # the workspace is the status word and the parts
+    for m, n, k in ((8, 2560, 5120), (292, 6412, 3920), (4099, 2560, 5120), (300, 520, 256)):
+        q = _lib.linear_plan(m, n, k, 1)
+        parts = (q.tiles - q.whole) * q.splits if q.splits > 1 else 0
+        assert L.ssd_linear_workspace_size(linear_params(m=m, n=n, k=k, ldx=k)) == 256 + 4 * parts * q.tile_rows * q.tile_cols
