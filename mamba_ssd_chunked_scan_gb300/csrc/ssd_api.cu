@@ -346,10 +346,6 @@ namespace {
 // Splits of at least this many chunks take the tensor-core aggregate kernel.
 constexpr int kAggMinChunks = 4;
 
-// Smallest wait cap the fault-injection entry point accepts: the drain waits
-// share the cap and must outlast the MMAs and copies still in flight.
-constexpr uint32_t kMinInjectWaitRounds = 4096;
-
 // Events recorded around each launch of one forward call (the measurement entry
 // point ssd_fwd_timed only).
 constexpr int kMaxTimedLaunches = 4;

@@ -232,10 +232,10 @@ struct Shared {
 };
 
 template <typename S>
-__device__ __forceinline__ bool bar_wait(S& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
-    if (ptx::mbar_wait(bar, parity, &sh.abort, kDefaultWaitIters)) return true;
+__device__ __forceinline__ bool bar_wait(S& sh, const GateScanArgs& a, uint64_t* bar, uint32_t parity, uint32_t where) {
+    if (ptx::mbar_wait(bar, parity, &sh.abort, a.wait_iters)) return true;
     if (!*(volatile int*)&sh.abort) {
-        record_error(ws, SSD_ERR_TIMEOUT, where);
+        record_error(a.ws, SSD_ERR_TIMEOUT, where);
         *(volatile int*)&sh.abort = 1;
     }
     return false;
@@ -307,13 +307,14 @@ __device__ __forceinline__ void loading(const ScanParams<T, ROWS, BWD>& p, uint8
         const int st = n % H::NS;
         if (n >= H::NS) {
             if (lane == 0) {
-                go = bar_wait(sh, a.ws, &sh.done[st], ((n / H::NS) - 1) & 1, kWhereDone);
+                go = bar_wait(sh, a, &sh.done[st], ((n / H::NS) - 1) & 1, kWhereDone);
                 if (go) send(n - H::NS);
                 ptx::bulk_wait_read0();
             }
             go = __shfl_sync(0xffffffffu, (int)go, 0) != 0;
             if (!go) break;
         }
+        if (n == a.loads) break;   // (an injected stall; else negative)
         __syncwarp();
         uint64_t* full = &sh.full[st];
         ++filled;
@@ -356,12 +357,12 @@ __device__ __forceinline__ void loading(const ScanParams<T, ROWS, BWD>& p, uint8
     if (lane != 0) return;
     // the outputs of the tiles still in stages, then everything in flight
     for (int j = n - H::NS + 1 > 0 ? n - H::NS + 1 : 0; go && j < n; ++j) {
-        go = bar_wait(sh, a.ws, &sh.done[j % H::NS], (j / H::NS) & 1, kWhereDone);
+        go = bar_wait(sh, a, &sh.done[j % H::NS], (j / H::NS) & 1, kWhereDone);
         if (go) send(j);
     }
     for (int st = 0; st < H::NS && st < filled; ++st) {
         const int last = ((filled - 1 - st) / H::NS) * H::NS + st;
-        if (!ptx::mbar_wait(&sh.full[st], (last / H::NS) & 1, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereStage);
+        if (!ptx::mbar_wait(&sh.full[st], (last / H::NS) & 1, &sh.never, a.wait_iters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereStage);
     }
     ptx::bulk_wait0();
 }
@@ -371,10 +372,10 @@ template <bool REV, typename S>
 __device__ __forceinline__ void publish_maps(const GateScanArgs& a, S& sh) {
     const int lane = threadIdx.x & 31;   // channels 2 * lane, 2 * lane + 1
     for (int n = 0;; ++n) {
-        if (!bar_wait(sh, a.ws, &sh.maps[n & 1], (n >> 1) & 1, kWhereMaps)) return;
+        if (!bar_wait(sh, a, &sh.maps[n & 1], (n >> 1) & 1, kWhereMaps)) return;
         const Tile t = sh.tile[n % kRing];
         if (!t.ntok) return;
-        if (t.step % kBlock != kBlock - 1 && t.step != a.nchunks - 1) {   // another tile of the block needs it
+        if (t.step % kBlock != kBlock - 1 && t.step != a.nchunks - 1 && !a.mute) {   // another tile of the block needs it
             float4 q[kMain];
 #pragma unroll
             for (int k = 0; k < kMain; ++k) q[k] = *reinterpret_cast<const float4*>(&sh.seg[n & 1][REV ? kMain - 1 - k : k][2 * lane]);
@@ -398,7 +399,7 @@ template <bool REV, typename S>
 __device__ __forceinline__ void take_states(const GateScanArgs& a, S& sh) {
     const int c = threadIdx.x - 32 * kMain, lane = threadIdx.x & 31;   // channel of the tile
     for (int n = 0;; ++n) {
-        if (!bar_wait(sh, a.ws, &sh.maps[n & 1], (n >> 1) & 1, kWhereMaps)) return;
+        if (!bar_wait(sh, a, &sh.maps[n & 1], (n >> 1) & 1, kWhereMaps)) return;
         const Tile t = sh.tile[n % kRing];
         float2 (*seg)[kCh] = sh.seg[n & 1];
         if (!t.ntok) return;
@@ -421,7 +422,7 @@ __device__ __forceinline__ void take_states(const GateScanArgs& a, S& sh) {
             for (int p = 0; p < kBlock - 1; ++p) missing = missing || w[p] == 0;
             if (!missing) break;
             if (it == 1) since = ptx::globaltimer();
-            if ((it & 15) == 0 && (it > (1u << 26) || *(volatile int*)&sh.abort || ptx::globaltimer() - since > kWaitNs)) {
+            if ((it & 15) == 0 && (it > a.wait_iters || *(volatile int*)&sh.abort || ptx::globaltimer() - since > kWaitNs)) {
                 record_error(a.ws, SSD_ERR_TIMEOUT, cw == 0 ? kWhereBlock : kWhereTile);
                 *(volatile int*)&sh.abort = 1;
                 break;
@@ -440,7 +441,7 @@ __device__ __forceinline__ void take_states(const GateScanArgs& a, S& sh) {
         float2 m[kMain];
 #pragma unroll
         for (int k = 0; k < kMain; ++k) m[k] = seg[REV ? kMain - 1 - k : k][c];
-        if (!bar_wait(sh, a.ws, &sh.told[n & 1], (n >> 1) & 1, kWhereMaps)) return;   // the maps have been read
+        if (!bar_wait(sh, a, &sh.told[n & 1], (n >> 1) & 1, kWhereMaps)) return;   // the maps have been read
 #pragma unroll
         for (int k = 0; k < kMain; ++k) {
             seg[REV ? kMain - 1 - k : k][c].x = h;
@@ -711,7 +712,7 @@ struct Main {
 
     // The first visit to tile n; false: there is none, or a wait ran out.
     __device__ __forceinline__ bool first(int n, uint8_t* sm, Keep& q) {
-        if (!bar_wait(sh, a.ws, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
+        if (!bar_wait(sh, a, &sh.full[n % H::NS], (n / H::NS) & 1, kWhereStage)) return false;
         open(n, sm);
         if (t.ntok) {
             if constexpr (BWD) {
@@ -727,7 +728,7 @@ struct Main {
         return t.ntok != 0;
     }
     __device__ __forceinline__ bool second(int n, uint8_t* sm, const Keep& q) {
-        if (!bar_wait(sh, a.ws, &sh.states[n & 1], (n >> 1) & 1, kWhereState)) return false;
+        if (!bar_wait(sh, a, &sh.states[n & 1], (n >> 1) & 1, kWhereState)) return false;
         open(n, sm);
         if constexpr (BWD) {
             if (plain && (!ROWS || all())) second_bwd<true, true>(q);
@@ -965,6 +966,10 @@ cudaError_t launch_gate_scan(const GateScanArgs& args, void* workspace, bool bwd
     a.ngroups = l.ngroups;
     a.nblocks = l.nblocks;
     a.ntiles = (uint32_t)(a.batch * l.ngroups * l.nchunks);
+    if (a.wait_iters == 0) {
+        a.wait_iters = kDefaultWaitIters;
+        a.loads = -1;
+    }
     a.ws = reinterpret_cast<WsHeader*>(w);
     a.ticket = reinterpret_cast<uint32_t*>(w + l.ticket_off);
     a.maps = reinterpret_cast<uint64_t*>(w + l.maps_off);

@@ -16,6 +16,9 @@ enum { kModeFull = 0, kModeAggregate = 1 };
 // (each poll is an mbarrier try_wait, which may suspend the thread for a while;
 // every wait also gives up after 2 s).
 constexpr uint32_t kDefaultWaitIters = 1u << 26;
+// Smallest wait cap the fault-injection entry points accept: the drain waits
+// share the cap and must outlast the MMAs and copies still in flight.
+constexpr uint32_t kMinInjectWaitRounds = 4096;
 
 // Everything one launch of a chunk kernel needs (passed by value).
 struct FwdArgs {
@@ -193,6 +196,10 @@ struct GateScanArgs {
     // the final states' and the initial states' gradients backwards
     const float* enter;
     float* leave;
+    // fault injection: bounded waits give up after so many polls (0: an ordinary call); tiles that a CTA loads before it stalls
+    // (negative: all), or no tile publishes its map
+    uint32_t wait_iters;
+    int loads, mute;
     // set at the launch
     WsHeader* ws;
     uint32_t* ticket;
@@ -246,6 +253,9 @@ struct LinearArgs {
     float* parts;          // per part, a tile of fp32 sums
     WsHeader* ws;
     int keep_status;       // the status word was cleared by the call already
+    // fault injection: bounded waits give up after so many polls (0: an ordinary call); blocks of the contraction that a CTA
+    // loads before it stalls
+    uint32_t wait_iters, loads;
     int swap, vec;         // set at the launch
 };
 struct LinearPlan {

@@ -80,10 +80,10 @@ struct Small {
     int abort, never;
 };
 
-__device__ __forceinline__ bool lin_wait(Small& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
-    if (ptx::mbar_wait(bar, parity, &sh.abort, kDefaultWaitIters)) return true;
+__device__ __forceinline__ bool lin_wait(Small& sh, const LinearArgs& a, uint64_t* bar, uint32_t parity, uint32_t where, const int* stop) {
+    if (ptx::mbar_wait(bar, parity, stop, a.wait_iters)) return true;
     if (!*(volatile int*)&sh.abort) {
-        record_error(ws, SSD_ERR_TIMEOUT, where);
+        record_error(a.ws, SSD_ERR_TIMEOUT, where);
         *(volatile int*)&sh.abort = 1;
     }
     return false;
@@ -176,9 +176,9 @@ __device__ __forceinline__ bool elected() {
 }
 // The same on a barrier where the cluster's other CTA arrives too.  (An acquire of the wait's own: a fence after it
 // held the MMAs up for 1600 cycles per tile.)
-__device__ __forceinline__ bool cluster_wait(Small& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
+__device__ __forceinline__ bool cluster_wait(Small& sh, const LinearArgs& a, uint64_t* bar, uint32_t parity, uint32_t where) {
     const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 0; it < kDefaultWaitIters; ++it) {
+    for (uint32_t it = 0; it < a.wait_iters; ++it) {
         uint32_t ok;
         asm volatile(
             "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
@@ -189,14 +189,14 @@ __device__ __forceinline__ bool cluster_wait(Small& sh, WsHeader* ws, uint64_t* 
         if ((it & 63) == 63 && (*(volatile int*)&sh.abort || ptx::globaltimer() - t0 > ptx::kWaitLimitNs)) break;
     }
     if (!*(volatile int*)&sh.abort) {
-        record_error(ws, SSD_ERR_TIMEOUT, where);
+        record_error(a.ws, SSD_ERR_TIMEOUT, where);
         *(volatile int*)&sh.abort = 1;
     }
     return false;
 }
 // A wait by a whole warp, whose lanes go on or give up together.
-__device__ __forceinline__ bool warp_wait(Small& sh, WsHeader* ws, uint64_t* bar, uint32_t parity, uint32_t where) {
-    return __all_sync(0xffffffffu, lin_wait(sh, ws, bar, parity, where));
+__device__ __forceinline__ bool warp_wait(Small& sh, const LinearArgs& a, uint64_t* bar, uint32_t parity, uint32_t where, const int* stop) {
+    return __all_sync(0xffffffffu, lin_wait(sh, a, bar, parity, where, stop));
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -449,7 +449,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             const Item i = item_at(p, item);
             const int row = i.r * kRows + rank * kTileM, col = i.c * TN + rank * C::TB;
             for (int kb = i.k0; kb < i.k1; ++kb) {
-                if (it >= (uint32_t)C::kStages && !warp_wait(sh, a.ws, &sh.empty[st], phase ^ 1, kWhereEmpty)) {
+                if (it == a.loads) {   // (an injected stall; else more than there are)
+                    go = false;
+                    break;
+                }
+                // A pair's loads count on one barrier: both CTAs have to stop at the same block, so neither gives up for what
+                // went wrong in it alone (`never`), only for a stage that neither gets back.
+                if (it >= (uint32_t)C::kStages &&
+                    !warp_wait(sh, a, &sh.empty[st], phase ^ 1, kWhereEmpty, PAIR ? &sh.never : &sh.abort)) {
                     go = false;
                     break;
                 }
@@ -482,10 +489,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
         }
         // every load that was issued has landed before the CTA may leave (a pair's count on the first's barriers, and
         // the pair leaves together)
+        if (PAIR && rank != 0 && !go && lane == 0) {
+            // should this CTA have gone a stage further than the first all the same, no barrier tells when that load lands
+            const uint64_t t0 = ptx::globaltimer();
+            for (uint32_t k = 0; k < kDefaultWaitIters && ptx::globaltimer() - t0 < 1000000; ++k) {}
+        }
         if (rank == 0 && lane == 0)
             for (uint32_t i = 0; i < (uint32_t)C::kStages && i < it; ++i) {
                 const uint32_t last = ((it - 1 - i) / C::kStages) * C::kStages + i;
-                if (!ptx::mbar_wait(&sh.full[i], (last / C::kStages) & 1, &sh.never, kDefaultWaitIters)) {
+                if (!ptx::mbar_wait(&sh.full[i], (last / C::kStages) & 1, &sh.never, a.wait_iters)) {
                     record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
                     *(volatile int*)&sh.abort = 1;
                 }
@@ -508,13 +520,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                 const uint32_t buf = tile & 1, d = tb + buf * TN;
                 if (tile >= 2) {
                     const uint32_t parity = ((tile >> 1) - 1) & 1;
-                    if (PAIR ? !__all_sync(0xffffffffu, cluster_wait(sh, a.ws, &sh.acc_free[buf], parity, kWhereAccFree))
-                             : !warp_wait(sh, a.ws, &sh.acc_free[buf], parity, kWhereAccFree))
+                    if (PAIR ? !__all_sync(0xffffffffu, cluster_wait(sh, a, &sh.acc_free[buf], parity, kWhereAccFree))
+                             : !warp_wait(sh, a, &sh.acc_free[buf], parity, kWhereAccFree, &sh.abort))
                         break;
                 }
                 ptx::tc_fence_after();
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!warp_wait(sh, a.ws, &sh.full[st], phase, kWhereFull)) {
+                    if (!warp_wait(sh, a, &sh.full[st], phase, kWhereFull, &sh.abort)) {
                         go = false;
                         break;
                     }
@@ -531,12 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                         phase ^= 1;
                     }
                 }
-                if (elected()) mma_commit<PAIR>(&sh.acc[buf]);
+                if (go && elected()) mma_commit<PAIR>(&sh.acc[buf]);   // of a sum that is not whole nothing is written
                 __syncwarp();
             }
             if (elected()) mma_commit<PAIR>(&sh.done);
             __syncwarp();
-            if (!ptx::mbar_wait(&sh.done, 0, &sh.never, kDefaultWaitIters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
+            if (!ptx::mbar_wait(&sh.done, 0, &sh.never, a.wait_iters)) record_error(a.ws, SSD_ERR_TIMEOUT, kWhereDrain);
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue
@@ -586,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
                 }
             }
             bool ok = true;
-            if (lane == 0) ok = lin_wait(sh, a.ws, &sh.acc[buf], (tile >> 1) & 1, kWhereAcc);
+            if (lane == 0) ok = lin_wait(sh, a, &sh.acc[buf], (tile >> 1) & 1, kWhereAcc, &sh.abort);
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             // a wait that runs out stops all of the warps, which share the barrier above
             if (whole && (a.bias || a.x_scales)) ok = !ptx::named_bar_any(2, 32 * kEpiWarps, !ok);
@@ -937,6 +949,10 @@ cudaError_t launch_linear(const LinearArgs& args, const LinearPlan& plan, cudaSt
     memset(&p, 0, sizeof(p));
     p.a = args;
     LinearArgs& a = p.a;
+    if (a.wait_iters == 0) {
+        a.wait_iters = kDefaultWaitIters;
+        a.loads = ~0u;
+    }
     a.swap = plan.swap;
     a.vec = a.n % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0 && ((uintptr_t)a.pre & 15) == 0;
     const int64_t dr = a.swap ? a.n : a.m, dc = a.swap ? a.m : a.n;
