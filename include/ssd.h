@@ -507,6 +507,21 @@ SSD_API int ssd_fwd_fault_inject(const ssd_params_t* p,
             void* y, float* final_states,
             void* workspace, size_t workspace_bytes, uint32_t max_wait_rounds, void* stream);
 
+/* Test aids for the failure paths of the operators around the scan: ssd_linear() and ssd_gate_scan() with an injected
+ * stall.  Each CTA issues `loads` loads (blocks of the contraction, or tiles of the sequence) and no more; every bounded wait
+ * gives up after max_wait_rounds polls.  What waits for the missing loads runs out; the first wait to do so records
+ * SSD_ERR_TIMEOUT and its code, and every CTA lets its copies and MMAs finish, frees its tensor memory and exits.
+ * ssd_gate_scan_fault_inject() with loads -1 loads everything, but no tile publishes its map, so the tiles after it wait in
+ * vain.  Outputs are undefined afterwards; the workspace, which has to be given, serves ordinary calls again.  Arguments
+ * as the ordinary calls; SSD_ERR_INVALID_ARG when max_wait_rounds < 4096 or loads is negative (below -1).  Not for
+ * production use. */
+SSD_API int ssd_linear_fault_inject(const ssd_linear_params_t* p, const void* x, const void* w, const float* x_scales,
+             const float* w_scales, const float* bias, const void* residual, void* y, void* pre,
+             void* workspace, size_t workspace_bytes, int32_t loads, uint32_t max_wait_rounds, void* stream);
+SSD_API int ssd_gate_scan_fault_inject(const ssd_gate_scan_params_t* p, const void* g, const void* x,
+             const float* initial_states, const int32_t* cu_seqlens, void* y, float* final_states, void* workspace,
+             size_t workspace_bytes, int32_t loads, uint32_t max_wait_rounds, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 SSD_API const char* ssd_status_string(int status);
 

@@ -23,7 +23,7 @@ EXPORTS = ("ssd_fwd_workspace_size", "ssd_workspace_init", "ssd_fwd", "ssd_check
            "ssd_gate_norm", "ssd_check_status_where", "ssd_fwd_fault_inject", "ssd_add_norm",
            "ssd_add_norm_bwd_workspace_size", "ssd_add_norm_bwd", "ssd_gate_scan_workspace_size", "ssd_gate_scan",
            "ssd_gate_scan_bwd", "ssd_gate_scan_step", "ssd_linear_workspace_size", "ssd_linear_bwd_workspace_size",
-           "ssd_linear", "ssd_linear_bwd", "ssd_linear_plan")
+           "ssd_linear", "ssd_linear_bwd", "ssd_linear_plan", "ssd_linear_fault_inject", "ssd_gate_scan_fault_inject")
 
 
 class SSDParams(ctypes.Structure):
@@ -119,6 +119,10 @@ def _load():
     lib.ssd_linear.restype = ctypes.c_int
     lib.ssd_linear_bwd.argtypes = [N] + [vp] * 8 + [sz, vp]
     lib.ssd_linear_bwd.restype = ctypes.c_int
+    lib.ssd_linear_fault_inject.argtypes = [N] + [vp] * 9 + [sz, i32, ctypes.c_uint32, vp]
+    lib.ssd_linear_fault_inject.restype = ctypes.c_int
+    lib.ssd_gate_scan_fault_inject.argtypes = [G] + [vp] * 7 + [sz, i32, ctypes.c_uint32, vp]
+    lib.ssd_gate_scan_fault_inject.restype = ctypes.c_int
     lib.ssd_linear_plan.argtypes = [N, ctypes.c_int, ctypes.POINTER(LinearPlan)]
     lib.ssd_linear_plan.restype = ctypes.c_int
     return lib

@@ -109,6 +109,81 @@ LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p) {
     return l;
 }
 
+// Fault injection (test aid): a cap on every bounded wait, in polls (0: an ordinary call), and how many loads a CTA issues;
+// the recurrence: negative, no tile publishes its map.
+struct Stall {
+    uint32_t rounds = 0;
+    int loads = 0;
+};
+
+int gate_scan_impl(const ssd_gate_scan_params_t* p, const void* g, const void* x, const float* initial_states,
+                   const int32_t* cu_seqlens, void* y, float* final_states, void* workspace, size_t workspace_bytes,
+                   void* stream, const Stall& stall) {
+    const int rc = check_scan(p);
+    if (rc != SSD_OK) return rc;
+    if (!g || !x || !y || (p->ndocs > 0) != (cu_seqlens != nullptr)) return SSD_ERR_INVALID_ARG;
+    const size_t es = elem(p->dtype);
+    if (!aligned(g, es) || !aligned(x, es) || !aligned(y, es) || !aligned(initial_states, 4) ||
+        !aligned(final_states, 4) || !aligned(cu_seqlens, 4))
+        return SSD_ERR_INVALID_ARG;
+    const size_t need = ssd_gate_scan_workspace_size(p);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
+    const int64_t rows = p->batch * p->seqlen, nst = p->ndocs > 0 ? p->ndocs : p->batch;
+    const Mat in[] = {{g, rows, p->width, p->g_stride, es}, {x, rows, p->width, p->x_stride, es},
+                      {initial_states, nst, p->width, p->width, 4}, {cu_seqlens, 1, p->ndocs + 1, p->ndocs + 1, 4}};
+    const Mat out[] = {{y, rows, p->width, p->width, es}, {final_states, nst, p->width, p->width, 4},
+                       {workspace, 1, (int64_t)need, (int64_t)need, 1}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Mat& m : in)
+            if (touch(out[i], m)) return SSD_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (touch(out[i], out[j])) return SSD_ERR_INVALID_ARG;
+    }
+    GateScanArgs a = {};
+    a.batch = p->batch; a.seqlen = p->seqlen; a.width = p->width; a.dtype = p->dtype; a.ndocs = p->ndocs;
+    a.g_stride = p->g_stride; a.x_stride = p->x_stride;
+    a.g = g; a.x = x; a.init = initial_states; a.cu = cu_seqlens; a.y = y;
+    a.enter = initial_states; a.leave = final_states;
+    a.wait_iters = stall.rounds; a.loads = stall.loads; a.mute = stall.loads < 0;
+    return launch_gate_scan(a, workspace, false, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+int linear_impl(const ssd_linear_params_t* p, const void* x, const void* w, const float* x_scales, const float* w_scales,
+                const float* bias, const void* residual, void* y, void* pre, void* workspace, size_t workspace_bytes,
+                void* stream, const Stall& stall) {
+    const int rc = check_linear(p);
+    if (rc != SSD_OK) return rc;
+    const bool e4m3 = p->dtype == SSD_E4M3;
+    if (e4m3 != (w_scales != nullptr) || (!e4m3 && x_scales) || (e4m3 && !x_scales && p->m > 0)) return SSD_ERR_INVALID_ARG;
+    if (p->m == 0) return SSD_OK;
+    if (!x || !w || !y) return SSD_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(bias, 4) ||
+        !aligned(residual, 2) || !aligned(y, 2) || !aligned(pre, 2))
+        return SSD_ERR_INVALID_ARG;
+    const size_t es = elem(p->dtype);
+    const LinearPlan plan = linear_plan(p->m, p->n, (int64_t)p->k * es, true);
+    const size_t need = sizeof(WsHeader) + plan.parts_bytes;
+    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
+    const Mat in[] = {{x, p->m, p->k, p->ldx, es}, {w, p->n, p->k, p->k, es}, {x_scales, 1, p->m, p->m, 4},
+                      {w_scales, 1, p->n, p->n, 4}, {bias, 1, p->n, p->n, 4}};
+    const Mat my = {y, p->m, p->n, p->n, 2}, mp = {pre, p->m, p->n, p->n, 2}, mr = {residual, p->m, p->n, p->n, 2},
+              mw = {workspace, 1, (int64_t)need, (int64_t)need, 1};
+    for (const Mat& m : in)
+        if (touch(my, m) || touch(mp, m) || touch(mw, m)) return SSD_ERR_INVALID_ARG;
+    if (touch(my, mp) || touch(mp, mr) || touch(mw, my) || touch(mw, mp) || touch(mw, mr) ||
+        (y != residual && touch(my, mr)))
+        return SSD_ERR_INVALID_ARG;
+    LinearArgs a = {};
+    a.m = p->m; a.n = p->n; a.k = p->k; a.dtype = p->dtype; a.act = p->act;
+    a.x = {x, p->ldx, false};
+    a.w = {w, p->k, false};
+    a.x_scales = x_scales; a.w_scales = w_scales; a.bias = bias; a.residual = residual; a.y = y; a.pre = pre;
+    a.wait_iters = stall.rounds; a.loads = (uint32_t)stall.loads;
+    a.ws = (WsHeader*)workspace;
+    a.parts = workspace ? (float*)((char*)workspace + sizeof(WsHeader)) : nullptr;
+    return launch_linear(a, plan, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -194,32 +269,16 @@ size_t ssd_gate_scan_workspace_size(const ssd_gate_scan_params_t* p) {
 int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const void* x, const float* initial_states,
                   const int32_t* cu_seqlens, void* y, float* final_states, void* workspace, size_t workspace_bytes,
                   void* stream) {
-    const int rc = check_scan(p);
-    if (rc != SSD_OK) return rc;
-    if (!g || !x || !y || (p->ndocs > 0) != (cu_seqlens != nullptr)) return SSD_ERR_INVALID_ARG;
-    const size_t es = elem(p->dtype);
-    if (!aligned(g, es) || !aligned(x, es) || !aligned(y, es) || !aligned(initial_states, 4) ||
-        !aligned(final_states, 4) || !aligned(cu_seqlens, 4))
-        return SSD_ERR_INVALID_ARG;
-    const size_t need = ssd_gate_scan_workspace_size(p);
-    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
-    const int64_t rows = p->batch * p->seqlen, nst = p->ndocs > 0 ? p->ndocs : p->batch;
-    const Mat in[] = {{g, rows, p->width, p->g_stride, es}, {x, rows, p->width, p->x_stride, es},
-                      {initial_states, nst, p->width, p->width, 4}, {cu_seqlens, 1, p->ndocs + 1, p->ndocs + 1, 4}};
-    const Mat out[] = {{y, rows, p->width, p->width, es}, {final_states, nst, p->width, p->width, 4},
-                       {workspace, 1, (int64_t)need, (int64_t)need, 1}};
-    for (int i = 0; i < 3; ++i) {
-        for (const Mat& m : in)
-            if (touch(out[i], m)) return SSD_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (touch(out[i], out[j])) return SSD_ERR_INVALID_ARG;
-    }
-    GateScanArgs a = {};
-    a.batch = p->batch; a.seqlen = p->seqlen; a.width = p->width; a.dtype = p->dtype; a.ndocs = p->ndocs;
-    a.g_stride = p->g_stride; a.x_stride = p->x_stride;
-    a.g = g; a.x = x; a.init = initial_states; a.cu = cu_seqlens; a.y = y;
-    a.enter = initial_states; a.leave = final_states;
-    return launch_gate_scan(a, workspace, false, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    return gate_scan_impl(p, g, x, initial_states, cu_seqlens, y, final_states, workspace, workspace_bytes, stream, Stall());
+}
+
+int ssd_gate_scan_fault_inject(const ssd_gate_scan_params_t* p, const void* g, const void* x, const float* initial_states,
+                               const int32_t* cu_seqlens, void* y, float* final_states, void* workspace,
+                               size_t workspace_bytes, int32_t loads, uint32_t max_wait_rounds, void* stream) {
+    if (loads < -1 || max_wait_rounds < kMinInjectWaitRounds) return SSD_ERR_INVALID_ARG;
+    if (!workspace) return SSD_ERR_WORKSPACE;
+    return gate_scan_impl(p, g, x, initial_states, cu_seqlens, y, final_states, workspace, workspace_bytes, stream,
+                          Stall{max_wait_rounds, loads});
 }
 
 int ssd_gate_scan_bwd(const ssd_gate_scan_params_t* p, const void* g, const void* x, const void* y,
@@ -312,36 +371,16 @@ int ssd_linear_plan(const ssd_linear_params_t* p, int product, ssd_linear_plan_t
 int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* w, const float* x_scales, const float* w_scales,
                const float* bias, const void* residual, void* y, void* pre, void* workspace, size_t workspace_bytes,
                void* stream) {
-    const int rc = check_linear(p);
-    if (rc != SSD_OK) return rc;
-    const bool e4m3 = p->dtype == SSD_E4M3;
-    if (e4m3 != (w_scales != nullptr) || (!e4m3 && x_scales) || (e4m3 && !x_scales && p->m > 0)) return SSD_ERR_INVALID_ARG;
-    if (p->m == 0) return SSD_OK;
-    if (!x || !w || !y) return SSD_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(bias, 4) ||
-        !aligned(residual, 2) || !aligned(y, 2) || !aligned(pre, 2))
-        return SSD_ERR_INVALID_ARG;
-    const size_t es = elem(p->dtype);
-    const LinearPlan plan = linear_plan(p->m, p->n, (int64_t)p->k * es, true);
-    const size_t need = sizeof(WsHeader) + plan.parts_bytes;
-    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
-    const Mat in[] = {{x, p->m, p->k, p->ldx, es}, {w, p->n, p->k, p->k, es}, {x_scales, 1, p->m, p->m, 4},
-                      {w_scales, 1, p->n, p->n, 4}, {bias, 1, p->n, p->n, 4}};
-    const Mat my = {y, p->m, p->n, p->n, 2}, mp = {pre, p->m, p->n, p->n, 2}, mr = {residual, p->m, p->n, p->n, 2},
-              mw = {workspace, 1, (int64_t)need, (int64_t)need, 1};
-    for (const Mat& m : in)
-        if (touch(my, m) || touch(mp, m) || touch(mw, m)) return SSD_ERR_INVALID_ARG;
-    if (touch(my, mp) || touch(mp, mr) || touch(mw, my) || touch(mw, mp) || touch(mw, mr) ||
-        (y != residual && touch(my, mr)))
-        return SSD_ERR_INVALID_ARG;
-    LinearArgs a = {};
-    a.m = p->m; a.n = p->n; a.k = p->k; a.dtype = p->dtype; a.act = p->act;
-    a.x = {x, p->ldx, false};
-    a.w = {w, p->k, false};
-    a.x_scales = x_scales; a.w_scales = w_scales; a.bias = bias; a.residual = residual; a.y = y; a.pre = pre;
-    a.ws = (WsHeader*)workspace;
-    a.parts = workspace ? (float*)((char*)workspace + sizeof(WsHeader)) : nullptr;
-    return launch_linear(a, plan, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    return linear_impl(p, x, w, x_scales, w_scales, bias, residual, y, pre, workspace, workspace_bytes, stream, Stall());
+}
+
+int ssd_linear_fault_inject(const ssd_linear_params_t* p, const void* x, const void* w, const float* x_scales,
+                            const float* w_scales, const float* bias, const void* residual, void* y, void* pre,
+                            void* workspace, size_t workspace_bytes, int32_t loads, uint32_t max_wait_rounds, void* stream) {
+    if (loads < 0 || max_wait_rounds < kMinInjectWaitRounds) return SSD_ERR_INVALID_ARG;
+    if (!workspace) return SSD_ERR_WORKSPACE;
+    return linear_impl(p, x, w, x_scales, w_scales, bias, residual, y, pre, workspace, workspace_bytes, stream,
+                       Stall{max_wait_rounds, loads});
 }
 
 int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, const void* pre, const void* dy, void* dx,

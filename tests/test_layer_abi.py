@@ -228,3 +228,18 @@ def test_linear_plan_query(L):
         q = _lib.linear_plan(m, n, k, 1)
         parts = (q.tiles - q.whole) * q.splits if q.splits > 1 else 0
         assert L.ssd_linear_workspace_size(linear_params(m=m, n=n, k=k, ldx=k)) == 256 + 4 * parts * q.tile_rows * q.tile_cols
+
+
+def test_fault_injection_refusals(L):
+    """An injected stall wants a workspace (its status word), a count of loads and a cap that the drains outlast."""
+    p, q = linear_params(), scan_params()
+    lin_args = [p, G, 2 * G, None, None, None, None, 3 * G, None]
+    scan_args = [q, G, G + 256, None, None, 3 * G, None]
+    for loads, rounds, code in ((-1, 1 << 14, 1), (0, 4095, 1), (0, 0, 1)):
+        assert L.ssd_linear_fault_inject(*lin_args, 4 * G, 1 << 29, loads, rounds, None) == code
+    for loads, rounds, code in ((-2, 1 << 14, 1), (0, 4095, 1), (-1, 0, 1)):
+        assert L.ssd_gate_scan_fault_inject(*scan_args, 4 * G, 1 << 28, loads, rounds, None) == code
+    assert L.ssd_linear_fault_inject(*lin_args, None, 0, 0, 1 << 14, None) == 3
+    assert L.ssd_gate_scan_fault_inject(*scan_args, None, 0, 0, 1 << 14, None) == 3
+    assert L.ssd_linear_fault_inject(linear_params(k=0), *lin_args[1:], 4 * G, 1 << 29, 0, 1 << 14, None) == 1
+    assert L.ssd_gate_scan_fault_inject(scan_params(width=0), *scan_args[1:], 4 * G, 1 << 28, 0, 1 << 14, None) == 1
