@@ -425,7 +425,8 @@ SSD_API int ssd_gate_scan(const ssd_gate_scan_params_t* p, const void* g, const 
  *   dfinal_states  (nstates, width) fp32, or NULL (zeros)
  *   dg, dx         (batch, seqlen, width) dtype, token strides g_stride, x_stride; written
  *   dinitial_states (nstates, width) fp32, or NULL
- * h_{t-1} is recomputed in fp32 from the h of every 8th token (every 4th in fp32), which is read from y.
+ * h_{t-1} is recomputed in fp32 from the h of every 8th token (every 4th in fp32), which is read from y: where h lies close
+ * to x, the difference in dg keeps the absolute error of y's rounding (2^-9 of h in bf16; none with fp32 tensors).
  * Workspace, launches, errors and aliasing as for ssd_gate_scan(). */
 SSD_API int ssd_gate_scan_bwd(const ssd_gate_scan_params_t* p, const void* g, const void* x, const void* y,
              const float* initial_states, const int32_t* cu_seqlens, const void* dy, const float* dfinal_states,

@@ -1,8 +1,12 @@
 """The operators around the scan: residual RMS norm, projection, gated recurrence.
 
-Thin wrappers over the C ABI like the package's other entry points: they check
+Wrappers over the C ABI like the package's other entry points: they check
 tensors, take device pointers and the stream, and call the library.  Outputs
 and workspaces are allocated on the stream that the call runs on.
+
+Device-side waits are bounded.  One that runs out (a stalled GPU) ends its kernel with outputs undefined, and offsets of
+documents that break their rule leave them so too; a call with check_status=True waits for its stream and raises then, without it
+nothing does.
 """
 from __future__ import annotations
 
@@ -361,7 +365,8 @@ def gate_scan_bwd(g, x, y, dy, initial_states=None, dfinal_states=None, cu_seqle
 
     dg and dx may be given to be written in place: of g's and x's shapes and token strides (column ranges of a
     projection's gradient, say); by default they are allocated with these strides.
-    Returns a dict with dg, dx and dinit (None unless want_dinit; by default with initial_states)."""
+    Returns a dict with dg, dx and dinit (None unless want_dinit; by default with initial_states).  States inside are recomputed
+    from y's every few tokens: with bf16 the difference of state and input in dg keeps y's rounding, 2^-9 of the state."""
     dev = _device("g", g)
     if stream is not None or _current_device() != dev:
         with _elsewhere(dev, stream):
