@@ -418,8 +418,13 @@ int64_t bwd_slots(int64_t rows, int width, bool lean, int* rows_per_cta, int* th
 
 // 16-byte vectors where every array starts on 16 bytes and rows hold one at least, elements otherwise.  33.5 M elements,
 // us by the rule and by the other side of it (fp32 residual unless said):
-//   lean, bf16 beyond 1280 columns   2560 columns 88.0 (8 elements 88.2), 4096 90.3 (94.4); bf16 residual 43.9 (54.1)
-//   not lean, fp32                   5120 columns 85.4 (97.2; it spills)
+//   lean, bf16 beyond 1280 columns   2048 columns 86.7 (8 elements 87.6), 2560 85.9 (84.0), 4096 87.9 (91.1); bf16 residual 2048
+//                                    49.9 (59.9), 2560 50.9 (52.0), 4096 52.0 (58.0); no residual 2048 40.9 (56.4), 4096 41.7 (52.6)
+//   not lean, bf16 up to there       1024 columns 83.1 (16 elements 130.9), 1280 82.5 (101.2); bf16 residual 1024 52.0 (72.7), 1280
+//                                    51.1 (73.9); no residual 512 46.6 (40.1), 1024 47.1 (57.4), 1280 44.8 (57.8)
+//   where the other side is faster   1536 columns, whose rows are 96 threads of 16: 96.4 (84.3), 66.1 (55.5), 54.2 (51.6); 5120, one CTA an
+//                                    SM either way: 87.4 (87.6), 65.1 (53.1), 49.9 (47.7)
+//   not lean, fp32                   5120 columns 85.4 (16 elements 97.2; it spills)
 //   not lean, bf16 shifted           2049 columns 99 (112; it spills), 4001 102 (107); bf16 residual lean, 4001 53 (62)
 //   rows beyond 5120 columns         8192 columns 91.6, fp32 83.7, bf16 residual 45 (1024 threads of 8, without the
 //                                    next row ahead: 119, 106)

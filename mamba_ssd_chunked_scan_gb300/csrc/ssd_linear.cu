@@ -22,8 +22,8 @@
 //
 // Measured: 16384 x 10240 x 2560 bf16 430-435 us back to back (1.97 PFLOP/s; the library's product 419) and 507 under
 // the power cap (1.69; the library's sustained rate 1.72); both gradients of it 906-928 us (library 880); e4m3
-// 4099 x 2560 x 5120 with its residual 46 us, from HBM; 8 rows of e4m3 by 10240 x 2560 7.2 us in a graph, of which
-// W's bytes need 3.9.  dpre of 8192 x 5120 42 us (6.0 TB/s).
+// 4099 x 2560 x 5120 with its residual 46-49 us, from HBM; 8 rows of e4m3 by 10240 x 2560 8.1 us in a graph, of which
+// W's bytes need 3.9, of bf16 12.5 (7.7).  dpre of 8192 x 5120 42 us (6.0 TB/s).
 //
 // Sums are fp32 in tensor memory.  Tiles run in waves of one per SM (or pair); those of the last wave, which would
 // leave SMs idle, are split along the contraction into parts that are summed in a fixed order
@@ -892,7 +892,10 @@ cudaError_t launch_kind(const LinearParams& p, const LinearPlan& plan, cudaStrea
 // 520 cycles by a pair and 541 by a CTA at 256 columns, where the MMAs bound it, but 417 at 128 and 390 at 64 (the
 // rows of A are read from shared memory for each MMA however few the columns); a tile's start 600; a
 // launch's first loads and last epilogue about 15 a column, and 3000 more for clusters; parts 6300 for the
-// join and a cycle per 4000 bytes of them, written and read.
+// join and a cycle per 4000 bytes of them, written and read.  (In bursts, us a block over three waves: a pair 0.324, a CTA 0.371, 0.223
+// at 128 columns, 0.216 at 64; two parts of 40 tiles of 128 x 256 over 128 blocks 31.3 us, one 48.2.)  Transposed or not (us, weights
+// from HBM, in a graph): 64 rows by 10240 x 2560 bf16 13.8 and 13.8, e4m3 9.5 and 9.3; by 2560 x 5120 11.9 and 14.0, 9.3 and 9.8;
+// 128 rows 21.7 and 14.1, 14.9 and 9.7; 13.3 and 14.8, 10.3 and 10.4.
 static LinearPlan find_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap) {
     LinearPlan best = {};
     const int64_t kblocks = (kbytes + kRowB - 1) / kRowB;
