@@ -512,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_linear_tc(const __grid_consta
             const uint64_t da0 = AMN ? ptx::sdesc_sw128(base, 8192, 1024) : ptx::sdesc_sw128(base, 16, 1024);
             const uint64_t db0 = BMN ? ptx::sdesc_sw128(base + C::kA, 8192, 1024) : ptx::sdesc_sw128(base + C::kA, 16, 1024);
             constexpr uint32_t ka = (AMN ? 2048 : 32) >> 4, kb_ = (BMN ? 2048 : 32) >> 4;
+            pdl_wait();   // (or the limit of the first wait would count the time of the launches before)
             uint32_t tile = 0, st = 0, phase = 0;
             bool go = true;
             for (int item = worker; go && item < p.items; item += workers, ++tile) {

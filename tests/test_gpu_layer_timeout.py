@@ -77,3 +77,42 @@ def test_stalled_recurrence(width, docs, dtype, loads):
     assert status(work) == (0, 0)
     assert lib.ssd_gate_scan(*args, st) == 0
     assert status(work) == (0, 0) and torch.equal(y, want[0]) and torch.equal(fin, want[1])
+
+
+def test_limits_count_from_the_end_of_earlier_launches():
+    """A launch that starts while a long one before it still runs does not count that time against its own waits: with caps far
+    below the earlier launch's time, and everything loaded, the calls are ordinary ones."""
+    from mamba_ssd_chunked_scan_gb300 import _lib
+    lib = _lib.lib
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    # the sum of many rows' gradients of eight columns: one CTA adds the shares, for tens of milliseconds, and the rest of the GPU is free
+    tall, small = torch.ones(1 << 29, 8, dtype=BF, device="cuda"), torch.ones(8, 8, dtype=BF, device="cuda")
+    long = lambda: ssd.linear_bwd(tall, tall, small, want_dx=False, want_dw=False, want_dbias=True)
+    assert (long()["dbias"] == 1 << 29).all()
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    long()
+    b.record()
+    torch.cuda.synchronize()
+    print("the call before: %.1f ms" % a.elapsed_time(b))
+
+    for m, n, k in ((8, 2560, 256), (300, 520, 2048)):
+        x, w = r(m, k).to(BF), r(n, k).to(BF)
+        want, y = ssd.linear(x, w), torch.empty(m, n, dtype=BF, device="cuda")
+        p = _lib.LinearParams(m, k, n, k, _lib.SSD_BF16, 0)
+        work = torch.empty(lib.ssd_linear_workspace_size(p), dtype=torch.uint8, device="cuda")
+        long()
+        assert lib.ssd_linear_fault_inject(ctypes.byref(p), x.data_ptr(), w.data_ptr(), None, None, None, None, y.data_ptr(), None,
+                                           work.data_ptr(), work.numel(), 0x7fffffff, 4096, st) == 0
+        assert status(work) == (0, 0) and torch.equal(y, want), (m, n, k)
+    for width in (256, 255):
+        g, x = r(1, 2000, width).to(BF), r(1, 2000, width).to(BF)
+        want, y = ssd.gate_scan(g, x), torch.empty_like(x)
+        p = _lib.GateScanParams(1, 2000, width, width, width, 0, _lib.SSD_BF16)
+        work = torch.empty(lib.ssd_gate_scan_workspace_size(p), dtype=torch.uint8, device="cuda")
+        long()
+        assert lib.ssd_gate_scan_fault_inject(ctypes.byref(p), g.data_ptr(), x.data_ptr(), None, None, y.data_ptr(), None,
+                                              work.data_ptr(), work.numel(), 0x7fffffff, 4096, st) == 0
+        assert status(work) == (0, 0) and torch.equal(y, want), width
