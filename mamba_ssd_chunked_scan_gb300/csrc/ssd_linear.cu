@@ -224,7 +224,9 @@ __device__ __forceinline__ float act_value(float v, int act) {
     if (act == SSD_ACT_GELU) return v * sigmoid(2.f * kGeluC * (v + kGeluA * v * v * v));
     return v;
 }
+// (Beyond a thousand either slope is 0 or 1 to the last bit, and squares of arguments would overflow into 0 times infinity.)
 __device__ __forceinline__ float act_slope(float v, int act) {
+    v = fabsf(v) > 1000.f ? copysignf(1000.f, v) : v;
     if (act == SSD_ACT_SILU) {
         const float s = sigmoid(v);
         return s * (1.f + v * (1.f - s));
