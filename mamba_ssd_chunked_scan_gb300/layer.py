@@ -32,6 +32,8 @@ _empty = torch.empty
 @contextlib.contextmanager
 def _elsewhere(dev, stream):
     """The given device, and stream if any, made current: a call's allocations and launches belong to them."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream: expected one of cuda:{dev}, where the tensors are, got one of {stream.device}")
     with torch.cuda.device(dev):
         if stream is None:
             yield

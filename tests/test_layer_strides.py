@@ -1,4 +1,4 @@
-"""Which views of a wider matrix the operators around the scan take as rows at one stride."""
+"""Which views of a wider matrix, and which streams, the operators around the scan take."""
 import pytest
 import torch
 
@@ -26,6 +26,17 @@ def test_rows_at_one_stride(row_stride, view, step):
 def test_others_are_refused(row_stride, view):
     with pytest.raises(ValueError):
         row_stride("x", view)
+
+
+def test_stream_of_another_device_is_refused():
+    """Made current, it would take the call to its own device, and the tensors' device would then get another stream."""
+    from types import SimpleNamespace
+    from mamba_ssd_chunked_scan_gb300 import build
+    build.build()
+    from mamba_ssd_chunked_scan_gb300 import layer
+    with pytest.raises(ValueError, match="stream"):
+        with layer._elsewhere(0, SimpleNamespace(device=torch.device("cuda", 1))):
+            pass
 
 
 @pytest.mark.gpu
