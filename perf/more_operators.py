@@ -365,7 +365,8 @@ def run(state):
                            out_dtype=None if s["out"] == "none" else DTYPES[s["out"]], pack=s["keep"])
     elif op == "block_bwd":
         r = ssd.block_norm_bwd(s["dout"], s["dres"], s["x"], s["h"], s["weight"], s["gatev"], s["next_weight"], scale=s["scale"], eps=EPS,
-                               x_scales=s["xs"], h_scales=s["hs"], gate_scales=s["gs"], dgate=s["dgate"])
+                               x_scales=s["xs"], h_scales=s["hs"], gate_scales=s["gs"], dgate=s["dgate"],
+                               dtype=DTYPES[s["dtype"]])
     else:
         r = ssd.linear_bwd(s["dy"], s["x"], s["w"], s["pre"], act=s["act"], x_scales=s["xs"], pre_scales=s["ps"], want_dbias=s["bias"])
     return {k: v for k, v in r.items() if v is not None}
