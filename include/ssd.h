@@ -310,6 +310,118 @@ SSD_API int ssd_add_norm_bwd(int64_t rows, int32_t width, int32_t dtype, int32_t
              const void* dout, const void* h, const float* weight, const float* rstd, const void* dresidual_out,
              void* dx, void* dresidual, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
+/* 8-bit rows, for activations that the backward pass reads again: each row's group of group_size columns
+ * (group_size divides width; width: one scale a row) becomes e4m3 numbers and a scale,
+ *
+ *     scale = the smallest power of two with max |x| <= 448 scale over the group's finite x, at least 2^-108
+ *     codes = x / scale, rounded once to nearest even;   an infinity or a NaN becomes NaN
+ *
+ * and stands for codes * scale, which is exact in bf16 and fp32.
+ *   x        (rows, width) dtype (SSD_F32 or SSD_BF16), x_stride elements between rows (>= width)
+ *   codes    (rows, width) e4m3, contiguous;  scales (rows, width / group_size) fp32
+ * Bases aligned to their elements (16-byte aligned ones, with sizes and strides of whole 16-byte vectors of x, run faster);
+ * no output may overlap an input.  rows >= 0 (0: nothing is launched), rows * groups < 2^31, group_size <= 16384, width and x_stride
+ * < 2^30 (else SSD_ERR_UNSUPPORTED).  One launch, no workspace; bitwise deterministic. */
+SSD_API int ssd_pack_rows(int64_t rows, int32_t width, int32_t group_size, int32_t dtype, int64_t x_stride,
+             const void* x, void* codes, float* scales, void* stream);
+
+/* out = codes * scale, in dtype (rounded once; exact for the scales of ssd_pack_rows()).  codes, scales and limits
+ * as there (any group_size that divides width); out (rows, width) contiguous. */
+SSD_API int ssd_unpack_rows(int64_t rows, int32_t width, int32_t group_size, int32_t dtype,
+             const void* codes, const float* scales, void* out, void* stream);
+
+/* The gate and norm after the scan (ssd_gate_norm()) in training: with u = y * silu(z) per row and group of
+ * group_size columns,
+ *
+ *     out = u * rstd * weight,   rstd = 1 / sqrt(mean_group(u^2) + eps),   silu(z) = z / (1 + exp(-z)) */
+typedef struct {
+    int64_t rows;
+    int64_t z_stride;   /* elements between rows of z, >= width (z may be a column range of a projection's rows) */
+    int64_t dz_stride;  /* ... of dz                                                                             */
+    int32_t width;
+    int32_t group_size; /* divides width; at most 8192 (else SSD_ERR_UNSUPPORTED)                                */
+    int32_t dtype;      /* SSD_F32 or SSD_BF16: of out, dout, dy, dz, and of y and z unless they are 8-bit rows   */
+    float eps;          /* >= 0, finite                                                                          */
+} ssd_gate_norm_params_t;
+
+/* out as above, and y and z as 8-bit rows for the backward pass (one scale a row and group).
+ *   y (rows, width) dtype contiguous;  z (rows, width) dtype, row stride z_stride;  weight (width) fp32
+ *   out (rows, width) dtype;  y_codes, z_codes (rows, width) e4m3;  y_scales, z_scales (rows, width / group_size) fp32
+ * All contiguous but z; limits, alignment and overlaps as for ssd_pack_rows().  One launch, no workspace; bitwise deterministic. */
+SSD_API int ssd_gate_norm_pack(const ssd_gate_norm_params_t* p, const void* y, const void* z, const float* weight,
+             void* out, void* y_codes, float* y_scales, void* z_codes, float* z_scales, void* stream);
+
+/* Gradients of <dout, out>.  With p = dout * weight and n = u * rstd,
+ *
+ *     du = rstd (p - n mean_group(p n));   dy = du silu(z);   dz = du y s (1 + z (1 - s)), s = 1 / (1 + exp(-z))
+ *     dweight = sum_rows dout n
+ *
+ *   y, z               dtype, or e4m3 codes where y_scales, z_scales (one a row and group) are given; codes are contiguous
+ *                      (z_stride == width)
+ *   dout, dy           (rows, width) dtype, contiguous;  dz (rows, width) dtype, row stride dz_stride (it may be a
+ *                      column range of a projection's gradient; columns outside of it are left alone)
+ *   out                (rows, width) dtype, or NULL: the forward's result, computed again
+ *   dweight            (width) fp32, written (zeros where rows == 0)
+ * `workspace`: ssd_gate_norm_bwd_workspace_size() bytes (0 on invalid parameters or rows == 0), 16-byte aligned, needs no
+ * initialisation; calls that share it must be ordered on one stream.  No output may overlap an input.  Two launches;
+ * bitwise deterministic (dweight is summed in a fixed order). */
+SSD_API size_t ssd_gate_norm_bwd_workspace_size(const ssd_gate_norm_params_t* p);
+SSD_API int ssd_gate_norm_bwd(const ssd_gate_norm_params_t* p, const void* dout, const void* y, const float* y_scales,
+             const void* z, const float* z_scales, const float* weight, void* dy, void* dz, void* out, float* dweight,
+             void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norm after a block, with the block's gate, the scaled addition to the residual stream and the next block's
+ * norm, in one pass.  Per row:
+ *
+ *     u   = x * silu(gate)                                     (gate NULL: u = x)
+ *     h   = residual + scale * (u * rstd1 * weight),           rstd1 = 1 / sqrt(mean(u^2) + eps)
+ *     out = h * rstd2 * next_weight,                           rstd2 = 1 / sqrt(mean(h^2) + eps)  (h unrounded)
+ */
+typedef struct {
+    int64_t rows;
+    int64_t gate_stride;     /* elements between rows of gate, >= width (ignored without a gate) */
+    int64_t dgate_stride;    /* ... of dgate                                                     */
+    int32_t width;           /* 1 to 8192 (else SSD_ERR_UNSUPPORTED)                             */
+    int32_t dtype;           /* SSD_F32 or SSD_BF16: of x, gate, dout, dx, dgate, and of out     */
+    int32_t residual_dtype;  /* SSD_F32, or SSD_BF16 where dtype is: of residual, h, dresidual   */
+    int32_t out_dtype;       /* dtype, or SSD_E4M3: out as 8-bit rows                            */
+    float scale;             /* finite                                                           */
+    float eps;               /* >= 0, finite                                                     */
+} ssd_block_norm_params_t;
+
+/*   x         (rows, width) dtype;  gate (rows, width) dtype, row stride gate_stride, or NULL
+ *   residual  (rows, width) residual_dtype;  residual_out (h) of the same type, may be residual (in place)
+ *   weight, next_weight (width) fp32; next_weight NULL: no second norm, and out and out_scales are ignored
+ *   out       (rows, width) out_dtype;  out_scales (rows) fp32, with SSD_E4M3: rows as ssd_pack_rows() makes them
+ *   x_codes (rows, width) e4m3, x_scales (rows) fp32 (and gate_codes, gate_scales with a gate): x and gate as 8-bit rows for
+ *             the backward pass, all given or all NULL
+ * All contiguous but gate; limits, alignment and (but for residual_out) overlaps as for ssd_pack_rows().  One launch, no
+ * workspace; bitwise deterministic. */
+SSD_API int ssd_block_norm(const ssd_block_norm_params_t* p, const void* x, const void* gate, const void* residual,
+             const float* weight, const float* next_weight, void* residual_out, void* out, float* out_scales,
+             void* x_codes, float* x_scales, void* gate_codes, float* gate_scales, void* stream);
+
+/* Gradients of <dout, out> + <dresidual_out, residual_out>.  With p2 = dout * next_weight and n2 = h rstd2,
+ *
+ *     dh = dresidual_out + rstd2 (p2 - n2 mean(p2 n2))         (no next_weight: dh = dresidual_out)
+ *     p1 = scale dh weight, n1 = u rstd1:  du = rstd1 (p1 - n1 mean(p1 n1))
+ *     dx = du silu(gate), dgate = du x s (1 + gate (1 - s)), s = 1 / (1 + exp(-gate));   dresidual = dh
+ *     dweight = sum_rows scale dh n1;   dnext_weight = sum_rows dout n2
+ *
+ *   x, gate, h      as the forward had and left them (h: its residual_out), or e4m3 codes where x_scales, gate_scales, h_scales
+ *                   (one a row) are given; codes are contiguous.  h is ignored without next_weight
+ *   dout            (rows, width) dtype, given with next_weight and only then
+ *   dresidual_out   (rows, width) residual_dtype
+ *   dx, dgate       (rows, width) dtype; dgate (with a gate) row stride dgate_stride;  dresidual (rows, width) residual_dtype
+ *   dweight, dnext_weight  (width) fp32, written
+ * `workspace`: ssd_block_norm_bwd_workspace_size() bytes (enough with and without next_weight).  Otherwise as for
+ * ssd_gate_norm_bwd(). */
+SSD_API size_t ssd_block_norm_bwd_workspace_size(const ssd_block_norm_params_t* p);
+SSD_API int ssd_block_norm_bwd(const ssd_block_norm_params_t* p, const void* dout, const void* dresidual_out,
+             const void* x, const float* x_scales, const void* gate, const float* gate_scales, const void* h, const float* h_scales,
+             const float* weight, const float* next_weight, void* dx, void* dgate, void* dresidual, float* dweight,
+             float* dnext_weight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Matrix product with its epilogue, for the projections before and after the scan:
  *
  *     v[m,n] = sx[m] sw[n] sum_k x[m,k] w[n,k] + bias[n]       (the scales with SSD_E4M3 only)
@@ -362,6 +474,17 @@ SSD_API int ssd_linear(const ssd_linear_params_t* p, const void* x, const void* 
  * determinism as for ssd_linear(), with ssd_linear_bwd_workspace_size(p). */
 SSD_API int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, const void* pre, const void* dy,
              void* dx, void* dw, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same from 8-bit rows, p->dtype being that of w and dy (SSD_BF16): x is (m, k) e4m3 codes, row stride ldx >= k,
+ * where x_scales (m) fp32 are given, and pre (m, n) e4m3 codes, contiguous, where pre_scales (m) fp32 are (neither: the
+ * call above).  They stand for codes * scale: x so in bf16, rounded once (nothing is lost with the scales of
+ * ssd_pack_rows()), as the product's operand in the workspace, pre in fp32.  Codes may start at any byte; ldx is any number from k on
+ * then. */
+SSD_API size_t ssd_linear_bwd_packed_workspace_size(const ssd_linear_params_t* p);
+SSD_API int ssd_linear_bwd_packed(const ssd_linear_params_t* p, const void* x, const float* x_scales, const void* w,
+             const void* pre, const float* pre_scales, const void* dy, void* dx, void* dw, float* dbias,
+             void* workspace, size_t workspace_bytes, void* stream);
+
 
 /* How a product of ssd_linear() or ssd_linear_bwd() runs (diagnostic, as ssd_fwd_plan(); needs no GPU).  product: 0 y,
  * 1 dx, 2 dw (both with SSD_BF16 only).  Returns SSD_OK, or the status that the call would return for these parameters;

@@ -16,8 +16,10 @@ import torch
 
 SSD_F32, SSD_BF16, SSD_E4M3 = 0, 1, 2
 
-# the operators around the scan (layer.py), loaded with the library on first use
+# the operators around the scan (layer.py) and the norms around a block with their 8-bit checkpoints (norms.py), loaded with
+# the library on first use
 _LAYER = ("add_norm", "add_norm_bwd", "gate_scan", "gate_scan_bwd", "gate_scan_step", "linear", "linear_bwd")
+_NORMS = ("pack_rows", "unpack_rows", "gate_norm_bwd", "block_norm", "block_norm_bwd")
 
 
 class _LazyLib:
@@ -34,14 +36,14 @@ _lib = _LazyLib()
 def __getattr__(name):
     if name == "SSDError":
         return _lib.SSDError
-    if name in _LAYER:
-        fn = getattr(importlib.import_module(__name__ + ".layer"), name)
+    if name in _LAYER or name in _NORMS:
+        fn = getattr(importlib.import_module(__name__ + (".layer" if name in _LAYER else ".norms")), name)
         globals()[name] = fn
         return fn
     raise AttributeError(name)
 
 __all__ = ["ssd_fwd", "SSDForward", "ssd_bwd", "ssd_step", "gate_norm", "segsum_dump", "check_status", "SSDError", "plan",
-           *_LAYER]
+           *_LAYER, *_NORMS]
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -224,10 +226,18 @@ def ssd_bwd(x, dt, A, B, C, dy, D=None, initial_states=None, dfinal_states=None,
     return g
 
 
-def gate_norm(y, z, weight, group_size, eps=1e-5, *, out=None, stream=None):
+def gate_norm(y, z, weight, group_size, eps=1e-5, *, out=None, pack=False, stream=None):
     """out = rmsnorm_groups(y * silu(z)) * weight over the last dimension, in one
     pass (groups of `group_size` channels).  y, z: (..., width) bf16 or fp32,
-    contiguous; weight: (width,) fp32.  `out` may be y (in place)."""
+    contiguous; weight: (width,) fp32.  `out` may be y (in place).
+
+    With pack, returns (out, kept): kept is a dict of y and z as 8-bit rows for gate_norm_bwd (``y``, ``y_scales``, ``z``,
+    ``z_scales``; one scale a row and group).  z may be a column range of a wider matrix then, and group_size any divisor of the
+    width."""
+    if pack:
+        if out is not None:
+            raise ValueError("out: not with pack")
+        return importlib.import_module(__name__ + ".norms").gate_norm_pack(y, z, weight, group_size, eps, stream=stream)
     width = y.shape[-1]
     rows = y.numel() // width if width else 0
     if tuple(z.shape) != tuple(y.shape) or z.dtype != y.dtype or not (y.is_contiguous() and z.is_contiguous()):

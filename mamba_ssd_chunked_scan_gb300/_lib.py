@@ -23,7 +23,10 @@ EXPORTS = ("ssd_fwd_workspace_size", "ssd_workspace_init", "ssd_fwd", "ssd_check
            "ssd_gate_norm", "ssd_check_status_where", "ssd_fwd_fault_inject", "ssd_add_norm",
            "ssd_add_norm_bwd_workspace_size", "ssd_add_norm_bwd", "ssd_gate_scan_workspace_size", "ssd_gate_scan",
            "ssd_gate_scan_bwd", "ssd_gate_scan_step", "ssd_linear_workspace_size", "ssd_linear_bwd_workspace_size",
-           "ssd_linear", "ssd_linear_bwd", "ssd_linear_plan", "ssd_linear_fault_inject", "ssd_gate_scan_fault_inject")
+           "ssd_linear", "ssd_linear_bwd", "ssd_linear_plan", "ssd_linear_fault_inject", "ssd_gate_scan_fault_inject",
+           "ssd_pack_rows", "ssd_unpack_rows", "ssd_gate_norm_pack", "ssd_gate_norm_bwd_workspace_size", "ssd_gate_norm_bwd",
+           "ssd_block_norm", "ssd_block_norm_bwd_workspace_size", "ssd_block_norm_bwd", "ssd_linear_bwd_packed_workspace_size",
+           "ssd_linear_bwd_packed")
 
 
 class SSDParams(ctypes.Structure):
@@ -42,6 +45,17 @@ class GateScanParams(ctypes.Structure):
 class LinearParams(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("ldx", ctypes.c_int64), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class GateNormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64), ("width", ctypes.c_int32),
+                ("group_size", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class BlockNormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("dgate_stride", ctypes.c_int64), ("width", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class LinearPlan(ctypes.Structure):
@@ -123,6 +137,28 @@ def _load():
     lib.ssd_linear_fault_inject.restype = ctypes.c_int
     lib.ssd_gate_scan_fault_inject.argtypes = [G] + [vp] * 7 + [sz, i32, ctypes.c_uint32, vp]
     lib.ssd_gate_scan_fault_inject.restype = ctypes.c_int
+    lib.ssd_linear_bwd_packed_workspace_size.argtypes = [N]
+    lib.ssd_linear_bwd_packed_workspace_size.restype = sz
+    lib.ssd_linear_bwd_packed.argtypes = [N] + [vp] * 10 + [sz, vp]
+    lib.ssd_linear_bwd_packed.restype = ctypes.c_int
+    lib.ssd_pack_rows.argtypes = [i64, i32, i32, i32, i64] + [vp] * 4
+    lib.ssd_pack_rows.restype = ctypes.c_int
+    lib.ssd_unpack_rows.argtypes = [i64, i32, i32, i32] + [vp] * 4
+    lib.ssd_unpack_rows.restype = ctypes.c_int
+    GN = ctypes.POINTER(GateNormParams)
+    lib.ssd_gate_norm_pack.argtypes = [GN] + [vp] * 9
+    lib.ssd_gate_norm_pack.restype = ctypes.c_int
+    lib.ssd_gate_norm_bwd_workspace_size.argtypes = [GN]
+    lib.ssd_gate_norm_bwd_workspace_size.restype = sz
+    lib.ssd_gate_norm_bwd.argtypes = [GN] + [vp] * 11 + [sz, vp]
+    lib.ssd_gate_norm_bwd.restype = ctypes.c_int
+    BN = ctypes.POINTER(BlockNormParams)
+    lib.ssd_block_norm.argtypes = [BN] + [vp] * 13
+    lib.ssd_block_norm.restype = ctypes.c_int
+    lib.ssd_block_norm_bwd_workspace_size.argtypes = [BN]
+    lib.ssd_block_norm_bwd_workspace_size.restype = sz
+    lib.ssd_block_norm_bwd.argtypes = [BN] + [vp] * 16 + [sz, vp]
+    lib.ssd_block_norm_bwd.restype = ctypes.c_int
     lib.ssd_linear_plan.argtypes = [N, ctypes.c_int, ctypes.POINTER(LinearPlan)]
     lib.ssd_linear_plan.restype = ctypes.c_int
     return lib

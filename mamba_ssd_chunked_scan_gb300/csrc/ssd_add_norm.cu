@@ -3,7 +3,7 @@
 //                             out = h rstd w  (bf16, fp32, or e4m3 rows with a scale each)
 //   ssd_add_norm_bwd_kernel   dh = rstd (w do - xh mean(w do xh)) + dres,  xh = h rstd,
 //                             and each row slot's share of dw = sum_rows do xh
-//   ssd_add_norm_bwd_reduce   dw from the shares, in a fixed order
+//   ssd_share_sum             dw from the shares, in a fixed order (of two weights, side by side in the shares, for ssd_block_norm_bwd)
 //
 // A row is held in registers from its one read to its one write, so both passes
 // are bound by HBM: 16384 x 2560, bf16 with an fp32 residual, 73.9 us forward (6.81 TB/s), e4m3 rows 69 us;
@@ -332,28 +332,28 @@ __global__ void __launch_bounds__(THREADS) ssd_add_norm_bwd_kernel(AddNormBwdArg
     }
 }
 
-// dw[e] = sum over the shares: COLS columns (16 or 32) per CTA, the shares dealt to its 1024 / COLS rows of threads, whose
+// dw[e] (next[e - W] from column W on) = sum over the shares: COLS columns (16 or 32) per CTA, the shares dealt to its 1024 / COLS rows of threads, whose
 // sums are added in their order.
 template <int COLS>
-__global__ void __launch_bounds__(1024) ssd_add_norm_bwd_reduce(const float* shares, int nshares, int W, float* dw) {
+__global__ void __launch_bounds__(1024) ssd_share_sum(const float* shares, int nshares, int columns, int W, float* dw, float* next) {
     __shared__ float part[32][COLS + 1];
     const int lane = threadIdx.x % COLS, w = threadIdx.x / COLS;
     const int e = blockIdx.x * COLS + lane;
     float s = 0.f;
     pdl_trigger();
     pdl_wait();   // launched while the shares are still being summed
-    if (e < W) {
+    if (e < columns) {
 #pragma unroll 4
-        for (int k = w; k < nshares; k += 1024 / COLS) s += shares[(size_t)k * W + e];
+        for (int k = w; k < nshares; k += 1024 / COLS) s += shares[(size_t)k * columns + e];
     }
     if (COLS == 16) s += __shfl_xor_sync(0xffffffffu, s, 16);   // the warp's two rows
     if ((threadIdx.x & 31) < COLS) part[threadIdx.x >> 5][lane] = s;
     __syncthreads();
-    if (threadIdx.x < COLS && e < W) {
+    if (threadIdx.x < COLS && e < columns) {
         float t = 0.f;
 #pragma unroll
         for (int k = 0; k < 32; ++k) t += part[k][lane];
-        dw[e] = t;
+        (e < W ? dw : next - W)[e] = t;
     }
 }
 
@@ -486,10 +486,14 @@ cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& args, cudaStream_t st) {
     else
         e = launch_bwd_typed<float, float>(a, &nshares, st);
     if (e != cudaSuccess) return e;
+    return launch_share_sum(a.shares, (int)nshares, a.width, a.width, a.dweight, nullptr, st);
+}
+
+cudaError_t launch_share_sum(const float* shares, int nshares, int width, int columns, float* dw, float* next, cudaStream_t st) {
     // 16 columns a CTA while all CTAs run at once (20000 x 256 in a graph 17.2 us, with 32 18.6; 4096 x 8192 94 and 89)
-    const int cols = a.width <= 16 * 2 * kAddNormSMs ? 16 : 32;
-    return launch_kernel(cols == 16 ? ssd_add_norm_bwd_reduce<16> : ssd_add_norm_bwd_reduce<32>, (unsigned)((a.width + cols - 1) / cols),
-                         1024, 0, st, true, (const float*)a.shares, (int)nshares, a.width, a.dweight);
+    const int cols = columns <= 16 * 2 * kAddNormSMs ? 16 : 32;
+    return launch_kernel(cols == 16 ? ssd_share_sum<16> : ssd_share_sum<32>, (unsigned)((columns + cols - 1) / cols), 1024, 0, st, true,
+                         shares, nshares, columns, width, dw, next);
 }
 
 }  // namespace ssd

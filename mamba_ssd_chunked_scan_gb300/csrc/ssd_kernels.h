@@ -169,6 +169,73 @@ struct AddNormBwdArgs {
     float inv_width;
 };
 
+// 8-bit rows (ssd_pack_rows, ssd_unpack_rows): units are rows' groups of columns.
+constexpr int kPackMaxSize = 16384;   // 1024 threads x 16 elements
+struct PackArgs {
+    int64_t units;         // rows * groups
+    int size;              // columns of a unit
+    int groups;
+    int dtype;             // of x or out
+    int64_t stride;        // elements between rows of x (packing) or of the codes (unpacking)
+    const void* x;
+    void* codes;
+    float* scales;         // [units]
+    void* out;
+    int units_per_cta;
+};
+
+// The norm after a block (ssd_block_norm) and the gate and norm after the scan with its checkpoint (ssd_gate_norm_pack), and their
+// gradients.  Units are rows, or rows' groups of columns (gate and norm; no residual then).
+constexpr int kBlockNormMaxSize = 8192;   // 512 threads x 16 elements
+struct BlockNormArgs {
+    int64_t units;         // rows * groups
+    int size;              // columns of a unit
+    int groups;
+    int dtype, residual_dtype, out_dtype;
+    int64_t gate_stride;   // elements between rows of gate
+    float scale, eps;
+    const void* x;
+    const void* gate;      // or NULL
+    const void* residual;  // or NULL: out is the first norm's result
+    const float* weight;
+    const float* next_weight;   // or NULL: no second norm
+    void* residual_out;
+    void* out;
+    float* out_scales;     // e4m3 out: [units]
+    void* x_codes;         // or NULL: nothing is kept
+    float* x_scales;
+    void* gate_codes;
+    float* gate_scales;
+    int units_per_cta;     // set at the launch
+    float inv_size;
+};
+struct BlockNormBwdArgs {
+    int64_t rows;
+    int size, groups;
+    int dtype, residual_dtype;
+    int64_t gate_stride, dgate_stride;
+    float scale, eps;
+    const void* dout;      // NULL: no second norm
+    const void* dres;      // NULL: no residual
+    const void* x;         // of dtype, or codes where it has scales; gate and h so too
+    const float* x_scales;
+    const void* gate;      // or NULL
+    const float* gate_scales;
+    const void* h;
+    const float* h_scales;
+    const float* weight;
+    const float* next_weight;
+    void* dx;
+    void* dgate;
+    void* dres_out;
+    void* out;             // the forward's, or NULL (gate and norm)
+    float* dweight;
+    float* dnext_weight;
+    float* shares;         // [lines * width * weights]
+    int slots, slots_per_cta;   // set at the launch
+    float inv_size;
+};
+
 // Gated linear recurrence (ssd_gate_scan, ssd_gate_scan_bwd): tiles of kScanSegs segments x kScanCh
 // channels.  A segment holds as many tokens as let two tiles' values stay in a thread's registers (one exp(-g)
 // per element forwards, two values backwards) and three or four tiles' operands in shared memory; fewer where
@@ -272,6 +339,7 @@ struct LinearDpreArgs {
     int64_t ldp;
     const void* dy;
     const void* pre;       // or NULL (no activation)
+    const float* pre_scales;   // [m]: pre is e4m3 codes; or NULL
     void* dpre;            // (m, ldp) bf16, or NULL
     float* shares;         // [slabs * n], or NULL
     float* dbias;          // [n], or NULL
@@ -315,6 +383,13 @@ cudaError_t launch_gate_norm(const GateNormArgs& a, cudaStream_t st);
 cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
 int64_t add_norm_bwd_shares(int64_t rows, int width);   // row slots of the backward
 cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
+// dw (and next, from column `width` on) = sums over nshares rows of `columns` shares, in a fixed order
+cudaError_t launch_share_sum(const float* shares, int nshares, int width, int columns, float* dw, float* next, cudaStream_t st);
+cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
+cudaError_t launch_unpack(const PackArgs& a, cudaStream_t st);
+cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t st);
+int64_t block_norm_bwd_lines(int64_t rows, int size, int groups);   // rows that the backward's grid walks at once
+cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, cudaStream_t st);
 size_t gate_scan_workspace(int64_t batch, int64_t seqlen, int width, int dtype);
 cudaError_t launch_gate_scan(const GateScanArgs& a, void* workspace, bool bwd, cudaStream_t st);
 cudaError_t launch_gate_scan_step(const GateStepArgs& a, cudaStream_t st);

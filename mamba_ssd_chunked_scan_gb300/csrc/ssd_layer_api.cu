@@ -1,4 +1,5 @@
-// C ABI of the operators around the scan (residual norm, projection, gated recurrence):
+// C ABI of the operators around the scan (residual norm, projection, gated recurrence, the norms around a block and their
+// 8-bit checkpoints):
 // argument checks and dispatch.  Nothing here allocates device memory; every launch is asynchronous
 // on the caller's stream.
 #include "ssd_common.cuh"
@@ -88,15 +89,26 @@ int check_linear(const ssd_linear_params_t* p) {
     return SSD_OK;
 }
 
+// The same with x in 8-bit rows, which may start at any byte.
+int check_linear_packed(const ssd_linear_params_t* p) {
+    if (!p) return SSD_ERR_INVALID_ARG;
+    if (p->ldx < p->k) return SSD_ERR_INVALID_ARG;
+    if (p->dtype != SSD_BF16 || p->ldx >= (int64_t)1 << 30) return SSD_ERR_UNSUPPORTED;
+    ssd_linear_params_t q = *p;
+    q.ldx = q.k;
+    return check_linear(&q);
+}
+
 // Workspace of the projection's backward, in bytes from its start: the status word, dpre
 // where it is not dy itself, the slabs' shares of dbias, and the parts of whichever product runs.
 struct LinearBwdLayout {
     bool own_dpre;
     int64_t ldp;
-    size_t dpre_off, shares_off, parts_off, total;
+    size_t dpre_off, shares_off, parts_off, rows_off, total;
     LinearPlan dx, dw;
 };
-LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p) {
+// packed: with room for x in bf16.
+LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p, bool packed) {
     LinearBwdLayout l;
     l.own_dpre = p->act != SSD_ACT_NONE || p->n % 8 != 0;
     l.ldp = (p->n + 7) / 8 * 8;
@@ -105,7 +117,12 @@ LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p) {
     l.parts_off = l.shares_off + align_up((size_t)linear_dpre_slabs(p->m, p->n) * p->n * 4, 256);
     l.dx = linear_plan(p->m, p->k, (int64_t)p->n * 2, false);
     l.dw = linear_plan(p->n, p->k, p->m * 2, false);
-    l.total = l.parts_off + (l.dx.parts_bytes > l.dw.parts_bytes ? l.dx.parts_bytes : l.dw.parts_bytes);
+    l.rows_off = l.parts_off + (l.dx.parts_bytes > l.dw.parts_bytes ? l.dx.parts_bytes : l.dw.parts_bytes);
+    l.total = l.rows_off;
+    if (packed) {
+        l.rows_off = align_up(l.rows_off, 256);
+        l.total = l.rows_off + (size_t)p->m * p->k * 2;
+    }
     return l;
 }
 
@@ -182,6 +199,120 @@ int linear_impl(const ssd_linear_params_t* p, const void* x, const void* w, cons
     a.ws = (WsHeader*)workspace;
     a.parts = workspace ? (float*)((char*)workspace + sizeof(WsHeader)) : nullptr;
     return launch_linear(a, plan, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+// x_scales, pre_scales: x, pre are 8-bit rows; packed: the workspace has room for x in bf16.
+int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_scales, const void* w, const void* pre,
+                    const float* pre_scales, const void* dy, void* dx, void* dw, float* dbias, void* workspace,
+                    size_t workspace_bytes, void* stream, bool packed) {
+    const int rc = x_scales ? check_linear_packed(p) : check_linear(p);
+    if (rc != SSD_OK) return rc;
+    if (p->dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (!aligned(dw, 2) || !aligned(dbias, 4) || !aligned(dx, 2)) return SSD_ERR_INVALID_ARG;
+    if (p->m == 0) {
+        if (dw && cudaMemsetAsync(dw, 0, (size_t)p->n * p->k * 2, st) != cudaSuccess) return SSD_ERR_CUDA;
+        if (dbias && cudaMemsetAsync(dbias, 0, (size_t)p->n * 4, st) != cudaSuccess) return SSD_ERR_CUDA;
+        return SSD_OK;
+    }
+    if (!x || !w || !dy || (!dx && !dw && !dbias) || (p->act != SSD_ACT_NONE) != (pre != nullptr)) return SSD_ERR_INVALID_ARG;
+    if ((pre_scales && !pre) || !aligned(x_scales, 4) || !aligned(pre_scales, 4)) return SSD_ERR_INVALID_ARG;
+    if (!aligned(x, x_scales ? 1 : 16) || !aligned(w, 16) || !aligned(dy, 16) || !aligned(pre, pre_scales ? 1 : 2)) return SSD_ERR_INVALID_ARG;
+    const LinearBwdLayout l = linear_bwd_layout(p, packed);
+    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
+    const size_t ex = x_scales ? 1 : 2, ep = pre_scales ? 1 : 2;
+    const Mat in[] = {{x, p->m, p->k, p->ldx, ex}, {w, p->n, p->k, p->k, 2}, {pre, p->m, p->n, p->n, ep}, {dy, p->m, p->n, p->n, 2},
+                      {x_scales, 1, p->m, p->m, 4}, {pre_scales, 1, p->m, p->m, 4}};
+    const Mat out[] = {{dx, p->m, p->k, p->k, 2}, {dw, p->n, p->k, p->k, 2}, {dbias, 1, p->n, p->n, 4},
+                       {workspace, 1, (int64_t)l.total, (int64_t)l.total, 1}};
+    for (int i = 0; i < 4; ++i) {
+        for (const Mat& m : in)
+            if (touch(out[i], m)) return SSD_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (touch(out[i], out[j])) return SSD_ERR_INVALID_ARG;
+    }
+    char* ws = (char*)workspace;
+    // the first product clears the status word
+    if (!dx && !dw && cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return SSD_ERR_CUDA;
+    LinearDpreArgs d = {};
+    d.m = p->m; d.n = p->n; d.act = p->act; d.ldp = l.ldp; d.dy = dy; d.pre = pre; d.pre_scales = pre_scales;
+    d.dpre = l.own_dpre && (dx || dw) ? ws + l.dpre_off : nullptr;
+    d.shares = dbias ? (float*)(ws + l.shares_off) : nullptr;
+    d.dbias = dbias;
+    if ((d.dpre || dbias) && launch_linear_dpre(d, st) != cudaSuccess) return SSD_ERR_CUDA;
+    const LinearOperand g = {l.own_dpre ? (const void*)(ws + l.dpre_off) : dy, l.own_dpre ? l.ldp : p->n, false};
+    LinearArgs a = {};
+    a.dtype = SSD_BF16; a.act = SSD_ACT_NONE;
+    a.ws = (WsHeader*)workspace;
+    a.parts = (float*)(ws + l.parts_off);
+    if (dx) {   // (m, k) = dpre (m, n) w (n, k): w's contraction runs along its rows
+        a.m = p->m; a.n = p->k; a.k = p->n; a.y = dx;
+        a.x = g;
+        a.w = {w, p->k, true};
+        if (launch_linear(a, l.dx, st) != cudaSuccess) return SSD_ERR_CUDA;
+    }
+    if (dw) {   // (n, k) = dpre^T (n, m) x (m, k): both contractions run along the rows
+        a.m = p->n; a.n = p->k; a.k = p->m; a.y = dw;
+        a.x = {g.p, g.ld, true};
+        a.keep_status = dx != nullptr;
+        a.w = {x, p->ldx, true};
+        if (x_scales) {
+            PackArgs u = {};
+            u.units = p->m; u.size = p->k; u.groups = 1; u.dtype = SSD_BF16; u.stride = p->ldx;
+            u.codes = const_cast<void*>(x); u.scales = const_cast<float*>(x_scales); u.out = ws + l.rows_off;
+            if (launch_unpack(u, st) != cudaSuccess) return SSD_ERR_CUDA;
+            a.w = {ws + l.rows_off, p->k, true};
+        }
+        if (launch_linear(a, l.dw, st) != cudaSuccess) return SSD_ERR_CUDA;
+    }
+    return SSD_OK;
+}
+
+// Units of 8-bit rows: rows, each of width / group columns' groups.
+int check_rows(int64_t rows, int32_t width, int32_t group, int32_t dtype, int64_t stride, int32_t most) {
+    if (rows < 0 || width < 1 || group < 1 || width % group != 0 || stride < width) return SSD_ERR_INVALID_ARG;
+    if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
+    const int64_t big = (int64_t)1 << 30;
+    if (group > most || width >= big || stride >= big || rows >= 2 * big / (width / group)) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+int check_gate(const ssd_gate_norm_params_t* p, int64_t dz_stride) {
+    if (!p) return SSD_ERR_INVALID_ARG;
+    if (!(p->eps >= 0.f) || p->eps > 3.0e38f || dz_stride < p->width) return SSD_ERR_INVALID_ARG;
+    if (dz_stride >= (int64_t)1 << 30) return SSD_ERR_UNSUPPORTED;
+    return check_rows(p->rows, p->width, p->group_size, p->dtype, p->z_stride, kBlockNormMaxSize);
+}
+
+// gate, dgate: whether the call has them, and so their strides.
+int check_block(const ssd_block_norm_params_t* p, bool gate, bool dgate) {
+    if (!p) return SSD_ERR_INVALID_ARG;
+    if (!(p->eps >= 0.f) || p->eps > 3.0e38f || !(p->scale >= -3.0e38f && p->scale <= 3.0e38f)) return SSD_ERR_INVALID_ARG;
+    if (p->residual_dtype != SSD_F32 && !(p->residual_dtype == SSD_BF16 && p->dtype == SSD_BF16)) return SSD_ERR_INVALID_ARG;
+    if (p->out_dtype != p->dtype && p->out_dtype != SSD_E4M3) return SSD_ERR_INVALID_ARG;
+    if (dgate && p->dgate_stride < p->width) return SSD_ERR_INVALID_ARG;
+    if (dgate && p->dgate_stride >= (int64_t)1 << 30) return SSD_ERR_UNSUPPORTED;
+    return check_rows(p->rows, p->width, p->width, p->dtype, gate ? p->gate_stride : p->width, kBlockNormMaxSize);
+}
+
+// Whether an output shares an element with an input, or with an output before it.
+template <int I, int O>
+bool mixed(const Mat (&in)[I], const Mat (&out)[O]) {
+    for (int i = 0; i < O; ++i) {
+        for (const Mat& m : in)
+            if (touch(out[i], m)) return true;
+        for (int j = 0; j < i; ++j)
+            if (touch(out[i], out[j])) return true;
+    }
+    return false;
+}
+
+// Whether each matrix starts on an element.
+template <int N>
+bool on_elements(const Mat (&m)[N]) {
+    for (const Mat& x : m)
+        if (!aligned(x.p, x.es)) return false;
+    return true;
 }
 
 }  // namespace
@@ -345,7 +476,12 @@ size_t ssd_linear_workspace_size(const ssd_linear_params_t* p) {
 
 size_t ssd_linear_bwd_workspace_size(const ssd_linear_params_t* p) {
     if (check_linear(p) != SSD_OK || p->dtype != SSD_BF16) return 0;
-    return p->m == 0 ? sizeof(WsHeader) : linear_bwd_layout(p).total;
+    return p->m == 0 ? sizeof(WsHeader) : linear_bwd_layout(p, false).total;
+}
+
+size_t ssd_linear_bwd_packed_workspace_size(const ssd_linear_params_t* p) {
+    if (check_linear_packed(p) != SSD_OK) return 0;
+    return p->m == 0 ? sizeof(WsHeader) : linear_bwd_layout(p, true).total;
 }
 
 int ssd_linear_plan(const ssd_linear_params_t* p, int product, ssd_linear_plan_t* plan) {
@@ -385,57 +521,175 @@ int ssd_linear_fault_inject(const ssd_linear_params_t* p, const void* x, const v
 
 int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const void* w, const void* pre, const void* dy, void* dx,
                    void* dw, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
-    const int rc = check_linear(p);
+    return linear_bwd_impl(p, x, nullptr, w, pre, nullptr, dy, dx, dw, dbias, workspace, workspace_bytes, stream, false);
+}
+
+int ssd_linear_bwd_packed(const ssd_linear_params_t* p, const void* x, const float* x_scales, const void* w, const void* pre,
+                          const float* pre_scales, const void* dy, void* dx, void* dw, float* dbias, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    return linear_bwd_impl(p, x, x_scales, w, pre, pre_scales, dy, dx, dw, dbias, workspace, workspace_bytes, stream, true);
+}
+
+int ssd_pack_rows(int64_t rows, int32_t width, int32_t group_size, int32_t dtype, int64_t x_stride, const void* x, void* codes,
+                  float* scales, void* stream) {
+    const int rc = check_rows(rows, width, group_size, dtype, x_stride, kPackMaxSize);
+    if (rc != SSD_OK || rows == 0) return rc;
+    if (!x || !codes || !scales) return SSD_ERR_INVALID_ARG;
+    const int groups = width / group_size;
+    const Mat in[] = {{x, rows, width, x_stride, elem(dtype)}};
+    const Mat out[] = {{codes, rows, width, width, 1}, {scales, rows, groups, groups, 4}};
+    if (!on_elements(in) || !on_elements(out) || mixed(in, out)) return SSD_ERR_INVALID_ARG;
+    PackArgs a = {};
+    a.units = rows * groups; a.size = group_size; a.groups = groups; a.dtype = dtype; a.stride = x_stride;
+    a.x = x; a.codes = codes; a.scales = scales;
+    return launch_pack(a, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+int ssd_unpack_rows(int64_t rows, int32_t width, int32_t group_size, int32_t dtype, const void* codes, const float* scales,
+                    void* out, void* stream) {
+    const int rc = check_rows(rows, width, group_size, dtype, width, 1 << 30);
+    if (rc != SSD_OK || rows == 0) return rc;
+    if (!codes || !scales || !out) return SSD_ERR_INVALID_ARG;
+    const int groups = width / group_size;
+    const Mat in[] = {{codes, rows, width, width, 1}, {scales, rows, groups, groups, 4}};
+    const Mat to[] = {{out, rows, width, width, elem(dtype)}};
+    if (!on_elements(in) || !on_elements(to) || mixed(in, to)) return SSD_ERR_INVALID_ARG;
+    PackArgs a = {};
+    a.units = rows * groups; a.size = group_size; a.groups = groups; a.dtype = dtype; a.stride = width;
+    a.codes = const_cast<void*>(codes); a.scales = const_cast<float*>(scales); a.out = out;
+    return launch_unpack(a, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+int ssd_gate_norm_pack(const ssd_gate_norm_params_t* p, const void* y, const void* z, const float* weight, void* out, void* y_codes,
+                       float* y_scales, void* z_codes, float* z_scales, void* stream) {
+    const int rc = check_gate(p, p ? p->width : 0);
+    if (rc != SSD_OK || p->rows == 0) return rc;
+    if (!y || !z || !weight || !out || !y_codes || !y_scales || !z_codes || !z_scales) return SSD_ERR_INVALID_ARG;
+    const int64_t r = p->rows, w = p->width, groups = w / p->group_size;
+    const size_t es = elem(p->dtype);
+    const Mat in[] = {{y, r, w, w, es}, {z, r, w, p->z_stride, es}, {weight, 1, w, w, 4}};
+    const Mat to[] = {{out, r, w, w, es}, {y_codes, r, w, w, 1}, {z_codes, r, w, w, 1}, {y_scales, r, groups, groups, 4},
+                      {z_scales, r, groups, groups, 4}};
+    if (!on_elements(in) || !on_elements(to) || mixed(in, to)) return SSD_ERR_INVALID_ARG;
+    BlockNormArgs a = {};
+    a.units = r * groups; a.size = p->group_size; a.groups = (int)groups;
+    a.dtype = a.residual_dtype = a.out_dtype = p->dtype;
+    a.gate_stride = p->z_stride; a.scale = 1.f; a.eps = p->eps;
+    a.x = y; a.gate = z; a.weight = weight; a.out = out;
+    a.x_codes = y_codes; a.x_scales = y_scales; a.gate_codes = z_codes; a.gate_scales = z_scales;
+    return launch_block_norm(a, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+size_t ssd_gate_norm_bwd_workspace_size(const ssd_gate_norm_params_t* p) {
+    if (check_gate(p, p ? p->width : 0) != SSD_OK || p->rows == 0) return 0;
+    return (size_t)block_norm_bwd_lines(p->rows, p->group_size, p->width / p->group_size) * p->width * sizeof(float);
+}
+
+int ssd_gate_norm_bwd(const ssd_gate_norm_params_t* p, const void* dout, const void* y, const float* y_scales, const void* z,
+                      const float* z_scales, const float* weight, void* dy, void* dz, void* out, float* dweight,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_gate(p, p ? p->dz_stride : 0);
     if (rc != SSD_OK) return rc;
-    if (p->dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
+    const int64_t r = p->rows, w = p->width, groups = w / p->group_size;
+    if (z_scales && p->z_stride != w) return SSD_ERR_INVALID_ARG;
+    if (!dweight || !aligned(dweight, 4)) return SSD_ERR_INVALID_ARG;
+    if (r == 0)
+        return cudaMemsetAsync(dweight, 0, (size_t)w * 4, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    if (!dout || !y || !z || !weight || !dy || !dz) return SSD_ERR_INVALID_ARG;
+    const size_t es = elem(p->dtype), need = ssd_gate_norm_bwd_workspace_size(p);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return SSD_ERR_WORKSPACE;
+    const Mat in[] = {{dout, r, w, w, es}, {y, r, w, w, y_scales ? 1 : es}, {z, r, w, p->z_stride, z_scales ? 1 : es},
+                      {y_scales, r, groups, groups, 4}, {z_scales, r, groups, groups, 4}, {weight, 1, w, w, 4}};
+    const Mat to[] = {{dy, r, w, w, es}, {dz, r, w, p->dz_stride, es}, {out, r, w, w, es}, {dweight, 1, w, w, 4},
+                      {workspace, 1, (int64_t)need, (int64_t)need, 1}};
+    if (!on_elements(in) || !on_elements(to) || mixed(in, to)) return SSD_ERR_INVALID_ARG;
+    BlockNormBwdArgs a = {};
+    a.rows = r; a.size = p->group_size; a.groups = (int)groups;
+    a.dtype = a.residual_dtype = p->dtype;
+    a.gate_stride = p->z_stride; a.dgate_stride = p->dz_stride; a.scale = 1.f; a.eps = p->eps;
+    a.dout = dout; a.x = y; a.x_scales = y_scales; a.gate = z; a.gate_scales = z_scales; a.weight = weight;
+    a.dx = dy; a.dgate = dz; a.out = out; a.dweight = dweight; a.shares = (float*)workspace;
+    return launch_block_norm_bwd(a, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+int ssd_block_norm(const ssd_block_norm_params_t* p, const void* x, const void* gate, const void* residual, const float* weight,
+                   const float* next_weight, void* residual_out, void* out, float* out_scales, void* x_codes, float* x_scales,
+                   void* gate_codes, float* gate_scales, void* stream) {
+    const int rc = check_block(p, gate != nullptr, false);
+    if (rc != SSD_OK || p->rows == 0) return rc;
+    const bool codes = p->out_dtype == SSD_E4M3;
+    if (!x || !residual || !weight || !residual_out || (next_weight && (!out || (codes && !out_scales)))) return SSD_ERR_INVALID_ARG;
+    if ((x_codes != nullptr) != (x_scales != nullptr) || (gate_codes != nullptr) != (gate_scales != nullptr) ||
+        (gate_codes != nullptr) != (gate && x_codes))
+        return SSD_ERR_INVALID_ARG;
+    if (!next_weight) out = nullptr;
+    if (!next_weight || !codes) out_scales = nullptr;
+    const int64_t r = p->rows, w = p->width;
+    const size_t es = elem(p->dtype), er = elem(p->residual_dtype);
+    const Mat in[] = {{x, r, w, w, es}, {gate, r, w, p->gate_stride, es}, {weight, 1, w, w, 4}, {next_weight, 1, w, w, 4}};
+    const Mat to[] = {{residual_out, r, w, w, er}, {out, r, w, w, elem(p->out_dtype)}, {out_scales, 1, r, r, 4}, {x_codes, r, w, w, 1},
+                      {x_scales, 1, r, r, 4}, {gate_codes, r, w, w, 1}, {gate_scales, 1, r, r, 4}};
+    const Mat res[] = {{residual, r, w, w, er}};
+    if (!on_elements(in) || !on_elements(to) || !on_elements(res) || mixed(in, to)) return SSD_ERR_INVALID_ARG;
+    for (const Mat& m : to)   // residual_out may be residual itself
+        if (touch(m, res[0]) && m.p != residual) return SSD_ERR_INVALID_ARG;
+    for (int k = 1; k < 7; ++k)
+        if (to[k].p && touch(to[k], res[0])) return SSD_ERR_INVALID_ARG;
+    BlockNormArgs a = {};
+    a.units = r; a.size = p->width; a.groups = 1;
+    a.dtype = p->dtype; a.residual_dtype = p->residual_dtype; a.out_dtype = p->out_dtype;
+    a.gate_stride = p->gate_stride; a.scale = p->scale; a.eps = p->eps;
+    a.x = x; a.gate = gate; a.residual = residual; a.weight = weight; a.next_weight = next_weight;
+    a.residual_out = residual_out; a.out = out; a.out_scales = out_scales;
+    a.x_codes = x_codes; a.x_scales = x_scales; a.gate_codes = gate_codes; a.gate_scales = gate_scales;
+    return launch_block_norm(a, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+size_t ssd_block_norm_bwd_workspace_size(const ssd_block_norm_params_t* p) {
+    if (check_block(p, false, false) != SSD_OK || p->rows == 0) return 0;
+    return (size_t)block_norm_bwd_lines(p->rows, p->width, 1) * p->width * 2 * sizeof(float);
+}
+
+int ssd_block_norm_bwd(const ssd_block_norm_params_t* p, const void* dout, const void* dresidual_out, const void* x,
+                       const float* x_scales, const void* gate, const float* gate_scales, const void* h, const float* h_scales,
+                       const float* weight, const float* next_weight, void* dx, void* dgate, void* dresidual, float* dweight,
+                       float* dnext_weight, void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_block(p, gate || dgate, gate || dgate);
+    if (rc != SSD_OK) return rc;
+    const int64_t r = p->rows, w = p->width;
     cudaStream_t st = (cudaStream_t)stream;
-    if (!aligned(dw, 2) || !aligned(dbias, 4) || !aligned(dx, 2)) return SSD_ERR_INVALID_ARG;
-    if (p->m == 0) {
-        if (dw && cudaMemsetAsync(dw, 0, (size_t)p->n * p->k * 2, st) != cudaSuccess) return SSD_ERR_CUDA;
-        if (dbias && cudaMemsetAsync(dbias, 0, (size_t)p->n * 4, st) != cudaSuccess) return SSD_ERR_CUDA;
+    if (gate_scales && p->gate_stride != w) return SSD_ERR_INVALID_ARG;
+    if (!dweight || !aligned(dweight, 4) || !aligned(dnext_weight, 4) || (next_weight != nullptr) != (dnext_weight != nullptr))
+        return SSD_ERR_INVALID_ARG;
+    if (r == 0) {
+        if (cudaMemsetAsync(dweight, 0, (size_t)w * 4, st) != cudaSuccess) return SSD_ERR_CUDA;
+        if (dnext_weight && cudaMemsetAsync(dnext_weight, 0, (size_t)w * 4, st) != cudaSuccess) return SSD_ERR_CUDA;
         return SSD_OK;
     }
-    if (!x || !w || !dy || (!dx && !dw && !dbias) || (p->act != SSD_ACT_NONE) != (pre != nullptr)) return SSD_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(dy, 16) || !aligned(pre, 2)) return SSD_ERR_INVALID_ARG;
-    const LinearBwdLayout l = linear_bwd_layout(p);
-    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
-    const Mat in[] = {{x, p->m, p->k, p->ldx, 2}, {w, p->n, p->k, p->k, 2}, {pre, p->m, p->n, p->n, 2}, {dy, p->m, p->n, p->n, 2}};
-    const Mat out[] = {{dx, p->m, p->k, p->k, 2}, {dw, p->n, p->k, p->k, 2}, {dbias, 1, p->n, p->n, 4},
-                       {workspace, 1, (int64_t)l.total, (int64_t)l.total, 1}};
-    for (int i = 0; i < 4; ++i) {
-        for (const Mat& m : in)
-            if (touch(out[i], m)) return SSD_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (touch(out[i], out[j])) return SSD_ERR_INVALID_ARG;
+    if (!dresidual_out || !x || !weight || !dx || !dresidual || (gate != nullptr) != (dgate != nullptr) || (gate_scales && !gate) ||
+        (next_weight != nullptr) != (dout != nullptr) || (next_weight && !h))
+        return SSD_ERR_INVALID_ARG;
+    if (!next_weight) {
+        h = nullptr;
+        h_scales = nullptr;
     }
-    char* ws = (char*)workspace;
-    // the first product clears the status word
-    if (!dx && !dw && cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return SSD_ERR_CUDA;
-    LinearDpreArgs d = {};
-    d.m = p->m; d.n = p->n; d.act = p->act; d.ldp = l.ldp; d.dy = dy; d.pre = pre;
-    d.dpre = l.own_dpre && (dx || dw) ? ws + l.dpre_off : nullptr;
-    d.shares = dbias ? (float*)(ws + l.shares_off) : nullptr;
-    d.dbias = dbias;
-    if ((d.dpre || dbias) && launch_linear_dpre(d, st) != cudaSuccess) return SSD_ERR_CUDA;
-    const LinearOperand g = {l.own_dpre ? (const void*)(ws + l.dpre_off) : dy, l.own_dpre ? l.ldp : p->n, false};
-    LinearArgs a = {};
-    a.dtype = SSD_BF16; a.act = SSD_ACT_NONE;
-    a.ws = (WsHeader*)workspace;
-    a.parts = (float*)(ws + l.parts_off);
-    if (dx) {   // (m, k) = dpre (m, n) w (n, k): w's contraction runs along its rows
-        a.m = p->m; a.n = p->k; a.k = p->n; a.y = dx;
-        a.x = g;
-        a.w = {w, p->k, true};
-        if (launch_linear(a, l.dx, st) != cudaSuccess) return SSD_ERR_CUDA;
-    }
-    if (dw) {   // (n, k) = dpre^T (n, m) x (m, k): both contractions run along the rows
-        a.m = p->n; a.n = p->k; a.k = p->m; a.y = dw;
-        a.x = {g.p, g.ld, true};
-        a.keep_status = dx != nullptr;
-        a.w = {x, p->ldx, true};
-        if (launch_linear(a, l.dw, st) != cudaSuccess) return SSD_ERR_CUDA;
-    }
-    return SSD_OK;
+    const size_t es = elem(p->dtype), er = elem(p->residual_dtype), need = ssd_block_norm_bwd_workspace_size(p);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return SSD_ERR_WORKSPACE;
+    const Mat in[] = {{dout, r, w, w, es}, {dresidual_out, r, w, w, er}, {x, r, w, w, x_scales ? 1 : es}, {x_scales, 1, r, r, 4},
+                      {gate, r, w, p->gate_stride, gate_scales ? 1 : es}, {gate_scales, 1, r, r, 4}, {h, r, w, w, h_scales ? 1 : er},
+                      {h_scales, 1, r, r, 4}, {weight, 1, w, w, 4}, {next_weight, 1, w, w, 4}};
+    const Mat to[] = {{dx, r, w, w, es}, {dgate, r, w, p->dgate_stride, es}, {dresidual, r, w, w, er}, {dweight, 1, w, w, 4},
+                      {dnext_weight, 1, w, w, 4}, {workspace, 1, (int64_t)need, (int64_t)need, 1}};
+    if (!on_elements(in) || !on_elements(to) || mixed(in, to)) return SSD_ERR_INVALID_ARG;
+    BlockNormBwdArgs a = {};
+    a.rows = r; a.size = p->width; a.groups = 1;
+    a.dtype = p->dtype; a.residual_dtype = p->residual_dtype;
+    a.gate_stride = p->gate_stride; a.dgate_stride = p->dgate_stride; a.scale = p->scale; a.eps = p->eps;
+    a.dout = dout; a.dres = dresidual_out; a.x = x; a.x_scales = x_scales; a.gate = gate; a.gate_scales = gate_scales;
+    a.h = h; a.h_scales = h_scales; a.weight = weight; a.next_weight = next_weight;
+    a.dx = dx; a.dgate = dgate; a.dres_out = dresidual; a.dweight = dweight; a.dnext_weight = dnext_weight;
+    a.shares = (float*)workspace;
+    return launch_block_norm_bwd(a, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -34,7 +34,7 @@
 
 #include "ssd_common.cuh"
 #include "ssd_kernels.h"
-#include "ssd_vec.cuh"
+#include "ssd_rows.cuh"
 #include "tc_ptx.cuh"
 
 namespace ssd {
@@ -734,7 +734,8 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
 // columns: together (V = 8: rows are whole 16-byte words) or 32 apart (V = 1).  Bound by HBM: four rows' loads are in
 // flight per warp.
 constexpr int kSlabRows = 128, kSlabCols = 256;
-template <int V>
+// P: the type of pre (e4m3: times its row's scale).
+template <typename P, int V>
 __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     __shared__ float part[8][kSlabCols];
     constexpr int C = 8 / V, kRowsAhead = 4;
@@ -746,11 +747,17 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     const int64_t m0 = (int64_t)slab * slab_rows;
     const int rows = a.m - m0 < slab_rows ? (int)(a.m - m0) : (int)slab_rows;
     const bf16_t* dy = static_cast<const bf16_t*>(a.dy) + (size_t)m0 * a.n + n0;
-    const bf16_t* pre = a.pre ? static_cast<const bf16_t*>(a.pre) + (size_t)m0 * a.n + n0 : nullptr;
+    const P* pre = a.pre ? static_cast<const P*>(a.pre) + (size_t)m0 * a.n + n0 : nullptr;
     bf16_t* dp = a.dpre ? static_cast<bf16_t*>(a.dpre) + (size_t)m0 * a.ldp + n0 : nullptr;
     float sum[C][V] = {};
     for (int k0 = w; k0 < rows; k0 += 8 * kRowsAhead) {
-        Raw<bf16_t, V> d[kRowsAhead][C], q[kRowsAhead][C];
+        Raw<bf16_t, V> d[kRowsAhead][C];
+        Raw<P, V> q[kRowsAhead][C];
+        float scale[sizeof(P) == 1 ? kRowsAhead : 1];
+        if constexpr (sizeof(P) == 1) {
+#pragma unroll
+            for (int u = 0; u < kRowsAhead; ++u) scale[u] = k0 + 8 * u < rows ? __ldg(a.pre_scales + m0 + k0 + 8 * u) : 0.f;
+        }
 #pragma unroll
         for (int u = 0; u < kRowsAhead; ++u)
 #pragma unroll
@@ -772,7 +779,13 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
                 float v[V], t[V];
                 d[u][c].get(v);
                 if (pre) {
-                    q[u][c].get(t);
+                    if constexpr (sizeof(P) == 1) {
+                        from_codes(q[u][c], t);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) t[e] *= scale[u];
+                    } else {
+                        q[u][c].get(t);
+                    }
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[e] *= act_slope(t[e], a.act);
                 }
@@ -1009,8 +1022,11 @@ cudaError_t launch_linear_dpre(const LinearDpreArgs& args, cudaStream_t st) {
     a.slab_rows = dpre_slab_rows(a.m, a.n);
     const int64_t slabs = linear_dpre_slabs(a.m, a.n);
     const unsigned grid = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
-    const bool vec = a.n % 8 == 0 && ((uintptr_t)a.pre & 15) == 0;
-    const cudaError_t e = launch_kernel(vec ? ssd_linear_dpre<8> : ssd_linear_dpre<1>, grid, 256, 0, st, true, a);
+    const bool codes = a.pre_scales != nullptr;
+    const bool vec = a.n % 8 == 0 && ((uintptr_t)a.pre & (codes ? 7 : 15)) == 0;
+    const cudaError_t e = launch_kernel(codes ? (vec ? ssd_linear_dpre<e4m3_t, 8> : ssd_linear_dpre<e4m3_t, 1>)
+                                              : (vec ? ssd_linear_dpre<bf16_t, 8> : ssd_linear_dpre<bf16_t, 1>),
+                                        grid, 256, 0, st, true, a);
     if (e != cudaSuccess || !a.dbias) return e;
     return launch_kernel(ssd_linear_dbias, (unsigned)((a.n + 31) / 32), 1024, 0, st, true, (const float*)a.shares, (int)slabs, a.n,
                          a.dbias);

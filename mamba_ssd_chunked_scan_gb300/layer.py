@@ -255,28 +255,57 @@ def linear(x, w, bias=None, residual=None, *, act="none", x_scales=None, w_scale
     return (y, pre) if return_pre else y
 
 
-def linear_bwd(dy, x, w, pre=None, *, act="none", want_dx=True, want_dw=True, want_dbias=False, check_status=False, stream=None):
+def _packed_params(x, w, act, dev):
+    """The parameters of the gradients of a product whose x is 8-bit rows and w bf16."""
+    shape, wshape = x.shape, w.shape
+    if x.dtype is not _E4M3:
+        raise TypeError(f"x: expected float8_e4m3fn with x_scales, got {x.dtype}")
+    if len(shape) < 1 or len(wshape) != 2 or wshape[1] != shape[-1]:
+        raise ValueError(f"expected x (..., k) and w (n, k), got {tuple(shape)} and {tuple(wshape)}")
+    code = _ACT.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {tuple(_ACT)}, got {act!r}")
+    n, k = wshape
+    _need("w", w, _BF16, wshape, dev)
+    ldx = k if x.is_contiguous() else _row_stride("x", x)
+    return shape[:-1], _lib.LinearParams(x.numel() // k if k else 0, ldx, n, k, _lib.SSD_BF16, code)
+
+
+def linear_bwd(dy, x, w, pre=None, *, act="none", x_scales=None, pre_scales=None, want_dx=True, want_dw=True, want_dbias=False,
+               check_status=False, stream=None):
     """Gradients of <dy, y> of one linear call of bf16 operands: dy (..., n) bf16, x and w as given to it, pre
     its second result (with an activation).  Returns a dict: ``dx`` (..., k) bf16, ``dw`` (n, k) bf16 and
-    ``dbias`` (n) fp32, None where not wanted.  (The residual's gradient is dy.)"""
+    ``dbias`` (n) fp32, None where not wanted.  (The residual's gradient is dy.)
+
+    x and pre may each be 8-bit rows (pack_rows', or add_norm's), float8_e4m3fn with x_scales, pre_scales (...) fp32: x stands
+    for x * x_scales rounded to bf16 (which loses nothing of pack_rows' rows); w stays bf16."""
     dev = _device("x", x)
     if stream is not None or _current_device() != dev:
         with _elsewhere(dev, stream):
-            return linear_bwd(dy, x, w, pre, act=act, want_dx=want_dx, want_dw=want_dw, want_dbias=want_dbias, check_status=check_status)
-    lead, p = _linear_params(x, w, act, dev)
+            return linear_bwd(dy, x, w, pre, act=act, x_scales=x_scales, pre_scales=pre_scales, want_dx=want_dx, want_dw=want_dw,
+                              want_dbias=want_dbias, check_status=check_status)
+    lead, p = _linear_params(x, w, act, dev) if x_scales is None else _packed_params(x, w, act, dev)
     device = x.device
-    if x.dtype is not _BF16:
-        raise TypeError(f"x must be bf16, got {x.dtype}")
+    if x_scales is None:
+        if x.dtype is not _BF16:
+            raise TypeError(f"x must be bf16, or float8_e4m3fn with x_scales, got {x.dtype}")
+    else:
+        _need("x_scales", x_scales, _F32, lead, dev)
     out_shape = (*lead, p.n)
     _need("dy", dy, _BF16, out_shape, dev)
     if (pre is None) != (act == "none"):
         raise ValueError("pre: given with an activation, and only then")
     if pre is not None:
-        _need("pre", pre, _BF16, out_shape, dev)
+        _need("pre", pre, _BF16 if pre_scales is None else _E4M3, out_shape, dev)
+    if pre_scales is not None:
+        if pre is None:
+            raise ValueError("pre_scales: only with pre")
+        _need("pre_scales", pre_scales, _F32, lead, dev)
     if not (want_dx or want_dw or want_dbias):
         raise ValueError("no gradient wanted")
     ref = ctypes.byref(p)
-    nbytes = _lib_c.ssd_linear_bwd_workspace_size(ref)
+    packed = x_scales is not None or pre_scales is not None
+    nbytes = (_lib_c.ssd_linear_bwd_packed_workspace_size if packed else _lib_c.ssd_linear_bwd_workspace_size)(ref)
     if nbytes == 0:
         raise _lib.SSDError(2, f"linear_bwd of {tuple(x.shape)} and {tuple(w.shape)}, row stride {p.ldx}")
     dx = _empty((*lead, p.k), dtype=_BF16, device=device) if want_dx else None
@@ -284,8 +313,12 @@ def linear_bwd(dy, x, w, pre=None, *, act="none", want_dx=True, want_dw=True, wa
     db = _empty(p.n, dtype=_F32, device=device) if want_dbias else None
     ws = _empty(nbytes, dtype=torch.uint8, device=device)
     st = _raw_stream(dev)
-    rc = _lib_c.ssd_linear_bwd(ref, x.data_ptr(), w.data_ptr(), _ptr(pre), dy.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db),
-                               ws.data_ptr(), nbytes, st)
+    if packed:
+        rc = _lib_c.ssd_linear_bwd_packed(ref, x.data_ptr(), _ptr(x_scales), w.data_ptr(), _ptr(pre), _ptr(pre_scales), dy.data_ptr(),
+                                          _ptr(dx), _ptr(dw), _ptr(db), ws.data_ptr(), nbytes, st)
+    else:
+        rc = _lib_c.ssd_linear_bwd(ref, x.data_ptr(), w.data_ptr(), _ptr(pre), dy.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db),
+                                   ws.data_ptr(), nbytes, st)
     if rc:
         _check(rc, "ssd_linear_bwd")
     if check_status and p.m:
