@@ -232,7 +232,9 @@ struct BlockNormBwdArgs {
     float* dweight;
     float* dnext_weight;
     float* shares;         // [lines * width * weights]
-    int slots, slots_per_cta;   // set at the launch
+    // set at the launch: the rows' slots, and their shared memory (weights, then stages of operands and scales)
+    int slots, slots_per_cta;
+    int stages, slot_bytes, weight_bytes, stage_bytes, offset[5], scale_offset[5];
     float inv_size;
 };
 
