@@ -17,7 +17,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libssd.so")
 SOURCES = ["ssd_api.cu", "ssd_simt.cu", "ssd_tc.cu", "ssd_agg.cu", "ssd_step.cu", "ssd_bwd.cu", "ssd_bwd_tc.cu", "ssd_gate_norm.cu",
            "ssd_layer_api.cu", "ssd_add_norm.cu", "ssd_gate_scan.cu", "ssd_linear.cu",
-           "ssd_pack.cu", "ssd_block_norm.cu", "ssd_block_norm_bwd.cu"]
+           "ssd_pack.cu", "ssd_block_norm.cu", "ssd_block_norm_bwd.cu",
+           "ssd_block_norm_bwd_f32.cu", "ssd_block_norm_bwd_bf16_f32.cu", "ssd_block_norm_bwd_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -18,7 +18,8 @@ constexpr int kElems = 16;   // elements of a row per thread
 template <typename T, typename R, int V, bool GATE, bool RES>
 __global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
     constexpr int C = kElems / V;
-    __shared__ float4 part[2][16];
+    __shared__ RowPart part[2];
+    __shared__ uint32_t tops[2][32];
     const bool one_warp = a.units_per_cta > 1 || blockDim.x == 32;
     const int slot = one_warp ? threadIdx.x >> 5 : 0;
     const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
         }
     }
     float u[C][V];
-    float ss = 0.f;
+    float ss[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         xr[c].get(u[c]);
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
             for (int k = 0; k < V; ++k) u[c][k] *= g[k] * sigmoid<T>(g[k]);
         }
 #pragma unroll
-        for (int k = 0; k < V; ++k) ss = fmaf(u[c][k], u[c][k], ss);
+        for (int k = 0; k < V; ++k) ss[0] = fmaf(u[c][k], u[c][k], ss[0]);
     }
     if (a.x_codes) {
         RowMaxima m = {0, 0};
@@ -77,9 +78,8 @@ __global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
                 m.a = max(m.a, finite_magnitude(xr[c]));
                 if (GATE) m.b = max(m.b, finite_magnitude(gr[c]));
             }
-            float none = 0.f;
-            row_sum_maxima(none, m, one_warp, part[1]);
-            if (!one_warp) __syncthreads();   // part[1] is written again below
+            m.a = row_maximum(m.a, one_warp, tops[0]);
+            m.b = row_maximum(m.b, one_warp, tops[1]);
         }
         const uint32_t sx = pack_scale_bits(m.a), sg = pack_scale_bits(m.b);
         if (tid == 0) {
@@ -105,11 +105,9 @@ __global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
             }
         }
     } else {
-        RowSums s = {ss, 0.f, 0.f};
-        row_sums<1>(s, one_warp, part[0]);
-        ss = s.a;
+        row_sums(ss, one_warp, part[0]);
     }
-    const float rstd = 1.f / sqrtf(ss * a.inv_size + a.eps);
+    const float rstd = rsqrt_of(ss[0] * a.inv_size + a.eps);
     float hh = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -139,9 +137,9 @@ __global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
     }
     if constexpr (RES) {
         if (!a.next_weight) return;
-        RowSums s = {hh, 0.f, 0.f};
-        row_sums<1>(s, one_warp, part[1]);
-        const float rstd2 = 1.f / sqrtf(s.a * a.inv_size + a.eps);
+        float s[1] = {hh};
+        row_sums(s, one_warp, part[1]);
+        const float rstd2 = rsqrt_of(s[0] * a.inv_size + a.eps);
         const bool codes = a.out_dtype == SSD_E4M3;
         uint32_t top = 0;
 #pragma unroll
@@ -164,9 +162,7 @@ __global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
             }
         }
         if (!codes) return;
-        RowMaxima m = {top, 0};
-        row_sum_maxima(hh, m, one_warp, part[0]);
-        const uint32_t so = pack_scale_bits(m.a);
+        const uint32_t so = pack_scale_bits(row_maximum(top, one_warp, tops[0]));
         if (tid == 0) a.out_scales[unit] = __uint_as_float(so);
 #pragma unroll
         for (int c = 0; c < C; ++c) {

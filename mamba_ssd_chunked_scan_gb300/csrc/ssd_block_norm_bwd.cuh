@@ -1,0 +1,675 @@
+// The kernels of ssd_block_norm_bwd.cu, which has the formulas; its instances are spread over several files so that they compile
+// side by side.
+#pragma once
+#include <atomic>
+
+#include "ssd_kernels.h"
+#include "ssd_rows.cuh"
+
+namespace ssd {
+
+constexpr int kWideElems = 16, kNarrowElems = 8;   // elements of a row per thread
+constexpr int kMaxStages = 4;
+constexpr int kSmemSM = 228 * 1024, kSmemCta = 227 * 1024;
+constexpr int kSmemOwn = 2048;                     // a CTA's static shared memory and what the system takes
+
+// Threads per SM that the registers of E elements a thread allow.
+constexpr int threads_sm(int elems, bool res) { return elems == kNarrowElems || !res ? 640 : 512; }
+
+// Copies of 16, 8 or 4 bytes, of which the first `n` are read and the others 0.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int n) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most the newest `n` groups of copies are under way.
+__device__ __forceinline__ void copies_wait(int n) {
+    if (n == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <bool, typename A, typename B> struct Pick { typedef A type; };
+template <typename A, typename B> struct Pick<false, A, B> { typedef B type; };
+
+// A warp's record of one row: its lanes' vectors of each operand, piece by piece (16 bytes a lane, then codes, then scales), so that
+// whole lines arrive in one place and every offset is a constant (records of a thread each, 112 bytes apart, took the copies from 5.5
+// to 3.6 TB/s).  Offsets here are a lane's bytes before a piece: 32 times that in the record.
+template <typename T, typename R, int E, bool GATE, bool RES, bool XP, bool HP>
+struct Record {
+    static constexpr int kVec = 16 / (int)sizeof(T);
+    static constexpr int t = E * (int)sizeof(T), r = E * (int)sizeof(R);   // bytes of an operand of these types; of codes E
+    static constexpr int dout = 0;
+    static constexpr int dres = dout + t;
+    static constexpr int h = dres + (RES ? r : 0);
+    static constexpr int x = h + (RES && !HP ? r : 0);
+    static constexpr int gate = x + (XP ? 0 : t);
+    static constexpr int codes = gate + (GATE && !XP ? t : 0);
+    static constexpr int x_codes = codes, gate_codes = x_codes + (XP ? E : 0), h_codes = gate_codes + (XP && GATE ? E : 0);
+    static constexpr int x_scale = h_codes + (RES && HP ? E : 0);
+    static constexpr int gate_scale = x_scale + (XP ? 4 : 0), h_scale = gate_scale + (XP && GATE ? 4 : 0);
+    static constexpr int bytes = h_scale + (RES && HP ? 4 : 0);
+    static constexpr int weight = E * 4, weights = (RES ? 2 : 1) * weight;   // the weights' record
+};
+
+// Where a lane's 16-byte half `h` of its vector c of type K lies, or all of it where K is shorter, from an operand's first piece on.
+template <typename K, int V>
+__device__ __forceinline__ int piece(int c, int h, int lane) {
+    constexpr int kBytes = (int)sizeof(K) * V, kHalves = kBytes > 16 ? kBytes / 16 : 1;
+    return (c * kHalves + h) * 32 * (kBytes / kHalves) + lane * (kBytes / kHalves);
+}
+
+// One vector (number c of the lane's) of an operand, whose pieces start at `at`.
+template <typename K, int V>
+__device__ __forceinline__ Raw<K, V> piece_vector(const unsigned char* at, int c, int lane) {
+    Raw<K, V> q;
+    if constexpr (sizeof(K) * V == 32) {
+        q.w.lo = *reinterpret_cast<const uint4*>(at + piece<K, V>(c, 0, lane));
+        q.w.hi = *reinterpret_cast<const uint4*>(at + piece<K, V>(c, 1, lane));
+    } else {
+        q.w = *reinterpret_cast<const typename Raw<K, V>::W*>(at + piece<K, V>(c, 0, lane));
+    }
+    return q;
+}
+// It as pairs: codes times s.
+template <typename K, int V>
+__device__ __forceinline__ void widen(const Raw<K, V>& q, Two s, Two (&v)[V / 2]) {
+    to_pairs(q, v);
+    if constexpr (sizeof(K) == 1) {
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) v[k] = v[k] * s;
+    }
+}
+
+// Ask for `count` elements of a vector of an operand (p: the array, at: the vector's first element) into its pieces.
+template <typename K, int V, bool SHIFTED>
+__device__ __forceinline__ void ask(uint32_t to, int c, int lane, const void* p, int64_t at, int count) {
+    constexpr int kBytes = (int)sizeof(K) * V, kHalves = kBytes > 16 ? kBytes / 16 : 1, kPiece = kBytes / kHalves;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+        const int bytes = SHIFTED ? max(0, min(kPiece, count * (int)sizeof(K) - kPiece * h)) : kPiece;
+        copy_async<kPiece>(to + piece<K, V>(c, h, lane), static_cast<const unsigned char*>(p) + at * (int)sizeof(K) + (bytes ? kPiece * h : 0), bytes);
+    }
+}
+
+// 0 in the elements of a vector that lie outside of a row's columns [0, n); the vector starts at column e.
+template <typename K, int V>
+__device__ __forceinline__ void clear_outside(unsigned char* at, int c, int lane, int e, int n) {
+    constexpr int kBytes = (int)sizeof(K) * V, kEach = kBytes > 16 ? 16 / (int)sizeof(K) : V;   // elements of a piece
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        if (e + k < 0 || e + k >= n)
+            reinterpret_cast<typename Word<(int)sizeof(K)>::type*>(at + piece<K, V>(c, k / kEach, lane))[k % kEach] = 0;
+}
+
+// The elements of a vector from column e of a row that lie in its columns [0, n).
+template <typename K, int V, bool SHIFTED>
+__device__ __forceinline__ void put(K* row, int e, int n, const Two (&v)[V / 2]) {
+    Raw<K, V> q;
+    from_pairs(v, q);
+    if constexpr (SHIFTED) {
+        if (e >= 0 && e + V <= n) q.store(row + e);
+        else q.store_within(row, e, n);
+    } else {
+        if (e < n) q.store(row + e);
+    }
+}
+
+// silu(z) and its slope s + z s (1 - s) = s (1 - silu) + silu.
+template <typename T>
+__device__ __forceinline__ void silu(Two z, Two& value, Two& slope) {
+    const Two s = sigmoid<T>(z);
+    value = z * s;
+    slope = fma(s, fma(value, both(-1.f), both(1.f)), value);
+}
+
+// XP: x (and gate) are codes; HP: h is.  SHIFTED: rows of n elements, n not a multiple of V.  Vectors lie on V-element boundaries of
+// the whole array: a row starts `shift` elements into its first one.  Those at its ends hold a neighbour's elements too,
+// which are read with them (and cleared) and never written.  A slot's rows are a multiple of 8 apart (or it has one): their
+// shift is one number, and a thread's columns stay its own for the weights' gradients.
+template <typename T, typename R, int E, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
+__global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(const __grid_constant__ BlockNormBwdArgs a) {
+    typedef Record<T, R, E, GATE, RES, XP, HP> Rec;
+    typedef typename Pick<XP, e4m3_t, T>::type X;
+    typedef typename Pick<HP, e4m3_t, R>::type H;
+    constexpr int V = Rec::kVec, C = E / V, P = V / 2;
+    // the operands' first pieces
+    constexpr int kD = 32 * Rec::dout, kR = 32 * Rec::dres, kX = 32 * (XP ? Rec::x_codes : Rec::x), kZ = 32 * (XP ? Rec::gate_codes : Rec::gate),
+                  kH = 32 * (HP ? Rec::h_codes : Rec::h);
+    constexpr bool kHold = false;
+    __shared__ RowPart part[2];
+    extern __shared__ __align__(16) unsigned char ring[];
+    const bool one_warp = a.slots_per_cta > 1 || blockDim.x == 32;
+    const int slot = one_warp ? threadIdx.x >> 5 : 0;
+    const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
+    const int nt = one_warp ? 32 : blockDim.x;
+    const int id = blockIdx.x * a.slots_per_cta + slot;
+    pdl_trigger();
+    pdl_wait();
+    if (id >= a.slots) return;   // whole warps of a many-slot CTA, which has no barrier
+    const int n = a.size;
+    const int line = id / a.groups, group = id - line * a.groups, first = group * n;   // the slot's first row, its group's first column
+    const int step = a.slots / a.groups;
+    const bool next = RES && a.dout;
+    const uint32_t unit0 = (uint32_t)line * a.groups + group;
+    const int shift = SHIFTED ? (int)((uint64_t)unit0 * n % V) : 0;
+    const int e0 = tid * V - shift, span = nt * V;   // first column of the thread's vector 0; columns from one vector to the next
+    const int lane = tid & 31, warp = tid >> 5;
+    unsigned char* const wrec = ring + slot * a.slot_bytes + warp * 32 * Rec::weights;
+    unsigned char* const rec0 = ring + slot * a.slot_bytes + nt * Rec::weights + warp * 32 * Rec::bytes;
+    // the weights' record; and zeros for vectors past the row's end, which nothing is copied into
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = e0 + c * span;
+        float w[V] = {}, w2[V] = {};
+        if (e < n) {
+            row_weights<V, SHIFTED>(a.weight + first, e, n, w);
+            if (next) row_weights<V, SHIFTED>(a.next_weight, e, n, w2);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            reinterpret_cast<float*>(wrec + piece<float, V>(c, k / 4, lane))[k % 4] = w[k];
+            if (RES) reinterpret_cast<float*>(wrec + 32 * Rec::weight + piece<float, V>(c, k / 4, lane))[k % 4] = w2[k];
+        }
+        if (e >= n) {
+            for (int s = 0; s < a.stages; ++s) {
+                unsigned char* r = rec0 + s * a.stage_bytes;
+                clear_outside<T, V>(r + kD, c, lane, e, n);
+                clear_outside<X, V>(r + kX, c, lane, e, n);
+                if (GATE) clear_outside<X, V>(r + kZ, c, lane, e, n);
+                if (RES) clear_outside<H, V>(r + kH, c, lane, e, n);
+                if (RES) clear_outside<R, V>(r + kR, c, lane, e, n);
+            }
+        }
+    }
+    auto weight = [&](int c, Two (&w)[P]) { to_pairs(piece_vector<float, V>(wrec, c, lane), w); };
+    auto next_weight = [&](int c, Two (&w)[P]) { to_pairs(piece_vector<float, V>(wrec + 32 * Rec::weight, c, lane), w); };
+    // elements from an array's start to the thread's vector 0, and between the slot's rows; `unit`: the scales' number
+    const int64_t row_elems = (int64_t)step * a.groups * n, gate_elems = (int64_t)step * a.gate_stride;
+    int64_t at_ask = (int64_t)unit0 * n + e0, gate_ask = (int64_t)line * a.gate_stride + first + e0;
+    int64_t at = at_ask - e0, dgate_at = (int64_t)line * a.dgate_stride + first;   // of the row at hand, its first column
+    const uint32_t units = (uint32_t)a.rows * a.groups, unit_step = (uint32_t)step * a.groups;
+    uint32_t unit_ask = unit0;
+    auto ask_row = [&](int stage) {
+        if (unit_ask < units) {
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(rec0) + stage * a.stage_bytes;
+            const bool last = SHIFTED && unit_ask + 1 == units;   // the arrays end with its last column
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (e0 + c * span >= n) continue;
+                const int count = last ? min(V, n - e0 - c * span) : V;
+                const int64_t k = at_ask + c * span;
+                if (!RES || next) ask<T, V, SHIFTED>(to + kD, c, lane, a.dout, k, count);
+                ask<X, V, SHIFTED>(to + kX, c, lane, a.x, k, count);
+                if (GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, a.gate, gate_ask + c * span, count);
+                if (next) ask<H, V, SHIFTED>(to + kH, c, lane, a.h, k, count);
+                if (RES) ask<R, V, SHIFTED>(to + kR, c, lane, a.dres, k, count);
+            }
+            if (XP) copy_async<4>(to + 32 * Rec::x_scale + 4 * lane, a.x_scales + unit_ask, 4);
+            if (XP && GATE) copy_async<4>(to + 32 * Rec::gate_scale + 4 * lane, a.gate_scales + unit_ask, 4);
+            if (HP && next) copy_async<4>(to + 32 * Rec::h_scale + 4 * lane, a.h_scales + unit_ask, 4);
+            unit_ask += unit_step;
+            at_ask += row_elems;
+            if (GATE) gate_ask += gate_elems;
+        }
+        copies_commit();
+    };
+    Two dw[C][P], dn[RES ? C : 1][P];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            dw[c][k] = both(0.f);
+            if (RES) dn[c][k] = both(0.f);
+        }
+    for (int s = 0; s < a.stages - (kHold ? 0 : 1); ++s) ask_row(s);
+    int stage = 0, turn = 0;
+    for (uint32_t unit = unit0; unit < units; unit += unit_step) {
+        unsigned char* const rec = rec0 + stage * a.stage_bytes;
+        if constexpr (!kHold) ask_row(stage > 0 ? stage - 1 : a.stages - 1);   // where the row before lay
+        copies_wait(a.stages - 1);
+        if constexpr (SHIFTED) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int e = e0 + c * span;
+                if (e < n && (e < 0 || e + V > n)) {
+                    if (!RES || next) clear_outside<T, V>(rec + kD, c, lane, e, n);
+                    clear_outside<X, V>(rec + kX, c, lane, e, n);
+                    if (GATE) clear_outside<X, V>(rec + kZ, c, lane, e, n);
+                    if (next) clear_outside<H, V>(rec + kH, c, lane, e, n);
+                    if (RES) clear_outside<R, V>(rec + kR, c, lane, e, n);
+                }
+            }
+        }
+        Two xs = both(0.f), gs = xs, hs = xs;
+        if (XP) xs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::x_scale + 4 * lane));
+        if (XP && GATE) gs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::gate_scale + 4 * lane));
+        if (HP && next) hs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::h_scale + 4 * lane));
+        // the row into registers, and its record to a row to come; where registers are short, from its record as often as it is read
+        Raw<T, V> dq[kHold ? C : 1];
+        Raw<X, V> xq[kHold ? C : 1], zq[kHold && GATE ? C : 1];
+        Raw<H, V> hq[kHold && RES ? C : 1];
+        Raw<R, V> rq[kHold && RES ? C : 1];
+        if constexpr (kHold) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (!RES || next) dq[c] = piece_vector<T, V>(rec + kD, c, lane);
+                xq[c] = piece_vector<X, V>(rec + kX, c, lane);
+                if (GATE) zq[c] = piece_vector<X, V>(rec + kZ, c, lane);
+                if (next) hq[c] = piece_vector<H, V>(rec + kH, c, lane);
+                if (RES) rq[c] = piece_vector<R, V>(rec + kR, c, lane);
+            }
+            ask_row(stage);
+        }
+        auto dout_of = [&](int c, Two (&v)[P]) {
+            if constexpr (kHold) widen(dq[c], xs, v);
+            else widen(piece_vector<T, V>(rec + kD, c, lane), xs, v);
+        };
+        auto x_of = [&](int c, Two (&v)[P]) {
+            if constexpr (kHold) widen(xq[c], xs, v);
+            else widen(piece_vector<X, V>(rec + kX, c, lane), xs, v);
+        };
+        auto gate_of = [&](int c, Two (&v)[P]) {
+            if constexpr (kHold) widen(zq[c], gs, v);
+            else widen(piece_vector<X, V>(rec + kZ, c, lane), gs, v);
+        };
+        auto h_of = [&](int c, Two (&v)[P]) {
+            if constexpr (kHold) widen(hq[c], hs, v);
+            else widen(piece_vector<H, V>(rec + kH, c, lane), hs, v);
+        };
+        auto dres_of = [&](int c, Two (&v)[P]) {
+            if constexpr (kHold) widen(rq[c], xs, v);
+            else widen(piece_vector<R, V>(rec + kR, c, lane), xs, v);
+        };
+        if (++stage == a.stages) stage = 0;
+        // What is kept beside it: the gate's sigmoid, and the gradient of u rstd1 weight (with a residual).
+        Two sg[GATE ? C : 1][P], g1[RES ? C : 1][P];
+        Two r2 = both(0.f), k2 = r2;
+        if constexpr (RES) {
+            if (next) {
+                Two hh = both(0.f), ph = hh;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    Two h[P], d[P], w[P];
+                    h_of(c, h);
+                    dout_of(c, d);
+                    next_weight(c, w);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        hh = fma(h[k], h[k], hh);
+                        ph = fma(d[k] * w[k], h[k], ph);
+                    }
+                }
+                float s[2] = {low(hh) + high(hh), low(ph) + high(ph)};
+                row_sums(s, one_warp, part[turn]);
+                turn ^= 1;
+                const float rstd2 = rsqrt_of(s[0] * a.inv_size + a.eps);
+                r2 = both(rstd2);
+                k2 = both(-(s[1] * rstd2 * rstd2 * a.inv_size) * rstd2);   // h times it: -rstd2 hh mean(p2 hh)
+            }
+        }
+        Two uu = both(0.f), pu = uu;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            Two x[P], w[P], g[P];
+            if constexpr (RES) {
+                dres_of(c, g);
+                if (next) {
+                    Two h[P], d[P];
+                    h_of(c, h);
+                    dout_of(c, d);
+                    next_weight(c, w);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        g[k] = fma(d[k], w[k] * r2, fma(h[k], k2, g[k]));
+                        dn[c][k] = fma(d[k], h[k] * r2, dn[c][k]);
+                    }
+                }
+                put<R, V, SHIFTED>(static_cast<R*>(a.dres_out) + at, e0 + c * span, n, g);
+#pragma unroll
+                for (int k = 0; k < P; ++k) g1[c][k] = g[k] = both(a.scale) * g[k];
+            } else {
+                dout_of(c, g);
+            }
+            x_of(c, x);
+            weight(c, w);
+            if constexpr (GATE) {
+                Two z[P];
+                gate_of(c, z);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    sg[c][k] = sigmoid<T>(z[k]);
+                    x[k] = x[k] * (z[k] * sg[c][k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                uu = fma(x[k], x[k], uu);
+                pu = fma(g[k] * w[k], x[k], pu);
+            }
+        }
+        float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
+        row_sums(s, one_warp, part[turn]);
+        turn ^= 1;
+        const float rstd = rsqrt_of(s[0] * a.inv_size + a.eps);
+        const Two r1 = both(rstd), k1 = both(-(s[1] * a.inv_size * rstd * rstd) * rstd);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            Two w[P], g[P], x[P], z[P], du[P], o[P];
+            weight(c, w);
+            x_of(c, x);
+            if constexpr (!RES) dout_of(c, g);
+            if constexpr (GATE) {
+                gate_of(c, z);
+#pragma unroll
+                for (int k = 0; k < P; ++k) z[k] = z[k] * sg[c][k];   // silu
+            }
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                if constexpr (RES) g[k] = g1[c][k];
+                const Two u = GATE ? x[k] * z[k] : x[k];
+                o[k] = u * r1;
+                du[k] = fma(g[k] * w[k], r1, u * k1);
+                dw[c][k] = fma(g[k], o[k], dw[c][k]);
+            }
+            if (!RES && a.out) {
+#pragma unroll
+                for (int k = 0; k < P; ++k) o[k] = o[k] * w[k];
+                put<T, V, SHIFTED>(static_cast<T*>(a.out) + at, e0 + c * span, n, o);
+            }
+            if constexpr (GATE) {
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    // silu's slope: s + gate s (1 - s) = s (1 - silu) + silu
+                    o[k] = du[k] * x[k] * fma(sg[c][k], fma(z[k], both(-1.f), both(1.f)), z[k]);
+                    du[k] = du[k] * z[k];
+                }
+                put<T, V, SHIFTED>(static_cast<T*>(a.dgate) + dgate_at, e0 + c * span, n, o);
+            }
+            put<T, V, SHIFTED>(static_cast<T*>(a.dx) + at, e0 + c * span, n, du);
+        }
+        at += row_elems;
+        if (GATE) dgate_at += (int64_t)step * a.dgate_stride;
+    }
+    const int width = n * a.groups, columns = RES && a.next_weight ? 2 * width : width;
+    float* share = a.shares + (int64_t)line * columns + first;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = e0 + c * span;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if (e + k < 0 || e + k >= n) continue;
+            share[e + k] = k % 2 ? high(dw[c][k / 2]) : low(dw[c][k / 2]);
+            if (RES && a.next_weight) share[width + e + k] = k % 2 ? high(dn[c][k / 2]) : low(dn[c][k / 2]);
+        }
+    }
+}
+
+// Two elements of a row, columns e and e + nt (0 past its end), straight from memory, whatever their alignment: of type K, or codes.
+template <typename K>
+__device__ __forceinline__ Two load_loose(const void* p, bool packed, float scale, int64_t at, int e, int nt, int n) {
+    float f[1], g[1] = {0.f};
+    const bool second = e + nt < n;
+    if (packed) {
+        Raw<e4m3_t, 1> q;
+        q.load(static_cast<const e4m3_t*>(p) + at + e);
+        from_codes(q, f);
+        if (second) {
+            q.load(static_cast<const e4m3_t*>(p) + at + e + nt);
+            from_codes(q, g);
+        }
+        return two(f[0] * scale, g[0] * scale);
+    }
+    Raw<K, 1> q;
+    q.load(static_cast<const K*>(p) + at + e);
+    q.get(f);
+    if (second) {
+        q.load(static_cast<const K*>(p) + at + e + nt);
+        q.get(g);
+    }
+    return two(f[0], g[0]);
+}
+template <typename K>
+__device__ __forceinline__ void put_loose(K* row, int e, int nt, int n, Two v) {
+    Raw<K, 1> q;
+    const float f[1] = {low(v)}, g[1] = {high(v)};
+    q.set(f);
+    q.store(row + e);
+    q.set(g);
+    if (e + nt < n) q.store(row + e + nt);
+}
+
+// The same for rows and operands that no vectors fit: pairs of single elements, read again from the caches by each pass.
+template <typename T, typename R, bool GATE, bool RES>
+__global__ void __launch_bounds__(512) ssd_block_norm_bwd_loose(const __grid_constant__ BlockNormBwdArgs a) {
+    constexpr int C = kWideElems / 2;
+    __shared__ RowPart part[2];
+    const bool one_warp = a.slots_per_cta > 1 || blockDim.x == 32;
+    const int slot = one_warp ? threadIdx.x >> 5 : 0;
+    const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
+    const int nt = one_warp ? 32 : blockDim.x;
+    const int id = blockIdx.x * a.slots_per_cta + slot;
+    pdl_trigger();
+    pdl_wait();
+    if (id >= a.slots) return;   // whole warps of a many-slot CTA, which has no barrier
+    const int n = a.size;
+    const int line = id / a.groups, group = id - line * a.groups, first = group * n;
+    const int step = a.slots / a.groups;
+    const bool next = RES && a.dout;
+    Two dw[C], dn[RES ? C : 1];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        dw[c] = both(0.f);
+        if (RES) dn[c] = both(0.f);
+    }
+    auto weights = [&](const float* p, int e) { return two(__ldg(p + e), e + nt < n ? __ldg(p + e + nt) : 0.f); };
+    int turn = 0;
+    for (uint32_t row = line; row < (uint32_t)a.rows; row += step) {
+        const uint32_t unit = row * a.groups + group;
+        const int64_t at = (int64_t)unit * n, gate_at = (int64_t)row * a.gate_stride + first;
+        const float xs = a.x_scales ? __ldg(a.x_scales + unit) : 1.f;
+        const float gs = GATE && a.gate_scales ? __ldg(a.gate_scales + unit) : 1.f;
+        const float hs = next && a.h_scales ? __ldg(a.h_scales + unit) : 1.f;
+        auto x_at = [&](int e) { return load_loose<T>(a.x, a.x_scales, xs, at, e, nt, n); };
+        auto dout_at = [&](int e) { return load_loose<T>(a.dout, false, 1.f, at, e, nt, n); };
+        auto h_at = [&](int e) { return load_loose<R>(a.h, a.h_scales, hs, at, e, nt, n); };
+        Two si[GATE ? C : 1], sl[GATE ? C : 1], g1[RES ? C : 1];
+        Two r2 = both(0.f), k2 = r2;
+        if constexpr (RES) {
+            if (next) {
+                Two hh = both(0.f), ph = hh;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int e = tid + 2 * c * nt;
+                    if (e >= n) continue;
+                    const Two h = h_at(e), d = dout_at(e);
+                    hh = fma(h, h, hh);
+                    ph = fma(d * weights(a.next_weight, e), h, ph);
+                }
+                float s[2] = {low(hh) + high(hh), low(ph) + high(ph)};
+                row_sums(s, one_warp, part[turn]);
+                turn ^= 1;
+                const float rstd2 = rsqrt_of(s[0] * a.inv_size + a.eps);
+                r2 = both(rstd2);
+                k2 = both(-(s[1] * rstd2 * rstd2 * a.inv_size) * rstd2);
+            }
+        }
+        Two uu = both(0.f), pu = uu;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = tid + 2 * c * nt;
+            if (e >= n) continue;
+            Two g;
+            if constexpr (RES) {
+                g = load_loose<R>(a.dres, false, 1.f, at, e, nt, n);
+                if (next) {
+                    const Two h = h_at(e), d = dout_at(e);
+                    g = fma(d, weights(a.next_weight, e) * r2, fma(h, k2, g));
+                    dn[c] = fma(d, h * r2, dn[c]);
+                }
+                put_loose(static_cast<R*>(a.dres_out) + at, e, nt, n, g);
+                g1[c] = g = both(a.scale) * g;
+            } else {
+                g = dout_at(e);
+            }
+            Two u = x_at(e);
+            if constexpr (GATE) {
+                silu<T>(load_loose<T>(a.gate, a.gate_scales, gs, gate_at, e, nt, n), si[c], sl[c]);
+                u = u * si[c];
+            }
+            uu = fma(u, u, uu);
+            pu = fma(g * weights(a.weight + first, e), u, pu);
+        }
+        float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
+        row_sums(s, one_warp, part[turn]);
+        turn ^= 1;
+        const float rstd = rsqrt_of(s[0] * a.inv_size + a.eps);
+        const Two r1 = both(rstd), k1 = both(-(s[1] * a.inv_size * rstd * rstd) * rstd);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = tid + 2 * c * nt;
+            if (e >= n) continue;
+            Two g;
+            if constexpr (RES) g = g1[c];
+            else g = dout_at(e);
+            const Two x = x_at(e), w = weights(a.weight + first, e), u = GATE ? x * si[c] : x, o = u * r1;
+            Two du = fma(g * w, r1, u * k1);
+            dw[c] = fma(g, o, dw[c]);
+            if (!RES && a.out) put_loose(static_cast<T*>(a.out) + at, e, nt, n, o * w);
+            if constexpr (GATE) {
+                put_loose(static_cast<T*>(a.dgate) + (int64_t)row * a.dgate_stride + first, e, nt, n, du * (x * sl[c]));
+                du = du * si[c];
+            }
+            put_loose(static_cast<T*>(a.dx) + at, e, nt, n, du);
+        }
+    }
+    const int width = n * a.groups, columns = RES && a.next_weight ? 2 * width : width;
+    float* share = a.shares + (int64_t)line * columns + first;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = tid + (2 * c + k) * nt;
+            if (e >= n) continue;
+            share[e] = k ? high(dw[c]) : low(dw[c]);
+            if (RES && a.next_weight) share[width + e] = k ? high(dn[c]) : low(dn[c]);
+        }
+}
+
+// How a call's rows are spread: threads of a CTA, its slots, and all slots (a number of rows at a time, each of its groups).
+struct RowPlan {
+    int threads, slots_per_cta, slots, grid;
+};
+
+inline int slot_threads(int span, int elems) { return ((span + elems - 1) / elems + 31) / 32 * 32; }
+
+inline RowPlan row_plan(int64_t rows, int span, int groups, int elems, int per_sm) {
+    RowPlan p;
+    p.threads = slot_threads(span, elems);
+    const int cta_slots = p.threads == 32 ? 4 : 1;
+    int64_t lines = (int64_t)kAddNormSMs * per_sm * cta_slots / groups / 8 * 8;
+    if (lines < 8) lines = 8;
+    if (lines > rows) lines = rows;
+    p.slots = (int)lines * groups;
+    p.slots_per_cta = p.slots < cta_slots ? p.slots : cta_slots;
+    p.threads *= p.slots_per_cta;
+    p.grid = (p.slots + p.slots_per_cta - 1) / p.slots_per_cta;
+    return p;
+}
+
+// CTAs that an SM's registers hold.
+inline int ctas_sm(int span, int elems, bool res) {
+    const int threads = slot_threads(span, elems) == 32 ? 128 : slot_threads(span, elems);
+    return threads_sm(elems, res) / threads > 0 ? threads_sm(elems, res) / threads : 1;
+}
+
+// Columns that the vectors of a row span: rows of other than whole vectors may reach into one more.
+inline int vector_span(int size) { return size % 8 == 0 ? size : size + 7; }
+
+// Elements per thread where vectors are taken: 8 while that makes at most 160 threads.
+inline int vector_elems(int span) { return span <= 160 * kNarrowElems ? kNarrowElems : kWideElems; }
+
+template <typename T, typename R, int E, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
+cudaError_t launch_ring(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
+    typedef Record<T, R, E, GATE, RES, XP, HP> Rec;
+    auto kern = ssd_block_norm_bwd_kernel<T, R, E, SHIFTED, GATE, RES, XP, HP>;
+    static std::atomic<uint8_t> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCta - kSmemOwn)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+            return e;
+        ready[dev].store(1, std::memory_order_release);
+    }
+    const int span = SHIFTED ? vector_span(a.size) : a.size;
+    const int nt = slot_threads(span, E), cta_slots = nt == 32 ? 4 : 1;
+    a.stage_bytes = nt * Rec::bytes;
+    int per_sm = ctas_sm(span, E, RES);
+    for (;; --per_sm) {
+        const int room = (kSmemSM / per_sm < kSmemCta + 1024 ? kSmemSM / per_sm : kSmemCta + 1024) - 1024 - kSmemOwn;
+        a.stages = (room / cta_slots - nt * Rec::weights) / a.stage_bytes;
+        if (a.stages >= 2 || per_sm == 1) break;
+    }
+    if (a.stages < 1) return cudaErrorNotSupported;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    a.slot_bytes = nt * Rec::weights + a.stages * a.stage_bytes;
+    const RowPlan p = row_plan(a.rows, span, a.groups, E, per_sm);
+    a.slots = p.slots;
+    a.slots_per_cta = p.slots_per_cta;
+    *lines = p.slots / a.groups;
+    return launch_kernel(kern, (unsigned)p.grid, (unsigned)p.threads, (size_t)a.slot_bytes * p.slots_per_cta, st, true, a);
+}
+
+template <typename T, typename R, bool GATE, bool RES, bool XP, bool HP>
+cudaError_t launch_vectors(BlockNormBwdArgs& a, bool shifted, int* lines, cudaStream_t st) {
+    if (vector_elems(vector_span(a.size)) == kNarrowElems)
+        return shifted ? launch_ring<T, R, kNarrowElems, true, GATE, RES, XP, HP>(a, lines, st)
+                       : launch_ring<T, R, kNarrowElems, false, GATE, RES, XP, HP>(a, lines, st);
+    return shifted ? launch_ring<T, R, kWideElems, true, GATE, RES, XP, HP>(a, lines, st)
+                   : launch_ring<T, R, kWideElems, false, GATE, RES, XP, HP>(a, lines, st);
+}
+
+// The main launch; *lines: rows of shares that it leaves.  Vectors where every array starts on 16 bytes (codes on a vector's), rows hold
+// one at least, x and gate are both codes or neither is, and an SM's shared memory holds a row's records.
+template <typename T, typename R, bool GATE, bool RES>
+cudaError_t launch_block_norm_bwd_typed(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    auto fits = [](const void* p, bool packed) { return ((uintptr_t)p & (packed ? V - 1 : 15)) == 0; };
+    const bool shifted = a.size % V != 0;
+    const int width = a.size * a.groups;
+    const bool xp = a.x_scales, hp = RES && a.dout && a.h_scales;
+    const bool vectors = a.size >= V && vector_span(a.size) <= 512 * kWideElems && fits(a.x, xp) && fits(a.h, hp) && fits(a.dout, false) &&
+                         fits(a.dres, false) && fits(a.dres_out, false) && fits(a.dx, false) && fits(a.out, false) &&
+                         (shifted || (fits(a.weight, false) && fits(a.next_weight, false))) &&
+                         (!GATE || (xp == (a.gate_scales != nullptr) && fits(a.gate, xp) && fits(a.dgate, false) &&
+                                    (shifted ? a.gate_stride == width && a.dgate_stride == width
+                                             : a.gate_stride % V == 0 && a.dgate_stride % V == 0)));
+    cudaError_t e = cudaErrorNotSupported;
+    if (vectors && hp) {
+        if constexpr (RES)
+            e = xp ? launch_vectors<T, R, GATE, RES, true, true>(a, shifted, lines, st)
+                   : launch_vectors<T, R, GATE, RES, false, true>(a, shifted, lines, st);
+    } else if (vectors) {
+        e = xp ? launch_vectors<T, R, GATE, RES, true, false>(a, shifted, lines, st)
+               : launch_vectors<T, R, GATE, RES, false, false>(a, shifted, lines, st);
+    }
+    if (e != cudaErrorNotSupported) return e;   // not even one row's records fit an SM: fp32 rows of all operands beyond 7488 columns
+    const RowPlan p = row_plan(a.rows, a.size, a.groups, kWideElems, ctas_sm(a.size, kWideElems, true));
+    a.slots = p.slots;
+    a.slots_per_cta = p.slots_per_cta;
+    *lines = p.slots / a.groups;
+    return launch_kernel(ssd_block_norm_bwd_loose<T, R, GATE, RES>, (unsigned)p.grid, (unsigned)p.threads, 0, st, true, a);
+}
+
+// One per file: the gate and norm after the scan; the norm after a block by types, without and with a gate.
+cudaError_t launch_gate_norm_bwd_typed(BlockNormBwdArgs& a, int* lines, cudaStream_t st);
+cudaError_t launch_block_norm_bwd_f32(BlockNormBwdArgs& a, int* lines, cudaStream_t st);
+cudaError_t launch_block_norm_bwd_bf16_f32(BlockNormBwdArgs& a, int* lines, cudaStream_t st);
+cudaError_t launch_block_norm_bwd_bf16(BlockNormBwdArgs& a, int* lines, cudaStream_t st);
+
+}  // namespace ssd

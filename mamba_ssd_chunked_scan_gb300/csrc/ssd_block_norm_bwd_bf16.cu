@@ -1,0 +1,11 @@
+// Instances of the norm after a block's gradient (ssd_block_norm_bwd.cu), by the types of x and of the residual.
+#include "ssd_block_norm_bwd.cuh"
+
+namespace ssd {
+
+cudaError_t launch_block_norm_bwd_bf16(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
+    return a.gate ? launch_block_norm_bwd_typed<bf16_t, bf16_t, true, true>(a, lines, st)
+                  : launch_block_norm_bwd_typed<bf16_t, bf16_t, false, true>(a, lines, st);
+}
+
+}  // namespace ssd

@@ -15,7 +15,7 @@ constexpr int kElems = 16;   // elements of a unit per thread
 template <typename T, int V>
 __global__ void __launch_bounds__(1024) ssd_pack_kernel(PackArgs a) {
     constexpr int C = kElems / V;
-    __shared__ float4 part[2][32];
+    __shared__ uint32_t part[2][32];
     const bool one_warp = a.units_per_cta > 1 || blockDim.x == 32;
     const int slot = one_warp ? threadIdx.x >> 5 : 0;
     const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(1024) ssd_pack_kernel(PackArgs a) {
     const T* x = static_cast<const T*>(a.x) + row * a.stride + (unit - row * a.groups) * n;
     e4m3_t* out = static_cast<e4m3_t*>(a.codes) + unit * n;
     Raw<T, V> r[C];
-    RowMaxima m = {0, 0};
+    uint32_t m = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int e = (tid + c * nt) * V;
@@ -36,17 +36,16 @@ __global__ void __launch_bounds__(1024) ssd_pack_kernel(PackArgs a) {
         if (e < n) r[c].load(x + e);
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) m.a = max(m.a, magnitude(r[c]));
-    float none = 0.f;
-    row_sum_maxima(none, m, one_warp, part[0]);
-    const bool bad = m.a >= kInfBits;   // the same in all of the unit's threads
+    for (int c = 0; c < C; ++c) m = max(m, magnitude(r[c]));
+    m = row_maximum(m, one_warp, part[0]);
+    const bool bad = m >= kInfBits;   // the same in all of the unit's threads
     if (bad) {
-        m.a = 0;
+        m = 0;
 #pragma unroll
-        for (int c = 0; c < C; ++c) m.a = max(m.a, finite_magnitude(r[c]));
-        row_sum_maxima(none, m, one_warp, part[1]);
+        for (int c = 0; c < C; ++c) m = max(m, finite_magnitude(r[c]));
+        m = row_maximum(m, one_warp, part[1]);
     }
-    const uint32_t scale = pack_scale_bits(m.a);
+    const uint32_t scale = pack_scale_bits(m);
     const float inv = pack_inverse(scale);
     if (tid == 0) a.scales[unit] = __uint_as_float(scale);
 #pragma unroll

@@ -81,46 +81,160 @@ __device__ __forceinline__ void from_codes(const Raw<e4m3_t, V>& r, float (&v)[V
     }
 }
 
-// Sums and maxima over the threads of a row: a warp, or the CTA (every thread of it calls; `part` has an entry per warp, and each
-// warp combines them for itself, in one order).  Calls in a row alternate between two arrays: whoever writes one again is past
-// a barrier that its readers reached after reading.
-struct RowSums {
-    float a, b, c;
+// Two fp32 numbers in a register pair: one instruction does both (fma.rn.f32x2 and the like), and what these kernels run
+// out of first is issue slots.
+struct Two {
+    uint64_t w;
 };
-__device__ __forceinline__ float warp_sum(float v) {
+__device__ __forceinline__ Two two(float lo, float hi) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.w) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ Two both(float v) { return two(v, v); }
+__device__ __forceinline__ float low(Two a) { return __uint_as_float((uint32_t)a.w); }
+__device__ __forceinline__ float high(Two a) { return __uint_as_float((uint32_t)(a.w >> 32)); }
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
+    return r;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.w) : "l"(a.w), "l"(b.w), "l"(c.w));
+    return r;
+}
+
+// V elements as pairs, and back.
+template <typename T, int V>
+__device__ __forceinline__ void to_pairs(const Raw<T, V>& r, Two (&v)[V / 2]) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r.w);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int k = 0; k < V / 2; ++k) v[k] = two(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+    } else {
+        float f[V];
+        if constexpr (sizeof(T) == 1) from_codes(r, f);
+        else r.get(f);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) v[k] = two(f[2 * k], f[2 * k + 1]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void from_pairs(const Two (&v)[V / 2], Raw<T, V>& r) {
+    float f[V];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+        f[2 * k] = low(v[k]);
+        f[2 * k + 1] = high(v[k]);
+    }
+    r.set(f);
+}
+
+// 1 / sqrt(x) by the special-function unit (relative error below 2^-22); 0 gives infinity.
+__device__ __forceinline__ float rsqrt_of(float x) {
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// One or two sums over the threads of a row: a warp, or the CTA of up to 20 warps (every thread of it calls, and adds the warps'
+// sums for itself, in one order).  Two sums share their shuffles: at the first a lane passes on the one that it does not
+// keep.  Calls in a row alternate between two arrays: whoever writes one again is past a barrier that its readers reached
+// after reading.
+struct RowPart {
+    __align__(16) float sums[40];
+    uint2 maxima[20];
+};
+// A warp's sums (of two, the second in lanes 16 to 31), and the CTA's from the warps'.
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&s)[N]) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    float v = s[0];
+    if constexpr (N == 2) {
+        const bool up = threadIdx.x & 16;
+        v = (up ? s[1] : s[0]) + __shfl_xor_sync(kAll, up ? s[0] : s[1], 16);
+    }
+#pragma unroll
+    for (int o = N == 2 ? 8 : 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
 template <int N>
-__device__ __forceinline__ void row_sums(RowSums& s, bool one_warp, float4* part) {
-    s.a = warp_sum(s.a);
-    if (N > 1) s.b = warp_sum(s.b);
-    if (N > 2) s.c = warp_sum(s.c);
-    if (one_warp) return;
+__device__ __forceinline__ void leave_sums(float v, RowPart& part) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) part[threadIdx.x >> 5] = make_float4(s.a, s.b, s.c, 0.f);
-    __syncthreads();
-    const float4 q = lane < (int)(blockDim.x >> 5) ? part[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-    s.a = warp_sum(q.x);
-    if (N > 1) s.b = warp_sum(q.y);
-    if (N > 2) s.c = warp_sum(q.z);
+    if (lane % (32 / N) == 0) part.sums[(threadIdx.x >> 5) * N + (N == 2 ? lane >> 4 : 0)] = v;
 }
+template <int N>
+__device__ __forceinline__ void join_sums(float (&s)[N], const RowPart& part) {
+    const int count = (blockDim.x >> 5) * N;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    int k = 0;
+#pragma unroll 4
+    for (; k + 4 <= count; k += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(part.sums + k);
+        t.x += q.x;
+        t.y += q.y;
+        t.z += q.z;
+        t.w += q.w;
+    }
+    if (k < count) {   // what is left
+        t.x += part.sums[k];
+        if (k + 1 < count) t.y += part.sums[k + 1];
+        if (k + 2 < count) t.z += part.sums[k + 2];
+    }
+    if constexpr (N == 1) {
+        s[0] = (t.x + t.y) + (t.z + t.w);
+    } else {
+        s[0] = t.x + t.z;
+        s[1] = t.y + t.w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], bool one_warp, RowPart& part) {
+    static_assert(N == 1 || N == 2, "");
+    const float v = warp_sums(s);
+    if (one_warp) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] = N == 1 ? v : __shfl_sync(0xffffffffu, v, 16 * k);
+        return;
+    }
+    leave_sums<N>(v, part);
+    __syncthreads();
+    join_sums(s, part);
+}
+
+// A sum (the same as row_sums') and two maxima, by one barrier.
 struct RowMaxima {
     uint32_t a, b;
 };
-__device__ __forceinline__ void row_sum_maxima(float& s, RowMaxima& m, bool one_warp, float4* part) {
-    s = warp_sum(s);
+__device__ __forceinline__ void row_sum_maxima(float (&s)[1], RowMaxima& m, bool one_warp, RowPart& part) {
+    const float v = warp_sums(s);
     m.a = __reduce_max_sync(0xffffffffu, m.a);
     m.b = __reduce_max_sync(0xffffffffu, m.b);
+    s[0] = v;
     if (one_warp) return;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) part[threadIdx.x >> 5] = make_float4(s, __uint_as_float(m.a), __uint_as_float(m.b), 0.f);
+    leave_sums<1>(v, part);
+    if (lane == 0) part.maxima[threadIdx.x >> 5] = make_uint2(m.a, m.b);
     __syncthreads();
-    const float4 q = lane < (int)(blockDim.x >> 5) ? part[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-    s = warp_sum(q.x);
-    m.a = __reduce_max_sync(0xffffffffu, __float_as_uint(q.y));
-    m.b = __reduce_max_sync(0xffffffffu, __float_as_uint(q.z));
+    join_sums(s, part);
+    const uint2 q = lane < (int)(blockDim.x >> 5) ? part.maxima[lane] : make_uint2(0, 0);
+    m.a = __reduce_max_sync(0xffffffffu, q.x);
+    m.b = __reduce_max_sync(0xffffffffu, q.y);
+}
+// A maximum over the threads of a row of up to 32 warps.
+__device__ __forceinline__ uint32_t row_maximum(uint32_t m, bool one_warp, uint32_t (&part)[32]) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (one_warp) return m;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
 }
 
 // 1 / (1 + e^-z).  bf16 inputs: ex2.approx and rcp.approx, a few 2^-23 each, far inside the inputs' rounding; fp32 inputs:
@@ -134,6 +248,22 @@ __device__ __forceinline__ float sigmoid(float z) {
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-z * kLog2e));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
         return r;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Two sigmoid(Two z) {
+    if constexpr (sizeof(T) == 4) {
+        return two(sigmoid<T>(low(z)), sigmoid<T>(high(z)));
+    } else {
+        const Two t = z * both(-kLog2e);
+        float e, f;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(low(t)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(high(t)));
+        const Two q = two(e, f) + both(1.f);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(low(q)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(high(q)));
+        return two(e, f);
     }
 }
 
