@@ -19,11 +19,11 @@ namespace ssd {
 
 // Enough for every shape: which one a call takes depends on its addresses and types too.
 int64_t block_norm_bwd_lines(int64_t rows, int size, int groups) {
-    int most = row_plan(rows, size, groups, kWideElems, ctas_sm(size, kWideElems, true)).slots;
+    int most = loose_plan(rows, size, groups).slots;
     for (int span : {size, vector_span(size)}) {
-        const int elems = vector_elems(vector_span(size));
-        const int slots = row_plan(rows, span, groups, elems, ctas_sm(span, elems, false)).slots;
-        if (slots > most) most = slots;
+        RowPlan p = vector_plan(span);
+        spread(p, rows, groups, ctas_sm(p.threads, threads_sm(p.elems, false)));
+        if (p.slots > most) most = p.slots;
     }
     return most / groups;
 }

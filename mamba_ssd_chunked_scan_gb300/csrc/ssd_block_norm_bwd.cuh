@@ -16,6 +16,8 @@ constexpr int kSmemOwn = 2048;                     // a CTA's static shared memo
 // Threads per SM that the registers of E elements a thread allow.
 constexpr int threads_sm(int elems, bool res) { return elems == kNarrowElems || !res ? 640 : 512; }
 
+constexpr int loose_threads_sm(int elems) { return elems == kNarrowElems ? 640 : 512; }   // where no vectors fit
+
 // Copies of 16, 8 or 4 bytes, of which the first `n` are read and the others 0.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int n) {
@@ -83,14 +85,14 @@ __device__ __forceinline__ void widen(const Raw<K, V>& q, Two s, Two (&v)[V / 2]
     }
 }
 
-// Ask for `count` elements of a vector of an operand (p: the array, at: the vector's first element) into its pieces.
+// Ask for `count` elements of a vector of an operand, `off` bytes from p, into its pieces.
 template <typename K, int V, bool SHIFTED>
-__device__ __forceinline__ void ask(uint32_t to, int c, int lane, const void* p, int64_t at, int count) {
+__device__ __forceinline__ void ask(uint32_t to, int c, int lane, const unsigned char* p, uint32_t off, int count) {
     constexpr int kBytes = (int)sizeof(K) * V, kHalves = kBytes > 16 ? kBytes / 16 : 1, kPiece = kBytes / kHalves;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
         const int bytes = SHIFTED ? max(0, min(kPiece, count * (int)sizeof(K) - kPiece * h)) : kPiece;
-        copy_async<kPiece>(to + piece<K, V>(c, h, lane), static_cast<const unsigned char*>(p) + at * (int)sizeof(K) + (bytes ? kPiece * h : 0), bytes);
+        copy_async<kPiece>(to + piece<K, V>(c, h, lane), p + off + (SHIFTED && bytes == 0 ? 0 : kPiece * h), bytes);
     }
 }
 
@@ -104,16 +106,17 @@ __device__ __forceinline__ void clear_outside(unsigned char* at, int c, int lane
             reinterpret_cast<typename Word<(int)sizeof(K)>::type*>(at + piece<K, V>(c, k / kEach, lane))[k % kEach] = 0;
 }
 
-// The elements of a vector from column e of a row that lie in its columns [0, n).
+// The elements of a vector that lie in a row's columns [0, n): it starts at column e, and at byte `off` from `row`.
 template <typename K, int V, bool SHIFTED>
-__device__ __forceinline__ void put(K* row, int e, int n, const Two (&v)[V / 2]) {
+__device__ __forceinline__ void put(unsigned char* row, uint32_t off, int e, int n, const Two (&v)[V / 2]) {
     Raw<K, V> q;
     from_pairs(v, q);
+    K* p = reinterpret_cast<K*>(row + off);
     if constexpr (SHIFTED) {
-        if (e >= 0 && e + V <= n) q.store(row + e);
-        else q.store_within(row, e, n);
+        if (e >= 0 && e + V <= n) q.store(p);
+        else q.store_within(p - e, e, n);
     } else {
-        if (e < n) q.store(row + e);
+        if (e < n) q.store(p);
     }
 }
 
@@ -125,40 +128,41 @@ __device__ __forceinline__ void silu(Two z, Two& value, Two& slope) {
     slope = fma(s, fma(value, both(-1.f), both(1.f)), value);
 }
 
-// XP: x (and gate) are codes; HP: h is.  SHIFTED: rows of n elements, n not a multiple of V.  Vectors lie on V-element boundaries of
-// the whole array: a row starts `shift` elements into its first one.  Those at its ends hold a neighbour's elements too,
-// which are read with them (and cleared) and never written.  A slot's rows are a multiple of 8 apart (or it has one): their
-// shift is one number, and a thread's columns stay its own for the weights' gradients.
-template <typename T, typename R, int E, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
+// LANES: lanes of a warp that take a row (a slot); 0: a CTA does, and where its rows lie is the same number for all of its
+// threads (uniform registers hold it).  XP: x (and gate) are codes; HP: h is.
+//
+// SHIFTED: rows of n elements, n not a multiple of V.  Vectors lie on V-element boundaries of the whole array: a row starts `shift`
+// elements into its first one.  Those at its ends hold a neighbour's elements too, which are read with them (and cleared)
+// and never written.  A slot's rows are a multiple of 8 apart (or it has one): their shift is one number, and a thread's
+// columns stay its own for the weights' gradients.
+template <typename T, typename R, int E, int LANES, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
 __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(const __grid_constant__ BlockNormBwdArgs a) {
     typedef Record<T, R, E, GATE, RES, XP, HP> Rec;
     typedef typename Pick<XP, e4m3_t, T>::type X;
     typedef typename Pick<HP, e4m3_t, R>::type H;
+    constexpr bool kCta = LANES == 0, kKeep = RES;   // kKeep: silu and its slope stay in registers from one pass to the next
     constexpr int V = Rec::kVec, C = E / V, P = V / 2;
     // the operands' first pieces
     constexpr int kD = 32 * Rec::dout, kR = 32 * Rec::dres, kX = 32 * (XP ? Rec::x_codes : Rec::x), kZ = 32 * (XP ? Rec::gate_codes : Rec::gate),
-                  kH = 32 * (HP ? Rec::h_codes : Rec::h);
-    constexpr bool kHold = false;
+                  kH = 32 * (HP ? Rec::h_codes : Rec::h), kStage = 32 * Rec::bytes;
     __shared__ RowPart part[2];
     extern __shared__ __align__(16) unsigned char ring[];
-    const bool one_warp = a.slots_per_cta > 1 || blockDim.x == 32;
-    const int slot = one_warp ? threadIdx.x >> 5 : 0;
-    const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
-    const int nt = one_warp ? 32 : blockDim.x;
-    const int id = blockIdx.x * a.slots_per_cta + slot;
+    const int tid = kCta ? threadIdx.x : threadIdx.x % (kCta ? 32 : LANES), nt = kCta ? blockDim.x : LANES;
+    const int id = kCta ? blockIdx.x : blockIdx.x * a.slots_per_cta + threadIdx.x / (kCta ? 32 : LANES);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
     pdl_wait();
-    if (id >= a.slots) return;   // whole warps of a many-slot CTA, which has no barrier
+    if (!kCta && id >= a.slots) return;
     const int n = a.size;
     const int line = id / a.groups, group = id - line * a.groups, first = group * n;   // the slot's first row, its group's first column
     const int step = a.slots / a.groups;
     const bool next = RES && a.dout;
-    const uint32_t unit0 = (uint32_t)line * a.groups + group;
+    const uint32_t units = (uint32_t)a.rows * a.groups, unit_step = (uint32_t)step * a.groups, unit0 = (uint32_t)line * a.groups + group;
     const int shift = SHIFTED ? (int)((uint64_t)unit0 * n % V) : 0;
     const int e0 = tid * V - shift, span = nt * V;   // first column of the thread's vector 0; columns from one vector to the next
-    const int lane = tid & 31, warp = tid >> 5;
-    unsigned char* const wrec = ring + slot * a.slot_bytes + warp * 32 * Rec::weights;
-    unsigned char* const rec0 = ring + slot * a.slot_bytes + nt * Rec::weights + warp * 32 * Rec::bytes;
+    // a warp's shared memory: its lanes' weights, then the stages
+    unsigned char* const wrec = ring + warp * (32 * Rec::weights + a.stages * kStage);
+    unsigned char* const rec0 = wrec + 32 * Rec::weights;
     // the weights' record; and zeros for vectors past the row's end, which nothing is copied into
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         }
         if (e >= n) {
             for (int s = 0; s < a.stages; ++s) {
-                unsigned char* r = rec0 + s * a.stage_bytes;
+                unsigned char* r = rec0 + s * kStage;
                 clear_outside<T, V>(r + kD, c, lane, e, n);
                 clear_outside<X, V>(r + kX, c, lane, e, n);
                 if (GATE) clear_outside<X, V>(r + kZ, c, lane, e, n);
@@ -186,35 +190,48 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     }
     auto weight = [&](int c, Two (&w)[P]) { to_pairs(piece_vector<float, V>(wrec, c, lane), w); };
     auto next_weight = [&](int c, Two (&w)[P]) { to_pairs(piece_vector<float, V>(wrec + 32 * Rec::weight, c, lane), w); };
-    // elements from an array's start to the thread's vector 0, and between the slot's rows; `unit`: the scales' number
-    const int64_t row_elems = (int64_t)step * a.groups * n, gate_elems = (int64_t)step * a.gate_stride;
-    int64_t at_ask = (int64_t)unit0 * n + e0, gate_ask = (int64_t)line * a.gate_stride + first + e0;
-    int64_t at = at_ask - e0, dgate_at = (int64_t)line * a.dgate_stride + first;   // of the row at hand, its first column
-    const uint32_t units = (uint32_t)a.rows * a.groups, unit_step = (uint32_t)step * a.groups;
+    // Where vector 0 of thread 0 lies in each operand of the next row to ask for, in each result of the row at hand, and how far it
+    // is from one of the slot's rows to the next (in elements).
+    const int64_t at0 = (int64_t)unit0 * n - shift, gate0 = (int64_t)line * a.gate_stride + first - shift;
+    const int64_t far = (int64_t)unit_step * n, gate_far = (int64_t)step * a.gate_stride;
+    auto in = [](const void* p, int64_t elems, int size) { return static_cast<const unsigned char*>(p) + elems * size; };
+    const unsigned char *p_dout = in(a.dout, at0, sizeof(T)), *p_x = in(a.x, at0, sizeof(X)), *p_gate = in(a.gate, gate0, sizeof(X)),
+                        *p_h = in(a.h, at0, sizeof(H)), *p_dres = in(a.dres, at0, sizeof(R));
+    auto out = [](void* p, int64_t elems, int size) { return static_cast<unsigned char*>(p) + elems * size; };
+    unsigned char *q_dx = out(a.dx, at0, sizeof(T)), *q_dres = out(a.dres_out, at0, sizeof(R)), *q_out = out(a.out, at0, sizeof(T)),
+                  *q_dgate = out(a.dgate, (int64_t)line * a.dgate_stride + first - shift, sizeof(T));
     uint32_t unit_ask = unit0;
     auto ask_row = [&](int stage) {
         if (unit_ask < units) {
-            const uint32_t to = (uint32_t)__cvta_generic_to_shared(rec0) + stage * a.stage_bytes;
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(rec0) + stage * kStage;
             const bool last = SHIFTED && unit_ask + 1 == units;   // the arrays end with its last column
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 if (e0 + c * span >= n) continue;
                 const int count = last ? min(V, n - e0 - c * span) : V;
-                const int64_t k = at_ask + c * span;
-                if (!RES || next) ask<T, V, SHIFTED>(to + kD, c, lane, a.dout, k, count);
-                ask<X, V, SHIFTED>(to + kX, c, lane, a.x, k, count);
-                if (GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, a.gate, gate_ask + c * span, count);
-                if (next) ask<H, V, SHIFTED>(to + kH, c, lane, a.h, k, count);
-                if (RES) ask<R, V, SHIFTED>(to + kR, c, lane, a.dres, k, count);
+                const uint32_t t = (uint32_t)tid * V;
+                const int64_t s = c * span;
+                if (!RES || next) ask<T, V, SHIFTED>(to + kD, c, lane, p_dout + s * sizeof(T), t * sizeof(T), count);
+                ask<X, V, SHIFTED>(to + kX, c, lane, p_x + s * sizeof(X), t * sizeof(X), count);
+                if (GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, p_gate + s * sizeof(X), t * sizeof(X), count);
+                if (next) ask<H, V, SHIFTED>(to + kH, c, lane, p_h + s * sizeof(H), t * sizeof(H), count);
+                if (RES) ask<R, V, SHIFTED>(to + kR, c, lane, p_dres + s * sizeof(R), t * sizeof(R), count);
             }
             if (XP) copy_async<4>(to + 32 * Rec::x_scale + 4 * lane, a.x_scales + unit_ask, 4);
             if (XP && GATE) copy_async<4>(to + 32 * Rec::gate_scale + 4 * lane, a.gate_scales + unit_ask, 4);
             if (HP && next) copy_async<4>(to + 32 * Rec::h_scale + 4 * lane, a.h_scales + unit_ask, 4);
             unit_ask += unit_step;
-            at_ask += row_elems;
-            if (GATE) gate_ask += gate_elems;
+            if (!RES || next) p_dout += far * sizeof(T);
+            p_x += far * sizeof(X);
+            if (GATE) p_gate += gate_far * sizeof(X);
+            if (next) p_h += far * sizeof(H);
+            if (RES) p_dres += far * sizeof(R);
         }
         copies_commit();
+    };
+    auto sums = [&](float (&s)[2], int turn) {
+        if constexpr (kCta) row_sums(s, false, part[turn]);
+        else lane_sums<LANES>(s);
     };
     Two dw[C][P], dn[RES ? C : 1][P];
 #pragma unroll
@@ -224,11 +241,12 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             dw[c][k] = both(0.f);
             if (RES) dn[c][k] = both(0.f);
         }
-    for (int s = 0; s < a.stages - (kHold ? 0 : 1); ++s) ask_row(s);
+    for (int s = 0; s < a.stages - 1; ++s) ask_row(s);
     int stage = 0, turn = 0;
     for (uint32_t unit = unit0; unit < units; unit += unit_step) {
-        unsigned char* const rec = rec0 + stage * a.stage_bytes;
-        if constexpr (!kHold) ask_row(stage > 0 ? stage - 1 : a.stages - 1);   // where the row before lay
+        unsigned char* const rec = rec0 + stage * kStage;
+        ask_row(stage > 0 ? stage - 1 : a.stages - 1);   // where the row before lay
+        if (++stage == a.stages) stage = 0;
         copies_wait(a.stages - 1);
         if constexpr (SHIFTED) {
 #pragma unroll
@@ -247,45 +265,13 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         if (XP) xs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::x_scale + 4 * lane));
         if (XP && GATE) gs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::gate_scale + 4 * lane));
         if (HP && next) hs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::h_scale + 4 * lane));
-        // the row into registers, and its record to a row to come; where registers are short, from its record as often as it is read
-        Raw<T, V> dq[kHold ? C : 1];
-        Raw<X, V> xq[kHold ? C : 1], zq[kHold && GATE ? C : 1];
-        Raw<H, V> hq[kHold && RES ? C : 1];
-        Raw<R, V> rq[kHold && RES ? C : 1];
-        if constexpr (kHold) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                if (!RES || next) dq[c] = piece_vector<T, V>(rec + kD, c, lane);
-                xq[c] = piece_vector<X, V>(rec + kX, c, lane);
-                if (GATE) zq[c] = piece_vector<X, V>(rec + kZ, c, lane);
-                if (next) hq[c] = piece_vector<H, V>(rec + kH, c, lane);
-                if (RES) rq[c] = piece_vector<R, V>(rec + kR, c, lane);
-            }
-            ask_row(stage);
-        }
-        auto dout_of = [&](int c, Two (&v)[P]) {
-            if constexpr (kHold) widen(dq[c], xs, v);
-            else widen(piece_vector<T, V>(rec + kD, c, lane), xs, v);
-        };
-        auto x_of = [&](int c, Two (&v)[P]) {
-            if constexpr (kHold) widen(xq[c], xs, v);
-            else widen(piece_vector<X, V>(rec + kX, c, lane), xs, v);
-        };
-        auto gate_of = [&](int c, Two (&v)[P]) {
-            if constexpr (kHold) widen(zq[c], gs, v);
-            else widen(piece_vector<X, V>(rec + kZ, c, lane), gs, v);
-        };
-        auto h_of = [&](int c, Two (&v)[P]) {
-            if constexpr (kHold) widen(hq[c], hs, v);
-            else widen(piece_vector<H, V>(rec + kH, c, lane), hs, v);
-        };
-        auto dres_of = [&](int c, Two (&v)[P]) {
-            if constexpr (kHold) widen(rq[c], xs, v);
-            else widen(piece_vector<R, V>(rec + kR, c, lane), xs, v);
-        };
-        if (++stage == a.stages) stage = 0;
-        // What is kept beside it: the gate's sigmoid, and the gradient of u rstd1 weight (with a residual).
-        Two sg[GATE ? C : 1][P], g1[RES ? C : 1][P];
+        auto dout_of = [&](int c, Two (&v)[P]) { widen(piece_vector<T, V>(rec + kD, c, lane), xs, v); };
+        auto x_of = [&](int c, Two (&v)[P]) { widen(piece_vector<X, V>(rec + kX, c, lane), xs, v); };
+        auto gate_of = [&](int c, Two (&v)[P]) { widen(piece_vector<X, V>(rec + kZ, c, lane), gs, v); };
+        auto h_of = [&](int c, Two (&v)[P]) { widen(piece_vector<H, V>(rec + kH, c, lane), hs, v); };
+        const uint32_t t = (uint32_t)tid * V;
+        // What is kept of a row beside its record: the gate's sigmoid (or silu and its slope), and the gradient of u rstd1 weight.
+        Two sg[GATE ? C : 1][P], sl[GATE && kKeep ? C : 1][P], g1[RES ? C : 1][P];
         Two r2 = both(0.f), k2 = r2;
         if constexpr (RES) {
             if (next) {
@@ -303,7 +289,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                     }
                 }
                 float s[2] = {low(hh) + high(hh), low(ph) + high(ph)};
-                row_sums(s, one_warp, part[turn]);
+                sums(s, turn);
                 turn ^= 1;
                 const float rstd2 = rsqrt_of(s[0] * a.inv_size + a.eps);
                 r2 = both(rstd2);
@@ -315,7 +301,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         for (int c = 0; c < C; ++c) {
             Two x[P], w[P], g[P];
             if constexpr (RES) {
-                dres_of(c, g);
+                to_pairs(piece_vector<R, V>(rec + kR, c, lane), g);
                 if (next) {
                     Two h[P], d[P];
                     h_of(c, h);
@@ -327,7 +313,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                         dn[c][k] = fma(d[k], h[k] * r2, dn[c][k]);
                     }
                 }
-                put<R, V, SHIFTED>(static_cast<R*>(a.dres_out) + at, e0 + c * span, n, g);
+                put<R, V, SHIFTED>(q_dres + c * span * (int64_t)sizeof(R), t * sizeof(R), e0 + c * span, n, g);
 #pragma unroll
                 for (int k = 0; k < P; ++k) g1[c][k] = g[k] = both(a.scale) * g[k];
             } else {
@@ -340,8 +326,13 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                 gate_of(c, z);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    sg[c][k] = sigmoid<T>(z[k]);
-                    x[k] = x[k] * (z[k] * sg[c][k]);
+                    if constexpr (kKeep) {
+                        silu<T>(z[k], sg[c][k], sl[c][k]);
+                        x[k] = x[k] * sg[c][k];
+                    } else {
+                        sg[c][k] = sigmoid<T>(z[k]);
+                        x[k] = x[k] * (z[k] * sg[c][k]);
+                    }
                 }
             }
 #pragma unroll
@@ -351,23 +342,21 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             }
         }
         float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
-        row_sums(s, one_warp, part[turn]);
+        sums(s, turn);
         turn ^= 1;
         const float rstd = rsqrt_of(s[0] * a.inv_size + a.eps);
         const Two r1 = both(rstd), k1 = both(-(s[1] * a.inv_size * rstd * rstd) * rstd);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             Two w[P], g[P], x[P], z[P], du[P], o[P];
+            const int e = e0 + c * span;
             weight(c, w);
             x_of(c, x);
             if constexpr (!RES) dout_of(c, g);
-            if constexpr (GATE) {
-                gate_of(c, z);
-#pragma unroll
-                for (int k = 0; k < P; ++k) z[k] = z[k] * sg[c][k];   // silu
-            }
+            if constexpr (GATE && !kKeep) gate_of(c, z);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
+                if constexpr (GATE) z[k] = kKeep ? sg[c][k] : z[k] * sg[c][k];   // silu
                 if constexpr (RES) g[k] = g1[c][k];
                 const Two u = GATE ? x[k] * z[k] : x[k];
                 o[k] = u * r1;
@@ -377,21 +366,24 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             if (!RES && a.out) {
 #pragma unroll
                 for (int k = 0; k < P; ++k) o[k] = o[k] * w[k];
-                put<T, V, SHIFTED>(static_cast<T*>(a.out) + at, e0 + c * span, n, o);
+                put<T, V, SHIFTED>(q_out + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, o);
             }
             if constexpr (GATE) {
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
                     // silu's slope: s + gate s (1 - s) = s (1 - silu) + silu
-                    o[k] = du[k] * x[k] * fma(sg[c][k], fma(z[k], both(-1.f), both(1.f)), z[k]);
+                    const Two slope = kKeep ? sl[c][k] : fma(sg[c][k], fma(z[k], both(-1.f), both(1.f)), z[k]);
+                    o[k] = du[k] * (x[k] * slope);
                     du[k] = du[k] * z[k];
                 }
-                put<T, V, SHIFTED>(static_cast<T*>(a.dgate) + dgate_at, e0 + c * span, n, o);
+                put<T, V, SHIFTED>(q_dgate + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, o);
             }
-            put<T, V, SHIFTED>(static_cast<T*>(a.dx) + at, e0 + c * span, n, du);
+            put<T, V, SHIFTED>(q_dx + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, du);
         }
-        at += row_elems;
-        if (GATE) dgate_at += (int64_t)step * a.dgate_stride;
+        q_dx += far * sizeof(T);
+        if (GATE) q_dgate += (int64_t)step * a.dgate_stride * (int64_t)sizeof(T);
+        if (RES) q_dres += far * sizeof(R);
+        if (!RES) q_out += far * sizeof(T);
     }
     const int width = n * a.groups, columns = RES && a.next_weight ? 2 * width : width;
     float* share = a.shares + (int64_t)line * columns + first;
@@ -407,44 +399,69 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     }
 }
 
-// Two elements of a row, columns e and e + nt (0 past its end), straight from memory, whatever their alignment: of type K, or codes.
-template <typename K>
-__device__ __forceinline__ Two load_loose(const void* p, bool packed, float scale, int64_t at, int e, int nt, int n) {
-    float f[1], g[1] = {0.f};
-    const bool second = e + nt < n;
-    if (packed) {
-        Raw<e4m3_t, 1> q;
-        q.load(static_cast<const e4m3_t*>(p) + at + e);
-        from_codes(q, f);
-        if (second) {
-            q.load(static_cast<const e4m3_t*>(p) + at + e + nt);
-            from_codes(q, g);
+// A thread's elements of a row for operands that no vectors fit: columns tid, tid + nt, ..., as they lie in memory.
+template <typename K, int E>
+struct Loose {
+    Raw<K, 1> q[E];
+    __device__ __forceinline__ void load(const void* p, int64_t at, int tid, int nt, int n) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            q[k].zero();
+            if (tid + k * nt < n) q[k].load(static_cast<const K*>(p) + at + tid + k * nt);
         }
-        return two(f[0] * scale, g[0] * scale);
     }
-    Raw<K, 1> q;
-    q.load(static_cast<const K*>(p) + at + e);
-    q.get(f);
-    if (second) {
-        q.load(static_cast<const K*>(p) + at + e + nt);
-        q.get(g);
+    __device__ __forceinline__ Two get(int c) const {
+        float f[1], g[1];
+        if constexpr (sizeof(K) == 1) {
+            from_codes(q[2 * c], f);
+            from_codes(q[2 * c + 1], g);
+        } else {
+            q[2 * c].get(f);
+            q[2 * c + 1].get(g);
+        }
+        return two(f[0], g[0]);
     }
-    return two(f[0], g[0]);
-}
+};
+// Of type K, or codes times the row's scale (these are one byte of each element's 16 or 32 bits).
+template <typename K, int E>
+struct Either {
+    Loose<K, E> plain;
+    __device__ __forceinline__ void load(const void* p, bool packed, int64_t at, int tid, int nt, int n) {
+        if (packed) {
+            Loose<e4m3_t, E> codes;
+            codes.load(p, at, tid, nt, n);
+#pragma unroll
+            for (int k = 0; k < E; ++k) plain.q[k].w = codes.q[k].w;
+        } else {
+            plain.load(p, at, tid, nt, n);
+        }
+    }
+    __device__ __forceinline__ Two get(bool packed, Two scale, int c) const {
+        if (!packed) return plain.get(c);
+        float f[1], g[1];
+        Raw<e4m3_t, 1> q;
+        q.w = (uint8_t)plain.q[2 * c].w;
+        from_codes(q, f);
+        q.w = (uint8_t)plain.q[2 * c + 1].w;
+        from_codes(q, g);
+        return two(f[0], g[0]) * scale;
+    }
+};
 template <typename K>
-__device__ __forceinline__ void put_loose(K* row, int e, int nt, int n, Two v) {
+__device__ __forceinline__ void put_loose(K* row, int c, int tid, int nt, int n, Two v) {
     Raw<K, 1> q;
     const float f[1] = {low(v)}, g[1] = {high(v)};
+    const int e = tid + 2 * c * nt;
     q.set(f);
-    q.store(row + e);
+    if (e < n) q.store(row + e);
     q.set(g);
     if (e + nt < n) q.store(row + e + nt);
 }
 
-// The same for rows and operands that no vectors fit: pairs of single elements, read again from the caches by each pass.
-template <typename T, typename R, bool GATE, bool RES>
-__global__ void __launch_bounds__(512) ssd_block_norm_bwd_loose(const __grid_constant__ BlockNormBwdArgs a) {
-    constexpr int C = kWideElems / 2;
+// The same for rows and operands that no vectors fit: single elements, all of a row's asked for before the first is used.
+template <typename T, typename R, int E, bool GATE, bool RES>
+__global__ void __launch_bounds__(loose_threads_sm(E)) ssd_block_norm_bwd_loose(const __grid_constant__ BlockNormBwdArgs a) {
+    constexpr int C = E / 2;
     __shared__ RowPart part[2];
     const bool one_warp = a.slots_per_cta > 1 || blockDim.x == 32;
     const int slot = one_warp ? threadIdx.x >> 5 : 0;
@@ -464,29 +481,36 @@ __global__ void __launch_bounds__(512) ssd_block_norm_bwd_loose(const __grid_con
         dw[c] = both(0.f);
         if (RES) dn[c] = both(0.f);
     }
-    auto weights = [&](const float* p, int e) { return two(__ldg(p + e), e + nt < n ? __ldg(p + e + nt) : 0.f); };
+    auto weights = [&](const float* p, int c) {
+        const int e = tid + 2 * c * nt;
+        return two(e < n ? __ldg(p + e) : 0.f, e + nt < n ? __ldg(p + e + nt) : 0.f);
+    };
     int turn = 0;
     for (uint32_t row = line; row < (uint32_t)a.rows; row += step) {
         const uint32_t unit = row * a.groups + group;
-        const int64_t at = (int64_t)unit * n, gate_at = (int64_t)row * a.gate_stride + first;
-        const float xs = a.x_scales ? __ldg(a.x_scales + unit) : 1.f;
-        const float gs = GATE && a.gate_scales ? __ldg(a.gate_scales + unit) : 1.f;
-        const float hs = next && a.h_scales ? __ldg(a.h_scales + unit) : 1.f;
-        auto x_at = [&](int e) { return load_loose<T>(a.x, a.x_scales, xs, at, e, nt, n); };
-        auto dout_at = [&](int e) { return load_loose<T>(a.dout, false, 1.f, at, e, nt, n); };
-        auto h_at = [&](int e) { return load_loose<R>(a.h, a.h_scales, hs, at, e, nt, n); };
-        Two si[GATE ? C : 1], sl[GATE ? C : 1], g1[RES ? C : 1];
+        const int64_t at = (int64_t)unit * n;
+        Loose<T, E> dq;
+        Either<T, E> xq, zq;
+        Either<R, E> hq;
+        Loose<R, E> rq;
+        xq.load(a.x, a.x_scales, at, tid, nt, n);
+        if (GATE) zq.load(a.gate, a.gate_scales, (int64_t)row * a.gate_stride + first, tid, nt, n);
+        if (!RES || next) dq.load(a.dout, at, tid, nt, n);
+        if (next) hq.load(a.h, a.h_scales, at, tid, nt, n);
+        if (RES) rq.load(a.dres, at, tid, nt, n);
+        const Two xs = both(a.x_scales ? __ldg(a.x_scales + unit) : 1.f);
+        const Two gs = both(GATE && a.gate_scales ? __ldg(a.gate_scales + unit) : 1.f);
+        const Two hs = both(next && a.h_scales ? __ldg(a.h_scales + unit) : 1.f);
+        Two sg[GATE ? C : 1], g1[RES ? C : 1];
         Two r2 = both(0.f), k2 = r2;
         if constexpr (RES) {
             if (next) {
                 Two hh = both(0.f), ph = hh;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const int e = tid + 2 * c * nt;
-                    if (e >= n) continue;
-                    const Two h = h_at(e), d = dout_at(e);
+                    const Two h = hq.get(a.h_scales, hs, c);
                     hh = fma(h, h, hh);
-                    ph = fma(d * weights(a.next_weight, e), h, ph);
+                    ph = fma(dq.get(c) * weights(a.next_weight, c), h, ph);
                 }
                 float s[2] = {low(hh) + high(hh), low(ph) + high(ph)};
                 row_sums(s, one_warp, part[turn]);
@@ -499,28 +523,27 @@ __global__ void __launch_bounds__(512) ssd_block_norm_bwd_loose(const __grid_con
         Two uu = both(0.f), pu = uu;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = tid + 2 * c * nt;
-            if (e >= n) continue;
             Two g;
             if constexpr (RES) {
-                g = load_loose<R>(a.dres, false, 1.f, at, e, nt, n);
+                g = rq.get(c);
                 if (next) {
-                    const Two h = h_at(e), d = dout_at(e);
-                    g = fma(d, weights(a.next_weight, e) * r2, fma(h, k2, g));
+                    const Two h = hq.get(a.h_scales, hs, c), d = dq.get(c);
+                    g = fma(d, weights(a.next_weight, c) * r2, fma(h, k2, g));
                     dn[c] = fma(d, h * r2, dn[c]);
                 }
-                put_loose(static_cast<R*>(a.dres_out) + at, e, nt, n, g);
+                put_loose(static_cast<R*>(a.dres_out) + at, c, tid, nt, n, g);
                 g1[c] = g = both(a.scale) * g;
             } else {
-                g = dout_at(e);
+                g = dq.get(c);
             }
-            Two u = x_at(e);
+            Two u = xq.get(a.x_scales, xs, c);
             if constexpr (GATE) {
-                silu<T>(load_loose<T>(a.gate, a.gate_scales, gs, gate_at, e, nt, n), si[c], sl[c]);
-                u = u * si[c];
+                const Two z = zq.get(a.gate_scales, gs, c);
+                sg[c] = sigmoid<T>(z);
+                u = u * (z * sg[c]);
             }
             uu = fma(u, u, uu);
-            pu = fma(g * weights(a.weight + first, e), u, pu);
+            pu = fma(g * weights(a.weight + first, c), u, pu);
         }
         float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
         row_sums(s, one_warp, part[turn]);
@@ -529,20 +552,25 @@ __global__ void __launch_bounds__(512) ssd_block_norm_bwd_loose(const __grid_con
         const Two r1 = both(rstd), k1 = both(-(s[1] * a.inv_size * rstd * rstd) * rstd);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = tid + 2 * c * nt;
-            if (e >= n) continue;
-            Two g;
+            Two g, z;
             if constexpr (RES) g = g1[c];
-            else g = dout_at(e);
-            const Two x = x_at(e), w = weights(a.weight + first, e), u = GATE ? x * si[c] : x, o = u * r1;
+            else g = dq.get(c);
+            const Two x = xq.get(a.x_scales, xs, c), w = weights(a.weight + first, c);
+            Two u = x;
+            if constexpr (GATE) {
+                z = zq.get(a.gate_scales, gs, c) * sg[c];
+                u = x * z;
+            }
+            const Two o = u * r1;
             Two du = fma(g * w, r1, u * k1);
             dw[c] = fma(g, o, dw[c]);
-            if (!RES && a.out) put_loose(static_cast<T*>(a.out) + at, e, nt, n, o * w);
+            if (!RES && a.out) put_loose(static_cast<T*>(a.out) + at, c, tid, nt, n, o * w);
             if constexpr (GATE) {
-                put_loose(static_cast<T*>(a.dgate) + (int64_t)row * a.dgate_stride + first, e, nt, n, du * (x * sl[c]));
-                du = du * si[c];
+                put_loose(static_cast<T*>(a.dgate) + (int64_t)row * a.dgate_stride + first, c, tid, nt, n,
+                          du * (x * fma(sg[c], fma(z, both(-1.f), both(1.f)), z)));
+                du = du * z;
             }
-            put_loose(static_cast<T*>(a.dx) + at, e, nt, n, du);
+            put_loose(static_cast<T*>(a.dx) + at, c, tid, nt, n, du);
         }
     }
     const int width = n * a.groups, columns = RES && a.next_weight ? 2 * width : width;
@@ -558,43 +586,52 @@ __global__ void __launch_bounds__(512) ssd_block_norm_bwd_loose(const __grid_con
         }
 }
 
-// How a call's rows are spread: threads of a CTA, its slots, and all slots (a number of rows at a time, each of its groups).
+// How a call's rows are spread: a slot's lanes (0: a CTA), threads of a CTA, its slots, and all slots (a number of rows at a time, each
+// of its groups).
 struct RowPlan {
-    int threads, slots_per_cta, slots, grid;
+    int elems, lanes, threads, slots_per_cta, slots, grid;
 };
 
-inline int slot_threads(int span, int elems) { return ((span + elems - 1) / elems + 31) / 32 * 32; }
+// Threads of a CTA that takes rows by itself, and CTAs that the registers of so many threads an SM hold.
+inline int row_threads(int span, int elems) { return ((span + elems - 1) / elems + 31) / 32 * 32; }
+inline int ctas_sm(int threads, int most) { return most / threads > 0 ? most / threads : 1; }
 
-inline RowPlan row_plan(int64_t rows, int span, int groups, int elems, int per_sm) {
-    RowPlan p;
-    p.threads = slot_threads(span, elems);
-    const int cta_slots = p.threads == 32 ? 4 : 1;
-    int64_t lines = (int64_t)kAddNormSMs * per_sm * cta_slots / groups / 8 * 8;
+inline void spread(RowPlan& p, int64_t rows, int groups, int per_sm) {
+    int64_t lines = (int64_t)kAddNormSMs * per_sm * p.slots_per_cta / groups / 8 * 8;
     if (lines < 8) lines = 8;
     if (lines > rows) lines = rows;
     p.slots = (int)lines * groups;
-    p.slots_per_cta = p.slots < cta_slots ? p.slots : cta_slots;
-    p.threads *= p.slots_per_cta;
     p.grid = (p.slots + p.slots_per_cta - 1) / p.slots_per_cta;
-    return p;
-}
-
-// CTAs that an SM's registers hold.
-inline int ctas_sm(int span, int elems, bool res) {
-    const int threads = slot_threads(span, elems) == 32 ? 128 : slot_threads(span, elems);
-    return threads_sm(elems, res) / threads > 0 ? threads_sm(elems, res) / threads : 1;
 }
 
 // Columns that the vectors of a row span: rows of other than whole vectors may reach into one more.
 inline int vector_span(int size) { return size % 8 == 0 ? size : size + 7; }
 
-// Elements per thread where vectors are taken: 8 while that makes at most 160 threads.
-inline int vector_elems(int span) { return span <= 160 * kNarrowElems ? kNarrowElems : kWideElems; }
+// Rows of up to 256 columns take 8, 16 or 32 lanes of a warp, others a CTA: 8 elements a thread while that makes at most 160 threads,
+// then 16.
+inline RowPlan vector_plan(int span) {
+    RowPlan p = {};
+    p.elems = span <= 160 * kNarrowElems ? kNarrowElems : kWideElems;
+    p.lanes = span <= 64 ? 8 : span <= 128 ? 16 : span <= 256 ? 32 : 0;
+    p.threads = p.lanes ? 128 : row_threads(span, p.elems);
+    p.slots_per_cta = p.lanes ? 128 / p.lanes : 1;
+    return p;
+}
+inline RowPlan loose_plan(int64_t rows, int size, int groups) {
+    RowPlan p = {};
+    p.elems = size <= 512 * kNarrowElems ? kNarrowElems : kWideElems;
+    p.threads = row_threads(size, p.elems);
+    p.slots_per_cta = p.threads == 32 ? 4 : 1;
+    spread(p, rows, groups, ctas_sm(p.threads * p.slots_per_cta, loose_threads_sm(p.elems)));
+    if (p.slots < p.slots_per_cta) p.slots_per_cta = p.slots;
+    p.threads *= p.slots_per_cta;
+    return p;
+}
 
-template <typename T, typename R, int E, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
-cudaError_t launch_ring(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
+template <typename T, typename R, int E, int LANES, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
+cudaError_t launch_ring(BlockNormBwdArgs& a, RowPlan p, int* lines, cudaStream_t st) {
     typedef Record<T, R, E, GATE, RES, XP, HP> Rec;
-    auto kern = ssd_block_norm_bwd_kernel<T, R, E, SHIFTED, GATE, RES, XP, HP>;
+    auto kern = ssd_block_norm_bwd_kernel<T, R, E, LANES, SHIFTED, GATE, RES, XP, HP>;
     static std::atomic<uint8_t> ready[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -606,32 +643,30 @@ cudaError_t launch_ring(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
             return e;
         ready[dev].store(1, std::memory_order_release);
     }
-    const int span = SHIFTED ? vector_span(a.size) : a.size;
-    const int nt = slot_threads(span, E), cta_slots = nt == 32 ? 4 : 1;
-    a.stage_bytes = nt * Rec::bytes;
-    int per_sm = ctas_sm(span, E, RES);
+    const int stage = p.threads * Rec::bytes, weights = p.threads * Rec::weights;
+    int per_sm = ctas_sm(p.threads, threads_sm(E, RES));
     for (;; --per_sm) {
         const int room = (kSmemSM / per_sm < kSmemCta + 1024 ? kSmemSM / per_sm : kSmemCta + 1024) - 1024 - kSmemOwn;
-        a.stages = (room / cta_slots - nt * Rec::weights) / a.stage_bytes;
+        a.stages = (room - weights) / stage;
         if (a.stages >= 2 || per_sm == 1) break;
     }
     if (a.stages < 1) return cudaErrorNotSupported;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    a.slot_bytes = nt * Rec::weights + a.stages * a.stage_bytes;
-    const RowPlan p = row_plan(a.rows, span, a.groups, E, per_sm);
+    spread(p, a.rows, a.groups, per_sm);
     a.slots = p.slots;
     a.slots_per_cta = p.slots_per_cta;
     *lines = p.slots / a.groups;
-    return launch_kernel(kern, (unsigned)p.grid, (unsigned)p.threads, (size_t)a.slot_bytes * p.slots_per_cta, st, true, a);
+    return launch_kernel(kern, (unsigned)p.grid, (unsigned)p.threads, (size_t)weights + (size_t)a.stages * stage, st, true, a);
 }
 
-template <typename T, typename R, bool GATE, bool RES, bool XP, bool HP>
-cudaError_t launch_vectors(BlockNormBwdArgs& a, bool shifted, int* lines, cudaStream_t st) {
-    if (vector_elems(vector_span(a.size)) == kNarrowElems)
-        return shifted ? launch_ring<T, R, kNarrowElems, true, GATE, RES, XP, HP>(a, lines, st)
-                       : launch_ring<T, R, kNarrowElems, false, GATE, RES, XP, HP>(a, lines, st);
-    return shifted ? launch_ring<T, R, kWideElems, true, GATE, RES, XP, HP>(a, lines, st)
-                   : launch_ring<T, R, kWideElems, false, GATE, RES, XP, HP>(a, lines, st);
+template <typename T, typename R, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
+cudaError_t launch_vectors(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
+    const RowPlan p = vector_plan(SHIFTED ? vector_span(a.size) : a.size);
+    if (p.lanes == 8) return launch_ring<T, R, kNarrowElems, 8, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
+    if (p.lanes == 16) return launch_ring<T, R, kNarrowElems, 16, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
+    if (p.lanes == 32) return launch_ring<T, R, kNarrowElems, 32, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
+    return p.elems == kNarrowElems ? launch_ring<T, R, kNarrowElems, 0, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st)
+                                   : launch_ring<T, R, kWideElems, 0, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
 }
 
 // The main launch; *lines: rows of shares that it leaves.  Vectors where every array starts on 16 bytes (codes on a vector's), rows hold
@@ -652,18 +687,24 @@ cudaError_t launch_block_norm_bwd_typed(BlockNormBwdArgs& a, int* lines, cudaStr
     cudaError_t e = cudaErrorNotSupported;
     if (vectors && hp) {
         if constexpr (RES)
-            e = xp ? launch_vectors<T, R, GATE, RES, true, true>(a, shifted, lines, st)
-                   : launch_vectors<T, R, GATE, RES, false, true>(a, shifted, lines, st);
+            e = xp ? (shifted ? launch_vectors<T, R, true, GATE, RES, true, true>(a, lines, st)
+                              : launch_vectors<T, R, false, GATE, RES, true, true>(a, lines, st))
+                   : (shifted ? launch_vectors<T, R, true, GATE, RES, false, true>(a, lines, st)
+                              : launch_vectors<T, R, false, GATE, RES, false, true>(a, lines, st));
     } else if (vectors) {
-        e = xp ? launch_vectors<T, R, GATE, RES, true, false>(a, shifted, lines, st)
-               : launch_vectors<T, R, GATE, RES, false, false>(a, shifted, lines, st);
+        e = xp ? (shifted ? launch_vectors<T, R, true, GATE, RES, true, false>(a, lines, st)
+                          : launch_vectors<T, R, false, GATE, RES, true, false>(a, lines, st))
+               : (shifted ? launch_vectors<T, R, true, GATE, RES, false, false>(a, lines, st)
+                          : launch_vectors<T, R, false, GATE, RES, false, false>(a, lines, st));
     }
-    if (e != cudaErrorNotSupported) return e;   // not even one row's records fit an SM: fp32 rows of all operands beyond 7488 columns
-    const RowPlan p = row_plan(a.rows, a.size, a.groups, kWideElems, ctas_sm(a.size, kWideElems, true));
+    if (e != cudaErrorNotSupported) return e;   // not even one row's records fit an SM: the widest fp32 rows
+    const RowPlan p = loose_plan(a.rows, a.size, a.groups);
     a.slots = p.slots;
     a.slots_per_cta = p.slots_per_cta;
     *lines = p.slots / a.groups;
-    return launch_kernel(ssd_block_norm_bwd_loose<T, R, GATE, RES>, (unsigned)p.grid, (unsigned)p.threads, 0, st, true, a);
+    return launch_kernel(p.elems == kNarrowElems ? ssd_block_norm_bwd_loose<T, R, kNarrowElems, GATE, RES>
+                                                 : ssd_block_norm_bwd_loose<T, R, kWideElems, GATE, RES>,
+                         (unsigned)p.grid, (unsigned)p.threads, 0, st, true, a);
 }
 
 // One per file: the gate and norm after the scan; the norm after a block by types, without and with a gate.

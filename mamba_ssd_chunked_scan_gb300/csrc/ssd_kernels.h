@@ -234,7 +234,7 @@ struct BlockNormBwdArgs {
     float* shares;         // [lines * width * weights]
     // set at the launch: the rows' slots, and their shared memory (weights, then stages of operands and scales)
     int slots, slots_per_cta;
-    int stages, slot_bytes, stage_bytes;
+    int stages;
     float inv_size;
 };
 

@@ -172,26 +172,24 @@ __device__ __forceinline__ void leave_sums(float v, RowPart& part) {
 template <int N>
 __device__ __forceinline__ void join_sums(float (&s)[N], const RowPart& part) {
     const int count = (blockDim.x >> 5) * N;
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    Two t = both(0.f), u = t;
     int k = 0;
 #pragma unroll 4
     for (; k + 4 <= count; k += 4) {
         const float4 q = *reinterpret_cast<const float4*>(part.sums + k);
-        t.x += q.x;
-        t.y += q.y;
-        t.z += q.z;
-        t.w += q.w;
+        t = t + two(q.x, q.y);
+        u = u + two(q.z, q.w);
     }
     if (k < count) {   // what is left
-        t.x += part.sums[k];
-        if (k + 1 < count) t.y += part.sums[k + 1];
-        if (k + 2 < count) t.z += part.sums[k + 2];
+        t = t + two(part.sums[k], k + 1 < count ? part.sums[k + 1] : 0.f);
+        if (k + 2 < count) u = u + two(part.sums[k + 2], 0.f);
     }
+    t = t + u;
     if constexpr (N == 1) {
-        s[0] = (t.x + t.y) + (t.z + t.w);
+        s[0] = low(t) + high(t);
     } else {
-        s[0] = t.x + t.z;
-        s[1] = t.y + t.w;
+        s[0] = low(t);
+        s[1] = high(t);
     }
 }
 template <int N>
@@ -206,6 +204,18 @@ __device__ __forceinline__ void row_sums(float (&s)[N], bool one_warp, RowPart& 
     leave_sums<N>(v, part);
     __syncthreads();
     join_sums(s, part);
+}
+
+// Two sums over LANES lanes of a warp that hold a row (a power of two of them, side by side).
+template <int LANES>
+__device__ __forceinline__ void lane_sums(float (&s)[2]) {
+    const uint32_t mask = LANES == 32 ? 0xffffffffu : ((1u << (LANES % 32)) - 1) << (threadIdx.x & (32 - LANES));
+    const bool up = threadIdx.x & (LANES / 2);
+    float v = (up ? s[1] : s[0]) + __shfl_xor_sync(mask, up ? s[0] : s[1], LANES / 2);
+#pragma unroll
+    for (int o = LANES / 4; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+    s[0] = __shfl_sync(mask, v, 0, LANES);
+    s[1] = __shfl_sync(mask, v, LANES / 2, LANES);
 }
 
 // A sum (the same as row_sums') and two maxima, by one barrier.
