@@ -33,6 +33,7 @@ __device__ __forceinline__ void copies_wait(int n) {
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+template <int N> struct Number { static constexpr int value = N; };
 template <bool, typename A, typename B> struct Pick { typedef A type; };
 template <typename A, typename B> struct Pick<false, A, B> { typedef B type; };
 
@@ -56,11 +57,15 @@ struct Record {
     static constexpr int weight = E * 4, weights = (RES ? 2 : 1) * weight;   // the weights' record
 };
 
-// Where a lane's 16-byte half `h` of its vector c of type K lies, or all of it where K is shorter, from an operand's first piece on.
+// Where the 16-byte half `k` of a lane's vector c of type K lies, or all of it where K is shorter, from an operand's first piece on.
+// Vectors of 32 bytes (fp32 beside bf16) are copied by pairs of lanes, 32 adjacent bytes at a time: a lane that took its own two
+// halves would ask for each 32-byte sector twice (588 MB of operands, half of them so, took 148 us).  The order of their places
+// keeps both the copies and the reads off each other's banks.
 template <typename K, int V>
-__device__ __forceinline__ int piece(int c, int h, int lane) {
-    constexpr int kBytes = (int)sizeof(K) * V, kHalves = kBytes > 16 ? kBytes / 16 : 1;
-    return (c * kHalves + h) * 32 * (kBytes / kHalves) + lane * (kBytes / kHalves);
+__device__ __forceinline__ int piece(int c, int k, int lane) {
+    constexpr int kBytes = (int)sizeof(K) * V;
+    if constexpr (kBytes == 32) return (c * 2 + (lane & 1)) * 512 + (((lane & 30) | k) ^ (lane & 1)) * 16;
+    else return (c * 32 + lane) * kBytes;
 }
 
 // One vector (number c of the lane's) of an operand, whose pieces start at `at`.
@@ -85,14 +90,25 @@ __device__ __forceinline__ void widen(const Raw<K, V>& q, Two s, Two (&v)[V / 2]
     }
 }
 
-// Ask for `count` elements of a vector of an operand, `off` bytes from p, into its pieces.
+// Ask for the elements of vector c (from column e, `off` bytes from p) that lie before column `end`, into its pieces: those of one lane
+// each for itself, 32-byte ones with the neighbouring lane.  A vector past the row's n columns is left alone.
 template <typename K, int V, bool SHIFTED>
-__device__ __forceinline__ void ask(uint32_t to, int c, int lane, const unsigned char* p, uint32_t off, int count) {
-    constexpr int kBytes = (int)sizeof(K) * V, kHalves = kBytes > 16 ? kBytes / 16 : 1, kPiece = kBytes / kHalves;
+__device__ __forceinline__ void ask(uint32_t to, int c, int lane, const unsigned char* p, uint32_t off, int e, int n, int end) {
+    constexpr int kBytes = (int)sizeof(K) * V;
+    if constexpr (kBytes == 32) {
+        const int k = lane & 1;
+        const unsigned char* pair = p + (off - 32 * k);
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h) {
-        const int bytes = SHIFTED ? max(0, min(kPiece, count * (int)sizeof(K) - kPiece * h)) : kPiece;
-        copy_async<kPiece>(to + piece<K, V>(c, h, lane), p + off + (SHIFTED && bytes == 0 ? 0 : kPiece * h), bytes);
+        for (int h = 0; h < 2; ++h) {
+            const int eo = e + (h - k) * V;   // the vector of the pair's lane h
+            if (eo >= n) continue;
+            const int bytes = SHIFTED ? max(0, min(16, (end - eo - k * V / 2) * (int)sizeof(K))) : 16;
+            copy_async<16>(to + piece<K, V>(c, k, (lane & 30) | h), pair + (SHIFTED && bytes == 0 ? 0 : 32 * h + 16 * k), bytes);
+        }
+    } else {
+        if (e >= n) return;
+        const int bytes = SHIFTED ? min(kBytes, (end - e) * (int)sizeof(K)) : kBytes;
+        copy_async<kBytes>(to + piece<K, V>(c, 0, lane), p + off, bytes);
     }
 }
 
@@ -106,17 +122,40 @@ __device__ __forceinline__ void clear_outside(unsigned char* at, int c, int lane
             reinterpret_cast<typename Word<(int)sizeof(K)>::type*>(at + piece<K, V>(c, k / kEach, lane))[k % kEach] = 0;
 }
 
-// The elements of a vector that lie in a row's columns [0, n): it starts at column e, and at byte `off` from `row`.
+// Store the elements of a vector (from column e, `off` bytes from `row`) that lie in a row's columns [0, n); 32-byte vectors with the
+// neighbouring lane, as they are copied (all lanes of `mask` call).
 template <typename K, int V, bool SHIFTED>
-__device__ __forceinline__ void put(unsigned char* row, uint32_t off, int e, int n, const Two (&v)[V / 2]) {
+__device__ __forceinline__ void put(unsigned char* row, uint32_t off, int e, int n, uint32_t mask, const Two (&v)[V / 2]) {
     Raw<K, V> q;
     from_pairs(v, q);
-    K* p = reinterpret_cast<K*>(row + off);
-    if constexpr (SHIFTED) {
-        if (e >= 0 && e + V <= n) q.store(p);
-        else q.store_within(p - e, e, n);
+    if constexpr ((int)sizeof(K) * V == 32) {
+        const int k = threadIdx.x & 1;
+        uint4 keep = k ? q.w.hi : q.w.lo, give = k ? q.w.lo : q.w.hi;
+        give.x = __shfl_xor_sync(mask, give.x, 1);
+        give.y = __shfl_xor_sync(mask, give.y, 1);
+        give.z = __shfl_xor_sync(mask, give.z, 1);
+        give.w = __shfl_xor_sync(mask, give.w, 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int eo = e + (h - k) * V + k * (V / 2);   // the first column of the half
+            Raw<K, V / 2> r;
+            r.w = h == k ? keep : give;
+            K* p = reinterpret_cast<K*>(row + (off - 32 * k + 32 * h + 16 * k));
+            if constexpr (SHIFTED) {
+                if (eo >= 0 && eo + V / 2 <= n) r.store(p);
+                else r.store_within(p - eo, eo, n);
+            } else {
+                if (eo < n) r.store(p);
+            }
+        }
     } else {
-        if (e < n) q.store(p);
+        K* p = reinterpret_cast<K*>(row + off);
+        if constexpr (SHIFTED) {
+            if (e >= 0 && e + V <= n) q.store(p);
+            else q.store_within(p - e, e, n);
+        } else {
+            if (e < n) q.store(p);
+        }
     }
 }
 
@@ -140,7 +179,12 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     typedef Record<T, R, E, GATE, RES, XP, HP> Rec;
     typedef typename Pick<XP, e4m3_t, T>::type X;
     typedef typename Pick<HP, e4m3_t, R>::type H;
-    constexpr bool kCta = LANES == 0, kKeep = RES;   // kKeep: silu and its slope stay in registers from one pass to the next
+    constexpr bool kCta = LANES == 0;
+    // With a residual silu and its slope stay in registers from one pass to the next, and all of a record but x is free for the next
+    // row before the last pass: one stage is enough then, which leaves room for three CTAs instead of two.
+    constexpr bool kKeep = RES, kEarly = RES;
+    constexpr bool kPairs = RES && sizeof(R) > sizeof(T);   // lanes copy for their neighbours
+    const uint32_t mask = row_mask<LANES>();
     constexpr int V = Rec::kVec, C = E / V, P = V / 2;
     // the operands' first pieces
     constexpr int kD = 32 * Rec::dout, kR = 32 * Rec::dres, kX = 32 * (XP ? Rec::x_codes : Rec::x), kZ = 32 * (XP ? Rec::gate_codes : Rec::gate),
@@ -201,33 +245,39 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     unsigned char *q_dx = out(a.dx, at0, sizeof(T)), *q_dres = out(a.dres_out, at0, sizeof(R)), *q_out = out(a.out, at0, sizeof(T)),
                   *q_dgate = out(a.dgate, (int64_t)line * a.dgate_stride + first - shift, sizeof(T));
     uint32_t unit_ask = unit0;
-    auto ask_row = [&](int stage) {
+    // Ask for the next row's x (kWhich 1), for the rest (0) or for all of it (2), into a stage.
+    auto ask_row = [&](auto which, int stage) {
+        constexpr int kWhich = decltype(which)::value;
+        constexpr bool kRest = kWhich != 1, kAskX = kWhich != 0;
         if (unit_ask < units) {
             const uint32_t to = (uint32_t)__cvta_generic_to_shared(rec0) + stage * kStage;
-            const bool last = SHIFTED && unit_ask + 1 == units;   // the arrays end with its last column
+            const int end = SHIFTED && unit_ask + 1 == units ? n : 1 << 24;   // the arrays end with the last row's last column
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                if (e0 + c * span >= n) continue;
-                const int count = last ? min(V, n - e0 - c * span) : V;
+                const int e = e0 + c * span;
                 const uint32_t t = (uint32_t)tid * V;
                 const int64_t s = c * span;
-                if (!RES || next) ask<T, V, SHIFTED>(to + kD, c, lane, p_dout + s * sizeof(T), t * sizeof(T), count);
-                ask<X, V, SHIFTED>(to + kX, c, lane, p_x + s * sizeof(X), t * sizeof(X), count);
-                if (GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, p_gate + s * sizeof(X), t * sizeof(X), count);
-                if (next) ask<H, V, SHIFTED>(to + kH, c, lane, p_h + s * sizeof(H), t * sizeof(H), count);
-                if (RES) ask<R, V, SHIFTED>(to + kR, c, lane, p_dres + s * sizeof(R), t * sizeof(R), count);
+                if (kRest && (!RES || next)) ask<T, V, SHIFTED>(to + kD, c, lane, p_dout + s * sizeof(T), t * sizeof(T), e, n, end);
+                if (kRest && next) ask<H, V, SHIFTED>(to + kH, c, lane, p_h + s * sizeof(H), t * sizeof(H), e, n, end);
+                if (kRest && RES) ask<R, V, SHIFTED>(to + kR, c, lane, p_dres + s * sizeof(R), t * sizeof(R), e, n, end);
+                if (kRest && GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, p_gate + s * sizeof(X), t * sizeof(X), e, n, end);
+                if (kAskX) ask<X, V, SHIFTED>(to + kX, c, lane, p_x + s * sizeof(X), t * sizeof(X), e, n, end);
             }
-            if (XP) copy_async<4>(to + 32 * Rec::x_scale + 4 * lane, a.x_scales + unit_ask, 4);
-            if (XP && GATE) copy_async<4>(to + 32 * Rec::gate_scale + 4 * lane, a.gate_scales + unit_ask, 4);
-            if (HP && next) copy_async<4>(to + 32 * Rec::h_scale + 4 * lane, a.h_scales + unit_ask, 4);
-            unit_ask += unit_step;
-            if (!RES || next) p_dout += far * sizeof(T);
-            p_x += far * sizeof(X);
-            if (GATE) p_gate += gate_far * sizeof(X);
-            if (next) p_h += far * sizeof(H);
-            if (RES) p_dres += far * sizeof(R);
+            if (kRest) {
+                if (XP) copy_async<4>(to + 32 * Rec::x_scale + 4 * lane, a.x_scales + unit_ask, 4);
+                if (XP && GATE) copy_async<4>(to + 32 * Rec::gate_scale + 4 * lane, a.gate_scales + unit_ask, 4);
+                if (HP && next) copy_async<4>(to + 32 * Rec::h_scale + 4 * lane, a.h_scales + unit_ask, 4);
+                if (!RES || next) p_dout += far * sizeof(T);
+                if (GATE) p_gate += gate_far * sizeof(X);
+                if (next) p_h += far * sizeof(H);
+                if (RES) p_dres += far * sizeof(R);
+            }
+            if (kAskX) {
+                unit_ask += unit_step;
+                p_x += far * sizeof(X);
+            }
         }
-        copies_commit();
+        if (kAskX) copies_commit();
     };
     auto sums = [&](float (&s)[2], int turn) {
         if constexpr (kCta) row_sums(s, false, part[turn]);
@@ -241,13 +291,16 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             dw[c][k] = both(0.f);
             if (RES) dn[c][k] = both(0.f);
         }
-    for (int s = 0; s < a.stages - 1; ++s) ask_row(s);
+    for (int s = 0; s < (kEarly ? 1 : a.stages - 1); ++s) ask_row(Number<2>(), s);
     int stage = 0, turn = 0;
     for (uint32_t unit = unit0; unit < units; unit += unit_step) {
         unsigned char* const rec = rec0 + stage * kStage;
-        ask_row(stage > 0 ? stage - 1 : a.stages - 1);   // where the row before lay
-        if (++stage == a.stages) stage = 0;
-        copies_wait(a.stages - 1);
+        if constexpr (!kEarly) {
+            ask_row(Number<2>(), stage > 0 ? stage - 1 : a.stages - 1);   // where the row before lay
+            if (++stage == a.stages) stage = 0;
+        }
+        copies_wait(kEarly ? 0 : a.stages - 1);
+        if constexpr (kPairs) __syncwarp(mask);
         if constexpr (SHIFTED) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
@@ -313,7 +366,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                         dn[c][k] = fma(d[k], h[k] * r2, dn[c][k]);
                     }
                 }
-                put<R, V, SHIFTED>(q_dres + c * span * (int64_t)sizeof(R), t * sizeof(R), e0 + c * span, n, g);
+                put<R, V, SHIFTED>(q_dres + c * span * (int64_t)sizeof(R), t * sizeof(R), e0 + c * span, n, mask, g);
 #pragma unroll
                 for (int k = 0; k < P; ++k) g1[c][k] = g[k] = both(a.scale) * g[k];
             } else {
@@ -341,6 +394,8 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                 pu = fma(g[k] * w[k], x[k], pu);
             }
         }
+        if constexpr (kPairs) __syncwarp(mask);
+        if constexpr (kEarly) ask_row(Number<0>(), 0);   // what this row needs no more
         float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
         sums(s, turn);
         turn ^= 1;
@@ -366,7 +421,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             if (!RES && a.out) {
 #pragma unroll
                 for (int k = 0; k < P; ++k) o[k] = o[k] * w[k];
-                put<T, V, SHIFTED>(q_out + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, o);
+                put<T, V, SHIFTED>(q_out + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, mask, o);
             }
             if constexpr (GATE) {
 #pragma unroll
@@ -376,10 +431,11 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                     o[k] = du[k] * (x[k] * slope);
                     du[k] = du[k] * z[k];
                 }
-                put<T, V, SHIFTED>(q_dgate + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, o);
+                put<T, V, SHIFTED>(q_dgate + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, mask, o);
             }
-            put<T, V, SHIFTED>(q_dx + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, du);
+            put<T, V, SHIFTED>(q_dx + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, mask, du);
         }
+        if constexpr (kEarly) ask_row(Number<1>(), 0);
         q_dx += far * sizeof(T);
         if (GATE) q_dgate += (int64_t)step * a.dgate_stride * (int64_t)sizeof(T);
         if (RES) q_dres += far * sizeof(R);
@@ -648,10 +704,10 @@ cudaError_t launch_ring(BlockNormBwdArgs& a, RowPlan p, int* lines, cudaStream_t
     for (;; --per_sm) {
         const int room = (kSmemSM / per_sm < kSmemCta + 1024 ? kSmemSM / per_sm : kSmemCta + 1024) - 1024 - kSmemOwn;
         a.stages = (room - weights) / stage;
-        if (a.stages >= 2 || per_sm == 1) break;
+        if (a.stages >= (RES ? 1 : 2) || per_sm == 1) break;
     }
     if (a.stages < 1) return cudaErrorNotSupported;
-    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    if (a.stages > (RES ? 1 : kMaxStages)) a.stages = RES ? 1 : kMaxStages;
     spread(p, a.rows, a.groups, per_sm);
     a.slots = p.slots;
     a.slots_per_cta = p.slots_per_cta;

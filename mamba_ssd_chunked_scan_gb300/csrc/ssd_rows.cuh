@@ -206,10 +206,15 @@ __device__ __forceinline__ void row_sums(float (&s)[N], bool one_warp, RowPart& 
     join_sums(s, part);
 }
 
-// Two sums over LANES lanes of a warp that hold a row (a power of two of them, side by side).
+// The lanes of a warp that share a row with this one: LANES of them side by side, a power of two (0: all).
+template <int LANES>
+__device__ __forceinline__ uint32_t row_mask() {
+    return LANES % 32 == 0 ? 0xffffffffu : ((1u << (LANES % 32)) - 1) << (threadIdx.x & (32 - LANES));
+}
+// Two sums over them.
 template <int LANES>
 __device__ __forceinline__ void lane_sums(float (&s)[2]) {
-    const uint32_t mask = LANES == 32 ? 0xffffffffu : ((1u << (LANES % 32)) - 1) << (threadIdx.x & (32 - LANES));
+    const uint32_t mask = row_mask<LANES>();
     const bool up = threadIdx.x & (LANES / 2);
     float v = (up ? s[1] : s[0]) + __shfl_xor_sync(mask, up ? s[0] : s[1], LANES / 2);
 #pragma unroll
