@@ -6,192 +6,162 @@
 // and x and gate as 8-bit rows, for the backward pass.
 //
 // A row (a group of one, where the norm goes by groups: no residual then) is held in registers from its one read to its
-// one write; h is normalised as it was summed, before its rounding to the residual's type.
+// one write; h is normalised as it was summed, before its rounding to the residual's type.  Groups of up to 256 columns
+// share warps; what a row's threads take is in ssd_rows.cuh.
 #include "ssd_kernels.h"
 #include "ssd_rows.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kElems = 16;   // elements of a row per thread
-
-template <typename T, typename R, int V, bool GATE, bool RES>
-__global__ void __launch_bounds__(512) ssd_block_norm_kernel(BlockNormArgs a) {
-    constexpr int C = kElems / V;
+template <typename T, typename R, int V, int E, int LANES, bool SHIFTED, bool GATE, bool RES>
+__global__ void __launch_bounds__(512) ssd_block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
+    constexpr int C = E / V, P = V / 2;
     __shared__ RowPart part[2];
     __shared__ uint32_t tops[2][32];
-    const bool one_warp = a.units_per_cta > 1 || blockDim.x == 32;
-    const int slot = one_warp ? threadIdx.x >> 5 : 0;
-    const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
-    const int nt = one_warp ? 32 : blockDim.x;
-    const int64_t unit = (int64_t)blockIdx.x * a.units_per_cta + slot;
+    const int tid = LANES ? threadIdx.x % (LANES ? LANES : 32) : threadIdx.x, nt = LANES ? LANES : blockDim.x;
+    const int64_t unit = LANES ? (int64_t)blockIdx.x * a.units_per_cta + threadIdx.x / (LANES ? LANES : 32) : blockIdx.x;
     pdl_wait();
-    if (unit >= a.units) return;   // whole warps of a many-row CTA, which has no barrier
+    if (unit >= a.units) return;   // all of a row's lanes
     const int n = a.size;
-    const int64_t row = unit / a.groups;
+    const int64_t row = unit / a.groups, base = unit * n;
     const int first = (int)(unit - row * a.groups) * n;   // the group's first column
-    const size_t base = (size_t)unit * n;
-    const T* x = static_cast<const T*>(a.x) + base;
-    const T* gate = GATE ? static_cast<const T*>(a.gate) + row * a.gate_stride + first : nullptr;
-    const R* res = RES ? static_cast<const R*>(a.residual) + base : nullptr;
-    Raw<T, V> xr[C], gr[GATE ? C : 1];
-    Raw<R, V> rr[RES ? C : 1];
+    const Place<V, SHIFTED> place = {tid, nt, SHIFTED ? (int)(base % V) : 0, n, (a.units - unit) * n};
+    Part<T, V, E, SHIFTED> xq, zq;
+    Part<R, V, E, SHIFTED> rq;
+    xq.load(static_cast<const T*>(a.x) + base, place);
+    if (GATE) zq.load(static_cast<const T*>(a.gate) + row * a.gate_stride + first, place);
+    if (RES) rq.load(static_cast<const R*>(a.residual) + base, place);
+    Two u[C][P], sum = both(0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int e = (tid + c * nt) * V;
-        xr[c].zero();
-        if (GATE) gr[c].zero();
-        if (RES) rr[c].zero();
-        if (e < n) {
-            xr[c].load(x + e);
-            if (GATE) gr[c].load(gate + e);
-            if (RES) rr[c].load(res + e);
-        }
-    }
-    float u[C][V];
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        xr[c].get(u[c]);
+        xq.get(c, u[c]);
         if (GATE) {
-            float g[V];
-            gr[c].get(g);
+            Two z[P];
+            zq.get(c, z);
 #pragma unroll
-            for (int k = 0; k < V; ++k) u[c][k] *= g[k] * sigmoid<T>(g[k]);
+            for (int k = 0; k < P; ++k) u[c][k] = u[c][k] * (z[k] * sigmoid<T>(z[k]));
         }
 #pragma unroll
-        for (int k = 0; k < V; ++k) ss[0] = fmaf(u[c][k], u[c][k], ss[0]);
+        for (int k = 0; k < P; ++k) sum = fma(u[c][k], u[c][k], sum);
     }
+    float ss[1] = {low(sum) + high(sum)};
     if (a.x_codes) {
-        RowMaxima m = {0, 0};
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            m.a = max(m.a, magnitude(xr[c]));
-            if (GATE) m.b = max(m.b, magnitude(gr[c]));
+        RowMaxima m = {xq.top(), GATE ? zq.top() : 0};
+        row_sum_maxima<LANES>(ss, m, part[0]);
+        const bool bad_x = m.a >= kInfBits, bad_z = m.b >= kInfBits;   // the same in all of the row's threads
+        if (bad_x || bad_z) {
+            m.a = row_maximum<LANES>(xq.finite_top(), tops[0]);
+            if (GATE) m.b = row_maximum<LANES>(zq.finite_top(), tops[1]);
         }
-        row_sum_maxima(ss, m, one_warp, part[0]);
-        const bool bad_x = m.a >= kInfBits, bad_g = m.b >= kInfBits;   // the same in all of the row's threads
-        if (bad_x || bad_g) {
-            m.a = m.b = 0;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                m.a = max(m.a, finite_magnitude(xr[c]));
-                if (GATE) m.b = max(m.b, finite_magnitude(gr[c]));
-            }
-            m.a = row_maximum(m.a, one_warp, tops[0]);
-            m.b = row_maximum(m.b, one_warp, tops[1]);
-        }
-        const uint32_t sx = pack_scale_bits(m.a), sg = pack_scale_bits(m.b);
+        const uint32_t sx = pack_scale_bits(m.a), sz = pack_scale_bits(m.b);
         if (tid == 0) {
             a.x_scales[unit] = __uint_as_float(sx);
-            if (GATE) a.gate_scales[unit] = __uint_as_float(sg);
+            if (GATE) a.gate_scales[unit] = __uint_as_float(sz);
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = (tid + c * nt) * V;
-            if (e < n) {
-                float v[V];
-                Raw<e4m3_t, V> q;
-                xr[c].get(v);
-                to_codes(v, pack_inverse(sx), bad_x);
-                q.set(v);
-                q.store(static_cast<e4m3_t*>(a.x_codes) + base + e);
-                if (GATE) {
-                    gr[c].get(v);
-                    to_codes(v, pack_inverse(sg), bad_g);
-                    q.set(v);
-                    q.store(static_cast<e4m3_t*>(a.gate_codes) + base + e);
-                }
+            Two v[P];
+            xq.get(c, v);
+            store_codes<V, E, SHIFTED>(static_cast<e4m3_t*>(a.x_codes) + base, place, c, v, pack_inverse(sx), bad_x);
+            if (GATE) {
+                zq.get(c, v);
+                store_codes<V, E, SHIFTED>(static_cast<e4m3_t*>(a.gate_codes) + base, place, c, v, pack_inverse(sz), bad_z);
             }
         }
     } else {
-        row_sums(ss, one_warp, part[0]);
+        row_sum<LANES>(ss, part[0]);
     }
-    const float rstd = rsqrt_of(ss[0] * a.inv_size + a.eps);
-    float hh = 0.f;
+    const Two rstd = both(rsqrt_of(ss[0] * a.inv_size + a.eps));
+    if constexpr (!RES) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int e = (tid + c * nt) * V;
-        if (e < n) {
-            float w[V];
-            row_weights<V, false>(a.weight + first, e, n, w);
-            if (RES) {
-                float r[V];
-                rr[c].get(r);
+        for (int c = 0; c < C; ++c) {
+            Two w[P];
+            weights_of<V, SHIFTED>(a.weight + first, place, c, w);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    u[c][k] = fmaf(a.scale, u[c][k] * rstd * w[k], r[k]);
-                    hh = fmaf(u[c][k], u[c][k], hh);
-                }
-                Raw<R, V> q;
-                q.set(u[c]);
-                q.store(static_cast<R*>(a.residual_out) + base + e);
-            } else {
-#pragma unroll
-                for (int k = 0; k < V; ++k) u[c][k] = u[c][k] * rstd * w[k];
-                Raw<T, V> q;
-                q.set(u[c]);
-                q.store(static_cast<T*>(a.out) + base + e);
-            }
+            for (int k = 0; k < P; ++k) w[k] = u[c][k] * rstd * w[k];
+            Part<T, V, E, SHIFTED> q;
+            q.set(c, w);
+            q.store(static_cast<T*>(a.out) + base, place, c);
         }
-    }
-    if constexpr (RES) {
+    } else {
+        sum = both(0.f);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            Two w[P], r[P];
+            weights_of<V, SHIFTED>(a.weight, place, c, w);
+            rq.get(c, r);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                u[c][k] = fma(both(a.scale), u[c][k] * rstd * w[k], r[k]);
+                sum = fma(u[c][k], u[c][k], sum);
+            }
+            Part<R, V, E, SHIFTED> q;
+            q.set(c, u[c]);
+            q.store(static_cast<R*>(a.residual_out) + base, place, c);
+        }
         if (!a.next_weight) return;
-        float s[1] = {hh};
-        row_sums(s, one_warp, part[1]);
-        const float rstd2 = rsqrt_of(s[0] * a.inv_size + a.eps);
+        ss[0] = low(sum) + high(sum);
+        row_sum<LANES>(ss, part[1]);
+        const Two rstd2 = both(rsqrt_of(ss[0] * a.inv_size + a.eps));
         const bool codes = a.out_dtype == SSD_E4M3;
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = (tid + c * nt) * V;
-            if (e < n) {
-                float w[V];
-                row_weights<V, false>(a.next_weight, e, n, w);
+            Two w[P];
+            weights_of<V, SHIFTED>(a.next_weight, place, c, w);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    u[c][k] = u[c][k] * rstd2 * w[k];
-                    const uint32_t b = __float_as_uint(u[c][k]) & 0x7fffffffu;
-                    if (b < kInfBits) top = max(top, b);
-                }
-                if (!codes) {
-                    Raw<T, V> q;
-                    q.set(u[c]);
-                    q.store(static_cast<T*>(a.out) + base + e);
-                }
+            for (int k = 0; k < P; ++k) u[c][k] = u[c][k] * rstd2 * w[k];
+            if (codes) {
+#pragma unroll
+                for (int k = 0; k < P; ++k)
+                    for (const float f : {low(u[c][k]), high(u[c][k])}) {
+                        const uint32_t b = __float_as_uint(f) & 0x7fffffffu;
+                        if (b < kInfBits) top = max(top, b);
+                    }
+            } else {
+                Part<T, V, E, SHIFTED> q;
+                q.set(c, u[c]);
+                q.store(static_cast<T*>(a.out) + base, place, c);
             }
         }
         if (!codes) return;
-        const uint32_t so = pack_scale_bits(row_maximum(top, one_warp, tops[0]));
+        const uint32_t so = pack_scale_bits(row_maximum<LANES>(top, tops[0]));
         if (tid == 0) a.out_scales[unit] = __uint_as_float(so);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = (tid + c * nt) * V;
-            if (e < n) {
-                Raw<e4m3_t, V> q;
-                to_codes(u[c], pack_inverse(so), true);
-                q.set(u[c]);
-                q.store(static_cast<e4m3_t*>(a.out) + base + e);
-            }
-        }
+        for (int c = 0; c < C; ++c)
+            store_codes<V, E, SHIFTED>(static_cast<e4m3_t*>(a.out) + base, place, c, u[c], pack_inverse(so), true);
     }
 }
 
 bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-template <typename T, typename R, bool RES>
-cudaError_t launch_typed(const BlockNormArgs& a, unsigned grid, unsigned threads, cudaStream_t st) {
+template <typename T, typename R, int V, bool SHIFTED, bool GATE, bool RES>
+cudaError_t launch_shape(const BlockNormArgs& args, cudaStream_t st) {
+    BlockNormArgs a = args;
+    const int span = SHIFTED ? a.size + V - 1 : a.size;   // columns that the vectors of a row may span
+    auto go = [&](auto kern, int lanes, int threads) {
+        a.units_per_cta = lanes ? threads / lanes : 1;
+        const unsigned grid = (unsigned)((a.units + a.units_per_cta - 1) / a.units_per_cta);
+        return launch_kernel(kern, grid, (unsigned)threads, 0, st, true, a);
+    };
+    if (span <= 64) return go(ssd_block_norm_kernel<T, R, V, 8, 8, SHIFTED, GATE, RES>, 8, 128);
+    if (span <= 128) return go(ssd_block_norm_kernel<T, R, V, 8, 16, SHIFTED, GATE, RES>, 16, 128);
+    if (span <= 256) return go(ssd_block_norm_kernel<T, R, V, 8, 32, SHIFTED, GATE, RES>, 32, 128);
+    return go(ssd_block_norm_kernel<T, R, V, 16, 0, SHIFTED, GATE, RES>, 0, ((span + 15) / 16 + 31) / 32 * 32);
+}
+
+// Vectors where every array starts on 16 bytes (codes on a vector's) and rows hold one at least, single elements otherwise.
+template <typename T, typename R, bool GATE, bool RES>
+cudaError_t launch_typed(const BlockNormArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.size % V == 0 && on16(a.x) && on16(a.residual) && on16(a.residual_out) && on16(a.weight) && on16(a.next_weight) &&
-                     on16(a.out) && ((uintptr_t)a.x_codes % V) == 0 && ((uintptr_t)a.gate_codes % V) == 0 &&
-                     (!a.gate || (a.gate_stride % V == 0 && on16(a.gate)));
-    if (a.gate)
-        return launch_kernel(vec ? ssd_block_norm_kernel<T, R, V, true, RES> : ssd_block_norm_kernel<T, R, 1, true, RES>, grid, threads, 0,
-                             st, true, a);
-    if constexpr (RES)
-        return launch_kernel(vec ? ssd_block_norm_kernel<T, R, V, false, RES> : ssd_block_norm_kernel<T, R, 1, false, RES>, grid, threads, 0,
-                             st, true, a);
-    return cudaErrorInvalidValue;   // a norm without gate or residual is ssd_add_norm's
+    const bool shifted = a.size % V != 0, e4m3 = a.out_dtype == SSD_E4M3;
+    const bool vectors = a.size >= V && (!shifted || a.size + V - 1 <= 512 * 16) && on16(a.x) && on16(a.residual) && on16(a.residual_out) &&
+                         (e4m3 ? ((uintptr_t)a.out % V) == 0 : on16(a.out)) && ((uintptr_t)a.x_codes % V) == 0 &&
+                         ((uintptr_t)a.gate_codes % V) == 0 && (shifted || (on16(a.weight) && on16(a.next_weight))) &&
+                         (!GATE || (on16(a.gate) && (shifted ? a.gate_stride == (int64_t)a.size * a.groups : a.gate_stride % V == 0)));
+    if (!vectors) return launch_shape<T, R, 2, false, GATE, RES>(a, st);
+    return shifted ? launch_shape<T, R, V, true, GATE, RES>(a, st) : launch_shape<T, R, V, false, GATE, RES>(a, st);
 }
 
 }  // namespace
@@ -199,21 +169,11 @@ cudaError_t launch_typed(const BlockNormArgs& a, unsigned grid, unsigned threads
 cudaError_t launch_block_norm(const BlockNormArgs& args, cudaStream_t st) {
     BlockNormArgs a = args;
     a.inv_size = 1.f / (float)a.size;
-    unsigned threads;
-    if (a.size <= 32 * kElems) {
-        a.units_per_cta = a.units < 4 ? (int)a.units : 4;
-        threads = 32 * a.units_per_cta;
-    } else {
-        a.units_per_cta = 1;
-        threads = ((a.size + kElems - 1) / kElems + 31) / 32 * 32;
-    }
-    const unsigned grid = (unsigned)((a.units + a.units_per_cta - 1) / a.units_per_cta);
-    if (!a.residual)
-        return a.dtype == SSD_BF16 ? launch_typed<bf16_t, bf16_t, false>(a, grid, threads, st) : launch_typed<float, float, false>(a, grid, threads, st);
-    if (a.dtype == SSD_BF16)
-        return a.residual_dtype == SSD_F32 ? launch_typed<bf16_t, float, true>(a, grid, threads, st)
-                                           : launch_typed<bf16_t, bf16_t, true>(a, grid, threads, st);
-    return launch_typed<float, float, true>(a, grid, threads, st);
+    if (!a.residual) return a.dtype == SSD_BF16 ? launch_typed<bf16_t, bf16_t, true, false>(a, st) : launch_typed<float, float, true, false>(a, st);
+    if (a.dtype == SSD_F32) return a.gate ? launch_typed<float, float, true, true>(a, st) : launch_typed<float, float, false, true>(a, st);
+    if (a.residual_dtype == SSD_F32)
+        return a.gate ? launch_typed<bf16_t, float, true, true>(a, st) : launch_typed<bf16_t, float, false, true>(a, st);
+    return a.gate ? launch_typed<bf16_t, bf16_t, true, true>(a, st) : launch_typed<bf16_t, bf16_t, false, true>(a, st);
 }
 
 }  // namespace ssd

@@ -19,11 +19,14 @@ namespace ssd {
 
 // Enough for every shape: which one a call takes depends on its addresses and types too.
 int64_t block_norm_bwd_lines(int64_t rows, int size, int groups) {
-    int most = loose_plan(rows, size, groups).slots;
+    const RowPlan loose = loose_plan(rows, size, groups);
+    int most = loose.slots + loose.late_slots;
     for (int span : {size, vector_span(size)}) {
         RowPlan p = vector_plan(span);
-        spread(p, rows, groups, ctas_sm(p.threads, threads_sm(p.elems, false)));
-        if (p.slots > most) most = p.slots;
+        for (int per_sm = ctas_sm(p.threads, threads_sm(p.elems, false)); per_sm > 0; --per_sm) {
+            spread(p, rows, groups, per_sm, true);
+            if (p.slots + p.late_slots > most) most = p.slots + p.late_slots;
+        }
     }
     return most / groups;
 }

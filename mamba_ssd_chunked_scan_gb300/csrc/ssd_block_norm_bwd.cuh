@@ -167,6 +167,22 @@ __device__ __forceinline__ void silu(Two z, Two& value, Two& slope) {
     slope = fma(s, fma(value, both(-1.f), both(1.f)), value);
 }
 
+// A slot's rows: place.row, place.row + place.step, ... before place.end, one group of each; and the row of shares that it leaves.
+struct Slot {
+    int group, row, end, step, share;
+};
+__device__ __forceinline__ Slot slot_of(const BlockNormBwdArgs& a, int id) {
+    const bool late = id >= a.slots;
+    const int k = late ? id - a.slots : id, line = k / a.groups;
+    Slot s;
+    s.group = k - line * a.groups;
+    s.row = late ? a.early_rows + line : line;
+    s.end = late ? (int)a.rows : a.early_rows;
+    s.step = (late ? a.late_slots : a.slots) / a.groups;
+    s.share = late ? a.slots / a.groups + line : line;
+    return s;
+}
+
 // LANES: lanes of a warp that take a row (a slot); 0: a CTA does, and where its rows lie is the same number for all of its
 // threads (uniform registers hold it).  XP: x (and gate) are codes; HP: h is.
 //
@@ -196,12 +212,14 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
     pdl_wait();
-    if (!kCta && id >= a.slots) return;
+    if (!kCta && id >= a.slots + a.late_slots) return;
     const int n = a.size;
-    const int line = id / a.groups, group = id - line * a.groups, first = group * n;   // the slot's first row, its group's first column
-    const int step = a.slots / a.groups;
+    const Slot place = slot_of(a, id);
+    const int group = place.group, first = group * n, step = place.step;   // the group's first column
+    const uint32_t line = place.row;                                       // the slot's first row
     const bool next = RES && a.dout;
-    const uint32_t units = (uint32_t)a.rows * a.groups, unit_step = (uint32_t)step * a.groups, unit0 = (uint32_t)line * a.groups + group;
+    const uint32_t units = (uint32_t)a.rows * a.groups, my_units = (uint32_t)place.end * a.groups, unit_step = (uint32_t)step * a.groups,
+                   unit0 = line * a.groups + group;
     const int shift = SHIFTED ? (int)((uint64_t)unit0 * n % V) : 0;
     const int e0 = tid * V - shift, span = nt * V;   // first column of the thread's vector 0; columns from one vector to the next
     // a warp's shared memory: its lanes' weights, then the stages
@@ -249,7 +267,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     auto ask_row = [&](auto which, int stage) {
         constexpr int kWhich = decltype(which)::value;
         constexpr bool kRest = kWhich != 1, kAskX = kWhich != 0;
-        if (unit_ask < units) {
+        if (unit_ask < my_units) {
             const uint32_t to = (uint32_t)__cvta_generic_to_shared(rec0) + stage * kStage;
             const int end = SHIFTED && unit_ask + 1 == units ? n : 1 << 24;   // the arrays end with the last row's last column
 #pragma unroll
@@ -293,7 +311,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         }
     for (int s = 0; s < (kEarly ? 1 : a.stages - 1); ++s) ask_row(Number<2>(), s);
     int stage = 0, turn = 0;
-    for (uint32_t unit = unit0; unit < units; unit += unit_step) {
+    for (uint32_t unit = unit0; unit < my_units; unit += unit_step) {
         unsigned char* const rec = rec0 + stage * kStage;
         if constexpr (!kEarly) {
             ask_row(Number<2>(), stage > 0 ? stage - 1 : a.stages - 1);   // where the row before lay
@@ -442,7 +460,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         if (!RES) q_out += far * sizeof(T);
     }
     const int width = n * a.groups, columns = RES && a.next_weight ? 2 * width : width;
-    float* share = a.shares + (int64_t)line * columns + first;
+    float* share = a.shares + (int64_t)place.share * columns + first;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int e = e0 + c * span;
@@ -526,10 +544,10 @@ __global__ void __launch_bounds__(loose_threads_sm(E)) ssd_block_norm_bwd_loose(
     const int id = blockIdx.x * a.slots_per_cta + slot;
     pdl_trigger();
     pdl_wait();
-    if (id >= a.slots) return;   // whole warps of a many-slot CTA, which has no barrier
+    if (id >= a.slots + a.late_slots) return;   // whole warps of a many-slot CTA, which has no barrier
     const int n = a.size;
-    const int line = id / a.groups, group = id - line * a.groups, first = group * n;
-    const int step = a.slots / a.groups;
+    const Slot place = slot_of(a, id);
+    const int group = place.group, first = group * n, step = place.step;
     const bool next = RES && a.dout;
     Two dw[C], dn[RES ? C : 1];
 #pragma unroll
@@ -542,7 +560,7 @@ __global__ void __launch_bounds__(loose_threads_sm(E)) ssd_block_norm_bwd_loose(
         return two(e < n ? __ldg(p + e) : 0.f, e + nt < n ? __ldg(p + e + nt) : 0.f);
     };
     int turn = 0;
-    for (uint32_t row = line; row < (uint32_t)a.rows; row += step) {
+    for (uint32_t row = place.row; row < (uint32_t)place.end; row += step) {
         const uint32_t unit = row * a.groups + group;
         const int64_t at = (int64_t)unit * n;
         Loose<T, E> dq;
@@ -630,7 +648,7 @@ __global__ void __launch_bounds__(loose_threads_sm(E)) ssd_block_norm_bwd_loose(
         }
     }
     const int width = n * a.groups, columns = RES && a.next_weight ? 2 * width : width;
-    float* share = a.shares + (int64_t)line * columns + first;
+    float* share = a.shares + (int64_t)place.share * columns + first;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -645,19 +663,33 @@ __global__ void __launch_bounds__(loose_threads_sm(E)) ssd_block_norm_bwd_loose(
 // How a call's rows are spread: a slot's lanes (0: a CTA), threads of a CTA, its slots, and all slots (a number of rows at a time, each
 // of its groups).
 struct RowPlan {
-    int elems, lanes, threads, slots_per_cta, slots, grid;
+    int elems, lanes, threads, slots_per_cta, slots, late_slots, early_rows, grid;
 };
 
 // Threads of a CTA that takes rows by itself, and CTAs that the registers of so many threads an SM hold.
 inline int row_threads(int span, int elems) { return ((span + elems - 1) / elems + 31) / 32 * 32; }
 inline int ctas_sm(int threads, int most) { return most / threads > 0 ? most / threads : 1; }
 
-inline void spread(RowPlan& p, int64_t rows, int groups, int per_sm) {
+constexpr int kLateRows = 16, kLatePart = 8;   // late slots from so many rows a slot on; the part of all rows that they take
+inline void spread(RowPlan& p, int64_t rows, int groups, int per_sm, bool may_late) {
     int64_t lines = (int64_t)kAddNormSMs * per_sm * p.slots_per_cta / groups / 8 * 8;
     if (lines < 8) lines = 8;
     if (lines > rows) lines = rows;
     p.slots = (int)lines * groups;
-    p.grid = (p.slots + p.slots_per_cta - 1) / p.slots_per_cta;
+    // SMs are not equally fast at memory (a fixed share of 3 operands read and 2 written each took 135 us where CTAs that
+    // start as others end took 122).  So the last rows may be left to as many slots again, which start on whichever SMs are done.
+    const bool late = may_late && rows >= kLateRows * lines;
+    p.late_slots = late ? p.slots : 0;
+    p.early_rows = (int)(late ? rows - rows / kLatePart : rows);
+    p.grid = (p.slots + p.late_slots + p.slots_per_cta - 1) / p.slots_per_cta;
+}
+
+inline int set_slots(BlockNormBwdArgs& a, const RowPlan& p) {   // and how many rows of shares there will be
+    a.slots = p.slots;
+    a.late_slots = p.late_slots;
+    a.early_rows = p.early_rows;
+    a.slots_per_cta = p.slots_per_cta;
+    return (p.slots + p.late_slots) / a.groups;
 }
 
 // Columns that the vectors of a row span: rows of other than whole vectors may reach into one more.
@@ -678,8 +710,8 @@ inline RowPlan loose_plan(int64_t rows, int size, int groups) {
     p.elems = size <= 512 * kNarrowElems ? kNarrowElems : kWideElems;
     p.threads = row_threads(size, p.elems);
     p.slots_per_cta = p.threads == 32 ? 4 : 1;
-    spread(p, rows, groups, ctas_sm(p.threads * p.slots_per_cta, loose_threads_sm(p.elems)));
-    if (p.slots < p.slots_per_cta) p.slots_per_cta = p.slots;
+    spread(p, rows, groups, ctas_sm(p.threads * p.slots_per_cta, loose_threads_sm(p.elems)), false);
+    if (p.slots < p.slots_per_cta) p.slots_per_cta = p.slots;   // no late ones then
     p.threads *= p.slots_per_cta;
     return p;
 }
@@ -708,10 +740,11 @@ cudaError_t launch_ring(BlockNormBwdArgs& a, RowPlan p, int* lines, cudaStream_t
     }
     if (a.stages < 1) return cudaErrorNotSupported;
     if (a.stages > (RES ? 1 : kMaxStages)) a.stages = RES ? 1 : kMaxStages;
-    spread(p, a.rows, a.groups, per_sm);
-    a.slots = p.slots;
-    a.slots_per_cta = p.slots_per_cta;
-    *lines = p.slots / a.groups;
+    // Late slots where HBM is the bound and the shares are those of one weight: bf16 gate and norm 16384 x 5120 153 us without,
+    // 140 with; 8192 x 80 groups of 64 81, 69; 16384 x 2048 63, 60.  From codes 124, 135; fp32 2048 columns 108, 112; one CTA an SM
+    // (8192 columns) 59, 68; with a residual 16384 x 2560 166, 170.
+    spread(p, a.rows, a.groups, per_sm, !RES && !XP && sizeof(T) == 2 && per_sm > 1);
+    *lines = set_slots(a, p);
     return launch_kernel(kern, (unsigned)p.grid, (unsigned)p.threads, (size_t)weights + (size_t)a.stages * stage, st, true, a);
 }
 
@@ -755,9 +788,7 @@ cudaError_t launch_block_norm_bwd_typed(BlockNormBwdArgs& a, int* lines, cudaStr
     }
     if (e != cudaErrorNotSupported) return e;   // not even one row's records fit an SM: the widest fp32 rows
     const RowPlan p = loose_plan(a.rows, a.size, a.groups);
-    a.slots = p.slots;
-    a.slots_per_cta = p.slots_per_cta;
-    *lines = p.slots / a.groups;
+    *lines = set_slots(a, p);
     return launch_kernel(p.elems == kNarrowElems ? ssd_block_norm_bwd_loose<T, R, kNarrowElems, GATE, RES>
                                                  : ssd_block_norm_bwd_loose<T, R, kWideElems, GATE, RES>,
                          (unsigned)p.grid, (unsigned)p.threads, 0, st, true, a);

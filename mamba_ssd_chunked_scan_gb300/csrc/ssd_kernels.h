@@ -233,7 +233,7 @@ struct BlockNormBwdArgs {
     float* dnext_weight;
     float* shares;         // [lines * width * weights]
     // set at the launch: the rows' slots, and their shared memory (weights, then stages of operands and scales)
-    int slots, slots_per_cta;
+    int slots, late_slots, early_rows, slots_per_cta;
     int stages;
     float inv_size;
 };

@@ -3,83 +3,106 @@
 //   ssd_unpack_kernel   what they stand for, in bf16 or fp32
 //
 // Both are bound by HBM: a unit (a row's group) stays in registers from its one read to its one write, since its
-// scale needs all of it; unpacking is element by element over the flat array.
+// scale needs all of it; unpacking goes by 16 elements of the flat array, whatever the rows' width.
 #include "ssd_kernels.h"
 #include "ssd_rows.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kElems = 16;   // elements of a unit per thread
-
-template <typename T, int V>
-__global__ void __launch_bounds__(1024) ssd_pack_kernel(PackArgs a) {
-    constexpr int C = kElems / V;
+template <typename T, int V, int E, int LANES, bool SHIFTED>
+__global__ void __launch_bounds__(1024) ssd_pack_kernel(const __grid_constant__ PackArgs a) {
     __shared__ uint32_t part[2][32];
-    const bool one_warp = a.units_per_cta > 1 || blockDim.x == 32;
-    const int slot = one_warp ? threadIdx.x >> 5 : 0;
-    const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x;
-    const int nt = one_warp ? 32 : blockDim.x;
-    const int64_t unit = (int64_t)blockIdx.x * a.units_per_cta + slot;
+    const int tid = LANES ? threadIdx.x % (LANES ? LANES : 32) : threadIdx.x, nt = LANES ? LANES : blockDim.x;
+    const int64_t unit = LANES ? (int64_t)blockIdx.x * a.units_per_cta + threadIdx.x / (LANES ? LANES : 32) : blockIdx.x;
     pdl_wait();
-    if (unit >= a.units) return;   // whole warps of a many-unit CTA, which has no barrier
-    const int64_t row = unit / a.groups;
+    if (unit >= a.units) return;   // all of a unit's lanes
     const int n = a.size;
-    const T* x = static_cast<const T*>(a.x) + row * a.stride + (unit - row * a.groups) * n;
-    e4m3_t* out = static_cast<e4m3_t*>(a.codes) + unit * n;
-    Raw<T, V> r[C];
-    uint32_t m = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int e = (tid + c * nt) * V;
-        r[c].zero();
-        if (e < n) r[c].load(x + e);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) m = max(m, magnitude(r[c]));
-    m = row_maximum(m, one_warp, part[0]);
+    const int64_t row = unit / a.groups, base = unit * n;
+    const Place<V, SHIFTED> place = {tid, nt, SHIFTED ? (int)(base % V) : 0, n, (a.units - unit) * n};
+    Part<T, V, E, SHIFTED> q;
+    q.load(static_cast<const T*>(a.x) + row * a.stride + (unit - row * a.groups) * n, place);
+    uint32_t m = row_maximum<LANES>(q.top(), part[0]);
     const bool bad = m >= kInfBits;   // the same in all of the unit's threads
-    if (bad) {
-        m = 0;
-#pragma unroll
-        for (int c = 0; c < C; ++c) m = max(m, finite_magnitude(r[c]));
-        m = row_maximum(m, one_warp, part[1]);
-    }
+    if (bad) m = row_maximum<LANES>(q.finite_top(), part[1]);
     const uint32_t scale = pack_scale_bits(m);
-    const float inv = pack_inverse(scale);
     if (tid == 0) a.scales[unit] = __uint_as_float(scale);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int e = (tid + c * nt) * V;
-        if (e < n) {
-            float v[V];
-            r[c].get(v);
-            to_codes(v, inv, bad);
-            Raw<e4m3_t, V> q;
-            q.set(v);
-            q.store(out + e);
-        }
+    for (int c = 0; c < E / V; ++c) {
+        Two v[V / 2];
+        q.get(c, v);
+        store_codes<V, E, SHIFTED>(static_cast<e4m3_t*>(a.codes) + base, place, c, v, pack_inverse(scale), bad);
     }
 }
 
-// One thread per V elements of the output, whose rows lie together; codes' rows are `stride` apart.
-template <typename T, int V>
-__global__ void __launch_bounds__(256) ssd_unpack_kernel(PackArgs a) {
+constexpr int kFlat = 16;   // elements per thread of the flat array
+
+// Where codes' rows lie together and both arrays start on 16 bytes: a thread takes 16 elements of the flat array, of one unit or of
+// several.  A CTA's first unit is divided out once, in 64 bits; the rest is in 32.
+template <typename T>
+__global__ void __launch_bounds__(256) ssd_unpack_kernel(const __grid_constant__ PackArgs a) {
     pdl_trigger();
     pdl_wait();
-    const int64_t per_row = ((int64_t)a.size * a.groups + V - 1) / V;
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = k / per_row;
-    if (row >= a.units / a.groups) return;
-    const int width = a.size * a.groups;
-    const int e = (int)(k - row * per_row) * V;
+    const int64_t total = a.units * a.size, begin = (int64_t)blockIdx.x * 256 * kFlat, at = begin + threadIdx.x * kFlat;
+    if (at >= total) return;
+    const int64_t unit0 = begin / a.size;
+    const uint32_t n = a.size, k = (uint32_t)(begin - unit0 * a.size) + threadIdx.x * kFlat, over = k / n;
+    uint32_t e = k - over * n;   // the first element's column in its unit
+    const float* scales = a.scales + unit0 + over;
+    const e4m3_t* codes = static_cast<const e4m3_t*>(a.codes) + at;
+    T* out = static_cast<T*>(a.out) + at;
+    const int count = total - at < kFlat ? (int)(total - at) : kFlat;
+    Raw<e4m3_t, kFlat> q;
+    q.zero();
+    if (count == kFlat) q.load(codes);
+    else q.load_some(codes, count);
+    Two v[kFlat / 2];
+    to_pairs(q, v);
+    float s = __ldg(scales);
+    if (e + kFlat <= n) {
+#pragma unroll
+        for (int j = 0; j < kFlat / 2; ++j) v[j] = v[j] * both(s);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kFlat; ++j) {
+            if (e == n && j < count) {
+                e = 0;
+                s = __ldg(++scales);
+            }
+            ++e;
+            if (j % 2) v[j / 2] = two(low(v[j / 2]), high(v[j / 2]) * s);
+            else v[j / 2] = two(low(v[j / 2]) * s, high(v[j / 2]));
+        }
+    }
+    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int h = 0; h < kFlat / V; ++h) {
+        Two p[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) p[j] = v[h * (V / 2) + j];
+        Raw<T, V> o;
+        from_pairs(p, o);
+        if (h * V + V <= count) o.store(out + h * V);
+        else o.store_within(out, h * V, count);
+    }
+}
+
+// Any alignment, and codes whose rows are `stride` apart: V elements of an output row per thread.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) ssd_unpack_rows_kernel(const __grid_constant__ PackArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int width = a.size * a.groups, per_row = (width + 256 * V - 1) / (256 * V);   // CTAs of a row
+    const int64_t row = blockIdx.x / per_row;
+    const int e = ((int)(blockIdx.x - row * per_row) * 256 + (int)threadIdx.x) * V;
+    if (e >= width) return;
     Raw<e4m3_t, V> q;
     q.load(static_cast<const e4m3_t*>(a.codes) + row * a.stride + e);
     float v[V];
     from_codes(q, v);
     const float* s = a.scales + row * a.groups;
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= __ldg(s + (e + j) / a.size);
+    for (int j = 0; j < V; ++j) v[j] *= __ldg(s + (a.groups == 1 ? 0 : (e + j) / a.size));
     Raw<T, V> o;
     o.set(v);
     o.store(static_cast<T*>(a.out) + row * width + e);
@@ -87,28 +110,41 @@ __global__ void __launch_bounds__(256) ssd_unpack_kernel(PackArgs a) {
 
 bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+template <typename T, int V, bool SHIFTED>
+cudaError_t launch_pack_shape(PackArgs& a, cudaStream_t st) {
+    const int span = SHIFTED ? a.size + V - 1 : a.size;   // columns that the vectors of a unit may span
+    auto go = [&](auto kern, int lanes, int threads) {
+        a.units_per_cta = lanes ? threads / lanes : 1;
+        const unsigned grid = (unsigned)((a.units + a.units_per_cta - 1) / a.units_per_cta);
+        return launch_kernel(kern, grid, (unsigned)threads, 0, st, true, a);
+    };
+    if (span <= 64) return go(ssd_pack_kernel<T, V, 8, 8, SHIFTED>, 8, 128);
+    if (span <= 128) return go(ssd_pack_kernel<T, V, 8, 16, SHIFTED>, 16, 128);
+    if (span <= 256) return go(ssd_pack_kernel<T, V, 8, 32, SHIFTED>, 32, 128);
+    return go(ssd_pack_kernel<T, V, 16, 0, SHIFTED>, 0, ((span + 15) / 16 + 31) / 32 * 32);
+}
+
+// Vectors where both arrays start on 16 bytes (codes on a vector's) and units hold one at least, single elements otherwise.
 template <typename T>
 cudaError_t launch_pack_typed(PackArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.size % V == 0 && a.stride % V == 0 && on16(a.x) && ((uintptr_t)a.codes % V) == 0;
-    int threads;
-    if (a.size <= 32 * kElems) {
-        a.units_per_cta = a.units < 4 ? (int)a.units : 4;
-        threads = 32 * a.units_per_cta;
-    } else {
-        a.units_per_cta = 1;
-        threads = ((a.size + kElems - 1) / kElems + 31) / 32 * 32;
-    }
-    const unsigned grid = (unsigned)((a.units + a.units_per_cta - 1) / a.units_per_cta);
-    return launch_kernel(vec ? ssd_pack_kernel<T, V> : ssd_pack_kernel<T, 1>, grid, (unsigned)threads, 0, st, true, a);
+    const bool shifted = a.size % V != 0;
+    const bool vectors = a.size >= V && (!shifted || a.size + V - 1 <= 1024 * 16) && on16(a.x) && ((uintptr_t)a.codes % V) == 0 &&
+                         (shifted ? a.stride == (int64_t)a.size * a.groups : a.stride % V == 0);
+    if (!vectors) return launch_pack_shape<T, 2, false>(a, st);
+    return shifted ? launch_pack_shape<T, V, true>(a, st) : launch_pack_shape<T, V, false>(a, st);
 }
 
 template <typename T>
 cudaError_t launch_unpack_typed(const PackArgs& a, cudaStream_t st) {
     const int64_t width = (int64_t)a.size * a.groups, rows = a.units / a.groups;
+    if (a.stride == width && on16(a.codes) && on16(a.out) && a.size < 1 << 30) {
+        const int64_t ctas = (rows * width + 256 * kFlat - 1) / (256 * kFlat);
+        return launch_kernel(ssd_unpack_kernel<T>, (unsigned)ctas, 256, 0, st, true, a);
+    }
     const bool vec = width % 8 == 0 && a.stride % 8 == 0 && on16(a.out) && ((uintptr_t)a.codes % 8) == 0;
-    const int64_t threads = rows * (vec ? width / 8 : width);
-    return launch_kernel(vec ? ssd_unpack_kernel<T, 8> : ssd_unpack_kernel<T, 1>, (unsigned)((threads + 255) / 256), 256, 0, st, true, a);
+    const int64_t ctas = rows * ((width + 256 * (vec ? 8 : 1) - 1) / (256 * (vec ? 8 : 1)));
+    return launch_kernel(vec ? ssd_unpack_rows_kernel<T, 8> : ssd_unpack_rows_kernel<T, 1>, (unsigned)ctas, 256, 0, st, true, a);
 }
 
 }  // namespace

@@ -55,14 +55,9 @@ __device__ __forceinline__ uint32_t finite_magnitude(const Raw<T, V>& r) {
     return m;
 }
 
-// V elements as codes; `bad`: some element of the row is infinite or NaN.
-template <int V>
-__device__ __forceinline__ void to_codes(float (&v)[V], float inv, bool bad) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        if (bad && (__float_as_uint(v[k]) & 0x7fffffffu) >= kInfBits) v[k] = __uint_as_float(0x7fffffffu);
-        v[k] *= inv;
-    }
+// NaN in place of an infinity or a NaN.
+__device__ __forceinline__ float nan_unless_finite(float v) {
+    return (__float_as_uint(v) & 0x7fffffffu) >= kInfBits ? __uint_as_float(0x7fffffffu) : v;
 }
 
 // V codes as fp32 numbers (exact).
@@ -143,13 +138,13 @@ __device__ __forceinline__ float rsqrt_of(float x) {
     return r;
 }
 
-// One or two sums over the threads of a row: a warp, or the CTA of up to 20 warps (every thread of it calls, and adds the warps'
+// One or two sums over the threads of a row: a warp, or the CTA of up to 32 warps (every thread of it calls, and adds the warps'
 // sums for itself, in one order).  Two sums share their shuffles: at the first a lane passes on the one that it does not
 // keep.  Calls in a row alternate between two arrays: whoever writes one again is past a barrier that its readers reached
 // after reading.
 struct RowPart {
-    __align__(16) float sums[40];
-    uint2 maxima[20];
+    __align__(16) float sums[64];
+    uint2 maxima[32];
 };
 // A warp's sums (of two, the second in lanes 16 to 31), and the CTA's from the warps'.
 template <int N>
@@ -223,33 +218,48 @@ __device__ __forceinline__ void lane_sums(float (&s)[2]) {
     s[1] = __shfl_sync(mask, v, LANES / 2, LANES);
 }
 
-// A sum (the same as row_sums') and two maxima, by one barrier.
+// A sum and two maxima over the threads of a row: LANES lanes of a warp, or (0) the CTA, by one barrier.
 struct RowMaxima {
     uint32_t a, b;
 };
-__device__ __forceinline__ void row_sum_maxima(float (&s)[1], RowMaxima& m, bool one_warp, RowPart& part) {
-    const float v = warp_sums(s);
-    m.a = __reduce_max_sync(0xffffffffu, m.a);
-    m.b = __reduce_max_sync(0xffffffffu, m.b);
-    s[0] = v;
-    if (one_warp) return;
-    const int lane = threadIdx.x & 31;
-    leave_sums<1>(v, part);
-    if (lane == 0) part.maxima[threadIdx.x >> 5] = make_uint2(m.a, m.b);
-    __syncthreads();
-    join_sums(s, part);
-    const uint2 q = lane < (int)(blockDim.x >> 5) ? part.maxima[lane] : make_uint2(0, 0);
-    m.a = __reduce_max_sync(0xffffffffu, q.x);
-    m.b = __reduce_max_sync(0xffffffffu, q.y);
+template <int LANES>
+__device__ __forceinline__ void row_sum(float (&s)[1], RowPart& part) {
+    if constexpr (LANES == 0) {
+        row_sums(s, false, part);
+    } else {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) s[0] += __shfl_xor_sync(row_mask<LANES>(), s[0], o);
+    }
 }
-// A maximum over the threads of a row of up to 32 warps.
-__device__ __forceinline__ uint32_t row_maximum(uint32_t m, bool one_warp, uint32_t (&part)[32]) {
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (one_warp) return m;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) part[threadIdx.x >> 5] = m;
-    __syncthreads();
-    return __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
+template <int LANES>
+__device__ __forceinline__ uint32_t row_maximum(uint32_t m, uint32_t (&part)[32]) {
+    m = __reduce_max_sync(row_mask<LANES>(), m);
+    if constexpr (LANES == 0) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();
+        m = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? part[lane] : 0u);
+    }
+    return m;
+}
+// The sum is the same as row_sum's.
+template <int LANES>
+__device__ __forceinline__ void row_sum_maxima(float (&s)[1], RowMaxima& m, RowPart& part) {
+    m.a = __reduce_max_sync(row_mask<LANES>(), m.a);
+    m.b = __reduce_max_sync(row_mask<LANES>(), m.b);
+    if constexpr (LANES != 0) {
+        row_sum<LANES>(s, part);
+    } else {
+        const float v = warp_sums(s);
+        const int lane = threadIdx.x & 31;
+        leave_sums<1>(v, part);
+        if (lane == 0) part.maxima[threadIdx.x >> 5] = make_uint2(m.a, m.b);
+        __syncthreads();
+        join_sums(s, part);
+        const uint2 q = lane < (int)(blockDim.x >> 5) ? part.maxima[lane] : make_uint2(0, 0);
+        m.a = __reduce_max_sync(0xffffffffu, q.x);
+        m.b = __reduce_max_sync(0xffffffffu, q.y);
+    }
 }
 
 // 1 / (1 + e^-z).  bf16 inputs: ex2.approx and rcp.approx, a few 2^-23 each, far inside the inputs' rounding; fp32 inputs:
@@ -279,6 +289,122 @@ __device__ __forceinline__ Two sigmoid(Two z) {
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(low(q)));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(high(q)));
         return two(e, f);
+    }
+}
+
+// A thread's part of a row, E elements: vectors of V (16 bytes of the row's type), vector c from column column(c) on; or (V = 2)
+// pairs of single elements, columns e and e + nt, whatever the alignment.  SHIFTED: see ssd_block_norm_bwd.cuh; `left`: columns to the
+// arrays' end from the row's start.
+template <int V, bool SHIFTED>
+struct Place {
+    int tid, nt, shift, n;
+    int64_t left;
+    __device__ __forceinline__ int column(int c) const { return V > 2 ? (tid + c * nt) * V - shift : tid + 2 * c * nt; }
+};
+template <typename K, int V, int E, bool SHIFTED>
+struct Part {
+    static constexpr int kEach = V > 2 ? V : 1, C = E / V;
+    Raw<K, kEach> q[E / kEach];
+    // `row`: the row's column 0
+    __device__ __forceinline__ void load(const K* row, const Place<V, SHIFTED>& p) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = p.column(c);
+            if constexpr (V > 2) {
+                q[c].zero();
+                if (e < p.n) {
+                    if (!SHIFTED || e + V <= p.left) q[c].load(row + e);
+                    else q[c].load_some(row + e, (int)(p.left - e));
+                    if (SHIFTED && (e < 0 || e + V > p.n)) {   // a neighbour's elements
+                        K* v = reinterpret_cast<K*>(&q[c].w);
+                        Raw<K, 1> none;
+                        none.zero();
+#pragma unroll
+                        for (int k = 0; k < V; ++k)
+                            if (e + k < 0 || e + k >= p.n) v[k] = *reinterpret_cast<K*>(&none.w);
+                    }
+                }
+            } else {
+                q[2 * c].zero();
+                q[2 * c + 1].zero();
+                if (e < p.n) q[2 * c].load(row + e);
+                if (e + p.nt < p.n) q[2 * c + 1].load(row + e + p.nt);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(K* row, const Place<V, SHIFTED>& p, int c) const {
+        const int e = p.column(c);
+        if constexpr (V > 2) {
+            if (SHIFTED && (e < 0 || e + V > p.n)) q[c].store_within(row, e, p.n);
+            else if (e < p.n) q[c].store(row + e);
+        } else {
+            if (e < p.n) q[2 * c].store(row + e);
+            if (e + p.nt < p.n) q[2 * c + 1].store(row + e + p.nt);
+        }
+    }
+    __device__ __forceinline__ void get(int c, Two (&v)[V / 2]) const {
+        if constexpr (V > 2) {
+            to_pairs(q[c], v);
+        } else {
+            float f[1], g[1];
+            q[2 * c].get(f);
+            q[2 * c + 1].get(g);
+            v[0] = two(f[0], g[0]);
+        }
+    }
+    __device__ __forceinline__ void set(int c, const Two (&v)[V / 2]) {
+        if constexpr (V > 2) {
+            from_pairs(v, q[c]);
+        } else {
+            const float f[1] = {low(v[0])}, g[1] = {high(v[0])};
+            q[2 * c].set(f);
+            q[2 * c + 1].set(g);
+        }
+    }
+    // largest magnitude; and over finite elements alone
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < E / kEach; ++c) m = max(m, magnitude(q[c]));
+        return m;
+    }
+    __device__ __forceinline__ uint32_t finite_top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < E / kEach; ++c) m = max(m, finite_magnitude(q[c]));
+        return m;
+    }
+};
+// Vector c of a row times `inv` as codes; `bad`: some element of the row is infinite or NaN.
+template <int V, int E, bool SHIFTED>
+__device__ __forceinline__ void store_codes(e4m3_t* row, const Place<V, SHIFTED>& p, int c, Two (&v)[V / 2], float inv, bool bad) {
+    if (bad) {
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) v[k] = two(nan_unless_finite(low(v[k])), nan_unless_finite(high(v[k])));
+    }
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) v[k] = v[k] * both(inv);
+    Part<e4m3_t, V, E, SHIFTED> q;
+    q.set(c, v);
+    q.store(row, p, c);
+}
+// Vector c of a row's weights, kept in the caches (16-byte aligned with it where V > 2 and !SHIFTED); 0 outside of the row.
+template <int V, bool SHIFTED>
+__device__ __forceinline__ void weights_of(const float* p, const Place<V, SHIFTED>& at, int c, Two (&w)[V / 2]) {
+    const int e = at.column(c);
+    if constexpr (V == 2) {
+        w[0] = two(e < at.n ? __ldg(p + e) : 0.f, e + at.nt < at.n ? __ldg(p + e + at.nt) : 0.f);
+    } else if constexpr (SHIFTED) {
+#pragma unroll
+        for (int k = 0; k < V; k += 2)
+            w[k / 2] = two(e + k >= 0 && e + k < at.n ? __ldg(p + e + k) : 0.f, e + k + 1 >= 0 && e + k + 1 < at.n ? __ldg(p + e + k + 1) : 0.f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+            const float4 q = e < at.n ? __ldg(reinterpret_cast<const float4*>(p + e + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[k / 2] = two(q.x, q.y);
+            w[k / 2 + 1] = two(q.z, q.w);
+        }
     }
 }
 
