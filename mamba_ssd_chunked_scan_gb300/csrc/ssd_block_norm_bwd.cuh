@@ -4,38 +4,16 @@
 #include <atomic>
 
 #include "ssd_kernels.h"
-#include "ssd_rows.cuh"
+#include "ssd_ring.cuh"
 
 namespace ssd {
 
-constexpr int kWideElems = 16, kNarrowElems = 8;   // elements of a row per thread
 constexpr int kMaxStages = 4;
-constexpr int kSmemSM = 228 * 1024, kSmemCta = 227 * 1024;
-constexpr int kSmemOwn = 2048;                     // a CTA's static shared memory and what the system takes
 
 // Threads per SM that the registers of E elements a thread allow.
 constexpr int threads_sm(int elems, bool res) { return elems == kNarrowElems || !res ? 640 : 512; }
 
 constexpr int loose_threads_sm(int elems) { return elems == kNarrowElems ? 640 : 512; }   // where no vectors fit
-
-// Copies of 16, 8 or 4 bytes, of which the first `n` are read and the others 0.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int n) {
-    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Until at most the newest `n` groups of copies are under way.
-__device__ __forceinline__ void copies_wait(int n) {
-    if (n == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-template <int N> struct Number { static constexpr int value = N; };
-template <bool, typename A, typename B> struct Pick { typedef A type; };
-template <typename A, typename B> struct Pick<false, A, B> { typedef B type; };
 
 // A warp's record of one row: its lanes' vectors of each operand, piece by piece (16 bytes a lane, then codes, then scales), so that
 // whole lines arrive in one place and every offset is a constant (records of a thread each, 112 bytes apart, took the copies from 5.5
@@ -56,108 +34,6 @@ struct Record {
     static constexpr int bytes = h_scale + (RES && HP ? 4 : 0);
     static constexpr int weight = E * 4, weights = (RES ? 2 : 1) * weight;   // the weights' record
 };
-
-// Where the 16-byte half `k` of a lane's vector c of type K lies, or all of it where K is shorter, from an operand's first piece on.
-// Vectors of 32 bytes (fp32 beside bf16) are copied by pairs of lanes, 32 adjacent bytes at a time: a lane that took its own two
-// halves would ask for each 32-byte sector twice (588 MB of operands, half of them so, took 148 us).  The order of their places
-// keeps both the copies and the reads off each other's banks.
-template <typename K, int V>
-__device__ __forceinline__ int piece(int c, int k, int lane) {
-    constexpr int kBytes = (int)sizeof(K) * V;
-    if constexpr (kBytes == 32) return (c * 2 + (lane & 1)) * 512 + (((lane & 30) | k) ^ (lane & 1)) * 16;
-    else return (c * 32 + lane) * kBytes;
-}
-
-// One vector (number c of the lane's) of an operand, whose pieces start at `at`.
-template <typename K, int V>
-__device__ __forceinline__ Raw<K, V> piece_vector(const unsigned char* at, int c, int lane) {
-    Raw<K, V> q;
-    if constexpr (sizeof(K) * V == 32) {
-        q.w.lo = *reinterpret_cast<const uint4*>(at + piece<K, V>(c, 0, lane));
-        q.w.hi = *reinterpret_cast<const uint4*>(at + piece<K, V>(c, 1, lane));
-    } else {
-        q.w = *reinterpret_cast<const typename Raw<K, V>::W*>(at + piece<K, V>(c, 0, lane));
-    }
-    return q;
-}
-// It as pairs: codes times s.
-template <typename K, int V>
-__device__ __forceinline__ void widen(const Raw<K, V>& q, Two s, Two (&v)[V / 2]) {
-    to_pairs(q, v);
-    if constexpr (sizeof(K) == 1) {
-#pragma unroll
-        for (int k = 0; k < V / 2; ++k) v[k] = v[k] * s;
-    }
-}
-
-// Ask for the elements of vector c (from column e, `off` bytes from p) that lie before column `end`, into its pieces: those of one lane
-// each for itself, 32-byte ones with the neighbouring lane.  A vector past the row's n columns is left alone.
-template <typename K, int V, bool SHIFTED>
-__device__ __forceinline__ void ask(uint32_t to, int c, int lane, const unsigned char* p, uint32_t off, int e, int n, int end) {
-    constexpr int kBytes = (int)sizeof(K) * V;
-    if constexpr (kBytes == 32) {
-        const int k = lane & 1;
-        const unsigned char* pair = p + (off - 32 * k);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int eo = e + (h - k) * V;   // the vector of the pair's lane h
-            if (eo >= n) continue;
-            const int bytes = SHIFTED ? max(0, min(16, (end - eo - k * V / 2) * (int)sizeof(K))) : 16;
-            copy_async<16>(to + piece<K, V>(c, k, (lane & 30) | h), pair + (SHIFTED && bytes == 0 ? 0 : 32 * h + 16 * k), bytes);
-        }
-    } else {
-        if (e >= n) return;
-        const int bytes = SHIFTED ? min(kBytes, (end - e) * (int)sizeof(K)) : kBytes;
-        copy_async<kBytes>(to + piece<K, V>(c, 0, lane), p + off, bytes);
-    }
-}
-
-// 0 in the elements of a vector that lie outside of a row's columns [0, n); the vector starts at column e.
-template <typename K, int V>
-__device__ __forceinline__ void clear_outside(unsigned char* at, int c, int lane, int e, int n) {
-    constexpr int kBytes = (int)sizeof(K) * V, kEach = kBytes > 16 ? 16 / (int)sizeof(K) : V;   // elements of a piece
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-        if (e + k < 0 || e + k >= n)
-            reinterpret_cast<typename Word<(int)sizeof(K)>::type*>(at + piece<K, V>(c, k / kEach, lane))[k % kEach] = 0;
-}
-
-// Store the elements of a vector (from column e, `off` bytes from `row`) that lie in a row's columns [0, n); 32-byte vectors with the
-// neighbouring lane, as they are copied (all lanes of `mask` call).
-template <typename K, int V, bool SHIFTED>
-__device__ __forceinline__ void put(unsigned char* row, uint32_t off, int e, int n, uint32_t mask, const Two (&v)[V / 2]) {
-    Raw<K, V> q;
-    from_pairs(v, q);
-    if constexpr ((int)sizeof(K) * V == 32) {
-        const int k = threadIdx.x & 1;
-        uint4 keep = k ? q.w.hi : q.w.lo, give = k ? q.w.lo : q.w.hi;
-        give.x = __shfl_xor_sync(mask, give.x, 1);
-        give.y = __shfl_xor_sync(mask, give.y, 1);
-        give.z = __shfl_xor_sync(mask, give.z, 1);
-        give.w = __shfl_xor_sync(mask, give.w, 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int eo = e + (h - k) * V + k * (V / 2);   // the first column of the half
-            Raw<K, V / 2> r;
-            r.w = h == k ? keep : give;
-            K* p = reinterpret_cast<K*>(row + (off - 32 * k + 32 * h + 16 * k));
-            if constexpr (SHIFTED) {
-                if (eo >= 0 && eo + V / 2 <= n) r.store(p);
-                else r.store_within(p - eo, eo, n);
-            } else {
-                if (eo < n) r.store(p);
-            }
-        }
-    } else {
-        K* p = reinterpret_cast<K*>(row + off);
-        if constexpr (SHIFTED) {
-            if (e >= 0 && e + V <= n) q.store(p);
-            else q.store_within(p - e, e, n);
-        } else {
-            if (e < n) q.store(p);
-        }
-    }
-}
 
 // silu(z) and its slope s + z s (1 - s) = s (1 - silu) + silu.
 template <typename T>
@@ -184,12 +60,7 @@ __device__ __forceinline__ Slot slot_of(const BlockNormBwdArgs& a, int id) {
 }
 
 // LANES: lanes of a warp that take a row (a slot); 0: a CTA does, and where its rows lie is the same number for all of its
-// threads (uniform registers hold it).  XP: x (and gate) are codes; HP: h is.
-//
-// SHIFTED: rows of n elements, n not a multiple of V.  Vectors lie on V-element boundaries of the whole array: a row starts `shift`
-// elements into its first one.  Those at its ends hold a neighbour's elements too, which are read with them (and cleared)
-// and never written.  A slot's rows are a multiple of 8 apart (or it has one): their shift is one number, and a thread's
-// columns stay its own for the weights' gradients.
+// threads (uniform registers hold it).  XP: x (and gate) are codes; HP: h is.  SHIFTED: see ssd_ring.cuh.
 template <typename T, typename R, int E, int LANES, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
 __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(const __grid_constant__ BlockNormBwdArgs a) {
     typedef Record<T, R, E, GATE, RES, XP, HP> Rec;
@@ -218,7 +89,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     const int group = place.group, first = group * n, step = place.step;   // the group's first column
     const uint32_t line = place.row;                                       // the slot's first row
     const bool next = RES && a.dout;
-    const uint32_t units = (uint32_t)a.rows * a.groups, my_units = (uint32_t)place.end * a.groups, unit_step = (uint32_t)step * a.groups,
+    const uint32_t my_units = (uint32_t)place.end * a.groups, unit_step = (uint32_t)step * a.groups,
                    unit0 = line * a.groups + group;
     const int shift = SHIFTED ? (int)((uint64_t)unit0 * n % V) : 0;
     const int e0 = tid * V - shift, span = nt * V;   // first column of the thread's vector 0; columns from one vector to the next
@@ -242,11 +113,11 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         if (e >= n) {
             for (int s = 0; s < a.stages; ++s) {
                 unsigned char* r = rec0 + s * kStage;
-                clear_outside<T, V>(r + kD, c, lane, e, n);
-                clear_outside<X, V>(r + kX, c, lane, e, n);
-                if (GATE) clear_outside<X, V>(r + kZ, c, lane, e, n);
-                if (RES) clear_outside<H, V>(r + kH, c, lane, e, n);
-                if (RES) clear_outside<R, V>(r + kR, c, lane, e, n);
+                clear_head<T, V>(r + kD, c, lane, V);
+                clear_head<X, V>(r + kX, c, lane, V);
+                if (GATE) clear_head<X, V>(r + kZ, c, lane, V);
+                if (RES) clear_head<H, V>(r + kH, c, lane, V);
+                if (RES) clear_head<R, V>(r + kR, c, lane, V);
             }
         }
     }
@@ -269,17 +140,16 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         constexpr bool kRest = kWhich != 1, kAskX = kWhich != 0;
         if (unit_ask < my_units) {
             const uint32_t to = (uint32_t)__cvta_generic_to_shared(rec0) + stage * kStage;
-            const int end = SHIFTED && unit_ask + 1 == units ? n : 1 << 24;   // the arrays end with the last row's last column
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int e = e0 + c * span;
                 const uint32_t t = (uint32_t)tid * V;
                 const int64_t s = c * span;
-                if (kRest && (!RES || next)) ask<T, V, SHIFTED>(to + kD, c, lane, p_dout + s * sizeof(T), t * sizeof(T), e, n, end);
-                if (kRest && next) ask<H, V, SHIFTED>(to + kH, c, lane, p_h + s * sizeof(H), t * sizeof(H), e, n, end);
-                if (kRest && RES) ask<R, V, SHIFTED>(to + kR, c, lane, p_dres + s * sizeof(R), t * sizeof(R), e, n, end);
-                if (kRest && GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, p_gate + s * sizeof(X), t * sizeof(X), e, n, end);
-                if (kAskX) ask<X, V, SHIFTED>(to + kX, c, lane, p_x + s * sizeof(X), t * sizeof(X), e, n, end);
+                if (kRest && (!RES || next)) ask<T, V, SHIFTED>(to + kD, c, lane, p_dout + s * sizeof(T), t * sizeof(T), e, n);
+                if (kRest && next) ask<H, V, SHIFTED>(to + kH, c, lane, p_h + s * sizeof(H), t * sizeof(H), e, n);
+                if (kRest && RES) ask<R, V, SHIFTED>(to + kR, c, lane, p_dres + s * sizeof(R), t * sizeof(R), e, n);
+                if (kRest && GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, p_gate + s * sizeof(X), t * sizeof(X), e, n);
+                if (kAskX) ask<X, V, SHIFTED>(to + kX, c, lane, p_x + s * sizeof(X), t * sizeof(X), e, n);
             }
             if (kRest) {
                 if (XP) copy_async<4>(to + 32 * Rec::x_scale + 4 * lane, a.x_scales + unit_ask, 4);
@@ -319,18 +189,12 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         }
         copies_wait(kEarly ? 0 : a.stages - 1);
         if constexpr (kPairs) __syncwarp(mask);
-        if constexpr (SHIFTED) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int e = e0 + c * span;
-                if (e < n && (e < 0 || e + V > n)) {
-                    if (!RES || next) clear_outside<T, V>(rec + kD, c, lane, e, n);
-                    clear_outside<X, V>(rec + kX, c, lane, e, n);
-                    if (GATE) clear_outside<X, V>(rec + kZ, c, lane, e, n);
-                    if (next) clear_outside<H, V>(rec + kH, c, lane, e, n);
-                    if (RES) clear_outside<R, V>(rec + kR, c, lane, e, n);
-                }
-            }
+        if (SHIFTED && e0 < 0) {
+            if (!RES || next) clear_head<T, V>(rec + kD, 0, lane, shift);
+            clear_head<X, V>(rec + kX, 0, lane, shift);
+            if (GATE) clear_head<X, V>(rec + kZ, 0, lane, shift);
+            if (next) clear_head<H, V>(rec + kH, 0, lane, shift);
+            if (RES) clear_head<R, V>(rec + kR, 0, lane, shift);
         }
         Two xs = both(0.f), gs = xs, hs = xs;
         if (XP) xs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::x_scale + 4 * lane));
@@ -691,9 +555,6 @@ inline int set_slots(BlockNormBwdArgs& a, const RowPlan& p) {   // and how many 
     a.slots_per_cta = p.slots_per_cta;
     return (p.slots + p.late_slots) / a.groups;
 }
-
-// Columns that the vectors of a row span: rows of other than whole vectors may reach into one more.
-inline int vector_span(int size) { return size % 8 == 0 ? size : size + 7; }
 
 // Rows of up to 256 columns take 8, 16 or 32 lanes of a warp, others a CTA: 8 elements a thread while that makes at most 160 threads,
 // then 16.

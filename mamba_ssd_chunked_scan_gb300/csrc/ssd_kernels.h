@@ -206,7 +206,9 @@ struct BlockNormArgs {
     float* x_scales;
     void* gate_codes;
     float* gate_scales;
-    int units_per_cta;     // set at the launch
+    // set at the launch: slots (a number of rows at a time, each of its groups), those of a CTA, rows on their way in shared memory
+    uint32_t slots;
+    int units_per_cta, stages;
     float inv_size;
 };
 struct BlockNormBwdArgs {

@@ -14,14 +14,15 @@ template <typename T, int V, int E, int LANES, bool SHIFTED>
 __global__ void __launch_bounds__(1024) ssd_pack_kernel(const __grid_constant__ PackArgs a) {
     __shared__ uint32_t part[2][32];
     const int tid = LANES ? threadIdx.x % (LANES ? LANES : 32) : threadIdx.x, nt = LANES ? LANES : blockDim.x;
-    const int64_t unit = LANES ? (int64_t)blockIdx.x * a.units_per_cta + threadIdx.x / (LANES ? LANES : 32) : blockIdx.x;
+    const uint32_t unit = LANES ? blockIdx.x * a.units_per_cta + threadIdx.x / (LANES ? LANES : 32) : blockIdx.x;
     pdl_wait();
     if (unit >= a.units) return;   // all of a unit's lanes
     const int n = a.size;
-    const int64_t row = unit / a.groups, base = unit * n;
-    const Place<V, SHIFTED> place = {tid, nt, SHIFTED ? (int)(base % V) : 0, n, (a.units - unit) * n};
+    const uint32_t row = a.groups == 1 ? unit : unit / (uint32_t)a.groups;
+    const int64_t base = (int64_t)unit * n;
+    const Place<V, SHIFTED> place = {tid, nt, SHIFTED ? (int)(base & (V - 1)) : 0, n, (a.units - unit) * n};
     Part<T, V, E, SHIFTED> q;
-    q.load(static_cast<const T*>(a.x) + row * a.stride + (unit - row * a.groups) * n, place);
+    q.load(static_cast<const T*>(a.x) + row * a.stride + (int64_t)(unit - row * a.groups) * n, place);
     uint32_t m = row_maximum<LANES>(q.top(), part[0]);
     const bool bad = m >= kInfBits;   // the same in all of the unit's threads
     if (bad) m = row_maximum<LANES>(q.finite_top(), part[1]);

@@ -19,22 +19,18 @@ from .layer import (_BF16, _CODE, _E4M3, _F32, _check, _current_device, _device,
 
 def _rows_of(name, t, dtype, shape, dev):
     """Elements between the rows of a (..., width) tensor, contiguous or a column range of a wider matrix."""
-    _typed(name, t, dtype, shape, dev)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return shape[-1] if t.is_contiguous() else _row_stride(name, t)
 
 
-def _typed(name, t, dtype, shape, dev):
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _packed(name, t, scales, scales_shape, dtype, shape, dev):
-    """Check an input that may be 8-bit rows; its row stride."""
+def _kept(name, t, scales, scales_shape, dtype, shape, dev):
+    """Check a contiguous input that may be 8-bit rows."""
     if scales is None:
-        return _rows_of(name, t, dtype, shape, dev)
-    _need(name, t, _E4M3, shape, dev)
-    _need(name + "_scales", scales, _F32, scales_shape, dev)
-    return shape[-1]
+        _need(name, t, dtype, shape, dev)
+    else:
+        _need(name, t, _E4M3, shape, dev)
+        _need(name + "_scales", scales, _F32, scales_shape, dev)
 
 
 def _groups(name, width, group_size):
@@ -140,10 +136,12 @@ def gate_norm_bwd(dout, y, z, weight, group_size, eps=1e-5, *, y_scales=None, z_
     groups = _groups("group_size", width, group_size)
     _need("dout", dout, dtype, shape, dev)
     per = (*shape[:-1], groups)
-    _packed("y", y, y_scales, per, dtype, shape, dev)
-    if not y.is_contiguous():
-        _need("y", y, dtype, shape, dev)
-    zs = _packed("z", z, z_scales, per, dtype, shape, dev)
+    _kept("y", y, y_scales, per, dtype, shape, dev)
+    if z_scales is None:
+        zs = _rows_of("z", z, dtype, shape, dev)
+    else:
+        _kept("z", z, z_scales, per, dtype, shape, dev)
+        zs = width
     _need("weight", weight, _F32, (width,), dev)
     if dz is None:
         dz, dzs = _empty(shape, dtype=dtype, device=device), width
@@ -242,17 +240,18 @@ def block_norm_bwd(dout, dresidual, x, h, weight, gate=None, next_weight=None, *
     _residual_type("dresidual", dtype, rtype)
     _need("dresidual", dresidual, rtype, shape, dev)
     lead = shape[:-1]
-    for name, t, scales, kind in (("dout", dout, None, dtype), ("x", x, x_scales, dtype), ("h", h, h_scales, rtype)):
-        if t is not None:
-            _packed(name, t, scales, lead, kind, shape, dev)
-            if not t.is_contiguous():
-                _need(name, t, kind, shape, dev)
+    _kept("x", x, x_scales, lead, dtype, shape, dev)
     _need("weight", weight, _F32, (width,), dev)
     if next_weight is not None:
+        _need("dout", dout, dtype, shape, dev)
+        _kept("h", h, h_scales, lead, rtype, shape, dev)
         _need("next_weight", next_weight, _F32, (width,), dev)
     step = dstep = width
     if gate is not None:
-        step = _packed("gate", gate, gate_scales, lead, dtype, shape, dev)
+        if gate_scales is None:
+            step = _rows_of("gate", gate, dtype, shape, dev)
+        else:
+            _kept("gate", gate, gate_scales, lead, dtype, shape, dev)
         if dgate is None:
             dgate = _empty(shape, dtype=dtype, device=device)
         else:
