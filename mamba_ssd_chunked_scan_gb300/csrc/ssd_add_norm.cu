@@ -333,15 +333,18 @@ __global__ void __launch_bounds__(THREADS) ssd_add_norm_bwd_kernel(AddNormBwdArg
 }
 
 // dw[e] (next[e - W] from column W on) = sum over the shares: COLS columns (16 or 32) per CTA, the shares dealt to its 1024 / COLS rows of threads, whose
-// sums are added in their order.
-template <int COLS>
+// sums are added in their order.  EARLY: the next launch may prepare while the shares are still being summed; where that one's CTAs
+// are to be spread evenly it may only while they are added (it would fill whichever SMs end first: fp32 block norm gradients of
+// 16384 x 2048 back to back 279 us, so 184).
+template <int COLS, bool EARLY>
 __global__ void __launch_bounds__(1024) ssd_share_sum(const float* shares, int nshares, int columns, int W, float* dw, float* next) {
     __shared__ float part[32][COLS + 1];
     const int lane = threadIdx.x % COLS, w = threadIdx.x / COLS;
     const int e = blockIdx.x * COLS + lane;
     float s = 0.f;
-    pdl_trigger();
+    if (EARLY) pdl_trigger();
     pdl_wait();   // launched while the shares are still being summed
+    if (!EARLY) pdl_trigger();
     if (e < columns) {
 #pragma unroll 4
         for (int k = w; k < nshares; k += 1024 / COLS) s += shares[(size_t)k * columns + e];
@@ -486,14 +489,15 @@ cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& args, cudaStream_t st) {
     else
         e = launch_bwd_typed<float, float>(a, &nshares, st);
     if (e != cudaSuccess) return e;
-    return launch_share_sum(a.shares, (int)nshares, a.width, a.width, a.dweight, nullptr, st);
+    return launch_share_sum(a.shares, (int)nshares, a.width, a.width, a.dweight, nullptr, true, st);
 }
 
-cudaError_t launch_share_sum(const float* shares, int nshares, int width, int columns, float* dw, float* next, cudaStream_t st) {
+cudaError_t launch_share_sum(const float* shares, int nshares, int width, int columns, float* dw, float* next, bool early, cudaStream_t st) {
     // 16 columns a CTA while all CTAs run at once (20000 x 256 in a graph 17.2 us, with 32 18.6; 4096 x 8192 94 and 89)
     const int cols = columns <= 16 * 2 * kAddNormSMs ? 16 : 32;
-    return launch_kernel(cols == 16 ? ssd_share_sum<16> : ssd_share_sum<32>, (unsigned)((columns + cols - 1) / cols), 1024, 0, st, true,
-                         shares, nshares, columns, width, dw, next);
+    auto kern = early ? (cols == 16 ? ssd_share_sum<16, true> : ssd_share_sum<32, true>)
+                      : (cols == 16 ? ssd_share_sum<16, false> : ssd_share_sum<32, false>);
+    return launch_kernel(kern, (unsigned)((columns + cols - 1) / cols), 1024, 0, st, true, shares, nshares, columns, width, dw, next);
 }
 
 }  // namespace ssd

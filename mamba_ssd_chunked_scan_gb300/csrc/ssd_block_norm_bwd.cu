@@ -46,7 +46,7 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& args, cudaStream_t st)
                                                            : launch_block_norm_bwd_bf16(a, &lines, st);
     if (e != cudaSuccess) return e;
     const int width = a.size * a.groups;
-    return launch_share_sum(a.shares, lines, width, a.next_weight ? 2 * width : width, a.dweight, a.dnext_weight, st);
+    return launch_share_sum(a.shares, lines, width, a.next_weight ? 2 * width : width, a.dweight, a.dnext_weight, false, st);
 }
 
 }  // namespace ssd

@@ -388,7 +388,7 @@ cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
 int64_t add_norm_bwd_shares(int64_t rows, int width);   // row slots of the backward
 cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
 // dw (and next, from column `width` on) = sums over nshares rows of `columns` shares, in a fixed order
-cudaError_t launch_share_sum(const float* shares, int nshares, int width, int columns, float* dw, float* next, cudaStream_t st);
+cudaError_t launch_share_sum(const float* shares, int nshares, int width, int columns, float* dw, float* next, bool early, cudaStream_t st);
 cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
 cudaError_t launch_unpack(const PackArgs& a, cudaStream_t st);
 cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t st);
