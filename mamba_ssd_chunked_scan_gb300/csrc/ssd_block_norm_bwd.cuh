@@ -196,18 +196,25 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             if (next) clear_head<H, V>(rec + kH, 0, lane, shift);
             if (RES) clear_head<R, V>(rec + kR, 0, lane, shift);
         }
-        Two xs = both(0.f), gs = xs, hs = xs;
-        if (XP) xs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::x_scale + 4 * lane));
-        if (XP && GATE) gs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::gate_scale + 4 * lane));
-        if (HP && next) hs = both(*reinterpret_cast<const float*>(rec + 32 * Rec::h_scale + 4 * lane));
-        auto dout_of = [&](int c, Two (&v)[P]) { widen(piece_vector<T, V>(rec + kD, c, lane), xs, v); };
-        auto x_of = [&](int c, Two (&v)[P]) { widen(piece_vector<X, V>(rec + kX, c, lane), xs, v); };
-        auto gate_of = [&](int c, Two (&v)[P]) { widen(piece_vector<X, V>(rec + kZ, c, lane), gs, v); };
-        auto h_of = [&](int c, Two (&v)[P]) { widen(piece_vector<H, V>(rec + kH, c, lane), hs, v); };
+        // codes of x and h stay codes; their scales join the sums' and the row's factors
+        float xs = 1.f, gs = 1.f, hs = 1.f;
+        if (XP) xs = *reinterpret_cast<const float*>(rec + 32 * Rec::x_scale + 4 * lane);
+        if (XP && GATE) gs = *reinterpret_cast<const float*>(rec + 32 * Rec::gate_scale + 4 * lane);
+        if (HP && next) hs = *reinterpret_cast<const float*>(rec + 32 * Rec::h_scale + 4 * lane);
+        auto dout_of = [&](int c, Two (&v)[P]) { to_pairs(piece_vector<T, V>(rec + kD, c, lane), v); };
+        auto x_of = [&](int c, Two (&v)[P]) { to_pairs(piece_vector<X, V>(rec + kX, c, lane), v); };
+        auto gate_of = [&](int c, Two (&v)[P]) {
+            to_pairs(piece_vector<X, V>(rec + kZ, c, lane), v);
+            if constexpr (XP) {
+#pragma unroll
+                for (int k = 0; k < P; ++k) v[k] = v[k] * both(gs);
+            }
+        };
+        auto h_of = [&](int c, Two (&v)[P]) { to_pairs(piece_vector<H, V>(rec + kH, c, lane), v); };
         const uint32_t t = (uint32_t)tid * V;
         // What is kept of a row beside its record: the gate's sigmoid (or silu and its slope), and the gradient of u rstd1 weight.
         Two sg[GATE ? C : 1][P], sl[GATE && kKeep ? C : 1][P], g1[RES ? C : 1][P];
-        Two r2 = both(0.f), k2 = r2;
+        Two r2 = both(0.f), r2h = r2, k2 = r2;
         if constexpr (RES) {
             if (next) {
                 Two hh = both(0.f), ph = hh;
@@ -226,9 +233,15 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                 float s[2] = {low(hh) + high(hh), low(ph) + high(ph)};
                 sums(s, turn);
                 turn ^= 1;
+                if (HP) {   // not hs * hs, which may be 0 or infinite
+                    s[0] = s[0] * hs * hs;
+                    s[1] *= hs;
+                }
                 const float rstd2 = rsqrt_of(s[0] * a.inv_size + a.eps);
                 r2 = both(rstd2);
-                k2 = both(-(s[1] * rstd2 * rstd2 * a.inv_size) * rstd2);   // h times it: -rstd2 hh mean(p2 hh)
+                r2h = both(HP ? rstd2 * hs : rstd2);
+                const float k = -(s[1] * rstd2 * rstd2 * a.inv_size) * rstd2;   // h times it: -rstd2 hh mean(p2 hh)
+                k2 = both(HP ? k * hs : k);
             }
         }
         Two uu = both(0.f), pu = uu;
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
                         g[k] = fma(d[k], w[k] * r2, fma(h[k], k2, g[k]));
-                        dn[c][k] = fma(d[k], h[k] * r2, dn[c][k]);
+                        dn[c][k] = fma(d[k], h[k] * r2h, dn[c][k]);
                     }
                 }
                 put<R, V, SHIFTED>(q_dres + c * span * (int64_t)sizeof(R), t * sizeof(R), e0 + c * span, n, mask, g);
@@ -263,6 +276,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                 for (int k = 0; k < P; ++k) {
                     if constexpr (kKeep) {
                         silu<T>(z[k], sg[c][k], sl[c][k]);
+                        if (XP) sl[c][k] = sl[c][k] * both(xs);
                         x[k] = x[k] * sg[c][k];
                     } else {
                         sg[c][k] = sigmoid<T>(z[k]);
@@ -281,8 +295,12 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
         sums(s, turn);
         turn ^= 1;
-        const float rstd = rsqrt_of(s[0] * a.inv_size + a.eps);
-        const Two r1 = both(rstd), k1 = both(-(s[1] * a.inv_size * rstd * rstd) * rstd);
+        if (XP) {
+            s[0] = s[0] * xs * xs;
+            s[1] *= xs;
+        }
+        const float rstd = rsqrt_of(s[0] * a.inv_size + a.eps), mean = -(s[1] * a.inv_size * rstd * rstd) * rstd;
+        const Two r1 = both(rstd), r1x = both(XP ? rstd * xs : rstd), k1 = both(XP ? mean * xs : mean);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             Two w[P], g[P], x[P], z[P], du[P], o[P];
@@ -296,7 +314,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                 if constexpr (GATE) z[k] = kKeep ? sg[c][k] : z[k] * sg[c][k];   // silu
                 if constexpr (RES) g[k] = g1[c][k];
                 const Two u = GATE ? x[k] * z[k] : x[k];
-                o[k] = u * r1;
+                o[k] = u * r1x;
                 du[k] = fma(g[k] * w[k], r1, u * k1);
                 dw[c][k] = fma(g[k], o[k], dw[c][k]);
             }
@@ -311,6 +329,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                     // silu's slope: s + gate s (1 - s) = s (1 - silu) + silu
                     const Two slope = kKeep ? sl[c][k] : fma(sg[c][k], fma(z[k], both(-1.f), both(1.f)), z[k]);
                     o[k] = du[k] * (x[k] * slope);
+                    if (XP && !kKeep) o[k] = o[k] * both(xs);
                     du[k] = du[k] * z[k];
                 }
                 put<T, V, SHIFTED>(q_dgate + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, mask, o);

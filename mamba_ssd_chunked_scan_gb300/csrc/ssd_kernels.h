@@ -181,6 +181,7 @@ struct PackArgs {
     void* codes;
     float* scales;         // [units]
     void* out;
+    bool power_only;       // unpacking: by the scales' powers of two alone (their factors are elsewhere)
     int units_per_cta;
 };
 
@@ -344,6 +345,10 @@ struct LinearDpreArgs {
     const void* dy;
     const void* pre;       // or NULL (no activation)
     const float* pre_scales;   // [m]: pre is e4m3 codes; or NULL
+    const float* x_scales;     // [m], or NULL: dpre is to be multiplied by the factors of these scales (see scale_factor)
+    float* inv_factors;        // [m]: their reciprocals, written
+    float* ones;               // [k]: written
+    int k;
     void* dpre;            // (m, ldp) bf16, or NULL
     float* shares;         // [slabs * n], or NULL
     float* dbias;          // [n], or NULL

@@ -104,10 +104,10 @@ int check_linear_packed(const ssd_linear_params_t* p) {
 struct LinearBwdLayout {
     bool own_dpre;
     int64_t ldp;
-    size_t dpre_off, shares_off, parts_off, rows_off, total;
+    size_t dpre_off, shares_off, parts_off, rows_off, inv_off, ones_off, total;
     LinearPlan dx, dw;
 };
-// packed: with room for x in bf16.
+// packed: with room for x in bf16, its scales' factors' reciprocals and a row of ones.
 LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p, bool packed) {
     LinearBwdLayout l;
     l.own_dpre = p->act != SSD_ACT_NONE || p->n % 8 != 0;
@@ -121,7 +121,9 @@ LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p, bool packed) {
     l.total = l.rows_off;
     if (packed) {
         l.rows_off = align_up(l.rows_off, 256);
-        l.total = l.rows_off + (size_t)p->m * p->k * 2;
+        l.inv_off = align_up(l.rows_off + (size_t)p->m * p->k * 2, 256);
+        l.ones_off = align_up(l.inv_off + (size_t)p->m * 4, 256);
+        l.total = l.ones_off + (size_t)p->k * 4;
     }
     return l;
 }
@@ -239,6 +241,15 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
     d.dpre = l.own_dpre && (dx || dw) ? ws + l.dpre_off : nullptr;
     d.shares = dbias ? (float*)(ws + l.shares_off) : nullptr;
     d.dbias = dbias;
+    const bool factors = x_scales && dw && d.dpre;
+    if (factors) {
+        d.x_scales = x_scales;
+        if (dx) {
+            d.inv_factors = (float*)(ws + l.inv_off);
+            d.ones = (float*)(ws + l.ones_off);
+            d.k = p->k;
+        }
+    }
     if ((d.dpre || dbias) && launch_linear_dpre(d, st) != cudaSuccess) return SSD_ERR_CUDA;
     const LinearOperand g = {l.own_dpre ? (const void*)(ws + l.dpre_off) : dy, l.own_dpre ? l.ldp : p->n, false};
     LinearArgs a = {};
@@ -249,7 +260,10 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
         a.m = p->m; a.n = p->k; a.k = p->n; a.y = dx;
         a.x = g;
         a.w = {w, p->k, true};
+        a.x_scales = d.inv_factors;
+        a.w_scales = d.ones;
         if (launch_linear(a, l.dx, st) != cudaSuccess) return SSD_ERR_CUDA;
+        a.x_scales = a.w_scales = nullptr;
     }
     if (dw) {   // (n, k) = dpre^T (n, m) x (m, k): both contractions run along the rows
         a.m = p->n; a.n = p->k; a.k = p->m; a.y = dw;
@@ -260,6 +274,7 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
             PackArgs u = {};
             u.units = p->m; u.size = p->k; u.groups = 1; u.dtype = SSD_BF16; u.stride = p->ldx;
             u.codes = const_cast<void*>(x); u.scales = const_cast<float*>(x_scales); u.out = ws + l.rows_off;
+            u.power_only = factors;
             if (launch_unpack(u, st) != cudaSuccess) return SSD_ERR_CUDA;
             a.w = {ws + l.rows_off, p->k, true};
         }

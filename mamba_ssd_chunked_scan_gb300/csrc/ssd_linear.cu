@@ -734,7 +734,8 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
 // columns: together (V = 8: rows are whole 16-byte words) or 32 apart (V = 1).  Bound by HBM: four rows' loads are in
 // flight per warp.
 constexpr int kSlabRows = 128, kSlabCols = 256;
-// P: the type of pre (e4m3: times its row's scale).
+// P: the type of pre (e4m3: times its row's scale).  Where x comes as 8-bit rows, their scales' factors go into dpre before its
+// rounding, so that the product with the codes rounds no operand twice; dx's epilogue takes them out.
 template <typename P, int V>
 __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     __shared__ float part[8][kSlabCols];
@@ -750,10 +751,18 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     const P* pre = a.pre ? static_cast<const P*>(a.pre) + (size_t)m0 * a.n + n0 : nullptr;
     bf16_t* dp = a.dpre ? static_cast<bf16_t*>(a.dpre) + (size_t)m0 * a.ldp + n0 : nullptr;
     float sum[C][V] = {};
+    if (a.ones)
+        for (int k = blockIdx.x * 256 + threadIdx.x; k < a.k; k += gridDim.x * 256) a.ones[k] = 1.f;
     for (int k0 = w; k0 < rows; k0 += 8 * kRowsAhead) {
         Raw<bf16_t, V> d[kRowsAhead][C];
         Raw<P, V> q[kRowsAhead][C];
-        float scale[sizeof(P) == 1 ? kRowsAhead : 1];
+        float scale[sizeof(P) == 1 ? kRowsAhead : 1], factor[kRowsAhead];
+#pragma unroll
+        for (int u = 0; u < kRowsAhead; ++u) {
+            const int k = k0 + 8 * u;
+            factor[u] = a.x_scales && k < rows ? scale_factor(__ldg(a.x_scales + m0 + k)) : 1.f;
+            if (a.inv_factors && k < rows && c0 == 0 && lane == 0) a.inv_factors[m0 + k] = 1.f / factor[u];
+        }
         if constexpr (sizeof(P) == 1) {
 #pragma unroll
             for (int u = 0; u < kRowsAhead; ++u) scale[u] = k0 + 8 * u < rows ? __ldg(a.pre_scales + m0 + k0 + 8 * u) : 0.f;
@@ -789,14 +798,16 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[e] *= act_slope(t[e], a.act);
                 }
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[c][e] += v[e];
                 if (dp) {
                     Raw<bf16_t, V> o;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] *= factor[u];
                     o.set(v);
                     // read next by the products, so left in L2
                     *reinterpret_cast<typename Raw<bf16_t, V>::W*>(dp + (size_t)k * a.ldp + 32 * c) = o.w;
                 }
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum[c][e] += v[e];
             }
     }
     if (!a.shares) return;

@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(256) ssd_unpack_kernel(const __grid_constant__
     else q.load_some(codes, count);
     Two v[kFlat / 2];
     to_pairs(q, v);
-    float s = __ldg(scales);
+    auto scale_at = [&](const float* p) { return a.power_only ? scale_power(__ldg(p)) : __ldg(p); };
+    float s = scale_at(scales);
     if (e + kFlat <= n) {
 #pragma unroll
         for (int j = 0; j < kFlat / 2; ++j) v[j] = v[j] * both(s);
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(256) ssd_unpack_kernel(const __grid_constant__
         for (int j = 0; j < kFlat; ++j) {
             if (e == n && j < count) {
                 e = 0;
-                s = __ldg(++scales);
+                s = scale_at(++scales);
             }
             ++e;
             if (j % 2) v[j / 2] = two(low(v[j / 2]), high(v[j / 2]) * s);
@@ -103,7 +104,10 @@ __global__ void __launch_bounds__(256) ssd_unpack_rows_kernel(const __grid_const
     from_codes(q, v);
     const float* s = a.scales + row * a.groups;
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= __ldg(s + (a.groups == 1 ? 0 : (e + j) / a.size));
+    for (int j = 0; j < V; ++j) {
+        const float f = __ldg(s + (a.groups == 1 ? 0 : (e + j) / a.size));
+        v[j] *= a.power_only ? scale_power(f) : f;
+    }
     Raw<T, V> o;
     o.set(v);
     o.store(static_cast<T*>(a.out) + row * width + e);

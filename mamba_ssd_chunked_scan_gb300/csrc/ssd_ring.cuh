@@ -59,16 +59,6 @@ __device__ __forceinline__ Raw<K, V> piece_vector(const unsigned char* at, int c
     }
     return q;
 }
-// It as pairs: codes times s.
-template <typename K, int V>
-__device__ __forceinline__ void widen(const Raw<K, V>& q, Two s, Two (&v)[V / 2]) {
-    to_pairs(q, v);
-    if constexpr (sizeof(K) == 1) {
-#pragma unroll
-        for (int k = 0; k < V / 2; ++k) v[k] = v[k] * s;
-    }
-}
-
 // Ask for the elements of vector c (from column e, `off` bytes from p) that lie before the row's end, n, into its pieces, and zeros for
 // the others: vectors of one lane each for itself, 32-byte ones with the neighbouring lane.  A vector past the end is left alone.
 template <typename K, int V, bool SHIFTED>

@@ -23,6 +23,16 @@ __device__ __forceinline__ uint32_t pack_scale_bits(uint32_t amax) {
 // Its reciprocal, a normal number too (exponents of scales are -108 to 120).
 __device__ __forceinline__ float pack_inverse(uint32_t scale_bits) { return __uint_as_float((254u << 23) - scale_bits); }
 
+// A scale as power * factor: a power of two of its sign, and a factor from 1 up to 2 (1 for zeros, subnormals, infinities and NaNs).
+__device__ __forceinline__ float scale_factor(float s) {
+    const uint32_t b = __float_as_uint(s), e = b >> 23 & 0xffu;
+    return e > 0 && e < 255 ? __uint_as_float((b & 0x7fffffu) | 0x3f800000u) : 1.f;
+}
+__device__ __forceinline__ float scale_power(float s) {
+    const uint32_t b = __float_as_uint(s), e = b >> 23 & 0xffu;
+    return e > 0 && e < 255 ? __uint_as_float(b & 0xff800000u) : s;
+}
+
 // Largest magnitude of V elements as fp32 bits, infinities and NaNs as they are (at least kInfBits).
 template <typename T, int V>
 __device__ __forceinline__ uint32_t magnitude(const Raw<T, V>& r) {

@@ -277,8 +277,8 @@ def linear_bwd(dy, x, w, pre=None, *, act="none", x_scales=None, pre_scales=None
     its second result (with an activation).  Returns a dict: ``dx`` (..., k) bf16, ``dw`` (n, k) bf16 and
     ``dbias`` (n) fp32, None where not wanted.  (The residual's gradient is dy.)
 
-    x and pre may each be 8-bit rows (pack_rows', or add_norm's), float8_e4m3fn with x_scales, pre_scales (...) fp32: x stands
-    for x * x_scales rounded to bf16 (which loses nothing of pack_rows' rows); w stays bf16."""
+    x and pre may each be 8-bit rows (pack_rows', or add_norm's), float8_e4m3fn with x_scales, pre_scales (...) fp32; w stays bf16.
+    Nothing of pack_rows' rows is lost; other scales cost one rounding to bf16 without an activation, none with one."""
     dev = _device("x", x)
     if stream is not None or _current_device() != dev:
         with _elsewhere(dev, stream):

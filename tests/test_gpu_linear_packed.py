@@ -1,7 +1,7 @@
 """A projection's gradients from 8-bit rows against the formula in 64 bits.
 
-x in 8 bits stands for a bf16 number (rounded once where its scale is no power of two), so the products are those of
-linear_bwd; dpre is formed from the activation's argument in fp32 and rounded to bf16 as the products' operand."""
+x in 8 bits stands for a bf16 number where its scale is a power of two, so the products are those of linear_bwd; dpre is
+formed from the activation's argument in fp32 and rounded to bf16 as the products' operand."""
 import pytest
 import torch
 
@@ -44,20 +44,21 @@ def test_gradients(m, n, k, extra, act, scales):
     x, xs, w, dy, pre, ps = make(m, n, k, m + n, act, scales, extra)
     got = ssd.linear_bwd(dy, x, w, pre, act=act, x_scales=xs, pre_scales=ps, want_dbias=True, check_status=True)
     d = dy.double()
-    # the slopes' errors (a few 2^-22 of terms below 2) and dpre's rounding as an operand
-    off = torch.zeros_like(d)
+    # the slopes' errors (a few 2^-22 of terms below 2) and dpre's rounding as an operand; scales that are no powers of two are in it
+    # where it is an array of its own, otherwise x is rounded
+    off, own = torch.zeros_like(d), act != "none" or n % 8 != 0
     if act != "none":
         d = d * slope(wide(pre, ps), act)
         off = 64 * U * dy.double().abs() + HALF * d.abs()
-    elif n % 8:
-        off = torch.zeros_like(d)   # a copy
+    elif own and scales != "packed":
+        off = HALF * d.abs()
     xd, wd = wide(x, xs), w.double()
-    off_x = 0 if scales == "packed" else HALF * xd.abs()
+    off_x = 0 if scales == "packed" or own else HALF * xd.abs()
     sums = (2 * max(m, n, k) + 64) * U
     dx, dw = d @ wd, d.t() @ xd
     close(got["dx"], dx, HALF * dx.abs() + off @ wd.abs() + sums * (d.abs() @ wd.abs()) + 1e-30, "dx")
     size = d.abs().t() @ xd.abs()
-    close(got["dw"], dw, HALF * dw.abs() + off.t() @ xd.abs() + (d.abs().t() @ off_x if scales != "packed" else 0) + sums * size + 1e-30, "dw")
+    close(got["dw"], dw, HALF * dw.abs() + off.t() @ xd.abs() + (0 if isinstance(off_x, int) else d.abs().t() @ off_x) + sums * size + 1e-30, "dw")
     close(got["dbias"], d.sum(0), (64 * U * dy.double().abs()).sum(0) + sums * d.abs().sum(0) + 1e-30, "dbias")
 
 
