@@ -480,7 +480,7 @@ SSD_API int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const vo
  * call above).  They stand for codes * scale: pre so in fp32; of x the codes times the scales' powers of two are the
  * product's operand, in bf16 in the workspace, which is exact, and the rest of the scales (1 for those of ssd_pack_rows()) is
  * in dpre before its rounding; where dpre is dy itself, x is codes * scale rounded once to bf16.  Codes may start at any
- * byte; ldx is any number from k on then. */
+ * byte; ldx is any number from k on then.  x may be NULL where dw is. */
 SSD_API size_t ssd_linear_bwd_packed_workspace_size(const ssd_linear_params_t* p);
 SSD_API int ssd_linear_bwd_packed(const ssd_linear_params_t* p, const void* x, const float* x_scales, const void* w,
              const void* pre, const float* pre_scales, const void* dy, void* dx, void* dw, float* dbias,

@@ -217,7 +217,7 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
         if (dbias && cudaMemsetAsync(dbias, 0, (size_t)p->n * 4, st) != cudaSuccess) return SSD_ERR_CUDA;
         return SSD_OK;
     }
-    if (!x || !w || !dy || (!dx && !dw && !dbias) || (p->act != SSD_ACT_NONE) != (pre != nullptr)) return SSD_ERR_INVALID_ARG;
+    if ((!x && (dw || x_scales || !packed)) || !w || !dy || (!dx && !dw && !dbias) || (p->act != SSD_ACT_NONE) != (pre != nullptr)) return SSD_ERR_INVALID_ARG;
     if ((pre_scales && !pre) || !aligned(x_scales, 4) || !aligned(pre_scales, 4)) return SSD_ERR_INVALID_ARG;
     if (!aligned(x, x_scales ? 1 : 16) || !aligned(w, 16) || !aligned(dy, 16) || !aligned(pre, pre_scales ? 1 : 2)) return SSD_ERR_INVALID_ARG;
     const LinearBwdLayout l = linear_bwd_layout(p, packed);

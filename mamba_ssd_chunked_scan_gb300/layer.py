@@ -255,10 +255,11 @@ def linear(x, w, bias=None, residual=None, *, act="none", x_scales=None, w_scale
     return (y, pre) if return_pre else y
 
 
-def _packed_params(x, w, act, dev):
-    """The parameters of the gradients of a product whose x is 8-bit rows and w bf16."""
-    shape, wshape = x.shape, w.shape
-    if x.dtype is not _E4M3:
+def _packed_params(x, w, act, dev, lead=None):
+    """The parameters of the gradients of a product whose x is 8-bit rows (or is not there, for rows of the shape `lead`) and w bf16."""
+    wshape = w.shape
+    shape = x.shape if lead is None else (*lead, wshape[-1])
+    if x is not None and x.dtype is not _E4M3:
         raise TypeError(f"x: expected float8_e4m3fn with x_scales, got {x.dtype}")
     if len(shape) < 1 or len(wshape) != 2 or wshape[1] != shape[-1]:
         raise ValueError(f"expected x (..., k) and w (n, k), got {tuple(shape)} and {tuple(wshape)}")
@@ -267,8 +268,11 @@ def _packed_params(x, w, act, dev):
         raise ValueError(f"act must be one of {tuple(_ACT)}, got {act!r}")
     n, k = wshape
     _need("w", w, _BF16, wshape, dev)
-    ldx = k if x.is_contiguous() else _row_stride("x", x)
-    return shape[:-1], _lib.LinearParams(x.numel() // k if k else 0, ldx, n, k, _lib.SSD_BF16, code)
+    ldx = k if x is None or x.is_contiguous() else _row_stride("x", x)
+    m = 1
+    for s in shape[:-1]:
+        m *= s
+    return shape[:-1], _lib.LinearParams(m if k else 0, ldx, n, k, _lib.SSD_BF16, code)
 
 
 def linear_bwd(dy, x, w, pre=None, *, act="none", x_scales=None, pre_scales=None, want_dx=True, want_dw=True, want_dbias=False,
@@ -278,16 +282,22 @@ def linear_bwd(dy, x, w, pre=None, *, act="none", x_scales=None, pre_scales=None
     ``dbias`` (n) fp32, None where not wanted.  (The residual's gradient is dy.)
 
     x and pre may each be 8-bit rows (pack_rows', or add_norm's), float8_e4m3fn with x_scales, pre_scales (...) fp32; w stays bf16.
-    Nothing of pack_rows' rows is lost; other scales cost one rounding to bf16 without an activation, none with one."""
-    dev = _device("x", x)
+    Nothing of pack_rows' rows is lost; other scales cost one rounding to bf16 without an activation, none with one.  x is only
+    read for dw: it may be None with want_dw=False."""
+    dev = _device("dy", dy) if x is None else _device("x", x)
     if stream is not None or _current_device() != dev:
         with _elsewhere(dev, stream):
             return linear_bwd(dy, x, w, pre, act=act, x_scales=x_scales, pre_scales=pre_scales, want_dx=want_dx, want_dw=want_dw,
                               want_dbias=want_dbias, check_status=check_status)
-    lead, p = _linear_params(x, w, act, dev) if x_scales is None else _packed_params(x, w, act, dev)
-    device = x.device
+    if x is None:
+        if want_dw or x_scales is not None:
+            raise ValueError("x: None only with want_dw=False, and without x_scales")
+        lead, p = _packed_params(None, w, act, dev, dy.shape[:-1])
+    else:
+        lead, p = _linear_params(x, w, act, dev) if x_scales is None else _packed_params(x, w, act, dev)
+    device = dy.device
     if x_scales is None:
-        if x.dtype is not _BF16:
+        if x is not None and x.dtype is not _BF16:
             raise TypeError(f"x must be bf16, or float8_e4m3fn with x_scales, got {x.dtype}")
     else:
         _need("x_scales", x_scales, _F32, lead, dev)
@@ -304,17 +314,17 @@ def linear_bwd(dy, x, w, pre=None, *, act="none", x_scales=None, pre_scales=None
     if not (want_dx or want_dw or want_dbias):
         raise ValueError("no gradient wanted")
     ref = ctypes.byref(p)
-    packed = x_scales is not None or pre_scales is not None
+    packed = x is None or x_scales is not None or pre_scales is not None
     nbytes = (_lib_c.ssd_linear_bwd_packed_workspace_size if packed else _lib_c.ssd_linear_bwd_workspace_size)(ref)
     if nbytes == 0:
-        raise _lib.SSDError(2, f"linear_bwd of {tuple(x.shape)} and {tuple(w.shape)}, row stride {p.ldx}")
+        raise _lib.SSDError(2, f"linear_bwd of {(*lead, p.k)} and {tuple(w.shape)}, row stride {p.ldx}")
     dx = _empty((*lead, p.k), dtype=_BF16, device=device) if want_dx else None
     dw = _empty((p.n, p.k), dtype=_BF16, device=device) if want_dw else None
     db = _empty(p.n, dtype=_F32, device=device) if want_dbias else None
     ws = _empty(nbytes, dtype=torch.uint8, device=device)
     st = _raw_stream(dev)
     if packed:
-        rc = _lib_c.ssd_linear_bwd_packed(ref, x.data_ptr(), _ptr(x_scales), w.data_ptr(), _ptr(pre), _ptr(pre_scales), dy.data_ptr(),
+        rc = _lib_c.ssd_linear_bwd_packed(ref, _ptr(x), _ptr(x_scales), w.data_ptr(), _ptr(pre), _ptr(pre_scales), dy.data_ptr(),
                                           _ptr(dx), _ptr(dw), _ptr(db), ws.data_ptr(), nbytes, st)
     else:
         rc = _lib_c.ssd_linear_bwd(ref, x.data_ptr(), w.data_ptr(), _ptr(pre), dy.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db),

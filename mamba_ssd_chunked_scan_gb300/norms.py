@@ -232,7 +232,7 @@ def block_norm_bwd(dout, dresidual, x, h, weight, gate=None, next_weight=None, *
                                   gate_scales=gate_scales, dgate=dgate, dtype=dtype)
     rtype, shape, device = dresidual.dtype, dresidual.shape, dresidual.device
     width = _width("dresidual", shape)
-    if (dout is None) != (next_weight is None) or (h is None) != (next_weight is None):
+    if (dout is None) != (next_weight is None) or (h is None) != (next_weight is None) or (h is None and h_scales is not None):
         raise ValueError("dout, h: given with next_weight, and only then")
     if dtype is None:
         dtype = dout.dtype if dout is not None else x.dtype if x_scales is None else None

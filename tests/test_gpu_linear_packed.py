@@ -108,3 +108,21 @@ def test_refusals():
             bad()
     with pytest.raises(ssd.SSDError):   # k is a multiple of 8
         ssd.linear_bwd(dy, x[:, :44].contiguous(), w[:, :44].contiguous(), x_scales=xs)
+
+
+def test_without_the_operand():
+    """dx and dbias need no x: the same bits without it, and from bf16 pre as from 8-bit rows' values."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    x, w, dy = r(2, 77, 64), r(40, 64), r(2, 77, 40)
+    codes, scales = ssd.pack_rows(r(2, 77, 40))
+    for pre in (ssd.unpack_rows(codes, scales), None):
+        act = "none" if pre is None else "silu"
+        want = ssd.linear_bwd(dy, x, w, pre, act=act, want_dbias=True)
+        got = ssd.linear_bwd(dy, None, w, pre, act=act, want_dw=False, want_dbias=True)
+        assert got["dw"] is None and torch.equal(got["dx"], want["dx"]) and torch.equal(got["dbias"], want["dbias"])
+    want = ssd.linear_bwd(dy, x, w, ssd.unpack_rows(codes, scales), act="silu", want_dw=False)
+    got = ssd.linear_bwd(dy, None, w, codes, act="silu", pre_scales=scales, want_dw=False)
+    assert torch.equal(got["dx"], want["dx"])
+    assert torch.equal(ssd.linear_bwd(dy, None, w, want_dw=False, want_dx=False, want_dbias=True)["dbias"],
+                       ssd.linear_bwd(dy, x, w, want_dw=False, want_dx=False, want_dbias=True)["dbias"])
