@@ -243,8 +243,7 @@ __global__ void __launch_bounds__(fwd_threads_sm(E)) ssd_block_norm_kernel(const
 // Where no vectors fit: single elements, a row a slot, all of it asked for before the first is used.
 template <typename T, typename R, int E, int LANES, bool GATE, bool RES>
 __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_loose(const __grid_constant__ BlockNormArgs a) {
-    constexpr int V = 2, C = E / V, P = V / 2;
-    constexpr bool SHIFTED = false;
+    constexpr int V = 2, C = E / V, P = 1;   // pairs of single elements
     __shared__ RowPart part[2];
     __shared__ uint32_t tops[2][32];
     const int tid = LANES ? threadIdx.x % (LANES ? LANES : 32) : threadIdx.x, nt = LANES ? LANES : blockDim.x;
@@ -255,9 +254,9 @@ __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_
     const uint32_t row = a.groups == 1 ? unit : unit / (uint32_t)a.groups;
     const int64_t base = (int64_t)unit * n;
     const int first = (int)(unit - row * a.groups) * n;   // the group's first column
-    const Place<V, SHIFTED> place = {tid, nt, SHIFTED ? (int)(base & (V - 1)) : 0, n, (a.units - unit) * n};
-    Part<T, V, E, SHIFTED> xq, zq;
-    Part<R, V, E, SHIFTED> rq;
+    const Place<V, false> place = {tid, nt, 0, n, n};
+    Part<T, V, E, false> xq, zq;
+    Part<R, V, E, false> rq;
     xq.load(static_cast<const T*>(a.x) + base, place);
     if (GATE) zq.load(static_cast<const T*>(a.gate) + row * a.gate_stride + first, place);
     if (RES) rq.load(static_cast<const R*>(a.residual) + base, place);
@@ -268,11 +267,9 @@ __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_
         if (GATE) {
             Two z[P];
             zq.get(c, z);
-#pragma unroll
-            for (int k = 0; k < P; ++k) u[c][k] = u[c][k] * (z[k] * sigmoid<T>(z[k]));
+            u[c][0] = u[c][0] * (z[0] * sigmoid<T>(z[0]));
         }
-#pragma unroll
-        for (int k = 0; k < P; ++k) sum = fma(u[c][k], u[c][k], sum);
+        sum = fma(u[c][0], u[c][0], sum);
     }
     float ss[1] = {low(sum) + high(sum)};
     if (a.x_codes) {
@@ -292,10 +289,10 @@ __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_
         for (int c = 0; c < C; ++c) {
             Two v[P];
             xq.get(c, v);
-            store_codes<V, E, SHIFTED>(static_cast<e4m3_t*>(a.x_codes) + base, place, c, v, pack_inverse(sx), bad_x);
+            store_codes<V, E, false>(static_cast<e4m3_t*>(a.x_codes) + base, place, c, v, pack_inverse(sx), bad_x);
             if (GATE) {
                 zq.get(c, v);
-                store_codes<V, E, SHIFTED>(static_cast<e4m3_t*>(a.gate_codes) + base, place, c, v, pack_inverse(sz), bad_z);
+                store_codes<V, E, false>(static_cast<e4m3_t*>(a.gate_codes) + base, place, c, v, pack_inverse(sz), bad_z);
             }
         }
     } else {
@@ -305,11 +302,8 @@ __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_
     if constexpr (!RES) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            Two w[P];
-            weights_of<V, SHIFTED>(a.weight + first, place, c, w);
-#pragma unroll
-            for (int k = 0; k < P; ++k) w[k] = u[c][k] * rstd * w[k];
-            Part<T, V, E, SHIFTED> q;
+            const Two w[P] = {u[c][0] * rstd * pair_weights(a.weight + first, place, c)};
+            Part<T, V, E, false> q;
             q.set(c, w);
             q.store(static_cast<T*>(a.out) + base, place, c);
         }
@@ -317,15 +311,11 @@ __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_
         sum = both(0.f);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            Two w[P], r[P];
-            weights_of<V, SHIFTED>(a.weight, place, c, w);
+            Two r[P];
             rq.get(c, r);
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-                u[c][k] = fma(both(a.scale), u[c][k] * rstd * w[k], r[k]);
-                sum = fma(u[c][k], u[c][k], sum);
-            }
-            Part<R, V, E, SHIFTED> q;
+            u[c][0] = fma(both(a.scale), u[c][0] * rstd * pair_weights(a.weight, place, c), r[0]);
+            sum = fma(u[c][0], u[c][0], sum);
+            Part<R, V, E, false> q;
             q.set(c, u[c]);
             q.store(static_cast<R*>(a.residual_out) + base, place, c);
         }
@@ -337,19 +327,14 @@ __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            Two w[P];
-            weights_of<V, SHIFTED>(a.next_weight, place, c, w);
-#pragma unroll
-            for (int k = 0; k < P; ++k) u[c][k] = u[c][k] * rstd2 * w[k];
+            u[c][0] = u[c][0] * rstd2 * pair_weights(a.next_weight, place, c);
             if (codes) {
-#pragma unroll
-                for (int k = 0; k < P; ++k)
-                    for (const float f : {low(u[c][k]), high(u[c][k])}) {
-                        const uint32_t b = __float_as_uint(f) & 0x7fffffffu;
-                        if (b < kInfBits) top = max(top, b);
-                    }
+                for (const float f : {low(u[c][0]), high(u[c][0])}) {
+                    const uint32_t b = __float_as_uint(f) & 0x7fffffffu;
+                    if (b < kInfBits) top = max(top, b);
+                }
             } else {
-                Part<T, V, E, SHIFTED> q;
+                Part<T, V, E, false> q;
                 q.set(c, u[c]);
                 q.store(static_cast<T*>(a.out) + base, place, c);
             }
@@ -359,13 +344,14 @@ __global__ void __launch_bounds__(E == kNarrowElems ? 640 : 512) ssd_block_norm_
         if (tid == 0) a.out_scales[unit] = __uint_as_float(so);
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            store_codes<V, E, SHIFTED>(static_cast<e4m3_t*>(a.out) + base, place, c, u[c], pack_inverse(so), true);
+            store_codes<V, E, false>(static_cast<e4m3_t*>(a.out) + base, place, c, u[c], pack_inverse(so), true);
     }
 }
 
 bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// Rows that a slot takes one after another, where there are enough for all SMs.
+// Rows that a slot takes one after another, where there are enough for all SMs (block norm with its checkpoint 16384 x 2560 107 us, with
+// 4 108, with 16 121; fp32 2048 columns 126, with 4 131; gate and norm 16384 x 5120 104, 103.5, 109).
 constexpr int kSlotRows = 8;
 
 template <typename T, typename R, int E, int LANES, bool SHIFTED, bool GATE, bool RES>
@@ -399,13 +385,16 @@ cudaError_t launch_ring(const BlockNormArgs& args, int threads, cudaStream_t st)
     return launch_kernel(kern, (a.slots + a.units_per_cta - 1) / a.units_per_cta, (unsigned)threads, (size_t)weights + (size_t)a.stages * stage, st, true, a);
 }
 
+// Rows of up to 256 columns take lanes of a warp, others a CTA; 8 elements a thread up to 1024 columns, then 16.  65536 rows of bf16, 8 and
+// 16 elements a thread: gate and norm with its checkpoint at 768 columns 65.5 and 66.6 us, at 1024 83.9 and 82.3, at 1280 111 and
+// 102; with a residual and no gate 91.6 and 94.2, 119 and 121; fp32 1024 columns 139 and 143.
 template <typename T, typename R, bool SHIFTED, bool GATE, bool RES>
 cudaError_t launch_vectors(const BlockNormArgs& a, cudaStream_t st) {
     const int span = SHIFTED ? vector_span(a.size) : a.size;
     if (span <= 64) return launch_ring<T, R, kNarrowElems, 8, SHIFTED, GATE, RES>(a, 128, st);
     if (span <= 128) return launch_ring<T, R, kNarrowElems, 16, SHIFTED, GATE, RES>(a, 128, st);
     if (span <= 256) return launch_ring<T, R, kNarrowElems, 32, SHIFTED, GATE, RES>(a, 128, st);
-    if (span <= 160 * kNarrowElems) return launch_ring<T, R, kNarrowElems, 0, SHIFTED, GATE, RES>(a, ((span + 7) / 8 + 31) / 32 * 32, st);
+    if (span <= 128 * kNarrowElems) return launch_ring<T, R, kNarrowElems, 0, SHIFTED, GATE, RES>(a, ((span + 7) / 8 + 31) / 32 * 32, st);
     return launch_ring<T, R, kWideElems, 0, SHIFTED, GATE, RES>(a, ((span + 15) / 16 + 31) / 32 * 32, st);
 }
 

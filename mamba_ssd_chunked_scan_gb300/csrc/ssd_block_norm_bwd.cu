@@ -21,13 +21,14 @@ namespace ssd {
 int64_t block_norm_bwd_lines(int64_t rows, int size, int groups) {
     const RowPlan loose = loose_plan(rows, size, groups);
     int most = loose.slots + loose.late_slots;
-    for (int span : {size, vector_span(size)}) {
-        RowPlan p = vector_plan(span);
-        for (int per_sm = ctas_sm(p.threads, threads_sm(p.elems, false)); per_sm > 0; --per_sm) {
-            spread(p, rows, groups, per_sm, true);
-            if (p.slots + p.late_slots > most) most = p.slots + p.late_slots;
+    for (int narrow : {kNarrowSpan, kNarrowSpanLong})
+        for (int span : {size, vector_span(size)}) {
+            RowPlan p = vector_plan(span, narrow);
+            for (int per_sm = ctas_sm(p.threads, threads_sm(p.elems, false)); per_sm > 0; --per_sm) {
+                spread(p, rows, groups, per_sm, true);
+                if (p.slots + p.late_slots > most) most = p.slots + p.late_slots;
+            }
         }
-    }
     return most / groups;
 }
 

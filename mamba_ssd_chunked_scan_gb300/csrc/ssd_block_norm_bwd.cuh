@@ -575,11 +575,15 @@ inline int set_slots(BlockNormBwdArgs& a, const RowPlan& p) {   // and how many 
     return (p.slots + p.late_slots) / a.groups;
 }
 
-// Rows of up to 256 columns take 8, 16 or 32 lanes of a warp, others a CTA: 8 elements a thread while that makes at most 160 threads,
-// then 16.
-inline RowPlan vector_plan(int span) {
+// Rows of up to 256 columns take 8, 16 or 32 lanes of a warp, others a CTA (131072 x 256 with a residual 122 us, by CTAs of a warp
+// 129; without 64, 71): 8 elements a thread up to 512 columns, or 1280 of fp32 or of rows of no whole vectors, then 16.  33.5 M
+// elements with gate and residual, 8 and 16 elements a thread: bf16 768 columns 152 and 129 us, 1024 148 and 133, 1280 148 and 133
+// (512 by single warps of 16: 198; by 8 136); fp32 768 columns 168 and 189, 1024 165 and 173, 2048 198 and 184; 1023 columns 176
+// and 185.  Codes of 1024 columns 163 and 110.
+constexpr int kNarrowSpan = 512, kNarrowSpanLong = 1280;
+inline RowPlan vector_plan(int span, int narrow) {
     RowPlan p = {};
-    p.elems = span <= 160 * kNarrowElems ? kNarrowElems : kWideElems;
+    p.elems = span <= narrow ? kNarrowElems : kWideElems;
     p.lanes = span <= 64 ? 8 : span <= 128 ? 16 : span <= 256 ? 32 : 0;
     p.threads = p.lanes ? 128 : row_threads(span, p.elems);
     p.slots_per_cta = p.lanes ? 128 / p.lanes : 1;
@@ -630,7 +634,7 @@ cudaError_t launch_ring(BlockNormBwdArgs& a, RowPlan p, int* lines, cudaStream_t
 
 template <typename T, typename R, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
 cudaError_t launch_vectors(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
-    const RowPlan p = vector_plan(SHIFTED ? vector_span(a.size) : a.size);
+    const RowPlan p = vector_plan(SHIFTED ? vector_span(a.size) : a.size, SHIFTED || sizeof(T) == 4 ? kNarrowSpanLong : kNarrowSpan);
     if (p.lanes == 8) return launch_ring<T, R, kNarrowElems, 8, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
     if (p.lanes == 16) return launch_ring<T, R, kNarrowElems, 16, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
     if (p.lanes == 32) return launch_ring<T, R, kNarrowElems, 32, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);

@@ -123,6 +123,8 @@ cudaError_t launch_pack_shape(PackArgs& a, cudaStream_t st) {
         const unsigned grid = (unsigned)((a.units + a.units_per_cta - 1) / a.units_per_cta);
         return launch_kernel(kern, grid, (unsigned)threads, 0, st, true, a);
     };
+    // Lanes of a warp for up to 256 columns (131072 x 256 bf16 18 us, a CTA of a warp each 67); then CTAs, of 16 elements a thread: with 8
+    // 16384 x 5120 56 us instead of 40, 65536 x 1024 35.3 instead of 34.7.
     if (span <= 64) return go(ssd_pack_kernel<T, V, 8, 8, SHIFTED>, 8, 128);
     if (span <= 128) return go(ssd_pack_kernel<T, V, 8, 16, SHIFTED>, 16, 128);
     if (span <= 256) return go(ssd_pack_kernel<T, V, 8, 32, SHIFTED>, 32, 128);

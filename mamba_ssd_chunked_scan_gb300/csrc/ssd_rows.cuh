@@ -303,7 +303,7 @@ __device__ __forceinline__ Two sigmoid(Two z) {
 }
 
 // A thread's part of a row, E elements: vectors of V (16 bytes of the row's type), vector c from column column(c) on; or (V = 2)
-// pairs of single elements, columns e and e + nt, whatever the alignment.  SHIFTED: see ssd_block_norm_bwd.cuh; `left`: columns to the
+// pairs of single elements, columns e and e + nt, whatever the alignment.  SHIFTED: see ssd_ring.cuh; `left`: columns to the
 // arrays' end from the row's start.
 template <int V, bool SHIFTED>
 struct Place {
@@ -398,33 +398,17 @@ __device__ __forceinline__ void store_codes(e4m3_t* row, const Place<V, SHIFTED>
     q.set(c, v);
     q.store(row, p, c);
 }
-// Vector c of a row's weights, kept in the caches (16-byte aligned with it where V > 2 and !SHIFTED); 0 outside of the row.
-template <int V, bool SHIFTED>
-__device__ __forceinline__ void weights_of(const float* p, const Place<V, SHIFTED>& at, int c, Two (&w)[V / 2]) {
+// Pair c of a row's weights, kept in the caches; 0 outside of the row.
+__device__ __forceinline__ Two pair_weights(const float* p, const Place<2, false>& at, int c) {
     const int e = at.column(c);
-    if constexpr (V == 2) {
-        w[0] = two(e < at.n ? __ldg(p + e) : 0.f, e + at.nt < at.n ? __ldg(p + e + at.nt) : 0.f);
-    } else if constexpr (SHIFTED) {
-#pragma unroll
-        for (int k = 0; k < V; k += 2)
-            w[k / 2] = two(e + k >= 0 && e + k < at.n ? __ldg(p + e + k) : 0.f, e + k + 1 >= 0 && e + k + 1 < at.n ? __ldg(p + e + k + 1) : 0.f);
-    } else {
-#pragma unroll
-        for (int k = 0; k < V; k += 4) {
-            const float4 q = e < at.n ? __ldg(reinterpret_cast<const float4*>(p + e + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            w[k / 2] = two(q.x, q.y);
-            w[k / 2 + 1] = two(q.z, q.w);
-        }
-    }
+    return two(e < at.n ? __ldg(p + e) : 0.f, e + at.nt < at.n ? __ldg(p + e + at.nt) : 0.f);
 }
 
-// V weights from column e of a row (16-byte aligned with e where V > 1 and !SHIFTED), kept in the caches; those outside of
+// V weights from column e of a row (16-byte aligned with e where !SHIFTED), kept in the caches; those outside of
 // [0, n) are 0.
 template <int V, bool SHIFTED>
 __device__ __forceinline__ void row_weights(const float* p, int e, int n, float (&w)[V]) {
-    if constexpr (V == 1) {
-        w[0] = __ldg(p + e);
-    } else if constexpr (SHIFTED) {
+    if constexpr (SHIFTED) {
 #pragma unroll
         for (int k = 0; k < V; ++k) w[k] = e + k >= 0 && e + k < n ? __ldg(p + e + k) : 0.f;
     } else {
