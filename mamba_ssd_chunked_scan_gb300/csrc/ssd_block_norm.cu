@@ -10,6 +10,9 @@
 // way through shared memory (ssd_ring.cuh) while one is worked on: a row a CTA, from registers, left HBM idle between a row's
 // loads and its stores (16384 x 5120 with its checkpoint 148 us).  Slots take few rows, so that SMs share the work as
 // they finish.  Where no vectors fit, single elements go through registers.
+//
+// HBM bounds it: gate and norm of 16384 x 5120 bf16 with its checkpoint 104 us, 95 % of the copy's rate; norm after a gated block of
+// 16384 x 2560, bf16 beside an fp32 residual, with its checkpoint 107 us, 93 %; 65536 x 1024 without gate and checkpoint 119 us, all of it.
 #include <atomic>
 
 #include "ssd_kernels.h"
