@@ -233,7 +233,7 @@ def gate_norm(y, z, weight, group_size, eps=1e-5, *, out=None, pack=False, strea
 
     With pack, returns (out, kept): kept is a dict of y and z as 8-bit rows for gate_norm_bwd (``y``, ``y_scales``, ``z``,
     ``z_scales``; one scale a row and group).  z may be a column range of a wider matrix then, and group_size any divisor of the
-    width."""
+    width up to 8192."""
     if pack:
         if out is not None:
             raise ValueError("out: not with pack")
