@@ -26,9 +26,10 @@ struct Record {
     static constexpr int dres = dout + t;
     static constexpr int h = dres + (RES ? r : 0);
     static constexpr int x = h + (RES && !HP ? r : 0);
-    static constexpr int gate = x + (XP ? 0 : t);
+    static constexpr int xs = RES ? 2 : 1;   // of x two rows' where the record is one row's otherwise
+    static constexpr int gate = x + (XP ? 0 : xs * t);
     static constexpr int codes = gate + (GATE && !XP ? t : 0);
-    static constexpr int x_codes = codes, gate_codes = x_codes + (XP ? E : 0), h_codes = gate_codes + (XP && GATE ? E : 0);
+    static constexpr int x_codes = codes, gate_codes = x_codes + (XP ? xs * E : 0), h_codes = gate_codes + (XP && GATE ? E : 0);
     static constexpr int x_scale = h_codes + (RES && HP ? E : 0);
     static constexpr int gate_scale = x_scale + (XP ? 4 : 0), h_scale = gate_scale + (XP && GATE ? 4 : 0);
     static constexpr int bytes = h_scale + (RES && HP ? 4 : 0);
@@ -68,14 +69,14 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     typedef typename Pick<HP, e4m3_t, R>::type H;
     constexpr bool kCta = LANES == 0;
     // With a residual silu and its slope stay in registers from one pass to the next, and all of a record but x is free for the next
-    // row before the last pass: one stage is enough then, which leaves room for three CTAs instead of two.
+    // row before the last pass: one stage is enough then, which leaves room for three CTAs instead of two, and a second place for x.
     constexpr bool kKeep = RES, kEarly = RES;
     constexpr bool kPairs = RES && sizeof(R) > sizeof(T);   // lanes copy for their neighbours
     const uint32_t mask = row_mask<LANES>();
     constexpr int V = Rec::kVec, C = E / V, P = V / 2;
     // the operands' first pieces
     constexpr int kD = 32 * Rec::dout, kR = 32 * Rec::dres, kX = 32 * (XP ? Rec::x_codes : Rec::x), kZ = 32 * (XP ? Rec::gate_codes : Rec::gate),
-                  kH = 32 * (HP ? Rec::h_codes : Rec::h), kStage = 32 * Rec::bytes;
+                  kH = 32 * (HP ? Rec::h_codes : Rec::h), kStage = 32 * Rec::bytes, kXs = 32 * E * (int)sizeof(X);
     __shared__ RowPart part[2];
     extern __shared__ __align__(16) unsigned char ring[];
     const int tid = kCta ? threadIdx.x : threadIdx.x % (kCta ? 32 : LANES), nt = kCta ? blockDim.x : LANES;
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             for (int s = 0; s < a.stages; ++s) {
                 unsigned char* r = rec0 + s * kStage;
                 clear_head<T, V>(r + kD, c, lane, V);
-                clear_head<X, V>(r + kX, c, lane, V);
+                for (int k = 0; k < Rec::xs; ++k) clear_head<X, V>(r + kX + k * kXs, c, lane, V);
                 if (GATE) clear_head<X, V>(r + kZ, c, lane, V);
                 if (RES) clear_head<H, V>(r + kH, c, lane, V);
                 if (RES) clear_head<R, V>(r + kR, c, lane, V);
@@ -134,10 +135,8 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
     unsigned char *q_dx = out(a.dx, at0, sizeof(T)), *q_dres = out(a.dres_out, at0, sizeof(R)), *q_out = out(a.out, at0, sizeof(T)),
                   *q_dgate = out(a.dgate, (int64_t)line * a.dgate_stride + first - shift, sizeof(T));
     uint32_t unit_ask = unit0;
-    // Ask for the next row's x (kWhich 1), for the rest (0) or for all of it (2), into a stage.
-    auto ask_row = [&](auto which, int stage) {
-        constexpr int kWhich = decltype(which)::value;
-        constexpr bool kRest = kWhich != 1, kAskX = kWhich != 0;
+    // Ask for the next row, into a stage; x into its place at `x_at`.
+    auto ask_row = [&](int stage, int x_at) {
         if (unit_ask < my_units) {
             const uint32_t to = (uint32_t)__cvta_generic_to_shared(rec0) + stage * kStage;
 #pragma unroll
@@ -145,27 +144,23 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
                 const int e = e0 + c * span;
                 const uint32_t t = (uint32_t)tid * V;
                 const int64_t s = c * span;
-                if (kRest && (!RES || next)) ask<T, V, SHIFTED>(to + kD, c, lane, p_dout + s * sizeof(T), t * sizeof(T), e, n);
-                if (kRest && next) ask<H, V, SHIFTED>(to + kH, c, lane, p_h + s * sizeof(H), t * sizeof(H), e, n);
-                if (kRest && RES) ask<R, V, SHIFTED>(to + kR, c, lane, p_dres + s * sizeof(R), t * sizeof(R), e, n);
-                if (kRest && GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, p_gate + s * sizeof(X), t * sizeof(X), e, n);
-                if (kAskX) ask<X, V, SHIFTED>(to + kX, c, lane, p_x + s * sizeof(X), t * sizeof(X), e, n);
+                if (!RES || next) ask<T, V, SHIFTED>(to + kD, c, lane, p_dout + s * sizeof(T), t * sizeof(T), e, n);
+                if (next) ask<H, V, SHIFTED>(to + kH, c, lane, p_h + s * sizeof(H), t * sizeof(H), e, n);
+                if (RES) ask<R, V, SHIFTED>(to + kR, c, lane, p_dres + s * sizeof(R), t * sizeof(R), e, n);
+                if (GATE) ask<X, V, SHIFTED>(to + kZ, c, lane, p_gate + s * sizeof(X), t * sizeof(X), e, n);
+                ask<X, V, SHIFTED>(to + kX + x_at, c, lane, p_x + s * sizeof(X), t * sizeof(X), e, n);
             }
-            if (kRest) {
-                if (XP) copy_async<4>(to + 32 * Rec::x_scale + 4 * lane, a.x_scales + unit_ask, 4);
-                if (XP && GATE) copy_async<4>(to + 32 * Rec::gate_scale + 4 * lane, a.gate_scales + unit_ask, 4);
-                if (HP && next) copy_async<4>(to + 32 * Rec::h_scale + 4 * lane, a.h_scales + unit_ask, 4);
-                if (!RES || next) p_dout += far * sizeof(T);
-                if (GATE) p_gate += gate_far * sizeof(X);
-                if (next) p_h += far * sizeof(H);
-                if (RES) p_dres += far * sizeof(R);
-            }
-            if (kAskX) {
-                unit_ask += unit_step;
-                p_x += far * sizeof(X);
-            }
+            if (XP) copy_async<4>(to + 32 * Rec::x_scale + 4 * lane, a.x_scales + unit_ask, 4);
+            if (XP && GATE) copy_async<4>(to + 32 * Rec::gate_scale + 4 * lane, a.gate_scales + unit_ask, 4);
+            if (HP && next) copy_async<4>(to + 32 * Rec::h_scale + 4 * lane, a.h_scales + unit_ask, 4);
+            if (!RES || next) p_dout += far * sizeof(T);
+            if (GATE) p_gate += gate_far * sizeof(X);
+            if (next) p_h += far * sizeof(H);
+            if (RES) p_dres += far * sizeof(R);
+            p_x += far * sizeof(X);
+            unit_ask += unit_step;
         }
-        if (kAskX) copies_commit();
+        copies_commit();
     };
     auto sums = [&](float (&s)[2], int turn) {
         if constexpr (kCta) row_sums(s, false, part[turn]);
@@ -179,19 +174,19 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             dw[c][k] = both(0.f);
             if (RES) dn[c][k] = both(0.f);
         }
-    for (int s = 0; s < (kEarly ? 1 : a.stages - 1); ++s) ask_row(Number<2>(), s);
-    int stage = 0, turn = 0;
+    for (int s = 0; s < (kEarly ? 1 : a.stages - 1); ++s) ask_row(s, 0);
+    int stage = 0, turn = 0, x_at = 0;
     for (uint32_t unit = unit0; unit < my_units; unit += unit_step) {
         unsigned char* const rec = rec0 + stage * kStage;
         if constexpr (!kEarly) {
-            ask_row(Number<2>(), stage > 0 ? stage - 1 : a.stages - 1);   // where the row before lay
+            ask_row(stage > 0 ? stage - 1 : a.stages - 1, 0);   // where the row before lay
             if (++stage == a.stages) stage = 0;
         }
         copies_wait(kEarly ? 0 : a.stages - 1);
         if constexpr (kPairs) __syncwarp(mask);
         if (SHIFTED && e0 < 0) {
             if (!RES || next) clear_head<T, V>(rec + kD, 0, lane, shift);
-            clear_head<X, V>(rec + kX, 0, lane, shift);
+            clear_head<X, V>(rec + kX + x_at, 0, lane, shift);
             if (GATE) clear_head<X, V>(rec + kZ, 0, lane, shift);
             if (next) clear_head<H, V>(rec + kH, 0, lane, shift);
             if (RES) clear_head<R, V>(rec + kR, 0, lane, shift);
@@ -202,7 +197,8 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
         if (XP && GATE) gs = *reinterpret_cast<const float*>(rec + 32 * Rec::gate_scale + 4 * lane);
         if (HP && next) hs = *reinterpret_cast<const float*>(rec + 32 * Rec::h_scale + 4 * lane);
         auto dout_of = [&](int c, Two (&v)[P]) { to_pairs(piece_vector<T, V>(rec + kD, c, lane), v); };
-        auto x_of = [&](int c, Two (&v)[P]) { to_pairs(piece_vector<X, V>(rec + kX, c, lane), v); };
+        const unsigned char* const rec_x = rec + kX + x_at;
+        auto x_of = [&](int c, Two (&v)[P]) { to_pairs(piece_vector<X, V>(rec_x, c, lane), v); };
         auto gate_of = [&](int c, Two (&v)[P]) {
             to_pairs(piece_vector<X, V>(rec + kZ, c, lane), v);
             if constexpr (XP) {
@@ -291,7 +287,10 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             }
         }
         if constexpr (kPairs) __syncwarp(mask);
-        if constexpr (kEarly) ask_row(Number<0>(), 0);   // what this row needs no more
+        if constexpr (kEarly) {   // this row needs no more than x
+            x_at ^= kXs;
+            ask_row(0, x_at);
+        }
         float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
         sums(s, turn);
         turn ^= 1;
@@ -336,7 +335,6 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             }
             put<T, V, SHIFTED>(q_dx + c * span * (int64_t)sizeof(T), t * sizeof(T), e, n, mask, du);
         }
-        if constexpr (kEarly) ask_row(Number<1>(), 0);
         q_dx += far * sizeof(T);
         if (GATE) q_dgate += (int64_t)step * a.dgate_stride * (int64_t)sizeof(T);
         if (RES) q_dres += far * sizeof(R);

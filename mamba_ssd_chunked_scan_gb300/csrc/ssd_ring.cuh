@@ -32,7 +32,6 @@ __device__ __forceinline__ void copies_wait(int n) {
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <int N> struct Number { static constexpr int value = N; };
 template <bool, typename A, typename B> struct Pick { typedef A type; };
 template <typename A, typename B> struct Pick<false, A, B> { typedef B type; };
 
