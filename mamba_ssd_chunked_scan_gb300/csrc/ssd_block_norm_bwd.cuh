@@ -574,10 +574,11 @@ inline int set_slots(BlockNormBwdArgs& a, const RowPlan& p) {   // and how many 
 }
 
 // Rows of up to 256 columns take 8, 16 or 32 lanes of a warp, others a CTA (131072 x 256 with a residual 122 us, by CTAs of a warp
-// 129; without 64, 71): 8 elements a thread up to 512 columns, or 1280 of fp32 or of rows of no whole vectors, then 16.  33.5 M
-// elements with gate and residual, 8 and 16 elements a thread: bf16 768 columns 152 and 129 us, 1024 148 and 133, 1280 148 and 133
-// (512 by single warps of 16: 198; by 8 136); fp32 768 columns 168 and 189, 1024 165 and 173, 2048 198 and 184; 1023 columns 176
-// and 185.  Codes of 1024 columns 163 and 110.
+// 129; without 64, 71): 8 elements a thread up to 512 columns, or up to 1280 of fp32, then 16.  33.5 M elements with gate and fp32
+// residual, 8 and 16 elements a thread: bf16 768 columns 145 and 121 us, 1024 140 and 132, 1280 137 and 124 (512 by single warps of 16:
+// 198; by 8 133); fp32 768 columns 164 and 186, 1024 176 and 166, 1280 168 and 182, 2048 198 and 169.  Rows of no whole vectors: 765
+// columns 188 and 154, without a residual 1023 columns 106 and 87, from 8 bits 1261 columns 148 and 138; but with a residual 1023
+// columns 161 and 172, 1261 140 and 147 (their last warp's threads are idle), so 8 for those beyond 1024.
 constexpr int kNarrowSpan = 512, kNarrowSpanLong = 1280;
 inline RowPlan vector_plan(int span, int narrow) {
     RowPlan p = {};
@@ -632,7 +633,8 @@ cudaError_t launch_ring(BlockNormBwdArgs& a, RowPlan p, int* lines, cudaStream_t
 
 template <typename T, typename R, bool SHIFTED, bool GATE, bool RES, bool XP, bool HP>
 cudaError_t launch_vectors(BlockNormBwdArgs& a, int* lines, cudaStream_t st) {
-    const RowPlan p = vector_plan(SHIFTED ? vector_span(a.size) : a.size, SHIFTED || sizeof(T) == 4 ? kNarrowSpanLong : kNarrowSpan);
+    const int span = SHIFTED ? vector_span(a.size) : a.size;
+    const RowPlan p = vector_plan(span, sizeof(T) == 4 || (SHIFTED && RES && !XP && span > 1024) ? kNarrowSpanLong : kNarrowSpan);
     if (p.lanes == 8) return launch_ring<T, R, kNarrowElems, 8, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
     if (p.lanes == 16) return launch_ring<T, R, kNarrowElems, 16, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
     if (p.lanes == 32) return launch_ring<T, R, kNarrowElems, 32, SHIFTED, GATE, RES, XP, HP>(a, p, lines, st);
