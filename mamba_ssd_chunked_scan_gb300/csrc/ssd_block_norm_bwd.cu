@@ -15,10 +15,10 @@
 // slots: arithmetic is on pairs of numbers, and a record's pieces lie at constant offsets.
 //
 // Times with the shares' sum (7 us of them), and parts of the copy's rate: gate and norm 16384 x 5120 bf16 140 us, 89 %; from 8 bits
-// 12289 x 5120, with the result computed again, 121 us, 77 % (issue slots 57 % busy: codes are decoded in both passes); with a residual
-// in fp32 16384 x 2560 163 us, 83 % (one stage: two barriers a row that three CTAs an SM have to cover); all operands in 8 bits
-// 9001 x 1533 71 us, 37 % (1536 columns 53 us: 15 rows a slot, each with three barriers; at 1533 97 of 128 threads have columns, and
-// first and last vectors go by elements).
+// 12289 x 5120, with the result computed again, 121 us, 77 % (issue slots 57 % busy, shared memory's and the stores' wavefronts 62 %:
+// codes are decoded and the weights read in both passes); with a residual in fp32 16384 x 2560 155 us, 88 % (163 us while x was asked
+// for after the last pass); all operands in 8 bits 9001 x 1533 68 us, 39 % (1536 columns 52 us: three passes a row, the codes decoded in
+// each; at 1533 97 of 128 threads have columns, and first and last vectors go by elements).
 #include "ssd_block_norm_bwd.cuh"
 
 namespace ssd {
