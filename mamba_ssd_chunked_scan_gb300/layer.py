@@ -12,11 +12,11 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 
 import torch
 
-from . import _lib
-
+_lib = importlib.import_module(__package__ + "._lib")   # the module itself: the package's own name finds it anew at each use
 _lib_c = _lib.lib
 _BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _CODE = {_F32: _lib.SSD_F32, _BF16: _lib.SSD_BF16, _E4M3: _lib.SSD_E4M3}

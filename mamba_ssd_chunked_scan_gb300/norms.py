@@ -12,8 +12,7 @@ import ctypes
 
 import torch
 
-from . import _lib
-from .layer import (_BF16, _CODE, _E4M3, _F32, _check, _current_device, _device, _elsewhere, _empty, _lib_c, _need, _ptr, _raw_stream,
+from .layer import (_lib, _BF16, _CODE, _E4M3, _F32, _check, _current_device, _device, _elsewhere, _empty, _lib_c, _need, _ptr, _raw_stream,
                     _real, _row_stride, _width)
 
 
