@@ -353,6 +353,8 @@ struct LinearDpreArgs {
     float* shares;         // [slabs * n], or NULL
     float* dbias;          // [n], or NULL
     int slab_rows;
+    PackArgs expand;       // out not NULL: x to be unpacked to bf16 in the same launch, by CTAs from number ctas on
+    unsigned ctas;
 };
 
 // Constants of division by an invariant divisor d >= 1 through one high
@@ -396,6 +398,7 @@ cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, cudaStream_t st);
 cudaError_t launch_share_sum(const float* shares, int nshares, int width, int columns, float* dw, float* next, bool early, cudaStream_t st);
 cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
 cudaError_t launch_unpack(const PackArgs& a, cudaStream_t st);
+unsigned unpack_flat_ctas(const PackArgs& a);   // CTAs of 256 threads that unpack_flat takes for it; 0: not to be had so
 cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t st);
 int64_t block_norm_bwd_lines(int64_t rows, int size, int groups);   // rows that the backward's grid walks at once
 cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, cudaStream_t st);

@@ -250,6 +250,14 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
             d.k = p->k;
         }
     }
+    PackArgs u = {};   // x as the products' operand
+    if (x_scales && dw) {
+        u.units = p->m; u.size = p->k; u.groups = 1; u.dtype = SSD_BF16; u.stride = p->ldx;
+        u.codes = const_cast<void*>(x); u.scales = const_cast<float*>(x_scales); u.out = ws + l.rows_off;
+        u.power_only = factors;
+    }
+    const bool together = u.out && (d.dpre || dbias) && unpack_flat_ctas(u) > 0;
+    if (together) d.expand = u;
     if ((d.dpre || dbias) && launch_linear_dpre(d, st) != cudaSuccess) return SSD_ERR_CUDA;
     const LinearOperand g = {l.own_dpre ? (const void*)(ws + l.dpre_off) : dy, l.own_dpre ? l.ldp : p->n, false};
     LinearArgs a = {};
@@ -271,11 +279,7 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
         a.keep_status = dx != nullptr;
         a.w = {x, p->ldx, true};
         if (x_scales) {
-            PackArgs u = {};
-            u.units = p->m; u.size = p->k; u.groups = 1; u.dtype = SSD_BF16; u.stride = p->ldx;
-            u.codes = const_cast<void*>(x); u.scales = const_cast<float*>(x_scales); u.out = ws + l.rows_off;
-            u.power_only = factors;
-            if (launch_unpack(u, st) != cudaSuccess) return SSD_ERR_CUDA;
+            if (!together && launch_unpack(u, st) != cudaSuccess) return SSD_ERR_CUDA;
             a.w = {ws + l.rows_off, p->k, true};
         }
         if (launch_linear(a, l.dw, st) != cudaSuccess) return SSD_ERR_CUDA;

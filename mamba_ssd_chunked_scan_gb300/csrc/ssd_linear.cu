@@ -34,7 +34,7 @@
 
 #include "ssd_common.cuh"
 #include "ssd_kernels.h"
-#include "ssd_rows.cuh"
+#include "ssd_unpack.cuh"
 #include "tc_ptx.cuh"
 
 namespace ssd {
@@ -735,14 +735,19 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
 // flight per warp (8192 x 5120 42 us, 89 % of the copy's rate; with pre in 8 bits 47 us, 66 %).
 constexpr int kSlabRows = 128, kSlabCols = 256;
 // P: the type of pre (e4m3: times its row's scale; two rows in flight, since decoding takes the registers that more warps run on: all
-// gradients of 8192 x 2560 to 5120 293 us, with four 297, with eight 309).  Where x comes as 8-bit rows, their scales' factors go into dpre before its
+// gradients of 8192 x 2560 to 5120 293 us, with four 297, with eight 309).  CTAs from a.ctas on unpack x (290 us, 100 x 512 to 512 16.3;
+// in a launch of its own 293 and 18.3).  Where x comes as 8-bit rows, their scales' factors go into dpre before its
 // rounding, so that the product with the codes rounds no operand twice; dx's epilogue takes them out.
 template <typename P, int V>
-__global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
+__global__ void __launch_bounds__(256) ssd_linear_dpre(const __grid_constant__ LinearDpreArgs a) {
     __shared__ float part[8][kSlabCols];
     constexpr int C = 8 / V, kRowsAhead = sizeof(P) == 1 ? 2 : 4;
     pdl_trigger();
     pdl_wait();
+    if (blockIdx.x >= a.ctas) {
+        unpack_flat<bf16_t>(a.expand, blockIdx.x - a.ctas);
+        return;
+    }
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const unsigned ncol = (unsigned)(a.n + kSlabCols - 1) / kSlabCols, slab = blockIdx.x / ncol, slab_rows = a.slab_rows;
     const int c0 = (int)(blockIdx.x - slab * ncol) * kSlabCols, n0 = c0 + lane * V;
@@ -753,7 +758,7 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a) {
     bf16_t* dp = a.dpre ? static_cast<bf16_t*>(a.dpre) + (size_t)m0 * a.ldp + n0 : nullptr;
     float sum[C][V] = {};
     if (a.ones)
-        for (int k = blockIdx.x * 256 + threadIdx.x; k < a.k; k += gridDim.x * 256) a.ones[k] = 1.f;
+        for (int k = blockIdx.x * 256 + threadIdx.x; k < a.k; k += a.ctas * 256) a.ones[k] = 1.f;
     for (int k0 = w; k0 < rows; k0 += 8 * kRowsAhead) {
         Raw<bf16_t, V> d[kRowsAhead][C];
         Raw<P, V> q[kRowsAhead][C];
@@ -1033,7 +1038,8 @@ cudaError_t launch_linear_dpre(const LinearDpreArgs& args, cudaStream_t st) {
     LinearDpreArgs a = args;
     a.slab_rows = dpre_slab_rows(a.m, a.n);
     const int64_t slabs = linear_dpre_slabs(a.m, a.n);
-    const unsigned grid = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
+    a.ctas = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
+    const unsigned grid = a.ctas + (a.expand.out ? unpack_flat_ctas(a.expand) : 0);
     const bool codes = a.pre_scales != nullptr;
     const bool vec = a.n % 8 == 0 && ((uintptr_t)a.pre & (codes ? 7 : 15)) == 0;
     const cudaError_t e = launch_kernel(codes ? (vec ? ssd_linear_dpre<e4m3_t, 8> : ssd_linear_dpre<e4m3_t, 1>)

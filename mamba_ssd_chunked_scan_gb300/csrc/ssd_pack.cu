@@ -7,10 +7,12 @@
 // of it); unpacking goes by 16 elements of the flat array, whatever the rows' width (4099 x 2557 to fp32 12 us, 63 %: 8 us of HBM
 // leave a launch's start and end uncovered; 16384 x 2560 to bf16 20 us, 91 %).
 #include "ssd_kernels.h"
-#include "ssd_rows.cuh"
+#include "ssd_unpack.cuh"
 
 namespace ssd {
 namespace {
+
+bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 template <typename T, int V, int E, int LANES, bool SHIFTED>
 __global__ void __launch_bounds__(1024) ssd_pack_kernel(const __grid_constant__ PackArgs a) {
@@ -38,57 +40,11 @@ __global__ void __launch_bounds__(1024) ssd_pack_kernel(const __grid_constant__ 
     }
 }
 
-constexpr int kFlat = 16;   // elements per thread of the flat array
-
-// Where codes' rows lie together and both arrays start on 16 bytes: a thread takes 16 elements of the flat array, of one unit or of
-// several.  A CTA's first unit is divided out once, in 64 bits; the rest is in 32.
 template <typename T>
-__global__ void __launch_bounds__(256) ssd_unpack_kernel(const __grid_constant__ PackArgs a) {
+__global__ void __launch_bounds__(kFlatThreads) ssd_unpack_kernel(const __grid_constant__ PackArgs a) {
     pdl_trigger();
     pdl_wait();
-    const int64_t total = a.units * a.size, begin = (int64_t)blockIdx.x * 256 * kFlat, at = begin + threadIdx.x * kFlat;
-    if (at >= total) return;
-    const int64_t unit0 = begin / a.size;
-    const uint32_t n = a.size, k = (uint32_t)(begin - unit0 * a.size) + threadIdx.x * kFlat, over = k / n;
-    uint32_t e = k - over * n;   // the first element's column in its unit
-    const float* scales = a.scales + unit0 + over;
-    const e4m3_t* codes = static_cast<const e4m3_t*>(a.codes) + at;
-    T* out = static_cast<T*>(a.out) + at;
-    const int count = total - at < kFlat ? (int)(total - at) : kFlat;
-    Raw<e4m3_t, kFlat> q;
-    q.zero();
-    if (count == kFlat) q.load(codes);
-    else q.load_some(codes, count);
-    Two v[kFlat / 2];
-    to_pairs(q, v);
-    auto scale_at = [&](const float* p) { return a.power_only ? scale_power(__ldg(p)) : __ldg(p); };
-    float s = scale_at(scales);
-    if (e + kFlat <= n) {
-#pragma unroll
-        for (int j = 0; j < kFlat / 2; ++j) v[j] = v[j] * both(s);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kFlat; ++j) {
-            if (e == n && j < count) {
-                e = 0;
-                s = scale_at(++scales);
-            }
-            ++e;
-            if (j % 2) v[j / 2] = two(low(v[j / 2]), high(v[j / 2]) * s);
-            else v[j / 2] = two(low(v[j / 2]) * s, high(v[j / 2]));
-        }
-    }
-    constexpr int V = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int h = 0; h < kFlat / V; ++h) {
-        Two p[V / 2];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) p[j] = v[h * (V / 2) + j];
-        Raw<T, V> o;
-        from_pairs(p, o);
-        if (h * V + V <= count) o.store(out + h * V);
-        else o.store_within(out, h * V, count);
-    }
+    unpack_flat<T>(a, blockIdx.x);
 }
 
 // Any alignment, and codes whose rows are `stride` apart: V elements of an output row per thread.
@@ -115,7 +71,6 @@ __global__ void __launch_bounds__(256) ssd_unpack_rows_kernel(const __grid_const
     o.store(static_cast<T*>(a.out) + row * width + e);
 }
 
-bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 template <typename T, int V, bool SHIFTED>
 cudaError_t launch_pack_shape(PackArgs& a, cudaStream_t st) {
@@ -147,16 +102,18 @@ cudaError_t launch_pack_typed(PackArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_unpack_typed(const PackArgs& a, cudaStream_t st) {
     const int64_t width = (int64_t)a.size * a.groups, rows = a.units / a.groups;
-    if (a.stride == width && on16(a.codes) && on16(a.out) && a.size < 1 << 30) {
-        const int64_t ctas = (rows * width + 256 * kFlat - 1) / (256 * kFlat);
-        return launch_kernel(ssd_unpack_kernel<T>, (unsigned)ctas, 256, 0, st, true, a);
-    }
+    if (const unsigned ctas = unpack_flat_ctas(a)) return launch_kernel(ssd_unpack_kernel<T>, ctas, kFlatThreads, 0, st, true, a);
     const bool vec = width % 8 == 0 && a.stride % 8 == 0 && on16(a.out) && ((uintptr_t)a.codes % 8) == 0;
     const int64_t ctas = rows * ((width + 256 * (vec ? 8 : 1) - 1) / (256 * (vec ? 8 : 1)));
     return launch_kernel(vec ? ssd_unpack_rows_kernel<T, 8> : ssd_unpack_rows_kernel<T, 1>, (unsigned)ctas, 256, 0, st, true, a);
 }
 
 }  // namespace
+
+unsigned unpack_flat_ctas(const PackArgs& a) {
+    if (a.stride != (int64_t)a.size * a.groups || !on16(a.codes) || !on16(a.out)) return 0;
+    return (unsigned)((a.units * a.size + kFlatThreads * kFlat - 1) / (kFlatThreads * kFlat));
+}
 
 cudaError_t launch_pack(const PackArgs& args, cudaStream_t st) {
     PackArgs a = args;
