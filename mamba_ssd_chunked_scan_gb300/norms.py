@@ -219,8 +219,8 @@ def block_norm_bwd(dout, dresidual, x, h, weight, gate=None, next_weight=None, *
     """Gradients of <dout, out> + <dresidual, residual> of one block_norm call (out in x's type).
 
     dout (..., width) in dtype, bf16 or fp32 (None without next_weight); dresidual in the residual's type; x and gate as given to
-    it, h its ``residual`` (None without next_weight), each of them 8-bit rows where its scales (...) are given: the forward's with
-    pack, or pack_rows'.  dtype is that of dout, x and gate; it need only be given where there is no dout and they are 8-bit
+    it, h its ``residual`` (not read without next_weight, and may be None then), each of them 8-bit rows where its scales (...) are
+    given: the forward's with pack, or pack_rows'.  dtype is that of dout, x and gate; it need only be given where there is no dout and they are 8-bit
     rows.  dgate may be given to be written in place, at any row stride.  Returns a dict: ``dx``, ``dgate`` (None
     without a gate) in dtype, ``dresidual`` in the residual's, ``dweight`` and ``dnext_weight`` (None without
     next_weight) fp32."""
@@ -231,8 +231,12 @@ def block_norm_bwd(dout, dresidual, x, h, weight, gate=None, next_weight=None, *
                                   gate_scales=gate_scales, dgate=dgate, dtype=dtype)
     rtype, shape, device = dresidual.dtype, dresidual.shape, dresidual.device
     width = _width("dresidual", shape)
-    if (dout is None) != (next_weight is None) or (h is None) != (next_weight is None) or (h is None and h_scales is not None):
-        raise ValueError("dout, h: given with next_weight, and only then")
+    if (dout is None) != (next_weight is None):
+        raise ValueError("dout: given with next_weight, and only then")
+    if h is None and (next_weight is not None or h_scales is not None):
+        raise ValueError("h: given with next_weight, and with h_scales")
+    if next_weight is None:
+        h = h_scales = None
     if dtype is None:
         dtype = dout.dtype if dout is not None else x.dtype if x_scales is None else None
     _real("dtype", dtype)
