@@ -36,12 +36,15 @@ struct Record {
     static constexpr int weight = E * 4, weights = (RES ? 2 : 1) * weight;   // the weights' record
 };
 
-// silu(z) and its slope s + z s (1 - s) = s (1 - silu) + silu.
+// silu's slope s + silu (1 - s), of s = 1 / (1 + e^-z) and silu = z s.  Where s is 1 so is the slope, however large z is (as
+// s (1 - silu) + silu it is 0 or 2 from z = 2^24 on, where 1 - silu is rounded).
+__device__ __forceinline__ Two silu_slope(Two s, Two silu) { return fma(silu, fma(s, both(-1.f), both(1.f)), s); }
+// silu(z) and its slope.
 template <typename T>
 __device__ __forceinline__ void silu(Two z, Two& value, Two& slope) {
     const Two s = sigmoid<T>(z);
     value = z * s;
-    slope = fma(s, fma(value, both(-1.f), both(1.f)), value);
+    slope = silu_slope(s, value);
 }
 
 // A slot's rows: place.row, place.row + place.step, ... before place.end, one group of each; and the row of shares that it leaves.
@@ -325,8 +328,7 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             if constexpr (GATE) {
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    // silu's slope: s + gate s (1 - s) = s (1 - silu) + silu
-                    const Two slope = kKeep ? sl[c][k] : fma(sg[c][k], fma(z[k], both(-1.f), both(1.f)), z[k]);
+                    const Two slope = kKeep ? sl[c][k] : silu_slope(sg[c][k], z[k]);
                     o[k] = du[k] * (x[k] * slope);
                     if (XP && !kKeep) o[k] = o[k] * both(xs);
                     du[k] = du[k] * z[k];
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(loose_threads_sm(E)) ssd_block_norm_bwd_loose(
             if (!RES && a.out) put_loose(static_cast<T*>(a.out) + at, c, tid, nt, n, o * w);
             if constexpr (GATE) {
                 put_loose(static_cast<T*>(a.dgate) + (int64_t)row * a.dgate_stride + first, c, tid, nt, n,
-                          du * (x * fma(sg[c], fma(z, both(-1.f), both(1.f)), z)));
+                          du * (x * silu_slope(sg[c], z)));
                 du = du * z;
             }
             put_loose(static_cast<T*>(a.dx) + at, c, tid, nt, n, du);
