@@ -295,12 +295,12 @@ __global__ void __launch_bounds__(threads_sm(E, RES)) ssd_block_norm_bwd_kernel(
             ask_row(0, x_at);
         }
         float s[2] = {low(uu) + high(uu), low(pu) + high(pu)};
-        sums(s, turn);
-        turn ^= 1;
-        if (XP) {
+        if (XP) {   // a thread's sums already: codes are up to 448, and all of a row's times large gates may pass fp32's range
             s[0] = s[0] * xs * xs;
             s[1] *= xs;
         }
+        sums(s, turn);
+        turn ^= 1;
         const float rstd = rsqrt_of(s[0] * a.inv_size + a.eps), mean = -(s[1] * a.inv_size * rstd * rstd) * rstd;
         const Two r1 = both(rstd), r1x = both(XP ? rstd * xs : rstd), k1 = both(XP ? mean * xs : mean);
 #pragma unroll
