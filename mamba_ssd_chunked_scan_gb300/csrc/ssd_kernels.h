@@ -345,14 +345,17 @@ struct LinearDpreArgs {
     const void* dy;
     const void* pre;       // or NULL (no activation)
     const float* pre_scales;   // [m]: pre is e4m3 codes; or NULL
-    const float* x_scales;     // [m], or NULL: dpre is to be multiplied by the factors of these scales (see scale_factor)
-    float* inv_factors;        // [m]: their reciprocals, written
-    float* ones;               // [k]: written
-    int k;
     void* dpre;            // (m, ldp) bf16, or NULL
     float* shares;         // [slabs * n], or NULL
     float* dbias;          // [n], or NULL
     int slab_rows;
+};
+// What comes with x in 8-bit rows.
+struct LinearDpreRows {
+    const float* x_scales;     // [m], or NULL: dpre is to be multiplied by the factors of these scales (see scale_factor)
+    float* inv_factors;        // [m]: their reciprocals, written; or NULL
+    float* ones;               // [k]: written; or NULL
+    int k;
     PackArgs expand;       // out not NULL: x to be unpacked to bf16 in the same launch, by CTAs from number ctas on
     unsigned ctas;
 };
@@ -409,7 +412,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // NULL when the drive
 LinearPlan linear_plan(int64_t rows, int64_t cols, int64_t kbytes, bool may_swap);
 cudaError_t launch_linear(const LinearArgs& a, const LinearPlan& plan, cudaStream_t st);
 int64_t linear_dpre_slabs(int64_t m, int n);
-cudaError_t launch_linear_dpre(const LinearDpreArgs& a, cudaStream_t st);
+cudaError_t launch_linear_dpre(const LinearDpreArgs& a, const LinearDpreRows& x, cudaStream_t st);
 size_t bwd_smem_bytes(int Qb, int P, int N);
 int bwd_chunk(int P, int N, size_t smem_limit);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t st);

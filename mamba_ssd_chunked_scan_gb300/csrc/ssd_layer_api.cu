@@ -241,13 +241,14 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
     d.dpre = l.own_dpre && (dx || dw) ? ws + l.dpre_off : nullptr;
     d.shares = dbias ? (float*)(ws + l.shares_off) : nullptr;
     d.dbias = dbias;
+    LinearDpreRows e = {};
     const bool factors = x_scales && dw && d.dpre;
     if (factors) {
-        d.x_scales = x_scales;
+        e.x_scales = x_scales;
         if (dx) {
-            d.inv_factors = (float*)(ws + l.inv_off);
-            d.ones = (float*)(ws + l.ones_off);
-            d.k = p->k;
+            e.inv_factors = (float*)(ws + l.inv_off);
+            e.ones = (float*)(ws + l.ones_off);
+            e.k = p->k;
         }
     }
     PackArgs u = {};   // x as the products' operand
@@ -257,8 +258,8 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
         u.power_only = factors;
     }
     const bool together = u.out && (d.dpre || dbias) && unpack_flat_ctas(u) > 0;
-    if (together) d.expand = u;
-    if ((d.dpre || dbias) && launch_linear_dpre(d, st) != cudaSuccess) return SSD_ERR_CUDA;
+    if (together) e.expand = u;
+    if ((d.dpre || dbias) && launch_linear_dpre(d, e, st) != cudaSuccess) return SSD_ERR_CUDA;
     const LinearOperand g = {l.own_dpre ? (const void*)(ws + l.dpre_off) : dy, l.own_dpre ? l.ldp : p->n, false};
     LinearArgs a = {};
     a.dtype = SSD_BF16; a.act = SSD_ACT_NONE;
@@ -268,8 +269,8 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
         a.m = p->m; a.n = p->k; a.k = p->n; a.y = dx;
         a.x = g;
         a.w = {w, p->k, true};
-        a.x_scales = d.inv_factors;
-        a.w_scales = d.ones;
+        a.x_scales = e.inv_factors;
+        a.w_scales = e.ones;
         if (launch_linear(a, l.dx, st) != cudaSuccess) return SSD_ERR_CUDA;
         a.x_scales = a.w_scales = nullptr;
     }

@@ -738,14 +738,16 @@ constexpr int kSlabRows = 128, kSlabCols = 256;
 // gradients of 8192 x 2560 to 5120 293 us, with four 297, with eight 309).  CTAs from a.ctas on unpack x (290 us, 100 x 512 to 512 16.3;
 // in a launch of its own 293 and 18.3).  Where x comes as 8-bit rows, their scales' factors go into dpre before its
 // rounding, so that the product with the codes rounds no operand twice; dx's epilogue takes them out.
-template <typename P, int V>
-__global__ void __launch_bounds__(256) ssd_linear_dpre(const __grid_constant__ LinearDpreArgs a) {
+// X: whether x does.  What only that takes lies in an argument of its own, so that the others stay in registers (in one kernel for both
+// single elements of 32768 x 1001 bf16 took 131 us instead of 78, vectors of 8192 x 5120 49 instead of 46).
+template <typename P, int V, bool X>
+__global__ void __launch_bounds__(256) ssd_linear_dpre(LinearDpreArgs a, const __grid_constant__ LinearDpreRows x) {
     __shared__ float part[8][kSlabCols];
     constexpr int C = 8 / V, kRowsAhead = sizeof(P) == 1 ? 2 : 4;
     pdl_trigger();
     pdl_wait();
-    if (blockIdx.x >= a.ctas) {
-        unpack_flat<bf16_t>(a.expand, blockIdx.x - a.ctas);
+    if (X && blockIdx.x >= x.ctas) {
+        unpack_flat<bf16_t>(x.expand, blockIdx.x - x.ctas);
         return;
     }
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -757,17 +759,19 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(const __grid_constant__ L
     const P* pre = a.pre ? static_cast<const P*>(a.pre) + (size_t)m0 * a.n + n0 : nullptr;
     bf16_t* dp = a.dpre ? static_cast<bf16_t*>(a.dpre) + (size_t)m0 * a.ldp + n0 : nullptr;
     float sum[C][V] = {};
-    if (a.ones)
-        for (int k = blockIdx.x * 256 + threadIdx.x; k < a.k; k += a.ctas * 256) a.ones[k] = 1.f;
+    if (X && x.ones)
+        for (int k = blockIdx.x * 256 + threadIdx.x; k < x.k; k += x.ctas * 256) x.ones[k] = 1.f;
     for (int k0 = w; k0 < rows; k0 += 8 * kRowsAhead) {
         Raw<bf16_t, V> d[kRowsAhead][C];
         Raw<P, V> q[kRowsAhead][C];
-        float scale[sizeof(P) == 1 ? kRowsAhead : 1], factor[kRowsAhead];
+        float scale[sizeof(P) == 1 ? kRowsAhead : 1], factor[X ? kRowsAhead : 1];
+        if constexpr (X) {
 #pragma unroll
-        for (int u = 0; u < kRowsAhead; ++u) {
-            const int k = k0 + 8 * u;
-            factor[u] = a.x_scales && k < rows ? scale_factor(__ldg(a.x_scales + m0 + k)) : 1.f;
-            if (a.inv_factors && k < rows && c0 == 0 && lane == 0) a.inv_factors[m0 + k] = 1.f / factor[u];
+            for (int u = 0; u < kRowsAhead; ++u) {
+                const int k = k0 + 8 * u;
+                factor[u] = x.x_scales && k < rows ? scale_factor(__ldg(x.x_scales + m0 + k)) : 1.f;
+                if (x.inv_factors && k < rows && c0 == 0 && lane == 0) x.inv_factors[m0 + k] = 1.f / factor[u];
+            }
         }
         if constexpr (sizeof(P) == 1) {
 #pragma unroll
@@ -804,16 +808,20 @@ __global__ void __launch_bounds__(256) ssd_linear_dpre(const __grid_constant__ L
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[e] *= act_slope(t[e], a.act);
                 }
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum[c][e] += v[e];
                 if (dp) {
                     Raw<bf16_t, V> o;
+                    if constexpr (X) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) v[e] *= factor[u];
-                    o.set(v);
+                        for (int e = 0; e < V; ++e) t[e] = v[e] * factor[u];
+                        o.set(t);
+                    } else {
+                        o.set(v);
+                    }
                     // read next by the products, so left in L2
                     *reinterpret_cast<typename Raw<bf16_t, V>::W*>(dp + (size_t)k * a.ldp + 32 * c) = o.w;
                 }
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[c][e] += v[e];
             }
     }
     if (!a.shares) return;
@@ -1034,17 +1042,21 @@ int64_t linear_dpre_slabs(int64_t m, int n) {
     return (m + rows - 1) / rows;
 }
 
-cudaError_t launch_linear_dpre(const LinearDpreArgs& args, cudaStream_t st) {
+cudaError_t launch_linear_dpre(const LinearDpreArgs& args, const LinearDpreRows& rows, cudaStream_t st) {
     LinearDpreArgs a = args;
+    LinearDpreRows x = rows;
     a.slab_rows = dpre_slab_rows(a.m, a.n);
     const int64_t slabs = linear_dpre_slabs(a.m, a.n);
-    a.ctas = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
-    const unsigned grid = a.ctas + (a.expand.out ? unpack_flat_ctas(a.expand) : 0);
+    x.ctas = (unsigned)(slabs * ((a.n + kSlabCols - 1) / kSlabCols));
+    const unsigned grid = x.ctas + (x.expand.out ? unpack_flat_ctas(x.expand) : 0);
     const bool codes = a.pre_scales != nullptr;
     const bool vec = a.n % 8 == 0 && ((uintptr_t)a.pre & (codes ? 7 : 15)) == 0;
-    const cudaError_t e = launch_kernel(codes ? (vec ? ssd_linear_dpre<e4m3_t, 8> : ssd_linear_dpre<e4m3_t, 1>)
-                                              : (vec ? ssd_linear_dpre<bf16_t, 8> : ssd_linear_dpre<bf16_t, 1>),
-                                        grid, 256, 0, st, true, a);
+    const bool from_rows = x.x_scales || x.expand.out;
+    auto kern = codes ? (vec ? (from_rows ? ssd_linear_dpre<e4m3_t, 8, true> : ssd_linear_dpre<e4m3_t, 8, false>)
+                             : (from_rows ? ssd_linear_dpre<e4m3_t, 1, true> : ssd_linear_dpre<e4m3_t, 1, false>))
+                      : (vec ? (from_rows ? ssd_linear_dpre<bf16_t, 8, true> : ssd_linear_dpre<bf16_t, 8, false>)
+                             : (from_rows ? ssd_linear_dpre<bf16_t, 1, true> : ssd_linear_dpre<bf16_t, 1, false>));
+    const cudaError_t e = launch_kernel(kern, grid, 256, 0, st, true, a, x);
     if (e != cudaSuccess || !a.dbias) return e;
     return launch_kernel(ssd_linear_dbias, (unsigned)((a.n + 31) / 32), 1024, 0, st, true, (const float*)a.shares, (int)slabs, a.n,
                          a.dbias);
