@@ -479,8 +479,9 @@ SSD_API int ssd_linear_bwd(const ssd_linear_params_t* p, const void* x, const vo
  * where x_scales (m) fp32 are given, and pre (m, n) e4m3 codes, contiguous, where pre_scales (m) fp32 are (neither: the
  * call above).  They stand for codes * scale: pre so in fp32; of x the codes times the scales' powers of two are the
  * product's operand, in bf16 in the workspace, which is exact, and the rest of the scales (1 for those of ssd_pack_rows()) is
- * in dpre before its rounding; where dpre is dy itself, x is codes * scale rounded once to bf16.  Codes may start at any
- * byte; ldx is any number from k on then.  x may be NULL where dw is. */
+ * in dpre before its rounding; where dpre is dy itself, x is codes * scale rounded to bf16.  Codes may start at any
+ * byte; ldx is any number from k on then.  x may be NULL where dw is.  Where x_scales or dw is NULL no codes are expanded, and
+ * ssd_linear_bwd_workspace_size() bytes are enough (it asks for an ldx of whole 16-byte units; k is one). */
 SSD_API size_t ssd_linear_bwd_packed_workspace_size(const ssd_linear_params_t* p);
 SSD_API int ssd_linear_bwd_packed(const ssd_linear_params_t* p, const void* x, const float* x_scales, const void* w,
              const void* pre, const float* pre_scales, const void* dy, void* dx, void* dw, float* dbias,

@@ -107,8 +107,8 @@ struct LinearBwdLayout {
     size_t dpre_off, shares_off, parts_off, rows_off, inv_off, ones_off, total;
     LinearPlan dx, dw;
 };
-// packed: with room for x in bf16, its scales' factors' reciprocals and a row of ones.
-LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p, bool packed) {
+// expand: with room for x in bf16, its scales' factors' reciprocals and a row of ones.
+LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p, bool expand) {
     LinearBwdLayout l;
     l.own_dpre = p->act != SSD_ACT_NONE || p->n % 8 != 0;
     l.ldp = (p->n + 7) / 8 * 8;
@@ -119,7 +119,7 @@ LinearBwdLayout linear_bwd_layout(const ssd_linear_params_t* p, bool packed) {
     l.dw = linear_plan(p->n, p->k, p->m * 2, false);
     l.rows_off = l.parts_off + (l.dx.parts_bytes > l.dw.parts_bytes ? l.dx.parts_bytes : l.dw.parts_bytes);
     l.total = l.rows_off;
-    if (packed) {
+    if (expand) {
         l.rows_off = align_up(l.rows_off, 256);
         l.inv_off = align_up(l.rows_off + (size_t)p->m * p->k * 2, 256);
         l.ones_off = align_up(l.inv_off + (size_t)p->m * 4, 256);
@@ -203,7 +203,7 @@ int linear_impl(const ssd_linear_params_t* p, const void* x, const void* w, cons
     return launch_linear(a, plan, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
-// x_scales, pre_scales: x, pre are 8-bit rows; packed: the workspace has room for x in bf16.
+// x_scales, pre_scales: x, pre are 8-bit rows; packed: x may be missing where dw is.
 int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_scales, const void* w, const void* pre,
                     const float* pre_scales, const void* dy, void* dx, void* dw, float* dbias, void* workspace,
                     size_t workspace_bytes, void* stream, bool packed) {
@@ -220,7 +220,7 @@ int linear_bwd_impl(const ssd_linear_params_t* p, const void* x, const float* x_
     if ((!x && (dw || x_scales || !packed)) || !w || !dy || (!dx && !dw && !dbias) || (p->act != SSD_ACT_NONE) != (pre != nullptr)) return SSD_ERR_INVALID_ARG;
     if ((pre_scales && !pre) || !aligned(x_scales, 4) || !aligned(pre_scales, 4)) return SSD_ERR_INVALID_ARG;
     if (!aligned(x, x_scales ? 1 : 16) || !aligned(w, 16) || !aligned(dy, 16) || !aligned(pre, pre_scales ? 1 : 2)) return SSD_ERR_INVALID_ARG;
-    const LinearBwdLayout l = linear_bwd_layout(p, packed);
+    const LinearBwdLayout l = linear_bwd_layout(p, x_scales && dw);
     if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return SSD_ERR_WORKSPACE;
     const size_t ex = x_scales ? 1 : 2, ep = pre_scales ? 1 : 2;
     const Mat in[] = {{x, p->m, p->k, p->ldx, ex}, {w, p->n, p->k, p->k, 2}, {pre, p->m, p->n, p->n, ep}, {dy, p->m, p->n, p->n, 2},

@@ -314,8 +314,12 @@ def linear_bwd(dy, x, w, pre=None, *, act="none", x_scales=None, pre_scales=None
     if not (want_dx or want_dw or want_dbias):
         raise ValueError("no gradient wanted")
     ref = ctypes.byref(p)
+    if x_scales is not None and not want_dw:   # codes that nothing reads
+        x = x_scales = None
+        p.ldx = p.k
     packed = x is None or x_scales is not None or pre_scales is not None
-    nbytes = (_lib_c.ssd_linear_bwd_packed_workspace_size if packed else _lib_c.ssd_linear_bwd_workspace_size)(ref)
+    # room for x's codes in bf16 only where they are expanded
+    nbytes = (_lib_c.ssd_linear_bwd_workspace_size if x_scales is None else _lib_c.ssd_linear_bwd_packed_workspace_size)(ref)
     if nbytes == 0:
         raise _lib.SSDError(2, f"linear_bwd of {(*lead, p.k)} and {tuple(w.shape)}, row stride {p.ldx}")
     dx = _empty((*lead, p.k), dtype=_BF16, device=device) if want_dx else None
