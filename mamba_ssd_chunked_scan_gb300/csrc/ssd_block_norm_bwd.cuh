@@ -630,6 +630,7 @@ cudaError_t launch_ring(BlockNormBwdArgs& a, RowPlan p, int* lines, cudaStream_t
     // (8192 columns) 59, 68; with a residual 16384 x 2560 166, 170.
     spread(p, a.rows, a.groups, per_sm, !RES && !XP && sizeof(T) == 2 && per_sm > 1);
     *lines = set_slots(a, p);
+    if (*lines > a.share_lines) return cudaErrorInvalidValue;
     return launch_kernel(kern, (unsigned)p.grid, (unsigned)p.threads, (size_t)weights + (size_t)a.stages * stage, st, true, a);
 }
 
@@ -675,6 +676,7 @@ cudaError_t launch_block_norm_bwd_typed(BlockNormBwdArgs& a, int* lines, cudaStr
     if (e != cudaErrorNotSupported) return e;   // not even one row's records fit an SM: the widest fp32 rows
     const RowPlan p = loose_plan(a.rows, a.size, a.groups);
     *lines = set_slots(a, p);
+    if (*lines > a.share_lines) return cudaErrorInvalidValue;
     return launch_kernel(p.elems == kNarrowElems ? ssd_block_norm_bwd_loose<T, R, kNarrowElems, GATE, RES>
                                                  : ssd_block_norm_bwd_loose<T, R, kWideElems, GATE, RES>,
                          (unsigned)p.grid, (unsigned)p.threads, 0, st, true, a);

@@ -234,7 +234,8 @@ struct BlockNormBwdArgs {
     void* out;             // the forward's, or NULL (gate and norm)
     float* dweight;
     float* dnext_weight;
-    float* shares;         // [lines * width * weights]
+    float* shares;         // [share_lines * width * weights]
+    int64_t share_lines;   // a launch that would leave more is refused
     // set at the launch: the rows' slots, and their shared memory (weights, then stages of operands and scales)
     int slots, late_slots, early_rows, slots_per_cta;
     int stages;

@@ -629,6 +629,7 @@ int ssd_gate_norm_bwd(const ssd_gate_norm_params_t* p, const void* dout, const v
     a.gate_stride = p->z_stride; a.dgate_stride = p->dz_stride; a.scale = 1.f; a.eps = p->eps;
     a.dout = dout; a.x = y; a.x_scales = y_scales; a.gate = z; a.gate_scales = z_scales; a.weight = weight;
     a.dx = dy; a.dgate = dz; a.out = out; a.dweight = dweight; a.shares = (float*)workspace;
+    a.share_lines = (int64_t)(need / (w * sizeof(float)));
     return launch_block_norm_bwd(a, (cudaStream_t)stream) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -709,6 +710,7 @@ int ssd_block_norm_bwd(const ssd_block_norm_params_t* p, const void* dout, const
     a.h = h; a.h_scales = h_scales; a.weight = weight; a.next_weight = next_weight;
     a.dx = dx; a.dgate = dgate; a.dres_out = dresidual; a.dweight = dweight; a.dnext_weight = dnext_weight;
     a.shares = (float*)workspace;
+    a.share_lines = (int64_t)(need / (2 * w * sizeof(float)));
     return launch_block_norm_bwd(a, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
