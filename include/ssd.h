@@ -325,7 +325,7 @@ SSD_API int ssd_add_norm_bwd(int64_t rows, int32_t width, int32_t dtype, int32_t
 SSD_API int ssd_pack_rows(int64_t rows, int32_t width, int32_t group_size, int32_t dtype, int64_t x_stride,
              const void* x, void* codes, float* scales, void* stream);
 
-/* out = codes * scale, in dtype (rounded once; exact for the scales of ssd_pack_rows()).  codes, scales and limits
+/* out = codes * scale in fp32, then in dtype (both exact for the scales of ssd_pack_rows()).  codes, scales and limits
  * as there (any group_size that divides width); out (rows, width) contiguous. */
 SSD_API int ssd_unpack_rows(int64_t rows, int32_t width, int32_t group_size, int32_t dtype,
              const void* codes, const float* scales, void* out, void* stream);
@@ -362,6 +362,8 @@ SSD_API int ssd_gate_norm_pack(const ssd_gate_norm_params_t* p, const void* y, c
  *                      column range of a projection's gradient; columns outside of it are left alone)
  *   out                (rows, width) dtype, or NULL: the forward's result, computed again
  *   dweight            (width) fp32, written (zeros where rows == 0)
+ * Sums are fp32, of u, or of codes * silu(z) with the scale joined to each thread's (8 or 16 elements): gates from 1e16 on may overflow
+ * them.  One of y and z in 8 bits and the other not is slower (single elements instead of vectors).
  * `workspace`: ssd_gate_norm_bwd_workspace_size() bytes (0 on invalid parameters or rows == 0), 16-byte aligned, needs no
  * initialisation; calls that share it must be ordered on one stream.  No output may overlap an input.  Two launches;
  * bitwise deterministic (dweight is summed in a fixed order). */

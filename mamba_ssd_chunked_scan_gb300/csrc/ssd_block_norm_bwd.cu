@@ -15,10 +15,12 @@
 // slots: arithmetic is on pairs of numbers, and a record's pieces lie at constant offsets.
 //
 // Times with the shares' sum (7 us of them), and parts of the copy's rate: gate and norm 16384 x 5120 bf16 140 us, 89 %; from 8 bits
-// 12289 x 5120, with the result computed again, 121 us, 77 % (issue slots 57 % busy, shared memory's and the stores' wavefronts 62 %:
+// 12289 x 5120, with the result computed again, 123 us, 76 % (issue slots 57 % busy, shared memory's and the stores' wavefronts 62 %:
 // codes are decoded and the weights read in both passes); with a residual in fp32 16384 x 2560 155 us, 88 % (163 us while x was asked
-// for after the last pass); all operands in 8 bits 9001 x 1533 68 us, 39 % (1536 columns 52 us: three passes a row, the codes decoded in
-// each; at 1533 97 of 128 threads have columns, and first and last vectors go by elements).
+// for after the last pass); all operands in 8 bits 9001 x 1533 69 us, 39 % (1536 columns 52 us).  There neither HBM nor the issue slots
+// (54 %) are full: h is decoded in passes one and two, x in two and three, the gate once, and a CTA's next row, 10.7 KB, is
+// asked for after the second pass only; at 1533 columns 97 of 128 threads have any, and first and last
+// vectors go by elements.
 #include "ssd_block_norm_bwd.cuh"
 
 namespace ssd {

@@ -735,9 +735,10 @@ __global__ void __launch_bounds__(256) ssd_linear_join(const __grid_constant__ L
 // flight per warp (8192 x 5120 42 us, 89 % of the copy's rate; with pre in 8 bits 47 us, 66 %).
 constexpr int kSlabRows = 128, kSlabCols = 256;
 // P: the type of pre (e4m3: times its row's scale; two rows in flight, since decoding takes the registers that more warps run on: all
-// gradients of 8192 x 2560 to 5120 293 us, with four 297, with eight 309).  CTAs from a.ctas on unpack x (290 us, 100 x 512 to 512 16.3;
-// in a launch of its own 293 and 18.3).  Where x comes as 8-bit rows, their scales' factors go into dpre before its
-// rounding, so that the product with the codes rounds no operand twice; dx's epilogue takes them out.
+// gradients of 8192 x 2560 to 5120 293 us, with four 297, with eight 309).  CTAs from x.ctas on unpack x (290 us, 100 x 512 to 512 16.3;
+// in a launch of its own 293 and 18.3; these figures are of calls in turns: the products are bound by power, and after other work the
+// same call takes up to 320).  Where x comes as 8-bit rows, their scales' factors go into dpre before its rounding, so that the product
+// with the codes rounds no operand twice; dx's epilogue takes them out.
 // X: whether x does.  What only that takes lies in an argument of its own, so that the others stay in registers (in one kernel for both
 // single elements of 32768 x 1001 bf16 took 131 us instead of 78, vectors of 8192 x 5120 49 instead of 46).
 template <typename P, int V, bool X>

@@ -4,8 +4,9 @@
 //
 // Both are bound by HBM: a unit (a row's group) stays in registers from its one read to its one write, since its
 // scale needs all of it (16384 x 5120 bf16 columns of a wider matrix 40 us, 93 % of the copy's rate; 4096 columns of fp32 49 us, all
-// of it); unpacking goes by 16 elements of the flat array, whatever the rows' width (4099 x 2557 to fp32 12 us, 63 %: 8 us of HBM
-// leave a launch's start and end uncovered; 16384 x 2560 to bf16 20 us, 91 %).
+// of it); unpacking goes by 16 elements of the flat array, whatever the rows' width (16384 x 2560 to bf16 20 us, 91 %; to fp32 45 us,
+// 69 %, and 4099 x 2557 12 us, 63 %: a thread's four 16-byte stores lie 64 bytes from its neighbour's, so that each store instruction
+// writes half of every sector it touches).
 #include "ssd_kernels.h"
 #include "ssd_unpack.cuh"
 

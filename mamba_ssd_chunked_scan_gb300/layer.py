@@ -282,8 +282,8 @@ def linear_bwd(dy, x, w, pre=None, *, act="none", x_scales=None, pre_scales=None
     ``dbias`` (n) fp32, None where not wanted.  (The residual's gradient is dy.)
 
     x and pre may each be 8-bit rows (pack_rows', or add_norm's), float8_e4m3fn with x_scales, pre_scales (...) fp32; w stays bf16.
-    Nothing of pack_rows' rows is lost; other scales cost one rounding to bf16 without an activation, none with one.  x is only
-    read for dw: it may be None with want_dw=False."""
+    Nothing of pack_rows' rows is lost; with other scales x is rounded to bf16 where dy itself is the products' operand (no activation, n
+    a multiple of 8), not otherwise.  x is only read for dw: it may be None with want_dw=False."""
     dev = _device("dy", dy) if x is None else _device("x", x)
     if stream is not None or _current_device() != dev:
         with _elsewhere(dev, stream):

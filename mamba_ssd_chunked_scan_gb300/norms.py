@@ -67,7 +67,7 @@ def pack_rows(x, group_size=None, *, stream=None):
 
 
 def unpack_rows(codes, scales, *, dtype=_BF16, stream=None):
-    """What 8-bit rows stand for, in dtype (bf16 or fp32): codes (..., width) float8_e4m3fn, contiguous, and scales fp32, (...) or
+    """What 8-bit rows stand for, codes * scales in fp32, in dtype (bf16 or fp32; exact for pack_rows' scales): codes (..., width) float8_e4m3fn, contiguous, and scales fp32, (...) or
     (..., groups)."""
     dev = _device("codes", codes)
     if stream is not None or _current_device() != dev:
@@ -122,7 +122,7 @@ def gate_norm_bwd(dout, y, z, weight, group_size, eps=1e-5, *, y_scales=None, z_
 
     dout (..., width) bf16 or fp32; y and z as given to it (z may be a column range of a wider matrix), or 8-bit rows with
     y_scales, z_scales (..., width / group_size): ``gate_norm_bwd(dout, weight=w, group_size=n, **packed)`` takes what
-    gate_norm(..., pack=True) left.  dz may be given to be written in place, at any row stride (a column range of
+    gate_norm(..., pack=True) left (one in 8 bits and the other not is slower).  dz may be given to be written in place, at any row stride (a column range of
     a projection's gradient, say).  Returns a dict: ``dy``, ``dz`` (dout's type), ``dweight`` (fp32) and, with want_out, ``out``: the
     call's result, computed again (else None)."""
     dev = _device("dout", dout)
@@ -220,7 +220,7 @@ def block_norm_bwd(dout, dresidual, x, h, weight, gate=None, next_weight=None, *
 
     dout (..., width) in dtype, bf16 or fp32 (None without next_weight); dresidual in the residual's type; x and gate as given to
     it, h its ``residual`` (not read without next_weight, and may be None then), each of them 8-bit rows where its scales (...) are
-    given: the forward's with pack, or pack_rows'.  dtype is that of dout, x and gate; it need only be given where there is no dout and they are 8-bit
+    given: the forward's with pack, or pack_rows' (one of x and gate in 8 bits and the other not is slower).  dtype is that of dout, x and gate; it need only be given where there is no dout and they are 8-bit
     rows.  dgate may be given to be written in place, at any row stride.  Returns a dict: ``dx``, ``dgate`` (None
     without a gate) in dtype, ``dresidual`` in the residual's, ``dweight`` and ``dnext_weight`` (None without
     next_weight) fp32."""
